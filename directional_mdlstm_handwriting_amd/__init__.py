@@ -49,6 +49,7 @@ INFO_KEYS = ("n", "canvas_h", "canvas_w", "rows", "real_pixels", "computed_cells
 # every exported entry point: (name, restype, argtypes)
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _SIGS = [
     ("mdl_pack", _I32, [_P, _P, _I32, _I32, _I32, _I32, ctypes.POINTER(_P)]),
@@ -80,6 +81,11 @@ _SIGS = [
     ("mdl_ctc_workspace_size", _I32, [_P, _I32, _I32, _I32, ctypes.POINTER(_SZ)]),
     ("mdl_ctc_head", _I32, [_P, _P, _P, _I32, _P, _P, _I32, _P, _P, ctypes.c_int64, _I32, _P, _P, _P, _P, _P,
                             _SZ, _P]),
+    ("mdl_scan_workspace_size", _I32, [_I64, _I32, _I32, ctypes.POINTER(_SZ)]),
+    ("mdl_scan_forward", _I32, [_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, _SZ, _P]),
+    ("mdl_scan_backward", _I32, [_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, _P, _P,
+                                 _I64, _P, _P, _SZ, _P]),
+    ("mdl_scan_step", _I32, [_I32, _I32, _I32, _P, _P, _P, _I64, _P, _I32, _P, _P, _P, _I64, _P]),
     ("mdl_timing", _I32, [_I32]),
     ("mdl_set_wgrad_overlap", _I32, [_I32]),
     ("mdl_timing_only", _I32, [ctypes.c_char_p]),
@@ -325,6 +331,31 @@ def mdl_blockconv_backward_noalloc(lk: Layout, d_desc_k, lk1: Layout, d_desc_k1,
     _check(_lib.mdl_blockconv_backward_noalloc(lk.handle, _ptr(d_desc_k), lk1.handle, _ptr(d_desc_k1), _ptr(h_dirs_k),
                                                H, kh, kw, _ptr(Wc), Cout, _ptr(dx_canvas_k1), _ptr(dh_dirs_k),
                                                _ptr(dWc), _ptr(dbc), _stream(stream)))
+
+
+def mdl_scan_workspace_size(T: int, D: int, dtype: int) -> int:
+    b = _SZ()
+    _check(_lib.mdl_scan_workspace_size(T, D, dtype, ctypes.byref(b)))
+    return b.value
+
+
+def mdl_scan_forward(seq_off, S: int, T: int, D: int, dtype: int, reverse: int, zf, g, zo, ldz: int, h0, y, ldy: int,
+                     hT, ws, ws_bytes: int, stream=None):
+    _check(_lib.mdl_scan_forward(_ptr(seq_off), S, T, D, dtype, reverse, _ptr(zf), _ptr(g), _ptr(zo), ldz, _ptr(h0),
+                                 _ptr(y), ldy, _ptr(hT), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def mdl_scan_backward(seq_off, S: int, T: int, D: int, dtype: int, reverse: int, zf, g, zo, ldz: int, h0, dy,
+                      ldy: int, dhT, dzf, dg, dzo, ldd: int, dh0, ws, ws_bytes: int, stream=None):
+    _check(_lib.mdl_scan_backward(_ptr(seq_off), S, T, D, dtype, reverse, _ptr(zf), _ptr(g), _ptr(zo), ldz, _ptr(h0),
+                                  _ptr(dy), ldy, _ptr(dhT), _ptr(dzf), _ptr(dg), _ptr(dzo), ldd, _ptr(dh0), _ptr(ws),
+                                  ws_bytes, _stream(stream)))
+
+
+def mdl_scan_step(S: int, D: int, dtype: int, zf, g, zo, ldz: int, slots, n_slots: int, h_in, h_out, y, ldy: int,
+                  stream=None):
+    _check(_lib.mdl_scan_step(S, D, dtype, _ptr(zf), _ptr(g), _ptr(zo), ldz, _ptr(slots), n_slots, _ptr(h_in),
+                              _ptr(h_out), _ptr(y), ldy, _stream(stream)))
 
 
 def mdl_set_wgrad_overlap(mode):

@@ -944,6 +944,150 @@ int mdl_ctc_head(const mdl_layout* layout, const void* d_desc, const float* y_fl
     GUARD_END
 }
 
+// ---- the gated recurrence over packed sequences ---------------------------------------------------
+static int check_dtype(const std::string& F, int32_t dtype) {
+    if (dtype != MDL_F32 && dtype != MDL_BF16) return fail(MDL_EINVAL, F + ": unknown dtype");
+    return MDL_OK;
+}
+// a row stride of at least `cols` elements whose largest element offset stays far inside 64 bits
+static int check_stride(const std::string& F, const char* name, int64_t rows, int64_t cols, int64_t ld) {
+    if (ld < cols) return fail(MDL_EINVAL, F + ": " + name + " below the row length");
+    if (ld >= (int64_t(1) << 60) / std::max<int64_t>(rows, 1))
+        return fail(MDL_EOVERFLOW, F + ": rows times " + name + " reach 2^60");
+    return MDL_OK;
+}
+// sizes and workspace of a scan; need receives the workspace bytes
+static int check_scan(const std::string& F, int64_t T, int32_t D, int32_t dtype, size_t& need) {
+    int rc = check_dtype(F, dtype);
+    if (rc) return rc;
+    if (T < 0 || D < 1) return fail(MDL_EINVAL, F + ": need T >= 0 and D >= 1");
+    if (T >= (int64_t(1) << 60) / D) return fail(MDL_EOVERFLOW, F + ": rows times channels reach 2^60");
+    const mdl::ScanPlan p = mdl::scan_plan(T, D, dtype);
+    if (p.ntiles >= (int64_t(1) << 31) / p.ncb) return fail(MDL_EOVERFLOW, F + ": the launch reaches 2^31 workgroups");
+    need = p.total;
+    return MDL_OK;
+}
+static int check_ws(const std::string& F, const char* size_fn, size_t need, const void* ws, size_t ws_bytes) {
+    if (need > 0 && !ws) return fail(MDL_EINVAL, F + ": null workspace");
+    if (need > 0 && reinterpret_cast<uintptr_t>(ws) % 16) return fail(MDL_EINVAL, F + ": workspace not 16-byte aligned");
+    if (ws_bytes < need) return fail(MDL_ESIZE, F + ": workspace smaller than " + size_fn);
+    return MDL_OK;
+}
+
+int mdl_scan_workspace_size(int64_t T, int32_t D, int32_t dtype, size_t* bytes) {
+    GUARD_BEGIN
+    if (!bytes) return fail(MDL_EINVAL, "mdl_scan_workspace_size: null argument");
+    size_t need = 0;
+    const int rc = check_scan("mdl_scan_workspace_size", T, D, dtype, need);
+    if (rc) return rc;
+    *bytes = need;
+    return MDL_OK;
+    GUARD_END
+}
+
+int mdl_scan_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, int32_t dtype, int32_t reverse,
+                     const void* zf, const void* g, const void* zo, int64_t ldz, const float* h0, void* y,
+                     int64_t ldy, float* hT, void* ws, size_t ws_bytes, void* stream) {
+    GUARD_BEGIN
+    const std::string F("mdl_scan_forward");
+    size_t need = 0;
+    int rc = check_scan(F, T, D, dtype, need);
+    if (rc) return rc;
+    if (S < 1) return fail(MDL_EINVAL, F + ": need S >= 1");
+    if (!seq_off || (T > 0 && (!zf || !g || !y))) return fail(MDL_EINVAL, F + ": null tensor");
+    if ((rc = check_stride(F, "ldz", T, D, ldz)) || (rc = check_stride(F, "ldy", T, D, ldy))) return rc;
+    if ((rc = check_ws(F, "mdl_scan_workspace_size", need, ws, ws_bytes))) return rc;
+    mdl::ScanArgs a{};
+    a.off = seq_off;
+    a.S = S;
+    a.D = D;
+    a.reverse = reverse != 0;
+    a.T = T;
+    a.zf = zf;
+    a.g = g;
+    a.zo = zo;
+    a.ldz = ldz;
+    a.ldy = ldy;
+    a.h0 = h0;
+    a.y = y;
+    a.hT = hT;
+    hipError_t e;
+    {
+        Timed t("scan_fwd");
+        e = mdl::launch_scan_fwd(a, dtype, ws, static_cast<hipStream_t>(stream));
+    }
+    if (e != hipSuccess) return hip_fail(e, F);
+    return MDL_OK;
+    GUARD_END
+}
+
+int mdl_scan_backward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, int32_t dtype, int32_t reverse,
+                      const void* zf, const void* g, const void* zo, int64_t ldz, const float* h0, const void* dy,
+                      int64_t ldy, const float* dhT, void* dzf, void* dg, void* dzo, int64_t ldd, float* dh0,
+                      void* ws, size_t ws_bytes, void* stream) {
+    GUARD_BEGIN
+    const std::string F("mdl_scan_backward");
+    size_t need = 0;
+    int rc = check_scan(F, T, D, dtype, need);
+    if (rc) return rc;
+    if (S < 1) return fail(MDL_EINVAL, F + ": need S >= 1");
+    if (!seq_off || (T > 0 && (!zf || !g || !dy || !dzf || !dg))) return fail(MDL_EINVAL, F + ": null tensor");
+    if (T > 0 && (zo == nullptr) != (dzo == nullptr)) return fail(MDL_EINVAL, F + ": dzo goes with zo, and only with it");
+    if ((rc = check_stride(F, "ldz", T, D, ldz)) || (rc = check_stride(F, "ldy", T, D, ldy)) ||
+        (rc = check_stride(F, "ldd", T, D, ldd)))
+        return rc;
+    if ((rc = check_ws(F, "mdl_scan_workspace_size", need, ws, ws_bytes))) return rc;
+    mdl::ScanArgs a{};
+    a.off = seq_off;
+    a.S = S;
+    a.D = D;
+    a.reverse = reverse != 0;
+    a.T = T;
+    a.zf = zf;
+    a.g = g;
+    a.zo = zo;
+    a.dy = dy;
+    a.ldz = ldz;
+    a.ldy = ldy;
+    a.ldd = ldd;
+    a.h0 = h0;
+    a.dhT = dhT;
+    a.dzf = dzf;
+    a.dg = dg;
+    a.dzo = dzo;
+    a.dh0 = dh0;
+    hipError_t e;
+    {
+        Timed t("scan_bwd");
+        e = mdl::launch_scan_bwd(a, dtype, ws, static_cast<hipStream_t>(stream));
+    }
+    if (e != hipSuccess) return hip_fail(e, F);
+    return MDL_OK;
+    GUARD_END
+}
+
+int mdl_scan_step(int32_t S, int32_t D, int32_t dtype, const void* zf, const void* g, const void* zo, int64_t ldz,
+                  const int32_t* slots, int32_t n_slots, const float* h_in, float* h_out, void* y, int64_t ldy,
+                  void* stream) {
+    GUARD_BEGIN
+    const std::string F("mdl_scan_step");
+    int rc = check_dtype(F, dtype);
+    if (rc) return rc;
+    if (S < 1 || D < 1 || n_slots < 1) return fail(MDL_EINVAL, F + ": need S, D and n_slots >= 1");
+    if (!zf || !g || !h_in || !h_out || !y) return fail(MDL_EINVAL, F + ": null tensor");
+    if (!slots && n_slots < S) return fail(MDL_EINVAL, F + ": n_slots below S without slots");
+    if ((rc = check_stride(F, "ldz", S, D, ldz)) || (rc = check_stride(F, "ldy", S, D, ldy))) return rc;
+    hipError_t e;
+    {
+        Timed t("scan_step");
+        e = mdl::launch_scan_step(S, D, dtype, zf, g, zo, ldz, slots, n_slots, h_in, h_out, y, ldy,
+                                  static_cast<hipStream_t>(stream));
+    }
+    if (e != hipSuccess) return hip_fail(e, F);
+    return MDL_OK;
+    GUARD_END
+}
+
 int mdl_set_wgrad_overlap(int32_t mode) {
     if (mode < 0 || mode > 2) return fail(MDL_EINVAL, "mdl_set_wgrad_overlap: mode must be 0, 1 or 2");
     g_overlap.store(mode);

@@ -1,0 +1,533 @@
+// k_scan.hip — the gated linear recurrence over packed sequences: forward, backward and the single-token step.
+//
+// Per channel, with gates that do not read the state (the Leaky cell's update s = f s + (1 - f) g along one axis):
+//   f = sigmoid(zf), o = sigmoid(zo);  h_t = f_t h_{t-1} + (1 - f_t) g_t;  y_t = o_t h_t  (y = h without zo)
+// and, with l_t = dL/dh_t,
+//   l_t = o_t dy_t + f_{t+1} l_{t+1}  (dhT instead of the second term at a sequence's last token)
+//   dg = (1 - f) l;  dzf = f (1 - f) (h_{t-1} - g) l;  dzo = dy h o (1 - o);  dh0 = f_first l_first.
+//
+// Both recurrences are affine maps x -> A x + B composed along time, so they are cut into tiles of TT tokens by CB
+// channels that run at once: the packed token axis is tiled evenly whatever the sequences' lengths, and a sequence
+// start inside a tile is a map that ignores its argument, written A = -1 (A is a product of sigmoids otherwise).
+// A thread owns V channels (16 bytes of a row) and NT consecutive tokens; the 256 / CL threads of one channel vector
+// hold the tile's successive token groups. Thread maps meet in LDS, where one thread per channel chains them.
+// The tile maps are joined over time per channel, and the second pass over the data applies the joined states.
+// All states, maps and sums are fp32; a stream of bfloat16 is rounded once, as it is stored.
+#include "kernels.h"
+#include "seqio.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace mdl {
+
+namespace {
+
+constexpr int SCAN_THREADS = 256;
+constexpr float kReset = -1.0f;  // the A of a map that ignores its argument
+
+// the states of a map applied to x
+__device__ inline float apply_map(float A, float B, float x) { return A < 0.f ? B : __builtin_fmaf(A, x, B); }
+
+// First index i in [0, n) with off[i] >= v (n if none), off ascending: 64 probes a round, one per lane, every lane of
+// the wave in it. Any contents of off keep the probes inside [0, n).
+__device__ inline int lower_bound_wave(const int64_t* off, int n, int64_t v) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, len = n;
+    while (len > 0) {
+        const int step = (len + 63) >> 6;
+        const int64_t idx = (int64_t)lane * step;
+        const bool below = idx < len && off[lo + idx] < v;
+        const int cnt = __popcll(__ballot(below));
+        if (cnt == 0) break;
+        const int used = (cnt - 1) * step + 1;
+        lo += used;
+        len = min(step - 1, len - used);
+    }
+    return lo;
+}
+
+struct Tile {
+    int64_t p0;   // first position (token order of the scan) of the tile
+    int c0;       // first channel
+};
+
+// Sequence marks of the tile's positions: start[p] / last[p] hold sequence + 1 where position p0 + p is a sequence's
+// first / last in scan order, 0 elsewhere. Sequences without tokens hand `from` to `to` ([S][D], zero if null).
+template <int TT, int CB>
+__device__ inline void mark_tile(const ScanArgs& a, Tile t, int* start, int* last, const float* from, float* to) {
+    for (int i = threadIdx.x; i < TT; i += SCAN_THREADS) start[i] = last[i] = 0;
+    const int64_t t1 = a.reverse ? a.T - t.p0 : min(t.p0 + TT, a.T);      // tokens [t0, t1) of the tile
+    const int64_t t0 = a.reverse ? max<int64_t>(a.T - t.p0 - TT, 0) : t.p0;
+    const bool final_tile = t1 >= a.T;
+    const int sa = max(lower_bound_wave(a.off, a.S, t0) - 1, 0);
+    __syncthreads();
+    for (int64_t s = sa + (int)threadIdx.x; s < a.S; s += SCAN_THREADS) {
+        const int64_t b = a.off[s], e = a.off[s + 1];
+        if (b >= t1 && !final_tile) break;
+        if (e <= b) {
+            // by the tile that holds the offset, the last one for offsets at the end
+            const bool mine = b >= t0 && (b < t1 || final_tile);
+            if (mine && to) {
+                for (int c = t.c0; c < min(t.c0 + CB, a.D); ++c) to[s * a.D + c] = from ? from[s * a.D + c] : 0.f;
+            }
+            continue;
+        }
+        const int64_t ps = (a.reverse ? a.T - e : b) - t.p0, pl = (a.reverse ? a.T - 1 - b : e - 1) - t.p0;
+        if (ps >= 0 && ps < TT) start[ps] = (int)s + 1;
+        if (pl >= 0 && pl < TT) last[pl] = (int)s + 1;
+    }
+    __syncthreads();
+}
+
+// a thread's share of the tile
+template <int V, int CL, int NT>
+struct Share {
+    int64_t p;          // its first position
+    int group;          // its token group
+    int ch;             // its first channel (inside the row)
+    bool active;        // false: a lane past the row's end, which repeats the last vector and stores nothing
+    unsigned inside;    // bit i: position p + i is a token of a sequence
+    __device__ inline Share(const ScanArgs& a, Tile t) {
+        group = threadIdx.x / CL;
+        const int c = t.c0 + (threadIdx.x % CL) * V;
+        p = t.p0 + group * NT;
+        active = c < a.D;
+        ch = min(c, a.D - V);
+        inside = 0;
+    }
+    // token of position p + i, moved inside [0, T) for positions past the end (their loads go unused)
+    __device__ inline int64_t token(const ScanArgs& a, int i) const {
+        const int64_t q = min(p + i, a.T - 1);
+        return a.reverse ? a.T - 1 - q : q;
+    }
+    __device__ inline void bounds(const ScanArgs& a) {
+        const int64_t lo = a.off[0], hi = a.off[a.S];
+        for (int i = 0; i < NT; ++i) {
+            const int64_t q = p + i, tok = a.reverse ? a.T - 1 - q : q;
+            if (q < a.T && tok >= lo && tok < hi) inside |= 1u << i;
+        }
+    }
+};
+
+__device__ inline Tile tile_of(const ScanArgs& a, int64_t linear, int tt, int cb) {
+    return {(linear / a.ncb) * tt, (int)(linear % a.ncb) * cb};
+}
+
+// Forward. PART: the tile's map into a.words; otherwise the states from the tile's incoming state in a.carry.
+template <typename T, int V, int CL, int NT, bool PART>
+__global__ __launch_bounds__(SCAN_THREADS) void k_scan_fwd(ScanArgs a) {
+    constexpr int G = SCAN_THREADS / CL, TT = G * NT, CB = CL * V;
+    __shared__ int start[TT], last[TT];
+    __shared__ f32x2 maps[G][CB];
+    const Tile tile = tile_of(a, blockIdx.x, TT, CB);
+    Share<V, CL, NT> me(a, tile);
+    Raw<T, V> rf[NT], rg[NT], ro[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int64_t t = me.token(a, i);
+        rf[i] = load_raw<V>(static_cast<const T*>(a.zf) + t * a.ldz + me.ch);
+        rg[i] = load_raw<V>(static_cast<const T*>(a.g) + t * a.ldz + me.ch);
+        if (!PART && a.zo) ro[i] = load_raw<V>(static_cast<const T*>(a.zo) + t * a.ldz + me.ch);
+    }
+    me.bounds(a);
+    mark_tile<TT, CB>(a, tile, start, last, a.h0, PART ? nullptr : a.hT);
+    float f[NT][V], b[NT][V], A[V], B[V];
+    unsigned reset = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        A[v] = 1.f;
+        B[v] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const bool in = me.inside >> i & 1;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float s, c;
+            sigm2<T>(rf[i][v], s, c);
+            f[i][v] = in ? s : 1.f;
+            b[i][v] = in ? c * rg[i][v] : 0.f;
+        }
+        const int st = in ? start[me.group * NT + i] : 0;
+        if (st) {
+            reset |= 1u << i;
+            if (a.h0) {
+                float h[V];
+                load_f32<V>(a.h0 + (int64_t)(st - 1) * a.D + me.ch, h);
+#pragma unroll
+                for (int v = 0; v < V; ++v) b[i][v] = __builtin_fmaf(f[i][v], h[v], b[i][v]);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            B[v] = st ? b[i][v] : __builtin_fmaf(f[i][v], B[v], b[i][v]);
+            A[v] = A[v] * f[i][v];
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) maps[me.group][(threadIdx.x % CL) * V + v] = f32x2{reset ? kReset : A[v], B[v]};
+    __syncthreads();
+    const int64_t slot = (int64_t)blockIdx.x * CB;
+    for (int c = threadIdx.x; c < CB; c += SCAN_THREADS) {
+        if constexpr (PART) {
+            float ta = 1.f, tb = 0.f;
+            for (int k = 0; k < G; ++k) {
+                const f32x2 m = maps[k][c];
+                tb = apply_map(m[0], m[1], tb);
+                ta = m[0] < 0.f || ta < 0.f ? kReset : ta * m[0];
+            }
+            a.words[slot + c] = f32x2{ta, tb};
+        } else {
+            float h = a.carry ? a.carry[slot + c] : 0.f;
+            for (int k = 0; k < G; ++k) {
+                const f32x2 m = maps[k][c];
+                maps[k][c][1] = h;
+                h = apply_map(m[0], m[1], h);
+            }
+        }
+    }
+    if constexpr (!PART) {
+        __syncthreads();
+        float h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = maps[me.group][(threadIdx.x % CL) * V + v][1];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const bool r = reset >> i & 1;
+            float y[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                h[v] = r ? b[i][v] : __builtin_fmaf(f[i][v], h[v], b[i][v]);
+                y[v] = h[v];
+                if (a.zo) {
+                    float s, c;
+                    sigm2<T>(ro[i][v], s, c);
+                    y[v] *= s;
+                }
+            }
+            if (me.active && (me.inside >> i & 1)) {
+                store_vec<V>(static_cast<T*>(a.y) + me.token(a, i) * a.ldy + me.ch, y);
+                const int en = last[me.group * NT + i];
+                if (en && a.hT) store_f32<V>(a.hT + (int64_t)(en - 1) * a.D + me.ch, h);
+            }
+        }
+    }
+}
+
+// Backward. PART: the tile's map of the reverse recurrence into a.words; otherwise the gradients, from the tile's
+// incoming state in a.carry and the later tiles' gradient in a.dcarry.
+template <typename T, int V, int CL, int NT, bool PART>
+__global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd(ScanArgs a) {
+    constexpr int G = SCAN_THREADS / CL, TT = G * NT, CB = CL * V;
+    __shared__ int start[TT], last[TT];
+    __shared__ f32x2 maps[G][CB], rmaps[G][CB];
+    const Tile tile = tile_of(a, blockIdx.x, TT, CB);
+    Share<V, CL, NT> me(a, tile);
+    Raw<T, V> rf[NT], rg[NT], ro[NT], rd[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int64_t t = me.token(a, i);
+        rf[i] = load_raw<V>(static_cast<const T*>(a.zf) + t * a.ldz + me.ch);
+        if (!PART) rg[i] = load_raw<V>(static_cast<const T*>(a.g) + t * a.ldz + me.ch);
+        if (a.zo) ro[i] = load_raw<V>(static_cast<const T*>(a.zo) + t * a.ldz + me.ch);
+        rd[i] = load_raw<V>(static_cast<const T*>(a.dy) + t * a.ldy + me.ch);
+    }
+    me.bounds(a);
+    mark_tile<TT, CB>(a, tile, start, last, a.dhT, PART ? nullptr : a.dh0);
+    unsigned reset = 0, ends = 0;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        if (!(me.inside >> i & 1)) continue;
+        if (start[me.group * NT + i]) reset |= 1u << i;
+        if (last[me.group * NT + i]) ends |= 1u << i;
+    }
+    // f of token i, and the gradient it receives from its own output
+    float f[NT][V], l[NT][V], A[V], B[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        A[v] = 1.f;
+        B[v] = 0.f;
+    }
+#pragma unroll
+    for (int i = NT - 1; i >= 0; --i) {
+        const bool in = me.inside >> i & 1, en = ends >> i & 1;
+        float extra[V] = {};
+        if (en && a.dhT) load_f32<V>(a.dhT + (int64_t)(last[me.group * NT + i] - 1) * a.D + me.ch, extra);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float s, c, so = 1.f, co;
+            sigm2<T>(rf[i][v], s, c);
+            if (a.zo) sigm2<T>(ro[i][v], so, co);
+            f[i][v] = in ? s : 1.f;
+            l[i][v] = in ? __builtin_fmaf(so, rd[i][v], extra[v]) : 0.f;
+            B[v] = f[i][v] * (en ? l[i][v] : l[i][v] + B[v]);
+            A[v] = A[v] * f[i][v];
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) rmaps[me.group][(threadIdx.x % CL) * V + v] = f32x2{ends ? kReset : A[v], B[v]};
+    float b[NT][V];
+    if constexpr (!PART) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            A[v] = 1.f;
+            B[v] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const bool in = me.inside >> i & 1, r = reset >> i & 1;
+            float h[V] = {};
+            if (r && a.h0) load_f32<V>(a.h0 + (int64_t)(start[me.group * NT + i] - 1) * a.D + me.ch, h);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float s, c;
+                sigm2<T>(rf[i][v], s, c);
+                b[i][v] = in ? c * rg[i][v] : 0.f;
+                B[v] = __builtin_fmaf(f[i][v], r ? h[v] : B[v], b[i][v]);
+                A[v] = A[v] * f[i][v];
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) maps[me.group][(threadIdx.x % CL) * V + v] = f32x2{reset ? kReset : A[v], B[v]};
+    }
+    __syncthreads();
+    const int64_t slot = (int64_t)blockIdx.x * CB;
+    for (int c = threadIdx.x; c < CB; c += SCAN_THREADS) {
+        if constexpr (PART) {
+            float ta = 1.f, tb = 0.f;
+            for (int k = G - 1; k >= 0; --k) {
+                const f32x2 m = rmaps[k][c];
+                tb = apply_map(m[0], m[1], tb);
+                ta = m[0] < 0.f || ta < 0.f ? kReset : ta * m[0];
+            }
+            a.words[slot + c] = f32x2{ta, tb};
+        } else {
+            float h = a.carry ? a.carry[slot + c] : 0.f, d = a.dcarry ? a.dcarry[slot + c] : 0.f;
+            for (int k = 0; k < G; ++k) {
+                const f32x2 m = maps[k][c];
+                maps[k][c][1] = h;
+                h = apply_map(m[0], m[1], h);
+            }
+            for (int k = G - 1; k >= 0; --k) {
+                const f32x2 m = rmaps[k][c];
+                rmaps[k][c][1] = d;
+                d = apply_map(m[0], m[1], d);
+            }
+        }
+    }
+    if constexpr (!PART) {
+        __syncthreads();
+        float h[V], d[V], prev[NT][V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            h[v] = maps[me.group][(threadIdx.x % CL) * V + v][1];
+            d[v] = rmaps[me.group][(threadIdx.x % CL) * V + v][1];
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            float h0[V] = {};
+            const bool r = reset >> i & 1;
+            if (r && a.h0) load_f32<V>(a.h0 + (int64_t)(start[me.group * NT + i] - 1) * a.D + me.ch, h0);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                prev[i][v] = r ? h0[v] : h[v];
+                h[v] = __builtin_fmaf(f[i][v], prev[i][v], b[i][v]);
+            }
+        }
+#pragma unroll
+        for (int i = NT - 1; i >= 0; --i) {
+            const bool en = ends >> i & 1;
+            float dzf[V], dg[V], dzo[V], dp[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float s, c;
+                sigm2<T>(rf[i][v], s, c);
+                const float lam = en ? l[i][v] : l[i][v] + d[v];
+                dg[v] = c * lam;
+                dzf[v] = s * dg[v] * (prev[i][v] - rg[i][v]);
+                if (a.zo) {
+                    float so, co;
+                    sigm2<T>(ro[i][v], so, co);
+                    const float hv = __builtin_fmaf(f[i][v], prev[i][v], b[i][v]);
+                    dzo[v] = rd[i][v] * hv * so * co;
+                }
+                dp[v] = f[i][v] * lam;
+                d[v] = dp[v];
+            }
+            if (me.active && (me.inside >> i & 1)) {
+                const int64_t o = me.token(a, i) * a.ldd + me.ch;
+                store_vec<V>(static_cast<T*>(a.dzf) + o, dzf);
+                store_vec<V>(static_cast<T*>(a.dg) + o, dg);
+                if (a.zo) store_vec<V>(static_cast<T*>(a.dzo) + o, dzo);
+                if ((reset >> i & 1) && a.dh0)
+                    store_f32<V>(a.dh0 + (int64_t)(start[me.group * NT + i] - 1) * a.D + me.ch, dp);
+            }
+        }
+    }
+}
+
+// the tiles' maps chained over time, one thread per channel slot: each tile's incoming value into out
+__global__ __launch_bounds__(256) void k_scan_join(const f32x2* __restrict__ words, float* __restrict__ out,
+                                                   int64_t ntiles, int64_t slots, int backwards) {
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= slots) return;
+    float h = 0.f;
+    for (int64_t k = 0; k < ntiles; ++k) {
+        const int64_t i = (backwards ? ntiles - 1 - k : k) * slots + c;
+        const f32x2 m = words[i];
+        out[i] = h;
+        h = apply_map(m[0], m[1], h);
+    }
+}
+
+// sequences without tokens, where there is no token at all
+__global__ __launch_bounds__(256) void k_scan_copy(const float* __restrict__ from, float* __restrict__ to, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        to[i] = from ? from[i] : 0.f;
+}
+
+// one token of each row: state rows h_in[slot] -> h_out[slot]
+template <typename T, int V>
+__global__ __launch_bounds__(256) void k_scan_step(int S, int D, const T* __restrict__ zf, const T* __restrict__ g,
+                                                   const T* __restrict__ zo, int64_t ldz,
+                                                   const int32_t* __restrict__ slots, int n_slots, const float* h_in,
+                                                   float* h_out, T* __restrict__ y, int64_t ldy) {
+    const int per = (D + V - 1) / V;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)S * per) return;
+    const int s = (int)(i / per), c = (int)(i % per) * V;
+    const int slot = slots ? slots[s] : s;
+    if (slot < 0 || slot >= n_slots) return;
+    // the row's last vector, moved back, shares elements with its neighbour: with the state written in place it takes
+    // them one at a time instead
+    const int n = min(V, D - c);
+    auto body = [&](auto vtag, int ch) {
+        constexpr int W = decltype(vtag)::value;
+        const auto rf = load_raw<W>(zf + (int64_t)s * ldz + ch);
+        const auto rg = load_raw<W>(g + (int64_t)s * ldz + ch);
+        float h[W], out[W];
+        load_f32<W>(h_in + (int64_t)slot * D + ch, h);
+#pragma unroll
+        for (int v = 0; v < W; ++v) {
+            float f, fc;
+            sigm2<T>(rf[v], f, fc);
+            h[v] = __builtin_fmaf(f, h[v], fc * rg[v]);
+            out[v] = h[v];
+        }
+        if (zo) {
+            const auto ro = load_raw<W>(zo + (int64_t)s * ldz + ch);
+#pragma unroll
+            for (int v = 0; v < W; ++v) {
+                float so, co;
+                sigm2<T>(ro[v], so, co);
+                out[v] *= so;
+            }
+        }
+        store_f32<W>(h_out + (int64_t)slot * D + ch, h);
+        store_vec<W>(y + (int64_t)s * ldy + ch, out);
+    };
+    if (n == V) {
+        body(std::integral_constant<int, V>{}, c);
+    } else {
+        for (int k = 0; k < n; ++k) body(std::integral_constant<int, 1>{}, c + k);
+    }
+}
+
+// the tile shape for a row: a vector of 16 bytes a lane (one element where the row is shorter), as many lanes along
+// the row as it fills, at most 16
+template <typename F>
+void with_shape(int D, int dtype, F&& fn) {
+    auto go = [&](auto ty) {
+        using T = decltype(ty);
+        constexpr int V = Width<T>::v;
+        if (D < V) return fn(ty, ScanShape<1, 8, 4>{});
+        const int lanes = (D + V - 1) / V;
+        if (lanes <= 4) return fn(ty, ScanShape<V, 4, 4>{});
+        if (lanes <= 8) return fn(ty, ScanShape<V, 8, 4>{});
+        return fn(ty, ScanShape<V, 16, 4>{});
+    };
+    if (dtype == 1) go(bf16{});
+    else go(float{});
+}
+
+}  // namespace
+
+ScanPlan scan_plan(int64_t T, int D, int dtype) {
+    ScanPlan p;
+    with_shape(D, dtype, [&](auto, auto sh) {
+        using S = decltype(sh);
+        const int64_t cb = S::CL * S::V, tt = (int64_t)(SCAN_THREADS / S::CL) * S::NT;
+        p.tt = (int)tt;
+        p.ncb = (int)((D + cb - 1) / cb);
+        p.slots = p.ncb * cb;
+        p.ntiles = (T + tt - 1) / tt;
+    });
+    if (p.ntiles > 1) {
+        auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+        p.carry = 0;
+        p.dcarry = up(p.ntiles * p.slots * 4);
+        p.words = p.dcarry + up(p.ntiles * p.slots * 4);
+        p.total = p.words + up(p.ntiles * p.slots * 8);
+    }
+    return p;
+}
+
+static hipError_t scan_run(ScanArgs a, int dtype, void* ws, bool backward, hipStream_t st) {
+    if (a.T == 0) {
+        const int64_t n = (int64_t)a.S * a.D;
+        float* to = backward ? a.dh0 : a.hT;
+        if (n > 0 && to)
+            launch(k_scan_copy, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 4096)), dim3(256), 0, st,
+                   backward ? a.dhT : a.h0, to, n);
+        return hipGetLastError();
+    }
+    const ScanPlan p = scan_plan(a.T, a.D, dtype);
+    a.ncb = p.ncb;
+    a.ntiles = p.ntiles;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    if (p.ntiles > 1) {
+        a.carry = reinterpret_cast<float*>(w + p.carry);
+        a.dcarry = reinterpret_cast<float*>(w + p.dcarry);
+        a.words = reinterpret_cast<f32x2*>(w + p.words);
+    }
+    const dim3 grid((unsigned)(p.ntiles * p.ncb)), block(SCAN_THREADS);
+    with_shape(a.D, dtype, [&](auto ty, auto sh) {
+        using T = decltype(ty);
+        using S = decltype(sh);
+        if (p.ntiles > 1) {
+            if (backward) launch(k_scan_bwd<T, S::V, S::CL, S::NT, true>, grid, block, 0, st, a);
+            else launch(k_scan_fwd<T, S::V, S::CL, S::NT, true>, grid, block, 0, st, a);
+            launch(k_scan_join, dim3((unsigned)((p.slots + 255) / 256)), dim3(256), 0, st, a.words,
+                   backward ? a.dcarry : a.carry, p.ntiles, p.slots, backward ? 1 : 0);
+        }
+        if (backward) launch(k_scan_bwd<T, S::V, S::CL, S::NT, false>, grid, block, 0, st, a);
+        else launch(k_scan_fwd<T, S::V, S::CL, S::NT, false>, grid, block, 0, st, a);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_scan_fwd(const ScanArgs& a, int dtype, void* ws, hipStream_t st) {
+    return scan_run(a, dtype, ws, false, st);
+}
+hipError_t launch_scan_bwd(const ScanArgs& a, int dtype, void* ws, hipStream_t st) {
+    return scan_run(a, dtype, ws, true, st);
+}
+
+hipError_t launch_scan_step(int S, int D, int dtype, const void* zf, const void* g, const void* zo, int64_t ldz,
+                            const int32_t* slots, int n_slots, const float* h_in, float* h_out, void* y, int64_t ldy,
+                            hipStream_t st) {
+    auto go = [&](auto ty) {
+        using T = decltype(ty);
+        constexpr int V = Width<T>::v;
+        const int64_t n = (int64_t)S * ((D + V - 1) / V);
+        launch(k_scan_step<T, V>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, S, D, static_cast<const T*>(zf),
+               static_cast<const T*>(g), static_cast<const T*>(zo), ldz, slots, n_slots, h_in, h_out,
+               static_cast<T*>(y), ldy);
+    };
+    if (dtype == 1) go(bf16{});
+    else go(float{});
+    return hipGetLastError();
+}
+
+}  // namespace mdl

@@ -299,4 +299,37 @@ hipError_t launch_ctc_head(const Dev& D, const float* y_flat, int H, const float
                            float* ws, float* loss, float* dy_flat, float* dW, float* db, size_t lds_limit,
                            hipStream_t st);
 
+// the gated linear recurrence over packed sequences (k_scan.hip)
+typedef float scan_f2 __attribute__((ext_vector_type(2)));
+struct ScanArgs {
+    const int64_t* off;           // [S + 1] first token of each sequence
+    int S, D, reverse;
+    int64_t T;                    // tokens of the tensors
+    const void *zf, *g, *zo, *dy; // [T][D] at row strides ldz (zf, g, zo) and ldy (dy, y)
+    int64_t ldz, ldy, ldd;        // ldd: of dzf, dg, dzo
+    const float *h0, *dhT;        // [S][D] or null
+    void *y, *dzf, *dg, *dzo;
+    float *hT, *dh0;              // [S][D] or null
+    // set by the launchers
+    int ncb = 0;                  // channel blocks
+    int64_t ntiles = 0;
+    float *carry = nullptr, *dcarry = nullptr;  // [ntiles][slots] state entering a tile, gradient entering it
+    scan_f2* words = nullptr;                   // [ntiles][slots] the tiles' maps
+};
+template <int V_, int CL_, int NT_>
+struct ScanShape {  // channels a thread, lanes along the row, tokens a thread
+    static constexpr int V = V_, CL = CL_, NT = NT_;
+};
+struct ScanPlan {
+    int tt = 0, ncb = 0;
+    int64_t ntiles = 0, slots = 0;
+    size_t carry = 0, dcarry = 0, words = 0, total = 0;  // byte offsets into the workspace
+};
+ScanPlan scan_plan(int64_t T, int D, int dtype);
+hipError_t launch_scan_fwd(const ScanArgs& a, int dtype, void* ws, hipStream_t st);
+hipError_t launch_scan_bwd(const ScanArgs& a, int dtype, void* ws, hipStream_t st);
+hipError_t launch_scan_step(int S, int D, int dtype, const void* zf, const void* g, const void* zo, int64_t ldz,
+                            const int32_t* slots, int n_slots, const float* h_in, float* h_out, void* y, int64_t ldy,
+                            hipStream_t st);
+
 }  // namespace mdl

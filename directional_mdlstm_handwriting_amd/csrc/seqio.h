@@ -1,0 +1,144 @@
+// seqio.h — element access and gates of the sequence kernels (scan, block norms, distillation), gfx950.
+//
+// Rows are read and written in vectors of 16 bytes per lane at any element alignment: gfx950 takes unaligned global
+// accesses, so rows whose length is no multiple of 16 bytes need no second code path. A row's last vector is moved
+// back to end with the row (start min(c, D - V)); the lanes then share a few elements, which they compute alike.
+#pragma once
+
+#include "devmath.h"
+
+namespace mdl {
+
+struct bf16 {
+    uint16_t u;
+};
+
+// V elements of T as they lie in memory
+template <typename T, int V>
+struct Raw;
+template <int V>
+struct Raw<float, V> {
+    float w[V];
+    __device__ inline float operator[](int i) const { return w[i]; }
+};
+template <int V>
+struct Raw<bf16, V> {
+    uint32_t w[(V + 1) / 2];  // element 2i in the low half
+    __device__ inline float operator[](int i) const {
+        return __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
+    }
+};
+
+typedef uint32_t u32x4_e __attribute__((ext_vector_type(4), aligned(2), may_alias));
+typedef float f32x4_e __attribute__((ext_vector_type(4), aligned(4), may_alias));
+
+template <int V>
+__device__ inline Raw<float, V> load_raw(const float* p) {
+    Raw<float, V> r;
+    static_assert(V == 1 || V == 4, "16 bytes or one element");
+    if constexpr (V == 4) {
+        const f32x4_e q = *reinterpret_cast<const f32x4_e*>(p);
+        for (int i = 0; i < 4; ++i) r.w[i] = q[i];
+    } else {
+        r.w[0] = *p;
+    }
+    return r;
+}
+template <int V>
+__device__ inline Raw<bf16, V> load_raw(const bf16* p) {
+    Raw<bf16, V> r;
+    static_assert(V == 1 || V == 8, "16 bytes or one element");
+    if constexpr (V == 8) {
+        const u32x4_e q = *reinterpret_cast<const u32x4_e*>(p);
+        for (int i = 0; i < 4; ++i) r.w[i] = q[i];
+    } else {
+        r.w[0] = p->u;
+    }
+    return r;
+}
+
+// two fp32 values rounded to nearest even into one word of bfloat16 (v_cvt_pk_bf16_f32)
+__device__ inline uint32_t pack_bf16(float lo, float hi) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    const b2 v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+template <int V>
+__device__ inline void store_vec(float* p, const float (&v)[V]) {
+    if constexpr (V == 4) {
+        *reinterpret_cast<f32x4_e*>(p) = f32x4_e{v[0], v[1], v[2], v[3]};
+    } else {
+        *p = v[0];
+    }
+}
+template <int V>
+__device__ inline void store_vec(bf16* p, const float (&v)[V]) {
+    if constexpr (V == 8) {
+        *reinterpret_cast<u32x4_e*>(p) =
+            u32x4_e{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+    } else {
+        p->u = (uint16_t)pack_bf16(v[0], 0.f);
+    }
+}
+// V floats at p (any 4-byte alignment)
+template <int V>
+__device__ inline void load_f32(const float* p, float (&v)[V]) {
+    if constexpr (V == 1) {
+        v[0] = *p;
+    } else {
+        for (int i = 0; i < V; i += 4) {
+            const f32x4_e q = *reinterpret_cast<const f32x4_e*>(p + i);
+            for (int j = 0; j < 4; ++j) v[i + j] = q[j];
+        }
+    }
+}
+template <int V>
+__device__ inline void store_f32(float* p, const float (&v)[V]) {
+    if constexpr (V == 1) {
+        *p = v[0];
+    } else {
+        for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<f32x4_e*>(p + i) = f32x4_e{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    }
+}
+
+template <typename T>
+struct Width;  // elements in 16 bytes
+template <>
+struct Width<float> {
+    static constexpr int v = 4;
+};
+template <>
+struct Width<bf16> {
+    static constexpr int v = 8;
+};
+
+// e^x for x <= 0. Where the result is rounded to bfloat16, the hardware exp2 of the rounded product x log2 e, whose
+// relative error of up to |x| 2^-24 is far below half a bfloat16 step; for fp32 results the product's rounding error
+// is carried along (its remainder and log2 e's own low part, to first order), which leaves about 1.5 ulp at any x.
+template <typename T>
+__device__ inline float exp_neg(float x) {
+    constexpr float hi = 1.44269502162933349609f, lo = 1.92596299112661746887e-8f;  // log2 e in two floats
+    if constexpr (sizeof(T) == 2) {
+        return __builtin_amdgcn_exp2f(x * hi);
+    } else {
+        // x = -inf (and every x below exp2's range) gives 0: the remainder, NaN or infinite there, is not used
+        const float t = x * hi;
+        const float r = __builtin_fmaf(x, lo, __builtin_fmaf(x, hi, -t));
+        const float e = __builtin_amdgcn_exp2f(t);
+        return t < -150.f ? e : __builtin_fmaf(e * r, 0.693147180559945309f, e);
+    }
+}
+
+// sigmoid(z) and 1 - sigmoid(z), each from e^-|z| without cancellation: exact 0 and 1 at infinite z
+template <typename T>
+__device__ inline void sigm2(float z, float& s, float& c) {
+    const float e = exp_neg<T>(-fabsf(z));
+    const float r = frcp(1.0f + e);
+    const float q = e * r;
+    s = z >= 0.f ? r : q;
+    c = z >= 0.f ? q : r;
+}
+
+}  // namespace mdl

@@ -7,7 +7,9 @@ and runs scatter -> forward -> direction sum/un-pack, and the backward.
 level re-packed from the previous level's output sizes ("No Padding Please",
 §V-A: packing happens just before each MDLSTM layer). ``CTCHead`` runs the
 model head (height collapse, shared fully-connected layer, CTC loss) on the
-last level's output.
+last level's output. ``SequenceScan`` and ``ScanState`` run the gated linear
+recurrence along the rows or frames of the packed examples, whole sequences
+at once or a token at a time.
 """
 
 from __future__ import annotations
@@ -21,7 +23,7 @@ import torch
 from . import (MDL_BF16, MDL_CELL_LEAKY_LP, MDL_CELL_MDLSTM, MDL_F32, MDL_PACK_ALG1, MDL_PACK_EXACT, MDL_PACK_PADDED, Layout, mdl_backward,
                mdl_blockconv_backward, mdl_blockconv_forward, mdl_blockconv_workspace_size, mdl_dirsum_unpack, mdl_forward, mdl_forward_dirsum,
                mdl_layout_device_size, mdl_layout_rects, mdl_layout_upload, mdl_pack, mdl_pack_level, mdl_scatter, mdl_workspace_size,
-               mdl_ctc_head, mdl_ctc_workspace_size)
+               mdl_ctc_head, mdl_ctc_workspace_size, mdl_scan_backward, mdl_scan_forward, mdl_scan_step, mdl_scan_workspace_size)
 
 
 def _dev(a, device, dtype=torch.float32):
@@ -86,6 +88,18 @@ class DeviceLayout:
         """(heights, widths) of the examples, input order."""
         _, real = mdl_layout_rects(self.layout)
         return real[:, 2].copy(), real[:, 3].copy()
+
+    def row_offsets(self) -> np.ndarray:
+        """Offsets (int64) of every image row of every example in the flat [h][w][K] tensors, as sequences of w
+        tokens: what a SequenceScan along the rows takes."""
+        h, w = self.sizes()
+        return np.concatenate([[0], np.cumsum(np.repeat(w.astype(np.int64), h))])
+
+    def frame_offsets(self) -> np.ndarray:
+        """Offsets (int64) of the examples' frames, one sequence of w tokens per example: the sequences of a
+        height-collapsed [sum w][K] tensor."""
+        _, w = self.sizes()
+        return np.concatenate([[0], np.cumsum(w.astype(np.int64))])
 
     def device_maps(self):
         Hc, Wc = self.layout.Hc, self.layout.Wc
@@ -258,3 +272,134 @@ class CTCHead:
                      self.n_labels, self.max_label, self.loss, self.dy if want_dy else None, dWfc, dbfc, self.ws,
                      self.ws_bytes, stream)
         return self.loss
+
+
+_DTYPES = {"f32": (MDL_F32, torch.float32), "bf16": (MDL_BF16, torch.bfloat16)}
+
+
+def _x_dtype(name: str):
+    if name not in _DTYPES:
+        raise ValueError(f"unknown dtype {name!r}; one of {sorted(_DTYPES)}")
+    return _DTYPES[name]
+
+
+def _device(device) -> torch.device:
+    d = torch.device(device)
+    if d.type == "cuda" and d.index is None:
+        d = torch.device("cuda", torch.cuda.current_device())
+    return d
+
+
+def _rows(name: str, t: torch.Tensor, shape, dtype, device) -> int:
+    """Checks a tensor of rows (any row stride, elements of a row adjacent) and returns its row stride."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: need {shape} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    if shape[0] <= 1 and (shape[1] <= 1 or t.stride(1) == 1):
+        return max(shape[1], 1)
+    if (shape[1] > 1 and t.stride(1) != 1) or t.stride(0) < shape[1]:
+        raise ValueError(f"{name}: need adjacent elements within a row and rows that do not overlap")
+    return t.stride(0)
+
+
+def _same_rows(names, ts, shape, dtype, device) -> int:
+    """_rows of several tensors that share one row stride (column blocks of one matrix, or separate ones); None is
+    left out. A tensor of one row takes any stride."""
+    lds = {_rows(n, t, shape, dtype, device) for n, t in zip(names, ts) if t is not None}
+    if len(lds) != 1:
+        raise ValueError(f"{', '.join(names)}: one row stride for all, got {sorted(lds)}")
+    return lds.pop()
+
+
+def _full(name: str, t: Optional[torch.Tensor], shape, dtype, device):
+    """Checks a contiguous tensor (None passes)."""
+    if t is not None and (t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous()):
+        raise ValueError(f"{name}: need contiguous {shape} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} on "
+                         f"{t.device}")
+
+
+def _here(device: torch.device):
+    if torch.cuda.current_device() != device.index:
+        raise ValueError(f"buffers are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+class SequenceScan:
+    """The gated linear recurrence (mdl_scan_forward / _backward) over the sequences given by `seq_off` among T rows
+    of D channels. seq_off: S + 1 ascending offsets, from the host (checked) or an int64 device tensor (taken as it
+    is). Holds the outputs, the gradients and the workspace: a forward's results stand until the next forward, and a
+    backward belongs to the forward before it."""
+
+    def __init__(self, seq_off, T: int, D: int, x_dtype: str = "f32", reverse: bool = False, device: str = "cuda"):
+        on_device = isinstance(seq_off, torch.Tensor) and seq_off.is_cuda
+        self.device = seq_off.device if on_device else _device(device)
+        if on_device:
+            if seq_off.dtype != torch.int64 or seq_off.dim() != 1 or seq_off.numel() < 2:
+                raise ValueError("seq_off: need S + 1 int64 offsets")
+            self.off = seq_off.contiguous()
+        else:
+            host = np.asarray(seq_off, dtype=np.int64).reshape(-1)
+            if host.size < 2 or host[0] < 0 or host[-1] > T or (np.diff(host) < 0).any():
+                raise ValueError("seq_off: need S + 1 offsets that ascend within [0, T]")
+            self.off = torch.as_tensor(host, device=self.device)
+        self.S, self.T, self.D, self.reverse = int(self.off.numel()) - 1, int(T), int(D), int(bool(reverse))
+        self.x_dtype, self.tdt = _x_dtype(x_dtype)
+        self.ws_bytes = mdl_scan_workspace_size(self.T, self.D, self.x_dtype)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        # zeros: rows in no sequence are never written
+        self.y = torch.zeros(self.T, self.D, dtype=self.tdt, device=self.device)
+        self.hT = torch.empty(self.S, self.D, dtype=torch.float32, device=self.device)
+        self.dzf = self.dg = self.dzo = self.dh0 = None
+
+    def _inputs(self, zf, g, zo, h0):
+        _here(self.device)
+        ldz = _same_rows(("zf", "g", "zo"), (zf, g, zo), (self.T, self.D), self.tdt, self.device)
+        _full("h0", h0, (self.S, self.D), torch.float32, self.device)
+        return ldz
+
+    def forward(self, zf, g, zo=None, h0=None, stream=None):
+        """(y, hT): zf, g, zo [T][D] at one row stride, h0 [S][D] float32."""
+        ldz = self._inputs(zf, g, zo, h0)
+        mdl_scan_forward(self.off, self.S, self.T, self.D, self.x_dtype, self.reverse, zf, g, zo, ldz, h0, self.y,
+                         self.D, self.hT, self.ws, self.ws_bytes, stream)
+        return self.y, self.hT
+
+    def backward(self, zf, g, zo, dy, h0=None, dhT=None, stream=None):
+        """(dzf, dg, dzo, dh0), dzo None without zo and dh0 None without h0, of the forward() just run on the same
+        inputs."""
+        ldz = self._inputs(zf, g, zo, h0)
+        ldy = _rows("dy", dy, (self.T, self.D), self.tdt, self.device)
+        _full("dhT", dhT, (self.S, self.D), torch.float32, self.device)
+        if self.dzf is None:
+            self.dzf, self.dg = torch.zeros_like(self.y), torch.zeros_like(self.y)
+        if zo is not None and self.dzo is None:
+            self.dzo = torch.zeros_like(self.y)
+        if h0 is not None and self.dh0 is None:
+            self.dh0 = torch.empty_like(self.hT)
+        dzo, dh0 = self.dzo if zo is not None else None, self.dh0 if h0 is not None else None
+        mdl_scan_backward(self.off, self.S, self.T, self.D, self.x_dtype, self.reverse, zf, g, zo, ldz, h0, dy, ldy,
+                          dhT, self.dzf, self.dg, dzo, self.D, dh0, self.ws, self.ws_bytes, stream)
+        return self.dzf, self.dg, dzo, dh0
+
+
+class ScanState:
+    """The recurrence's states of n_slots live streams, advanced a token at a time (mdl_scan_step)."""
+
+    def __init__(self, n_slots: int, D: int, x_dtype: str = "f32", device: str = "cuda"):
+        self.device = _device(device)
+        self.n_slots, self.D = int(n_slots), int(D)
+        self.x_dtype, self.tdt = _x_dtype(x_dtype)
+        self.state = torch.zeros(self.n_slots, self.D, dtype=torch.float32, device=self.device)
+        self._y = None
+
+    def step(self, zf, g, zo=None, slots=None, out=None, stream=None):
+        """y [S][D] of one token for each row's slot (slots int32 [S], all different; the first S rows if None). The
+        states advance in place, or into the same rows of `out` ([n_slots][D])."""
+        _here(self.device)
+        S = int(zf.shape[0])
+        ldz = _same_rows(("zf", "g", "zo"), (zf, g, zo), (S, self.D), self.tdt, self.device)
+        _full("slots", slots, (S,), torch.int32, self.device)
+        _full("out", out, (self.n_slots, self.D), torch.float32, self.device)
+        if self._y is None or self._y.shape[0] != S:
+            self._y = torch.zeros(S, self.D, dtype=self.tdt, device=self.device)
+        mdl_scan_step(S, self.D, self.x_dtype, zf, g, zo, ldz, slots, self.n_slots, self.state,
+                      self.state if out is None else out, self._y, self.D, stream)
+        return self._y

@@ -420,12 +420,72 @@ int mdl_ctc_head(const mdl_layout* layout, const void* d_desc, const float* y_fl
                  float* dy_flat, float* dWfc, float* dbfc, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Gated linear recurrence over packed sequences: the leaky update of the
+ * MDL_CELL_LEAKY_LP cell along one axis, with gates that do not read the state,
+ * so that all tokens of a sequence are computed at once. Per channel of a
+ * sequence, in scan order (first token to last, or last to first with reverse):
+ *     f_t = sigmoid(zf_t),  o_t = sigmoid(zo_t)
+ *     h_t = f_t h_{t-1} + (1 - f_t) g_t,   h before the first token = h0 (zero if NULL)
+ *     y_t = o_t h_t                        (y_t = h_t when zo is NULL)
+ * Sequence s holds the tokens [seq_off[s], seq_off[s + 1]) of the tensors'
+ * T rows; seq_off (device, int64, S + 1 entries) ascends within [0, T].
+ * Rows in no sequence (before seq_off[0], from seq_off[S] on) are not written,
+ * and what they hold is not used. A sequence may be empty: its hT is its h0.
+ * The rows of every example of a flat tensor are such sequences (each image row
+ * h_t runs over w tokens), and so are the frames of examples of height 1.
+ * seq_off is read on the device and not validated: with entries that do not
+ * ascend within [0, T] the results are unspecified, but nothing outside the
+ * tensors is read or written.
+ * zf, g, zo: [T][D] of `dtype` at a row stride of ldz >= D elements (column
+ * blocks of one projection); y, dy: row stride ldy. h0, hT: [S][D] float32.
+ * States, their gradients and all sums are float32; a bfloat16 output is
+ * rounded once. Any alignment of the element type is taken.
+ *
+ * mdl_scan_forward writes y and, unless NULL, hT (each sequence's last state in
+ * scan order). ws: >= mdl_scan_workspace_size bytes, 16-byte aligned (may be
+ * NULL where that is 0); it carries what the backward needs and is passed,
+ * unmodified, to the mdl_scan_backward calls that follow with the same seq_off,
+ * S, T, D, dtype, reverse and inputs. It belongs to one such pair at a time:
+ * calls that may overlap need one each.
+ *
+ * mdl_scan_backward: from dy and, unless NULL, dhT (gradient of hT, [S][D]),
+ * with l_t = dL/dh_t = o_t dy_t + f_{t+1} l_{t+1} (dhT at the last token),
+ *     dg = (1 - f) l,  dzf = f (1 - f) (h_{t-1} - g) l,  dzo = dy h o (1 - o),
+ *     dh0 = f l at the first token (dhT for an empty sequence)
+ * dzf, dg, dzo [T][D] at row stride ldd; dzo exactly when zo is given; dh0
+ * [S][D] may be NULL. No output may overlap an input or another output.
+ *
+ * mdl_scan_step: one token for each of S streams (serving). Row i advances the
+ * state row slots[i] (device, int32; i itself if NULL) from h_in to h_out
+ * ([n_slots][D] float32; the same array to update in place) and writes row i
+ * of y. A row whose slot lies outside [0, n_slots) is left out: neither its y
+ * nor any state is written. Slots must differ from each other.
+ *
+ * Errors: MDL_EINVAL for null tensors, S, D < 1, T < 0, a stride below D, an
+ * unknown dtype, dzo without zo or zo without dzo, n_slots < 1, slots NULL with
+ * n_slots < S, or a misaligned workspace; MDL_ESIZE for a short workspace;
+ * MDL_EOVERFLOW when rows times a stride reach 2^60 or the launch 2^31
+ * workgroups. With T = 0 the token tensors may be NULL.
+ */
+int mdl_scan_workspace_size(int64_t T, int32_t D, int32_t dtype, size_t* bytes);
+int mdl_scan_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, int32_t dtype, int32_t reverse,
+                     const void* zf, const void* g, const void* zo, int64_t ldz, const float* h0, void* y,
+                     int64_t ldy, float* hT, void* ws, size_t ws_bytes, void* stream);
+int mdl_scan_backward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, int32_t dtype, int32_t reverse,
+                      const void* zf, const void* g, const void* zo, int64_t ldz, const float* h0, const void* dy,
+                      int64_t ldy, const float* dhT, void* dzf, void* dg, void* dzo, int64_t ldd, float* dh0,
+                      void* ws, size_t ws_bytes, void* stream);
+int mdl_scan_step(int32_t S, int32_t D, int32_t dtype, const void* zf, const void* g, const void* zo, int64_t ldz,
+                  const int32_t* slots, int32_t n_slots, const float* h_in, float* h_out, void* y, int64_t ldy,
+                  void* stream);
+
+/*
  * Kernel timing (measurement support). mdl_timing(1) makes every later launch
  * of a kernel group (names: "build_maps", "scatter", "zero_fill", "projection",
  * "fwd_wavefront", "dirsum_overlap" (on the library's own stream, concurrent with
  * "fwd_wavefront"), "dirsum", "bwd_wavefront", "wgrad_overlap" (on the library's
  * own stream, concurrent with "bwd_wavefront"), "wgrad", "conv_fwd", "conv_bwd",
- * "ctc_head")
+ * "ctc_head", "scan_fwd", "scan_bwd", "scan_step")
  * hand each of its dispatches a HIP event pair that the dispatch itself
  * records (hipExtLaunchKernel): the group's time runs from its first
  * dispatch's start to its last one's end, with no marker packets between

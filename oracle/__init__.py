@@ -15,10 +15,11 @@ Modules:
   leaky      the Leaky-LP cell (lambda gate, two output gates), forward and 2D BPTT (§III, Fig. 4(b), §IX-A)
   blockconv  block-strided convolution with tensor-list chunking (§V-B)
   stack      three MDLSTM levels with block convs, re-packed per level (§II, §V)
+  sequence   the sequence operators: gated linear recurrence, block norms, top-k distillation
 
 Every function is pinned by a ``-m "not gpu"`` test in ``tests/test_oracle_*.py``
 against something other than itself (brute force, closed forms, a library
 routine, finite differences, invariants the pages state).
 """
 
-from . import pack, canvas, mdlstm, leaky, blockconv, stack  # noqa: F401
+from . import pack, canvas, mdlstm, leaky, blockconv, stack, sequence  # noqa: F401

@@ -50,6 +50,7 @@ INFO_KEYS = ("n", "canvas_h", "canvas_w", "rows", "real_pixels", "computed_cells
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
+_F32 = ctypes.c_float
 _SZ = ctypes.c_size_t
 _SIGS = [
     ("mdl_pack", _I32, [_P, _P, _I32, _I32, _I32, _I32, ctypes.POINTER(_P)]),
@@ -86,6 +87,12 @@ _SIGS = [
     ("mdl_scan_backward", _I32, [_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, _P, _P,
                                  _I64, _P, _P, _SZ, _P]),
     ("mdl_scan_step", _I32, [_I32, _I32, _I32, _P, _P, _P, _I64, _P, _I32, _P, _P, _P, _I64, _P]),
+    ("mdl_blocknorm_forward", _I32, [_I64, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _F32, _P, _P, _I64,
+                                     _P]),
+    ("mdl_blocknorm_workspace_size", _I32, [_I64, _I32, _I32, ctypes.POINTER(_SZ)]),
+    ("mdl_blocknorm_backward", _I32, [_I64, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _F32, _P, _P, _I64,
+                                      _P, _P, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
+    ("mdl_distill", _I32, [_I64, _I32, _I32, _I32, _P, _I64, _P, _P, _I32, _P, _F32, _P, _P, _I64, _P]),
     ("mdl_timing", _I32, [_I32]),
     ("mdl_set_wgrad_overlap", _I32, [_I32]),
     ("mdl_timing_only", _I32, [ctypes.c_char_p]),
@@ -356,6 +363,33 @@ def mdl_scan_step(S: int, D: int, dtype: int, zf, g, zo, ldz: int, slots, n_slot
                   stream=None):
     _check(_lib.mdl_scan_step(S, D, dtype, _ptr(zf), _ptr(g), _ptr(zo), ldz, _ptr(slots), n_slots, _ptr(h_in),
                               _ptr(h_out), _ptr(y), ldy, _stream(stream)))
+
+
+def mdl_blocknorm_forward(N: int, D: int, dtype: int, x, ldx: int, z, ldz: int, u, ldu: int, w_post, scale, w_pre,
+                          eps: float, r, v, ldr: int, stream=None):
+    _check(_lib.mdl_blocknorm_forward(N, D, dtype, _ptr(x), ldx, _ptr(z), ldz, _ptr(u), ldu, _ptr(w_post),
+                                      _ptr(scale), _ptr(w_pre), eps, _ptr(r), _ptr(v), ldr, _stream(stream)))
+
+
+def mdl_blocknorm_workspace_size(N: int, D: int, dtype: int) -> int:
+    b = _SZ()
+    _check(_lib.mdl_blocknorm_workspace_size(N, D, dtype, ctypes.byref(b)))
+    return b.value
+
+
+def mdl_blocknorm_backward(N: int, D: int, dtype: int, x, ldx: int, z, ldz: int, u, ldu: int, w_post, scale, w_pre,
+                           eps: float, dr, dv, ldr: int, dx, dz, du, ldd: int, dw_post, dscale, dw_pre, ws,
+                           ws_bytes: int, stream=None):
+    _check(_lib.mdl_blocknorm_backward(N, D, dtype, _ptr(x), ldx, _ptr(z), ldz, _ptr(u), ldu, _ptr(w_post),
+                                       _ptr(scale), _ptr(w_pre), eps, _ptr(dr), _ptr(dv), ldr, _ptr(dx), _ptr(dz),
+                                       _ptr(du), ldd, _ptr(dw_post), _ptr(dscale), _ptr(dw_pre), _ptr(ws), ws_bytes,
+                                       _stream(stream)))
+
+
+def mdl_distill(N: int, V: int, k: int, dtype: int, z, ldz: int, ids, t, t_dtype: int, w, tau: float, loss, dz,
+                ldd: int, stream=None):
+    _check(_lib.mdl_distill(N, V, k, dtype, _ptr(z), ldz, _ptr(ids), _ptr(t), t_dtype, _ptr(w), tau, _ptr(loss),
+                            _ptr(dz), ldd, _stream(stream)))
 
 
 def mdl_set_wgrad_overlap(mode):

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <new>
 #include <map>
@@ -1082,6 +1083,157 @@ int mdl_scan_step(int32_t S, int32_t D, int32_t dtype, const void* zf, const voi
         Timed t("scan_step");
         e = mdl::launch_scan_step(S, D, dtype, zf, g, zo, ldz, slots, n_slots, h_in, h_out, y, ldy,
                                   static_cast<hipStream_t>(stream));
+    }
+    if (e != hipSuccess) return hip_fail(e, F);
+    return MDL_OK;
+    GUARD_END
+}
+
+// ---- the norms before and after a block --------------------------------------------------------------
+static int check_norm(const std::string& F, int64_t N, int32_t D, int32_t dtype) {
+    int rc = check_dtype(F, dtype);
+    if (rc) return rc;
+    if (N < 0 || D < 1) return fail(MDL_EINVAL, F + ": need N >= 0 and D >= 1");
+    if (D > mdl::norm_max_d()) return fail(MDL_EUNSUPPORTED, F + ": D above " + std::to_string(mdl::norm_max_d()));
+    if (N >= (int64_t(1) << 31)) return fail(MDL_EOVERFLOW, F + ": the launch reaches 2^31 workgroups");
+    return MDL_OK;
+}
+static int check_norm_parts(const std::string& F, const mdl::NormArgs& a) {
+    if (a.N > 0 && !a.x) return fail(MDL_EINVAL, F + ": null tensor");
+    if (a.N > 0 && !a.z && (a.u || a.w_post || a.scale))
+        return fail(MDL_EINVAL, F + ": a gate, w_post or scale without z");
+    if (!(a.eps >= 0.f && a.eps < INFINITY)) return fail(MDL_EINVAL, F + ": eps must be finite and >= 0");
+    int rc = check_stride(F, "ldx", a.N, a.D, a.ldx);
+    if (!rc && a.z) rc = check_stride(F, "ldz", a.N, a.D, a.ldz);
+    if (!rc && a.u) rc = check_stride(F, "ldu", a.N, a.D, a.ldu);
+    if (!rc) rc = check_stride(F, "ldr", a.N, a.D, a.ldr);
+    return rc;
+}
+
+int mdl_blocknorm_forward(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx, const void* z, int64_t ldz,
+                          const void* u, int64_t ldu, const float* w_post, const float* scale, const float* w_pre,
+                          float eps, void* r, void* v, int64_t ldr, void* stream) {
+    GUARD_BEGIN
+    const std::string F("mdl_blocknorm_forward");
+    int rc = check_norm(F, N, D, dtype);
+    if (rc) return rc;
+    mdl::NormArgs a{};
+    a.N = N;
+    a.D = D;
+    a.x = x;
+    a.z = z;
+    a.u = u;
+    a.ldx = ldx;
+    a.ldz = ldz;
+    a.ldu = ldu;
+    a.ldr = ldr;
+    a.w_post = w_post;
+    a.scale = scale;
+    a.w_pre = w_pre;
+    a.eps = eps;
+    a.inv_d = 1.f / (float)D;
+    a.r = r;
+    a.v = v;
+    if ((rc = check_norm_parts(F, a))) return rc;
+    if (N > 0) {
+        if ((z == nullptr) != (r == nullptr)) return fail(MDL_EINVAL, F + ": r goes with z, and only with it");
+        if ((w_pre == nullptr) != (v == nullptr)) return fail(MDL_EINVAL, F + ": v goes with w_pre, and only with it");
+        if (!r && !v) return fail(MDL_EINVAL, F + ": nothing to compute");
+    }
+    hipError_t e;
+    {
+        Timed t("norm_fwd");
+        e = mdl::launch_norm_fwd(a, dtype, static_cast<hipStream_t>(stream));
+    }
+    if (e != hipSuccess) return hip_fail(e, F);
+    return MDL_OK;
+    GUARD_END
+}
+
+int mdl_blocknorm_workspace_size(int64_t N, int32_t D, int32_t dtype, size_t* bytes) {
+    GUARD_BEGIN
+    if (!bytes) return fail(MDL_EINVAL, "mdl_blocknorm_workspace_size: null argument");
+    const int rc = check_norm("mdl_blocknorm_workspace_size", N, D, dtype);
+    if (rc) return rc;
+    *bytes = mdl::norm_bwd_ws(N, D, dtype);
+    return MDL_OK;
+    GUARD_END
+}
+
+int mdl_blocknorm_backward(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx, const void* z, int64_t ldz,
+                           const void* u, int64_t ldu, const float* w_post, const float* scale, const float* w_pre,
+                           float eps, const void* dr, const void* dv, int64_t ldr, void* dx, void* dz, void* du,
+                           int64_t ldd, float* dw_post, float* dscale, float* dw_pre, void* ws, size_t ws_bytes,
+                           void* stream) {
+    GUARD_BEGIN
+    const std::string F("mdl_blocknorm_backward");
+    int rc = check_norm(F, N, D, dtype);
+    if (rc) return rc;
+    mdl::NormArgs a{};
+    a.N = N;
+    a.D = D;
+    a.x = x;
+    a.z = z;
+    a.u = u;
+    a.ldx = ldx;
+    a.ldz = ldz;
+    a.ldu = ldu;
+    a.ldr = ldr;
+    a.ldd = ldd;
+    a.w_post = w_post;
+    a.scale = scale;
+    a.w_pre = w_pre;
+    a.eps = eps;
+    a.inv_d = 1.f / (float)D;
+    a.dr = dr;
+    a.dv = dv;
+    a.dx = dx;
+    a.dz = dz;
+    a.du = du;
+    a.part = static_cast<float*>(ws);
+    if ((rc = check_norm_parts(F, a))) return rc;
+    if ((rc = check_stride(F, "ldd", N, D, ldd))) return rc;
+    if (N > 0) {
+        if (!dx) return fail(MDL_EINVAL, F + ": null tensor");
+        if ((z == nullptr) != (dz == nullptr) || (u == nullptr) != (du == nullptr))
+            return fail(MDL_EINVAL, F + ": dz goes with z and du with u, and only with them");
+        if ((w_pre == nullptr) != (dv == nullptr)) return fail(MDL_EINVAL, F + ": dv goes with w_pre, and only with it");
+        if (!dr && !dv) return fail(MDL_EINVAL, F + ": neither dr nor dv");
+    }
+    if ((w_post == nullptr) != (dw_post == nullptr) || (scale == nullptr) != (dscale == nullptr) ||
+        (w_pre == nullptr) != (dw_pre == nullptr))
+        return fail(MDL_EINVAL, F + ": each weight's gradient goes with the weight, and only with it");
+    if ((rc = check_ws(F, "mdl_blocknorm_workspace_size", mdl::norm_bwd_ws(N, D, dtype), ws, ws_bytes))) return rc;
+    hipError_t e;
+    {
+        Timed t("norm_bwd");
+        e = mdl::launch_norm_bwd(a, dtype, dw_post, dscale, dw_pre, static_cast<hipStream_t>(stream));
+    }
+    if (e != hipSuccess) return hip_fail(e, F);
+    return MDL_OK;
+    GUARD_END
+}
+
+// ---- distillation from a teacher's top logits ----------------------------------------------------------
+int mdl_distill(int64_t N, int32_t V, int32_t k, int32_t dtype, const void* z, int64_t ldz, const int32_t* ids,
+                const void* t, int32_t t_dtype, const float* w, float tau, float* loss, void* dz, int64_t ldd,
+                void* stream) {
+    GUARD_BEGIN
+    const std::string F("mdl_distill");
+    int rc = check_dtype(F, dtype);
+    if (rc || (rc = check_dtype(F, t_dtype))) return rc;
+    if (N < 0 || V < 1 || k < 1 || k > V) return fail(MDL_EINVAL, F + ": need N >= 0, V >= 1 and k in [1, V]");
+    if (k > mdl::distill_max_k()) return fail(MDL_EUNSUPPORTED, F + ": k above " + std::to_string(mdl::distill_max_k()));
+    if (N >= (int64_t(1) << 31)) return fail(MDL_EOVERFLOW, F + ": the launch reaches 2^31 workgroups");
+    if (N > 0 && (!z || !ids || !t || !loss)) return fail(MDL_EINVAL, F + ": null tensor");
+    if (!(tau > 0.f && tau < INFINITY)) return fail(MDL_EINVAL, F + ": tau must be finite and positive");
+    if ((rc = check_stride(F, "ldz", N, V, ldz))) return rc;
+    if (dz && (rc = check_stride(F, "ldd", N, V, ldd))) return rc;
+    hipError_t e;
+    {
+        Timed tm("distill");
+        e = mdl::launch_distill(N, V, k, dtype, z, ldz, ids, t, t_dtype, w, tau, loss, dz, ldd,
+                                static_cast<hipStream_t>(stream));
     }
     if (e != hipSuccess) return hip_fail(e, F);
     return MDL_OK;

@@ -1,0 +1,245 @@
+// k_distill.hip — distillation from a teacher's top logits: loss and gradient per frame in one pass.
+//
+// With the teacher's k kept classes id_j and logits t_j, the student's logits z over V classes and a temperature tau:
+//   p = softmax_j(t / tau),  q = softmax(z / tau)
+//   loss = w tau^2 sum_j p_j (ln p_j - ln q_{id_j}),  dz = w tau (q - sum_j p_j [id_j = .])
+// Written with e_j = exp((t_j - max t) / tau), T = sum e, m = max z and L = sum exp((z - m) / tau):
+//   loss / (w tau^2) = (1/T) sum_j e_j ((t_j - max t) - (z_{id_j} - m)) / tau - ln T + ln L.
+//
+// R lanes share a row. A row that fits their registers is read once, kept as it lies in memory, and its gradient is
+// formed from there; longer rows are read twice, the first time with a running maximum and sum. The few kept classes sit
+// in LDS; their gradients are written over the row's after it, by the lanes that own the slots (a class named twice gets
+// both slots' p). Statistics are fp32; the gradient is rounded once.
+#include "kernels.h"
+#include "seqio.h"
+
+namespace mdl {
+
+namespace {
+
+constexpr float kLn2 = 0.693147180559945309f;
+
+template <int V_, int R_, int NV_>
+struct DistillShape {  // elements a vector, lanes a row, vectors a lane (0: the row is read twice)
+    static constexpr int V = V_, R = R_, NV = NV_;
+    static constexpr int threads = R_ > 256 ? R_ : 256;
+    static constexpr int rows = threads / R_;
+};
+
+template <int R>
+__device__ inline void row_sync() {
+    if constexpr (R > 64) {
+        __syncthreads();
+    } else {  // the lanes of one wave: order their LDS and global accesses
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+    }
+}
+// maxima (MAX) or sums of K values over a row's lanes, the same in all of them
+template <int R, int K, bool MAX>
+__device__ inline void row_reduce(float (&s)[K], float* red) {
+    constexpr int W = R < 64 ? R : 64;
+#pragma unroll
+    for (int k = 0; k < K; ++k) s[k] = MAX ? group_max<W>(s[k]) : group_sum<W>(s[k]);
+    if constexpr (R > 64) {
+        const int wave = threadIdx.x >> 6;
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0)
+            for (int k = 0; k < K; ++k) red[wave * K + k] = s[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            s[k] = red[k];
+            for (int w = 1; w < R / 64; ++w) s[k] = MAX ? fmaxf(s[k], red[w * K + k]) : s[k] + red[w * K + k];
+        }
+    }
+}
+
+struct DistillArgs {
+    int64_t N;
+    int V, k;
+    const void* z;
+    int64_t ldz;
+    const int32_t* ids;
+    const void* t;
+    int t_bf16;
+    const float* w;
+    float tau, inv_tau;
+    float* loss;
+    void* dz;
+    int64_t ldd;
+};
+
+// exp of x <= 0 (x = (z - max) / tau): as exp_neg, NaN where the row's maximum is not finite
+template <typename T, typename S>
+__global__ __launch_bounds__(S::threads) void k_distill(DistillArgs a) {
+    constexpr int V = S::V, R = S::R, NV = S::NV > 0 ? S::NV : 1;
+    constexpr bool kTwice = S::NV == 0;
+    __shared__ float red[S::threads / 64 * 5];
+    extern __shared__ float top[];  // [rows][3][k]: class, e_j, z of the class
+    const int lane = threadIdx.x % R, group = threadIdx.x / R;
+    const int64_t row = (int64_t)blockIdx.x * S::rows + group;
+    const bool live = row < a.N;
+    const int64_t n = live ? row : a.N - 1;
+    const T* z = static_cast<const T*>(a.z) + n * a.ldz;
+    int* const cls = reinterpret_cast<int*>(top + (size_t)group * 3 * a.k);
+    float* const ej = top + (size_t)group * 3 * a.k + a.k;
+    float* const zj = ej + a.k;
+
+    // the row: its vectors, each element counted once (a vector moved back from the row's end skips its first ones)
+    Raw<T, V> q[NV];
+    const int full = a.V / V, tail = full * V;
+    float mx = -INFINITY, run = 0.f;
+    if constexpr (!kTwice) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) q[i] = load_raw<V>(z + min((lane + i * R) * V, a.V - V));
+    } else {
+        // running maximum and sum of a lane's elements
+        auto take = [&](float x) {
+            if (x > mx) {
+                run = run * exp_neg<T>((mx - x) * a.inv_tau) + 1.f;
+                mx = x;
+            } else {
+                run += x == mx ? 1.f : exp_neg<T>((x - mx) * a.inv_tau);
+            }
+        };
+        for (int i = lane; i < full; i += R) {
+            const Raw<T, V> r = load_raw<V>(z + (int64_t)i * V);
+#pragma unroll
+            for (int v = 0; v < V; ++v) take(r[v]);
+        }
+        for (int i = tail + lane; i < a.V; i += R) take(load_raw<1>(z + i)[0]);
+    }
+    // the kept classes
+    float m2[2] = {mx, -INFINITY};
+    float kept = 0.f, bad = 0.f;
+    for (int j = lane; j < a.k; j += R) {
+        int c = a.ids[n * a.k + j];
+        const float t = a.t_bf16 ? load_raw<1>(static_cast<const bf16*>(a.t) + n * a.k + j)[0]
+                                 : static_cast<const float*>(a.t)[n * a.k + j];
+        const bool ok = c >= 0 && c < a.V;
+        kept += ok ? 1.f : 0.f;
+        bad += !ok && c != -1 ? 1.f : 0.f;
+        cls[j] = ok ? c : -1;
+        ej[j] = t;
+        zj[j] = ok ? load_raw<1>(z + c)[0] : 0.f;
+        if (ok) m2[1] = fmaxf(m2[1], t);
+    }
+    if constexpr (!kTwice) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) m2[0] = fmaxf(m2[0], q[i][v]);
+    }
+    row_reduce<R, 2, true>(m2, red);
+    const float m = m2[0], tm = m2[1];
+    float s[5] = {0.f, 0.f, 0.f, kept, bad};  // L, T, sum e_j (...), kept classes, classes that do not exist
+    if constexpr (!kTwice) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + i * R) * V, skip = c - min(c, a.V - V);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float e = exp_neg<T>((q[i][v] - m) * a.inv_tau);
+                s[0] += v >= skip ? e : 0.f;
+            }
+        }
+    } else {
+        s[0] = mx == m ? run : run * exp_neg<T>((mx - m) * a.inv_tau);
+    }
+    for (int j = lane; j < a.k; j += R) {
+        if (cls[j] < 0) {
+            ej[j] = 0.f;
+            continue;
+        }
+        const float d = ej[j] - tm, e = exp_neg<float>(d * a.inv_tau);
+        s[1] += e;
+        if (e > 0.f || e != e) s[2] += e * ((d - (zj[j] - m)) * a.inv_tau);
+        ej[j] = e;
+    }
+    row_reduce<R, 5, false>(s, red);
+    const float w = a.w ? a.w[n] : 1.f;
+    const bool counts = s[3] > 0.f && s[4] == 0.f && w != 0.f;
+    const float inv_l = 1.f / s[0], inv_t = 1.f / s[1];
+    if (live && lane == 0) {
+        const float kl = s[2] * inv_t - __builtin_amdgcn_logf(s[1]) * kLn2 + __builtin_amdgcn_logf(s[0]) * kLn2;
+        a.loss[n] = s[4] > 0.f ? NAN : counts ? w * a.tau * a.tau * kl : 0.f;
+    }
+    if (!a.dz) return;
+    const float g = counts ? w * a.tau : 0.f, gl = g * inv_l;
+    T* const dz = static_cast<T*>(a.dz) + n * a.ldd;
+    auto grad = [&](float x) { return counts ? exp_neg<T>((x - m) * a.inv_tau) * gl : 0.f; };
+    row_sync<R>();  // the row and its kept classes have been read: dz may be z
+    if constexpr (!kTwice) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + i * R) * V;
+            float o[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] = grad(q[i][v]);
+            if (live && c < a.V) store_vec<V>(dz + min(c, a.V - V), o);
+        }
+    } else {
+        for (int i = lane; i < full; i += R) {
+            const Raw<T, V> r = load_raw<V>(z + (int64_t)i * V);
+            float o[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] = grad(r[v]);
+            if (live) store_vec<V>(dz + (int64_t)i * V, o);
+        }
+        for (int i = tail + lane; i < a.V; i += R) {
+            const float o[1] = {grad(load_raw<1>(z + i)[0])};
+            if (live) store_vec<1>(dz + i, o);
+        }
+    }
+    row_sync<R>();  // the row's stores come before those of its kept classes
+    if (!live || !counts) return;
+    for (int j = lane; j < a.k; j += R) {
+        const int c = cls[j];
+        if (c < 0) continue;
+        float p = 0.f;
+        for (int i = 0; i < a.k; ++i) p += cls[i] == c ? ej[i] : 0.f;
+        const float o[1] = {grad(zj[j]) - g * (p * inv_t)};
+        store_vec<1>(dz + c, o);
+    }
+}
+
+template <typename F>
+void with_shape(int64_t V_, int dtype, F&& fn) {
+    auto go = [&](auto ty) {
+        using T = decltype(ty);
+        constexpr int V = Width<T>::v;
+        const int64_t nv = (V_ + V - 1) / V;
+        if (V_ < V) return fn(ty, DistillShape<1, 8, 1>{});
+        if (nv <= 16) return fn(ty, DistillShape<V, 16, 1>{});
+        if (nv <= 64) return fn(ty, DistillShape<V, 64, 1>{});
+        if (nv <= 256) return fn(ty, DistillShape<V, 64, 4>{});
+        if (nv <= 1024) return fn(ty, DistillShape<V, 256, 4>{});
+        if (nv <= 4096) return fn(ty, DistillShape<V, 1024, 4>{});
+        if (nv <= 8192) return fn(ty, DistillShape<V, 1024, 8>{});
+        if (nv <= 16384) return fn(ty, DistillShape<V, 1024, 16>{});
+        return fn(ty, DistillShape<V, 1024, 0>{});
+    };
+    if (dtype == 1) go(bf16{});
+    else go(float{});
+}
+
+}  // namespace
+
+int distill_max_k() { return 1024; }
+
+hipError_t launch_distill(int64_t N, int V, int k, int dtype, const void* z, int64_t ldz, const int32_t* ids,
+                          const void* t, int t_dtype, const float* w, float tau, float* loss, void* dz, int64_t ldd,
+                          hipStream_t st) {
+    if (N == 0) return hipSuccess;
+    const DistillArgs a{N, V, k, z, ldz, ids, t, t_dtype == 1, w, tau, 1.f / tau, loss, dz, ldd};
+    with_shape(V, dtype, [&](auto ty, auto sh) {
+        using S = decltype(sh);
+        launch(k_distill<decltype(ty), S>, dim3((unsigned)((N + S::rows - 1) / S::rows)), dim3(S::threads),
+               sizeof(float) * 3 * k * S::rows, st, a);
+    });
+    return hipGetLastError();
+}
+
+}  // namespace mdl

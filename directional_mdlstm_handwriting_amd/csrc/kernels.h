@@ -332,4 +332,30 @@ hipError_t launch_scan_step(int S, int D, int dtype, const void* zf, const void*
                             const int32_t* slots, int n_slots, const float* h_in, float* h_out, void* y, int64_t ldy,
                             hipStream_t st);
 
+// the norms before and after a block (k_norm.hip)
+struct NormArgs {
+    int64_t N;
+    int D;
+    const void *x, *z, *u;      // [N][D]; z and u may be null
+    int64_t ldx, ldz, ldu, ldr; // ldr: r, v, dr, dv
+    const float *w_post, *scale, *w_pre;  // [D] or null
+    float eps, inv_d;
+    void *r, *v;
+    const void *dr, *dv;
+    void *dx, *dz, *du;
+    int64_t ldd;
+    float* part;                // [workgroups][2][D] column sums
+};
+int norm_max_d();
+size_t norm_bwd_ws(int64_t N, int D, int dtype);
+hipError_t launch_norm_fwd(const NormArgs& a, int dtype, hipStream_t st);
+hipError_t launch_norm_bwd(const NormArgs& a, int dtype, float* dw_post, float* dscale, float* dw_pre,
+                           hipStream_t st);
+
+// distillation from a teacher's top logits (k_distill.hip)
+int distill_max_k();
+hipError_t launch_distill(int64_t N, int V, int k, int dtype, const void* z, int64_t ldz, const int32_t* ids,
+                          const void* t, int t_dtype, const float* w, float tau, float* loss, void* dz, int64_t ldd,
+                          hipStream_t st);
+
 }  // namespace mdl

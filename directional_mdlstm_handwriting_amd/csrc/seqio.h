@@ -141,4 +141,37 @@ __device__ inline void sigm2(float z, float& s, float& c) {
     c = z >= 0.f ? q : r;
 }
 
+// Sum over each group of R neighbouring lanes (R a power of two up to 64), the same bits in every lane of the group:
+// rotations inside rows of 16 lanes (v_add with a DPP operand), then exchanges between rows.
+template <int CTRL>
+__device__ inline float dpp_add(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int R>
+__device__ inline float group_sum(float v) {
+    constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+    if constexpr (R >= 2) v = dpp_add<kQuadXor1>(v);
+    if constexpr (R >= 4) v = dpp_add<kQuadXor2>(v);
+    if constexpr (R >= 8) v = dpp_add<kHalfMirror>(v);   // lane i with 7 - i: the other quad, whose sums are equal
+    if constexpr (R >= 16) v = dpp_add<kMirror>(v);      // lane i with 15 - i: the other half row
+    if constexpr (R >= 32) v += __shfl_xor(v, 16);
+    if constexpr (R >= 64) v += __shfl_xor(v, 32);
+    return v;
+}
+template <int CTRL>
+__device__ inline float dpp_max(float v) {
+    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true)));
+}
+template <int R>
+__device__ inline float group_max(float v) {
+    constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+    if constexpr (R >= 2) v = dpp_max<kQuadXor1>(v);
+    if constexpr (R >= 4) v = dpp_max<kQuadXor2>(v);
+    if constexpr (R >= 8) v = dpp_max<kHalfMirror>(v);
+    if constexpr (R >= 16) v = dpp_max<kMirror>(v);
+    if constexpr (R >= 32) v = fmaxf(v, __shfl_xor(v, 16));
+    if constexpr (R >= 64) v = fmaxf(v, __shfl_xor(v, 32));
+    return v;
+}
+
 }  // namespace mdl

@@ -9,7 +9,8 @@ level re-packed from the previous level's output sizes ("No Padding Please",
 model head (height collapse, shared fully-connected layer, CTC loss) on the
 last level's output. ``SequenceScan`` and ``ScanState`` run the gated linear
 recurrence along the rows or frames of the packed examples, whole sequences
-at once or a token at a time.
+at once or a token at a time; ``BlockNorm`` the norms around such a block with
+its gate and residual; ``TopKDistill`` the distillation loss of its logits.
 """
 
 from __future__ import annotations
@@ -23,7 +24,8 @@ import torch
 from . import (MDL_BF16, MDL_CELL_LEAKY_LP, MDL_CELL_MDLSTM, MDL_F32, MDL_PACK_ALG1, MDL_PACK_EXACT, MDL_PACK_PADDED, Layout, mdl_backward,
                mdl_blockconv_backward, mdl_blockconv_forward, mdl_blockconv_workspace_size, mdl_dirsum_unpack, mdl_forward, mdl_forward_dirsum,
                mdl_layout_device_size, mdl_layout_rects, mdl_layout_upload, mdl_pack, mdl_pack_level, mdl_scatter, mdl_workspace_size,
-               mdl_ctc_head, mdl_ctc_workspace_size, mdl_scan_backward, mdl_scan_forward, mdl_scan_step, mdl_scan_workspace_size)
+               mdl_ctc_head, mdl_ctc_workspace_size, mdl_scan_backward, mdl_scan_forward, mdl_scan_step, mdl_scan_workspace_size,
+               mdl_blocknorm_backward, mdl_blocknorm_forward, mdl_blocknorm_workspace_size, mdl_distill)
 
 
 def _dev(a, device, dtype=torch.float32):
@@ -403,3 +405,78 @@ class ScanState:
         mdl_scan_step(S, self.D, self.x_dtype, zf, g, zo, ldz, slots, self.n_slots, self.state,
                       self.state if out is None else out, self._y, self.D, stream)
         return self._y
+
+
+class BlockNorm:
+    """The norms before and after a block over N rows of D channels, with the block's gate and scaled residual
+    (mdl_blocknorm_forward / _backward). Weights are the caller's, [D] float32. Holds outputs and gradients: a call's
+    results stand until the next call of the same method."""
+
+    def __init__(self, N: int, D: int, x_dtype: str = "f32", eps: float = 1e-6, device: str = "cuda"):
+        self.device = _device(device)
+        self.N, self.D, self.eps = int(N), int(D), float(eps)
+        self.x_dtype, self.tdt = _x_dtype(x_dtype)
+        self.ws_bytes = mdl_blocknorm_workspace_size(self.N, self.D, self.x_dtype)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self._bufs = {}
+
+    def _out(self, name, wanted, weight=False):
+        if not wanted:
+            return None
+        if name not in self._bufs:
+            shape, dt = ((self.D,), torch.float32) if weight else ((self.N, self.D), self.tdt)
+            self._bufs[name] = torch.empty(shape, dtype=dt, device=self.device)
+        return self._bufs[name]
+
+    def _inputs(self, x, z, u, w_post, scale, w_pre):
+        _here(self.device)
+        lds = [_rows(n, t, (self.N, self.D), self.tdt, self.device) if t is not None else 0
+               for n, t in (("x", x), ("z", z), ("u", u))]
+        for n, t in (("w_post", w_post), ("scale", scale), ("w_pre", w_pre)):
+            _full(n, t, (self.D,), torch.float32, self.device)
+        return lds
+
+    def forward(self, x, z=None, u=None, w_post=None, scale=None, w_pre=None, stream=None):
+        """(r, v): r is x itself without z, v None without w_pre."""
+        ldx, ldz, ldu = self._inputs(x, z, u, w_post, scale, w_pre)
+        r, v = self._out("r", z is not None), self._out("v", w_pre is not None)
+        mdl_blocknorm_forward(self.N, self.D, self.x_dtype, x, ldx, z, ldz, u, ldu, w_post, scale, w_pre, self.eps, r,
+                              v, self.D, stream)
+        return (x if z is None else r), v
+
+    def backward(self, x, z, u, w_post, scale, w_pre, dr, dv, stream=None):
+        """(dx, dz, du, dw_post, dscale, dw_pre), None where the input is."""
+        ldx, ldz, ldu = self._inputs(x, z, u, w_post, scale, w_pre)
+        _full("dr", dr, (self.N, self.D), self.tdt, self.device)
+        _full("dv", dv, (self.N, self.D), self.tdt, self.device)
+        out = [self._out(n, t is not None) for n, t in (("dx", x), ("dz", z), ("du", u))]
+        out += [self._out(n, t is not None, True) for n, t in (("dw_post", w_post), ("dscale", scale), ("dw_pre", w_pre))]
+        mdl_blocknorm_backward(self.N, self.D, self.x_dtype, x, ldx, z, ldz, u, ldu, w_post, scale, w_pre, self.eps,
+                               dr, dv, self.D, *out[:3], self.D, *out[3:], self.ws, self.ws_bytes, stream)
+        return tuple(out)
+
+
+class TopKDistill:
+    """Distillation loss of N frames over V classes from a teacher's k kept logits (mdl_distill): the loss per frame
+    and its gradient in one call. Holds both; they stand until the next call."""
+
+    def __init__(self, N: int, V: int, k: int, x_dtype: str = "f32", tau: float = 1.0, device: str = "cuda"):
+        self.device = _device(device)
+        self.N, self.V, self.k, self.tau = int(N), int(V), int(k), float(tau)
+        self.x_dtype, self.tdt = _x_dtype(x_dtype)
+        self.loss = torch.empty(self.N, dtype=torch.float32, device=self.device)
+        self.dz = torch.empty(self.N, self.V, dtype=self.tdt, device=self.device)
+
+    def run(self, z, ids, t, w=None, want_dz: bool = True, stream=None):
+        """(loss [N], dz [N][V] or None): z [N][V] at any row stride, ids int32 and t (float32 or bfloat16) [N][k],
+        w [N] float32 or None."""
+        _here(self.device)
+        ldz = _rows("z", z, (self.N, self.V), self.tdt, self.device)
+        _full("ids", ids, (self.N, self.k), torch.int32, self.device)
+        t_dtype = "bf16" if t.dtype == torch.bfloat16 else "f32"
+        _full("t", t, (self.N, self.k), _DTYPES[t_dtype][1], self.device)
+        _full("w", w, (self.N,), torch.float32, self.device)
+        dz = self.dz if want_dz else None
+        mdl_distill(self.N, self.V, self.k, self.x_dtype, z, ldz, ids, t, _DTYPES[t_dtype][0], w, self.tau, self.loss,
+                    dz, self.V, stream)
+        return self.loss, dz

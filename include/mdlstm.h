@@ -480,12 +480,76 @@ int mdl_scan_step(int32_t S, int32_t D, int32_t dtype, const void* zf, const voi
                   void* stream);
 
 /*
+ * The norms before and after a block, fused with the block's gate and the
+ * scaled residual, over N rows of D channels: x the residual stream, z the
+ * block's output, u the pre-activation of its gate,
+ *     r = x + scale * sigmoid(u) * w_post * z / sqrt(mean(z^2) + eps)
+ *     v = w_pre * r / sqrt(mean(r^2) + eps)      (what the next block reads)
+ * Each part can be left out: z NULL (then u, w_post, scale and r are NULL too:
+ * r is x, only the norm before a block), u NULL (no gate), w_post or scale NULL
+ * (ones), w_pre and v NULL (after the last block). x, z, u, r, v, dr, dv are
+ * [N][D] of `dtype`; row strides in elements: ldx (x), ldz (z), ldu (u), ldr
+ * (r, v, dr, dv), ldd (dx, dz, du); ldz and ldu are ignored without z and u.
+ * Weights and their gradients are [D] float32. Row and column sums are float32;
+ * v is formed from r before r's rounding; each output is rounded once. Any
+ * alignment of the element type is taken.
+ * mdl_blocknorm_backward, from dr and dv (gradients of r and v; one of them may
+ * be NULL: dv exactly when w_pre is, dr where nothing else reads r): dx; dz and
+ * du exactly when z and u are given; dw_post, dscale, dw_pre, each exactly when
+ * its weight is. The weight gradients are fixed-order sums over the rows
+ * (workgroup sums added in order). ws: >= mdl_blocknorm_workspace_size bytes,
+ * 16-byte aligned, contents not kept. With N = 0 the row tensors may be NULL
+ * and the weight gradients are zero.
+ * An output may be an input of the same row at the same address and stride (r
+ * over x, dx over dr); other overlaps are not allowed.
+ * Errors: MDL_EINVAL for null tensors or parts that do not go together, N < 0,
+ * D < 1, a stride below D, an unknown dtype, eps that is not finite and >= 0,
+ * or a misaligned workspace; MDL_EUNSUPPORTED for D > 16384; MDL_EOVERFLOW when
+ * rows times a stride reach 2^60 or the launch 2^31 workgroups; MDL_ESIZE for a
+ * short workspace.
+ */
+int mdl_blocknorm_forward(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx, const void* z, int64_t ldz,
+                          const void* u, int64_t ldu, const float* w_post, const float* scale, const float* w_pre,
+                          float eps, void* r, void* v, int64_t ldr, void* stream);
+int mdl_blocknorm_workspace_size(int64_t N, int32_t D, int32_t dtype, size_t* bytes);
+int mdl_blocknorm_backward(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx, const void* z, int64_t ldz,
+                           const void* u, int64_t ldu, const float* w_post, const float* scale, const float* w_pre,
+                           float eps, const void* dr, const void* dv, int64_t ldr, void* dx, void* dz, void* du,
+                           int64_t ldd, float* dw_post, float* dscale, float* dw_pre, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/*
+ * Distillation from a teacher's top logits: loss and gradient per frame. Row n
+ * of z [N][V] (`dtype`, row stride ldz) holds the student's logits over V
+ * classes, ids [N][k] (int32) and t [N][k] (t_dtype) the k classes that were
+ * kept of the teacher's and their logits; with the temperature tau
+ *     p = softmax over the kept classes of t / tau,  q = softmax of z / tau
+ *     loss[n] = w[n] tau^2 sum_j p_j (ln p_j - ln q_{id_j})     (KL(p || q))
+ *     dz[n]   = w[n] tau (q - sum_j p_j [id_j = .])             (d loss[n] / dz)
+ * w [N] float32 (NULL: ones) weights a frame in the loss; dz (row stride ldd)
+ * may be NULL, or z itself at the same stride. id -1 marks an empty slot. A row
+ * whose slots are all empty, or of weight 0, counts for nothing, whatever z
+ * holds: loss 0, gradient 0. Any other id outside [0, V) gives loss NaN and
+ * gradient 0 (found on the device). A class named twice counts with both
+ * probabilities. A kept logit of -inf has p = 0 and adds nothing. Statistics
+ * and loss are float32; the gradient is rounded once. No workspace.
+ * Errors: MDL_EINVAL for null tensors, N < 0, V < 1, k outside [1, V], a stride
+ * below V, an unknown dtype, or tau that is not finite and positive;
+ * MDL_EUNSUPPORTED for k > 1024; MDL_EOVERFLOW when rows times a stride reach
+ * 2^60 or the launch 2^31 workgroups.
+ */
+int mdl_distill(int64_t N, int32_t V, int32_t k, int32_t dtype, const void* z, int64_t ldz, const int32_t* ids,
+                const void* t, int32_t t_dtype, const float* w, float tau, float* loss, void* dz, int64_t ldd,
+                void* stream);
+
+/*
  * Kernel timing (measurement support). mdl_timing(1) makes every later launch
  * of a kernel group (names: "build_maps", "scatter", "zero_fill", "projection",
  * "fwd_wavefront", "dirsum_overlap" (on the library's own stream, concurrent with
  * "fwd_wavefront"), "dirsum", "bwd_wavefront", "wgrad_overlap" (on the library's
  * own stream, concurrent with "bwd_wavefront"), "wgrad", "conv_fwd", "conv_bwd",
- * "ctc_head", "scan_fwd", "scan_bwd", "scan_step")
+ * "ctc_head", "scan_fwd", "scan_bwd", "scan_step", "norm_fwd", "norm_bwd",
+ * "distill")
  * hand each of its dispatches a HIP event pair that the dispatch itself
  * records (hipExtLaunchKernel): the group's time runs from its first
  * dispatch's start to its last one's end, with no marker packets between

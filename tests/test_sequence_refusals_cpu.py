@@ -68,3 +68,54 @@ def test_scan_workspace_sizes():
     assert _code(M.mdl_scan_workspace_size, 1 << 50, 8, M.MDL_F32) == M.MDL_EOVERFLOW
     assert _code(M.mdl_scan_workspace_size, 5, 0, M.MDL_F32) == M.MDL_EINVAL
     assert _code(M.mdl_scan_workspace_size, 5, 8, 3) == M.MDL_EINVAL
+
+
+NORM_F = dict(N=10, D=8, dtype=M.MDL_F32, x=P, ldx=8, z=P, ldz=8, u=P, ldu=8, w_post=P, scale=P, w_pre=P, eps=1e-6, r=P,
+              v=P, ldr=8, stream=0)
+NORM_B = dict(N=10, D=8, dtype=M.MDL_F32, x=P, ldx=8, z=P, ldz=8, u=P, ldu=8, w_post=P, scale=P, w_pre=P, eps=1e-6,
+              dr=P, dv=P, ldr=8, dx=P, dz=P, du=P, ldd=8, dw_post=P, dscale=P, dw_pre=P, ws=P, ws_bytes=BIG, stream=0)
+DISTILL = dict(N=10, V=80, k=8, dtype=M.MDL_F32, z=P, ldz=80, ids=P, t=P, t_dtype=M.MDL_F32, w=P, tau=2.0, loss=P, dz=P,
+               ldd=80, stream=0)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(x=None), M.MDL_EINVAL), (dict(z=None), M.MDL_EINVAL), (dict(r=None), M.MDL_EINVAL),
+    (dict(v=None), M.MDL_EINVAL), (dict(w_pre=None), M.MDL_EINVAL), (dict(N=-1), M.MDL_EINVAL),
+    (dict(D=0), M.MDL_EINVAL), (dict(dtype=5), M.MDL_EINVAL), (dict(ldx=7), M.MDL_EINVAL), (dict(ldz=0), M.MDL_EINVAL),
+    (dict(ldu=7), M.MDL_EINVAL), (dict(ldr=7), M.MDL_EINVAL), (dict(eps=-1.0), M.MDL_EINVAL),
+    (dict(eps=float("nan")), M.MDL_EINVAL), (dict(eps=float("inf")), M.MDL_EINVAL),
+    (dict(z=None, u=None, w_post=None, scale=None, r=None, w_pre=None, v=None), M.MDL_EINVAL),
+    (dict(D=16385, ldx=16385, ldz=16385, ldu=16385, ldr=16385), M.MDL_EUNSUPPORTED),
+    (dict(N=1 << 31), M.MDL_EOVERFLOW), (dict(ldx=1 << 59), M.MDL_EOVERFLOW),
+])
+def test_blocknorm_forward_refuses(change, code):
+    assert _code(M.mdl_blocknorm_forward, **_with(NORM_F, **change)) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(dx=None), M.MDL_EINVAL), (dict(dz=None), M.MDL_EINVAL), (dict(du=None), M.MDL_EINVAL),
+    (dict(dv=None), M.MDL_EINVAL), (dict(dw_post=None), M.MDL_EINVAL), (dict(dscale=None), M.MDL_EINVAL),
+    (dict(dw_pre=None), M.MDL_EINVAL), (dict(scale=None), M.MDL_EINVAL), (dict(ldd=7), M.MDL_EINVAL),
+    (dict(ws=None), M.MDL_EINVAL), (dict(ws=P + 8), M.MDL_EINVAL), (dict(ws_bytes=8), M.MDL_ESIZE),
+    (dict(w_pre=None, dw_pre=None, dv=None, dr=None), M.MDL_EINVAL),
+])
+def test_blocknorm_backward_refuses(change, code):
+    assert _code(M.mdl_blocknorm_backward, **_with(NORM_B, **change)) == code
+
+
+def test_blocknorm_workspace_sizes():
+    assert M.mdl_blocknorm_workspace_size(1000, 8, M.MDL_F32) > 0
+    assert _code(M.mdl_blocknorm_workspace_size, 10, 20000, M.MDL_F32) == M.MDL_EUNSUPPORTED
+    assert _code(M.mdl_blocknorm_workspace_size, -1, 8, M.MDL_F32) == M.MDL_EINVAL
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(z=None), M.MDL_EINVAL), (dict(ids=None), M.MDL_EINVAL), (dict(t=None), M.MDL_EINVAL),
+    (dict(loss=None), M.MDL_EINVAL), (dict(N=-1), M.MDL_EINVAL), (dict(V=0), M.MDL_EINVAL), (dict(k=0), M.MDL_EINVAL),
+    (dict(k=81), M.MDL_EINVAL), (dict(dtype=2), M.MDL_EINVAL), (dict(t_dtype=2), M.MDL_EINVAL),
+    (dict(tau=0.0), M.MDL_EINVAL), (dict(tau=-1.0), M.MDL_EINVAL), (dict(tau=float("nan")), M.MDL_EINVAL),
+    (dict(tau=float("inf")), M.MDL_EINVAL), (dict(ldz=79), M.MDL_EINVAL), (dict(ldd=79), M.MDL_EINVAL),
+    (dict(V=5000, ldz=5000, ldd=5000, k=1025), M.MDL_EUNSUPPORTED), (dict(N=1 << 31), M.MDL_EOVERFLOW),
+])
+def test_distill_refuses(change, code):
+    assert _code(M.mdl_distill, **_with(DISTILL, **change)) == code

@@ -11,8 +11,8 @@
 // start inside a tile is a map that ignores its argument, written A = -1 (A is a product of sigmoids otherwise).
 // A thread owns V channels (16 bytes of a row) and NT consecutive tokens; the 256 / CL threads of one channel vector
 // hold the tile's successive token groups. Thread maps meet in LDS, where one thread per channel chains them.
-// The tile maps are joined over time per channel, and the second pass over the data applies the joined states.
-// All states, maps and sums are fp32; a stream of bfloat16 is rounded once, as it is stored.
+// The tiles' maps are handed from tile to tile in the same launch (see look_back), so every stream is read and written
+// once. All states, maps and sums are fp32; a stream of bfloat16 is rounded once, as it is stored.
 #include "kernels.h"
 #include "seqio.h"
 
@@ -114,13 +114,65 @@ __device__ inline Tile tile_of(const ScanArgs& a, int64_t linear, int tt, int cb
     return {(linear / a.ncb) * tt, (int)(linear % a.ncb) * cb};
 }
 
-// Forward. PART: the tile's map into a.words; otherwise the states from the tile's incoming state in a.carry.
-template <typename T, int V, int CL, int NT, bool PART>
+// The tiles' maps are handed on through a.words [ntiles][slots], one 64-bit word (A, B) per tile and channel, cleared to
+// kEmpty before the launch: a tile first stores its own map, and, once it knows its incoming state, the state it ends
+// in as a map that ignores its argument. A tile looks at the words of its last kWindow predecessors, one thread per
+// channel, until the nearest state and all maps after it are there, and chains from that state on. States are always
+// the same chain of multiply-adds, wherever a tile found the nearest one, so the results do not depend on timing. Words
+// are loaded and stored whole by relaxed device-scope atomics and carry all that is handed on: no other memory has to
+// be ordered with them.
+// Every wait ends: tiles are taken in ticket order, in which a tile comes after all that it waits for, so the earliest
+// unfinished tile is held by a running workgroup and waits for none.
+constexpr uint64_t kEmpty = ~uint64_t(0);
+constexpr int kWindow = 8;
+__device__ inline uint64_t pack_map(float A, float B) {
+    if (A != A) A = __uint_as_float(0x7fc00000u);  // no NaN is taken for an empty word
+    return (uint64_t)__float_as_uint(B) << 32 | __float_as_uint(A);
+}
+__device__ inline void put_word(uint64_t* p, float A, float B) {
+    __hip_atomic_store(p, pack_map(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// the state (or gradient) that enters tile number `tile` of the chain: word k lies at w + k stride
+__device__ inline float look_back(const uint64_t* w, int64_t tile, int64_t stride) {
+    while (true) {
+        uint64_t m[kWindow];
+#pragma unroll
+        for (int i = 0; i < kWindow; ++i) {
+            const int64_t k = tile - 1 - i;
+            m[i] = k >= 0 ? __hip_atomic_load(w + k * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                          : (uint64_t)__float_as_uint(kReset);  // before the first tile: state 0
+        }
+        bool known = false;
+        float h = 0.f;
+#pragma unroll
+        for (int i = kWindow - 1; i >= 0; --i) {
+            const float A = __uint_as_float((uint32_t)m[i]), B = __uint_as_float((uint32_t)(m[i] >> 32));
+            const bool state = A < 0.f;
+            h = state ? B : __builtin_fmaf(A, h, B);
+            known = m[i] != kEmpty && (state || known);
+        }
+        if (known) return h;
+        __builtin_amdgcn_s_sleep(2);
+    }
+}
+// the workgroup's tile number in the launch: by ticket where tiles wait for each other
+__device__ inline int64_t take_tile(const ScanArgs& a, int* shared) {
+    if (a.ntiles == 1) return blockIdx.x;
+    if (threadIdx.x == 0) *shared = 1 + atomicAdd(a.ticket, 1);  // cleared to -1 like the words
+    __syncthreads();
+    const int t = *shared;
+    __syncthreads();
+    return t;
+}
+
+template <typename T, int V, int CL, int NT>
 __global__ __launch_bounds__(SCAN_THREADS) void k_scan_fwd(ScanArgs a) {
     constexpr int G = SCAN_THREADS / CL, TT = G * NT, CB = CL * V;
+    static_assert(CB <= SCAN_THREADS, "one thread per channel");
     __shared__ int start[TT], last[TT];
     __shared__ f32x2 maps[G][CB];
-    const Tile tile = tile_of(a, blockIdx.x, TT, CB);
+    const int64_t linear = take_tile(a, start);
+    const Tile tile = tile_of(a, linear, TT, CB);
     Share<V, CL, NT> me(a, tile);
     Raw<T, V> rf[NT], rg[NT], ro[NT];
 #pragma unroll
@@ -128,10 +180,10 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_fwd(ScanArgs a) {
         const int64_t t = me.token(a, i);
         rf[i] = load_raw<V>(static_cast<const T*>(a.zf) + t * a.ldz + me.ch);
         rg[i] = load_raw<V>(static_cast<const T*>(a.g) + t * a.ldz + me.ch);
-        if (!PART && a.zo) ro[i] = load_raw<V>(static_cast<const T*>(a.zo) + t * a.ldz + me.ch);
+        if (a.zo) ro[i] = load_raw<V>(static_cast<const T*>(a.zo) + t * a.ldz + me.ch);
     }
     me.bounds(a);
-    mark_tile<TT, CB>(a, tile, start, last, a.h0, PART ? nullptr : a.hT);
+    mark_tile<TT, CB>(a, tile, start, last, a.h0, a.hT);
     float f[NT][V], b[NT][V], A[V], B[V];
     unsigned reset = 0;
 #pragma unroll
@@ -165,219 +217,239 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_fwd(ScanArgs a) {
             A[v] = A[v] * f[i][v];
         }
     }
+    const int col = (threadIdx.x % CL) * V;
 #pragma unroll
-    for (int v = 0; v < V; ++v) maps[me.group][(threadIdx.x % CL) * V + v] = f32x2{reset ? kReset : A[v], B[v]};
+    for (int v = 0; v < V; ++v) maps[me.group][col + v] = f32x2{reset ? kReset : A[v], B[v]};
     __syncthreads();
-    const int64_t slot = (int64_t)blockIdx.x * CB;
-    for (int c = threadIdx.x; c < CB; c += SCAN_THREADS) {
-        if constexpr (PART) {
+    if (threadIdx.x < CB) {
+        const int c = threadIdx.x;
+        float h = 0.f;
+        if (a.ntiles > 1) {
+            const int64_t k = linear / a.ncb, slot = tile.c0 + c;
             float ta = 1.f, tb = 0.f;
-            for (int k = 0; k < G; ++k) {
-                const f32x2 m = maps[k][c];
+#pragma unroll 8
+            for (int j = 0; j < G; ++j) {
+                const f32x2 m = maps[j][c];
                 tb = apply_map(m[0], m[1], tb);
                 ta = m[0] < 0.f || ta < 0.f ? kReset : ta * m[0];
             }
-            a.words[slot + c] = f32x2{ta, tb};
-        } else {
-            float h = a.carry ? a.carry[slot + c] : 0.f;
-            for (int k = 0; k < G; ++k) {
-                const f32x2 m = maps[k][c];
-                maps[k][c][1] = h;
-                h = apply_map(m[0], m[1], h);
-            }
+            uint64_t* const w = a.words + slot;
+            put_word(w + k * a.slots, ta, tb);
+            h = look_back(w, k, a.slots);
+            if (!(ta < 0.f)) put_word(w + k * a.slots, kReset, __builtin_fmaf(ta, h, tb));
+            a.carry[k * a.slots + slot] = h;
+        }
+#pragma unroll 8
+        for (int j = 0; j < G; ++j) {
+            const f32x2 m = maps[j][c];
+            maps[j][c][1] = h;
+            h = apply_map(m[0], m[1], h);
         }
     }
-    if constexpr (!PART) {
-        __syncthreads();
-        float h[V];
+    __syncthreads();
+    float h[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = maps[me.group][(threadIdx.x % CL) * V + v][1];
+    for (int v = 0; v < V; ++v) h[v] = maps[me.group][col + v][1];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const bool r = reset >> i & 1;
-            float y[V];
+    for (int i = 0; i < NT; ++i) {
+        const bool r = reset >> i & 1;
+        float y[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                h[v] = r ? b[i][v] : __builtin_fmaf(f[i][v], h[v], b[i][v]);
-                y[v] = h[v];
-                if (a.zo) {
-                    float s, c;
-                    sigm2<T>(ro[i][v], s, c);
-                    y[v] *= s;
-                }
+        for (int v = 0; v < V; ++v) {
+            h[v] = r ? b[i][v] : __builtin_fmaf(f[i][v], h[v], b[i][v]);
+            y[v] = h[v];
+            if (a.zo) {
+                float s, c;
+                sigm2<T>(ro[i][v], s, c);
+                y[v] *= s;
             }
-            if (me.active && (me.inside >> i & 1)) {
-                store_vec<V>(static_cast<T*>(a.y) + me.token(a, i) * a.ldy + me.ch, y);
-                const int en = last[me.group * NT + i];
-                if (en && a.hT) store_f32<V>(a.hT + (int64_t)(en - 1) * a.D + me.ch, h);
-            }
+        }
+        if (me.active && (me.inside >> i & 1)) {
+            store_vec<V>(static_cast<T*>(a.y) + me.token(a, i) * a.ldy + me.ch, y);
+            const int en = last[me.group * NT + i];
+            if (en && a.hT) store_f32<V>(a.hT + (int64_t)(en - 1) * a.D + me.ch, h);
         }
     }
 }
 
-// Backward. PART: the tile's map of the reverse recurrence into a.words; otherwise the gradients, from the tile's
-// incoming state in a.carry and the later tiles' gradient in a.dcarry.
-template <typename T, int V, int CL, int NT, bool PART>
+// Backward: the tile's states again from its incoming one in a.carry, and the reverse recurrence, whose tiles are
+// chained from the last to the first. Gates stay encoded (sigm_enc) between the passes over the registers.
+template <typename T, int V, int CL, int NT>
 __global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd(ScanArgs a) {
     constexpr int G = SCAN_THREADS / CL, TT = G * NT, CB = CL * V;
+    static_assert(CB <= SCAN_THREADS, "one thread per channel");
     __shared__ int start[TT], last[TT];
     __shared__ f32x2 maps[G][CB], rmaps[G][CB];
-    const Tile tile = tile_of(a, blockIdx.x, TT, CB);
+    const int64_t ticket = take_tile(a, start);
+    // the chain's k-th tile is the k-th from the end
+    const int64_t k = ticket / a.ncb, linear = (a.ntiles - 1 - k) * a.ncb + ticket % a.ncb;
+    const Tile tile = tile_of(a, linear, TT, CB);
     Share<V, CL, NT> me(a, tile);
     Raw<T, V> rf[NT], rg[NT], ro[NT], rd[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const int64_t t = me.token(a, i);
         rf[i] = load_raw<V>(static_cast<const T*>(a.zf) + t * a.ldz + me.ch);
-        if (!PART) rg[i] = load_raw<V>(static_cast<const T*>(a.g) + t * a.ldz + me.ch);
+        rg[i] = load_raw<V>(static_cast<const T*>(a.g) + t * a.ldz + me.ch);
         if (a.zo) ro[i] = load_raw<V>(static_cast<const T*>(a.zo) + t * a.ldz + me.ch);
         rd[i] = load_raw<V>(static_cast<const T*>(a.dy) + t * a.ldy + me.ch);
     }
     me.bounds(a);
-    mark_tile<TT, CB>(a, tile, start, last, a.dhT, PART ? nullptr : a.dh0);
+    mark_tile<TT, CB>(a, tile, start, last, a.dhT, a.dh0);
     unsigned reset = 0, ends = 0;
+    float qf[NT][V], qo[NT][V];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        if (!(me.inside >> i & 1)) continue;
-        if (start[me.group * NT + i]) reset |= 1u << i;
-        if (last[me.group * NT + i]) ends |= 1u << i;
-    }
-    // f of token i, and the gradient it receives from its own output
-    float f[NT][V], l[NT][V], A[V], B[V];
+        const bool in = me.inside >> i & 1;
+        if (in && start[me.group * NT + i]) reset |= 1u << i;
+        if (in && last[me.group * NT + i]) ends |= 1u << i;
+        if (!in) {  // a token of no sequence: state and gradient pass through, nothing enters
+            rg[i] = Raw<T, V>{};
+            rd[i] = Raw<T, V>{};
+        }
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        A[v] = 1.f;
-        B[v] = 0.f;
+        for (int v = 0; v < V; ++v) {
+            qf[i][v] = in ? sigm_enc<T>(rf[i][v]) : kSigmOne;
+            qo[i][v] = a.zo && in ? sigm_enc<T>(ro[i][v]) : kSigmOne;
+        }
     }
+    // a sequence's incoming state at its first token, and the gradient of its last state at its last: rare, so read
+    // where they are needed
+    auto first_state = [&](int i, float(&h)[V]) {
+        if ((reset >> i & 1)) {
+            if (a.h0) load_f32<V>(a.h0 + (int64_t)(start[me.group * NT + i] - 1) * a.D + me.ch, h);
+            else
+#pragma unroll
+                for (int v = 0; v < V; ++v) h[v] = 0.f;
+        }
+    };
+    auto last_grad = [&](int i, float(&d)[V]) {
+        if ((ends >> i & 1)) {
+            if (a.dhT) load_f32<V>(a.dhT + (int64_t)(last[me.group * NT + i] - 1) * a.D + me.ch, d);
+            else
+#pragma unroll
+                for (int v = 0; v < V; ++v) d[v] = 0.f;
+        }
+    };
+    // decoded gates are not kept from one pass over the registers to the next (they would double its registers)
+    auto forget = [&] {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) asm volatile("" : "+v"(qf[i][v]), "+v"(qo[i][v]));
+    };
+    const int col = (threadIdx.x % CL) * V;
+    float A[V], h[V] = {}, d[V] = {};
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = 1.f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        first_state(i, h);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float f, c;
+            sigm_dec(qf[i][v], f, c);
+            h[v] = __builtin_fmaf(f, h[v], c * rg[i][v]);
+            A[v] *= f;
+        }
+    }
+    forget();
 #pragma unroll
     for (int i = NT - 1; i >= 0; --i) {
-        const bool in = me.inside >> i & 1, en = ends >> i & 1;
-        float extra[V] = {};
-        if (en && a.dhT) load_f32<V>(a.dhT + (int64_t)(last[me.group * NT + i] - 1) * a.D + me.ch, extra);
+        last_grad(i, d);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float s, c, so = 1.f, co;
-            sigm2<T>(rf[i][v], s, c);
-            if (a.zo) sigm2<T>(ro[i][v], so, co);
-            f[i][v] = in ? s : 1.f;
-            l[i][v] = in ? __builtin_fmaf(so, rd[i][v], extra[v]) : 0.f;
-            B[v] = f[i][v] * (en ? l[i][v] : l[i][v] + B[v]);
-            A[v] = A[v] * f[i][v];
+            float f, c, so, co;
+            sigm_dec(qf[i][v], f, c);
+            sigm_dec(qo[i][v], so, co);
+            d[v] = f * __builtin_fmaf(so, rd[i][v], d[v]);
         }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) rmaps[me.group][(threadIdx.x % CL) * V + v] = f32x2{ends ? kReset : A[v], B[v]};
-    float b[NT][V];
-    if constexpr (!PART) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            A[v] = 1.f;
-            B[v] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const bool in = me.inside >> i & 1, r = reset >> i & 1;
-            float h[V] = {};
-            if (r && a.h0) load_f32<V>(a.h0 + (int64_t)(start[me.group * NT + i] - 1) * a.D + me.ch, h);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float s, c;
-                sigm2<T>(rf[i][v], s, c);
-                b[i][v] = in ? c * rg[i][v] : 0.f;
-                B[v] = __builtin_fmaf(f[i][v], r ? h[v] : B[v], b[i][v]);
-                A[v] = A[v] * f[i][v];
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) maps[me.group][(threadIdx.x % CL) * V + v] = f32x2{reset ? kReset : A[v], B[v]};
+    for (int v = 0; v < V; ++v) {
+        maps[me.group][col + v] = f32x2{reset ? kReset : A[v], h[v]};
+        rmaps[me.group][col + v] = f32x2{ends ? kReset : A[v], d[v]};
     }
     __syncthreads();
-    const int64_t slot = (int64_t)blockIdx.x * CB;
-    for (int c = threadIdx.x; c < CB; c += SCAN_THREADS) {
-        if constexpr (PART) {
+    // one thread per channel chains the reverse maps, another the forward ones (the same where CB = 256)
+    if (threadIdx.x < CB) {
+        const int c = threadIdx.x;
+        float x = 0.f;
+        if (a.ntiles > 1) {
+            const int64_t slot = tile.c0 + c;
             float ta = 1.f, tb = 0.f;
-            for (int k = G - 1; k >= 0; --k) {
-                const f32x2 m = rmaps[k][c];
+#pragma unroll 8
+            for (int j = G - 1; j >= 0; --j) {
+                const f32x2 m = rmaps[j][c];
                 tb = apply_map(m[0], m[1], tb);
                 ta = m[0] < 0.f || ta < 0.f ? kReset : ta * m[0];
             }
-            a.words[slot + c] = f32x2{ta, tb};
-        } else {
-            float h = a.carry ? a.carry[slot + c] : 0.f, d = a.dcarry ? a.dcarry[slot + c] : 0.f;
-            for (int k = 0; k < G; ++k) {
-                const f32x2 m = maps[k][c];
-                maps[k][c][1] = h;
-                h = apply_map(m[0], m[1], h);
-            }
-            for (int k = G - 1; k >= 0; --k) {
-                const f32x2 m = rmaps[k][c];
-                rmaps[k][c][1] = d;
-                d = apply_map(m[0], m[1], d);
-            }
+            uint64_t* const w = a.words + slot;
+            put_word(w + k * a.slots, ta, tb);
+            x = look_back(w, k, a.slots);
+            if (!(ta < 0.f)) put_word(w + k * a.slots, kReset, __builtin_fmaf(ta, x, tb));
+        }
+#pragma unroll 8
+        for (int j = G - 1; j >= 0; --j) {
+            const f32x2 m = rmaps[j][c];
+            rmaps[j][c][1] = x;
+            x = apply_map(m[0], m[1], x);
         }
     }
-    if constexpr (!PART) {
-        __syncthreads();
-        float h[V], d[V], prev[NT][V];
+    constexpr int kSecond = CB <= SCAN_THREADS / 2 ? SCAN_THREADS / 2 : 0;
+    if (threadIdx.x >= kSecond && threadIdx.x < kSecond + CB) {
+        const int c = threadIdx.x - kSecond;
+        float x = a.ntiles > 1 ? a.carry[linear / a.ncb * a.slots + tile.c0 + c] : 0.f;
+#pragma unroll 8
+        for (int j = 0; j < G; ++j) {
+            const f32x2 m = maps[j][c];
+            maps[j][c][1] = x;
+            x = apply_map(m[0], m[1], x);
+        }
+    }
+    __syncthreads();
+    forget();
+    float prev[NT][V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        h[v] = maps[me.group][col + v][1];
+        d[v] = rmaps[me.group][col + v][1];
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        first_state(i, h);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            h[v] = maps[me.group][(threadIdx.x % CL) * V + v][1];
-            d[v] = rmaps[me.group][(threadIdx.x % CL) * V + v][1];
-        }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            float h0[V] = {};
-            const bool r = reset >> i & 1;
-            if (r && a.h0) load_f32<V>(a.h0 + (int64_t)(start[me.group * NT + i] - 1) * a.D + me.ch, h0);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                prev[i][v] = r ? h0[v] : h[v];
-                h[v] = __builtin_fmaf(f[i][v], prev[i][v], b[i][v]);
-            }
-        }
-#pragma unroll
-        for (int i = NT - 1; i >= 0; --i) {
-            const bool en = ends >> i & 1;
-            float dzf[V], dg[V], dzo[V], dp[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float s, c;
-                sigm2<T>(rf[i][v], s, c);
-                const float lam = en ? l[i][v] : l[i][v] + d[v];
-                dg[v] = c * lam;
-                dzf[v] = s * dg[v] * (prev[i][v] - rg[i][v]);
-                if (a.zo) {
-                    float so, co;
-                    sigm2<T>(ro[i][v], so, co);
-                    const float hv = __builtin_fmaf(f[i][v], prev[i][v], b[i][v]);
-                    dzo[v] = rd[i][v] * hv * so * co;
-                }
-                dp[v] = f[i][v] * lam;
-                d[v] = dp[v];
-            }
-            if (me.active && (me.inside >> i & 1)) {
-                const int64_t o = me.token(a, i) * a.ldd + me.ch;
-                store_vec<V>(static_cast<T*>(a.dzf) + o, dzf);
-                store_vec<V>(static_cast<T*>(a.dg) + o, dg);
-                if (a.zo) store_vec<V>(static_cast<T*>(a.dzo) + o, dzo);
-                if ((reset >> i & 1) && a.dh0)
-                    store_f32<V>(a.dh0 + (int64_t)(start[me.group * NT + i] - 1) * a.D + me.ch, dp);
-            }
+            float f, c;
+            sigm_dec(qf[i][v], f, c);
+            prev[i][v] = h[v];
+            h[v] = __builtin_fmaf(f, h[v], c * rg[i][v]);
         }
     }
-}
-
-// the tiles' maps chained over time, one thread per channel slot: each tile's incoming value into out
-__global__ __launch_bounds__(256) void k_scan_join(const f32x2* __restrict__ words, float* __restrict__ out,
-                                                   int64_t ntiles, int64_t slots, int backwards) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= slots) return;
-    float h = 0.f;
-    for (int64_t k = 0; k < ntiles; ++k) {
-        const int64_t i = (backwards ? ntiles - 1 - k : k) * slots + c;
-        const f32x2 m = words[i];
-        out[i] = h;
-        h = apply_map(m[0], m[1], h);
+    forget();
+#pragma unroll
+    for (int i = NT - 1; i >= 0; --i) {
+        float dzf[V], dg[V], dzo[V];
+        last_grad(i, d);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float f, c, so, co;
+            sigm_dec(qf[i][v], f, c);
+            sigm_dec(qo[i][v], so, co);
+            const float g = rg[i][v], own = so * rd[i][v], lam = own + d[v];
+            dg[v] = c * lam;
+            dzf[v] = f * dg[v] * (prev[i][v] - g);
+            dzo[v] = own * co * __builtin_fmaf(f, prev[i][v], c * g);
+            d[v] = f * lam;
+        }
+        if (me.active && (me.inside >> i & 1)) {
+            const int64_t o = me.token(a, i) * a.ldd + me.ch;
+            store_vec<V>(static_cast<T*>(a.dzf) + o, dzf);
+            store_vec<V>(static_cast<T*>(a.dg) + o, dg);
+            if (a.zo) store_vec<V>(static_cast<T*>(a.dzo) + o, dzo);
+            if ((reset >> i & 1) && a.dh0)
+                store_f32<V>(a.dh0 + (int64_t)(start[me.group * NT + i] - 1) * a.D + me.ch, d);
+        }
     }
 }
 
@@ -434,13 +506,12 @@ __global__ __launch_bounds__(256) void k_scan_step(int S, int D, const T* __rest
     }
 }
 
-// the tile shape for a row: a vector of 16 bytes a lane (one element where the row is shorter), as many lanes along
-// the row as it fills, at most 16
+// the tile shape for a row: V channels a thread (one where the row is shorter), as many lanes along the row as it
+// fills, at most 16; forward and backward have the same
 template <typename F>
 void with_shape(int D, int dtype, F&& fn) {
     auto go = [&](auto ty) {
-        using T = decltype(ty);
-        constexpr int V = Width<T>::v;
+        constexpr int V = 4;
         if (D < V) return fn(ty, ScanShape<1, 8, 4>{});
         const int lanes = (D + V - 1) / V;
         if (lanes <= 4) return fn(ty, ScanShape<V, 4, 4>{});
@@ -458,17 +529,13 @@ ScanPlan scan_plan(int64_t T, int D, int dtype) {
     with_shape(D, dtype, [&](auto, auto sh) {
         using S = decltype(sh);
         const int64_t cb = S::CL * S::V, tt = (int64_t)(SCAN_THREADS / S::CL) * S::NT;
-        p.tt = (int)tt;
         p.ncb = (int)((D + cb - 1) / cb);
         p.slots = p.ncb * cb;
         p.ntiles = (T + tt - 1) / tt;
     });
     if (p.ntiles > 1) {
-        auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
-        p.carry = 0;
-        p.dcarry = up(p.ntiles * p.slots * 4);
-        p.words = p.dcarry + up(p.ntiles * p.slots * 4);
-        p.total = p.words + up(p.ntiles * p.slots * 8);
+        p.carry = p.ntiles * p.slots * 8 + 16;
+        p.total = p.carry + p.ntiles * p.slots * 4;
     }
     return p;
 }
@@ -485,24 +552,22 @@ static hipError_t scan_run(ScanArgs a, int dtype, void* ws, bool backward, hipSt
     const ScanPlan p = scan_plan(a.T, a.D, dtype);
     a.ncb = p.ncb;
     a.ntiles = p.ntiles;
-    uint8_t* w = static_cast<uint8_t*>(ws);
+    a.slots = p.slots;
     if (p.ntiles > 1) {
+        uint8_t* w = static_cast<uint8_t*>(ws);
+        a.words = reinterpret_cast<uint64_t*>(w);
+        a.ticket = reinterpret_cast<int32_t*>(w + p.carry - 16);
         a.carry = reinterpret_cast<float*>(w + p.carry);
-        a.dcarry = reinterpret_cast<float*>(w + p.dcarry);
-        a.words = reinterpret_cast<f32x2*>(w + p.words);
+        // words and ticket: all bits set
+        const hipError_t e = launch_fill_i32(reinterpret_cast<int32_t*>(w), (int64_t)(p.carry / 4), -1, st);
+        if (e != hipSuccess) return e;
     }
     const dim3 grid((unsigned)(p.ntiles * p.ncb)), block(SCAN_THREADS);
     with_shape(a.D, dtype, [&](auto ty, auto sh) {
         using T = decltype(ty);
         using S = decltype(sh);
-        if (p.ntiles > 1) {
-            if (backward) launch(k_scan_bwd<T, S::V, S::CL, S::NT, true>, grid, block, 0, st, a);
-            else launch(k_scan_fwd<T, S::V, S::CL, S::NT, true>, grid, block, 0, st, a);
-            launch(k_scan_join, dim3((unsigned)((p.slots + 255) / 256)), dim3(256), 0, st, a.words,
-                   backward ? a.dcarry : a.carry, p.ntiles, p.slots, backward ? 1 : 0);
-        }
-        if (backward) launch(k_scan_bwd<T, S::V, S::CL, S::NT, false>, grid, block, 0, st, a);
-        else launch(k_scan_fwd<T, S::V, S::CL, S::NT, false>, grid, block, 0, st, a);
+        if (backward) launch(k_scan_bwd<T, S::V, S::CL, S::NT>, grid, block, 0, st, a);
+        else launch(k_scan_fwd<T, S::V, S::CL, S::NT>, grid, block, 0, st, a);
     });
     return hipGetLastError();
 }

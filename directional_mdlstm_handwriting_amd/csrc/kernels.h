@@ -300,7 +300,6 @@ hipError_t launch_ctc_head(const Dev& D, const float* y_flat, int H, const float
                            hipStream_t st);
 
 // the gated linear recurrence over packed sequences (k_scan.hip)
-typedef float scan_f2 __attribute__((ext_vector_type(2)));
 struct ScanArgs {
     const int64_t* off;           // [S + 1] first token of each sequence
     int S, D, reverse;
@@ -313,17 +312,19 @@ struct ScanArgs {
     // set by the launchers
     int ncb = 0;                  // channel blocks
     int64_t ntiles = 0;
-    float *carry = nullptr, *dcarry = nullptr;  // [ntiles][slots] state entering a tile, gradient entering it
-    scan_f2* words = nullptr;                   // [ntiles][slots] the tiles' maps
+    int64_t slots = 0;            // channels of all blocks
+    float* carry = nullptr;       // [ntiles][slots] state entering each tile: the forward's, for the backward
+    uint64_t* words = nullptr;    // [ntiles][slots] the tiles' maps as they are handed on
+    int32_t* ticket = nullptr;
 };
 template <int V_, int CL_, int NT_>
 struct ScanShape {  // channels a thread, lanes along the row, tokens a thread
     static constexpr int V = V_, CL = CL_, NT = NT_;
 };
 struct ScanPlan {
-    int tt = 0, ncb = 0;
+    int ncb = 0;
     int64_t ntiles = 0, slots = 0;
-    size_t carry = 0, dcarry = 0, words = 0, total = 0;  // byte offsets into the workspace
+    size_t carry = 0, total = 0;  // workspace bytes: words and ticket up to carry, then the tiles' incoming states
 };
 ScanPlan scan_plan(int64_t T, int D, int dtype);
 hipError_t launch_scan_fwd(const ScanArgs& a, int dtype, void* ws, hipStream_t st);

@@ -29,6 +29,7 @@ struct Raw<bf16, V> {
     }
 };
 
+typedef uint32_t u32x2_e __attribute__((ext_vector_type(2), aligned(2), may_alias));
 typedef uint32_t u32x4_e __attribute__((ext_vector_type(4), aligned(2), may_alias));
 typedef float f32x4_e __attribute__((ext_vector_type(4), aligned(4), may_alias));
 
@@ -47,10 +48,13 @@ __device__ inline Raw<float, V> load_raw(const float* p) {
 template <int V>
 __device__ inline Raw<bf16, V> load_raw(const bf16* p) {
     Raw<bf16, V> r;
-    static_assert(V == 1 || V == 8, "16 bytes or one element");
+    static_assert(V == 1 || V == 4 || V == 8, "16 or 8 bytes, or one element");
     if constexpr (V == 8) {
         const u32x4_e q = *reinterpret_cast<const u32x4_e*>(p);
         for (int i = 0; i < 4; ++i) r.w[i] = q[i];
+    } else if constexpr (V == 4) {
+        const u32x2_e q = *reinterpret_cast<const u32x2_e*>(p);
+        for (int i = 0; i < 2; ++i) r.w[i] = q[i];
     } else {
         r.w[0] = p->u;
     }
@@ -77,6 +81,8 @@ __device__ inline void store_vec(bf16* p, const float (&v)[V]) {
     if constexpr (V == 8) {
         *reinterpret_cast<u32x4_e*>(p) =
             u32x4_e{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+    } else if constexpr (V == 4) {
+        *reinterpret_cast<u32x2_e*>(p) = u32x2_e{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     } else {
         p->u = (uint16_t)pack_bf16(v[0], 0.f);
     }
@@ -173,5 +179,20 @@ __device__ inline float group_max(float v) {
     if constexpr (R >= 64) v = fmaxf(v, __shfl_xor(v, 32));
     return v;
 }
+
+// sigmoid(z) and 1 - sigmoid(z) in one register: the smaller of the two, its sign bit set where that is 1 - sigmoid
+template <typename T>
+__device__ inline float sigm_enc(float z) {
+    const float e = exp_neg<T>(-fabsf(z));
+    const float q = e * frcp(1.0f + e);
+    return z >= 0.f ? -q : q;
+}
+__device__ inline void sigm_dec(float q, float& s, float& c) {
+    const float t = fabsf(q), o = 1.f - t;
+    const bool neg = (int)__float_as_uint(q) < 0;
+    s = neg ? o : t;
+    c = neg ? t : o;
+}
+constexpr float kSigmOne = -0.f;  // sigmoid 1
 
 }  // namespace mdl

@@ -276,22 +276,27 @@ __global__ __launch_bounds__(S::threads) void k_norm_bwd(NormArgs a) {
     }
 }
 
-// the weight gradients from the workgroups' column sums, in workgroup order: 64 columns by 4 threads a column
-__global__ __launch_bounds__(256) void k_norm_wreduce(const float* __restrict__ part, int nb, int D,
-                                                      const float* __restrict__ w_post,
-                                                      const float* __restrict__ scale, float* __restrict__ dw_post,
-                                                      float* __restrict__ dscale, float* __restrict__ dw_pre) {
-    __shared__ float red[4][64];
-    const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
-    const int i = blockIdx.x * 64 + lane;
+// the weight gradients from the workgroups' column sums: 16 columns by 64 threads a column, thread g adding workgroups
+// g, g + 64, ... in order, then the 64 sums pairwise
+constexpr int kWredCols = 16, kWredGroups = 64;
+__global__ __launch_bounds__(kWredCols * kWredGroups) void k_norm_wreduce(
+    const float* __restrict__ part, int nb, int D, const float* __restrict__ w_post, const float* __restrict__ scale,
+    float* __restrict__ dw_post, float* __restrict__ dscale, float* __restrict__ dw_pre) {
+    __shared__ float red[kWredGroups][kWredCols];
+    const int lane = threadIdx.x % kWredCols, g = threadIdx.x / kWredCols;
+    const int i = blockIdx.x * kWredCols + lane;
     float s = 0.f;
     if (i < 2 * D) {
-        for (int b = g; b < nb; b += 4) s += part[(int64_t)b * 2 * D + i];
+#pragma unroll 4
+        for (int b = g; b < nb; b += kWredGroups) s += part[(int64_t)b * 2 * D + i];
     }
     red[g][lane] = s;
-    __syncthreads();
+    for (int h = kWredGroups / 2; h > 0; h >>= 1) {
+        __syncthreads();
+        if (g < h) red[g][lane] += red[g + h][lane];
+    }
     if (g || i >= 2 * D) return;
-    for (int k = 1; k < 4; ++k) s += red[k][lane];
+    s = red[0][lane];
     if (i >= D) {
         if (dw_pre) dw_pre[i - D] = s;
         return;
@@ -352,7 +357,7 @@ hipError_t launch_norm_bwd(const NormArgs& a, int dtype, float* dw_post, float* 
         const size_t lds = S::rows > 1 ? sizeof(float) * S::threads * S::NV * S::V : 0;
         launch(k_norm_bwd<decltype(ty), S>, dim3(nb), dim3(S::threads), lds, st, a);
         if (dw_post || dscale || dw_pre)
-            launch(k_norm_wreduce, dim3((2 * a.D + 63) / 64), dim3(256), 0, st, a.part, nb, a.D, a.w_post, a.scale,
+            launch(k_norm_wreduce, dim3((2 * a.D + kWredCols - 1) / kWredCols), dim3(kWredCols * kWredGroups), 0, st, a.part, nb, a.D, a.w_post, a.scale,
                    dw_post, dscale, dw_pre);
     });
     return hipGetLastError();

@@ -54,16 +54,36 @@ struct Tile {
 
 // Sequence marks of the tile's positions: start[p] / last[p] hold sequence + 1 where position p0 + p is a sequence's
 // first / last in scan order, 0 elsewhere. Sequences without tokens hand `from` to `to` ([S][D], zero if null).
+template <int TT>
+__device__ inline void tile_tokens(const ScanArgs& a, int64_t p0, int64_t& t0, int64_t& t1) {  // tokens [t0, t1)
+    t1 = a.reverse ? a.T - p0 : min(p0 + TT, a.T);
+    t0 = a.reverse ? max<int64_t>(a.T - p0 - TT, 0) : p0;
+}
+// the first sequence that may hold tokens of [t0, ...): the one before the first that starts there
+__device__ inline int first_sequence(const ScanArgs& a, int64_t t0) {
+    return max(lower_bound_wave(a.off, a.S, t0) - 1, 0);
+}
+// a thread's sequence of the tile: read before the tile's rows, so that it does not wait for them
+struct Seq {
+    int64_t s, b, e;
+    __device__ inline Seq(const ScanArgs& a, int first) : s(first + (int64_t)threadIdx.x), b(0), e(0) { read(a); }
+    __device__ inline void read(const ScanArgs& a) {
+        if (s < a.S) {
+            b = a.off[s];
+            e = a.off[s + 1];
+        }
+    }
+};
 template <int TT, int CB>
-__device__ inline void mark_tile(const ScanArgs& a, Tile t, int* start, int* last, const float* from, float* to) {
+__device__ inline void mark_tile(const ScanArgs& a, Tile t, Seq q, int* start, int* last, const float* from,
+                                 float* to) {
     for (int i = threadIdx.x; i < TT; i += SCAN_THREADS) start[i] = last[i] = 0;
-    const int64_t t1 = a.reverse ? a.T - t.p0 : min(t.p0 + TT, a.T);      // tokens [t0, t1) of the tile
-    const int64_t t0 = a.reverse ? max<int64_t>(a.T - t.p0 - TT, 0) : t.p0;
+    int64_t t0, t1;
+    tile_tokens<TT>(a, t.p0, t0, t1);
     const bool final_tile = t1 >= a.T;
-    const int sa = max(lower_bound_wave(a.off, a.S, t0) - 1, 0);
     __syncthreads();
-    for (int64_t s = sa + (int)threadIdx.x; s < a.S; s += SCAN_THREADS) {
-        const int64_t b = a.off[s], e = a.off[s + 1];
+    for (; q.s < a.S; q.s += SCAN_THREADS, q.read(a)) {
+        const int64_t s = q.s, b = q.b, e = q.e;
         if (b >= t1 && !final_tile) break;
         if (e <= b) {
             // by the tile that holds the offset, the last one for offsets at the end
@@ -110,8 +130,8 @@ struct Share {
     }
 };
 
-__device__ inline Tile tile_of(const ScanArgs& a, int64_t linear, int tt, int cb) {
-    return {(linear / a.ncb) * tt, (int)(linear % a.ncb) * cb};
+__device__ inline Tile tile_of(const ScanArgs& a, int linear, int tt, int cb) {
+    return {(int64_t)(linear / a.ncb) * tt, linear % a.ncb * cb};
 }
 
 // The tiles' maps are handed on through a.words [ntiles][slots], one 64-bit word (A, B) per tile and channel, cleared to
@@ -131,6 +151,13 @@ __device__ inline uint64_t pack_map(float A, float B) {
 }
 __device__ inline void put_word(uint64_t* p, float A, float B) {
     __hip_atomic_store(p, pack_map(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// A tile's map handed on by other waves than those that look back (a wave's loads wait for its stores before them): the
+// state, if it is there already, stays.
+__device__ inline void offer_word(uint64_t* p, float A, float B) {
+    uint64_t want = kEmpty;
+    __hip_atomic_compare_exchange_strong(p, &want, pack_map(A, B), __ATOMIC_RELAXED, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
 }
 // the state (or gradient) that enters tile number `tile` of the chain: word k lies at w + k stride
 __device__ inline float look_back(const uint64_t* w, int64_t tile, int64_t stride) {
@@ -156,24 +183,48 @@ __device__ inline float look_back(const uint64_t* w, int64_t tile, int64_t strid
     }
 }
 // the workgroup's tile number in the launch: by ticket where tiles wait for each other
-__device__ inline int64_t take_tile(const ScanArgs& a, int* shared) {
+__device__ inline int take_tile(const ScanArgs& a, int* shared) {
     if (a.ntiles == 1) return blockIdx.x;
     if (threadIdx.x == 0) *shared = 1 + atomicAdd(a.ticket, 1);  // cleared to -1 like the words
     __syncthreads();
-    const int t = *shared;
+    const int t = __builtin_amdgcn_readfirstlane(*shared);
     __syncthreads();
     return t;
+}
+// before tiles that hand on their maps: words and ticket cleared, and each tile's first sequence found
+template <int TT>
+__global__ __launch_bounds__(SCAN_THREADS) void k_scan_init(ScanArgs a) {
+    const int64_t n = a.ntiles * a.slots + 1, step = (int64_t)gridDim.x * SCAN_THREADS;
+    for (int64_t i = (int64_t)blockIdx.x * SCAN_THREADS + threadIdx.x; i < n; i += step) a.words[i] = kEmpty;
+    for (int64_t k = ((int64_t)blockIdx.x * SCAN_THREADS + threadIdx.x) >> 6; k < a.ntiles; k += step >> 6) {
+        int64_t t0, t1;
+        tile_tokens<TT>(a, k * TT, t0, t1);
+        const int s = first_sequence(a, t0);
+        if ((threadIdx.x & 63) == 0) a.seq[k] = s;
+    }
+}
+template <int TT>
+__device__ inline int tile_sequence(const ScanArgs& a, Tile t) {
+    if (a.ntiles > 1) return a.seq[t.p0 / TT];
+    int64_t t0, t1;
+    tile_tokens<TT>(a, t.p0, t0, t1);
+    return first_sequence(a, t0);
 }
 
 template <typename T, int V, int CL, int NT>
 __global__ __launch_bounds__(SCAN_THREADS) void k_scan_fwd(ScanArgs a) {
     constexpr int G = SCAN_THREADS / CL, TT = G * NT, CB = CL * V;
-    static_assert(CB <= SCAN_THREADS, "one thread per channel");
+    // the waves that hold one thread per channel
+    constexpr int CW = (CB + 63) / 64 * 64;
+    static_assert(2 * CW <= SCAN_THREADS, "two sets of one thread per channel");
     __shared__ int start[TT], last[TT];
-    __shared__ f32x2 maps[G][CB];
-    const int64_t linear = take_tile(a, start);
+    __shared__ f32x2 maps[G][CB];  // of the token groups, and the states that enter them
+    __shared__ float into[G][CB];
+    const int linear = take_tile(a, start);
     const Tile tile = tile_of(a, linear, TT, CB);
     Share<V, CL, NT> me(a, tile);
+    const Seq seq(a, tile_sequence<TT>(a, tile));
+    me.bounds(a);
     Raw<T, V> rf[NT], rg[NT], ro[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -182,8 +233,7 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_fwd(ScanArgs a) {
         rg[i] = load_raw<V>(static_cast<const T*>(a.g) + t * a.ldz + me.ch);
         if (a.zo) ro[i] = load_raw<V>(static_cast<const T*>(a.zo) + t * a.ldz + me.ch);
     }
-    me.bounds(a);
-    mark_tile<TT, CB>(a, tile, start, last, a.h0, a.hT);
+    mark_tile<TT, CB>(a, tile, seq, start, last, a.h0, a.hT);
     float f[NT][V], b[NT][V], A[V], B[V];
     unsigned reset = 0;
 #pragma unroll
@@ -221,20 +271,30 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_fwd(ScanArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) maps[me.group][col + v] = f32x2{reset ? kReset : A[v], B[v]};
     __syncthreads();
+    // the tile's own map of channel c
+    auto tile_map = [&](int c, float& ta, float& tb) {
+        ta = 1.f;
+        tb = 0.f;
+#pragma unroll 8
+        for (int j = 0; j < G; ++j) {
+            const f32x2 m = maps[j][c];
+            tb = apply_map(m[0], m[1], tb);
+            ta = m[0] < 0.f || ta < 0.f ? kReset : ta * m[0];
+        }
+    };
+    if (const int c = (int)threadIdx.x - (SCAN_THREADS - CW); a.ntiles > 1 && c >= 0 && c < CB) {
+        float ta, tb;
+        tile_map(c, ta, tb);
+        offer_word(a.words + (int64_t)(linear / a.ncb) * a.slots + tile.c0 + c, ta, tb);
+    }
     if (threadIdx.x < CB) {
         const int c = threadIdx.x;
         float h = 0.f;
         if (a.ntiles > 1) {
             const int64_t k = linear / a.ncb, slot = tile.c0 + c;
-            float ta = 1.f, tb = 0.f;
-#pragma unroll 8
-            for (int j = 0; j < G; ++j) {
-                const f32x2 m = maps[j][c];
-                tb = apply_map(m[0], m[1], tb);
-                ta = m[0] < 0.f || ta < 0.f ? kReset : ta * m[0];
-            }
+            float ta, tb;
+            tile_map(c, ta, tb);
             uint64_t* const w = a.words + slot;
-            put_word(w + k * a.slots, ta, tb);
             h = look_back(w, k, a.slots);
             if (!(ta < 0.f)) put_word(w + k * a.slots, kReset, __builtin_fmaf(ta, h, tb));
             a.carry[k * a.slots + slot] = h;
@@ -242,14 +302,14 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_fwd(ScanArgs a) {
 #pragma unroll 8
         for (int j = 0; j < G; ++j) {
             const f32x2 m = maps[j][c];
-            maps[j][c][1] = h;
+            into[j][c] = h;
             h = apply_map(m[0], m[1], h);
         }
     }
     __syncthreads();
     float h[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = maps[me.group][col + v][1];
+    for (int v = 0; v < V; ++v) h[v] = into[me.group][col + v];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const bool r = reset >> i & 1;
@@ -277,14 +337,19 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_fwd(ScanArgs a) {
 template <typename T, int V, int CL, int NT>
 __global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd(ScanArgs a) {
     constexpr int G = SCAN_THREADS / CL, TT = G * NT, CB = CL * V;
-    static_assert(CB <= SCAN_THREADS, "one thread per channel");
+    // the waves that hold one thread per channel
+    constexpr int CW = (CB + 63) / 64 * 64;
+    static_assert(2 * CW <= SCAN_THREADS, "two sets of one thread per channel");
     __shared__ int start[TT], last[TT];
-    __shared__ f32x2 maps[G][CB], rmaps[G][CB];
-    const int64_t ticket = take_tile(a, start);
+    __shared__ f32x2 maps[G][CB], rmaps[G][CB];  // of the token groups, and what enters them
+    __shared__ float into[G][CB], rinto[G][CB];
+    const int ticket = take_tile(a, start);
     // the chain's k-th tile is the k-th from the end
-    const int64_t k = ticket / a.ncb, linear = (a.ntiles - 1 - k) * a.ncb + ticket % a.ncb;
+    const int k = ticket / a.ncb, linear = ((int)a.ntiles - 1 - k) * a.ncb + ticket % a.ncb;
     const Tile tile = tile_of(a, linear, TT, CB);
     Share<V, CL, NT> me(a, tile);
+    const Seq seq(a, tile_sequence<TT>(a, tile));
+    me.bounds(a);
     Raw<T, V> rf[NT], rg[NT], ro[NT], rd[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -294,8 +359,7 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd(ScanArgs a) {
         if (a.zo) ro[i] = load_raw<V>(static_cast<const T*>(a.zo) + t * a.ldz + me.ch);
         rd[i] = load_raw<V>(static_cast<const T*>(a.dy) + t * a.ldy + me.ch);
     }
-    me.bounds(a);
-    mark_tile<TT, CB>(a, tile, start, last, a.dhT, a.dh0);
+    mark_tile<TT, CB>(a, tile, seq, start, last, a.dhT, a.dh0);
     unsigned reset = 0, ends = 0;
     float qf[NT][V], qo[NT][V];
 #pragma unroll
@@ -371,49 +435,58 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd(ScanArgs a) {
         rmaps[me.group][col + v] = f32x2{ends ? kReset : A[v], d[v]};
     }
     __syncthreads();
-    // one thread per channel chains the reverse maps, another the forward ones (the same where CB = 256)
+    // one thread per channel chains the reverse maps, one of other waves the forward ones, and a third, where there are
+    // waves left, hands on the tile's own map
+    constexpr bool kThird = 3 * CW <= SCAN_THREADS;
+    auto tile_map = [&](int c, float& ta, float& tb) {
+        ta = 1.f;
+        tb = 0.f;
+#pragma unroll 8
+        for (int j = G - 1; j >= 0; --j) {
+            const f32x2 m = rmaps[j][c];
+            tb = apply_map(m[0], m[1], tb);
+            ta = m[0] < 0.f || ta < 0.f ? kReset : ta * m[0];
+        }
+    };
     if (threadIdx.x < CB) {
         const int c = threadIdx.x;
         float x = 0.f;
         if (a.ntiles > 1) {
-            const int64_t slot = tile.c0 + c;
-            float ta = 1.f, tb = 0.f;
-#pragma unroll 8
-            for (int j = G - 1; j >= 0; --j) {
-                const f32x2 m = rmaps[j][c];
-                tb = apply_map(m[0], m[1], tb);
-                ta = m[0] < 0.f || ta < 0.f ? kReset : ta * m[0];
-            }
-            uint64_t* const w = a.words + slot;
-            put_word(w + k * a.slots, ta, tb);
+            float ta, tb;
+            tile_map(c, ta, tb);
+            uint64_t* const w = a.words + tile.c0 + c;
+            if (!kThird) put_word(w + k * a.slots, ta, tb);
             x = look_back(w, k, a.slots);
             if (!(ta < 0.f)) put_word(w + k * a.slots, kReset, __builtin_fmaf(ta, x, tb));
         }
 #pragma unroll 8
         for (int j = G - 1; j >= 0; --j) {
             const f32x2 m = rmaps[j][c];
-            rmaps[j][c][1] = x;
+            rinto[j][c] = x;
             x = apply_map(m[0], m[1], x);
         }
     }
-    constexpr int kSecond = CB <= SCAN_THREADS / 2 ? SCAN_THREADS / 2 : 0;
-    if (threadIdx.x >= kSecond && threadIdx.x < kSecond + CB) {
-        const int c = threadIdx.x - kSecond;
+    if (const int c = (int)threadIdx.x - CW; c >= 0 && c < CB) {
         float x = a.ntiles > 1 ? a.carry[linear / a.ncb * a.slots + tile.c0 + c] : 0.f;
 #pragma unroll 8
         for (int j = 0; j < G; ++j) {
             const f32x2 m = maps[j][c];
-            maps[j][c][1] = x;
+            into[j][c] = x;
             x = apply_map(m[0], m[1], x);
         }
+    }
+    if (const int c = (int)threadIdx.x - 2 * CW; kThird && a.ntiles > 1 && c >= 0 && c < CB) {
+        float ta, tb;
+        tile_map(c, ta, tb);
+        offer_word(a.words + k * a.slots + tile.c0 + c, ta, tb);
     }
     __syncthreads();
     forget();
     float prev[NT][V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        h[v] = maps[me.group][col + v][1];
-        d[v] = rmaps[me.group][col + v][1];
+        h[v] = into[me.group][col + v];
+        d[v] = rinto[me.group][col + v];
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -506,17 +579,16 @@ __global__ __launch_bounds__(256) void k_scan_step(int S, int D, const T* __rest
     }
 }
 
-// the tile shape for a row: V channels a thread (one where the row is shorter), as many lanes along the row as it
-// fills, at most 16; forward and backward have the same
+// the tile shape for a row: a vector of 16 bytes a thread (one element where the row is shorter), as many lanes along
+// the row as it fills, at most 8; forward and backward have the same
 template <typename F>
 void with_shape(int D, int dtype, F&& fn) {
     auto go = [&](auto ty) {
-        constexpr int V = 4;
+        constexpr int V = Width<decltype(ty)>::v;
         if (D < V) return fn(ty, ScanShape<1, 8, 4>{});
         const int lanes = (D + V - 1) / V;
         if (lanes <= 4) return fn(ty, ScanShape<V, 4, 4>{});
-        if (lanes <= 8) return fn(ty, ScanShape<V, 8, 4>{});
-        return fn(ty, ScanShape<V, 16, 4>{});
+        return fn(ty, ScanShape<V, 8, 4>{});
     };
     if (dtype == 1) go(bf16{});
     else go(float{});
@@ -534,7 +606,8 @@ ScanPlan scan_plan(int64_t T, int D, int dtype) {
         p.ntiles = (T + tt - 1) / tt;
     });
     if (p.ntiles > 1) {
-        p.carry = p.ntiles * p.slots * 8 + 16;
+        p.seq = p.ntiles * p.slots * 8 + 8;
+        p.carry = (p.seq + p.ntiles * 4 + 15) & ~size_t(15);
         p.total = p.carry + p.ntiles * p.slots * 4;
     }
     return p;
@@ -556,16 +629,19 @@ static hipError_t scan_run(ScanArgs a, int dtype, void* ws, bool backward, hipSt
     if (p.ntiles > 1) {
         uint8_t* w = static_cast<uint8_t*>(ws);
         a.words = reinterpret_cast<uint64_t*>(w);
-        a.ticket = reinterpret_cast<int32_t*>(w + p.carry - 16);
+        a.ticket = reinterpret_cast<int32_t*>(w + p.ntiles * p.slots * 8);  // the word after the tiles'
+        a.seq = reinterpret_cast<int32_t*>(w + p.seq);
         a.carry = reinterpret_cast<float*>(w + p.carry);
-        // words and ticket: all bits set
-        const hipError_t e = launch_fill_i32(reinterpret_cast<int32_t*>(w), (int64_t)(p.carry / 4), -1, st);
-        if (e != hipSuccess) return e;
     }
     const dim3 grid((unsigned)(p.ntiles * p.ncb)), block(SCAN_THREADS);
     with_shape(a.D, dtype, [&](auto ty, auto sh) {
         using T = decltype(ty);
         using S = decltype(sh);
+        if (p.ntiles > 1) {
+            const int64_t n = std::max(p.ntiles * p.slots + 1, p.ntiles * 64);
+            launch(k_scan_init<SCAN_THREADS / S::CL * S::NT>,
+                   dim3((unsigned)std::min<int64_t>((n + SCAN_THREADS - 1) / SCAN_THREADS, 8192)), block, 0, st, a);
+        }
         if (backward) launch(k_scan_bwd<T, S::V, S::CL, S::NT>, grid, block, 0, st, a);
         else launch(k_scan_fwd<T, S::V, S::CL, S::NT>, grid, block, 0, st, a);
     });

@@ -315,7 +315,8 @@ struct ScanArgs {
     int64_t slots = 0;            // channels of all blocks
     float* carry = nullptr;       // [ntiles][slots] state entering each tile: the forward's, for the backward
     uint64_t* words = nullptr;    // [ntiles][slots] the tiles' maps as they are handed on
-    int32_t* ticket = nullptr;
+    int32_t* ticket = nullptr;    // the word after the last
+    int32_t* seq = nullptr;       // [ntiles] first sequence that may hold tokens of the tile
 };
 template <int V_, int CL_, int NT_>
 struct ScanShape {  // channels a thread, lanes along the row, tokens a thread
@@ -324,7 +325,7 @@ struct ScanShape {  // channels a thread, lanes along the row, tokens a thread
 struct ScanPlan {
     int ncb = 0;
     int64_t ntiles = 0, slots = 0;
-    size_t carry = 0, total = 0;  // workspace bytes: words and ticket up to carry, then the tiles' incoming states
+    size_t seq = 0, carry = 0, total = 0;  // byte offsets into the workspace, which starts with the words
 };
 ScanPlan scan_plan(int64_t T, int D, int dtype);
 hipError_t launch_scan_fwd(const ScanArgs& a, int dtype, void* ws, hipStream_t st);

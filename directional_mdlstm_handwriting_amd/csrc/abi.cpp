@@ -957,6 +957,11 @@ static int check_stride(const std::string& F, const char* name, int64_t rows, in
         return fail(MDL_EOVERFLOW, F + ": rows times " + name + " reach 2^60");
     return MDL_OK;
 }
+// as check_stride, for the kernels that keep strides in 32 bits
+static int check_stride32(const std::string& F, const char* name, int64_t rows, int64_t cols, int64_t ld) {
+    if (ld >= (int64_t(1) << 31)) return fail(MDL_EOVERFLOW, F + ": " + name + " reaches 2^31");
+    return check_stride(F, name, rows, cols, ld);
+}
 // sizes and workspace of a scan; need receives the workspace bytes
 static int check_scan(const std::string& F, int64_t T, int32_t D, int32_t dtype, size_t& need) {
     int rc = check_dtype(F, dtype);
@@ -996,7 +1001,7 @@ int mdl_scan_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, in
     if (rc) return rc;
     if (S < 1) return fail(MDL_EINVAL, F + ": need S >= 1");
     if (!seq_off || (T > 0 && (!zf || !g || !y))) return fail(MDL_EINVAL, F + ": null tensor");
-    if ((rc = check_stride(F, "ldz", T, D, ldz)) || (rc = check_stride(F, "ldy", T, D, ldy))) return rc;
+    if ((rc = check_stride32(F, "ldz", T, D, ldz)) || (rc = check_stride32(F, "ldy", T, D, ldy))) return rc;
     if ((rc = check_ws(F, "mdl_scan_workspace_size", need, ws, ws_bytes))) return rc;
     mdl::ScanArgs a{};
     a.off = seq_off;
@@ -1007,8 +1012,8 @@ int mdl_scan_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, in
     a.zf = zf;
     a.g = g;
     a.zo = zo;
-    a.ldz = ldz;
-    a.ldy = ldy;
+    a.ldz = (int)ldz;
+    a.ldy = (int)ldy;
     a.h0 = h0;
     a.y = y;
     a.hT = hT;
@@ -1034,8 +1039,8 @@ int mdl_scan_backward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, i
     if (S < 1) return fail(MDL_EINVAL, F + ": need S >= 1");
     if (!seq_off || (T > 0 && (!zf || !g || !dy || !dzf || !dg))) return fail(MDL_EINVAL, F + ": null tensor");
     if (T > 0 && (zo == nullptr) != (dzo == nullptr)) return fail(MDL_EINVAL, F + ": dzo goes with zo, and only with it");
-    if ((rc = check_stride(F, "ldz", T, D, ldz)) || (rc = check_stride(F, "ldy", T, D, ldy)) ||
-        (rc = check_stride(F, "ldd", T, D, ldd)))
+    if ((rc = check_stride32(F, "ldz", T, D, ldz)) || (rc = check_stride32(F, "ldy", T, D, ldy)) ||
+        (rc = check_stride32(F, "ldd", T, D, ldd)))
         return rc;
     if ((rc = check_ws(F, "mdl_scan_workspace_size", need, ws, ws_bytes))) return rc;
     mdl::ScanArgs a{};
@@ -1048,9 +1053,9 @@ int mdl_scan_backward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, i
     a.g = g;
     a.zo = zo;
     a.dy = dy;
-    a.ldz = ldz;
-    a.ldy = ldy;
-    a.ldd = ldd;
+    a.ldz = (int)ldz;
+    a.ldy = (int)ldy;
+    a.ldd = (int)ldd;
     a.h0 = h0;
     a.dhT = dhT;
     a.dzf = dzf;

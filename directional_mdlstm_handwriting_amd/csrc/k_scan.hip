@@ -23,6 +23,9 @@ namespace mdl {
 
 namespace {
 
+// (min and max of two int64_t go through double)
+__device__ inline int64_t lesser(int64_t a, int64_t b) { return a < b ? a : b; }
+
 constexpr int SCAN_THREADS = 256;
 constexpr float kReset = -1.0f;  // the A of a map that ignores its argument
 
@@ -56,8 +59,8 @@ struct Tile {
 // first / last in scan order, 0 elsewhere. Sequences without tokens hand `from` to `to` ([S][D], zero if null).
 template <int TT>
 __device__ inline void tile_tokens(const ScanArgs& a, int64_t p0, int64_t& t0, int64_t& t1) {  // tokens [t0, t1)
-    t1 = a.reverse ? a.T - p0 : min(p0 + TT, a.T);
-    t0 = a.reverse ? max<int64_t>(a.T - p0 - TT, 0) : p0;
+    t1 = a.reverse ? a.T - p0 : lesser(p0 + TT, a.T);
+    t0 = a.reverse ? -lesser(p0 + TT - a.T, 0) : p0;
 }
 // the first sequence that may hold tokens of [t0, ...): the one before the first that starts there
 __device__ inline int first_sequence(const ScanArgs& a, int64_t t0) {
@@ -82,20 +85,29 @@ __device__ inline void mark_tile(const ScanArgs& a, Tile t, Seq q, int* start, i
     tile_tokens<TT>(a, t.p0, t0, t1);
     const bool final_tile = t1 >= a.T;
     __syncthreads();
-    for (; q.s < a.S; q.s += SCAN_THREADS, q.read(a)) {
+    // one sequence: false where the tile's sequences have ended
+    auto mark = [&]() {
         const int64_t s = q.s, b = q.b, e = q.e;
-        if (b >= t1 && !final_tile) break;
+        if (s >= a.S || (b >= t1 && !final_tile)) return false;
         if (e <= b) {
             // by the tile that holds the offset, the last one for offsets at the end
             const bool mine = b >= t0 && (b < t1 || final_tile);
             if (mine && to) {
                 for (int c = t.c0; c < min(t.c0 + CB, a.D); ++c) to[s * a.D + c] = from ? from[s * a.D + c] : 0.f;
             }
-            continue;
+            return true;
         }
         const int64_t ps = (a.reverse ? a.T - e : b) - t.p0, pl = (a.reverse ? a.T - 1 - b : e - 1) - t.p0;
         if (ps >= 0 && ps < TT) start[ps] = (int)s + 1;
         if (pl >= 0 && pl < TT) last[pl] = (int)s + 1;
+        return true;
+    };
+    // the first, read before the tile's rows, does not wait for them (loads return in order); more of them are rare
+    bool more = mark();
+    while (more) {
+        q.s += SCAN_THREADS;
+        q.read(a);
+        more = mark();
     }
     __syncthreads();
 }
@@ -103,31 +115,33 @@ __device__ inline void mark_tile(const ScanArgs& a, Tile t, Seq q, int* start, i
 // a thread's share of the tile
 template <int V, int CL, int NT>
 struct Share {
-    int64_t p;          // its first position
-    int group;          // its token group
-    int ch;             // its first channel (inside the row)
-    bool active;        // false: a lane past the row's end, which repeats the last vector and stores nothing
-    unsigned inside;    // bit i: position p + i is a token of a sequence
+    int group;        // its token group
+    int ch;           // its first channel (inside the row)
+    bool active;      // false: a lane past the row's end, which repeats the last vector and stores nothing
+    int64_t tok;      // its first token, moved inside [0, T) if past the end (loads from there go unused)
+    int room;         // how many of its next tokens lie inside
+    int dir;          // the tokens' order
+    unsigned inside;  // bit i: its i-th position is a token of a sequence
     __device__ inline Share(const ScanArgs& a, Tile t) {
         group = threadIdx.x / CL;
         const int c = t.c0 + (threadIdx.x % CL) * V;
-        p = t.p0 + group * NT;
         active = c < a.D;
         ch = min(c, a.D - V);
-        inside = 0;
-    }
-    // token of position p + i, moved inside [0, T) for positions past the end (their loads go unused)
-    __device__ inline int64_t token(const ScanArgs& a, int i) const {
-        const int64_t q = min(p + i, a.T - 1);
-        return a.reverse ? a.T - 1 - q : q;
-    }
-    __device__ inline void bounds(const ScanArgs& a) {
+        // the tile's positions that are rows, and those that are tokens of a sequence, counted from its first
+        const int rows = (int)lesser(a.T - t.p0, 1 << 20), g0 = group * NT;
         const int64_t lo = a.off[0], hi = a.off[a.S];
-        for (int i = 0; i < NT; ++i) {
-            const int64_t q = p + i, tok = a.reverse ? a.T - 1 - q : q;
-            if (q < a.T && tok >= lo && tok < hi) inside |= 1u << i;
-        }
+        const int64_t b = (a.reverse ? a.T - hi : lo) - t.p0, e = (a.reverse ? a.T - lo : hi) - t.p0;
+        const int sb = (int)lesser(b < 0 ? 0 : b, 1 << 20), se = min((int)lesser(e < 0 ? 0 : e, 1 << 20), rows);
+        const int p = min(g0, rows - 1);
+        room = min(rows - 1 - p, NT - 1);
+        dir = a.reverse ? -1 : 1;
+        tok = a.reverse ? a.T - 1 - t.p0 - p : t.p0 + p;
+        const int ib = max(0, min(sb - g0, NT)), ie = max(0, min(se - g0, NT));
+        inside = ((1u << ie) - 1) & ~((1u << ib) - 1);
     }
+    // offset of the i-th token's elements in rows of stride ld
+    __device__ inline int64_t at(int i, int ld, int64_t base) const { return base + (int64_t)min(i, room) * (dir * ld); }
+    __device__ inline int64_t base(int ld) const { return tok * ld + ch; }
 };
 
 __device__ inline Tile tile_of(const ScanArgs& a, int linear, int tt, int cb) {
@@ -211,9 +225,48 @@ __device__ inline int tile_sequence(const ScanArgs& a, Tile t) {
     return first_sequence(a, t0);
 }
 
+// The registers of a thread's tokens hold the gates encoded (sigm_enc) and the other streams as loaded. Decoded gates are
+// not kept from one pass over them to the next, and the scheduler works on half a vector at a time: either would double
+// the registers, which other workgroups need to keep loads in flight.
+template <int N, int V>
+__device__ inline void forget(float (&q)[N][V]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) asm volatile("" : "+v"(q[i][v]));
+}
+template <typename T, int N, int V>
+__device__ inline void forget(Raw<T, V> (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (auto& w : r[i].w) asm volatile("" : "+v"(w));
+}
+__device__ inline float settle(float q) {  // form the value here, not where it is used
+    asm volatile("" : "+v"(q));
+    return q;
+}
+__device__ inline void one_at_a_time() { __builtin_amdgcn_sched_barrier(0); }
+// positions of no sequence: their state and gradient pass through (f = 1), and nothing enters
+template <int NT, typename R>
+__device__ inline void outside(unsigned inside, R (&r)[NT], float x) {
+    if (inside == (1u << NT) - 1) return;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+        if (!(inside >> i & 1)) r[i].fill(x);
+}
+// a sequence's row of p (zeros if null) into x: at its first or last token, so rarely that it is read on the spot
+template <int V>
+__device__ inline void enter(const float* p, int seq1, int D, int ch, float (&x)[V]) {
+    if (p) load_f32<V>(p + (int64_t)(seq1 - 1) * D + ch, x);
+    else
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = 0.f;
+}
+
 template <typename T, int V, int CL, int NT>
-__global__ __launch_bounds__(SCAN_THREADS) void k_scan_fwd(ScanArgs a) {
-    constexpr int G = SCAN_THREADS / CL, TT = G * NT, CB = CL * V;
+__global__ __launch_bounds__(SCAN_THREADS, 4) void k_scan_fwd(ScanArgs a) {
+    constexpr int G = SCAN_THREADS / CL, TT = G * NT, CB = CL * V, HV = V > 4 ? 4 : V;
     // the waves that hold one thread per channel
     constexpr int CW = (CB + 63) / 64 * 64;
     static_assert(2 * CW <= SCAN_THREADS, "two sets of one thread per channel");
@@ -224,52 +277,40 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_fwd(ScanArgs a) {
     const Tile tile = tile_of(a, linear, TT, CB);
     Share<V, CL, NT> me(a, tile);
     const Seq seq(a, tile_sequence<TT>(a, tile));
-    me.bounds(a);
     Raw<T, V> rf[NT], rg[NT], ro[NT];
+    const int64_t bz = me.base(a.ldz);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const int64_t t = me.token(a, i);
-        rf[i] = load_raw<V>(static_cast<const T*>(a.zf) + t * a.ldz + me.ch);
-        rg[i] = load_raw<V>(static_cast<const T*>(a.g) + t * a.ldz + me.ch);
-        if (a.zo) ro[i] = load_raw<V>(static_cast<const T*>(a.zo) + t * a.ldz + me.ch);
+        const int64_t t = me.at(i, a.ldz, bz);
+        rf[i] = load_raw<V>(static_cast<const T*>(a.zf) + t);
+        rg[i] = load_raw<V>(static_cast<const T*>(a.g) + t);
+        if (a.zo) ro[i] = load_raw<V>(static_cast<const T*>(a.zo) + t);
     }
     mark_tile<TT, CB>(a, tile, seq, start, last, a.h0, a.hT);
-    float f[NT][V], b[NT][V], A[V], B[V];
+    outside(me.inside, rf, INFINITY);
+    outside(me.inside, rg, 0.f);
+    const int* const first = start + me.group * NT;
+    float qf[NT][V], A[V], h[V] = {};
     unsigned reset = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        A[v] = 1.f;
-        B[v] = 0.f;
-    }
+    for (int v = 0; v < V; ++v) A[v] = 1.f;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const bool in = me.inside >> i & 1;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float s, c;
-            sigm2<T>(rf[i][v], s, c);
-            f[i][v] = in ? s : 1.f;
-            b[i][v] = in ? c * rg[i][v] : 0.f;
-        }
-        const int st = in ? start[me.group * NT + i] : 0;
-        if (st) {
+        if (first[i]) {
             reset |= 1u << i;
-            if (a.h0) {
-                float h[V];
-                load_f32<V>(a.h0 + (int64_t)(st - 1) * a.D + me.ch, h);
-#pragma unroll
-                for (int v = 0; v < V; ++v) b[i][v] = __builtin_fmaf(f[i][v], h[v], b[i][v]);
-            }
+            enter<V>(a.h0, first[i], a.D, me.ch, h);
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            B[v] = st ? b[i][v] : __builtin_fmaf(f[i][v], B[v], b[i][v]);
-            A[v] = A[v] * f[i][v];
+            float f, c;
+            qf[i][v] = settle(sigm_enc<T>(rf[i][v], f, c));
+            h[v] = __builtin_fmaf(f, h[v], c * rg[i][v]);
+            A[v] *= f;
         }
     }
     const int col = (threadIdx.x % CL) * V;
 #pragma unroll
-    for (int v = 0; v < V; ++v) maps[me.group][col + v] = f32x2{reset ? kReset : A[v], B[v]};
+    for (int v = 0; v < V; ++v) maps[me.group][col + v] = f32x2{reset ? kReset : A[v], h[v]};
     __syncthreads();
     // the tile's own map of channel c
     auto tile_map = [&](int c, float& ta, float& tb) {
@@ -289,43 +330,47 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_fwd(ScanArgs a) {
     }
     if (threadIdx.x < CB) {
         const int c = threadIdx.x;
-        float h = 0.f;
+        float x = 0.f;
         if (a.ntiles > 1) {
             const int64_t k = linear / a.ncb, slot = tile.c0 + c;
             float ta, tb;
             tile_map(c, ta, tb);
             uint64_t* const w = a.words + slot;
-            h = look_back(w, k, a.slots);
-            if (!(ta < 0.f)) put_word(w + k * a.slots, kReset, __builtin_fmaf(ta, h, tb));
-            a.carry[k * a.slots + slot] = h;
+            x = look_back(w, k, a.slots);
+            if (!(ta < 0.f)) put_word(w + k * a.slots, kReset, __builtin_fmaf(ta, x, tb));
+            a.carry[k * a.slots + slot] = x;
         }
 #pragma unroll 8
         for (int j = 0; j < G; ++j) {
             const f32x2 m = maps[j][c];
-            into[j][c] = h;
-            h = apply_map(m[0], m[1], h);
+            into[j][c] = x;
+            x = apply_map(m[0], m[1], x);
         }
     }
     __syncthreads();
-    float h[V];
+    forget(qf);
+    forget(rg);
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = into[me.group][col + v];
+    const int64_t by = me.base(a.ldy);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const bool r = reset >> i & 1;
+        if (reset >> i & 1) enter<V>(a.h0, first[i], a.D, me.ch, h);
         float y[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            h[v] = r ? b[i][v] : __builtin_fmaf(f[i][v], h[v], b[i][v]);
-            y[v] = h[v];
-            if (a.zo) {
-                float s, c;
-                sigm2<T>(ro[i][v], s, c);
-                y[v] *= s;
+        for (int v0 = 0; v0 < V; v0 += HV) {
+            one_at_a_time();
+#pragma unroll
+            for (int v = v0; v < v0 + HV; ++v) {
+                float f, c, so = 1.f, co;
+                sigm_dec(qf[i][v], f, c);
+                h[v] = __builtin_fmaf(f, h[v], c * rg[i][v]);
+                if (a.zo) sigm2<T>(ro[i][v], so, co);
+                y[v] = so * h[v];
             }
         }
         if (me.active && (me.inside >> i & 1)) {
-            store_vec<V>(static_cast<T*>(a.y) + me.token(a, i) * a.ldy + me.ch, y);
+            store_vec<V>(static_cast<T*>(a.y) + me.at(i, a.ldy, by), y);
             const int en = last[me.group * NT + i];
             if (en && a.hT) store_f32<V>(a.hT + (int64_t)(en - 1) * a.D + me.ch, h);
         }
@@ -333,11 +378,10 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_fwd(ScanArgs a) {
 }
 
 // Backward: the tile's states again from its incoming one in a.carry, and the reverse recurrence, whose tiles are
-// chained from the last to the first. Gates stay encoded (sigm_enc) between the passes over the registers.
+// chained from the last to the first.
 template <typename T, int V, int CL, int NT>
-__global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd(ScanArgs a) {
-    constexpr int G = SCAN_THREADS / CL, TT = G * NT, CB = CL * V;
-    // the waves that hold one thread per channel
+__global__ __launch_bounds__(SCAN_THREADS, V == 8 ? 3 : 4) void k_scan_bwd(ScanArgs a) {
+    constexpr int G = SCAN_THREADS / CL, TT = G * NT, CB = CL * V, HV = V > 4 ? 4 : V;
     constexpr int CW = (CB + 63) / 64 * 64;
     static_assert(2 * CW <= SCAN_THREADS, "two sets of one thread per channel");
     __shared__ int start[TT], last[TT];
@@ -349,179 +393,164 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd(ScanArgs a) {
     const Tile tile = tile_of(a, linear, TT, CB);
     Share<V, CL, NT> me(a, tile);
     const Seq seq(a, tile_sequence<TT>(a, tile));
-    me.bounds(a);
     Raw<T, V> rf[NT], rg[NT], ro[NT], rd[NT];
+    const int64_t bz = me.base(a.ldz), by = me.base(a.ldy);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const int64_t t = me.token(a, i);
-        rf[i] = load_raw<V>(static_cast<const T*>(a.zf) + t * a.ldz + me.ch);
-        rg[i] = load_raw<V>(static_cast<const T*>(a.g) + t * a.ldz + me.ch);
-        if (a.zo) ro[i] = load_raw<V>(static_cast<const T*>(a.zo) + t * a.ldz + me.ch);
-        rd[i] = load_raw<V>(static_cast<const T*>(a.dy) + t * a.ldy + me.ch);
+        const int64_t t = me.at(i, a.ldz, bz);
+        rf[i] = load_raw<V>(static_cast<const T*>(a.zf) + t);
+        rg[i] = load_raw<V>(static_cast<const T*>(a.g) + t);
+        if (a.zo) ro[i] = load_raw<V>(static_cast<const T*>(a.zo) + t);
+        else ro[i].fill(INFINITY);  // an open gate
+        rd[i] = load_raw<V>(static_cast<const T*>(a.dy) + me.at(i, a.ldy, by));
     }
     mark_tile<TT, CB>(a, tile, seq, start, last, a.dhT, a.dh0);
+    outside(me.inside, rf, INFINITY);
+    outside(me.inside, rg, 0.f);
+    outside(me.inside, ro, 0.f);
+    outside(me.inside, rd, 0.f);
+    const int *const first = start + me.group * NT, *const fin = last + me.group * NT;
+    // Both maps in one walk over the tokens: with P_t = f_first ... f_t, the reverse one is x -> P_last x + sum_t P_t e_t
+    // for the gradients e_t = o_t dy_t that enter at the tokens, up to the first sequence's end.
+    float qf[NT][V], qo[NT][V], A[V], h[V] = {}, d[V] = {};
     unsigned reset = 0, ends = 0;
-    float qf[NT][V], qo[NT][V];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const bool in = me.inside >> i & 1;
-        if (in && start[me.group * NT + i]) reset |= 1u << i;
-        if (in && last[me.group * NT + i]) ends |= 1u << i;
-        if (!in) {  // a token of no sequence: state and gradient pass through, nothing enters
-            rg[i] = Raw<T, V>{};
-            rd[i] = Raw<T, V>{};
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            qf[i][v] = in ? sigm_enc<T>(rf[i][v]) : kSigmOne;
-            qo[i][v] = a.zo && in ? sigm_enc<T>(ro[i][v]) : kSigmOne;
-        }
-    }
-    // a sequence's incoming state at its first token, and the gradient of its last state at its last: rare, so read
-    // where they are needed
-    auto first_state = [&](int i, float(&h)[V]) {
-        if ((reset >> i & 1)) {
-            if (a.h0) load_f32<V>(a.h0 + (int64_t)(start[me.group * NT + i] - 1) * a.D + me.ch, h);
-            else
-#pragma unroll
-                for (int v = 0; v < V; ++v) h[v] = 0.f;
-        }
-    };
-    auto last_grad = [&](int i, float(&d)[V]) {
-        if ((ends >> i & 1)) {
-            if (a.dhT) load_f32<V>(a.dhT + (int64_t)(last[me.group * NT + i] - 1) * a.D + me.ch, d);
-            else
-#pragma unroll
-                for (int v = 0; v < V; ++v) d[v] = 0.f;
-        }
-    };
-    // decoded gates are not kept from one pass over the registers to the next (they would double its registers)
-    auto forget = [&] {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) asm volatile("" : "+v"(qf[i][v]), "+v"(qo[i][v]));
-    };
-    const int col = (threadIdx.x % CL) * V;
-    float A[V], h[V] = {}, d[V] = {};
 #pragma unroll
     for (int v = 0; v < V; ++v) A[v] = 1.f;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        first_state(i, h);
+        if (first[i]) {
+            reset |= 1u << i;
+            enter<V>(a.h0, first[i], a.D, me.ch, h);
+        }
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float f, c;
-            sigm_dec(qf[i][v], f, c);
-            h[v] = __builtin_fmaf(f, h[v], c * rg[i][v]);
-            A[v] *= f;
+        for (int v0 = 0; v0 < V; v0 += HV) {
+            one_at_a_time();
+#pragma unroll
+            for (int v = v0; v < v0 + HV; ++v) {
+                float f, c, so, co;
+                qf[i][v] = settle(sigm_enc<T>(rf[i][v], f, c));
+                qo[i][v] = settle(sigm_enc<T>(ro[i][v], so, co));
+                h[v] = __builtin_fmaf(f, h[v], c * rg[i][v]);
+                A[v] *= f;
+                if (!ends) d[v] = __builtin_fmaf(A[v], so * rd[i][v], d[v]);
+            }
+        }
+        if (fin[i]) {
+            if (!ends) {
+                float x[V];
+                enter<V>(a.dhT, fin[i], a.D, me.ch, x);
+#pragma unroll
+                for (int v = 0; v < V; ++v) d[v] = __builtin_fmaf(A[v], x[v], d[v]);
+            }
+            ends |= 1u << i;
         }
     }
-    forget();
-#pragma unroll
-    for (int i = NT - 1; i >= 0; --i) {
-        last_grad(i, d);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float f, c, so, co;
-            sigm_dec(qf[i][v], f, c);
-            sigm_dec(qo[i][v], so, co);
-            d[v] = f * __builtin_fmaf(so, rd[i][v], d[v]);
-        }
-    }
+    const int col = (threadIdx.x % CL) * V;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         maps[me.group][col + v] = f32x2{reset ? kReset : A[v], h[v]};
         rmaps[me.group][col + v] = f32x2{ends ? kReset : A[v], d[v]};
     }
     __syncthreads();
-    // one thread per channel chains the reverse maps, one of other waves the forward ones, and a third, where there are
-    // waves left, hands on the tile's own map
+    // Waves in parallel, one thread per channel: the first composes the tile's reverse map, the next chains the forward
+    // maps from the incoming state, a third hands on the reverse map where there are waves left.
     constexpr bool kThird = 3 * CW <= SCAN_THREADS;
-    auto tile_map = [&](int c, float& ta, float& tb) {
-        ta = 1.f;
-        tb = 0.f;
+    uint64_t* const w = a.words + tile.c0;
+    const int c1 = threadIdx.x, c2 = c1 - CW, c3 = c2 - CW;
+    float ta = 1.f, tb = 0.f;
+    if (a.ntiles > 1 && (c1 < CB || (kThird && c3 >= 0 && c3 < CB))) {
+        const int c = c1 < CB ? c1 : c3;
 #pragma unroll 8
         for (int j = G - 1; j >= 0; --j) {
             const f32x2 m = rmaps[j][c];
             tb = apply_map(m[0], m[1], tb);
             ta = m[0] < 0.f || ta < 0.f ? kReset : ta * m[0];
         }
-    };
-    if (threadIdx.x < CB) {
-        const int c = threadIdx.x;
+        if (!kThird) put_word(w + k * a.slots + c, ta, tb);
+        else if (c1 >= CB) offer_word(w + k * a.slots + c, ta, tb);
+    }
+    if (c2 >= 0 && c2 < CB) {
+        float x = a.ntiles > 1 ? a.carry[(int64_t)(linear / a.ncb) * a.slots + tile.c0 + c2] : 0.f;
+#pragma unroll 8
+        for (int j = 0; j < G; ++j) {
+            const f32x2 m = maps[j][c2];
+            into[j][c2] = x;
+            x = apply_map(m[0], m[1], x);
+        }
+    }
+    __syncthreads();
+    // the first wave looks back while the others walk forward
+    if (c1 < CB) {
         float x = 0.f;
         if (a.ntiles > 1) {
-            float ta, tb;
-            tile_map(c, ta, tb);
-            uint64_t* const w = a.words + tile.c0 + c;
-            if (!kThird) put_word(w + k * a.slots, ta, tb);
-            x = look_back(w, k, a.slots);
-            if (!(ta < 0.f)) put_word(w + k * a.slots, kReset, __builtin_fmaf(ta, x, tb));
+            x = look_back(w + c1, k, a.slots);
+            if (!(ta < 0.f)) put_word(w + k * a.slots + c1, kReset, __builtin_fmaf(ta, x, tb));
         }
 #pragma unroll 8
         for (int j = G - 1; j >= 0; --j) {
-            const f32x2 m = rmaps[j][c];
-            rinto[j][c] = x;
+            const f32x2 m = rmaps[j][c1];
+            rinto[j][c1] = x;
             x = apply_map(m[0], m[1], x);
         }
     }
-    if (const int c = (int)threadIdx.x - CW; c >= 0 && c < CB) {
-        float x = a.ntiles > 1 ? a.carry[linear / a.ncb * a.slots + tile.c0 + c] : 0.f;
-#pragma unroll 8
-        for (int j = 0; j < G; ++j) {
-            const f32x2 m = maps[j][c];
-            into[j][c] = x;
-            x = apply_map(m[0], m[1], x);
-        }
-    }
-    if (const int c = (int)threadIdx.x - 2 * CW; kThird && a.ntiles > 1 && c >= 0 && c < CB) {
-        float ta, tb;
-        tile_map(c, ta, tb);
-        offer_word(a.words + k * a.slots + tile.c0 + c, ta, tb);
-    }
-    __syncthreads();
-    forget();
-    float prev[NT][V];
+    // Forward: the states, with which the output gates' gradients are done. What is left of the other streams is the
+    // entering gradient e = o dy and h_{t-1} - g.
+    forget(qf);
+    forget(qo);
+    forget(rg);
+    forget(rd);
+    const int64_t bd = me.base(a.ldd);
+    float e[NT][V], pg[NT][V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        h[v] = into[me.group][col + v];
-        d[v] = rinto[me.group][col + v];
-    }
+    for (int v = 0; v < V; ++v) h[v] = into[me.group][col + v];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        first_state(i, h);
+        if (reset >> i & 1) enter<V>(a.h0, first[i], a.D, me.ch, h);
+        float dzo[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float f, c;
-            sigm_dec(qf[i][v], f, c);
-            prev[i][v] = h[v];
-            h[v] = __builtin_fmaf(f, h[v], c * rg[i][v]);
+        for (int v0 = 0; v0 < V; v0 += HV) {
+            one_at_a_time();
+#pragma unroll
+            for (int v = v0; v < v0 + HV; ++v) {
+                float f, c, so, co;
+                sigm_dec(qf[i][v], f, c);
+                sigm_dec(qo[i][v], so, co);
+                const float g = rg[i][v];
+                pg[i][v] = settle(h[v] - g);
+                h[v] = __builtin_fmaf(f, h[v], c * g);
+                e[i][v] = settle(so * rd[i][v]);
+                dzo[v] = e[i][v] * co * h[v];
+            }
         }
+        if (a.zo && me.active && (me.inside >> i & 1)) store_vec<V>(static_cast<T*>(a.dzo) + me.at(i, a.ldd, bd), dzo);
     }
-    forget();
+    __syncthreads();
+    forget(qf);
+#pragma unroll
+    for (int v = 0; v < V; ++v) d[v] = rinto[me.group][col + v];
 #pragma unroll
     for (int i = NT - 1; i >= 0; --i) {
-        float dzf[V], dg[V], dzo[V];
-        last_grad(i, d);
+        float dzf[V], dg[V];
+        if (ends >> i & 1) enter<V>(a.dhT, fin[i], a.D, me.ch, d);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float f, c, so, co;
-            sigm_dec(qf[i][v], f, c);
-            sigm_dec(qo[i][v], so, co);
-            const float g = rg[i][v], own = so * rd[i][v], lam = own + d[v];
-            dg[v] = c * lam;
-            dzf[v] = f * dg[v] * (prev[i][v] - g);
-            dzo[v] = own * co * __builtin_fmaf(f, prev[i][v], c * g);
-            d[v] = f * lam;
+        for (int v0 = 0; v0 < V; v0 += HV) {
+            one_at_a_time();
+#pragma unroll
+            for (int v = v0; v < v0 + HV; ++v) {
+                float f, c;
+                sigm_dec(qf[i][v], f, c);
+                const float lam = e[i][v] + d[v];
+                dg[v] = c * lam;
+                d[v] = f * lam;
+                dzf[v] = f * dg[v] * pg[i][v];
+            }
         }
         if (me.active && (me.inside >> i & 1)) {
-            const int64_t o = me.token(a, i) * a.ldd + me.ch;
+            const int64_t o = me.at(i, a.ldd, bd);
             store_vec<V>(static_cast<T*>(a.dzf) + o, dzf);
             store_vec<V>(static_cast<T*>(a.dg) + o, dg);
-            if (a.zo) store_vec<V>(static_cast<T*>(a.dzo) + o, dzo);
             if ((reset >> i & 1) && a.dh0)
-                store_f32<V>(a.dh0 + (int64_t)(start[me.group * NT + i] - 1) * a.D + me.ch, d);
+                store_f32<V>(a.dh0 + (int64_t)(first[i] - 1) * a.D + me.ch, d);
         }
     }
 }

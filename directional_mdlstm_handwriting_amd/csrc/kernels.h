@@ -305,7 +305,7 @@ struct ScanArgs {
     int S, D, reverse;
     int64_t T;                    // tokens of the tensors
     const void *zf, *g, *zo, *dy; // [T][D] at row strides ldz (zf, g, zo) and ldy (dy, y)
-    int64_t ldz, ldy, ldd;        // ldd: of dzf, dg, dzo
+    int ldz, ldy, ldd;            // ldd: of dzf, dg, dzo
     const float *h0, *dhT;        // [S][D] or null
     void *y, *dzf, *dg, *dzo;
     float *hT, *dh0;              // [S][D] or null

@@ -19,11 +19,20 @@ struct Raw;
 template <int V>
 struct Raw<float, V> {
     float w[V];
+    __device__ inline void fill(float x) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[i] = x;
+    }
     __device__ inline float operator[](int i) const { return w[i]; }
 };
 template <int V>
 struct Raw<bf16, V> {
     uint32_t w[(V + 1) / 2];  // element 2i in the low half
+    __device__ inline void fill(float x) {  // x exact in bfloat16
+        const uint32_t u = __float_as_uint(x) >> 16;
+#pragma unroll
+        for (int i = 0; i < (V + 1) / 2; ++i) w[i] = u | u << 16;
+    }
     __device__ inline float operator[](int i) const {
         return __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
     }
@@ -180,19 +189,20 @@ __device__ inline float group_max(float v) {
     return v;
 }
 
-// sigmoid(z) and 1 - sigmoid(z) in one register: the smaller of the two, its sign bit set where that is 1 - sigmoid
+// sigmoid(z) and 1 - sigmoid(z) with both of them in one register, q: the smaller one, with the sign of z
 template <typename T>
-__device__ inline float sigm_enc(float z) {
+__device__ inline float sigm_enc(float z, float& s, float& c) {
     const float e = exp_neg<T>(-fabsf(z));
-    const float q = e * frcp(1.0f + e);
-    return z >= 0.f ? -q : q;
+    const float r = frcp(1.0f + e), q = e * r;
+    s = z >= 0.f ? r : q;
+    c = z >= 0.f ? q : r;
+    return __builtin_copysignf(q, z);
 }
 __device__ inline void sigm_dec(float q, float& s, float& c) {
     const float t = fabsf(q), o = 1.f - t;
     const bool neg = (int)__float_as_uint(q) < 0;
-    s = neg ? o : t;
-    c = neg ? t : o;
+    s = neg ? t : o;
+    c = neg ? o : t;
 }
-constexpr float kSigmOne = -0.f;  // sigmoid 1
 
 }  // namespace mdl

@@ -945,6 +945,10 @@ int mdl_ctc_head(const mdl_layout* layout, const void* d_desc, const float* y_fl
     GUARD_END
 }
 
+// Looks at another tile's word before a scan's tile forms what it waits for itself: about a millisecond, many times what
+// a tile takes. None in the mode that allows no wait any time.
+constexpr int kScanPolls = 1024;
+
 // ---- the gated recurrence over packed sequences ---------------------------------------------------
 static int check_dtype(const std::string& F, int32_t dtype) {
     if (dtype != MDL_F32 && dtype != MDL_BF16) return fail(MDL_EINVAL, F + ": unknown dtype");
@@ -1008,6 +1012,7 @@ int mdl_scan_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, in
     a.S = S;
     a.D = D;
     a.reverse = reverse != 0;
+    a.polls = g_overlap.load() == 2 ? -1 : kScanPolls;
     a.T = T;
     a.zf = zf;
     a.g = g;
@@ -1048,6 +1053,7 @@ int mdl_scan_backward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, i
     a.S = S;
     a.D = D;
     a.reverse = reverse != 0;
+    a.polls = g_overlap.load() == 2 ? -1 : kScanPolls;
     a.T = T;
     a.zf = zf;
     a.g = g;

@@ -309,13 +309,13 @@ struct ScanArgs {
     const float *h0, *dhT;        // [S][D] or null
     void *y, *dzf, *dg, *dzo;
     float *hT, *dh0;              // [S][D] or null
+    int polls;                    // looks at other tiles' words before a thread goes on by itself
     // set by the launchers
     int ncb = 0;                  // channel blocks
     int64_t ntiles = 0;
     int64_t slots = 0;            // channels of all blocks
     float* carry = nullptr;       // [ntiles][slots] state entering each tile: the forward's, for the backward
     uint64_t* words = nullptr;    // [ntiles][slots] the tiles' maps as they are handed on
-    int32_t* ticket = nullptr;    // the word after the last
     int32_t* seq = nullptr;       // [ntiles] first sequence that may hold tokens of the tile
 };
 template <int V_, int CL_, int NT_>

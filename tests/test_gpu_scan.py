@@ -256,6 +256,27 @@ def test_results_repeat_bit_for_bit_on_any_stream():
         assert again2[0] is again[0]
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_tiles_that_wait_for_nothing(reverse, dtype):
+    """With no time allowed for any wait, every tile forms the maps it needs from the inputs: the same bits."""
+    lens = [500, 3, 0, 700, 64, 1]
+    off = _off(lens, first=5)
+    T = int(off[-1]) + 150
+    for D, gate, h0 in ((72, True, True), (20, False, True), (5, True, False)):
+        zf, g, zo, h, dy, dhT = _inputs(12, T, len(lens), D, dtype, gate, h0)
+        sc = SequenceScan(off, T, D, dtype, reverse=reverse, device=DEV)
+        ref = [t.clone() for t in (*sc.forward(zf, g, zo, h), *sc.backward(zf, g, zo, dy, h, dhT)) if t is not None]
+        try:
+            M.mdl_set_wgrad_overlap(2)
+            got = [t for t in (*sc.forward(zf, g, zo, h), *sc.backward(zf, g, zo, dy, h, dhT)) if t is not None]
+            torch.cuda.synchronize()
+        finally:
+            M.mdl_set_wgrad_overlap(1)
+        for i, (a, b) in enumerate(zip(got, ref)):
+            assert torch.equal(a, b), (D, i)
+
+
 def test_row_strides_and_unaligned_rows():
     """Outputs through the C ABI at strides of their own, rows starting at odd elements."""
     off = _off([50, 210, 5])

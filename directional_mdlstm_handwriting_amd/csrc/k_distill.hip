@@ -7,7 +7,7 @@
 //   loss / (w tau^2) = (1/T) sum_j e_j ((t_j - max t) - (z_{id_j} - m)) / tau - ln T + ln L.
 //
 // R lanes share a row. A row that fits their registers is read once, kept as it lies in memory, and its gradient is
-// formed from there; longer rows are read twice, the first time with a running maximum and sum. The few kept classes sit
+// formed from there; longer rows are read twice. The maximum and the sum run along with the reading. The few kept classes sit
 // in LDS; their gradients are written over the row's after it, by the lanes that own the slots (a class named twice gets
 // both slots' p). Statistics are fp32; the gradient is rounded once.
 #include "kernels.h"
@@ -51,9 +51,62 @@ __device__ inline void row_reduce(float (&s)[K], float* red) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             s[k] = red[k];
+#pragma unroll 2
             for (int w = 1; w < R / 64; ++w) s[k] = MAX ? fmaxf(s[k], red[w * K + k]) : s[k] + red[w * K + k];
         }
     }
+}
+
+// element 0 of a vector
+template <int V>
+__device__ inline void set_first(Raw<float, V>& r, const Raw<float, 1>& x) {
+    if constexpr (V == 1) r.w = x.w;
+    else r.w[0] = x.w;
+}
+template <int V>
+__device__ inline void set_first(Raw<bf16, V>& r, const Raw<bf16, 1>& x) {
+    if constexpr (V == 1) r.w = x.w;
+    else r.w[0] = (r.w[0] & 0xffff0000u) | x.w;
+}
+// the first n elements set to -inf
+template <int V>
+__device__ inline void hide(Raw<float, V>& r, int n) {
+    if constexpr (V == 1) {
+        if (n > 0) r.w = -INFINITY;
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) r.w[v] = v < n ? -INFINITY : r.w[v];
+    }
+}
+template <int V>
+__device__ inline void hide(Raw<bf16, V>& r, int n) {
+    if constexpr (V == 1) {
+        if (n > 0) r.w = 0xff80u;
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            uint32_t w = r.w[v / 2];
+            if (v < n) w = (w & 0xffff0000u) | 0xff80u;
+            if (v + 1 < n) w = (w & 0xffffu) | 0xff800000u;
+            r.w[v / 2] = w;
+        }
+    }
+}
+template <int V>
+__device__ inline void store_zeros(float* p) {
+    const float o[V] = {};
+    store_vec<V>(p, o);
+}
+template <int V>
+__device__ inline void store_zeros(bf16* p) {
+    const float o[V] = {};
+    store_vec<V>(p, o);
+}
+
+// a copy that the compiler takes for another value: places formed from it are not kept in registers for later walks
+__device__ inline int anew(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
 }
 
 struct DistillArgs {
@@ -65,17 +118,21 @@ struct DistillArgs {
     const void* t;
     int t_bf16;
     const float* w;
-    float tau, inv_tau;
+    float tau, inv_tau, log2e_tau;
     float* loss;
     void* dz;
     int64_t ldd;
 };
 
-// exp of x <= 0 (x = (z - max) / tau): as exp_neg, NaN where the row's maximum is not finite
+// exp(d / tau) for d <= 0 (NaN where the row's maximum is not finite), from the product with log2 e / tau: with the
+// rounding of d, the argument is off by 3 |d / tau| 2^-24, no more than by way of d / tau
+__device__ inline float exp_tau(float d, const DistillArgs& a) { return __builtin_amdgcn_exp2f(d * a.log2e_tau); }
+
 template <typename T, typename S>
-__global__ __launch_bounds__(S::threads) void k_distill(DistillArgs a) {
+__global__ __launch_bounds__(S::threads, 4) void k_distill(DistillArgs a) {
     constexpr int V = S::V, R = S::R, NV = S::NV > 0 ? S::NV : 1;
     constexpr bool kTwice = S::NV == 0;
+    constexpr int kAhead = S::NV == 0 || NV % 4 == 0 ? 4 : NV % 2 == 0 ? 2 : 1;  // vectors walked at a time
     __shared__ float red[S::threads / 64 * 5];
     extern __shared__ float top[];  // [rows][3][k]: class, e_j, z of the class
     const int lane = threadIdx.x % R, group = threadIdx.x / R;
@@ -87,29 +144,66 @@ __global__ __launch_bounds__(S::threads) void k_distill(DistillArgs a) {
     float* const ej = top + (size_t)group * 3 * a.k + a.k;
     float* const zj = ej + a.k;
 
-    // the row: its vectors, each element counted once (a vector moved back from the row's end skips its first ones)
+    // the row: each lane's running maximum and sum, some vectors at a time, as they arrive
     Raw<T, V> q[NV];
     const int full = a.V / V, tail = full * V;
     float mx = -INFINITY, run = 0.f;
+    auto take = [&](const Raw<T, V>* r) {
+        float b = mx, p = 0.f;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) b = fmaxf(b, r[i][v]);
+        if (b > mx) run *= exp_tau(mx - b, a);
+        mx = b;
+        const float c = b == -INFINITY ? 0.f : b;  // nothing but -inf so far: exp(-inf) = 0
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) p += exp_tau(r[i][v] - c, a);
+        run += p;
+    };
     if constexpr (!kTwice) {
+        // a vector past the row's end is moved back to end with it: what it repeats is hidden from the sums
 #pragma unroll
-        for (int i = 0; i < NV; ++i) q[i] = load_raw<V>(z + min((lane + i * R) * V, a.V - V));
-    } else {
-        // running maximum and sum of a lane's elements
-        auto take = [&](float x) {
-            if (x > mx) {
-                run = run * exp_neg<T>((mx - x) * a.inv_tau) + 1.f;
-                mx = x;
-            } else {
-                run += x == mx ? 1.f : exp_neg<T>((x - mx) * a.inv_tau);
-            }
-        };
-        for (int i = lane; i < full; i += R) {
-            const Raw<T, V> r = load_raw<V>(z + (int64_t)i * V);
-#pragma unroll
-            for (int v = 0; v < V; ++v) take(r[v]);
+        for (int i = 0; i < NV; ++i) {
+            one_at_a_time();
+            q[i] = load_raw<V>(z + min((lane + i * R) * V, a.V - V));
         }
-        for (int i = tail + lane; i < a.V; i += R) take(load_raw<1>(z + i)[0]);
+#pragma unroll
+        for (int i = 0; i < NV; i += kAhead) {
+            one_at_a_time();
+            const int at = anew(lane);
+#pragma unroll
+            for (int j = i; j < i + kAhead; ++j)
+                if (const int skip = (at + j * R) * V - (a.V - V); skip > 0) hide(q[j], skip);
+            take(q + i);
+        }
+        mx = settle(mx);
+        run = settle(run);
+        forget(q);
+    } else {
+        int i = lane;
+        for (; i + (kAhead - 1) * R < full; i += kAhead * R) {
+            Raw<T, V> r[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) r[j] = load_raw<V>(z + (int64_t)(i + j * R) * V);
+            take(r);
+        }
+        for (; i < full; i += R) {
+            Raw<T, V> r[kAhead];
+            r[0] = load_raw<V>(z + (int64_t)i * V);
+#pragma unroll
+            for (int j = 1; j < kAhead; ++j) r[j].fill(-INFINITY);
+            take(r);
+        }
+        for (i = tail + lane; i < a.V; i += R) {
+            Raw<T, V> r[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) r[j].fill(-INFINITY);
+            set_first(r[0], load_raw<1>(z + i));
+            take(r);
+        }
     }
     // the kept classes
     float m2[2] = {mx, -INFINITY};
@@ -126,34 +220,16 @@ __global__ __launch_bounds__(S::threads) void k_distill(DistillArgs a) {
         zj[j] = ok ? load_raw<1>(z + c)[0] : 0.f;
         if (ok) m2[1] = fmaxf(m2[1], t);
     }
-    if constexpr (!kTwice) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) m2[0] = fmaxf(m2[0], q[i][v]);
-    }
     row_reduce<R, 2, true>(m2, red);
     const float m = m2[0], tm = m2[1];
-    float s[5] = {0.f, 0.f, 0.f, kept, bad};  // L, T, sum e_j (...), kept classes, classes that do not exist
-    if constexpr (!kTwice) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + i * R) * V, skip = c - min(c, a.V - V);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float e = exp_neg<T>((q[i][v] - m) * a.inv_tau);
-                s[0] += v >= skip ? e : 0.f;
-            }
-        }
-    } else {
-        s[0] = mx == m ? run : run * exp_neg<T>((mx - m) * a.inv_tau);
-    }
+    // L, T, sum e_j (...), kept classes, classes that do not exist (a lane that has seen only -inf: nothing)
+    float s[5] = {mx == m ? run : run * exp_tau(mx - m, a), 0.f, 0.f, kept, bad};
     for (int j = lane; j < a.k; j += R) {
         if (cls[j] < 0) {
             ej[j] = 0.f;
             continue;
         }
-        const float d = ej[j] - tm, e = exp_neg<float>(d * a.inv_tau);
+        const float d = ej[j] - tm, e = exp_tau(d, a);
         s[1] += e;
         if (e > 0.f || e != e) s[2] += e * ((d - (zj[j] - m)) * a.inv_tau);
         ej[j] = e;
@@ -167,28 +243,49 @@ __global__ __launch_bounds__(S::threads) void k_distill(DistillArgs a) {
         a.loss[n] = s[4] > 0.f ? NAN : counts ? w * a.tau * a.tau * kl : 0.f;
     }
     if (!a.dz) return;
-    const float g = counts ? w * a.tau : 0.f, gl = g * inv_l;
+    const float g = w * a.tau, gl = g * inv_l;
     T* const dz = static_cast<T*>(a.dz) + n * a.ldd;
-    auto grad = [&](float x) { return counts ? exp_neg<T>((x - m) * a.inv_tau) * gl : 0.f; };
+    auto grad = [&](float x) { return exp_tau(x - m, a) * gl; };
     row_sync<R>();  // the row and its kept classes have been read: dz may be z
-    if constexpr (!kTwice) {
+    if (!counts) {
+        for (int i = lane; i < full && live; i += R) store_zeros<V>(dz + (int64_t)i * V);
+        for (int i = tail + lane; i < a.V && live; i += R) store_zeros<1>(dz + i);
+    } else if constexpr (!kTwice) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (lane + i * R) * V;
+            const int c = (anew(lane) + i * R) * V, skip = c - (a.V - V);
             float o[V];
+            one_at_a_time();
 #pragma unroll
             for (int v = 0; v < V; ++v) o[v] = grad(q[i][v]);
-            if (live && c < a.V) store_vec<V>(dz + min(c, a.V - V), o);
+            if (!live) continue;
+            if (skip <= 0) {
+                store_vec<V>(dz + c, o);
+            } else if (skip < V) {
+#pragma unroll
+                for (int v = 1; v < V; ++v) {
+                    const float x[1] = {o[v]};
+                    if (v >= skip) store_vec<1>(dz + (a.V - V) + v, x);
+                }
+            }
         }
     } else {
-        for (int i = lane; i < full; i += R) {
-            const Raw<T, V> r = load_raw<V>(z + (int64_t)i * V);
+        auto put = [&](const Raw<T, V>& r, int i) {
             float o[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) o[v] = grad(r[v]);
             if (live) store_vec<V>(dz + (int64_t)i * V, o);
+        };
+        int i = lane;
+        for (; i + (kAhead - 1) * R < full; i += kAhead * R) {
+            Raw<T, V> r[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) r[j] = load_raw<V>(z + (int64_t)(i + j * R) * V);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) put(r[j], i + j * R);
         }
-        for (int i = tail + lane; i < a.V; i += R) {
+        for (; i < full; i += R) put(load_raw<V>(z + (int64_t)i * V), i);
+        for (i = tail + lane; i < a.V; i += R) {
             const float o[1] = {grad(load_raw<1>(z + i)[0])};
             if (live) store_vec<1>(dz + i, o);
         }
@@ -216,9 +313,11 @@ void with_shape(int64_t V_, int dtype, F&& fn) {
         if (nv <= 64) return fn(ty, DistillShape<V, 64, 1>{});
         if (nv <= 256) return fn(ty, DistillShape<V, 64, 4>{});
         if (nv <= 1024) return fn(ty, DistillShape<V, 256, 4>{});
-        if (nv <= 4096) return fn(ty, DistillShape<V, 1024, 4>{});
-        if (nv <= 8192) return fn(ty, DistillShape<V, 1024, 8>{});
+        if (nv <= 2048) return fn(ty, DistillShape<V, 256, 8>{});
+        if (nv <= 4096) return fn(ty, DistillShape<V, 256, 16>{});
+        if (nv <= 8192) return fn(ty, DistillShape<V, 512, 16>{});
         if (nv <= 16384) return fn(ty, DistillShape<V, 1024, 16>{});
+        if (nv <= 26624) return fn(ty, DistillShape<V, 1024, 26>{});
         return fn(ty, DistillShape<V, 1024, 0>{});
     };
     if (dtype == 1) go(bf16{});
@@ -233,7 +332,7 @@ hipError_t launch_distill(int64_t N, int V, int k, int dtype, const void* z, int
                           const void* t, int t_dtype, const float* w, float tau, float* loss, void* dz, int64_t ldd,
                           hipStream_t st) {
     if (N == 0) return hipSuccess;
-    const DistillArgs a{N, V, k, z, ldz, ids, t, t_dtype == 1, w, tau, 1.f / tau, loss, dz, ldd};
+    const DistillArgs a{N, V, k, z, ldz, ids, t, t_dtype == 1, w, tau, 1.f / tau, (float)(1.4426950408889634 / tau), loss, dz, ldd};
     with_shape(V, dtype, [&](auto ty, auto sh) {
         using S = decltype(sh);
         launch(k_distill<decltype(ty), S>, dim3((unsigned)((N + S::rows - 1) / S::rows)), dim3(S::threads),

@@ -335,27 +335,8 @@ __device__ inline int tile_sequence(const ScanArgs& a, Tile t) {
 }
 
 // The registers of a thread's tokens hold the gates encoded (sigm_enc) and the other streams as loaded. Decoded gates are
-// not kept from one pass over them to the next, and the scheduler works on half a vector at a time: either would double
-// the registers, which other workgroups need to keep loads in flight.
-template <int N, int V>
-__device__ inline void forget(float (&q)[N][V]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int v = 0; v < V; ++v) asm volatile("" : "+v"(q[i][v]));
-}
-template <typename T, int N, int V>
-__device__ inline void forget(Raw<T, V> (&r)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (auto& w : r[i].w) asm volatile("" : "+v"(w));
-}
-__device__ inline float settle(float q) {  // form the value here, not where it is used
-    asm volatile("" : "+v"(q));
-    return q;
-}
-__device__ inline void one_at_a_time() { __builtin_amdgcn_sched_barrier(0); }
+// not kept from one pass over them to the next (forget), and the scheduler works on half a vector at a time: either would
+// double the registers, which other workgroups need to keep loads in flight.
 // positions of no sequence: their state and gradient pass through (f = 1), and nothing enters
 template <int NT, typename R>
 __device__ inline void outside(unsigned inside, R (&r)[NT], float x) {

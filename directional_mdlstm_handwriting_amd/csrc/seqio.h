@@ -13,60 +13,58 @@ struct bf16 {
     uint16_t u;
 };
 
-// V elements of T as they lie in memory
+// V elements of T as they lie in memory, in whole registers (4, 2 or 1 words)
+template <typename W, int N>
+struct WordsOf {
+    typedef W type __attribute__((ext_vector_type(N)));
+};
+template <typename W>
+struct WordsOf<W, 1> {
+    typedef W type;
+};
 template <typename T, int V>
 struct Raw;
 template <int V>
 struct Raw<float, V> {
-    float w[V];
-    __device__ inline void fill(float x) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) w[i] = x;
+    typename WordsOf<float, V>::type w;
+    __device__ inline void fill(float x) { w = x; }
+    __device__ inline float operator[](int i) const {
+        if constexpr (V == 1) return w;
+        else return w[i];
     }
-    __device__ inline float operator[](int i) const { return w[i]; }
 };
 template <int V>
 struct Raw<bf16, V> {
-    uint32_t w[(V + 1) / 2];  // element 2i in the low half
-    __device__ inline void fill(float x) {  // x exact in bfloat16
+    typename WordsOf<uint32_t, (V + 1) / 2>::type w;  // element 2i in the low half of word i
+    __device__ inline void fill(float x) {             // x exact in bfloat16
         const uint32_t u = __float_as_uint(x) >> 16;
-#pragma unroll
-        for (int i = 0; i < (V + 1) / 2; ++i) w[i] = u | u << 16;
+        w = u | u << 16;
     }
     __device__ inline float operator[](int i) const {
-        return __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
+        uint32_t u;
+        if constexpr (V <= 2) u = w;
+        else u = w[i >> 1];
+        return __uint_as_float((i & 1) ? (u & 0xffff0000u) : (u << 16));
     }
 };
 
-typedef uint32_t u32x2_e __attribute__((ext_vector_type(2), aligned(2), may_alias));
 typedef uint32_t u32x4_e __attribute__((ext_vector_type(4), aligned(2), may_alias));
 typedef float f32x4_e __attribute__((ext_vector_type(4), aligned(4), may_alias));
 
 template <int V>
 __device__ inline Raw<float, V> load_raw(const float* p) {
-    Raw<float, V> r;
     static_assert(V == 1 || V == 4, "16 bytes or one element");
-    if constexpr (V == 4) {
-        const f32x4_e q = *reinterpret_cast<const f32x4_e*>(p);
-        for (int i = 0; i < 4; ++i) r.w[i] = q[i];
-    } else {
-        r.w[0] = *p;
-    }
+    Raw<float, V> r;
+    if constexpr (V == 4) r.w = *reinterpret_cast<const f32x4_e*>(p);
+    else r.w = *p;
     return r;
 }
 template <int V>
 __device__ inline Raw<bf16, V> load_raw(const bf16* p) {
+    static_assert(V == 1 || V == 8, "16 bytes or one element");
     Raw<bf16, V> r;
-    static_assert(V == 1 || V == 4 || V == 8, "16 or 8 bytes, or one element");
-    if constexpr (V == 8) {
-        const u32x4_e q = *reinterpret_cast<const u32x4_e*>(p);
-        for (int i = 0; i < 4; ++i) r.w[i] = q[i];
-    } else if constexpr (V == 4) {
-        const u32x2_e q = *reinterpret_cast<const u32x2_e*>(p);
-        for (int i = 0; i < 2; ++i) r.w[i] = q[i];
-    } else {
-        r.w[0] = p->u;
-    }
+    if constexpr (V == 8) r.w = *reinterpret_cast<const u32x4_e*>(p);
+    else r.w = p->u;
     return r;
 }
 
@@ -90,8 +88,6 @@ __device__ inline void store_vec(bf16* p, const float (&v)[V]) {
     if constexpr (V == 8) {
         *reinterpret_cast<u32x4_e*>(p) =
             u32x4_e{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
-    } else if constexpr (V == 4) {
-        *reinterpret_cast<u32x2_e*>(p) = u32x2_e{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     } else {
         p->u = (uint16_t)pack_bf16(v[0], 0.f);
     }
@@ -204,5 +200,25 @@ __device__ inline void sigm_dec(float q, float& s, float& c) {
     s = neg ? t : o;
     c = neg ? o : t;
 }
+
+// Register economy. forget: what was computed from these values before is computed again when it is needed after.
+// settle: the value is formed here, not where it is used. one_at_a_time: the scheduler moves nothing across.
+template <int N, int V>
+__device__ inline void forget(float (&q)[N][V]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) asm volatile("" : "+v"(q[i][v]));
+}
+template <typename T, int N, int V>
+__device__ inline void forget(Raw<T, V> (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(r[i].w));
+}
+__device__ inline float settle(float q) {
+    asm volatile("" : "+v"(q));
+    return q;
+}
+__device__ inline void one_at_a_time() { __builtin_amdgcn_sched_barrier(0); }
 
 }  // namespace mdl

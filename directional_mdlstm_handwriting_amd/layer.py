@@ -294,27 +294,35 @@ def _device(device) -> torch.device:
 
 def _rows(name: str, t: torch.Tensor, shape, dtype, device) -> int:
     """Checks a tensor of rows (any row stride, elements of a row adjacent) and returns its row stride."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
+    if t.dtype != dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name}: need {shape} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
-    if shape[0] <= 1 and (shape[1] <= 1 or t.stride(1) == 1):
-        return max(shape[1], 1)
-    if (shape[1] > 1 and t.stride(1) != 1) or t.stride(0) < shape[1]:
-        raise ValueError(f"{name}: need adjacent elements within a row and rows that do not overlap")
-    return t.stride(0)
+    ld, inner = t.stride()
+    if inner == 1 or shape[1] <= 1:
+        if ld >= shape[1]:
+            return ld
+        if shape[0] <= 1:
+            return shape[1]
+    raise ValueError(f"{name}: need adjacent elements within a row and rows that do not overlap")
 
 
 def _same_rows(names, ts, shape, dtype, device) -> int:
     """_rows of several tensors that share one row stride (column blocks of one matrix, or separate ones); None is
-    left out. A tensor of one row takes any stride."""
-    lds = {_rows(n, t, shape, dtype, device) for n, t in zip(names, ts) if t is not None}
-    if len(lds) != 1:
-        raise ValueError(f"{', '.join(names)}: one row stride for all, got {sorted(lds)}")
-    return lds.pop()
+    left out. With one row, or none, the strides do not matter."""
+    ld = None
+    for n, t in zip(names, ts):
+        if t is None:
+            continue
+        s = _rows(n, t, shape, dtype, device)
+        if ld is None or shape[0] <= 1:
+            ld = s
+        elif s != ld:
+            raise ValueError(f"{', '.join(names)}: one row stride for all, got {ld} and {s}")
+    return ld
 
 
 def _full(name: str, t: Optional[torch.Tensor], shape, dtype, device):
     """Checks a contiguous tensor (None passes)."""
-    if t is not None and (t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous()):
+    if t is not None and (t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous()):
         raise ValueError(f"{name}: need contiguous {shape} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} on "
                          f"{t.device}")
 

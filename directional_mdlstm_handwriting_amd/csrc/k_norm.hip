@@ -180,6 +180,16 @@ __global__ __launch_bounds__(S::threads) void k_norm_bwd(NormArgs a) {
             row_sums<S::R>(s, red);
             sig = __builtin_amdgcn_rsqf(__builtin_fmaf(s[0], a.inv_d, a.eps));
         }
+        // long rows: what was unpacked for one walk over the row is unpacked again for the next
+        auto anew = [&] {
+            if constexpr (NV >= 4) {
+                one_at_a_time();
+                if (a.z) forget(z);
+                if (a.u) forget(u);
+                if (a.dv) forget(dv);
+            }
+        };
+        anew();
         float d[NV][V];
         if (a.dv) {
             float r[NV][V], s[2] = {0.f, 0.f};
@@ -200,6 +210,7 @@ __global__ __launch_bounds__(S::threads) void k_norm_bwd(NormArgs a) {
             row_sums<S::R>(s, red);
             const float rho = __builtin_amdgcn_rsqf(__builtin_fmaf(s[0], a.inv_d, a.eps));
             const float m = s[1] * rho * a.inv_d;  // m(t rh)
+            anew();
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -215,6 +226,7 @@ __global__ __launch_bounds__(S::threads) void k_norm_bwd(NormArgs a) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) d[i][v] = dr[i][v];
         }
+        anew();
         float pz[NV][V], du[NV][V];
         float s[1] = {0.f};
         if (a.z) {
@@ -319,8 +331,9 @@ void with_shape(int D, int dtype, F&& fn) {
         if (nv <= 128) return fn(ty, NormShape<V, 64, 2>{});
         if (nv <= 256) return fn(ty, NormShape<V, 256, 1>{});
         if (nv <= 512) return fn(ty, NormShape<V, 256, 2>{});
-        if (nv <= 1024) return fn(ty, NormShape<V, 1024, 1>{});
-        if (nv <= 2048) return fn(ty, NormShape<V, 1024, 2>{});
+        if (nv <= 1024) return fn(ty, NormShape<V, 512, 2>{});
+        if constexpr (V == 8) return fn(ty, NormShape<V, 1024, 2>{});
+        if (nv <= 2048) return fn(ty, NormShape<V, 512, 4>{});
         return fn(ty, NormShape<V, 1024, 4>{});
     };
     if (dtype == 1) go(bf16{});

@@ -472,7 +472,7 @@ __global__ __launch_bounds__(SCAN_THREADS, 4) void k_scan_fwd(ScanArgs a) {
 // Backward: the tile's states again from its incoming one in a.carry, and the reverse recurrence, whose tiles are
 // chained from the last to the first.
 template <typename T, int V, int CL, int NT>
-__global__ __launch_bounds__(SCAN_THREADS, V == 8 ? 3 : 4) void k_scan_bwd(ScanArgs a) {
+__global__ __launch_bounds__(SCAN_THREADS, V == 4 ? 4 : 3) void k_scan_bwd(ScanArgs a) {
     constexpr int G = SCAN_THREADS / CL, TT = G * NT, CB = CL * V, HV = V > 4 ? 4 : V;
     constexpr int CW = (CB + 63) / 64 * 64;
     static_assert(2 * CW <= SCAN_THREADS, "two sets of one thread per channel");
@@ -701,13 +701,16 @@ __global__ __launch_bounds__(256) void k_scan_step(int S, int D, const T* __rest
     }
 }
 
-// the tile shape for a row: a vector of 16 bytes a thread (one element where the row is shorter), as many lanes along
-// the row as it fills, at most 8; forward and backward have the same
+// the tile shape for a row: a vector of 16 bytes a thread and as many lanes along the row as it fills, at most 8; rows of
+// no more than one vector take one element a lane and more tokens instead; forward and backward have the same
 template <typename F>
 void with_shape(int D, int dtype, F&& fn) {
     auto go = [&](auto ty) {
         constexpr int V = Width<decltype(ty)>::v;
-        if (D < V) return fn(ty, ScanShape<1, 8, 4>{});
+        if (D <= 4) return fn(ty, ScanShape<1, 4, 16>{});
+        if constexpr (V > 4) {
+            if (D <= V) return fn(ty, ScanShape<1, 8, 16>{});
+        }
         const int lanes = (D + V - 1) / V;
         if (lanes <= 4) return fn(ty, ScanShape<V, 4, 4>{});
         return fn(ty, ScanShape<V, 8, 4>{});

@@ -340,8 +340,12 @@ void with_shape(int D, int dtype, F&& fn) {
     else go(float{});
 }
 
-// workgroups of the backward: each leaves 8 D bytes of column sums, so no more than fill the device a few times
-int bwd_blocks(int64_t N, int rows) { return (int)std::max<int64_t>(1, std::min<int64_t>((N + rows - 1) / rows, 1024)); }
+// workgroups of the backward: each leaves 8 D bytes of column sums, so at least four turns each where there are rows
+// enough to fill the device with a quarter of that many, and no more than fill it a few times
+int bwd_blocks(int64_t N, int rows) {
+    const int64_t turns = (N + rows - 1) / rows;
+    return (int)std::max<int64_t>(1, std::min(turns, std::max<int64_t>(256, std::min<int64_t>(turns / 4, 1024))));
+}
 
 }  // namespace
 

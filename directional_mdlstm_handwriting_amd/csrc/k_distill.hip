@@ -168,10 +168,11 @@ __global__ __launch_bounds__(S::threads, 4) void k_distill(DistillArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             one_at_a_time();
-            q[i] = load_raw<V>(z + min((lane + i * R) * V, a.V - V));
+            if (i / kAhead * kAhead * R * V < a.V) q[i] = load_raw<V>(z + min((lane + i * R) * V, a.V - V));
         }
 #pragma unroll
         for (int i = 0; i < NV; i += kAhead) {
+            if (i * R * V >= a.V) continue;  // none of the row's lanes has a part in these
             one_at_a_time();
             const int at = anew(lane);
 #pragma unroll
@@ -253,6 +254,7 @@ __global__ __launch_bounds__(S::threads, 4) void k_distill(DistillArgs a) {
     } else if constexpr (!kTwice) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+            if (i * R * V >= a.V) continue;
             const int c = (anew(lane) + i * R) * V, skip = c - (a.V - V);
             float o[V];
             one_at_a_time();

@@ -215,6 +215,23 @@ def test_strides_alignment_and_in_place(D, dtype):
     assert torch.equal(x, ref["r"]) and torch.equal(z, ref["v"])
 
 
+def test_more_than_2_31_elements():
+    """Rows past 2^31 elements: the last rows' results are those of a small call on them alone."""
+    N, D = 1100003, 2000
+    print(f"[gpu] norm N={N} D={D}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    t = make(9, 4, D, "bf16")
+    for k in ("x", "z", "u", "dr", "dv"):
+        t[k] = torch.randn(N, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    bn = BlockNorm(N, D, "bf16", device=DEV)
+    got = dict(zip(NAMES, (*bn.forward(*(t[k] for k in INPUTS)),
+                           *bn.backward(*(t[k] for k in INPUTS), t["dr"], t["dv"]))))
+    small = {k: (v[N - 7:].contiguous() if v.dim() == 2 else v) for k, v in t.items()}
+    ref = run(BlockNorm(7, D, "bf16", device=DEV), small)
+    for k in NAMES[:5]:
+        assert torch.equal(got[k][N - 7:], ref[k]), k
+
+
 def test_captured_backward_replays():
     N, D = 700, 96
     sets = [make(40 + i, N, D, "bf16") for i in range(2)]

@@ -116,6 +116,31 @@ def test_kept_counts(k):
     run(z, ids, t, w, 1.0, "f32")
 
 
+@pytest.mark.parametrize("V,dtype", [(128, "bf16"), (256, "bf16"), (512, "bf16"), (1024, "bf16"), (128, "f32"), (512, "f32")])
+def test_every_class_kept(V, dtype):
+    """As many kept classes as there are: the most LDS that a workgroup's rows can ask for."""
+    z, ids, t, w = make(V, 70, V, V, dtype)
+    run(z, ids, t, w, 1.3, dtype)
+
+
+def test_more_than_2_31_elements():
+    """Rows past 2^31 elements: the last rows' results are those of a small call on them alone."""
+    N, V, k = 36000, 60001, 4
+    g = torch.Generator(device=DEV).manual_seed(3)
+    print(f"[gpu] distill N={N} V={V}", flush=True)
+    z = torch.empty(N, V, dtype=torch.bfloat16, device=DEV)
+    for a in range(0, N, 4000):
+        z[a:a + 4000] = torch.randn(4000, V, generator=g, device=DEV, dtype=torch.bfloat16)
+    ids = torch.randint(0, V, (N, k), generator=g, device=DEV, dtype=torch.int32)
+    t = torch.randn(N, k, generator=g, device=DEV)
+    loss, dz = TopKDistill(N, V, k, "bf16", 1.5, device=DEV).run(z, ids, t)
+    part = slice(N - 5, N)
+    l2, d2 = TopKDistill(5, V, k, "bf16", 1.5, device=DEV).run(z[part], ids[part].contiguous(), t[part].contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(loss[part], l2) and torch.equal(dz[part], d2)
+    check(z[part], ids[part], t[part], None, 1.5, l2, d2, "bf16")
+
+
 @pytest.mark.parametrize("V", [6, 100, 500, 3001, 90001])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_rows_that_count_for_nothing_and_masked_classes(V, dtype):

@@ -399,6 +399,27 @@ def test_image_rows_of_a_packed_layout():
     run(off, int(off[-1]), 16, "f32", reverse=True)
 
 
+@pytest.mark.parametrize("reverse", [False, True])
+def test_more_than_2_31_elements(reverse):
+    """Tokens past 2^31 elements: a sequence there, cut out at tile borders, gives the same bits alone."""
+    D, L = 2056, 512 * 3
+    T = 512 * 2100
+    print(f"[gpu] scan T={T} D={D} reverse={reverse}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    zf, gg, dy = (torch.randn(T, D, generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(3))
+    h0, dhT = torch.randn(2, D, generator=g, device=DEV), torch.randn(2, D, generator=g, device=DEV)
+    sc = SequenceScan([0, T - L, T], T, D, "bf16", reverse=reverse, device=DEV)
+    got = (*sc.forward(zf, gg, None, h0), *sc.backward(zf, gg, None, dy, h0, dhT))
+    part = slice(T - L, T)
+    one = SequenceScan([0, L], L, D, "bf16", reverse=reverse, device=DEV)
+    a = (zf[part], gg[part], None)
+    ref = (*one.forward(*a, h0[1:].contiguous()), *one.backward(*a, dy[part], h0[1:].contiguous(), dhT[1:].contiguous()))
+    torch.cuda.synchronize()
+    for i in (0, 2, 3):
+        assert torch.equal(got[i][part], ref[i]), i
+    assert torch.equal(got[1][1:], ref[1]) and torch.equal(got[5][1:], ref[5])
+
+
 def test_no_tokens_at_all():
     h = torch.randn(3, 6, device=DEV)
     z = torch.empty(0, 6, device=DEV)

@@ -973,7 +973,8 @@ static int check_scan(const std::string& F, int64_t T, int32_t D, int32_t dtype,
     if (T < 0 || D < 1) return fail(MDL_EINVAL, F + ": need T >= 0 and D >= 1");
     if (T >= (int64_t(1) << 60) / D) return fail(MDL_EOVERFLOW, F + ": rows times channels reach 2^60");
     const mdl::ScanPlan p = mdl::scan_plan(T, D, dtype);
-    if (p.ntiles >= (int64_t(1) << 31) / p.ncb) return fail(MDL_EOVERFLOW, F + ": the launch reaches 2^31 workgroups");
+    if (p.ntiles > mdl::kMaxLaunchThreads / 256 / p.ncb)
+        return fail(MDL_EOVERFLOW, F + ": the launch exceeds 2^31 threads");
     need = p.total;
     return MDL_OK;
 }
@@ -1087,6 +1088,7 @@ int mdl_scan_step(int32_t S, int32_t D, int32_t dtype, const void* zf, const voi
     if (rc) return rc;
     if (S < 1 || D < 1 || n_slots < 1) return fail(MDL_EINVAL, F + ": need S, D and n_slots >= 1");
     if (!zf || !g || !h_in || !h_out || !y) return fail(MDL_EINVAL, F + ": null tensor");
+    if ((int64_t)S * D > mdl::kMaxLaunchThreads) return fail(MDL_EOVERFLOW, F + ": S times D exceeds 2^31");
     if (!slots && n_slots < S) return fail(MDL_EINVAL, F + ": n_slots below S without slots");
     if ((rc = check_stride(F, "ldz", S, D, ldz)) || (rc = check_stride(F, "ldy", S, D, ldy))) return rc;
     hipError_t e;
@@ -1106,7 +1108,7 @@ static int check_norm(const std::string& F, int64_t N, int32_t D, int32_t dtype)
     if (rc) return rc;
     if (N < 0 || D < 1) return fail(MDL_EINVAL, F + ": need N >= 0 and D >= 1");
     if (D > mdl::norm_max_d()) return fail(MDL_EUNSUPPORTED, F + ": D above " + std::to_string(mdl::norm_max_d()));
-    if (N >= (int64_t(1) << 31)) return fail(MDL_EOVERFLOW, F + ": the launch reaches 2^31 workgroups");
+    if (N >= (int64_t(1) << 40)) return fail(MDL_EOVERFLOW, F + ": N reaches 2^40");
     return MDL_OK;
 }
 static int check_norm_parts(const std::string& F, const mdl::NormArgs& a) {
@@ -1235,9 +1237,9 @@ int mdl_distill(int64_t N, int32_t V, int32_t k, int32_t dtype, const void* z, i
     if (rc || (rc = check_dtype(F, t_dtype))) return rc;
     if (N < 0 || V < 1 || k < 1 || k > V) return fail(MDL_EINVAL, F + ": need N >= 0, V >= 1 and k in [1, V]");
     if (k > mdl::distill_max_k()) return fail(MDL_EUNSUPPORTED, F + ": k above " + std::to_string(mdl::distill_max_k()));
-    if (N >= (int64_t(1) << 31)) return fail(MDL_EOVERFLOW, F + ": the launch reaches 2^31 workgroups");
+    if (N >= (int64_t(1) << 40)) return fail(MDL_EOVERFLOW, F + ": N reaches 2^40");
     if (N > 0 && (!z || !ids || !t || !loss)) return fail(MDL_EINVAL, F + ": null tensor");
-    if (!(tau > 0.f && tau < INFINITY)) return fail(MDL_EINVAL, F + ": tau must be finite and positive");
+    if (!(tau >= 1e-30f && tau < INFINITY)) return fail(MDL_EINVAL, F + ": tau must be finite and at least 1e-30");
     if ((rc = check_stride(F, "ldz", N, V, ldz))) return rc;
     if (dz && (rc = check_stride(F, "ldd", N, V, ldd))) return rc;
     hipError_t e;

@@ -13,6 +13,8 @@
 #include "kernels.h"
 #include "seqio.h"
 
+#include <algorithm>
+
 namespace mdl {
 
 namespace {
@@ -339,12 +341,20 @@ int distill_max_k() { return 1024; }
 hipError_t launch_distill(int64_t N, int V, int k, int dtype, const void* z, int64_t ldz, const int32_t* ids,
                           const void* t, int t_dtype, const float* w, float tau, float* loss, void* dz, int64_t ldd,
                           hipStream_t st) {
-    if (N == 0) return hipSuccess;
-    const DistillArgs a{N, V, k, z, ldz, ids, t, t_dtype == 1, w, tau, 1.f / tau, (float)(1.4426950408889634 / tau), loss, dz, ldd};
     with_shape(V, dtype, [&](auto ty, auto sh) {
+        using T = decltype(ty);
         using S = decltype(sh);
-        launch(k_distill<decltype(ty), S>, dim3((unsigned)((N + S::rows - 1) / S::rows)), dim3(S::threads),
-               sizeof(float) * 3 * k * S::rows, st, a);
+        const int64_t most = kMaxLaunchThreads / S::threads * S::rows;  // rows a launch can take
+        for (int64_t n = 0; n < N; n += most) {
+            const int64_t m = std::min(most, N - n);
+            const void* tn = t_dtype == 1 ? static_cast<const void*>(static_cast<const bf16*>(t) + n * k)
+                                          : static_cast<const void*>(static_cast<const float*>(t) + n * k);
+            const DistillArgs a{m, V, k, static_cast<const T*>(z) + n * ldz, ldz, ids + n * k, tn, t_dtype == 1,
+                                w ? w + n : nullptr, tau, 1.f / tau, (float)(1.4426950408889634 / tau), loss + n,
+                                dz ? static_cast<T*>(dz) + n * ldd : nullptr, ldd};
+            launch(k_distill<T, S>, dim3((unsigned)((m + S::rows - 1) / S::rows)), dim3(S::threads),
+                   sizeof(float) * 3 * k * S::rows, st, a);
+        }
     });
     return hipGetLastError();
 }

@@ -358,10 +358,20 @@ size_t norm_bwd_ws(int64_t N, int D, int dtype) {
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, int dtype, hipStream_t st) {
-    if (a.N == 0) return hipSuccess;
     with_shape(a.D, dtype, [&](auto ty, auto sh) {
+        using T = decltype(ty);
         using S = decltype(sh);
-        launch(k_norm_fwd<decltype(ty), S>, dim3((unsigned)((a.N + S::rows - 1) / S::rows)), dim3(S::threads), 0, st, a);
+        const int64_t most = kMaxLaunchThreads / S::threads * S::rows;  // rows a launch can take
+        for (int64_t n = 0; n < a.N; n += most) {
+            NormArgs b = a;
+            b.N = std::min(most, a.N - n);
+            b.x = static_cast<const T*>(a.x) + n * a.ldx;
+            if (a.z) b.z = static_cast<const T*>(a.z) + n * a.ldz;
+            if (a.u) b.u = static_cast<const T*>(a.u) + n * a.ldu;
+            if (a.r) b.r = static_cast<T*>(a.r) + n * a.ldr;
+            if (a.v) b.v = static_cast<T*>(a.v) + n * a.ldr;
+            launch(k_norm_fwd<T, S>, dim3((unsigned)((b.N + S::rows - 1) / S::rows)), dim3(S::threads), 0, st, b);
+        }
     });
     return hipGetLastError();
 }

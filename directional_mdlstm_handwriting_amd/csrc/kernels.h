@@ -299,6 +299,9 @@ hipError_t launch_ctc_head(const Dev& D, const float* y_flat, int H, const float
                            float* ws, float* loss, float* dy_flat, float* dW, float* db, size_t lds_limit,
                            hipStream_t st);
 
+// threads of one launch (workgroups times their size, which has to stay below 2^32)
+constexpr int64_t kMaxLaunchThreads = int64_t(1) << 31;
+
 // the gated linear recurrence over packed sequences (k_scan.hip)
 struct ScanArgs {
     const int64_t* off;           // [S + 1] first token of each sequence

@@ -465,8 +465,8 @@ int mdl_ctc_head(const mdl_layout* layout, const void* d_desc, const float* y_fl
  * unknown dtype, dzo without zo or zo without dzo, n_slots < 1, slots NULL with
  * n_slots < S, or a misaligned workspace; MDL_ESIZE for a short workspace;
  * MDL_EOVERFLOW when rows times a stride reach 2^60, a stride of the forward or
- * backward 2^31 or the launch 2^31 workgroups. With T = 0 the token tensors may
- * be NULL.
+ * backward 2^31, the launch exceeds 2^31 threads (each of them takes 16 elements
+ * or more), or S D of a step 2^31. With T = 0 the token tensors may be NULL.
  */
 int mdl_scan_workspace_size(int64_t T, int32_t D, int32_t dtype, size_t* bytes);
 int mdl_scan_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, int32_t dtype, int32_t reverse,
@@ -506,8 +506,7 @@ int mdl_scan_step(int32_t S, int32_t D, int32_t dtype, const void* zf, const voi
  * Errors: MDL_EINVAL for null tensors or parts that do not go together, N < 0,
  * D < 1, a stride below D, an unknown dtype, eps that is not finite and >= 0,
  * or a misaligned workspace; MDL_EUNSUPPORTED for D > 16384; MDL_EOVERFLOW when
- * rows times a stride reach 2^60 or the launch 2^31 workgroups; MDL_ESIZE for a
- * short workspace.
+ * N reaches 2^40 or rows times a stride 2^60; MDL_ESIZE for a short workspace.
  */
 int mdl_blocknorm_forward(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx, const void* z, int64_t ldz,
                           const void* u, int64_t ldu, const float* w_post, const float* scale, const float* w_pre,
@@ -532,12 +531,13 @@ int mdl_blocknorm_backward(int64_t N, int32_t D, int32_t dtype, const void* x, i
  * whose slots are all empty, or of weight 0, counts for nothing, whatever z
  * holds: loss 0, gradient 0. Any other id outside [0, V) gives loss NaN and
  * gradient 0 (found on the device). A class named twice counts with both
- * probabilities. A kept logit of -inf has p = 0 and adds nothing. Statistics
+ * probabilities. A kept logit of -inf has p = 0 and adds nothing (a row that
+ * keeps no other: NaN, as one whose z are all -inf). Statistics
  * and loss are float32; the gradient is rounded once. No workspace.
  * Errors: MDL_EINVAL for null tensors, N < 0, V < 1, k outside [1, V], a stride
- * below V, an unknown dtype, or tau that is not finite and positive;
- * MDL_EUNSUPPORTED for k > 1024; MDL_EOVERFLOW when rows times a stride reach
- * 2^60 or the launch 2^31 workgroups.
+ * below V, an unknown dtype, or tau that is not finite or below 1e-30;
+ * MDL_EUNSUPPORTED for k > 1024; MDL_EOVERFLOW when N reaches 2^40 or rows times
+ * a stride 2^60.
  */
 int mdl_distill(int64_t N, int32_t V, int32_t k, int32_t dtype, const void* z, int64_t ldz, const int32_t* ids,
                 const void* t, int32_t t_dtype, const float* w, float tau, float* loss, void* dz, int64_t ldd,

@@ -232,6 +232,18 @@ def test_more_than_2_31_elements():
         assert torch.equal(got[k][N - 7:], ref[k]), k
 
 
+def test_more_rows_than_one_launch_takes():
+    N = (1 << 28) + 5
+    print(f"[gpu] norm N={N} D=1", flush=True)
+    x = torch.randn(N, 1, device=DEV, dtype=torch.bfloat16)
+    w = torch.full((1,), 0.5, device=DEV)
+    _, v = BlockNorm(N, 1, "bf16", eps=0.25, device=DEV).forward(x, w_pre=w)
+    torch.cuda.synchronize()
+    for s in (slice(0, 7), slice((1 << 28) - 3, N)):
+        ref = (x[s].double() * 0.5 / torch.sqrt(x[s].double() ** 2 + 0.25)).cpu().numpy()
+        assert_within("v", _np(v[s]), Err(ref, 16 * U * np.abs(ref)), 2.0 ** -8)
+
+
 def test_captured_backward_replays():
     N, D = 700, 96
     sets = [make(40 + i, N, D, "bf16") for i in range(2)]

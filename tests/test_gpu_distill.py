@@ -141,6 +141,18 @@ def test_more_than_2_31_elements():
     check(z[part], ids[part], t[part], None, 1.5, l2, d2, "bf16")
 
 
+def test_more_rows_than_one_launch_takes():
+    N = (1 << 28) + 3
+    print(f"[gpu] distill N={N} V=2", flush=True)
+    z = torch.randn(N, 2, device=DEV, dtype=torch.bfloat16)
+    ids = torch.ones(N, 1, dtype=torch.int32, device=DEV)
+    t = torch.zeros(N, 1, device=DEV)
+    loss, dz = TopKDistill(N, 2, 1, "bf16", 1.0, device=DEV).run(z, ids, t)
+    torch.cuda.synchronize()
+    for s in (slice(0, 5), slice((1 << 28) - 4, N)):
+        check(z[s], ids[s], t[s], None, 1.0, loss[s], dz[s], "bf16")
+
+
 @pytest.mark.parametrize("V", [6, 100, 500, 3001, 90001])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_rows_that_count_for_nothing_and_masked_classes(V, dtype):

@@ -217,6 +217,66 @@ def test_a_sequence_with_nan_keeps_it_to_itself(dtype):
     assert torch.isnan(got[1][1]).all()
 
 
+def test_nan_gates_stay_in_their_sequence():
+    """NaN in the gates themselves, where whole tiles' maps become NaN: the sequences around keep their bits."""
+    off = _off([300, 900, 300])
+    T, D = int(off[-1]), 8
+    for dtype in ("f32", "bf16"):
+        zf, g, zo, h, dy, dhT = _inputs(14, T, 3, D, dtype)
+        sc = SequenceScan(off, T, D, dtype, device=DEV)
+        clean = [t.clone() for t in (*sc.forward(zf, g, zo, h), *sc.backward(zf, g, zo, dy, h, dhT))]
+        p = torch.cat([zf, g, zo], 1)
+        p[off[1] + 400, :D] = float("nan")
+        p[off[1] + 500, 2 * D:] = -float("nan")
+        a = (p[:, :D], p[:, D:2 * D], p[:, 2 * D:])
+        got = (*sc.forward(*a, h), *sc.backward(*a, dy, h, dhT))
+        torch.cuda.synchronize()
+        keep = torch.ones(T, dtype=torch.bool, device=DEV)
+        keep[off[1]:off[2]] = False
+        for i in (0, 2, 3, 4):
+            assert torch.equal(got[i][keep], clean[i][keep]), (dtype, i)
+        for i in (1, 5):
+            assert torch.equal(got[i][[0, 2]], clean[i][[0, 2]]), (dtype, i)
+        assert torch.equal(got[0][:off[1] + 400], clean[0][:off[1] + 400])
+        assert torch.isnan(got[0][off[1] + 400:off[2]].float()).all() and torch.isnan(got[5][1]).all()
+
+
+def test_sequences_without_tokens_only():
+    """Tokens in no sequence at all, and sequences that are all empty: at the front, at the end, in between."""
+    T, D = 700, 12
+    zf, g, zo, h, dy, dhT = _inputs(15, T, 5, D, "f32")
+    for off in ([0] * 6, [T] * 6, [0, 0, 300, 300, T, T], [333] * 6):
+        off = np.array(off)
+        for reverse in (False, True):
+            sc = SequenceScan(off, T, D, "f32", reverse=reverse, device=DEV)
+            y, hT = sc.forward(zf, g, zo, h)
+            dzf, dg, dzo, dh0 = sc.backward(zf, g, zo, dy, h, dhT)
+            torch.cuda.synchronize()
+            empty = torch.as_tensor(np.diff(off) == 0, device=DEV)
+            assert torch.equal(hT[empty], h[empty]) and torch.equal(dh0[empty], dhT[empty])
+            check(off.tolist(), zf, g, zo, h, dy, dhT, reverse, "f32", (y, hT, dzf, dg, dzo, dh0))
+            sc.forward(zf, g, zo)
+            assert not sc.hT[empty].any()
+
+
+def test_outputs_that_are_left_out():
+    """No last states, no gradient of them, no gradient of the first ones: the other outputs keep their bits."""
+    off = _off([90, 200, 0, 41])
+    T, D, S = int(off[-1]), 40, 4
+    zf, g, zo, h, dy, _ = _inputs(16, T, S, D, "bf16")
+    sc = SequenceScan(off, T, D, "bf16", device=DEV)
+    zero = torch.zeros(S, D, device=DEV)
+    ref = [t.clone() for t in (*sc.forward(zf, g, zo, zero), *sc.backward(zf, g, zo, dy, zero, zero))]
+    ld = zf.stride(0)
+    y, dzf, dg, dzo = (torch.empty(T, D, dtype=torch.bfloat16, device=DEV) for _ in range(4))
+    M.mdl_scan_forward(sc.off, S, T, D, 1, 0, zf, g, zo, ld, None, y, D, None, sc.ws, sc.ws_bytes)
+    M.mdl_scan_backward(sc.off, S, T, D, 1, 0, zf, g, zo, ld, None, dy, D, None, dzf, dg, dzo, D, None, sc.ws,
+                        sc.ws_bytes)
+    torch.cuda.synchronize()
+    for a, b in zip((y, dzf, dg, dzo), (ref[0], *ref[2:5])):
+        assert torch.equal(a, b)
+
+
 def test_gates_at_infinity():
     """f = 1 holds the state, f = 0 takes the input; the gradients follow."""
     off = _off([6])

@@ -55,7 +55,7 @@ def test_scan_backward_refuses(change, code):
     (dict(S=0), M.MDL_EINVAL), (dict(D=0), M.MDL_EINVAL), (dict(n_slots=0), M.MDL_EINVAL), (dict(zf=None), M.MDL_EINVAL),
     (dict(h_in=None), M.MDL_EINVAL), (dict(h_out=None), M.MDL_EINVAL), (dict(y=None), M.MDL_EINVAL),
     (dict(slots=None, n_slots=3), M.MDL_EINVAL), (dict(ldz=7), M.MDL_EINVAL), (dict(ldy=7), M.MDL_EINVAL),
-    (dict(dtype=9), M.MDL_EINVAL),
+    (dict(dtype=9), M.MDL_EINVAL), (dict(S=1 << 30, n_slots=1 << 30), M.MDL_EOVERFLOW),
 ])
 def test_scan_step_refuses(change, code):
     assert _code(M.mdl_scan_step, **_with(STEP, **change)) == code
@@ -86,7 +86,7 @@ DISTILL = dict(N=10, V=80, k=8, dtype=M.MDL_F32, z=P, ldz=80, ids=P, t=P, t_dtyp
     (dict(eps=float("nan")), M.MDL_EINVAL), (dict(eps=float("inf")), M.MDL_EINVAL),
     (dict(z=None, u=None, w_post=None, scale=None, r=None, w_pre=None, v=None), M.MDL_EINVAL),
     (dict(D=16385, ldx=16385, ldz=16385, ldu=16385, ldr=16385), M.MDL_EUNSUPPORTED),
-    (dict(N=1 << 31), M.MDL_EOVERFLOW), (dict(ldx=1 << 59), M.MDL_EOVERFLOW),
+    (dict(N=1 << 40), M.MDL_EOVERFLOW), (dict(ldx=1 << 59), M.MDL_EOVERFLOW),
 ])
 def test_blocknorm_forward_refuses(change, code):
     assert _code(M.mdl_blocknorm_forward, **_with(NORM_F, **change)) == code
@@ -115,7 +115,8 @@ def test_blocknorm_workspace_sizes():
     (dict(k=81), M.MDL_EINVAL), (dict(dtype=2), M.MDL_EINVAL), (dict(t_dtype=2), M.MDL_EINVAL),
     (dict(tau=0.0), M.MDL_EINVAL), (dict(tau=-1.0), M.MDL_EINVAL), (dict(tau=float("nan")), M.MDL_EINVAL),
     (dict(tau=float("inf")), M.MDL_EINVAL), (dict(ldz=79), M.MDL_EINVAL), (dict(ldd=79), M.MDL_EINVAL),
-    (dict(V=5000, ldz=5000, ldd=5000, k=1025), M.MDL_EUNSUPPORTED), (dict(N=1 << 31), M.MDL_EOVERFLOW),
+    (dict(V=5000, ldz=5000, ldd=5000, k=1025), M.MDL_EUNSUPPORTED), (dict(N=1 << 40), M.MDL_EOVERFLOW),
+    (dict(tau=1e-31), M.MDL_EINVAL),
 ])
 def test_distill_refuses(change, code):
     assert _code(M.mdl_distill, **_with(DISTILL, **change)) == code

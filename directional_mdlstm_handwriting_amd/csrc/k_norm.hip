@@ -13,6 +13,10 @@
 // again from x, z and u, so it needs no row statistics of the forward). Row sums are exchanged between the lanes, and
 // between waves through LDS where a row takes more than one. r enters the second norm as the fp32 value, before its
 // rounding to the output's type. All sums are fp32.
+//
+// Bound by HBM: 20480 x 2048 in bfloat16 takes 81 us forward (419 MB, 5.2 TB/s) and 137 us backward (671 MB, 4.9 TB/s) and
+// 7.4 us for the weight gradients out of the workgroups' column sums; 81920 x 50 in fp32, rows of 200 bytes, 14.2, 24.2
+// and 4.0 us (82, 131 and 0.8 MB, much of it still in the memory-side cache).
 #include "kernels.h"
 #include "seqio.h"
 
@@ -317,6 +321,9 @@ __global__ __launch_bounds__(kWredCols * kWredGroups) void k_norm_wreduce(
     if (dscale) dscale[i] = w_post ? s * w_post[i] : s;
 }
 
+// Lanes a row: the fewest that hold it in one vector each up to a wave, two vectors each up to 128 (the row sums then need
+// no LDS), and from there as many waves as keep the backward's row in its registers (five tensors, 224 registers at two
+// vectors of eight). Rows of more than 8192 elements spill some of them.
 template <typename F>
 void with_shape(int D, int dtype, F&& fn) {
     auto go = [&](auto ty) {

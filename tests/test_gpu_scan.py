@@ -316,6 +316,36 @@ def test_results_repeat_bit_for_bit_on_any_stream():
         assert again2[0] is again[0]
 
 
+def test_two_calls_at_once():
+    """Two scans on two streams, each with a workspace of its own, while a third stream keeps the device busy."""
+    lens = [4000, 9000, 1, 6000]
+    off = _off(lens)
+    T, D = int(off[-1]), 128
+    sets = [_inputs(60 + i, T, 4, D, "bf16") for i in range(2)]
+    scans = [SequenceScan(off, T, D, "bf16", reverse=bool(i), device=DEV) for i in range(2)]
+
+    def both(sc, s):
+        return (*sc.forward(*s[:4]), *sc.backward(s[0], s[1], s[2], s[4], s[3], s[5]))
+
+    ref = [[t.clone() for t in both(sc, s)] for sc, s in zip(scans, sets)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    noise = torch.randn(2048, 2048, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(streams[2]):
+            for _ in range(3):
+                noise @ noise
+        out = []
+        for st, sc, s in zip(streams, scans, sets):
+            with torch.cuda.stream(st):
+                out.append(both(sc, s))
+        torch.cuda.synchronize()
+        for a, b in zip(out, ref):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("reverse", [False, True])
 def test_tiles_that_wait_for_nothing(reverse, dtype):

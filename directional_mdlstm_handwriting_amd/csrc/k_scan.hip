@@ -376,13 +376,17 @@ __global__ __launch_bounds__(SCAN_THREADS, 4) void k_scan_fwd(ScanArgs a) {
     const Seq seq(a, tile_sequence<TT>(a, tile));
     Raw<T, V> rf[NT], rg[NT], ro[NT];
     const int64_t bz = me.base(a.ldz);
+    auto rows = [&](auto&& load) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int64_t t = me.at(i, a.ldz, bz);
-        rf[i] = load_raw<V>(static_cast<const T*>(a.zf) + t);
-        rg[i] = load_raw<V>(static_cast<const T*>(a.g) + t);
-        if (a.zo) ro[i] = load_raw<V>(static_cast<const T*>(a.zo) + t);
-    }
+        for (int i = 0; i < NT; ++i) {
+            const int64_t t = me.at(i, a.ldz, bz);
+            rf[i] = load(static_cast<const T*>(a.zf) + t);
+            rg[i] = load(static_cast<const T*>(a.g) + t);
+            if (a.zo) ro[i] = load(static_cast<const T*>(a.zo) + t);
+        }
+    };
+    if (a.once) rows([](const T* p) { return load_once<V>(p); });
+    else rows([](const T* p) { return load_raw<V>(p); });
     mark_tile<TT, CB>(a, tile, seq, start, last, a.h0, a.hT);
     outside(me.inside, rf, INFINITY);
     outside(me.inside, rg, 0.f);
@@ -493,15 +497,19 @@ __global__ __launch_bounds__(SCAN_THREADS, V == 4 ? 4 : 3) void k_scan_bwd(ScanA
     const Seq seq(a, tile_sequence<TT>(a, tile));
     Raw<T, V> rf[NT], rg[NT], ro[NT], rd[NT];
     const int64_t bz = me.base(a.ldz), by = me.base(a.ldy);
+    auto rows = [&](auto&& load) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int64_t t = me.at(i, a.ldz, bz);
-        rf[i] = load_raw<V>(static_cast<const T*>(a.zf) + t);
-        rg[i] = load_raw<V>(static_cast<const T*>(a.g) + t);
-        if (a.zo) ro[i] = load_raw<V>(static_cast<const T*>(a.zo) + t);
-        else ro[i].fill(INFINITY);  // an open gate
-        rd[i] = load_raw<V>(static_cast<const T*>(a.dy) + me.at(i, a.ldy, by));
-    }
+        for (int i = 0; i < NT; ++i) {
+            const int64_t t = me.at(i, a.ldz, bz);
+            rf[i] = load(static_cast<const T*>(a.zf) + t);
+            rg[i] = load(static_cast<const T*>(a.g) + t);
+            if (a.zo) ro[i] = load(static_cast<const T*>(a.zo) + t);
+            else ro[i].fill(INFINITY);  // an open gate
+            rd[i] = load(static_cast<const T*>(a.dy) + me.at(i, a.ldy, by));
+        }
+    };
+    if (a.once) rows([](const T* p) { return load_once<V>(p); });
+    else rows([](const T* p) { return load_raw<V>(p); });
     mark_tile<TT, CB>(a, tile, seq, start, last, a.dhT, a.dh0);
     outside(me.inside, rf, INFINITY);
     outside(me.inside, rg, 0.f);
@@ -764,6 +772,9 @@ static hipError_t scan_run(ScanArgs a, int dtype, void* ws, bool backward, hipSt
         a.seq = reinterpret_cast<int32_t*>(w + p.seq);
         a.carry = reinterpret_cast<float*>(w + p.carry);
     }
+    // Streams larger than the memory-side cache are read past it: nothing of them would be found there again (208246 x
+    // 1024 in bfloat16, 426 MB a stream, both ways: 925 us, 961 otherwise; 656603 x 32 in fp32, 84 MB a stream: 142 and 127).
+    a.once = a.T * a.D >= (int64_t(256) << 20) / (dtype == 1 ? 2 : 4);
     const dim3 grid((unsigned)(p.ntiles * p.ncb)), block(SCAN_THREADS);
     with_shape(a.D, dtype, [&](auto ty, auto sh) {
         using T = decltype(ty);

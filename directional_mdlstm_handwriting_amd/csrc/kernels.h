@@ -314,6 +314,7 @@ struct ScanArgs {
     float *hT, *dh0;              // [S][D] or null
     int polls;                    // looks at other tiles' words before a thread goes on by itself
     // set by the launchers
+    int once = 0;                 // whether the streams are read past the caches
     int ncb = 0;                  // channel blocks
     int64_t ntiles = 0;
     int64_t slots = 0;            // channels of all blocks

@@ -14,12 +14,13 @@
 // The tiles' maps are handed from tile to tile in the same launch (see look_back), so every stream is read and written
 // once. All states, maps and sums are fp32; a stream of bfloat16 is rounded once, as it is stored.
 //
-// Bound by HBM on long inputs: 208246 tokens x 1024 channels in bfloat16 take 369 us forward (1.71 GB, 4.6 TB/s; a copy
-// runs at 4.93) and 680 us backward (2.99 GB, 4.4 TB/s, its vector ALUs busy two thirds of the time); 656603 tokens x 32 in
-// fp32 without an output gate 60 us (252 MB) and 81 us (420 MB). One short generation of workgroups is bound by its
-// latency, read, chain, write: 20597 tokens x 512 in bfloat16 take 25 us (84 MB) and 40 us (148 MB).
-// The tile of 128 tokens by 128 bytes of channels: of 64 tokens, twice as many tiles wait for each other (documents
-// above 465 us forward), of 256 the threads' registers leave too few workgroups to hide the loads (437 and 873 us).
+// Bound by HBM on long inputs: 208246 tokens x 1024 channels in bfloat16 take 360 us forward (1.71 GB, 4.7 TB/s; a copy
+// runs at 4.93) and 620 us backward (2.99 GB, 4.8 TB/s, its vector ALUs busy two thirds of the time); 656603 tokens x 32 in
+// fp32 without an output gate 52 us (252 MB) and 74 us (420 MB). One short generation of workgroups is bound by its
+// latency, read, chain, write: 20597 tokens x 512 in bfloat16 take 24 us (84 MB) and 37 us (148 MB).
+// The tile of 128 tokens by 128 bytes of channels: of 64 tokens, twice as many tiles wait for each other (467 us
+// forward where this one took 372), of 256 the registers leave too few workgroups to hide the loads (437; backward 873
+// for 650).
 #include "kernels.h"
 #include "seqio.h"
 

@@ -11,8 +11,8 @@
 // in LDS; their gradients are written over the row's after it, by the lanes that own the slots (a class named twice gets
 // both slots' p). Statistics are fp32; the gradient is rounded once.
 //
-// Bound by HBM: 4096 x 32000 in bfloat16 takes 101 to 112 us (525 MB, 4.7 to 5.2 TB/s; a copy runs at 4.93), 1000 x 100003
-// in fp32 183 us (800 MB, 4.4 TB/s; read twice it took 233), 60000 x 80 in fp32 11 us (38 MB).
+// Bound by HBM: 4096 x 32000 in bfloat16 takes 101 us (525 MB, 5.2 TB/s; a copy runs at 4.93), 1000 x 100003 in fp32
+// 184 us (800 MB, 4.3 TB/s; read twice it took 233), 60000 x 80 in fp32 11 us (38 MB).
 #include "kernels.h"
 #include "seqio.h"
 

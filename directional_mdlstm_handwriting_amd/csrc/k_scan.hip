@@ -18,9 +18,9 @@
 // runs at 4.93) and 620 us backward (2.99 GB, 4.8 TB/s, its vector ALUs busy two thirds of the time); 656603 tokens x 32 in
 // fp32 without an output gate 52 us (252 MB) and 74 us (420 MB). One short generation of workgroups is bound by its
 // latency, read, chain, write: 20597 tokens x 512 in bfloat16 take 24 us (84 MB) and 37 us (148 MB).
-// The tile of 128 tokens by 128 bytes of channels: of 64 tokens, twice as many tiles wait for each other (467 us
-// forward where this one took 372), of 256 the registers leave too few workgroups to hide the loads (437; backward 873
-// for 650).
+// The tile of 128 tokens by 128 bytes of channels: timed side by side on the 208246 tokens, when the kernels took 365 us
+// forward and 649 us backward, one of 64 tokens by 128 bytes took 465 and 704 us, one of 64 by 256 bytes 474 and 675,
+// one of 256 by 64 bytes 438 and 873.
 #include "kernels.h"
 #include "seqio.h"
 

@@ -391,28 +391,32 @@ class SequenceScan:
 
 
 class ScanState:
-    """The recurrence's states of n_slots live streams, advanced a token at a time (mdl_scan_step)."""
+    """The recurrence's states of n_slots live streams, advanced a token at a time (mdl_scan_step). Holds one output
+    for every number of rows it was called with, so a call captured into a graph keeps its own while others run; a
+    result stands until the next call with as many rows."""
 
     def __init__(self, n_slots: int, D: int, x_dtype: str = "f32", device: str = "cuda"):
         self.device = _device(device)
         self.n_slots, self.D = int(n_slots), int(D)
         self.x_dtype, self.tdt = _x_dtype(x_dtype)
         self.state = torch.zeros(self.n_slots, self.D, dtype=torch.float32, device=self.device)
-        self._y = None
+        self._y = {}
 
     def step(self, zf, g, zo=None, slots=None, out=None, stream=None):
         """y [S][D] of one token for each row's slot (slots int32 [S], all different; the first S rows if None). The
-        states advance in place, or into the same rows of `out` ([n_slots][D])."""
+        states advance in place, or into the same rows of `out` ([n_slots][D]). A row whose slot is no slot (-1 in a
+        padded batch) is left out, and its y means nothing."""
         _here(self.device)
         S = int(zf.shape[0])
         ldz = _same_rows(("zf", "g", "zo"), (zf, g, zo), (S, self.D), self.tdt, self.device)
         _full("slots", slots, (S,), torch.int32, self.device)
         _full("out", out, (self.n_slots, self.D), torch.float32, self.device)
-        if self._y is None or self._y.shape[0] != S:
-            self._y = torch.zeros(S, self.D, dtype=self.tdt, device=self.device)
+        if S not in self._y:
+            self._y[S] = torch.zeros(S, self.D, dtype=self.tdt, device=self.device)
+        y = self._y[S]
         mdl_scan_step(S, self.D, self.x_dtype, zf, g, zo, ldz, slots, self.n_slots, self.state,
-                      self.state if out is None else out, self._y, self.D, stream)
-        return self._y
+                      self.state if out is None else out, y, self.D, stream)
+        return y
 
 
 class BlockNorm:

@@ -458,6 +458,32 @@ def test_step(D, dtype):
     assert torch.equal(st.state[S:], before[S:])
 
 
+def test_step_captured_beside_other_batch_sizes():
+    """A captured step keeps its output while eager steps of other numbers of rows come and go."""
+    D, n = 40, 6
+    zf, g, zo, _, _, _ = _inputs(33, n, n, D, "f32")
+    st, eager = ScanState(n, D, "f32", device=DEV), ScanState(n, D, "f32", device=DEV)
+    place = st.step(zf[:2], g[:2], zo[:2]).data_ptr()
+    st.state.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st.step(zf[:2], g[:2], zo[:2])
+    for rep in range(3):
+        st.step(zf, g, zo)
+        eager.step(zf, g, zo)
+        others = [torch.full((2, D), float(i), device=DEV) for i in range(8)]
+        graph.replay()
+        want = eager.step(zf[:2], g[:2], zo[:2])
+        torch.cuda.synchronize()
+        y = st.step(zf[:2], g[:2], zo[:2], out=torch.empty_like(st.state))
+        assert y.data_ptr() == place
+        graph.replay()
+        want = eager.step(zf[:2], g[:2], zo[:2])
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(st.state, eager.state), rep
+        assert all((o == i).all() for i, o in enumerate(others)), rep
+
+
 def test_stepped_tokens_continue_a_scanned_prefix():
     off = _off([90, 90])
     D, S = 40, 2

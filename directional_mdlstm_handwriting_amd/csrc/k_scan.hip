@@ -15,7 +15,8 @@
 // once. All states, maps and sums are fp32; a stream of bfloat16 is rounded once, as it is stored.
 //
 // Bound by HBM on long inputs: 208246 tokens x 1024 channels in bfloat16 take 360 us forward (1.71 GB, 4.7 TB/s; a copy
-// runs at 4.93) and 620 us backward (2.99 GB, 4.8 TB/s, its vector ALUs busy two thirds of the time); 656603 tokens x 32 in
+// runs at 4.93) and 620 us backward (2.99 GB, 4.8 TB/s), with the vector ALUs, by the count of their instructions, close
+// to busy as well (91 and 78 % of the cycles); 656603 tokens x 32 in
 // fp32 without an output gate 52 us (252 MB) and 74 us (420 MB). One short generation of workgroups is bound by its
 // latency, read, chain, write: 20597 tokens x 512 in bfloat16 take 24 us (84 MB) and 37 us (148 MB).
 // The tile of 128 tokens by 128 bytes of channels: timed side by side on the 208246 tokens, when the kernels took 365 us

@@ -15,6 +15,7 @@ its gate and residual; ``TopKDistill`` the distillation loss of its logits.
 
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 from typing import List, Optional, Sequence
 
@@ -25,7 +26,7 @@ from . import (MDL_BF16, MDL_CELL_LEAKY_LP, MDL_CELL_MDLSTM, MDL_F32, MDL_PACK_A
                mdl_blockconv_backward, mdl_blockconv_forward, mdl_blockconv_workspace_size, mdl_dirsum_unpack, mdl_forward, mdl_forward_dirsum,
                mdl_layout_device_size, mdl_layout_rects, mdl_layout_upload, mdl_pack, mdl_pack_level, mdl_scatter, mdl_workspace_size,
                mdl_ctc_head, mdl_ctc_workspace_size, mdl_scan_backward, mdl_scan_forward, mdl_scan_step, mdl_scan_workspace_size,
-               mdl_blocknorm_backward, mdl_blocknorm_forward, mdl_blocknorm_workspace_size, mdl_distill)
+               mdl_blocknorm_backward, mdl_blocknorm_forward, mdl_blocknorm_workspace_size, mdl_distill, _stream)
 
 
 def _dev(a, device, dtype=torch.float32):
@@ -332,7 +333,49 @@ def _here(device: torch.device):
         raise ValueError(f"buffers are on {device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
-class SequenceScan:
+def _on(handle: int, device: torch.device):
+    """The context in which torch allocates and fills on the stream of this handle."""
+    if handle == _stream(None):
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device))
+
+
+class _Buffers:
+    """Buffers that an operator keeps from call to call, ordered with the calls whatever their stream. Those of the
+    constructor are allocated and filled on torch's current stream: the first call on any other stream waits for that.
+    Those that only some calls need are allocated and filled on the stream of the first such call. From then on the
+    buffers are as any tensor's: the caller orders calls of one object that run on different streams. In a graph capture
+    nothing is waited for (torch.cuda.graph synchronizes before it), and a buffer that the capture is the first to need
+    belongs to the graph: the object does not keep it."""
+
+    def _made(self, device: torch.device):
+        self.device = device
+        home = torch.cuda.current_stream(device)
+        self._ready = None
+        with torch.cuda.device(device):
+            if not torch.cuda.is_current_stream_capturing():
+                self._ready = home.record_event()
+        self._joined = {home.cuda_stream}
+
+    def _launch(self, stream) -> int:
+        """The handle of the stream that a call launches on, with the constructor's work before it."""
+        _here(self.device)
+        handle = _stream(stream)
+        if handle not in self._joined and self._ready is not None:
+            with _on(handle, self.device):
+                if not torch.cuda.is_current_stream_capturing():
+                    torch.cuda.current_stream().wait_event(self._ready)
+                    self._joined.add(handle)
+        return handle
+
+    def _new(self, handle: int, shape, dtype, zero: bool):
+        """(tensor, whether to keep it)"""
+        with _on(handle, self.device):
+            make = torch.zeros if zero else torch.empty
+            return make(shape, dtype=dtype, device=self.device), not torch.cuda.is_current_stream_capturing()
+
+
+class SequenceScan(_Buffers):
     """The gated linear recurrence (mdl_scan_forward / _backward) over the sequences given by `seq_off` among T rows
     of D channels. seq_off: S + 1 ascending offsets, from the host (checked) or an int64 device tensor (taken as it
     is). Holds the outputs, the gradients and the workspace: a forward's results stand until the next forward, and a
@@ -358,15 +401,16 @@ class SequenceScan:
         self.y = torch.zeros(self.T, self.D, dtype=self.tdt, device=self.device)
         self.hT = torch.empty(self.S, self.D, dtype=torch.float32, device=self.device)
         self.dzf = self.dg = self.dzo = self.dh0 = None
+        self._made(self.device)
 
     def _inputs(self, zf, g, zo, h0):
-        _here(self.device)
         ldz = _same_rows(("zf", "g", "zo"), (zf, g, zo), (self.T, self.D), self.tdt, self.device)
         _full("h0", h0, (self.S, self.D), torch.float32, self.device)
         return ldz
 
     def forward(self, zf, g, zo=None, h0=None, stream=None):
         """(y, hT): zf, g, zo [T][D] at one row stride, h0 [S][D] float32."""
+        stream = self._launch(stream)
         ldz = self._inputs(zf, g, zo, h0)
         mdl_scan_forward(self.off, self.S, self.T, self.D, self.x_dtype, self.reverse, zf, g, zo, ldz, h0, self.y,
                          self.D, self.hT, self.ws, self.ws_bytes, stream)
@@ -375,22 +419,28 @@ class SequenceScan:
     def backward(self, zf, g, zo, dy, h0=None, dhT=None, stream=None):
         """(dzf, dg, dzo, dh0), dzo None without zo and dh0 None without h0, of the forward() just run on the same
         inputs."""
+        stream = self._launch(stream)
         ldz = self._inputs(zf, g, zo, h0)
         ldy = _rows("dy", dy, (self.T, self.D), self.tdt, self.device)
         _full("dhT", dhT, (self.S, self.D), torch.float32, self.device)
-        if self.dzf is None:
-            self.dzf, self.dg = torch.zeros_like(self.y), torch.zeros_like(self.y)
-        if zo is not None and self.dzo is None:
-            self.dzo = torch.zeros_like(self.y)
-        if h0 is not None and self.dh0 is None:
-            self.dh0 = torch.empty_like(self.hT)
-        dzo, dh0 = self.dzo if zo is not None else None, self.dh0 if h0 is not None else None
+        dzf, dg = self._grad("dzf", self.y, stream), self._grad("dg", self.y, stream)
+        dzo = None if zo is None else self._grad("dzo", self.y, stream)
+        dh0 = None if h0 is None else self._grad("dh0", self.hT, stream)
         mdl_scan_backward(self.off, self.S, self.T, self.D, self.x_dtype, self.reverse, zf, g, zo, ldz, h0, dy, ldy,
-                          dhT, self.dzf, self.dg, dzo, self.D, dh0, self.ws, self.ws_bytes, stream)
-        return self.dzf, self.dg, dzo, dh0
+                          dhT, dzf, dg, dzo, self.D, dh0, self.ws, self.ws_bytes, stream)
+        return dzf, dg, dzo, dh0
+
+    def _grad(self, name, like, stream):
+        t = getattr(self, name)
+        if t is None:
+            # zeros: as y, rows in no sequence are never written
+            t, keep = self._new(stream, like.shape, like.dtype, like is self.y)
+            if keep:
+                setattr(self, name, t)
+        return t
 
 
-class ScanState:
+class ScanState(_Buffers):
     """The recurrence's states of n_slots live streams, advanced a token at a time (mdl_scan_step). Holds one output
     for every number of rows it was called with, so a call captured into a graph keeps its own while others run; a
     result stands until the next call with as many rows."""
@@ -401,25 +451,28 @@ class ScanState:
         self.x_dtype, self.tdt = _x_dtype(x_dtype)
         self.state = torch.zeros(self.n_slots, self.D, dtype=torch.float32, device=self.device)
         self._y = {}
+        self._made(self.device)
 
     def step(self, zf, g, zo=None, slots=None, out=None, stream=None):
         """y [S][D] of one token for each row's slot (slots int32 [S], all different; the first S rows if None). The
         states advance in place, or into the same rows of `out` ([n_slots][D]). A row whose slot is no slot (-1 in a
         padded batch) is left out, and its y means nothing."""
-        _here(self.device)
+        stream = self._launch(stream)
         S = int(zf.shape[0])
         ldz = _same_rows(("zf", "g", "zo"), (zf, g, zo), (S, self.D), self.tdt, self.device)
         _full("slots", slots, (S,), torch.int32, self.device)
         _full("out", out, (self.n_slots, self.D), torch.float32, self.device)
-        if S not in self._y:
-            self._y[S] = torch.zeros(S, self.D, dtype=self.tdt, device=self.device)
-        y = self._y[S]
+        y = self._y.get(S)
+        if y is None:
+            y, keep = self._new(stream, (S, self.D), self.tdt, True)
+            if keep:
+                self._y[S] = y
         mdl_scan_step(S, self.D, self.x_dtype, zf, g, zo, ldz, slots, self.n_slots, self.state,
                       self.state if out is None else out, y, self.D, stream)
         return y
 
 
-class BlockNorm:
+class BlockNorm(_Buffers):
     """The norms before and after a block over N rows of D channels, with the block's gate and scaled residual
     (mdl_blocknorm_forward / _backward). Weights are the caller's, [D] float32. Holds outputs and gradients: a call's
     results stand until the next call of the same method."""
@@ -431,17 +484,20 @@ class BlockNorm:
         self.ws_bytes = mdl_blocknorm_workspace_size(self.N, self.D, self.x_dtype)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         self._bufs = {}
+        self._made(self.device)
 
-    def _out(self, name, wanted, weight=False):
+    def _out(self, stream, name, wanted, weight=False):
         if not wanted:
             return None
-        if name not in self._bufs:
+        t = self._bufs.get(name)
+        if t is None:
             shape, dt = ((self.D,), torch.float32) if weight else ((self.N, self.D), self.tdt)
-            self._bufs[name] = torch.empty(shape, dtype=dt, device=self.device)
-        return self._bufs[name]
+            t, keep = self._new(stream, shape, dt, False)
+            if keep:
+                self._bufs[name] = t
+        return t
 
     def _inputs(self, x, z, u, w_post, scale, w_pre):
-        _here(self.device)
         lds = [_rows(n, t, (self.N, self.D), self.tdt, self.device) if t is not None else 0
                for n, t in (("x", x), ("z", z), ("u", u))]
         for n, t in (("w_post", w_post), ("scale", scale), ("w_pre", w_pre)):
@@ -450,25 +506,28 @@ class BlockNorm:
 
     def forward(self, x, z=None, u=None, w_post=None, scale=None, w_pre=None, stream=None):
         """(r, v): r is x itself without z, v None without w_pre."""
+        stream = self._launch(stream)
         ldx, ldz, ldu = self._inputs(x, z, u, w_post, scale, w_pre)
-        r, v = self._out("r", z is not None), self._out("v", w_pre is not None)
+        r, v = self._out(stream, "r", z is not None), self._out(stream, "v", w_pre is not None)
         mdl_blocknorm_forward(self.N, self.D, self.x_dtype, x, ldx, z, ldz, u, ldu, w_post, scale, w_pre, self.eps, r,
                               v, self.D, stream)
         return (x if z is None else r), v
 
     def backward(self, x, z, u, w_post, scale, w_pre, dr, dv, stream=None):
         """(dx, dz, du, dw_post, dscale, dw_pre), None where the input is."""
+        stream = self._launch(stream)
         ldx, ldz, ldu = self._inputs(x, z, u, w_post, scale, w_pre)
         _full("dr", dr, (self.N, self.D), self.tdt, self.device)
         _full("dv", dv, (self.N, self.D), self.tdt, self.device)
-        out = [self._out(n, t is not None) for n, t in (("dx", x), ("dz", z), ("du", u))]
-        out += [self._out(n, t is not None, True) for n, t in (("dw_post", w_post), ("dscale", scale), ("dw_pre", w_pre))]
+        out = [self._out(stream, n, t is not None) for n, t in (("dx", x), ("dz", z), ("du", u))]
+        out += [self._out(stream, n, t is not None, True)
+                for n, t in (("dw_post", w_post), ("dscale", scale), ("dw_pre", w_pre))]
         mdl_blocknorm_backward(self.N, self.D, self.x_dtype, x, ldx, z, ldz, u, ldu, w_post, scale, w_pre, self.eps,
                                dr, dv, self.D, *out[:3], self.D, *out[3:], self.ws, self.ws_bytes, stream)
         return tuple(out)
 
 
-class TopKDistill:
+class TopKDistill(_Buffers):
     """Distillation loss of N frames over V classes from a teacher's k kept logits (mdl_distill): the loss per frame
     and its gradient in one call. Holds both; they stand until the next call."""
 
@@ -478,11 +537,12 @@ class TopKDistill:
         self.x_dtype, self.tdt = _x_dtype(x_dtype)
         self.loss = torch.empty(self.N, dtype=torch.float32, device=self.device)
         self.dz = torch.empty(self.N, self.V, dtype=self.tdt, device=self.device)
+        self._made(self.device)
 
     def run(self, z, ids, t, w=None, want_dz: bool = True, stream=None):
         """(loss [N], dz [N][V] or None): z [N][V] at any row stride, ids int32 and t (float32 or bfloat16) [N][k],
         w [N] float32 or None."""
-        _here(self.device)
+        stream = self._launch(stream)
         ldz = _rows("z", z, (self.N, self.V), self.tdt, self.device)
         _full("ids", ids, (self.N, self.k), torch.int32, self.device)
         t_dtype = "bf16" if t.dtype == torch.bfloat16 else "f32"

@@ -368,6 +368,10 @@ class _Buffers:
                     self._joined.add(handle)
         return handle
 
+    def _capturing(self, handle: int) -> bool:
+        with _on(handle, self.device):
+            return torch.cuda.is_current_stream_capturing()
+
     def _new(self, handle: int, shape, dtype, zero: bool):
         """(tensor, whether to keep it)"""
         with _on(handle, self.device):
@@ -441,17 +445,38 @@ class SequenceScan(_Buffers):
 
 
 class ScanState(_Buffers):
-    """The recurrence's states of n_slots live streams, advanced a token at a time (mdl_scan_step). Holds one output
-    for every number of rows it was called with, so a call captured into a graph keeps its own while others run; a
-    result stands until the next call with as many rows."""
+    """The recurrence's states of n_slots live streams, advanced a token at a time (mdl_scan_step). Holds an output for
+    each of the last `KEPT` numbers of rows that it met, so that calls of other sizes leave a result alone: a result
+    stands until the next call with as many rows. A captured step writes the output that is held for its size, which is
+    then held as long as the object (a server captures few sizes), or else one of the graph's own."""
+
+    KEPT = 8
 
     def __init__(self, n_slots: int, D: int, x_dtype: str = "f32", device: str = "cuda"):
         self.device = _device(device)
         self.n_slots, self.D = int(n_slots), int(D)
         self.x_dtype, self.tdt = _x_dtype(x_dtype)
         self.state = torch.zeros(self.n_slots, self.D, dtype=torch.float32, device=self.device)
-        self._y = {}
+        self._y = {}            # rows: (output, handle of the stream it was made on), the oldest first
+        self._captured = {}     # rows: output that a graph writes
         self._made(self.device)
+
+    def _output(self, S: int, handle: int) -> torch.Tensor:
+        y = self._captured.get(S)
+        if y is not None:
+            return y
+        y, home = self._y.get(S, (None, None))
+        if y is not None and self._capturing(handle):
+            self._captured[S] = self._y.pop(S)[0]
+        elif home != handle:
+            # never used on a stream but its own, on which its memory may be handed out again once it is dropped
+            y, keep = self._new(handle, (S, self.D), self.tdt, True)
+            if keep:
+                self._y.pop(S, None)
+                self._y[S] = y, handle
+                if len(self._y) > self.KEPT:
+                    del self._y[next(iter(self._y))]
+        return y
 
     def step(self, zf, g, zo=None, slots=None, out=None, stream=None):
         """y [S][D] of one token for each row's slot (slots int32 [S], all different; the first S rows if None). The
@@ -462,11 +487,7 @@ class ScanState(_Buffers):
         ldz = _same_rows(("zf", "g", "zo"), (zf, g, zo), (S, self.D), self.tdt, self.device)
         _full("slots", slots, (S,), torch.int32, self.device)
         _full("out", out, (self.n_slots, self.D), torch.float32, self.device)
-        y = self._y.get(S)
-        if y is None:
-            y, keep = self._new(stream, (S, self.D), self.tdt, True)
-            if keep:
-                self._y[S] = y
+        y = self._output(S, stream)
         mdl_scan_step(S, self.D, self.x_dtype, zf, g, zo, ldz, slots, self.n_slots, self.state,
                       self.state if out is None else out, y, self.D, stream)
         return y

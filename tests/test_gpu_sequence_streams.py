@@ -118,3 +118,58 @@ def test_a_capture_is_the_first_to_call(op):
             o.state.zero_()
         graph.replay()
         _same(out, ref)
+
+
+def test_step_holds_a_bounded_number_of_outputs():
+    """Every batch size from 1 to 64: results that are still referenced stand, what the object holds stays within the
+    outputs of its last sizes."""
+    n, d = 64, 256
+    print("[gpu] step sizes", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    z = [torch.randn(n, d, generator=g, device=DEV) for _ in range(3)]
+    st = ScanState(n, d, device=DEV)
+    keep = torch.empty_like(st.state)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    got = [st.step(*(t[:s] for t in z), out=keep) for s in range(1, n + 1)]
+    whole = ScanState(n, d, device=DEV).step(*z).clone()
+    torch.cuda.synchronize()
+    for s, y in enumerate(got, 1):
+        assert torch.equal(y, whole[:s]), s
+    del got, y, whole
+    assert torch.cuda.memory_allocated() - before <= ScanState.KEPT * n * d * 4
+
+
+def test_captured_step_outlives_other_sizes():
+    """The output that a graph writes is neither dropped nor handed out, however many sizes come between."""
+    n, d = 40, 64
+    print("[gpu] step captured", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(10)
+    z = [torch.randn(n, d, generator=g, device=DEV) for _ in range(3)]
+    st, eager = ScanState(n, d, device=DEV), ScanState(n, d, device=DEV)
+    two = [t[:2] for t in z]
+    st.step(*two)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = st.step(*two)
+    place = y.data_ptr()
+    del y
+    for rep in range(3):
+        st.state.zero_()
+        eager.state.zero_()
+        for s in range(1, n + 1):
+            st.step(*(t[:s] for t in z))
+            eager.step(*(t[:s] for t in z))
+        junk = [torch.full((2, d), float(i), device=DEV) for i in range(64)]
+        graph.replay()
+        want = eager.step(*two)
+        torch.cuda.synchronize()
+        y = st.step(*two, out=torch.empty_like(st.state))
+        assert y.data_ptr() == place
+        st.state.copy_(eager.state)
+        graph.replay()
+        want = eager.step(*two)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(st.state, eager.state), rep
+        assert all((j == i).all() for i, j in enumerate(junk)), rep
+        del y

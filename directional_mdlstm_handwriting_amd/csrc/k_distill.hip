@@ -246,7 +246,7 @@ __global__ __launch_bounds__(S::threads, 4) void k_distill(DistillArgs a) {
     const float inv_l = 1.f / s[0], inv_t = 1.f / s[1];
     if (live && lane == 0) {
         const float kl = s[2] * inv_t - __builtin_amdgcn_logf(s[1]) * kLn2 + __builtin_amdgcn_logf(s[0]) * kLn2;
-        a.loss[n] = s[4] > 0.f ? NAN : counts ? w * a.tau * a.tau * kl : 0.f;
+        a.loss[n] = s[4] > 0.f && w != 0.f ? NAN : counts ? w * a.tau * a.tau * kl : 0.f;
     }
     if (!a.dz) return;
     const float g = w * a.tau, gl = g * inv_l;

@@ -528,12 +528,12 @@ int mdl_blocknorm_backward(int64_t N, int32_t D, int32_t dtype, const void* x, i
  *     dz[n]   = w[n] tau (q - sum_j p_j [id_j = .])             (d loss[n] / dz)
  * w [N] float32 (NULL: ones) weights a frame in the loss; dz (row stride ldd)
  * may be NULL, or z itself at the same stride. id -1 marks an empty slot. A row
- * whose slots are all empty, or of weight 0, counts for nothing, whatever z
- * holds: loss 0, gradient 0. Any other id outside [0, V) gives loss NaN and
- * gradient 0 (found on the device). A class named twice counts with both
- * probabilities. A kept logit of -inf has p = 0 and adds nothing (a row that
- * keeps no other: NaN, as one whose z are all -inf). Statistics
- * and loss are float32; the gradient is rounded once. No workspace.
+ * whose slots are all empty, or of weight 0, counts for nothing, whatever z,
+ * t and its other ids hold: loss 0, gradient 0. In any other row an id outside
+ * [-1, V) gives loss NaN and gradient 0 (found on the device). A class named
+ * twice counts with both probabilities. A kept logit of -inf has p = 0 and adds
+ * nothing (a row that keeps no other: NaN, as one whose z are all -inf).
+ * Statistics and loss are float32; the gradient is rounded once. No workspace.
  * Errors: MDL_EINVAL for null tensors, N < 0, V < 1, k outside [1, V], a stride
  * below V, an unknown dtype, or tau that is not finite or below 1e-30;
  * MDL_EUNSUPPORTED for k > 1024; MDL_EOVERFLOW when N reaches 2^40 or rows times

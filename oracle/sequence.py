@@ -117,18 +117,18 @@ def blocknorm_backward(x, z, u, w_post, scale, w_pre, dr, dv, eps=1e-6):
 
 
 def distill(z, ids, t, w=None, tau=1.0):
-    """(loss [N], dz [N][V]). A slot with id -1 is empty; a row of empty slots counts for nothing; an id outside
-    [-1, V) makes its row's loss NaN and its gradient zero."""
+    """(loss [N], dz [N][V]). A slot with id -1 is empty; a row of empty slots, or of weight 0, counts for nothing; in any
+    other row an id outside [-1, V) makes the loss NaN and the gradient zero."""
     z, t = np.asarray(z, np.float64), np.asarray(t, np.float64)
     N, V = z.shape
     loss, dz = np.zeros(N), np.zeros((N, V))
     for n in range(N):
         wn = 1.0 if w is None else float(w[n])
         kept = [j for j, i in enumerate(ids[n]) if i != -1]
+        if not kept or wn == 0.0:
+            continue
         if any(not 0 <= ids[n][j] < V for j in kept):
             loss[n] = np.nan
-            continue
-        if not kept or wn == 0.0:
             continue
         a = z[n] / tau
         a = a - a.max()

@@ -174,3 +174,9 @@ def test_distill_against_autograd_and_closed_forms():
     # nothing kept, and a class that does not exist
     loss, dz = oseq.distill(z[:2], [[-1, -1], [0, V]], t[:2, :2])
     assert loss[0] == 0 and np.isnan(loss[1]) and not dz.any()
+
+
+def test_distill_weight_zero_wins_over_a_class_that_does_not_exist():
+    z, t = np.random.default_rng(4).normal(size=(3, 5)), np.zeros((3, 2))
+    loss, dz = oseq.distill(z, [[9, 1], [9, 1], [-1, -1]], t, [0.0, 1.0, 1.0], 1.5)
+    assert loss[0] == 0 and np.isnan(loss[1]) and loss[2] == 0 and not dz.any()

@@ -4,7 +4,8 @@
 //   p = softmax_j(t / tau),  q = softmax(z / tau)
 //   loss = w tau^2 sum_j p_j (ln p_j - ln q_{id_j}),  dz = w tau (q - sum_j p_j [id_j = .])
 // Written with e_j = exp((t_j - max t) / tau), T = sum e, m = max z and L = sum exp((z - m) / tau):
-//   loss / (w tau^2) = (1/T) sum_j e_j ((t_j - max t) - (z_{id_j} - m)) / tau - ln T + ln L.
+//   loss / (w tau) = (1/T) sum_j e_j ((t_j - max t) - (z_{id_j} - m)) + tau (ln L - ln T),
+// in which neither tau^2 nor 1 / tau can leave the range of fp32 before the loss does.
 //
 // R lanes share a row. A row that fits their registers is read once, kept as it lies in memory, and its gradient is
 // formed from there; longer rows are read twice. The maximum and the sum run along with the reading. The few kept classes sit
@@ -123,7 +124,7 @@ struct DistillArgs {
     const void* t;
     int t_bf16;
     const float* w;
-    float tau, inv_tau, log2e_tau;
+    float tau, log2e_tau;
     float* loss;
     void* dz;
     int64_t ldd;
@@ -237,7 +238,7 @@ __global__ __launch_bounds__(S::threads, 4) void k_distill(DistillArgs a) {
         }
         const float d = ej[j] - tm, e = exp_tau(d, a);
         s[1] += e;
-        if (e > 0.f || e != e) s[2] += e * ((d - (zj[j] - m)) * a.inv_tau);
+        if (e > 0.f || e != e) s[2] += e * (d - (zj[j] - m));
         ej[j] = e;
     }
     row_reduce<R, 5, false>(s, red);
@@ -245,8 +246,8 @@ __global__ __launch_bounds__(S::threads, 4) void k_distill(DistillArgs a) {
     const bool counts = s[3] > 0.f && s[4] == 0.f && w != 0.f;
     const float inv_l = 1.f / s[0], inv_t = 1.f / s[1];
     if (live && lane == 0) {
-        const float kl = s[2] * inv_t - __builtin_amdgcn_logf(s[1]) * kLn2 + __builtin_amdgcn_logf(s[0]) * kLn2;
-        a.loss[n] = s[4] > 0.f && w != 0.f ? NAN : counts ? w * a.tau * a.tau * kl : 0.f;
+        const float logs = __builtin_amdgcn_logf(s[0]) * kLn2 - __builtin_amdgcn_logf(s[1]) * kLn2;
+        a.loss[n] = s[4] > 0.f && w != 0.f ? NAN : counts ? w * a.tau * (s[2] * inv_t + a.tau * logs) : 0.f;
     }
     if (!a.dz) return;
     const float g = w * a.tau, gl = g * inv_l;
@@ -353,7 +354,7 @@ hipError_t launch_distill(int64_t N, int V, int k, int dtype, const void* z, int
             const void* tn = t_dtype == 1 ? static_cast<const void*>(static_cast<const bf16*>(t) + n * k)
                                           : static_cast<const void*>(static_cast<const float*>(t) + n * k);
             const DistillArgs a{m, V, k, static_cast<const T*>(z) + n * ldz, ldz, ids + n * k, tn, t_dtype == 1,
-                                w ? w + n : nullptr, tau, 1.f / tau, (float)(1.4426950408889634 / tau), loss + n,
+                                w ? w + n : nullptr, tau, (float)(1.4426950408889634 / tau), loss + n,
                                 dz ? static_cast<T*>(dz) + n * ldd : nullptr, ldd};
             launch(k_distill<T, S>, dim3((unsigned)((m + S::rows - 1) / S::rows)), dim3(S::threads),
                    sizeof(float) * 3 * k * S::rows, st, a);

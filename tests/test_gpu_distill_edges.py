@@ -24,3 +24,13 @@ def test_weight_zero_wins_over_a_class_that_does_not_exist(V, dtype):
     _, loss, dz = run(z, ids, t, w, 1.5, dtype)
     assert not loss[[1, 2, 4]].any() and torch.isnan(loss[3]) and not dz[1:5].any()
     assert torch.isfinite(loss[[0, 5]]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("tau", [1e-30, 1e-25, 1e-20, 3e-19, 1e15, 1e17])
+def test_temperatures_whose_square_is_no_fp32_number(tau, dtype):
+    """Sharp ones: the loss is w tau times the difference of the largest logits' gaps. Flat ones keep few classes, so
+    that the loss, about w tau^2 ln(V / k), is within fp32."""
+    z, ids, t, w = make(22, 9, 900, 6, dtype)
+    _, loss, _ = run(z, ids, t, w, tau, dtype)
+    assert torch.isfinite(loss).all() and (loss > 0).any()

@@ -138,6 +138,7 @@ template <typename T, typename S>
 __global__ __launch_bounds__(S::threads, 4) void k_distill(DistillArgs a) {
     constexpr int V = S::V, R = S::R, NV = S::NV > 0 ? S::NV : 1;
     constexpr bool kTwice = S::NV == 0;
+    static_assert(R >= V, "the elements past a row's whole vectors: one a lane");
     constexpr int kAhead = S::NV == 0 || NV % 4 == 0 ? 4 : NV % 2 == 0 ? 2 : 1;  // vectors walked at a time
     __shared__ float red[S::threads / 64 * 5];
     extern __shared__ float top[];  // [rows][3][k]: class, e_j, z of the class
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(S::threads, 4) void k_distill(DistillArgs a) {
 
     // the row: each lane's running maximum and sum, some vectors at a time, as they arrive
     Raw<T, V> q[NV];
-    const int full = a.V / V, tail = full * V;
+    const int full = a.V / V, tail = full * V, rest = a.V - tail;
     float mx = -INFINITY, run = 0.f;
     auto take = [&](const Raw<T, V>* r) {
         float b = mx, p = 0.f;
@@ -204,11 +205,11 @@ __global__ __launch_bounds__(S::threads, 4) void k_distill(DistillArgs a) {
             for (int j = 1; j < kAhead; ++j) r[j].fill(-INFINITY);
             take(r);
         }
-        for (i = tail + lane; i < a.V; i += R) {
+        if (lane < rest) {
             Raw<T, V> r[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) r[j].fill(-INFINITY);
-            set_first(r[0], load_raw<1>(z + i));
+            set_first(r[0], load_raw<1>(z + tail + lane));
             take(r);
         }
     }
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(S::threads, 4) void k_distill(DistillArgs a) {
     row_sync<R>();  // the row and its kept classes have been read: dz may be z
     if (!counts) {
         for (int i = lane; i < full && live; i += R) store_zeros<V>(dz + (int64_t)i * V);
-        for (int i = tail + lane; i < a.V && live; i += R) store_zeros<1>(dz + i);
+        if (lane < rest && live) store_zeros<1>(dz + tail + lane);
     } else if constexpr (!kTwice) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -293,9 +294,9 @@ __global__ __launch_bounds__(S::threads, 4) void k_distill(DistillArgs a) {
             for (int j = 0; j < kAhead; ++j) put(r[j], i + j * R);
         }
         for (; i < full; i += R) put(load_raw<V>(z + (int64_t)i * V), i);
-        for (i = tail + lane; i < a.V; i += R) {
-            const float o[1] = {grad(load_raw<1>(z + i)[0])};
-            if (live) store_vec<1>(dz + i, o);
+        if (lane < rest && live) {
+            const float o[1] = {grad(load_raw<1>(z + tail + lane)[0])};
+            store_vec<1>(dz + tail + lane, o);
         }
     }
     row_sync<R>();  // the row's stores come before those of its kept classes

@@ -5,12 +5,11 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import sequence as oseq
-
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
-    from test_gpu_distill import DEV, check, make, run
+    import directional_mdlstm_handwriting_amd as M
+    from test_gpu_distill import DEV, U, make, run
 
 
 @pytest.mark.parametrize("V,dtype", [(7, "f32"), (300, "bf16"), (5003, "f32")])
@@ -34,3 +33,53 @@ def test_temperatures_whose_square_is_no_fp32_number(tau, dtype):
     z, ids, t, w = make(22, 9, 900, 6, dtype)
     _, loss, _ = run(z, ids, t, w, tau, dtype)
     assert torch.isfinite(loss).all() and (loss > 0).any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("counts", [True, False])
+def test_as_many_classes_as_the_header_allows(counts, dtype):
+    """One row of 2^31 - 1 classes, between guards. A lane adds at most n = 2^31 / (4 1024 V) sums one after another
+    (V elements a vector, four of them at a time), each of at most 4 V terms; 1024 lanes are added in 6 + 16."""
+    V, k, tau, lead = 2 ** 31 - 1, 3, 2.0, 4096
+    print(f"[gpu] distill V={V} {dtype} counts={counts}", flush=True)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device=DEV).manual_seed(5)
+    z = torch.empty(1, V, dtype=dt, device=DEV)
+    step = 1 << 27
+    for a in range(0, V, step):
+        z[0, a:a + step] = torch.randn(min(step, V - a), generator=g, device=DEV)
+    ids = torch.tensor([[V - 1, 0, V - 2]], dtype=torch.int32, device=DEV)
+    t = torch.tensor([[1.0, 0.5, -1.0]], device=DEV)
+    z[0, ids[0].long()] = torch.tensor([2.0, -1.0, 3.0], device=DEV, dtype=dt)
+    w = torch.tensor([1.0 if counts else 0.0], device=DEV)
+    wide = torch.full((lead + V + lead,), 7.0, dtype=dt, device=DEV)
+    dz, loss = wide[lead:lead + V], torch.full((1,), 7.0, device=DEV)
+    M.mdl_distill(1, V, k, 1 if dtype == "bf16" else 0, z, V, ids, t, 0, w, tau, loss, dz, V)
+    torch.cuda.synchronize()
+    assert (wide[:lead] == 7).all() and (wide[lead + V:] == 7).all()
+    if not counts:
+        assert loss.item() == 0
+        assert not any(dz[a:a + step].any() for a in range(0, V, step))
+        return
+    m = max(z[0, a:a + step].max().double().item() for a in range(0, V, step))
+    L = sum(torch.exp((z[0, a:a + step].double() - m) / tau).sum().item() for a in range(0, V, step))
+    vec = 8 if dtype == "bf16" else 4
+    n = 2 ** 31 // (4096 * vec) + 4 * vec + 6 + 16
+    x = (t.double() / tau)[0]
+    p = torch.softmax(x, 0)
+    lq = (z[0, ids[0].long()].double() - m) / tau - np.log(L)
+    ref = tau * tau * (p * (torch.log(p) - lq)).sum().item()
+    # an exponential's argument, at most 12 / 2 here, is off by 4 u of it
+    rel = (n + 4 * 6 + 12) * U
+    assert abs(loss.item() - ref) <= tau * tau * (rel + 64 * U * abs(np.log(L)))
+    half = U if dtype == "f32" else 2.0 ** -8
+    for a in range(0, V, step):
+        q = torch.exp((z[0, a:a + step].double() - m) / tau) / L
+        for j, c in enumerate(ids[0].tolist()):
+            if a <= c < a + step:
+                q[c - a] -= p[j]
+        q *= tau
+        got = dz[a:a + step].double()
+        # the kept classes' own: p within 20 u of its magnitude
+        tol = (rel + half) * q.abs() + 20 * U * tau * (q < 0) + 1e-36
+        assert bool(((got - q).abs() <= tol).all()), a

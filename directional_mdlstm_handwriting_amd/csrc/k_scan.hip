@@ -35,6 +35,9 @@ namespace {
 // (min and max of two int64_t go through double)
 __device__ inline int64_t lesser(int64_t a, int64_t b) { return a < b ? a : b; }
 
+// vectors of V elements that hold a row of D, any D >= 1
+__host__ __device__ constexpr int vectors(int D, int V) { return (D - 1) / V + 1; }
+
 constexpr int SCAN_THREADS = 256;
 constexpr float kReset = -1.0f;  // the A of a map that ignores its argument
 
@@ -677,7 +680,7 @@ __global__ __launch_bounds__(256) void k_scan_step(int S, int D, const T* __rest
                                                    const T* __restrict__ zo, int64_t ldz,
                                                    const int32_t* __restrict__ slots, int n_slots, const float* h_in,
                                                    float* h_out, T* __restrict__ y, int64_t ldy) {
-    const int per = (D + V - 1) / V;
+    const int per = vectors(D, V);
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= (int64_t)S * per) return;
     const int s = (int)(i / per), c = (int)(i % per) * V;
@@ -728,7 +731,7 @@ void with_shape(int D, int dtype, F&& fn) {
         if constexpr (V > 4) {
             if (D <= V) return fn(ty, ScanShape<1, 8, 16>{});
         }
-        const int lanes = (D + V - 1) / V;
+        const int lanes = vectors(D, V);
         if (lanes <= 4) return fn(ty, ScanShape<V, 4, 4>{});
         return fn(ty, ScanShape<V, 8, 4>{});
     };
@@ -805,7 +808,7 @@ hipError_t launch_scan_step(int S, int D, int dtype, const void* zf, const void*
     auto go = [&](auto ty) {
         using T = decltype(ty);
         constexpr int V = Width<T>::v;
-        const int64_t n = (int64_t)S * ((D + V - 1) / V);
+        const int64_t n = (int64_t)S * vectors(D, V);
         launch(k_scan_step<T, V>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, S, D, static_cast<const T*>(zf),
                static_cast<const T*>(g), static_cast<const T*>(zo), ldz, slots, n_slots, h_in, h_out,
                static_cast<T*>(y), ldy);

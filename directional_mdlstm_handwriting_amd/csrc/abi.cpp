@@ -978,6 +978,12 @@ static int check_scan(const std::string& F, int64_t T, int32_t D, int32_t dtype,
     need = p.total;
     return MDL_OK;
 }
+// the search for a tile's first sequence adds up to 63 to a count of them
+static int check_sequences(const std::string& F, int32_t S) {
+    if (S < 1) return fail(MDL_EINVAL, F + ": need S >= 1");
+    if (S >= INT32_MAX - 63) return fail(MDL_EOVERFLOW, F + ": S reaches 2^31 - 64");
+    return MDL_OK;
+}
 static int check_ws(const std::string& F, const char* size_fn, size_t need, const void* ws, size_t ws_bytes) {
     if (need > 0 && !ws) return fail(MDL_EINVAL, F + ": null workspace");
     if (need > 0 && reinterpret_cast<uintptr_t>(ws) % 16) return fail(MDL_EINVAL, F + ": workspace not 16-byte aligned");
@@ -1004,7 +1010,7 @@ int mdl_scan_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, in
     size_t need = 0;
     int rc = check_scan(F, T, D, dtype, need);
     if (rc) return rc;
-    if (S < 1) return fail(MDL_EINVAL, F + ": need S >= 1");
+    if ((rc = check_sequences(F, S))) return rc;
     if (!seq_off || (T > 0 && (!zf || !g || !y))) return fail(MDL_EINVAL, F + ": null tensor");
     if ((rc = check_stride32(F, "ldz", T, D, ldz)) || (rc = check_stride32(F, "ldy", T, D, ldy))) return rc;
     if ((rc = check_ws(F, "mdl_scan_workspace_size", need, ws, ws_bytes))) return rc;
@@ -1042,7 +1048,7 @@ int mdl_scan_backward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, i
     size_t need = 0;
     int rc = check_scan(F, T, D, dtype, need);
     if (rc) return rc;
-    if (S < 1) return fail(MDL_EINVAL, F + ": need S >= 1");
+    if ((rc = check_sequences(F, S))) return rc;
     if (!seq_off || (T > 0 && (!zf || !g || !dy || !dzf || !dg))) return fail(MDL_EINVAL, F + ": null tensor");
     if (T > 0 && (zo == nullptr) != (dzo == nullptr)) return fail(MDL_EINVAL, F + ": dzo goes with zo, and only with it");
     if ((rc = check_stride32(F, "ldz", T, D, ldz)) || (rc = check_stride32(F, "ldy", T, D, ldy)) ||

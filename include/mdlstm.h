@@ -465,8 +465,9 @@ int mdl_ctc_head(const mdl_layout* layout, const void* d_desc, const float* y_fl
  * unknown dtype, dzo without zo or zo without dzo, n_slots < 1, slots NULL with
  * n_slots < S, or a misaligned workspace; MDL_ESIZE for a short workspace;
  * MDL_EOVERFLOW when rows times a stride reach 2^60, a stride of the forward or
- * backward 2^31, the launch exceeds 2^31 threads (each of them takes 16 elements
- * or more), or S D of a step exceeds 2^31. With T = 0 the token tensors may be NULL.
+ * backward 2^31, S of the forward or backward 2^31 - 64, the launch exceeds 2^31
+ * threads (each of them takes 16 elements or more), or S D of a step exceeds
+ * 2^31. With T = 0 the token tensors may be NULL.
  */
 int mdl_scan_workspace_size(int64_t T, int32_t D, int32_t dtype, size_t* bytes);
 int mdl_scan_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, int32_t dtype, int32_t reverse,

@@ -120,3 +120,10 @@ def test_blocknorm_workspace_sizes():
 ])
 def test_distill_refuses(change, code):
     assert _code(M.mdl_distill, **_with(DISTILL, **change)) == code
+
+
+@pytest.mark.parametrize("S", [(1 << 31) - 1, (1 << 31) - 64])
+def test_scan_refuses_more_sequences_than_its_search_counts(S):
+    """The search through the offsets probes 64 at a time: its counts stay inside 32 bits."""
+    assert _code(M.mdl_scan_forward, **_with(SCAN_F, S=S)) == M.MDL_EOVERFLOW
+    assert _code(M.mdl_scan_backward, **_with(SCAN_B, S=S)) == M.MDL_EOVERFLOW

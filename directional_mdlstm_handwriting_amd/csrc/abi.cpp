@@ -7,6 +7,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 #include <map>
 #include <mutex>
@@ -984,6 +985,22 @@ static int check_sequences(const std::string& F, int32_t S) {
     if (S >= INT32_MAX - 63) return fail(MDL_EOVERFLOW, F + ": S reaches 2^31 - 64");
     return MDL_OK;
 }
+// Outputs that start where an input or another output does: tiles read their inputs again, and those of other tiles,
+// after some have written. (Column blocks of one matrix lie between each other, so only the starts are compared.)
+static int check_apart(const std::string& F, std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        if (!*o) continue;
+        const bool over = std::count(ins.begin(), ins.end(), *o) || std::count(o + 1, outs.end(), *o);
+        if (over) return fail(MDL_EINVAL, F + ": an output over an input or another output");
+    }
+    return MDL_OK;
+}
+// whether two arrays [S][D] of float share elements
+static bool share_states(const void* a, const void* b, int32_t S, int32_t D) {
+    if (!a || !b) return false;
+    const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return (x > y ? x - y : y - x) / 4 < (uint64_t)S * (uint64_t)D;
+}
 static int check_ws(const std::string& F, const char* size_fn, size_t need, const void* ws, size_t ws_bytes) {
     if (need > 0 && !ws) return fail(MDL_EINVAL, F + ": null workspace");
     if (need > 0 && reinterpret_cast<uintptr_t>(ws) % 16) return fail(MDL_EINVAL, F + ": workspace not 16-byte aligned");
@@ -1014,6 +1031,8 @@ int mdl_scan_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, in
     if (!seq_off || (T > 0 && (!zf || !g || !y))) return fail(MDL_EINVAL, F + ": null tensor");
     if ((rc = check_stride32(F, "ldz", T, D, ldz)) || (rc = check_stride32(F, "ldy", T, D, ldy))) return rc;
     if ((rc = check_ws(F, "mdl_scan_workspace_size", need, ws, ws_bytes))) return rc;
+    if (T > 0 && (rc = check_apart(F, {y, hT}, {zf, g, zo}))) return rc;
+    if (share_states(h0, hT, S, D)) return fail(MDL_EINVAL, F + ": hT over h0");
     mdl::ScanArgs a{};
     a.off = seq_off;
     a.S = S;
@@ -1055,6 +1074,9 @@ int mdl_scan_backward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, i
         (rc = check_stride32(F, "ldd", T, D, ldd)))
         return rc;
     if ((rc = check_ws(F, "mdl_scan_workspace_size", need, ws, ws_bytes))) return rc;
+    if (T > 0 && (rc = check_apart(F, {dzf, dg, dzo}, {zf, g, zo, dy}))) return rc;
+    if (share_states(h0, dh0, S, D) || share_states(dhT, dh0, S, D))
+        return fail(MDL_EINVAL, F + ": dh0 over h0 or dhT");
     mdl::ScanArgs a{};
     a.off = seq_off;
     a.S = S;

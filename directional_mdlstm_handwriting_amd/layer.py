@@ -413,7 +413,8 @@ class SequenceScan(_Buffers):
         return ldz
 
     def forward(self, zf, g, zo=None, h0=None, stream=None):
-        """(y, hT): zf, g, zo [T][D] at one row stride, h0 [S][D] float32."""
+        """(y, hT): zf, g, zo [T][D] at one row stride, h0 [S][D] float32. Neither the object's own y nor its hT can be an
+        input: the last states of one piece of a long sequence are copied, or another object takes the next piece."""
         stream = self._launch(stream)
         ldz = self._inputs(zf, g, zo, h0)
         mdl_scan_forward(self.off, self.S, self.T, self.D, self.x_dtype, self.reverse, zf, g, zo, ldz, h0, self.y,

@@ -453,7 +453,13 @@ int mdl_ctc_head(const mdl_layout* layout, const void* d_desc, const float* y_fl
  *     dg = (1 - f) l,  dzf = f (1 - f) (h_{t-1} - g) l,  dzo = dy h o (1 - o),
  *     dh0 = f l at the first token (dhT for an empty sequence)
  * dzf, dg, dzo [T][D] at row stride ldd; dzo exactly when zo is given; dh0
- * [S][D] may be NULL. No output may overlap an input or another output.
+ * [S][D] may be NULL.
+ *
+ * No output of the forward or the backward may overlap an input or another
+ * output: tiles read inputs, their own and others', after some have written
+ * (so a long sequence taken in pieces hands its states on from one array to
+ * another). Token tensors that start at the same address and states that
+ * overlap are refused; column blocks of one matrix do not overlap.
  *
  * mdl_scan_step: one token for each of S streams (serving). Row i advances the
  * state row slots[i] (device, int32; i itself if NULL) from h_in to h_out
@@ -462,12 +468,12 @@ int mdl_ctc_head(const mdl_layout* layout, const void* d_desc, const float* y_fl
  * nor any state is written. Slots must differ from each other.
  *
  * Errors: MDL_EINVAL for null tensors, S, D < 1, T < 0, a stride below D, an
- * unknown dtype, dzo without zo or zo without dzo, n_slots < 1, slots NULL with
- * n_slots < S, or a misaligned workspace; MDL_ESIZE for a short workspace;
- * MDL_EOVERFLOW when rows times a stride reach 2^60, a stride of the forward or
- * backward 2^31, S of the forward or backward 2^31 - 64, the launch exceeds 2^31
- * threads (each of them takes 16 elements or more), or S D of a step exceeds
- * 2^31. With T = 0 the token tensors may be NULL.
+ * unknown dtype, dzo without zo or zo without dzo, outputs over inputs as above,
+ * n_slots < 1, slots NULL with n_slots < S, or a misaligned workspace; MDL_ESIZE
+ * for a short workspace; MDL_EOVERFLOW when rows times a stride reach 2^60, a
+ * stride of the forward or backward 2^31, S of the forward or backward 2^31 - 64,
+ * the launch exceeds 2^31 threads (each of them takes 16 elements or more), or
+ * S D of a step exceeds 2^31. With T = 0 the token tensors may be NULL.
  */
 int mdl_scan_workspace_size(int64_t T, int32_t D, int32_t dtype, size_t* bytes);
 int mdl_scan_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, int32_t dtype, int32_t reverse,

@@ -127,3 +127,27 @@ def test_scan_refuses_more_sequences_than_its_search_counts(S):
     """The search through the offsets probes 64 at a time: its counts stay inside 32 bits."""
     assert _code(M.mdl_scan_forward, **_with(SCAN_F, S=S)) == M.MDL_EOVERFLOW
     assert _code(M.mdl_scan_backward, **_with(SCAN_B, S=S)) == M.MDL_EOVERFLOW
+
+
+APART = {k: P + 4096 * (i + 1) for i, k in enumerate(("seq_off", "zf", "g", "zo", "h0", "y", "hT", "dy", "dhT", "dzf", "dg",
+                                                      "dzo", "dh0", "ws"))}
+
+
+@pytest.mark.parametrize("out,others", [("y", ("zf", "g", "zo", "hT")), ("hT", ("h0",))])
+def test_scan_forward_refuses_outputs_over_inputs(out, others):
+    base = _with(SCAN_F, **{k: v for k, v in APART.items() if k in SCAN_F})
+    for o in others:
+        assert _code(M.mdl_scan_forward, **_with(base, **{out: base[o]})) == M.MDL_EINVAL, o
+    if out == "hT":     # [S][D] float32, one element past the first and one before the last
+        n = base["S"] * base["D"] * 4
+        assert _code(M.mdl_scan_forward, **_with(base, hT=base["h0"] + n - 4)) == M.MDL_EINVAL
+        assert _code(M.mdl_scan_forward, **_with(base, h0=base["hT"] + 4)) == M.MDL_EINVAL
+        assert _code(M.mdl_scan_forward, **_with(base, T=0, ldz=8, hT=base["h0"])) == M.MDL_EINVAL
+
+
+@pytest.mark.parametrize("out,others", [("dzf", ("zf", "g", "zo", "dy", "dg", "dzo")), ("dg", ("zf", "g", "zo", "dy", "dzo")),
+                                        ("dzo", ("zf", "g", "zo", "dy")), ("dh0", ("h0", "dhT"))])
+def test_scan_backward_refuses_outputs_over_inputs(out, others):
+    base = _with(SCAN_B, **{k: v for k, v in APART.items() if k in SCAN_B})
+    for o in others:
+        assert _code(M.mdl_scan_backward, **_with(base, **{out: base[o]})) == M.MDL_EINVAL, o

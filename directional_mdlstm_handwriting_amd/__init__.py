@@ -95,6 +95,7 @@ _SIGS = [
     ("mdl_distill", _I32, [_I64, _I32, _I32, _I32, _P, _I64, _P, _P, _I32, _P, _F32, _P, _P, _I64, _P]),
     ("mdl_timing", _I32, [_I32]),
     ("mdl_set_wgrad_overlap", _I32, [_I32]),
+    ("mdl_set_scan_wait", _I32, [_I32]),
     ("mdl_timing_only", _I32, [ctypes.c_char_p]),
     ("mdl_timing_report", _I32, [_I32, _P, _P, _P, ctypes.POINTER(_I32)]),
     ("mdl_last_error", ctypes.c_char_p, []),
@@ -403,6 +404,11 @@ def mdl_set_wgrad_overlap(mode):
     """Weight-gradient overlap with the reverse wavefront: True / 1 on, False / 0 off, 2 on with every task
     given up beside the wavefront (the path of a wait that runs out of time)."""
     _check(_lib.mdl_set_wgrad_overlap(int(mode)))
+
+
+def mdl_set_scan_wait(on):
+    """Whether a scan's tiles wait for each other: True / 1 on, False / 0 off (the path of a wait that runs out)."""
+    _check(_lib.mdl_set_scan_wait(int(on)))
 
 
 def mdl_timing(enable: bool):

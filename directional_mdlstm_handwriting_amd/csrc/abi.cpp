@@ -48,6 +48,7 @@ int64_t nfflags_of(const mdl::Layout& L) { return 4 * (int64_t)L.n + 2 * (int64_
 // claimed beside the wavefront is given up and done after it); a stream (default priority) and fork / join
 // events per device
 std::atomic<int> g_overlap{1};
+std::atomic<bool> g_scan_wait{true};
 struct Side {
     hipStream_t s = nullptr;
     hipEvent_t fork = nullptr, join = nullptr;
@@ -947,7 +948,7 @@ int mdl_ctc_head(const mdl_layout* layout, const void* d_desc, const float* y_fl
 }
 
 // Looks at another tile's word before a scan's tile forms what it waits for itself: about a millisecond, many times what
-// a tile takes. None in the mode that allows no wait any time.
+// a tile takes. None where mdl_set_scan_wait(0) leaves out the wait.
 constexpr int kScanPolls = 1024;
 
 // ---- the gated recurrence over packed sequences ---------------------------------------------------
@@ -1038,7 +1039,7 @@ int mdl_scan_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, in
     a.S = S;
     a.D = D;
     a.reverse = reverse != 0;
-    a.polls = g_overlap.load() == 2 ? -1 : kScanPolls;
+    a.polls = g_scan_wait.load() ? kScanPolls : -1;
     a.T = T;
     a.zf = zf;
     a.g = g;
@@ -1082,7 +1083,7 @@ int mdl_scan_backward(const int64_t* seq_off, int32_t S, int64_t T, int32_t D, i
     a.S = S;
     a.D = D;
     a.reverse = reverse != 0;
-    a.polls = g_overlap.load() == 2 ? -1 : kScanPolls;
+    a.polls = g_scan_wait.load() ? kScanPolls : -1;
     a.T = T;
     a.zf = zf;
     a.g = g;
@@ -1279,6 +1280,12 @@ int mdl_distill(int64_t N, int32_t V, int32_t k, int32_t dtype, const void* z, i
     if (e != hipSuccess) return hip_fail(e, F);
     return MDL_OK;
     GUARD_END
+}
+
+int mdl_set_scan_wait(int32_t on) {
+    if (on < 0 || on > 1) return fail(MDL_EINVAL, "mdl_set_scan_wait: on must be 0 or 1");
+    g_scan_wait.store(on != 0);
+    return MDL_OK;
 }
 
 int mdl_set_wgrad_overlap(int32_t mode) {

@@ -580,10 +580,14 @@ int mdl_timing_only(const char* group);
 /* Sets the overlaps with the wavefronts, process-wide: the weight gradients beside the reverse wavefront
  * (mdl_backward) and the direction sum beside the forward one (mdl_forward_dirsum). 1 on (default), 0 off,
  * 2 on with no time allowed for any wait (every task or run claimed beside a wavefront is given up there and
- * computed after it: the path a wait that runs out of time takes, for tests). In mode 2 the tiles of
- * mdl_scan_forward / _backward do not wait for each other either; each then forms what it needs itself (slow on
- * long sequences). The results do not depend on the mode. MDL_EINVAL for any other mode. */
+ * computed after it: the path a wait that runs out of time takes, for tests). The results do not depend on
+ * it. MDL_EINVAL for any other mode. */
 int mdl_set_wgrad_overlap(int32_t mode);
+
+/* Whether the tiles of mdl_scan_forward / _backward wait for each other, process-wide: 1 on (default); 0 off,
+ * each then forms what it needs itself (the path a wait that runs out of time takes, for tests: slow on long
+ * sequences). The results do not depend on it. MDL_EINVAL for any other value. */
+int mdl_set_scan_wait(int32_t on);
 int mdl_timing_report(int32_t max, char* names, double* total_ms, int64_t* launches, int32_t* count);
 
 /* Message of the last failed call on this thread ("" if none). */

@@ -151,3 +151,10 @@ def test_scan_backward_refuses_outputs_over_inputs(out, others):
     base = _with(SCAN_B, **{k: v for k, v in APART.items() if k in SCAN_B})
     for o in others:
         assert _code(M.mdl_scan_backward, **_with(base, **{out: base[o]})) == M.MDL_EINVAL, o
+
+
+def test_scan_wait_is_on_or_off():
+    for bad in (-1, 2):
+        assert _code(M.mdl_set_scan_wait, bad) == M.MDL_EINVAL
+    for on in (0, 1):
+        M.mdl_set_scan_wait(on)

@@ -339,9 +339,12 @@ void with_shape(int D, int dtype, F&& fn) {
         if (nv <= 256) return fn(ty, NormShape<V, 256, 1>{});
         if (nv <= 512) return fn(ty, NormShape<V, 256, 2>{});
         if (nv <= 1024) return fn(ty, NormShape<V, 512, 2>{});
-        if constexpr (V == 8) return fn(ty, NormShape<V, 1024, 2>{});
-        if (nv <= 2048) return fn(ty, NormShape<V, 512, 4>{});
-        return fn(ty, NormShape<V, 1024, 4>{});
+        if constexpr (V == 8) {
+            return fn(ty, NormShape<V, 1024, 2>{});
+        } else {
+            if (nv <= 2048) return fn(ty, NormShape<V, 512, 4>{});
+            return fn(ty, NormShape<V, 1024, 4>{});
+        }
     };
     if (dtype == 1) go(bf16{});
     else go(float{});

@@ -67,10 +67,9 @@ struct Tile {
     int c0;       // first channel
 };
 
-// Sequence marks of the tile's positions: start[p] / last[p] hold sequence + 1 where position p0 + p is a sequence's
-// first / last in scan order, 0 elsewhere. Sequences without tokens hand `from` to `to` ([S][D], zero if null).
+// the tokens [t0, t1) of a tile that starts at position p0
 template <int TT>
-__device__ inline void tile_tokens(const ScanArgs& a, int64_t p0, int64_t& t0, int64_t& t1) {  // tokens [t0, t1)
+__device__ inline void tile_tokens(const ScanArgs& a, int64_t p0, int64_t& t0, int64_t& t1) {
     t1 = a.reverse ? a.T - p0 : lesser(p0 + TT, a.T);
     t0 = a.reverse ? -lesser(p0 + TT - a.T, 0) : p0;
 }
@@ -89,6 +88,8 @@ struct Seq {
         }
     }
 };
+// Sequence marks of the tile's positions: start[p] / last[p] hold sequence + 1 where position p0 + p is a sequence's
+// first / last in scan order, 0 elsewhere. Sequences without tokens hand `from` to `to` ([S][D], zero if null).
 template <int TT, int CB>
 __device__ inline void mark_tile(const ScanArgs& a, Tile t, Seq q, int* start, int* last, const float* from,
                                  float* to) {
@@ -491,7 +492,7 @@ template <typename T, int V, int CL, int NT>
 __global__ __launch_bounds__(SCAN_THREADS, V == 4 ? 4 : 3) void k_scan_bwd(ScanArgs a) {
     constexpr int G = SCAN_THREADS / CL, TT = G * NT, CB = CL * V, HV = V > 4 ? 4 : V;
     constexpr int CW = (CB + 63) / 64 * 64;
-    static_assert(2 * CW <= SCAN_THREADS, "two sets of one thread per channel");
+    static_assert(3 * CW <= SCAN_THREADS, "three sets of one thread per channel");
     __shared__ int start[TT], last[TT];
     __shared__ f32x2 maps[G][CB], rmaps[G][CB];  // of the token groups, and what enters them
     __shared__ float into[G][CB], rinto[G][CB];
@@ -564,12 +565,11 @@ __global__ __launch_bounds__(SCAN_THREADS, V == 4 ? 4 : 3) void k_scan_bwd(ScanA
     }
     __syncthreads();
     // Waves in parallel, one thread per channel: the first composes the tile's reverse map, the next chains the forward
-    // maps from the incoming state, a third hands on the reverse map where there are waves left.
-    constexpr bool kThird = 3 * CW <= SCAN_THREADS;
+    // maps from the incoming state, a third hands on the reverse map.
     uint64_t* const w = a.words + tile.c0;
     const int c1 = threadIdx.x, c2 = c1 - CW, c3 = c2 - CW;
     float ta = 1.f, tb = 0.f;
-    if (a.ntiles > 1 && (c1 < CB || (kThird && c3 >= 0 && c3 < CB))) {
+    if (a.ntiles > 1 && (c1 < CB || (c3 >= 0 && c3 < CB))) {
         const int c = c1 < CB ? c1 : c3;
 #pragma unroll 8
         for (int j = G - 1; j >= 0; --j) {
@@ -577,8 +577,7 @@ __global__ __launch_bounds__(SCAN_THREADS, V == 4 ? 4 : 3) void k_scan_bwd(ScanA
             tb = apply_map(m[0], m[1], tb);
             ta = m[0] < 0.f || ta < 0.f ? kReset : ta * m[0];
         }
-        if (!kThird) put_word(w + k * a.slots + c, ta, tb);
-        else if (c1 >= CB) offer_word(w + k * a.slots + c, ta, tb);
+        if (c1 >= CB) offer_word(w + k * a.slots + c, ta, tb);
     }
     if (c2 >= 0 && c2 < CB) {
         float x = a.ntiles > 1 ? a.carry[(int64_t)(linear / a.ncb) * a.slots + tile.c0 + c2] : 0.f;

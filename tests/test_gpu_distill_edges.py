@@ -1,6 +1,9 @@
 """mdl_distill where its range or its rules end: weight 0 beside classes that do not exist, temperatures whose square is
 no fp32 number, rows longer than the registers hold, and rows near 2^31 classes. Tolerances are test_gpu_distill.py's."""
 
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -9,7 +12,64 @@ pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
     import directional_mdlstm_handwriting_amd as M
+    import test_gpu_distill as td
     from test_gpu_distill import DEV, U, make, run
+
+VEC = {"f32": 4, "bf16": 8}
+
+
+def _held_vectors():
+    """The longest row, in vectors of 16 bytes, that a workgroup keeps in registers: from the kernel's own dispatch, so
+    that these tests follow it. Longer rows are read twice."""
+    src = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "directional_mdlstm_handwriting_amd",
+                       "csrc", "k_distill.hip")
+    bounds = re.findall(r"nv <= (\d+)\) return fn\(ty, DistillShape<V, \d+, (\d+)>", open(src).read())
+    assert bounds and all(int(nv) > 0 for _, nv in bounds)
+    return max(int(b) for b, _ in bounds)
+
+
+# the last row that is held; and of those read twice: the first, one of whole vectors, one of several walks and a tail
+LONG = [(d, more) for d in ("f32", "bf16") for more in (0, 1, 64, 40003)]
+
+
+def _long(dtype, more):
+    return _held_vectors() * VEC[dtype] + more
+
+
+@pytest.mark.parametrize("dtype,more", LONG)
+def test_rows_read_twice(dtype, more):
+    V = _long(dtype, more)
+    z, ids, t, w = make(V, 3, V, 7, dtype)
+    run(z, ids, t, w, 2.0, dtype)
+
+
+@pytest.mark.parametrize("dtype,more", LONG[1::2])
+def test_rows_read_twice_that_count_for_nothing_and_masked_classes(dtype, more):
+    td.test_rows_that_count_for_nothing_and_masked_classes(_long(dtype, more), dtype)
+
+
+@pytest.mark.parametrize("dtype,more", LONG[1:])
+def test_rows_read_twice_strides_in_place_and_loss_alone(dtype, more):
+    td.test_strides_in_place_and_loss_alone(_long(dtype, more), dtype)
+
+
+@pytest.mark.parametrize("dtype,more", LONG[1:])
+def test_rows_read_twice_keep_nan_and_infinities_to_themselves(dtype, more):
+    """NaN and -inf at the row's first element, inside and behind its last whole vector."""
+    V = _long(dtype, more)
+    z, ids, t, w = make(23, 5, V, 4, dtype)
+    _, l0, d0 = run(z, ids, t, w, 1.0, dtype)
+    l0, d0 = l0.clone(), d0.clone()
+    for at in (0, V // 2, V - 1):
+        bad = z.clone()
+        bad[2, at] = float("nan")
+        bad[3] = float("-inf")
+        bad[3, at] = 1.0
+        loss, dz = td.TopKDistill(5, V, 4, dtype, 1.0, device=DEV).run(bad, ids, t, w)
+        torch.cuda.synchronize()
+        assert torch.equal(loss[[0, 1, 4]], l0[[0, 1, 4]]) and torch.equal(dz[[0, 1, 4]], d0[[0, 1, 4]]), at
+        assert torch.isnan(loss[2]) and torch.isnan(dz[2].float()).all(), at
+        td.check(bad[3:4], ids[3:4], t[3:4], w[3:4], 1.0, loss[3:4], dz[3:4], dtype)
 
 
 @pytest.mark.parametrize("V,dtype", [(7, "f32"), (300, "bf16"), (5003, "f32")])

@@ -452,43 +452,47 @@ class ScanState(_Buffers):
     then held as long as the object (a server captures few sizes), or else one of the graph's own."""
 
     KEPT = 8
+    HELD = -1
 
     def __init__(self, n_slots: int, D: int, x_dtype: str = "f32", device: str = "cuda"):
         self.device = _device(device)
         self.n_slots, self.D = int(n_slots), int(D)
         self.x_dtype, self.tdt = _x_dtype(x_dtype)
         self.state = torch.zeros(self.n_slots, self.D, dtype=torch.float32, device=self.device)
-        self._y = {}            # rows: (output, handle of the stream it was made on), the oldest first
-        self._captured = {}     # rows: output that a graph writes
+        # rows: (output, handle of the stream it was made on; HELD where a graph writes it), the oldest first
+        self._y = {}
         self._made(self.device)
 
     def _output(self, S: int, handle: int) -> torch.Tensor:
-        y = self._captured.get(S)
-        if y is not None:
-            return y
         y, home = self._y.get(S, (None, None))
+        if home == self.HELD:
+            return y
         if y is not None and self._capturing(handle):
-            self._captured[S] = self._y.pop(S)[0]
+            self._y[S] = y, self.HELD
         elif home != handle:
             # never used on a stream but its own, on which its memory may be handed out again once it is dropped
             y, keep = self._new(handle, (S, self.D), self.tdt, True)
             if keep:
                 self._y.pop(S, None)
                 self._y[S] = y, handle
-                if len(self._y) > self.KEPT:
-                    del self._y[next(iter(self._y))]
+                loose = [s for s, (_, h) in self._y.items() if h != self.HELD]
+                if len(loose) > self.KEPT:
+                    del self._y[loose[0]]
         return y
 
     def step(self, zf, g, zo=None, slots=None, out=None, stream=None):
         """y [S][D] of one token for each row's slot (slots int32 [S], all different; the first S rows if None). The
         states advance in place, or into the same rows of `out` ([n_slots][D]). A row whose slot is no slot (-1 in a
         padded batch) is left out, and its y means nothing."""
+        current = stream is None
         stream = self._launch(stream)
         S = int(zf.shape[0])
         ldz = _same_rows(("zf", "g", "zo"), (zf, g, zo), (S, self.D), self.tdt, self.device)
         _full("slots", slots, (S,), torch.int32, self.device)
         _full("out", out, (self.n_slots, self.D), torch.float32, self.device)
-        y = self._output(S, stream)
+        y, home = self._y.get(S, (None, None))
+        if home != stream or not current or torch.cuda.is_current_stream_capturing():
+            y = self._output(S, stream)
         mdl_scan_step(S, self.D, self.x_dtype, zf, g, zo, ldz, slots, self.n_slots, self.state,
                       self.state if out is None else out, y, self.D, stream)
         return y

@@ -14,9 +14,11 @@
 // between waves through LDS where a row takes more than one. r enters the second norm as the fp32 value, before its
 // rounding to the output's type. All sums are fp32.
 //
-// Bound by HBM: 20480 x 2048 in bfloat16 takes 79 us forward (419 MB, 5.3 TB/s) and 143 us backward (671 MB, 4.7 TB/s) and
-// 7.4 us for the weight gradients out of the workgroups' column sums; 81920 x 50 in fp32, rows of 200 bytes, 13.7, 23.6
-// and 4.0 us (82, 131 and 0.8 MB; the first two above the rate of a large copy, 4.93 TB/s).
+// Bound by HBM: 20480 x 2048 in bfloat16 takes 80 us forward (419 MB, 5.2 TB/s) and 146 us backward (671 MB, 4.6 TB/s) and
+// 7.6 us for the weight gradients out of the workgroups' column sums; 81920 x 50 in fp32, rows of 200 bytes, 13.7, 23.6
+// and 4.7 us (82, 131 and 0.8 MB; the first two above the rate of a large copy, 4.93 TB/s). The backward of rows above
+// 8192 elements is bound by its spills: 4096 x 16384 takes 1.13 ms in bfloat16 and 1.33 ms in fp32 (1.07 and 2.15 GB; 4096 x
+// 8192: 0.17 and 0.26 ms).
 #include "kernels.h"
 #include "seqio.h"
 
@@ -323,7 +325,8 @@ __global__ __launch_bounds__(kWredCols * kWredGroups) void k_norm_wreduce(
 
 // Lanes a row: the fewest that hold it in one vector each up to a wave, two vectors each up to 128 (the row sums then need
 // no LDS), and from there as many waves as keep the backward's row in its registers (five tensors, 224 registers at two
-// vectors of eight). Rows of more than 8192 elements spill some of them.
+// vectors of eight). Rows of more than 8192 elements take 1024 threads of 128 registers each, of which the backward spills
+// 144 in bfloat16 (484 bytes a lane) and 195 in fp32 (544 bytes); in fp32 rows of more than 4096 spill 2 (12 bytes).
 template <typename F>
 void with_shape(int D, int dtype, F&& fn) {
     auto go = [&](auto ty) {

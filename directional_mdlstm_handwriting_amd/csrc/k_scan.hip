@@ -14,14 +14,19 @@
 // The tiles' maps are handed from tile to tile in the same launch (see look_back), so every stream is read and written
 // once. All states, maps and sums are fp32; a stream of bfloat16 is rounded once, as it is stored.
 //
-// Bound by HBM on long inputs: 208246 tokens x 1024 channels in bfloat16 take 360 us forward (1.71 GB, 4.7 TB/s; a copy
-// runs at 4.93) and 620 us backward (2.99 GB, 4.8 TB/s), with the vector ALUs, by the count of their instructions, close
-// to busy as well (91 and 78 % of the cycles); 656603 tokens x 32 in
-// fp32 without an output gate 52 us (252 MB) and 74 us (420 MB). One short generation of workgroups is bound by its
-// latency, read, chain, write: 20597 tokens x 512 in bfloat16 take 24 us (84 MB) and 37 us (148 MB).
-// The tile of 128 tokens by 128 bytes of channels: timed side by side on the 208246 tokens, when the kernels took 365 us
-// forward and 649 us backward, one of 64 tokens by 128 bytes took 465 and 704 us, one of 64 by 256 bytes 474 and 675,
-// one of 256 by 64 bytes 438 and 873.
+// Bound by HBM on long inputs: 208246 tokens x 1024 channels in bfloat16 take 352 us forward (1.71 GB, 4.9 TB/s, the rate
+// of a copy) and 597 us backward (2.99 GB, 5.0 TB/s), with the vector ALUs, by the count of their instructions, close to
+// busy as well (89 and 76 % of the cycles); 656603 tokens x 32 in fp32 without an output gate 52 us (252 MB) and 75 us
+// (420 MB). A generation or two of workgroups are bound by their latency, read, chain, write: 20597 tokens x 512 in
+// bfloat16 take 24 us (84 MB) and 38 us (148 MB). Rows that are no multiple of 128 bytes cost far more: a tile's 128 bytes
+// then straddle two lines of every row, which two workgroups read and write; 206796 x 1030 take 615 and 1377 us.
+// (Medians of 10 passes under the profiler; in 60 passes in a row the first case takes 338 and 563 us a pass, with the
+// launches that clear the words. The backward for bfloat16 spills 4 registers, 20 bytes a lane.)
+// The tile of 128 tokens by 128 bytes of channels, beside others in one session, us forward and backward:
+//   tokens by bytes             128 by 128     64 by 128     64 by 256     256 by 64
+//   208246 x 1024, bfloat16      352   597     446   697     455   599     457   849
+//   656603 x 32, fp32             52    75      62    82      85   114      70   106
+//   20597 x 512, bfloat16         24    38      27    41      25    38      33    49
 #include "kernels.h"
 #include "seqio.h"
 
@@ -159,8 +164,8 @@ struct Share {
 
 // Number of a workgroup's tile and channel block, tile ncb + block: the blocks of successive tiles are rotated by one, so
 // that a workgroup id's remainder by the 8 dies, whose L2s share the work round-robin, falls on every part of a row. (With
-// the plain order a die reads the same eighth of every row: 213k tokens x 1024 in bfloat16 took 476 us forward and 776
-// backward, rotated 359 and 650.)
+// the plain order a die reads the same eighth of every row: 208246 tokens x 1024 in bfloat16 take 439 us forward and 634
+// backward, rotated 352 and 597. Rows of one channel block are the same either way.)
 __device__ inline int tile_id(const ScanArgs& a) {
     const int k = blockIdx.x / a.ncb, c = blockIdx.x % a.ncb;
     return k * a.ncb + (c + k) % a.ncb;
@@ -776,8 +781,10 @@ static hipError_t scan_run(ScanArgs a, int dtype, void* ws, bool backward, hipSt
         a.seq = reinterpret_cast<int32_t*>(w + p.seq);
         a.carry = reinterpret_cast<float*>(w + p.carry);
     }
-    // Streams larger than the memory-side cache are read past it: nothing of them would be found there again (208246 x
-    // 1024 in bfloat16, 426 MB a stream, both ways: 925 us, 961 otherwise; 656603 x 32 in fp32, 84 MB a stream: 142 and 127).
+    // Streams larger than the memory-side cache are read past it: nothing of them would be found there again (both
+    // kernels: 208246 x 1024 in bfloat16, 426 MB a stream, 949 us, 1015 otherwise; 656603 x 32 in fp32, 84 MB a stream, 135
+    // us, 126 otherwise). Rows that are no multiple of 128 bytes lose by it, since the line that two workgroups share is
+    // then read twice: 206796 x 1030 takes 1992 us, 1669 otherwise.
     a.once = a.T * a.D >= (int64_t(256) << 20) / (dtype == 1 ? 2 : 4);
     const dim3 grid((unsigned)(p.ntiles * p.ncb)), block(SCAN_THREADS);
     with_shape(a.D, dtype, [&](auto ty, auto sh) {

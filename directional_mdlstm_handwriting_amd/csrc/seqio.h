@@ -86,8 +86,10 @@ __device__ inline uint32_t pack_bf16(float lo, float hi) {
 }
 
 // Whole vectors of an output are stored as data that is not read again here (nontemporal): they then leave the inputs in
-// the caches. 4096 x 32000 distilled in bfloat16 takes 99 us this way and 122 with plain stores, a scan of 656603 x 32 in
-// fp32 both ways 127 and 148, the norms of 20480 x 2048 in bfloat16 both ways 228 and 237.
+// the caches. 4096 x 32000 distilled in bfloat16 takes 102 us this way and 119 with plain stores, a scan of 656603 x 32 in
+// fp32 both ways 126 and 150, the norms of 20480 x 2048 in bfloat16 both ways 224 and 229 (each with the other in one
+// session). Rows that share lines between workgroups lose by it where they are many: a scan of 206796 x 1030 in bfloat16
+// takes 615 and 1377 us, 686 and 1208 with plain stores.
 template <int V>
 __device__ inline void store_vec(float* p, const float (&v)[V]) {
     if constexpr (V == 4) {
@@ -138,9 +140,12 @@ struct Width<bf16> {
     static constexpr int v = 8;
 };
 
-// e^x for x <= 0. Where the result is rounded to bfloat16, the hardware exp2 of the rounded product x log2 e, whose
-// relative error of up to |x| 2^-24 is far below half a bfloat16 step; for fp32 results the product's rounding error
-// is carried along (its remainder and log2 e's own low part, to first order), which leaves about 1.5 ulp at any x.
+// e^x for x <= 0. For streams of bfloat16 the hardware exp2 of the rounded product x log2 e: its relative error of up to
+// |x| 2^-24 is far below half a step of their outputs, and the fp32 states that such streams leave (last states, stepped
+// states, gradients of the first ones) carry it in their gates beside the roundings of the recurrence itself. For fp32
+// streams the product's rounding error is carried along (its remainder and log2 e's own low part, to first order), which
+// leaves about 1.5 ulp at any x. exp2, the reciprocal of the sigmoid and the norms' reciprocal root are the hardware's,
+// within 1 ulp where a division or root would be rounded.
 template <typename T>
 __device__ inline float exp_neg(float x) {
     constexpr float hi = 1.44269502162933349609f, lo = 1.92596299112661746887e-8f;  // log2 e in two floats

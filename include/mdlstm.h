@@ -498,16 +498,19 @@ int mdl_scan_step(int32_t S, int32_t D, int32_t dtype, const void* zf, const voi
  * (ones), w_pre and v NULL (after the last block). x, z, u, r, v, dr, dv are
  * [N][D] of `dtype`; row strides in elements: ldx (x), ldz (z), ldu (u), ldr
  * (r, v, dr, dv), ldd (dx, dz, du); ldz and ldu are ignored without z and u.
- * Weights and their gradients are [D] float32. Row and column sums are float32;
- * v is formed from r before r's rounding; each output is rounded once. Any
- * alignment of the element type is taken.
+ * Weights and their gradients are [D] float32. Row and column sums are float32,
+ * of squares among others: rows of z and r with elements of 1e17 and more are out
+ * of range, and with eps = 0 so are rows with none above 1e-18. v is formed from
+ * r before r's rounding; each output is rounded once. Any alignment of the
+ * element type is taken.
  * mdl_blocknorm_backward, from dr and dv (gradients of r and v; one of them may
  * be NULL: dv exactly when w_pre is, dr where nothing else reads r): dx; dz and
  * du exactly when z and u are given; dw_post, dscale, dw_pre, each exactly when
- * its weight is. The weight gradients are fixed-order sums over the rows
- * (workgroup sums added in order). ws: >= mdl_blocknorm_workspace_size bytes,
- * 16-byte aligned, contents not kept. With N = 0 the row tensors may be NULL
- * and the weight gradients are zero.
+ * its weight is. The weight gradients are sums over the rows in a fixed order
+ * (each workgroup's rows one after another; then the workgroups' sums, every
+ * 64th of them one after another and those 64 pairwise). ws: >=
+ * mdl_blocknorm_workspace_size bytes, 16-byte aligned, contents not kept. With
+ * N = 0 the row tensors may be NULL and the weight gradients are zero.
  * An output may be an input of the same row at the same address and stride (r
  * over x, dx over dr); other overlaps are not allowed.
  * Errors: MDL_EINVAL for null tensors or parts that do not go together, N < 0,

@@ -12,8 +12,8 @@
 // in LDS; their gradients are written over the row's after it, by the lanes that own the slots (a class named twice gets
 // both slots' p). Statistics are fp32; the gradient is rounded once.
 //
-// Bound by HBM: 4096 x 32000 in bfloat16 takes 100 us (525 MB, 5.2 TB/s; a copy runs at 4.93), 1000 x 100003 in fp32
-// 183 us (800 MB, 4.4 TB/s; 192 if it is read twice), 60000 x 80 in fp32 12 us (38 MB). Each kept class is compared with
+// Bound by HBM: 4096 x 32000 in bfloat16 takes 98 us (525 MB, 5.4 TB/s; a copy runs at 4.93), 1000 x 100003 in fp32
+// 186 us (800 MB, 4.3 TB/s; 192 if it is read twice), 60000 x 80 in fp32 13 us (38 MB). Each kept class is compared with
 // all of them, so that many of them on a short row are bound by that: 50000 x 256 in fp32 takes 23 us with 8 kept classes,
 // 71 with 64 and 967 with 256 (102 MB).
 #include "kernels.h"
@@ -314,8 +314,8 @@ __global__ __launch_bounds__(S::threads, 4) void k_distill(DistillArgs a) {
 }
 
 // Lanes a row: few with several vectors each, which leaves more rows to a workgroup and fewer exchanges between lanes
-// (60000 frames x 80 classes in fp32: 8 lanes of 4 vectors 12.3 us, 64 of one 32.8; 26225 x 4046 in bfloat16: 128 lanes of
-// 4 vectors 72 us, 256 of 4 112), up to 26 vectors, what 1024 threads' registers hold.
+// (60000 frames x 80 classes in fp32: 8 lanes of 4 vectors 12.9 us, 64 of one 32.9; 26225 x 4046 in bfloat16: 128 lanes of
+// 4 vectors 73 us, 256 of 4 112), up to 26 vectors, what 1024 threads' registers hold.
 template <typename F>
 void with_shape(int64_t V_, int dtype, F&& fn) {
     auto go = [&](auto ty) {

@@ -14,9 +14,9 @@
 // between waves through LDS where a row takes more than one. r enters the second norm as the fp32 value, before its
 // rounding to the output's type. All sums are fp32.
 //
-// Bound by HBM: 20480 x 2048 in bfloat16 takes 80 us forward (419 MB, 5.2 TB/s) and 146 us backward (671 MB, 4.6 TB/s) and
-// 7.6 us for the weight gradients out of the workgroups' column sums; 81920 x 50 in fp32, rows of 200 bytes, 13.7, 23.6
-// and 4.7 us (82, 131 and 0.8 MB; the first two above the rate of a large copy, 4.93 TB/s). The backward of rows above
+// Bound by HBM: 20480 x 2048 in bfloat16 takes 80 us forward (419 MB, 5.2 TB/s) and 145 us backward (671 MB, 4.6 TB/s) and
+// 7.5 us for the weight gradients out of the workgroups' column sums; 81920 x 50 in fp32, rows of 200 bytes, 13.0, 23.5
+// and 4.8 us (82, 131 and 0.8 MB; the first two above the rate of a large copy, 4.93 TB/s). The backward of rows above
 // 8192 elements is bound by its spills: 4096 x 16384 takes 1.13 ms in bfloat16 and 1.33 ms in fp32 (1.07 and 2.15 GB; 4096 x
 // 8192: 0.17 and 0.26 ms).
 #include "kernels.h"

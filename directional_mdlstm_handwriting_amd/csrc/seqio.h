@@ -88,8 +88,8 @@ __device__ inline uint32_t pack_bf16(float lo, float hi) {
 // Whole vectors of an output are stored as data that is not read again here (nontemporal): they then leave the inputs in
 // the caches. 4096 x 32000 distilled in bfloat16 takes 102 us this way and 119 with plain stores, a scan of 656603 x 32 in
 // fp32 both ways 126 and 150, the norms of 20480 x 2048 in bfloat16 both ways 224 and 229 (each with the other in one
-// session). Rows that share lines between workgroups lose by it where they are many: a scan of 206796 x 1030 in bfloat16
-// takes 615 and 1377 us, 686 and 1208 with plain stores.
+// session). Where rows share lines between workgroups it can lose: a scan of 206796 x 1030 in bfloat16 takes 615 us forward
+// and 1377 backward, 686 and 1208 with plain stores.
 template <int V>
 __device__ inline void store_vec(float* p, const float (&v)[V]) {
     if constexpr (V == 4) {

@@ -93,6 +93,14 @@ _SIGS = [
     ("mdl_blocknorm_backward", _I32, [_I64, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _F32, _P, _P, _I64,
                                       _P, _P, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
     ("mdl_distill", _I32, [_I64, _I32, _I32, _I32, _P, _I64, _P, _P, _I32, _P, _F32, _P, _P, _I64, _P]),
+    ("mdl_linattn_workspace_size", _I32, [_I64, _I32, _I32, _I32, _I32, ctypes.POINTER(_SZ)]),
+    ("mdl_linattn_forward", _I32, [_P, _I32, _I64, _I32, _I32, _I32, _I32, _I32, _P, _F32, _P, _I64, _P, _I64, _P, _I64,
+                                   _P, _P, _I64, _P, _P, _SZ, _P]),
+    ("mdl_linattn_backward", _I32, [_P, _I32, _I64, _I32, _I32, _I32, _I32, _I32, _P, _F32, _P, _I64, _P, _I64, _P,
+                                    _I64, _P, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _SZ, _P]),
+    ("mdl_linattn_step", _I32, [_I32, _I32, _I32, _I32, _I32, _P, _F32, _P, _I64, _P, _I64, _P, _I64, _P, _I32, _P, _P,
+                                _P, _I64, _P]),
+    ("mdl_dropout", _I32, [_I64, _I32, _I32, _P, _I64, _P, _I64, _F32, _P, _P, _I64, _P]),
     ("mdl_timing", _I32, [_I32]),
     ("mdl_set_wgrad_overlap", _I32, [_I32]),
     ("mdl_set_scan_wait", _I32, [_I32]),
@@ -398,6 +406,37 @@ def mdl_distill(N: int, V: int, k: int, dtype: int, z, ldz: int, ids, t, t_dtype
                 ldd: int, stream=None):
     _check(_lib.mdl_distill(N, V, k, dtype, _ptr(z), ldz, _ptr(ids), _ptr(t), t_dtype, _ptr(w), tau, _ptr(loss),
                             _ptr(dz), ldd, _stream(stream)))
+
+
+def mdl_linattn_workspace_size(T: int, H: int, Dk: int, Dv: int, dtype: int) -> int:
+    b = _SZ()
+    _check(_lib.mdl_linattn_workspace_size(T, H, Dk, Dv, dtype, ctypes.byref(b)))
+    return b.value
+
+
+def mdl_linattn_forward(seq_off, S: int, T: int, H: int, Dk: int, Dv: int, dtype: int, reverse: int, decay, scale: float,
+                        q, ldq: int, k, ldk: int, v, ldv: int, h0, y, ldy: int, hT, ws, ws_bytes: int, stream=None):
+    _check(_lib.mdl_linattn_forward(_ptr(seq_off), S, T, H, Dk, Dv, dtype, reverse, _ptr(decay), scale, _ptr(q), ldq,
+                                    _ptr(k), ldk, _ptr(v), ldv, _ptr(h0), _ptr(y), ldy, _ptr(hT), _ptr(ws), ws_bytes,
+                                    _stream(stream)))
+
+
+def mdl_linattn_backward(seq_off, S: int, T: int, H: int, Dk: int, Dv: int, dtype: int, reverse: int, decay,
+                         scale: float, q, ldq: int, k, ldk: int, v, ldv: int, h0, dy, lddy: int, dhT, dq, lddq: int, dk,
+                         lddk: int, dv, lddv: int, dh0, ws, ws_bytes: int, stream=None):
+    _check(_lib.mdl_linattn_backward(_ptr(seq_off), S, T, H, Dk, Dv, dtype, reverse, _ptr(decay), scale, _ptr(q), ldq,
+                                     _ptr(k), ldk, _ptr(v), ldv, _ptr(h0), _ptr(dy), lddy, _ptr(dhT), _ptr(dq), lddq,
+                                     _ptr(dk), lddk, _ptr(dv), lddv, _ptr(dh0), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def mdl_linattn_step(S: int, H: int, Dk: int, Dv: int, dtype: int, decay, scale: float, q, ldq: int, k, ldk: int, v,
+                     ldv: int, slots, n_slots: int, h_in, h_out, y, ldy: int, stream=None):
+    _check(_lib.mdl_linattn_step(S, H, Dk, Dv, dtype, _ptr(decay), scale, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv,
+                                 _ptr(slots), n_slots, _ptr(h_in), _ptr(h_out), _ptr(y), ldy, _stream(stream)))
+
+
+def mdl_dropout(N: int, D: int, dtype: int, x, ldx: int, r, ldr: int, p: float, rng, y, ldy: int, stream=None):
+    _check(_lib.mdl_dropout(N, D, dtype, _ptr(x), ldx, _ptr(r), ldr, p, _ptr(rng), _ptr(y), ldy, _stream(stream)))
 
 
 def mdl_set_wgrad_overlap(mode):

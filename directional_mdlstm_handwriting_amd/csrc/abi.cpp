@@ -1282,6 +1282,226 @@ int mdl_distill(int64_t N, int32_t V, int32_t k, int32_t dtype, const void* z, i
     GUARD_END
 }
 
+// ---- linear attention with a decay for each head -------------------------------------------------------
+// sizes of an attention call; need receives the workspace bytes
+static int check_attn(const std::string& F, int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype, size_t& need) {
+    int rc = check_dtype(F, dtype);
+    if (rc) return rc;
+    if (T < 0 || H < 1 || Dk < 1 || Dv < 1) return fail(MDL_EINVAL, F + ": need T >= 0 and H, Dk, Dv >= 1");
+    if (Dk > mdl::linattn_max_d() || Dv > mdl::linattn_max_d())
+        return fail(MDL_EUNSUPPORTED, F + ": Dk or Dv above " + std::to_string(mdl::linattn_max_d()));
+    if (H > 65535) return fail(MDL_EUNSUPPORTED, F + ": H above 65535");
+    if (T >= (int64_t(1) << 36)) return fail(MDL_EOVERFLOW, F + ": T reaches 2^36");
+    const mdl::AttnPlan p = mdl::attn_plan(T, H, Dk, Dv);
+    if (p.ntiles > mdl::kMaxLaunchThreads / 256) return fail(MDL_EOVERFLOW, F + ": the launch exceeds 2^31 threads");
+    need = p.total;
+    return MDL_OK;
+}
+// the sequences of a call whose states are walked: a launch over S times the states' elements
+static int check_attn_sequences(const std::string& F, int32_t S, int64_t T, int32_t H, int32_t Dk, int32_t Dv) {
+    int rc = check_sequences(F, S);
+    if (rc) return rc;
+    if (S > mdl::kMaxLaunchThreads / 256 / mdl::attn_plan(T, H, Dk, Dv).chain_blocks)
+        return fail(MDL_EOVERFLOW, F + ": S times the states exceeds 2^31 threads");
+    return MDL_OK;
+}
+// whether `bytes` bytes at a and b share any
+static bool share_bytes(const void* a, const void* b, uint64_t bytes) {
+    if (!a || !b) return false;
+    const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return (x > y ? x - y : y - x) < bytes;
+}
+static uint64_t state_bytes(int32_t S, int32_t H, int32_t Dk, int32_t Dv) {
+    return (uint64_t)S * (uint64_t)H * (uint64_t)Dk * (uint64_t)Dv * 4;
+}
+
+int mdl_linattn_workspace_size(int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype, size_t* bytes) {
+    GUARD_BEGIN
+    if (!bytes) return fail(MDL_EINVAL, "mdl_linattn_workspace_size: null argument");
+    size_t need = 0;
+    const int rc = check_attn("mdl_linattn_workspace_size", T, H, Dk, Dv, dtype, need);
+    if (rc) return rc;
+    *bytes = need;
+    return MDL_OK;
+    GUARD_END
+}
+
+int mdl_linattn_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype,
+                        int32_t reverse, const float* decay, float scale, const void* q, int64_t ldq, const void* k,
+                        int64_t ldk, const void* v, int64_t ldv, const float* h0, void* y, int64_t ldy, float* hT,
+                        void* ws, size_t ws_bytes, void* stream) {
+    GUARD_BEGIN
+    const std::string F("mdl_linattn_forward");
+    size_t need = 0;
+    int rc = check_attn(F, T, H, Dk, Dv, dtype, need);
+    if (rc || (rc = check_attn_sequences(F, S, T, H, Dk, Dv))) return rc;
+    if (!seq_off || !decay || (T > 0 && (!q || !k || !v || !y))) return fail(MDL_EINVAL, F + ": null tensor");
+    const int64_t nk = (int64_t)H * Dk, nv = (int64_t)H * Dv;
+    if ((rc = check_stride(F, "ldq", T, nk, ldq)) || (rc = check_stride(F, "ldk", T, nk, ldk)) ||
+        (rc = check_stride(F, "ldv", T, nv, ldv)) || (rc = check_stride(F, "ldy", T, nv, ldy)))
+        return rc;
+    if ((rc = check_ws(F, "mdl_linattn_workspace_size", need, ws, ws_bytes))) return rc;
+    if (T > 0 && (rc = check_apart(F, {y, hT}, {q, k, v}))) return rc;
+    if (share_bytes(h0, hT, state_bytes(S, H, Dk, Dv))) return fail(MDL_EINVAL, F + ": hT over h0");
+    mdl::AttnArgs a{};
+    a.off = seq_off;
+    a.S = S;
+    a.H = H;
+    a.Dk = Dk;
+    a.Dv = Dv;
+    a.reverse = reverse != 0;
+    a.T = T;
+    a.decay = decay;
+    a.scale = scale;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.h0 = h0;
+    a.y = y;
+    a.ldy = ldy;
+    a.hT = hT;
+    hipError_t e;
+    {
+        Timed t("attn_fwd");
+        e = mdl::launch_attn_fwd(a, dtype, ws, static_cast<hipStream_t>(stream));
+    }
+    if (e != hipSuccess) return hip_fail(e, F);
+    return MDL_OK;
+    GUARD_END
+}
+
+int mdl_linattn_backward(const int64_t* seq_off, int32_t S, int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype,
+                         int32_t reverse, const float* decay, float scale, const void* q, int64_t ldq, const void* k,
+                         int64_t ldk, const void* v, int64_t ldv, const float* h0, const void* dy, int64_t lddy,
+                         const float* dhT, void* dq, int64_t lddq, void* dk, int64_t lddk, void* dv, int64_t lddv,
+                         float* dh0, void* ws, size_t ws_bytes, void* stream) {
+    GUARD_BEGIN
+    const std::string F("mdl_linattn_backward");
+    size_t need = 0;
+    int rc = check_attn(F, T, H, Dk, Dv, dtype, need);
+    if (rc || (rc = check_attn_sequences(F, S, T, H, Dk, Dv))) return rc;
+    if (!seq_off || !decay || (T > 0 && (!q || !k || !v || !dy || !dq || !dk || !dv)))
+        return fail(MDL_EINVAL, F + ": null tensor");
+    const int64_t nk = (int64_t)H * Dk, nv = (int64_t)H * Dv;
+    if ((rc = check_stride(F, "ldq", T, nk, ldq)) || (rc = check_stride(F, "ldk", T, nk, ldk)) ||
+        (rc = check_stride(F, "ldv", T, nv, ldv)) || (rc = check_stride(F, "lddy", T, nv, lddy)) ||
+        (rc = check_stride(F, "lddq", T, nk, lddq)) || (rc = check_stride(F, "lddk", T, nk, lddk)) ||
+        (rc = check_stride(F, "lddv", T, nv, lddv)))
+        return rc;
+    if ((rc = check_ws(F, "mdl_linattn_workspace_size", need, ws, ws_bytes))) return rc;
+    if (T > 0 && (rc = check_apart(F, {dq, dk, dv}, {q, k, v, dy}))) return rc;
+    if (share_bytes(h0, dh0, state_bytes(S, H, Dk, Dv)) || share_bytes(dhT, dh0, state_bytes(S, H, Dk, Dv)))
+        return fail(MDL_EINVAL, F + ": dh0 over h0 or dhT");
+    mdl::AttnArgs a{};
+    a.off = seq_off;
+    a.S = S;
+    a.H = H;
+    a.Dk = Dk;
+    a.Dv = Dv;
+    a.reverse = reverse != 0;
+    a.T = T;
+    a.decay = decay;
+    a.scale = scale;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.dy = dy;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.lddy = lddy;
+    a.h0 = h0;
+    a.dhT = dhT;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.lddq = lddq;
+    a.lddk = lddk;
+    a.lddv = lddv;
+    a.dh0 = dh0;
+    hipError_t e;
+    {
+        Timed t("attn_bwd");
+        e = mdl::launch_attn_bwd(a, dtype, ws, static_cast<hipStream_t>(stream));
+    }
+    if (e != hipSuccess) return hip_fail(e, F);
+    return MDL_OK;
+    GUARD_END
+}
+
+int mdl_linattn_step(int32_t S, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype, const float* decay, float scale,
+                     const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                     const int32_t* slots, int32_t n_slots, const float* h_in, float* h_out, void* y, int64_t ldy,
+                     void* stream) {
+    GUARD_BEGIN
+    const std::string F("mdl_linattn_step");
+    size_t need = 0;
+    int rc = check_attn(F, 0, H, Dk, Dv, dtype, need);
+    if (rc) return rc;
+    if (S < 1 || n_slots < 1) return fail(MDL_EINVAL, F + ": need S and n_slots >= 1");
+    if (!decay || !q || !k || !v || !h_in || !h_out || !y) return fail(MDL_EINVAL, F + ": null tensor");
+    if ((int64_t)S * H > mdl::kMaxLaunchThreads / 256) return fail(MDL_EOVERFLOW, F + ": the launch exceeds 2^31 threads");
+    if (!slots && n_slots < S) return fail(MDL_EINVAL, F + ": n_slots below S without slots");
+    const int64_t nk = (int64_t)H * Dk, nv = (int64_t)H * Dv;
+    if ((rc = check_stride(F, "ldq", S, nk, ldq)) || (rc = check_stride(F, "ldk", S, nk, ldk)) ||
+        (rc = check_stride(F, "ldv", S, nv, ldv)) || (rc = check_stride(F, "ldy", S, nv, ldy)))
+        return rc;
+    if ((rc = check_apart(F, {y}, {q, k, v}))) return rc;
+    mdl::AttnArgs a{};
+    a.S = S;
+    a.H = H;
+    a.Dk = Dk;
+    a.Dv = Dv;
+    a.decay = decay;
+    a.scale = scale;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.y = y;
+    a.ldy = ldy;
+    hipError_t e;
+    {
+        Timed t("attn_step");
+        e = mdl::launch_attn_step(a, dtype, slots, n_slots, h_in, h_out, static_cast<hipStream_t>(stream));
+    }
+    if (e != hipSuccess) return hip_fail(e, F);
+    return MDL_OK;
+    GUARD_END
+}
+
+// ---- dropout ---------------------------------------------------------------------------------------------
+int mdl_dropout(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx, const void* r, int64_t ldr, float p,
+                const uint64_t* rng, void* y, int64_t ldy, void* stream) {
+    GUARD_BEGIN
+    const std::string F("mdl_dropout");
+    int rc = check_dtype(F, dtype);
+    if (rc) return rc;
+    if (N < 0 || D < 1) return fail(MDL_EINVAL, F + ": need N >= 0 and D >= 1");
+    if (!(p >= 0.f && p < 1.f)) return fail(MDL_EINVAL, F + ": p must lie in [0, 1)");
+    const int cut = (int)std::lrint((double)p * 65536.0);
+    if (cut > 65535) return fail(MDL_EINVAL, F + ": p rounds to 1 in steps of 2^-16");
+    if (!rng || (N > 0 && (!x || !y))) return fail(MDL_EINVAL, F + ": null tensor");
+    if (reinterpret_cast<uintptr_t>(rng) % 8) return fail(MDL_EINVAL, F + ": rng not 8-byte aligned");
+    if ((rc = check_stride(F, "ldx", N, D, ldx)) || (rc = check_stride(F, "ldy", N, D, ldy))) return rc;
+    if (r && (rc = check_stride(F, "ldr", N, D, ldr))) return rc;
+    if (N > mdl::dropout_max_groups() / (((int64_t)D + 7) / 8))
+        return fail(MDL_EOVERFLOW, F + ": the launch exceeds 2^31 threads");
+    hipError_t e;
+    {
+        Timed t("dropout");
+        e = mdl::launch_dropout(N, D, dtype, x, ldx, r, ldr, cut, rng, y, ldy, static_cast<hipStream_t>(stream));
+    }
+    if (e != hipSuccess) return hip_fail(e, F);
+    return MDL_OK;
+    GUARD_END
+}
+
 int mdl_set_scan_wait(int32_t on) {
     if (on < 0 || on > 1) return fail(MDL_EINVAL, "mdl_set_scan_wait: on must be 0 or 1");
     g_scan_wait.store(on != 0);

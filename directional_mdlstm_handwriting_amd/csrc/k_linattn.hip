@@ -1,0 +1,742 @@
+// k_linattn.hip — linear attention with a decay for each head over packed sequences, gfx950.
+//
+// Per head, with d its decay, and R the state [Da][Dc] (float32):
+//     R_t = b_t c_t^T + d R_{t-1},   out_t = a_t^T R_t
+// The forward is (a, b, c) = (q, k, v). All gradients are the same recurrence again: dq is (dy, v, k) in the forward's
+// order, on the transposed states; dv is (k, q, dy) and dk is (v, dy, q), both against the forward's order, on one state
+// (the gradient of the forward's) and its transpose. In blocks of C tokens i, j = 0.. after an entering state E:
+//     out_i = sum_{j <= i} d^{i-j} (a_i . b_j) c_j + d^{i+1} a_i^T E,   E' = d^n E + sum_j d^{n-1-j} b_j c_j^T
+// (one power less on E and one more on E' where the entering state is that of the token itself: the gradients).
+//
+// Tokens are tiled evenly in tiles of L, whatever the sequences; a piece is what a tile holds of a sequence. Three
+// launches: `states` forms what each piece adds to the state (written for a piece whose sequence goes on past its tile to
+// the slot of that boundary, for one that ends in it to the last states), `chain` walks each sequence's boundaries and
+// leaves in each slot the state that enters the next tile, `outputs` walks the pieces block by block. No tile waits for
+// another. The slots of the forward stand in the workspace for the backward's dq.
+#include "kernels.h"
+#include "seqio.h"
+
+#include <algorithm>
+
+namespace mdl {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+typedef __bf16 bh8 __attribute__((ext_vector_type(8)));
+typedef short h4 __attribute__((ext_vector_type(4)));
+
+// ---- operands of the matrix instructions ------------------------------------------------------------------------
+// A Quad holds four values of one row of a 16 x 16 tile, at the columns 4 g + 0..3 of lane group g = lane / 16 for row
+// lane % 16: the layout in which the 16 x 16 forms also leave their results (with rows and columns exchanged), so that a
+// result tile is an operand of the next product as it lies. mma2 multiplies over two tiles' depth.
+template <typename T>
+struct Op;
+template <>
+struct Op<bf16> {
+    typedef uint16_t lds_t;
+    typedef u32x2 Quad;
+    static constexpr int C = 64;  // tokens a block
+    static __device__ inline Quad make(f32x4 v) { return Quad{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}; }
+    static __device__ inline f32x4 values(Quad q) {
+        return f32x4{__uint_as_float(q[0] << 16), __uint_as_float(q[0] & 0xffff0000u), __uint_as_float(q[1] << 16),
+                     __uint_as_float(q[1] & 0xffff0000u)};
+    }
+    // out[m][n] += sum over the two tiles' depth of x[m][.] y[n][.]
+    static __device__ inline f32x4 mma2(f32x4 c, Quad x0, Quad x1, Quad y0, Quad y1) {
+        const u32x4 x = {x0[0], x0[1], x1[0], x1[1]}, y = {y0[0], y0[1], y1[0], y1[1]};
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bh8, x), __builtin_bit_cast(bh8, y), c, 0, 0, 0);
+    }
+    // row `row` of an LDS tile, columns col0 + 4 g ..
+    static __device__ inline Quad row(const lds_t* t, int stride, int row, int col0, int g) {
+        return *reinterpret_cast<const Quad*>(t + row * stride + col0 + 4 * g);
+    }
+    // column col0 + lane % 16 of an LDS tile, rows row0 + 4 g ..: a transposing read, in which each group of 16 lanes
+    // names 4 rows of 16 values
+    static __device__ inline Quad col(const lds_t* t, int stride, int row0, int col0, int g, int i) {
+        typedef __attribute__((address_space(3))) h4* P;
+        const lds_t* p = t + (row0 + 4 * g + (i >> 2)) * stride + col0 + 4 * (i & 3);
+        return __builtin_bit_cast(Quad, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p)));
+    }
+};
+template <>
+struct Op<float> {
+    typedef float lds_t;
+    typedef f32x4 Quad;
+    static constexpr int C = 32;
+    static __device__ inline Quad make(f32x4 v) { return v; }
+    static __device__ inline f32x4 values(Quad q) { return q; }
+    static __device__ inline f32x4 mma2(f32x4 c, Quad x0, Quad x1, Quad y0, Quad y1) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x0[r], y0[r], c, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x1[r], y1[r], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ inline Quad row(const lds_t* t, int stride, int row, int col0, int g) {
+        return *reinterpret_cast<const Quad*>(t + row * stride + col0 + 4 * g);
+    }
+    static __device__ inline Quad col(const lds_t* t, int stride, int row0, int col0, int g, int i) {
+        const lds_t* p = t + (row0 + 4 * g) * stride + col0 + i;
+        return Quad{p[0], p[stride], p[2 * stride], p[3 * stride]};
+    }
+};
+
+// log2 d in double: near 1 the fp32 instruction's result is good to its last bit only in absolute terms
+__device__ inline float log2_of(float d) { return (float)log2((double)d); }
+// d^e for whole e >= 0, from log2 d: d^0 is 1 also for d = 0
+__device__ inline float power(float l2, int e) { return e == 0 ? 1.f : __builtin_amdgcn_exp2f((float)e * l2); }
+
+// ---- pieces -----------------------------------------------------------------------------------------------------
+// The first of the S sequences whose end lies beyond t (S if none), 64 probes at a time, alike in every wave.
+__device__ inline int first_past(const int64_t* off, int S, int64_t t) {
+    int lo = 0, hi = S;
+    const int lane = threadIdx.x & 63;
+    while (lo < hi) {
+        const int step = (int)(((int64_t)(hi - lo) + 63) / 64);
+        const int64_t p = lo + (int64_t)lane * step;
+        const uint64_t m = __ballot(p < hi && off[p + 1] > t);
+        if (m == 0) {
+            lo += ((hi - lo - 1) / step) * step + 1;
+        } else {
+            const int f = __builtin_ctzll(m);
+            hi = lo + f * step;
+            if (f > 0) lo += (f - 1) * step + 1;
+        }
+    }
+    return lo;
+}
+
+// What a kernel of this file works on.
+struct Args {
+    const int64_t* off;
+    int S, H;
+    int64_t T;
+    int L;                     // tokens a tile
+    int64_t ntiles;
+    int dir;                   // +1: tokens ascending, -1: descending
+    int post;                  // 1: the entering state is the previous token's; 0: it is the token's own
+    const void *a, *b, *c;     // [T][H][da or dc] at row strides
+    int64_t lda, ldb, ldc;
+    int da, dc, trans;         // states are stored [da][dc], or [dc][da]
+    const float* decay;
+    float pscale, sscale, oscale;  // of a . b, of b c^T in the state, of the output
+    float* slots;              // [ntiles - 1][H][da][dc], a tile boundary's state
+    const float* init;         // [S][H][da][dc] or null
+    float* last;               // [S][H][da][dc] or null
+    void* out;                 // [T][H][dc]
+    int64_t ldo;
+};
+
+struct Piece {
+    int64_t begin, end;        // tokens
+    bool enters, leaves;       // in scan order: the sequence began, goes on in another tile
+};
+// offsets that leave [0, T] end there: a sequence enters or leaves a tile only where there is a tile to go to
+__device__ inline int64_t offset(const Args& a, int64_t s) {
+    const int64_t o = a.off[s];
+    return o < 0 ? 0 : (o > a.T ? a.T : o);
+}
+__device__ inline bool piece_of(const Args& a, int s, int64_t t0, int64_t t1, Piece& p) {
+    const int64_t o0 = offset(a, s), o1 = offset(a, (int64_t)s + 1);
+    p.begin = o0 > t0 ? o0 : t0;
+    p.end = o1 < t1 ? o1 : t1;
+    const bool before = o0 < t0, after = o1 > t1;
+    p.enters = a.dir > 0 ? before : after;
+    p.leaves = a.dir > 0 ? after : before;
+    return p.begin < p.end;
+}
+
+// ---- blocks of rows ---------------------------------------------------------------------------------------------
+// n rows of d elements from `first` on in scan order, staged in registers and then laid as an LDS tile of C x D, zero
+// outside: what lies behind a sequence or beside a head never meets a product.
+template <typename T, int D>
+struct Rows {
+    static constexpr int V = Width<T>::v, per = D / V, C = Op<T>::C, n_vec = C * per / kThreads;
+    static constexpr int stride = D + 16 / sizeof(T);
+    static_assert(n_vec >= 1 && C * per % kThreads == 0, "whole vectors a thread");
+    u32x4 q[n_vec];
+    __device__ inline void load(const T* base, int64_t ld, int64_t first, int dir, int n, int d) {
+#pragma unroll
+        for (int i = 0; i < n_vec; ++i) {
+            const int v = i * kThreads + threadIdx.x, r = v / per, c = v % per * V;
+            q[i] = u32x4{0, 0, 0, 0};
+            if (r < n && c < d) {
+                const T* p = base + (first + (int64_t)dir * r) * ld + c;
+                if (c + V <= d) {
+                    q[i] = *reinterpret_cast<const u32x4_e*>(p);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        if (c + e >= d) continue;
+                        if constexpr (sizeof(T) == 2) q[i][e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
+                        else q[i][e] = reinterpret_cast<const uint32_t*>(p)[e];
+                    }
+                }
+            }
+        }
+    }
+    __device__ inline void lay(typename Op<T>::lds_t* t) const {
+#pragma unroll
+        for (int i = 0; i < n_vec; ++i) {
+            const int v = i * kThreads + threadIdx.x, r = v / per, c = v % per * V;
+            *reinterpret_cast<u32x4*>(t + r * stride + c) = q[i];
+        }
+    }
+};
+
+// ---- states -----------------------------------------------------------------------------------------------------
+// A wave holds DC / 4 columns of the state: result tiles of 16 x 16, rows 16 t + 4 g + r, column lane % 16.
+template <int DA, int DC>
+struct State {
+    static constexpr int NT = DC / 64, AT = DA / 16;
+    f32x4 x[AT][NT];
+    __device__ inline void clear() {
+#pragma unroll
+        for (int t = 0; t < AT; ++t)
+#pragma unroll
+            for (int u = 0; u < NT; ++u) x[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    __device__ inline void scale(float f) {
+#pragma unroll
+        for (int t = 0; t < AT; ++t)
+#pragma unroll
+            for (int u = 0; u < NT; ++u) x[t][u] *= f;
+    }
+    // f(value, element of the stored state) returns the value to keep
+    template <typename F>
+    __device__ inline void each(const Args& a, F f) {
+        const int lane = threadIdx.x & 63, g = lane >> 4, n0 = (threadIdx.x >> 6) * (DC / 4) + (lane & 15);
+#pragma unroll
+        for (int t = 0; t < AT; ++t)
+#pragma unroll
+            for (int u = 0; u < NT; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int m = 16 * t + 4 * g + r, n = n0 + 16 * u;
+                    if (m < a.da && n < a.dc) x[t][u][r] = f(x[t][u][r], a.trans ? n * a.da + m : m * a.dc + n);
+                }
+    }
+    __device__ inline void load(const Args& a, const float* p) {
+        clear();
+        each(a, [&](float, int e) { return p[e]; });
+    }
+    __device__ inline void store(const Args& a, float* p) {
+        each(a, [&](float v, int e) { return p[e] = v; });
+    }
+};
+
+// x += sum over the block's rows j of b_j w_j c_j^T; PARTS: how many bfloat16 terms w c is taken as (one for fp32)
+template <typename T, int DA, int DC, int PARTS>
+__device__ inline void add_block(State<DA, DC>& s, const typename Op<T>::lds_t* B, const typename Op<T>::lds_t* Cv,
+                                 float l2, float scale, int n, int post) {
+    typedef Op<T> O;
+    constexpr int JT = O::C / 16;
+    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15, n0 = (threadIdx.x >> 6) * (DC / 4);
+    constexpr int sb = Rows<T, DA>::stride, sc = Rows<T, DC>::stride;
+    typename O::Quad w[PARTS][JT][State<DA, DC>::NT];
+#pragma unroll
+    for (int t = 0; t < JT; ++t) {
+        f32x4 f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) f[r] = scale * power(l2, max(n - post - (16 * t + 4 * g + r), 0));
+#pragma unroll
+        for (int u = 0; u < State<DA, DC>::NT; ++u) {
+            f32x4 v = O::values(O::col(Cv, sc, 16 * t, n0 + 16 * u, g, i)) * f;
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+                w[p][t][u] = O::make(v);
+                v -= O::values(w[p][t][u]);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < State<DA, DC>::AT; ++m) {
+#pragma unroll
+        for (int t = 0; t < JT; t += 2) {
+            const auto b0 = O::col(B, sb, 16 * t, 16 * m, g, i), b1 = O::col(B, sb, 16 * t + 16, 16 * m, g, i);
+#pragma unroll
+            for (int u = 0; u < State<DA, DC>::NT; ++u)
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) s.x[m][u] = O::mma2(s.x[m][u], b0, b1, w[p][t][u], w[p][t + 1][u]);
+        }
+    }
+}
+
+// What each piece adds to its sequence's state. bfloat16: w c is split into three terms (24 bits, as fp32 has), so that
+// the states are sums of fp32 products.
+template <typename T, int DA, int DC>
+__global__ __launch_bounds__(kThreads, 2) void states(const Args a) {
+    typedef Op<T> O;
+    constexpr int C = O::C, PARTS = sizeof(T) == 2 ? 3 : 1;
+    __shared__ alignas(16) typename O::lds_t lb[C * Rows<T, DA>::stride], lc[C * Rows<T, DC>::stride];
+    const int64_t tile = blockIdx.x, t0 = tile * a.L, t1 = t0 + a.L < a.T ? t0 + a.L : a.T;
+    const int h = blockIdx.y;
+    const float l2 = log2_of(a.decay[h]);
+    const T* pb = static_cast<const T*>(a.b) + (int64_t)h * a.da;
+    const T* pc = static_cast<const T*>(a.c) + (int64_t)h * a.dc;
+    const int64_t size = (int64_t)a.da * a.dc;
+    for (int s = first_past(a.off, a.S, t0); s < a.S; ++s) {
+        if (a.off[s] >= t1) break;
+        Piece p;
+        if (!piece_of(a, s, t0, t1, p)) continue;
+        if (!p.leaves && !a.last) continue;
+        State<DA, DC> x;
+        x.clear();
+        const int64_t len = p.end - p.begin;
+        const int64_t from = a.dir > 0 ? p.begin : p.end - 1;
+        Rows<T, DA> rb;
+        Rows<T, DC> rc;
+        rb.load(pb, a.ldb, from, a.dir, (int)min((int64_t)C, len), a.da);
+        rc.load(pc, a.ldc, from, a.dir, (int)min((int64_t)C, len), a.dc);
+        for (int64_t k = 0; k < len; k += C) {
+            const int n = (int)min((int64_t)C, len - k);
+            __syncthreads();
+            rb.lay(lb);
+            rc.lay(lc);
+            if (k + C < len) {
+                rb.load(pb, a.ldb, from + a.dir * (k + C), a.dir, (int)min((int64_t)C, len - k - C), a.da);
+                rc.load(pc, a.ldc, from + a.dir * (k + C), a.dir, (int)min((int64_t)C, len - k - C), a.dc);
+            }
+            __syncthreads();
+            if (k > 0) x.scale(power(l2, n));
+            add_block<T, DA, DC, PARTS>(x, lb, lc, l2, a.sscale, n, a.post);
+        }
+        const int64_t slot = a.dir > 0 ? tile : tile - 1;
+        float* to = p.leaves ? a.slots + (slot * a.H + h) * size : a.last + ((int64_t)s * a.H + h) * size;
+        x.store(a, to);
+    }
+}
+
+// Per sequence, head and four state elements: the boundaries in scan order.
+__global__ __launch_bounds__(kThreads) void chain(const Args a, int blocks_per_head) {
+    const int64_t id = blockIdx.x;
+    const int eb = (int)(id % blocks_per_head), h = (int)(id / blocks_per_head % a.H);
+    const int64_t s = id / blocks_per_head / a.H, size = (int64_t)a.da * a.dc;
+    const int64_t e = (int64_t)eb * kThreads + threadIdx.x;
+    if (e >= size) return;
+    const int64_t o0 = offset(a, s), o1 = offset(a, s + 1);
+    const int64_t at = (s * a.H + h) * size + e;
+    float x = a.init ? a.init[at] : 0.f;
+    if (o0 >= o1) {
+        if (a.last) a.last[at] = x;
+        return;
+    }
+    const int64_t first = o0 / a.L, end = (o1 - 1) / a.L;
+    const float l2 = log2_of(a.decay[h]);
+    for (int64_t i = first; i < end; ++i) {
+        const int64_t t = a.dir > 0 ? i : end - (i - first);     // the tile that is left
+        const int64_t lo = max(o0, t * a.L), hi = min(o1, t * a.L + a.L);
+        float* p = a.slots + ((a.dir > 0 ? t : t - 1) * a.H + h) * size + e;
+        x = __builtin_fmaf(x, power(l2, (int)(hi - lo)), *p);
+        *p = x;
+    }
+    if (a.last) {
+        const int64_t t = a.dir > 0 ? end : first;
+        const int64_t lo = max(o0, t * a.L), hi = min(o1, t * a.L + a.L);
+        a.last[at] = __builtin_fmaf(x, power(l2, (int)(hi - lo)), a.last[at]);
+    }
+}
+
+template <typename T>
+__device__ inline void store_quad(T* p, f32x4 v, int n) {
+    if constexpr (sizeof(T) == 2) {
+        typedef u32x2 u32x2_e __attribute__((aligned(2), may_alias));
+        const u32x2 q = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        if (n >= 4) *reinterpret_cast<u32x2_e*>(p) = q;
+        else
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (r < n) p[r].u = (uint16_t)(q[r >> 1] >> (16 * (r & 1)));
+    } else {
+        if (n >= 4) *reinterpret_cast<f32x4_e*>(p) = v;
+        else
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (r < n) p[r] = v[r];
+    }
+}
+
+// The pieces' outputs, block by block. bfloat16 roundings on the way: of (a . b) d^{i-j} before its product with c, of the
+// entering state before its product with a, and of w c before it is added to the state that is handed on within the tile
+// (two terms there); each is half a step of values that reach the output as a sum with its own half step. Sums and states
+// are fp32.
+template <typename T, int DA, int DC>
+__global__ __launch_bounds__(kThreads, 2) void outputs(const Args a) {
+    typedef Op<T> O;
+    typedef typename O::Quad Quad;
+    constexpr int C = O::C, CT = C / 16, PARTS = sizeof(T) == 2 ? 2 : 1, NT = DC / 64;
+    constexpr int sa = Rows<T, DA>::stride, sc = Rows<T, DC>::stride, sp = C + 16 / (int)sizeof(T);
+    extern __shared__ u32x4 smem[];
+    typename O::lds_t* la = reinterpret_cast<typename O::lds_t*>(smem);
+    typename O::lds_t *lb = la + C * sa, *lc = lb + C * sa, *lp = lc + C * sc;
+    const int64_t tile = blockIdx.x, t0 = tile * a.L, t1 = t0 + a.L < a.T ? t0 + a.L : a.T;
+    const int h = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+    const float l2 = log2_of(a.decay[h]);
+    const T* pa = static_cast<const T*>(a.a) + (int64_t)h * a.da;
+    const T* pb = static_cast<const T*>(a.b) + (int64_t)h * a.da;
+    const T* pc = static_cast<const T*>(a.c) + (int64_t)h * a.dc;
+    T* po = static_cast<T*>(a.out) + (int64_t)h * a.dc;
+    const int64_t size = (int64_t)a.da * a.dc;
+    for (int s = first_past(a.off, a.S, t0); s < a.S; ++s) {
+        if (a.off[s] >= t1) break;
+        Piece p;
+        if (!piece_of(a, s, t0, t1, p)) continue;
+        const int64_t len = p.end - p.begin, from = a.dir > 0 ? p.begin : p.end - 1;
+        Rows<T, DA> ra, rb;
+        Rows<T, DC> rc;
+        const int n0 = (int)min((int64_t)C, len);
+        ra.load(pa, a.lda, from, a.dir, n0, a.da);
+        rb.load(pb, a.ldb, from, a.dir, n0, a.da);
+        rc.load(pc, a.ldc, from, a.dir, n0, a.dc);
+        State<DA, DC> x;
+        bool zero = false;
+        if (p.enters) x.load(a, a.slots + ((a.dir > 0 ? tile - 1 : tile) * a.H + h) * size);
+        else if (a.init) x.load(a, a.init + ((int64_t)s * a.H + h) * size);
+        else {
+            x.clear();
+            zero = true;
+        }
+        for (int64_t k = 0; k < len; k += C) {
+            const int n = (int)min((int64_t)C, len - k);
+            __syncthreads();
+            ra.lay(la);
+            rb.lay(lb);
+            rc.lay(lc);
+            if (k + C < len) {
+                const int nn = (int)min((int64_t)C, len - k - C);
+                const int64_t f = from + a.dir * (k + C);
+                ra.load(pa, a.lda, f, a.dir, nn, a.da);
+                rb.load(pb, a.ldb, f, a.dir, nn, a.da);
+                rc.load(pc, a.ldc, f, a.dir, nn, a.dc);
+            }
+            __syncthreads();
+            // (a_i . b_j) d^{i-j}: tiles of 16 x 16 dealt out to the waves, row i at lane % 16, j at 4 g + r
+            for (int t = wave; t < CT * CT; t += 4) {
+                const int it = t / CT, jt = t % CT;
+                if (jt > it) continue;
+                f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int m = 0; m < DA; m += 32)
+                    v = O::mma2(v, O::row(lb, sa, 16 * jt + i, m, g), O::row(lb, sa, 16 * jt + i, m + 16, g),
+                                O::row(la, sa, 16 * it + i, m, g), O::row(la, sa, 16 * it + i, m + 16, g));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int e = 16 * (it - jt) + i - (4 * g + r);
+                    v[r] = e < 0 ? 0.f : v[r] * (a.pscale * power(l2, e));
+                }
+                *reinterpret_cast<Quad*>(lp + (16 * it + i) * sp + 16 * jt + 4 * g) = O::make(v);
+            }
+            __syncthreads();
+            // outputs: row i at lane % 16, columns 4 g + r of the wave's tiles
+            f32x4 o[CT][NT];
+#pragma unroll
+            for (int it = 0; it < CT; ++it)
+#pragma unroll
+                for (int u = 0; u < NT; ++u) o[it][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (k > 0 || !zero) {
+#pragma unroll
+                for (int m = 0; m < DA / 16; m += 2) {
+                    Quad x0[NT], x1[NT];
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) {
+                        x0[u] = O::make(x.x[m][u]);
+                        x1[u] = O::make(x.x[m + 1][u]);
+                    }
+#pragma unroll
+                    for (int it = 0; it < CT; ++it) {
+                        const Quad a0 = O::row(la, sa, 16 * it + i, 16 * m, g), a1 = O::row(la, sa, 16 * it + i, 16 * m + 16, g);
+#pragma unroll
+                        for (int u = 0; u < NT; ++u) o[it][u] = O::mma2(o[it][u], x0[u], x1[u], a0, a1);
+                    }
+                }
+#pragma unroll
+                for (int it = 0; it < CT; ++it) {
+                    const float f = power(l2, 16 * it + i + a.post);
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) o[it][u] *= f;
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < CT; t += 2) {
+                Quad c0[NT], c1[NT];
+#pragma unroll
+                for (int u = 0; u < NT; ++u) {
+                    const int n = wave * (DC / 4) + 16 * u;
+                    c0[u] = O::col(lc, sc, 16 * t, n, g, i);
+                    c1[u] = O::col(lc, sc, 16 * t + 16, n, g, i);
+                }
+#pragma unroll
+                for (int it = 0; it < CT; ++it) {
+                    if (it < t) continue;
+                    const Quad p0 = O::row(lp, sp, 16 * it + i, 16 * t, g);
+                    // the tile past the diagonal is never written
+                    const Quad p1 = it > t ? O::row(lp, sp, 16 * it + i, 16 * t + 16, g) : O::make(f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) o[it][u] = O::mma2(o[it][u], c0[u], c1[u], p0, p1);
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < CT; ++it) {
+                const int row = 16 * it + i;
+                if (row >= n) continue;
+                T* q = po + (from + (int64_t)a.dir * (k + row)) * a.ldo;
+#pragma unroll
+                for (int u = 0; u < NT; ++u) {
+                    const int col = wave * (DC / 4) + 16 * u + 4 * g;
+                    if (col < a.dc) store_quad<T>(q + col, o[it][u] * a.oscale, a.dc - col);
+                }
+            }
+            if (k + C < len) {
+                x.scale(power(l2, n));
+                add_block<T, DA, DC, PARTS>(x, lb, lc, l2, a.sscale, n, a.post);
+            }
+        }
+    }
+}
+
+template <typename T, int DA, int DC>
+constexpr size_t outputs_lds() {
+    constexpr int C = Op<T>::C;
+    return sizeof(T) * (2 * C * Rows<T, DA>::stride + C * Rows<T, DC>::stride + C * (C + 16 / sizeof(T)));
+}
+
+template <typename T, int DA, int DC>
+hipError_t go(const Args& a, int what, hipStream_t st) {
+    const dim3 grid((uint32_t)a.ntiles, (uint32_t)a.H);
+    if (what == 0) {
+        launch(states<T, DA, DC>, grid, dim3(kThreads), 0, st, a);
+    } else {
+        constexpr size_t lds = outputs_lds<T, DA, DC>();
+        if (lds > 65536) {
+            const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(outputs<T, DA, DC>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+            if (e != hipSuccess) return e;
+        }
+        launch(outputs<T, DA, DC>, grid, dim3(kThreads), lds, st, a);
+    }
+    return hipGetLastError();
+}
+template <typename T>
+hipError_t go_sizes(const Args& a, int what, hipStream_t st) {
+    if (a.da <= 64) return a.dc <= 64 ? go<T, 64, 64>(a, what, st) : go<T, 64, 128>(a, what, st);
+    return a.dc <= 64 ? go<T, 128, 64>(a, what, st) : go<T, 128, 128>(a, what, st);
+}
+hipError_t go_any(const Args& a, int dtype, int what, hipStream_t st) {
+    return dtype == 1 ? go_sizes<bf16>(a, what, st) : go_sizes<float>(a, what, st);
+}
+
+hipError_t go_chain(const Args& a, hipStream_t st) {
+    const int per = (int)(((int64_t)a.da * a.dc + kThreads - 1) / kThreads);
+    launch(chain, dim3((uint32_t)((int64_t)a.S * a.H * per)), dim3(kThreads), 0, st, a, per);
+    return hipGetLastError();
+}
+
+// ---- one token of each stream -----------------------------------------------------------------------------------
+// A workgroup takes one row's head: lanes along the state's columns (V of them a lane), the rows dealt out to the lane
+// groups, each row read, advanced, written and taken into y. Bound by the state's bytes.
+struct StepArgs {
+    int S, H, Dk, Dv, n_slots;
+    const float* decay;
+    float scale;
+    const void *q, *k, *v;
+    int64_t ldq, ldk, ldv, ldy;
+    const int32_t* slots;
+    const float* h_in;
+    float* h_out;
+    void* y;
+};
+template <typename T, int V>
+__global__ __launch_bounds__(kThreads) void step(const StepArgs a) {
+    constexpr int kMaxD = 128, LC = V == 4 ? 32 : 128, G = kThreads / LC, RU = 8;  // lanes a row, row groups, rows at once
+    __shared__ float lq[kMaxD], lk[kMaxD], lv[kMaxD], ly[G][LC * V + 4];
+    const int h = blockIdx.x % a.H, row = blockIdx.x / a.H;
+    const int slot = a.slots ? a.slots[row] : row;
+    if (slot < 0 || slot >= a.n_slots) return;
+    const int64_t at = ((int64_t)slot * a.H + h) * a.Dk * a.Dv;
+    const float* in = a.h_in + at;
+    float* out = a.h_out + at;
+    const int t = threadIdx.x, col = t % LC * V, grp = t / LC;
+    const auto value = [&](const void* p, int64_t ld, int d, int i) {
+        return load_raw<1>(static_cast<const T*>(p) + row * ld + (int64_t)h * d + i)[0];
+    };
+    if (t < a.Dk) lq[t] = value(a.q, a.ldq, a.Dk, t);
+    if (t >= kMaxD && t - kMaxD < a.Dk) lk[t - kMaxD] = value(a.k, a.ldk, a.Dk, t - kMaxD);
+    if (t < a.Dv) lv[t] = value(a.v, a.ldv, a.Dv, t);
+    const float d = a.decay[h];
+    float y[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) y[j] = 0.f;
+    const bool live = col < a.Dv;
+    for (int m0 = 0; m0 < a.Dk; m0 += RU * G) {
+        float x[RU][V];
+#pragma unroll
+        for (int u = 0; u < RU; ++u) {
+            const int m = m0 + u * G + grp;
+            if (live && m < a.Dk) load_f32<V>(in + m * a.Dv + col, x[u]);
+        }
+        if (m0 == 0) __syncthreads();
+#pragma unroll
+        for (int u = 0; u < RU; ++u) {
+            const int m = m0 + u * G + grp;
+            if (!live || m >= a.Dk) continue;
+            const float k = lk[m], q = lq[m];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                x[u][j] = __builtin_fmaf(k, lv[col + j], d * x[u][j]);
+                y[j] = __builtin_fmaf(q, x[u][j], y[j]);
+            }
+            store_f32<V>(out + m * a.Dv + col, x[u]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) ly[grp][col + j] = y[j];
+    __syncthreads();
+    if (t < a.Dv) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < G; ++i) sum += ly[i][t];
+        const float one[1] = {sum * a.scale};
+        store_vec<1>(static_cast<T*>(a.y) + row * a.ldy + (int64_t)h * a.Dv + t, one);
+    }
+}
+
+}  // namespace
+
+int linattn_max_d() { return 128; }
+
+// Tiles: long enough that the slots (a state a tile and head) stay few beside the tokens, short enough that there are
+// some workgroups a compute unit.
+AttnPlan attn_plan(int64_t T, int H, int Dk, int Dv) {
+    AttnPlan p;
+    int L = 256;
+    while (L < 2048 && T / (2 * L) * H >= 1024) L *= 2;
+    p.L = L;
+    p.ntiles = (T + L - 1) / L;
+    const int64_t state = (int64_t)H * Dk * Dv;
+    p.slots = (size_t)std::max<int64_t>(p.ntiles - 1, 0) * (size_t)state;
+    p.total = 2 * ((p.slots * sizeof(float) + 15) / 16 * 16);
+    p.chain_blocks = (int64_t)H * ((Dk * (int64_t)Dv + kThreads - 1) / kThreads);
+    return p;
+}
+
+namespace {
+Args args_of(const AttnArgs& x, const AttnPlan& p) {
+    Args a{};
+    a.off = x.off;
+    a.S = x.S;
+    a.H = x.H;
+    a.T = x.T;
+    a.L = p.L;
+    a.ntiles = p.ntiles;
+    a.decay = x.decay;
+    return a;
+}
+}  // namespace
+
+hipError_t launch_attn_fwd(const AttnArgs& x, int dtype, void* ws, hipStream_t st) {
+    const AttnPlan p = attn_plan(x.T, x.H, x.Dk, x.Dv);
+    Args a = args_of(x, p);
+    a.dir = x.reverse ? -1 : 1;
+    a.post = 1;
+    a.a = x.q;
+    a.b = x.k;
+    a.c = x.v;
+    a.lda = x.ldq;
+    a.ldb = x.ldk;
+    a.ldc = x.ldv;
+    a.da = x.Dk;
+    a.dc = x.Dv;
+    a.pscale = a.sscale = 1.f;
+    a.oscale = x.scale;
+    a.slots = static_cast<float*>(ws);
+    a.init = x.h0;
+    a.last = x.hT;
+    a.out = x.y;
+    a.ldo = x.ldy;
+    hipError_t e = hipSuccess;
+    if (x.T > 0 && (p.ntiles > 1 || x.hT) && (e = go_any(a, dtype, 0, st)) != hipSuccess) return e;
+    if ((p.ntiles > 1 || x.hT) && (e = go_chain(a, st)) != hipSuccess) return e;
+    return x.T > 0 ? go_any(a, dtype, 1, st) : e;
+}
+
+hipError_t launch_attn_bwd(const AttnArgs& x, int dtype, void* ws, hipStream_t st) {
+    const AttnPlan p = attn_plan(x.T, x.H, x.Dk, x.Dv);
+    float* fwd = static_cast<float*>(ws);
+    float* bwd = reinterpret_cast<float*>(static_cast<char*>(ws) + p.total / 2);
+    // the state's gradient, against the forward's order
+    Args g = args_of(x, p);
+    g.dir = x.reverse ? 1 : -1;
+    g.post = 0;
+    g.b = x.q;
+    g.c = x.dy;
+    g.ldb = x.ldq;
+    g.ldc = x.lddy;
+    g.da = x.Dk;
+    g.dc = x.Dv;
+    g.sscale = x.scale;
+    g.slots = bwd;
+    g.init = x.dhT;
+    g.last = x.dh0;
+    hipError_t e = hipSuccess;
+    if (x.T > 0 && (p.ntiles > 1 || x.dh0) && (e = go_any(g, dtype, 0, st)) != hipSuccess) return e;
+    if ((p.ntiles > 1 || x.dh0) && (e = go_chain(g, st)) != hipSuccess) return e;
+    if (x.T == 0) return e;
+    g.pscale = x.scale;
+    g.oscale = 1.f;
+    g.a = x.k;
+    g.lda = x.ldk;
+    g.out = x.dv;
+    g.ldo = x.lddv;
+    if ((e = go_any(g, dtype, 1, st)) != hipSuccess) return e;
+    g.a = x.v;
+    g.b = x.dy;
+    g.c = x.q;
+    g.lda = x.ldv;
+    g.ldb = x.lddy;
+    g.ldc = x.ldq;
+    g.da = x.Dv;
+    g.dc = x.Dk;
+    g.trans = 1;
+    g.out = x.dk;
+    g.ldo = x.lddk;
+    if ((e = go_any(g, dtype, 1, st)) != hipSuccess) return e;
+    Args f = args_of(x, p);
+    f.dir = x.reverse ? -1 : 1;
+    f.post = 1;
+    f.a = x.dy;
+    f.b = x.v;
+    f.c = x.k;
+    f.lda = x.lddy;
+    f.ldb = x.ldv;
+    f.ldc = x.ldk;
+    f.da = x.Dv;
+    f.dc = x.Dk;
+    f.trans = 1;
+    f.pscale = f.sscale = 1.f;
+    f.oscale = x.scale;
+    f.slots = fwd;
+    f.init = x.h0;
+    f.out = x.dq;
+    f.ldo = x.lddq;
+    return go_any(f, dtype, 1, st);
+}
+
+hipError_t launch_attn_step(const AttnArgs& x, int dtype, const int32_t* slots, int n_slots, const float* h_in,
+                            float* h_out, hipStream_t st) {
+    const StepArgs a{x.S, x.H, x.Dk, x.Dv, n_slots, x.decay, x.scale, x.q, x.k, x.v, x.ldq, x.ldk, x.ldv, x.ldy,
+                     slots, h_in, h_out, x.y};
+    const dim3 grid((uint32_t)((int64_t)x.S * x.H));
+    const bool wide = x.Dv % 4 == 0;
+    if (dtype == 1) {
+        if (wide) launch(step<bf16, 4>, grid, dim3(kThreads), 0, st, a);
+        else launch(step<bf16, 1>, grid, dim3(kThreads), 0, st, a);
+    } else {
+        if (wide) launch(step<float, 4>, grid, dim3(kThreads), 0, st, a);
+        else launch(step<float, 1>, grid, dim3(kThreads), 0, st, a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace mdl

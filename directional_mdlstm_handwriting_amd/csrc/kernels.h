@@ -364,4 +364,35 @@ hipError_t launch_distill(int64_t N, int V, int k, int dtype, const void* z, int
                           const void* t, int t_dtype, const float* w, float tau, float* loss, void* dz, int64_t ldd,
                           hipStream_t st);
 
+// linear attention with a decay for each head over packed sequences (k_linattn.hip)
+struct AttnArgs {
+    const int64_t* off;             // [S + 1] first token of each sequence
+    int S, H, Dk, Dv, reverse;
+    int64_t T;
+    const float* decay;             // [H]
+    float scale;
+    const void *q, *k, *v, *dy;     // [T][H][Dk or Dv] at row strides
+    int64_t ldq, ldk, ldv, ldy, lddy;
+    const float *h0, *dhT;          // [S][H][Dk][Dv] or null
+    void *y, *dq, *dk, *dv;
+    int64_t lddq, lddk, lddv;
+    float *hT, *dh0;                // [S][H][Dk][Dv] or null
+};
+struct AttnPlan {
+    int L = 0;                      // tokens a tile
+    int64_t ntiles = 0, chain_blocks = 0;  // chain_blocks: workgroups a sequence
+    size_t slots = 0, total = 0;    // floats of one direction's tile states; bytes of both
+};
+int linattn_max_d();
+AttnPlan attn_plan(int64_t T, int H, int Dk, int Dv);
+hipError_t launch_attn_fwd(const AttnArgs& a, int dtype, void* ws, hipStream_t st);
+hipError_t launch_attn_bwd(const AttnArgs& a, int dtype, void* ws, hipStream_t st);
+hipError_t launch_attn_step(const AttnArgs& a, int dtype, const int32_t* slots, int n_slots, const float* h_in,
+                            float* h_out, hipStream_t st);
+
+// dropout (k_dropout.hip): groups of eight elements of a row that one launch takes
+int64_t dropout_max_groups();
+hipError_t launch_dropout(int64_t N, int D, int dtype, const void* x, int64_t ldx, const void* r, int64_t ldr, int cut,
+                          const uint64_t* rng, void* y, int64_t ldy, hipStream_t st);
+
 }  // namespace mdl

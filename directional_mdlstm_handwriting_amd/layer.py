@@ -10,7 +10,9 @@ model head (height collapse, shared fully-connected layer, CTC loss) on the
 last level's output. ``SequenceScan`` and ``ScanState`` run the gated linear
 recurrence along the rows or frames of the packed examples, whole sequences
 at once or a token at a time; ``BlockNorm`` the norms around such a block with
-its gate and residual; ``TopKDistill`` the distillation loss of its logits.
+its gate and residual; ``LinearAttention`` and ``AttentionState`` the recurrence
+with a matrix for a state and a decay for each head; ``Dropout`` a block's
+dropout onto the residual; ``TopKDistill`` the distillation loss of its logits.
 """
 
 from __future__ import annotations
@@ -26,7 +28,8 @@ from . import (MDL_BF16, MDL_CELL_LEAKY_LP, MDL_CELL_MDLSTM, MDL_F32, MDL_PACK_A
                mdl_blockconv_backward, mdl_blockconv_forward, mdl_blockconv_workspace_size, mdl_dirsum_unpack, mdl_forward, mdl_forward_dirsum,
                mdl_layout_device_size, mdl_layout_rects, mdl_layout_upload, mdl_pack, mdl_pack_level, mdl_scatter, mdl_workspace_size,
                mdl_ctc_head, mdl_ctc_workspace_size, mdl_scan_backward, mdl_scan_forward, mdl_scan_step, mdl_scan_workspace_size,
-               mdl_blocknorm_backward, mdl_blocknorm_forward, mdl_blocknorm_workspace_size, mdl_distill, _stream)
+               mdl_blocknorm_backward, mdl_blocknorm_forward, mdl_blocknorm_workspace_size, mdl_distill, mdl_dropout,
+               mdl_linattn_backward, mdl_linattn_forward, mdl_linattn_step, mdl_linattn_workspace_size, _stream)
 
 
 def _dev(a, device, dtype=torch.float32):
@@ -379,6 +382,19 @@ class _Buffers:
             return make(shape, dtype=dtype, device=self.device), not torch.cuda.is_current_stream_capturing()
 
 
+def _sequences(seq_off, T: int, device):
+    """(device, offsets on it): S + 1 ascending offsets from the host, checked, or an int64 device tensor as it is."""
+    if isinstance(seq_off, torch.Tensor) and seq_off.is_cuda:
+        if seq_off.dtype != torch.int64 or seq_off.dim() != 1 or seq_off.numel() < 2:
+            raise ValueError("seq_off: need S + 1 int64 offsets")
+        return seq_off.device, seq_off.contiguous()
+    host = np.asarray(seq_off, dtype=np.int64).reshape(-1)
+    if host.size < 2 or host[0] < 0 or host[-1] > T or (np.diff(host) < 0).any():
+        raise ValueError("seq_off: need S + 1 offsets that ascend within [0, T]")
+    device = _device(device)
+    return device, torch.as_tensor(host, device=device)
+
+
 class SequenceScan(_Buffers):
     """The gated linear recurrence (mdl_scan_forward / _backward) over the sequences given by `seq_off` among T rows
     of D channels. seq_off: S + 1 ascending offsets, from the host (checked) or an int64 device tensor (taken as it
@@ -386,17 +402,7 @@ class SequenceScan(_Buffers):
     backward belongs to the forward before it."""
 
     def __init__(self, seq_off, T: int, D: int, x_dtype: str = "f32", reverse: bool = False, device: str = "cuda"):
-        on_device = isinstance(seq_off, torch.Tensor) and seq_off.is_cuda
-        self.device = seq_off.device if on_device else _device(device)
-        if on_device:
-            if seq_off.dtype != torch.int64 or seq_off.dim() != 1 or seq_off.numel() < 2:
-                raise ValueError("seq_off: need S + 1 int64 offsets")
-            self.off = seq_off.contiguous()
-        else:
-            host = np.asarray(seq_off, dtype=np.int64).reshape(-1)
-            if host.size < 2 or host[0] < 0 or host[-1] > T or (np.diff(host) < 0).any():
-                raise ValueError("seq_off: need S + 1 offsets that ascend within [0, T]")
-            self.off = torch.as_tensor(host, device=self.device)
+        self.device, self.off = _sequences(seq_off, T, device)
         self.S, self.T, self.D, self.reverse = int(self.off.numel()) - 1, int(T), int(D), int(bool(reverse))
         self.x_dtype, self.tdt = _x_dtype(x_dtype)
         self.ws_bytes = mdl_scan_workspace_size(self.T, self.D, self.x_dtype)
@@ -445,20 +451,17 @@ class SequenceScan(_Buffers):
         return t
 
 
-class ScanState(_Buffers):
-    """The recurrence's states of n_slots live streams, advanced a token at a time (mdl_scan_step). Holds an output for
-    each of the last `KEPT` numbers of rows that it met, so that calls of other sizes leave a result alone: a result
-    stands until the next call with as many rows. A captured step writes the output that is held for its size, which is
-    then held as long as the object (a server captures few sizes), or else one of the graph's own."""
+class _StepOutputs(_Buffers):
+    """The outputs of a stepped state: one for each of the last `KEPT` numbers of rows that it met, so that calls of other
+    sizes leave a result alone: a result stands until the next call with as many rows. A captured step writes the output
+    that is held for its size, which is then held as long as the object (a server captures few sizes), or else one of the
+    graph's own."""
 
     KEPT = 8
     HELD = -1
 
-    def __init__(self, n_slots: int, D: int, x_dtype: str = "f32", device: str = "cuda"):
-        self.device = _device(device)
-        self.n_slots, self.D = int(n_slots), int(D)
-        self.x_dtype, self.tdt = _x_dtype(x_dtype)
-        self.state = torch.zeros(self.n_slots, self.D, dtype=torch.float32, device=self.device)
+    def _outputs(self, width: int):
+        self._width = width
         # rows: (output, handle of the stream it was made on; HELD where a graph writes it), the oldest first
         self._y = {}
         self._made(self.device)
@@ -471,7 +474,7 @@ class ScanState(_Buffers):
             self._y[S] = y, self.HELD
         elif home != handle:
             # never used on a stream but its own, on which its memory may be handed out again once it is dropped
-            y, keep = self._new(handle, (S, self.D), self.tdt, True)
+            y, keep = self._new(handle, (S, self._width), self.tdt, True)
             if keep:
                 self._y.pop(S, None)
                 self._y[S] = y, handle
@@ -479,6 +482,18 @@ class ScanState(_Buffers):
                 if len(loose) > self.KEPT:
                     del self._y[loose[0]]
         return y
+
+
+class ScanState(_StepOutputs):
+    """The recurrence's states of n_slots live streams, advanced a token at a time (mdl_scan_step). Holds its outputs by
+    their number of rows: a result stands until the next call with as many rows."""
+
+    def __init__(self, n_slots: int, D: int, x_dtype: str = "f32", device: str = "cuda"):
+        self.device = _device(device)
+        self.n_slots, self.D = int(n_slots), int(D)
+        self.x_dtype, self.tdt = _x_dtype(x_dtype)
+        self.state = torch.zeros(self.n_slots, self.D, dtype=torch.float32, device=self.device)
+        self._outputs(self.D)
 
     def step(self, zf, g, zo=None, slots=None, out=None, stream=None):
         """y [S][D] of one token for each row's slot (slots int32 [S], all different; the first S rows if None). The
@@ -578,3 +593,162 @@ class TopKDistill(_Buffers):
         mdl_distill(self.N, self.V, self.k, self.x_dtype, z, ldz, ids, t, _DTYPES[t_dtype][0], w, self.tau, self.loss,
                     dz, self.V, stream)
         return self.loss, dz
+
+
+def _decays(decay, H: int, device) -> torch.Tensor:
+    """[H] float32 on the device: a device tensor as it is, numbers from the host checked."""
+    if isinstance(decay, torch.Tensor) and decay.is_cuda:
+        _full("decay", decay, (H,), torch.float32, device)
+        return decay
+    host = np.asarray(decay, dtype=np.float32).reshape(-1)
+    if host.shape != (H,) or not ((host >= 0) & (host <= 1)).all():
+        raise ValueError(f"decay: need {H} numbers in [0, 1]")
+    return torch.as_tensor(host, device=device)
+
+
+class LinearAttention(_Buffers):
+    """Linear attention with a decay for each head (mdl_linattn_forward / _backward) over the sequences given by `seq_off`
+    among T rows of `heads` heads, keys of Dk and values of Dv channels. seq_off: S + 1 ascending offsets, from the host
+    (checked) or an int64 device tensor (taken as it is); decay: `heads` numbers in [0, 1], or a float32 device tensor
+    (taken as it is); scale: of the outputs, Dk^-1/2 if None. Holds the outputs, the gradients and the workspace: a
+    forward's results stand until the next forward, and a backward belongs to the forward before it."""
+
+    def __init__(self, seq_off, T: int, heads: int, Dk: int, Dv: int, decay, x_dtype: str = "f32",
+                 scale: Optional[float] = None, reverse: bool = False, device: str = "cuda"):
+        self.device, self.off = _sequences(seq_off, T, device)
+        self.S, self.T, self.H, self.Dk, self.Dv = int(self.off.numel()) - 1, int(T), int(heads), int(Dk), int(Dv)
+        self.reverse, self.scale = int(bool(reverse)), float(Dk ** -0.5 if scale is None else scale)
+        self.x_dtype, self.tdt = _x_dtype(x_dtype)
+        self.decay = _decays(decay, self.H, self.device)
+        self.ws_bytes = mdl_linattn_workspace_size(self.T, self.H, self.Dk, self.Dv, self.x_dtype)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        # zeros: rows in no sequence are never written
+        self.y = torch.zeros(self.T, self.H * self.Dv, dtype=self.tdt, device=self.device)
+        self.hT = torch.empty(self.S, self.H, self.Dk, self.Dv, dtype=torch.float32, device=self.device)
+        self.dq = self.dk = self.dv = self.dh0 = None
+        self._made(self.device)
+
+    def _inputs(self, q, k, v, h0):
+        nk, nv = self.H * self.Dk, self.H * self.Dv
+        lds = [_rows(n, t, (self.T, c), self.tdt, self.device) for n, t, c in (("q", q, nk), ("k", k, nk), ("v", v, nv))]
+        _full("h0", h0, self.hT.shape, torch.float32, self.device)
+        return lds
+
+    def forward(self, q, k, v, h0=None, stream=None):
+        """(y, hT): q, k [T][heads * Dk], v [T][heads * Dv] at any row strides, h0 [S][heads][Dk][Dv] float32. Neither the
+        object's own y nor its hT can be an input: the last states of one piece of a long sequence are copied, or another
+        object takes the next piece."""
+        stream = self._launch(stream)
+        ldq, ldk, ldv = self._inputs(q, k, v, h0)
+        mdl_linattn_forward(self.off, self.S, self.T, self.H, self.Dk, self.Dv, self.x_dtype, self.reverse, self.decay,
+                            self.scale, q, ldq, k, ldk, v, ldv, h0, self.y, self.H * self.Dv, self.hT, self.ws,
+                            self.ws_bytes, stream)
+        return self.y, self.hT
+
+    def backward(self, q, k, v, dy, h0=None, dhT=None, stream=None):
+        """(dq, dk, dv, dh0), dh0 None without h0, of the forward() just run on the same inputs."""
+        stream = self._launch(stream)
+        ldq, ldk, ldv = self._inputs(q, k, v, h0)
+        nk, nv = self.H * self.Dk, self.H * self.Dv
+        lddy = _rows("dy", dy, (self.T, nv), self.tdt, self.device)
+        _full("dhT", dhT, self.hT.shape, torch.float32, self.device)
+        dq, dk = self._grad("dq", (self.T, nk), self.tdt, stream), self._grad("dk", (self.T, nk), self.tdt, stream)
+        dv = self._grad("dv", (self.T, nv), self.tdt, stream)
+        dh0 = None if h0 is None else self._grad("dh0", self.hT.shape, torch.float32, stream)
+        mdl_linattn_backward(self.off, self.S, self.T, self.H, self.Dk, self.Dv, self.x_dtype, self.reverse, self.decay,
+                             self.scale, q, ldq, k, ldk, v, ldv, h0, dy, lddy, dhT, dq, nk, dk, nk, dv, nv, dh0, self.ws,
+                             self.ws_bytes, stream)
+        return dq, dk, dv, dh0
+
+    def _grad(self, name, shape, dtype, stream):
+        t = getattr(self, name)
+        if t is None:
+            # zeros: as y, rows in no sequence are never written
+            t, keep = self._new(stream, shape, dtype, name != "dh0")
+            if keep:
+                setattr(self, name, t)
+        return t
+
+
+class AttentionState(_StepOutputs):
+    """The attention's states of n_slots live streams, advanced a token at a time (mdl_linattn_step). Outputs are held as
+    ScanState holds them."""
+
+    def __init__(self, n_slots: int, heads: int, Dk: int, Dv: int, decay, x_dtype: str = "f32",
+                 scale: Optional[float] = None, device: str = "cuda"):
+        self.device = _device(device)
+        self.n_slots, self.H, self.Dk, self.Dv = int(n_slots), int(heads), int(Dk), int(Dv)
+        self.scale = float(Dk ** -0.5 if scale is None else scale)
+        self.x_dtype, self.tdt = _x_dtype(x_dtype)
+        self.decay = _decays(decay, self.H, self.device)
+        self.state = torch.zeros(self.n_slots, self.H, self.Dk, self.Dv, dtype=torch.float32, device=self.device)
+        self._outputs(self.H * self.Dv)
+
+    def step(self, q, k, v, slots=None, out=None, stream=None):
+        """y [S][heads * Dv] of one token for each row's slot (slots int32 [S], all different; the first S rows if None).
+        The states advance in place, or into the same rows of `out` ([n_slots][heads][Dk][Dv]). A row whose slot is no
+        slot (-1 in a padded batch) is left out, and its y means nothing."""
+        current = stream is None
+        stream = self._launch(stream)
+        S = int(q.shape[0])
+        ldq = _rows("q", q, (S, self.H * self.Dk), self.tdt, self.device)
+        ldk = _rows("k", k, (S, self.H * self.Dk), self.tdt, self.device)
+        ldv = _rows("v", v, (S, self.H * self.Dv), self.tdt, self.device)
+        _full("slots", slots, (S,), torch.int32, self.device)
+        _full("out", out, self.state.shape, torch.float32, self.device)
+        y, home = self._y.get(S, (None, None))
+        if home != stream or not current or torch.cuda.is_current_stream_capturing():
+            y = self._output(S, stream)
+        mdl_linattn_step(S, self.H, self.Dk, self.Dv, self.x_dtype, self.decay, self.scale, q, ldq, k, ldk, v, ldv, slots,
+                         self.n_slots, self.state, self.state if out is None else out, y, self.H * self.Dv, stream)
+        return y
+
+
+class Dropout(_Buffers):
+    """Dropout of N rows of D channels, onto a residual where one is given (mdl_dropout). The mask follows from `rng`, two
+    64-bit words (seed, call) in an int64 device tensor: the object's own, or the caller's. A backward takes the words of
+    its forward; advance() before the next step draws new masks. Holds an output of the forward and one of the backward:
+    a call's result stands until the next call of the same method."""
+
+    def __init__(self, N: int, D: int, p: float, x_dtype: str = "f32", seed: int = 0, call: int = 0,
+                 device: str = "cuda"):
+        self.device = _device(device)
+        self.N, self.D, self.p = int(N), int(D), float(p)
+        if not 0.0 <= self.p < 1.0 or round(self.p * 65536) > 65535:
+            raise ValueError("p: need a probability in [0, 1) that does not round to 1 in steps of 2^-16")
+        self.x_dtype, self.tdt = _x_dtype(x_dtype)
+        words = np.array([seed % 2 ** 64, call % 2 ** 64], dtype=np.uint64).view(np.int64)
+        self.rng = torch.as_tensor(words, device=self.device)
+        self.y = self.dx = None
+        self._made(self.device)
+
+    def advance(self, by: int = 1, stream=None):
+        """Adds to the call's number: other masks from here on (recorded in a captured graph, once a replay)."""
+        handle = self._launch(stream)
+        with _on(handle, self.device):
+            self.rng[1:].add_(by)
+
+    def _apply(self, name, x, residual, rng, out, stream):
+        stream = self._launch(stream)
+        ldx = _rows("x" if name == "y" else "dy", x, (self.N, self.D), self.tdt, self.device)
+        ldr = 0 if residual is None else _rows("residual", residual, (self.N, self.D), self.tdt, self.device)
+        rng = self.rng if rng is None else rng
+        _full("rng", rng, (2,), torch.int64, self.device)
+        if out is None:
+            out, ldo = getattr(self, name), self.D
+            if out is None:
+                out, keep = self._new(stream, (self.N, self.D), self.tdt, False)
+                if keep:
+                    setattr(self, name, out)
+        else:
+            ldo = _rows("out", out, (self.N, self.D), self.tdt, self.device)
+        mdl_dropout(self.N, self.D, self.x_dtype, x, ldx, residual, ldr, self.p, rng, out, ldo, stream)
+        return out
+
+    def forward(self, x, residual=None, rng=None, out=None, stream=None):
+        """residual + x with elements dropped and the others scaled; out may be x or residual themselves."""
+        return self._apply("y", x, residual, rng, out, stream)
+
+    def backward(self, dy, rng=None, out=None, stream=None):
+        """dx (the residual's gradient is dy itself); out may be dy itself."""
+        return self._apply("dx", dy, None, rng, out, stream)

@@ -557,13 +557,105 @@ int mdl_distill(int64_t N, int32_t V, int32_t k, int32_t dtype, const void* z, i
                 void* stream);
 
 /*
+ * Linear attention with a decay for each head over packed sequences: the
+ * recurrence above with a matrix for a state, whose update is the token's own.
+ * Per sequence and head, in scan order, with d = decay[head],
+ *     S_t = d S_{t-1} + k_t v_t^T,   S before the first token = h0 (zero if NULL)
+ *     y_t = scale S_t^T q_t
+ * q, k: [T][H][Dk], v, y, dy: [T][H][Dv] of `dtype`, heads adjacent within a row,
+ * each tensor at its own row stride (in elements, at least its row's length), so
+ * that column blocks of one projection are taken as they lie. Any alignment of
+ * the element type is taken. decay: [H] float32, device, each in [0, 1] (not
+ * checked; others are taken at the formula's word). States h0, hT and their
+ * gradients: [S][H][Dk][Dv] float32. Sequences, seq_off, reverse, rows in no
+ * sequence and empty sequences are as for mdl_scan_forward. No value of one
+ * sequence or head reaches another, NaN included; within a sequence and head, one
+ * NaN or infinity leaves all of its outputs unspecified, those of earlier tokens
+ * too (blocks of tokens are products of matrices).
+ *
+ * States and sums are float32. bfloat16: products of rows are rounded to
+ * bfloat16 on the way to a token's output, as y itself is at its end; last states
+ * and the states' gradients are sums of unrounded products.
+ *
+ * ws: >= mdl_linattn_workspace_size bytes, 16-byte aligned (may be NULL where that
+ * is 0). The forward leaves in it what the backward needs: it is passed,
+ * unmodified, to the mdl_linattn_backward calls that follow with the same seq_off,
+ * S, T, H, Dk, Dv, dtype, reverse, decay and inputs, and belongs to one such pair
+ * at a time: calls that may overlap need one each.
+ *
+ * mdl_linattn_backward: from dy and, unless NULL, dhT (gradient of hT), with
+ * G_t = dL/dS_t = scale q_t dy_t^T + d G_{t+1} (dhT added at the last token),
+ *     dq_t = scale S_t dy_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,
+ *     dh0 = d G at the first token (dhT for an empty sequence)
+ * dq, dk, dv at row strides of their own; dh0 may be NULL. The decay is a constant
+ * of its head: it has no gradient.
+ *
+ * No output may overlap an input or another output (tensors that start at the
+ * same address and states that overlap are refused; column blocks of one matrix
+ * do not overlap).
+ *
+ * mdl_linattn_step: one token for each of S streams (serving). Row i advances the
+ * states slots[i] (device, int32; i itself if NULL) from h_in to h_out
+ * ([n_slots][H][Dk][Dv] float32; the same array to update in place) and writes
+ * row i of y. A row whose slot lies outside [0, n_slots) is left out: neither its
+ * y nor any state is written. Slots must differ from each other.
+ *
+ * Errors: MDL_EINVAL for null tensors, S, H, Dk, Dv < 1, T < 0, a stride below its
+ * row, an unknown dtype, outputs over inputs as above, n_slots < 1, slots NULL with
+ * n_slots < S, or a misaligned workspace; MDL_EUNSUPPORTED for Dk or Dv above 128
+ * or H above 65535; MDL_ESIZE for a short workspace; MDL_EOVERFLOW when T reaches
+ * 2^36, rows times a stride 2^60, S 2^31 - 64, or a launch 2^31 threads (a sequence,
+ * or a row of a step, takes 256 threads a head, and as many more for each 256
+ * elements of a sequence's state). With T = 0 the token tensors may be NULL.
+ */
+int mdl_linattn_workspace_size(int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype, size_t* bytes);
+int mdl_linattn_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype,
+                        int32_t reverse, const float* decay, float scale, const void* q, int64_t ldq, const void* k,
+                        int64_t ldk, const void* v, int64_t ldv, const float* h0, void* y, int64_t ldy, float* hT,
+                        void* ws, size_t ws_bytes, void* stream);
+int mdl_linattn_backward(const int64_t* seq_off, int32_t S, int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype,
+                         int32_t reverse, const float* decay, float scale, const void* q, int64_t ldq, const void* k,
+                         int64_t ldk, const void* v, int64_t ldv, const float* h0, const void* dy, int64_t lddy,
+                         const float* dhT, void* dq, int64_t lddq, void* dk, int64_t lddk, void* dv, int64_t lddv,
+                         float* dh0, void* ws, size_t ws_bytes, void* stream);
+int mdl_linattn_step(int32_t S, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype, const float* decay, float scale,
+                     const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                     const int32_t* slots, int32_t n_slots, const float* h_in, float* h_out, void* y, int64_t ldy,
+                     void* stream);
+
+/*
+ * Dropout from a counter-based generator, onto the residual: over N rows of D
+ * channels,
+ *     y = r + x [u >= c] 65536 / (65536 - c),   c = round(65536 p)
+ * (y = x [..] .. when r is NULL). u: 16 bits of Philox 4x32-10 for each element;
+ * the mask is a function of N, D, the element's place and the pair rng = (seed,
+ * call) alone, the same for both dtypes and any strides, and is never stored: the
+ * gradient of x is this call on dy, with the same rng, N, D and p and no r (that
+ * of r is dy). rng: two 64-bit words, device, 8-byte aligned, read by the kernel
+ * when it runs, so that a captured graph draws new masks when they have changed.
+ * Element (n, d) takes counter n ceil(D / 8) + d / 8 in the low 64 bits and `call`
+ * in the high ones, the key is `seed`, and of the 8 halves of the result it takes
+ * number d % 8, low halves first. The probability is rounded to a multiple of
+ * 2^-16, and the scale is that of the rounded one. A dropped element adds 0
+ * whatever x holds; p = 0 gives r + x.
+ * x, r, y: [N][D] of `dtype` at row strides ldx, ldr, ldy (ldr is ignored without
+ * r); any alignment of the element type. One float32 sum, rounded once. y may be x
+ * or r at the same stride; other overlaps are not allowed.
+ * Errors: MDL_EINVAL for null tensors, N < 0, D < 1, a stride below D, an unknown
+ * dtype, p outside [0, 1) or rounded to 1, or a misaligned rng; MDL_EOVERFLOW when
+ * rows times a stride reach 2^60 or N ceil(D / 8) exceeds 2^33.
+ */
+int mdl_dropout(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx, const void* r, int64_t ldr, float p,
+                const uint64_t* rng, void* y, int64_t ldy, void* stream);
+
+/*
  * Kernel timing (measurement support). mdl_timing(1) makes every later launch
  * of a kernel group (names: "build_maps", "scatter", "zero_fill", "projection",
  * "fwd_wavefront", "dirsum_overlap" (on the library's own stream, concurrent with
  * "fwd_wavefront"), "dirsum", "bwd_wavefront", "wgrad_overlap" (on the library's
  * own stream, concurrent with "bwd_wavefront"), "wgrad", "conv_fwd", "conv_bwd",
  * "ctc_head", "scan_fwd", "scan_bwd", "scan_step", "norm_fwd", "norm_bwd",
- * "distill")
+ * "distill", "attn_fwd", "attn_bwd", "attn_step", "dropout")
  * hand each of its dispatches a HIP event pair that the dispatch itself
  * records (hipExtLaunchKernel): the group's time runs from its first
  * dispatch's start to its last one's end, with no marker packets between

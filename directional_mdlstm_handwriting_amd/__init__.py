@@ -101,6 +101,8 @@ _SIGS = [
     ("mdl_linattn_step", _I32, [_I32, _I32, _I32, _I32, _I32, _P, _F32, _P, _I64, _P, _I64, _P, _I64, _P, _I32, _P, _P,
                                 _P, _I64, _P]),
     ("mdl_dropout", _I32, [_I64, _I32, _I32, _P, _I64, _P, _I64, _F32, _P, _P, _I64, _P]),
+    ("mdl_vocab_loss_workspace_size", _I32, [_I64, _I32, _I32, _I32, _I32, ctypes.POINTER(_SZ)]),
+    ("mdl_vocab_loss", _I32, [_I64, _I32, _I32, _I32, _P, _I64, _P, _P, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
     ("mdl_timing", _I32, [_I32]),
     ("mdl_set_wgrad_overlap", _I32, [_I32]),
     ("mdl_set_scan_wait", _I32, [_I32]),
@@ -437,6 +439,18 @@ def mdl_linattn_step(S: int, H: int, Dk: int, Dv: int, dtype: int, decay, scale:
 
 def mdl_dropout(N: int, D: int, dtype: int, x, ldx: int, r, ldr: int, p: float, rng, y, ldy: int, stream=None):
     _check(_lib.mdl_dropout(N, D, dtype, _ptr(x), ldx, _ptr(r), ldr, p, _ptr(rng), _ptr(y), ldy, _stream(stream)))
+
+
+def mdl_vocab_loss_workspace_size(N: int, D: int, V: int, dtype: int, grads: bool) -> int:
+    b = _SZ()
+    _check(_lib.mdl_vocab_loss_workspace_size(N, D, V, dtype, int(grads), ctypes.byref(b)))
+    return b.value
+
+
+def mdl_vocab_loss(N: int, D: int, V: int, dtype: int, h, ldh: int, W, ids, w, loss, dh, lddh: int, dW, ws, ws_bytes: int,
+                   stream=None):
+    _check(_lib.mdl_vocab_loss(N, D, V, dtype, _ptr(h), ldh, _ptr(W), _ptr(ids), _ptr(w), _ptr(loss), _ptr(dh), lddh,
+                               _ptr(dW), _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def mdl_set_wgrad_overlap(mode):

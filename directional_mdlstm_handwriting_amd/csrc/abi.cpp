@@ -1502,6 +1502,60 @@ int mdl_dropout(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx,
     GUARD_END
 }
 
+// ---- cross entropy over a vocabulary ---------------------------------------------------------------------
+static int check_vocab(const std::string& F, int64_t N, int32_t D, int32_t V, int32_t dtype, bool grads, size_t& need) {
+    int rc = check_dtype(F, dtype);
+    if (rc) return rc;
+    if (N < 0 || D < 1 || V < 1) return fail(MDL_EINVAL, F + ": need N >= 0, D >= 1 and V >= 1");
+    if (D > mdl::vocab_max_d()) return fail(MDL_EUNSUPPORTED, F + ": D above " + std::to_string(mdl::vocab_max_d()));
+    if (V > mdl::vocab_max_classes())
+        return fail(MDL_EUNSUPPORTED, F + ": V above " + std::to_string(mdl::vocab_max_classes()));
+    // the widest launches: 256 threads for each 256 values of dh or dW, and for each tile of the logits
+    const int64_t most = mdl::kMaxLaunchThreads, cols = ((int64_t)D + 255) / 256 * 256;
+    if (N > most / cols || N > most / (((int64_t)V + 127) / 128) || V > most / cols)
+        return fail(MDL_EOVERFLOW, F + ": a launch exceeds 2^31 threads");
+    need = mdl::vocab_plan(N, D, V, dtype, grads).total;
+    return MDL_OK;
+}
+
+int mdl_vocab_loss_workspace_size(int64_t N, int32_t D, int32_t V, int32_t dtype, int32_t grads, size_t* bytes) {
+    GUARD_BEGIN
+    if (!bytes) return fail(MDL_EINVAL, "mdl_vocab_loss_workspace_size: null argument");
+    size_t need = 0;
+    const int rc = check_vocab("mdl_vocab_loss_workspace_size", N, D, V, dtype, grads != 0, need);
+    if (rc) return rc;
+    *bytes = need;
+    return MDL_OK;
+    GUARD_END
+}
+
+int mdl_vocab_loss(int64_t N, int32_t D, int32_t V, int32_t dtype, const void* h, int64_t ldh, const void* W,
+                   const int32_t* ids, const float* w, float* loss, void* dh, int64_t lddh, void* dW, void* ws,
+                   size_t ws_bytes, void* stream) {
+    GUARD_BEGIN
+    const std::string F("mdl_vocab_loss");
+    size_t need = 0;
+    int rc = check_vocab(F, N, D, V, dtype, dW != nullptr, need);
+    if (rc) return rc;
+    if (!W || (N > 0 && (!h || !ids || !loss))) return fail(MDL_EINVAL, F + ": null tensor");
+    if (N > 0 && (dh == nullptr) != (dW == nullptr)) return fail(MDL_EINVAL, F + ": dh and dW go together");
+    if ((rc = check_stride(F, "ldh", N, D, ldh))) return rc;
+    if (dh && (rc = check_stride(F, "lddh", N, D, lddh))) return rc;
+    if (D % (dtype == MDL_BF16 ? 8 : 4) == 0 && reinterpret_cast<uintptr_t>(W) % 16)
+        return fail(MDL_EINVAL, F + ": W not 16-byte aligned");
+    if ((rc = check_ws(F, "mdl_vocab_loss_workspace_size", need, ws, ws_bytes))) return rc;
+    if ((rc = check_apart(F, {dW}, {h, W, dh})) || (rc = check_apart(F, {dh}, {W}))) return rc;
+    const mdl::VocabArgs a{N, D, V, h, W, ldh, lddh, ids, w, loss, dh, dW};
+    hipError_t e;
+    {
+        Timed t("vocab_loss");
+        e = mdl::launch_vocab(a, dtype, ws, static_cast<hipStream_t>(stream));
+    }
+    if (e != hipSuccess) return hip_fail(e, F);
+    return MDL_OK;
+    GUARD_END
+}
+
 int mdl_set_scan_wait(int32_t on) {
     if (on < 0 || on > 1) return fail(MDL_EINVAL, "mdl_set_scan_wait: on must be 0 or 1");
     g_scan_wait.store(on != 0);

@@ -1,0 +1,565 @@
+// k_vocab.hip — softmax cross entropy over a vocabulary from the hidden states and the class weights, with its gradients,
+// without the logits in memory.
+//
+//   z = h W^T,  loss_n = w_n (ln sum_c exp z_nc - z_n,id),  G = w (softmax z - [c = id]),  dh = G W,  dW = G^T h
+//
+// A first product over the whole vocabulary leaves per row and 256 (or 128) classes their maximum and sum of exponentials,
+// and the target's logit; `join` makes the losses of them. Then, piece of the vocabulary by piece, a second product of the
+// same operands forms G of the piece (its values rounded once to the inputs' type), and two more take it into dh and dW.
+// So the memory held is that of one piece, and the work is 8 N V D operations where 6 N V D are the least.
+//
+// Products: tiles of BM x BN by 8 (4) waves, 32 x 32 results of the matrix instructions (32x32x16 bfloat16, 32x32x2 fp32),
+// 128 bytes of depth at a time from global memory straight into LDS, one step ahead of the products. An operand whose rows
+// run along the depth is laid row by row, its 16-byte chunks rotated by the row so that a wave's reads meet all banks; one
+// whose rows run across it is laid as it comes and read by transposing reads (bfloat16) or word by word (fp32).
+#include "kernels.h"
+#include "seqio.h"
+
+#include <algorithm>
+
+namespace mdl {
+
+namespace {
+
+typedef __bf16 bh8 __attribute__((ext_vector_type(8)));
+typedef short h4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+#define MDL_LDS __attribute__((address_space(3)))
+
+// ---- operand tiles ----------------------------------------------------------------------------------------------
+// ROWS rows (of the result) by 128 bytes of depth in LDS. ALONG: the operand's rows in memory run along the depth.
+template <typename T, int ROWS, int THREADS, bool ALONG>
+struct Tile {
+    static constexpr int E = sizeof(T), BK = 128 / E, per_thread = ROWS * 8 / THREADS, bytes = ROWS * 128;
+    static constexpr int row_bytes = ALONG ? 128 : ROWS * E, row_chunks = row_bytes / 16;
+    static_assert(ROWS * 8 % THREADS == 0, "whole chunks a thread");
+    const char* base;     // ALONG: row 0 at the depth of the next step; else the next step's first row
+    int64_t ld;           // bytes
+    int rows, width;      // ALONG: rows of the tile that exist; else: bytes of a row that exist
+    int64_t depth;        // ALONG: bytes of depth that are left; else rows
+    uint32_t off[per_thread];
+
+    // row0: the tile's first row of the result, k0: first element of depth, k1: its end
+    __device__ inline void init(const void* p, int64_t ld_elems, int64_t row0, int64_t n_rows, int64_t k0, int64_t k1) {
+        ld = ld_elems * E;
+        if constexpr (ALONG) {
+            base = static_cast<const char*>(p) + row0 * ld + k0 * E;
+            rows = (int)(n_rows - row0 < ROWS ? n_rows - row0 : ROWS);
+            width = 0;
+            depth = (k1 - k0) * E;
+        } else {
+            base = static_cast<const char*>(p) + k0 * ld + row0 * E;
+            rows = 0;
+            const int64_t left = (n_rows - row0) * E;
+            width = (int)(left < row_bytes ? left : row_bytes);
+            depth = k1 - k0;
+        }
+#pragma unroll
+        for (int i = 0; i < per_thread; ++i) {
+            const int q = i * THREADS + threadIdx.x, r = q / row_chunks, c = q % row_chunks;
+            if constexpr (ALONG) off[i] = (uint32_t)(r * ld) + 16 * (c ^ (r & 7));
+            else off[i] = (uint32_t)(r * ld) + 16 * (c ^ (E == 2 ? (r & 3) << 2 : (r >> 2 & 1) << 3));
+        }
+    }
+    // the next 128 bytes of depth into the LDS tile; zeros past the depth's end and the operand's edge. Chunks are whole:
+    // the depth (ALONG) and the row's width (else) count in chunks of 16 bytes, of which the caller keeps the last one
+    // readable and finite.
+    __device__ inline void load(char* lds) {
+        constexpr uint32_t kOut = 0x80000000u;
+        const bool any = depth > 0;
+        int64_t records;
+        if constexpr (ALONG) records = any ? (rows - 1) * ld + (depth < 128 ? depth : 128) + 15 : 0;
+        else records = any ? ((depth < BK ? depth : BK) - 1) * ld + width + 15 : 0;
+        const __amdgpu_buffer_rsrc_t r = rsrc(base, records & ~int64_t(15));
+        const bool part = ALONG ? depth < 128 : width < row_bytes;
+#pragma unroll
+        for (int i = 0; i < per_thread; ++i) {
+            uint32_t o = off[i];
+            if (part) {
+                const int q = i * THREADS + threadIdx.x, row = q / row_chunks, c = q % row_chunks;
+                if constexpr (ALONG) o = 16 * (c ^ (row & 7)) < depth ? o : kOut;
+                else o = 16 * (c ^ (E == 2 ? (row & 3) << 2 : (row >> 2 & 1) << 3)) < width ? o : kOut;
+            }
+            const int first = (i * THREADS + (int)(threadIdx.x & ~63u)) * 16;  // of the wave
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MDL_LDS void*)(lds + first), 16, o, 0, 0, 0);
+        }
+        if constexpr (ALONG) {
+            base += 128;
+            depth -= 128;
+        } else {
+            base += BK * ld;
+            depth -= BK;
+        }
+    }
+    // this lane's part of the operand for 32 rows from row0 on, at 32 bytes of depth: 16 bytes of row lane % 32, the lower
+    // half of the depth in the lower 32 lanes
+    static __device__ inline u32x4 part(const char* lds, int row0, int s) {
+        const int lane = threadIdx.x & 63;
+        if constexpr (ALONG) {
+            const int r = row0 + (lane & 31);
+            return *reinterpret_cast<const u32x4*>(lds + r * 128 + 16 * ((2 * s + (lane >> 5)) ^ (r & 7)));
+        } else if constexpr (E == 2) {
+            typedef MDL_LDS h4* P;
+            const int q = lane >> 4, i = lane & 15, k = 16 * s + 8 * (q >> 1) + (i >> 2);
+            const int col = (row0 + 16 * (q & 1)) * 2 + 8 * (i & 3);
+            const char* p = lds + k * row_bytes + (col ^ (i >> 2) << 6);
+            const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p)));
+            const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p + 4 * row_bytes)));
+            return u32x4{a[0], a[1], b[0], b[1]};
+        } else {
+            const int h = lane >> 5, k = 8 * s + 4 * h;
+            const char* p = lds + k * row_bytes + ((row0 + (lane & 31)) * 4 ^ h << 7);
+            u32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const uint32_t*>(p + e * row_bytes);
+            return v;
+        }
+    }
+};
+
+template <typename T>
+__device__ inline f32x16 mma(u32x4 x, u32x4 y, f32x16 c) {
+    if constexpr (sizeof(T) == 2) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bh8, x), __builtin_bit_cast(bh8, y), c, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(x[e]), __uint_as_float(y[e]), c, 0, 0, 0);
+        return c;
+    }
+}
+
+// (maximum, sum) of two parts of a row; the sum beside a maximum of -inf is 0 or NaN
+__device__ inline float2 joined(float2 a, float2 b) {
+    const float top = fmaxf(a.x, b.x);
+    const float x = a.x == -INFINITY ? a.y : a.y * exp_neg<float>(a.x - top);
+    const float y = b.x == -INFINITY ? b.y : b.y * exp_neg<float>(b.x - top);
+    return make_float2(top, x + y);
+}
+
+// ---- the product ------------------------------------------------------------------------------------------------
+template <int WM_, int WN_, int TM_, int TN_>
+struct Shape {  // waves down and across, 32 x 32 tiles of a wave down and across
+    static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, threads = 64 * WM * WN, BM = 32 * WM * TM, BN = 32 * WN * TN;
+};
+typedef Shape<2, 4, 4, 2> Large;  // 256 x 256
+typedef Shape<2, 2, 2, 2> Small;  // 128 x 128
+
+struct Args {
+    const void *a, *b;            // result rows and columns' operands
+    int64_t lda, ldb, M, N, K;
+    int64_t tiles_m, tiles_n, splits;
+    // epilogues
+    float2* stats;                // [tiles_n][M] maximum and sum
+    float *target, *lse;          // [M]
+    const int32_t* ids;           // [M] -1: none
+    const float* coef;            // [M]
+    int64_t n_first;              // class of column 0
+    void* out;
+    int64_t ldo, cols;            // cols: columns that are written (zeros past N)
+    float* slab;                  // [splits][M][N]
+    int add;                      // onto what the slab holds
+};
+
+enum { kStats, kGrad, kStore, kSlab };
+
+template <typename T, typename S, bool AA, bool BA, int EPI>
+__global__ __launch_bounds__(S::threads, 2) void product(const Args g) {
+    typedef Tile<T, S::BM, S::threads, AA> TA;
+    typedef Tile<T, S::BN, S::threads, BA> TB;
+    // four arrays: the compiler sees that loads into one pair do not meet the reads of the other
+    __shared__ alignas(16) char a0[TA::bytes], b0[TB::bytes], a1[TA::bytes], b1[TB::bytes];
+    // neighbouring workgroups go to the eight dies in turn: each die takes one run of tiles, in groups of 8 rows of tiles
+    const int64_t total = (int64_t)gridDim.x;
+    int64_t id = blockIdx.x;
+    {
+        const int64_t per = total / 8, more = total % 8, x = id % 8;
+        id = x * per + (x < more ? x : more) + id / 8;
+    }
+    const int64_t tiles = g.tiles_m * g.tiles_n, split = id / tiles;
+    id -= split * tiles;
+    const int64_t band = 8 * g.tiles_n, first = id / band * 8;
+    const int64_t high = g.tiles_m - first < 8 ? g.tiles_m - first : 8;
+    const int64_t tm = first + id % band % high, tn = id % band / high;
+    const int64_t m0 = tm * S::BM, n0 = tn * S::BN;
+    constexpr int BK = TA::BK;
+    const int64_t steps_all = (g.K + BK - 1) / BK;
+    const int64_t s0 = steps_all * split / g.splits, s1 = steps_all * (split + 1) / g.splits;
+    const int64_t k1 = s1 * BK < g.K ? s1 * BK : g.K;
+    TA ta;
+    TB tb;
+    ta.init(g.a, g.lda, m0, g.M, s0 * BK, k1);
+    tb.init(g.b, g.ldb, n0, g.N, s0 * BK, k1);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
+    const int wm = wave / S::WN * (32 * S::TM), wn = wave % S::WN * (32 * S::TN);
+    f32x16 c[S::TM][S::TN];
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) c[i][j][e] = 0.f;
+    const auto step = [&](const char* la, const char* lb) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            u32x4 x[S::TM], y[S::TN];
+#pragma unroll
+            for (int i = 0; i < S::TM; ++i) x[i] = TA::part(la, wm + 32 * i, s);
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j) y[j] = TB::part(lb, wn + 32 * j, s);
+#pragma unroll
+            for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+                for (int j = 0; j < S::TN; ++j) c[i][j] = mma<T>(y[j], x[i], c[i][j]);
+        }
+    };
+    ta.load(a0);
+    tb.load(b0);
+    __syncthreads();
+    const int64_t steps = s1 - s0;
+    for (int64_t t = 0; t < steps; t += 2) {
+        ta.load(a1);
+        tb.load(b1);
+        step(a0, b0);
+        __syncthreads();
+        if (t + 1 >= steps) break;
+        ta.load(a0);
+        tb.load(b0);
+        step(a1, b1);
+        __syncthreads();
+    }
+    // A lane holds row lane % 32 of each of its tiles, columns 8 (e / 4) + 4 h + e % 4.
+    if constexpr (EPI == kStats) {
+        float2* part = reinterpret_cast<float2*>(a0);  // [WN][BM]; all reads of the tiles are done
+        const int64_t limit = g.N - n0;
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i) {
+            const int row = wm + 32 * i + (lane & 31);
+            const int64_t m = m0 + row;
+            const int64_t id = m < g.M ? (int64_t)g.ids[m] - n0 : -1;
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int n = wn + 32 * j + 8 * (e >> 2) + 4 * h + (e & 3);
+                    if (n >= limit) c[i][j][e] = -INFINITY;
+                    if (n == id) g.target[m] = c[i][j][e];
+                    top = fmaxf(top, c[i][j][e]);
+                }
+            top = fmaxf(top, __shfl_xor(top, 32));
+            // a row of -inf alone: sum 0, and NaN where one of them is NaN, which the maximum passes over
+            const float base = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) sum += exp_neg<T>(c[i][j][e] - base);
+            sum += __shfl_xor(sum, 32);
+            if (h == 0) part[wave % S::WN * S::BM + row] = make_float2(top, sum);
+        }
+        __syncthreads();
+        for (int row = threadIdx.x; row < S::BM; row += S::threads) {
+            if (m0 + row >= g.M) continue;
+            float2 p = part[row];
+#pragma unroll
+            for (int w = 1; w < S::WN; ++w) p = joined(p, part[w * S::BM + row]);
+            g.stats[tn * g.M + m0 + row] = p;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i) {
+            const int64_t m = m0 + wm + 32 * i + (lane & 31);
+            if (m >= g.M) continue;
+            float lse = 0.f, coef = 0.f;
+            int64_t id = -1;
+            if constexpr (EPI == kGrad) {
+                lse = g.lse[m];
+                coef = g.coef[m];
+                id = (int64_t)g.ids[m] - g.n_first - n0;
+            }
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const int n = wn + 32 * j + 2 * e + 4 * h;
+                    float v[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        v[r] = c[i][j][e + r];
+                        if constexpr (EPI == kGrad) {
+                            const float p = exp_neg<T>(v[r] - lse) - (n + r == id ? 1.f : 0.f);
+                            v[r] = coef == 0.f || n0 + n + r >= g.N ? 0.f : coef * p;
+                        }
+                    }
+                    if constexpr (EPI == kSlab) {
+                        float* o = g.slab + (split * g.M + m) * g.N + n0 + n;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (n0 + n + r < g.N) o[r] = g.add ? o[r] + v[r] : v[r];
+                    } else {
+                        T* o = static_cast<T*>(g.out) + m * g.ldo + n0 + n;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float one[1] = {v[r]};
+                            if (n0 + n + r < g.cols) store_vec<1>(o + r, one);
+                        }
+                    }
+                }
+        }
+    }
+}
+
+template <typename T, bool AA, bool BA, int EPI>
+void go(Args g, bool large, int64_t splits, hipStream_t st) {
+    const int64_t bm = large ? Large::BM : Small::BM, bn = large ? Large::BN : Small::BN;
+    g.tiles_m = (g.M + bm - 1) / bm;
+    g.tiles_n = (g.N + bn - 1) / bn;
+    g.splits = splits;
+    const dim3 grid((uint32_t)(g.tiles_m * g.tiles_n * splits));
+    if (large) launch(product<T, Large, AA, BA, EPI>, grid, dim3(Large::threads), 0, st, g);
+    else launch(product<T, Small, AA, BA, EPI>, grid, dim3(Small::threads), 0, st, g);
+}
+
+// ---- the rows before and after ------------------------------------------------------------------------------------
+// Rows of src as rows of a whole number of 16-byte chunks, zeros past their end; with ids, each row's target and weight,
+// and zeros for a row that counts for nothing, so that nothing it holds meets a product.
+template <typename T, bool ROWS>
+__global__ __launch_bounds__(256) void pack(const T* src, int64_t ld, int64_t n, int D, T* dst, int64_t ldd,
+                                            const int32_t* ids, const float* w, int V, int32_t* target, float* coef) {
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= n) return;
+    const int lane = threadIdx.x & 63;
+    bool live = true;
+    if constexpr (ROWS) {
+        const int id = ids[row];
+        const float c = w ? w[row] : 1.f;
+        live = c != 0.f && id >= 0 && id < V;
+        if (lane == 0) {
+            target[row] = live ? id : (c == 0.f || id == -1 ? -1 : -2);
+            coef[row] = live ? c : 0.f;
+        }
+    }
+    constexpr int E = Width<T>::v;
+    for (int64_t d = (int64_t)lane * E; d < ldd; d += 64 * E) {
+        T* o = dst + row * ldd + d;
+        if (live && d + E <= D) {
+            *reinterpret_cast<u32x4*>(o) = *reinterpret_cast<const u32x4_e*>(src + row * ld + d);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float one[1] = {live && d + e < D ? load_raw<1>(src + row * ld + d + e)[0] : 0.f};
+                store_vec<1>(o + e, one);
+            }
+        }
+    }
+}
+
+// A row's tiles joined, 32 rows by 8 groups of tiles a workgroup.
+__global__ __launch_bounds__(256) void join(const float2* stats, int64_t tiles, int64_t N, const float* target_logit,
+                                            const int32_t* target, const float* coef, float* lse, float* loss) {
+    __shared__ float2 part[8][32];
+    const int r = threadIdx.x & 31, grp = threadIdx.x >> 5;
+    const int64_t n = (int64_t)blockIdx.x * 32 + r;
+    float2 p = make_float2(-INFINITY, 0.f);
+    if (n < N)
+        for (int64_t t = grp; t < tiles; t += 8) p = joined(p, stats[t * N + n]);
+    part[grp][r] = p;
+    __syncthreads();
+    if (grp != 0 || n >= N) return;
+    for (int i = 1; i < 8; ++i) p = joined(p, part[i][r]);
+    const float l = p.x + logf(p.y);
+    lse[n] = l;
+    const int id = target[n];
+    loss[n] = id >= 0 ? coef[n] * (l - target_logit[n]) : (id == -1 ? 0.f : NAN);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void clear(T* p, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const float one[1] = {0.f};
+    if (i < n) store_vec<1>(p + i, one);
+}
+
+// out = sum of the slabs, in their order
+template <typename T>
+__global__ __launch_bounds__(256) void sum_slabs(const float* slab, int64_t slabs, int64_t M, int64_t N, T* out,
+                                                 int64_t ldo) {
+    const int64_t per = (N + 255) / 256, m = blockIdx.x / per, n = blockIdx.x % per * 256 + threadIdx.x;
+    if (n >= N) return;
+    float v = 0.f;
+    for (int64_t s = 0; s < slabs; ++s) v += slab[(s * M + m) * N + n];
+    const float one[1] = {v};
+    store_vec<1>(out + m * ldo + n, one);
+}
+
+// ---- plan ---------------------------------------------------------------------------------------------------------
+int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+// the larger tiles where they fill the compute units
+bool large_tiles(int64_t M, int64_t N) {
+    return ((M + 255) / 256) * ((N + 255) / 256) >= 192;
+}
+// how often the depth is split where there are few tiles: so that some 512 workgroups share the work, none with less than
+// eight steps of it
+int64_t splits_of(int64_t M, int64_t N, int64_t K, int e) {
+    if (large_tiles(M, N)) return 1;
+    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128), steps = (K * e + 127) / 128;
+    return std::max<int64_t>(1, std::min<int64_t>({512 / tiles, steps / 8, int64_t(64)}));
+}
+
+}  // namespace
+
+// rows of a tile times a row's bytes stay inside the 31 bits of a buffer's offsets: 256 rows of 2^20 fp32 logits are 2^30
+int64_t vocab_max_classes() { return int64_t(1) << 20; }
+int vocab_max_d() { return 1 << 16; }
+
+// Workspace: the hidden states as they meet the products, the weights too where their rows are no whole number of chunks,
+// the tiles' statistics, a row's numbers, and with gradients a piece of G, dh's slabs and dW's.
+VocabPlan vocab_plan(int64_t N, int D, int V, int dtype, bool grads) {
+    const int e = dtype == 1 ? 2 : 4, chunk = 16 / e;
+    VocabPlan p;
+    p.ldh = up(D, chunk);
+    p.pack_w = D % chunk != 0;
+    p.large = large_tiles(N, V);
+    p.tiles = (V + (p.large ? 255 : 127)) / (p.large ? 256 : 128);
+    size_t at = 0;
+    const auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += (bytes + 255) / 256 * 256;
+        return o;
+    };
+    p.h = take((size_t)N * p.ldh * e);
+    p.w = take(p.pack_w ? (size_t)V * p.ldh * e : 0);
+    p.stats = take((size_t)p.tiles * N * sizeof(float2));
+    p.lse = take((size_t)N * 4);
+    p.target_logit = take((size_t)N * 4);
+    p.target = take((size_t)N * 4);
+    p.coef = take((size_t)N * 4);
+    if (grads && N > 0) {
+        // a piece of G holds up to 128 MB, so that it stays in the cache between the products; at least 2048 classes
+        const int64_t fit = (int64_t(128) << 20) / (N * e) / 256 * 256;
+        p.piece = std::min<int64_t>(up(V, 256), std::max<int64_t>(2048, fit));
+        const int64_t pieces = (V + p.piece - 1) / p.piece;
+        p.piece = up((V + pieces - 1) / pieces, 256);
+        p.dh_splits = splits_of(N, D, p.piece, e);
+        p.dw_splits = splits_of(p.piece, D, N, e);
+        p.g = take((size_t)N * p.piece * e);
+        p.dh_slab = p.dh_splits > 1 || p.piece < V;
+        p.dh = take(p.dh_slab ? (size_t)p.dh_splits * N * D * 4 : 0);
+        p.dw = take(p.dw_splits > 1 ? (size_t)p.dw_splits * p.piece * D * 4 : 0);
+    }
+    p.total = at;
+    return p;
+}
+
+template <typename T>
+static hipError_t vocab_loss(const VocabArgs& x, int dtype, void* ws, hipStream_t st) {
+    const bool grads = x.dW != nullptr;
+    const VocabPlan p = vocab_plan(x.N, x.D, x.V, dtype, grads);
+    char* w = static_cast<char*>(ws);
+    T* h = reinterpret_cast<T*>(w + p.h);
+    const T* W = static_cast<const T*>(x.W);
+    int32_t* target = reinterpret_cast<int32_t*>(w + p.target);
+    float* coef = reinterpret_cast<float*>(w + p.coef);
+    float* lse = reinterpret_cast<float*>(w + p.lse);
+    if (x.N > 0)
+        launch(pack<T, true>, dim3((uint32_t)((x.N + 3) / 4)), dim3(256), 0, st, static_cast<const T*>(x.h), x.ldh, x.N, x.D, h,
+               p.ldh, x.ids, x.w, x.V, target, coef);
+    if (p.pack_w && x.N > 0) {
+        T* to = reinterpret_cast<T*>(w + p.w);
+        launch(pack<T, false>, dim3((uint32_t)((x.V + 3) / 4)), dim3(256), 0, st, W, (int64_t)x.D, (int64_t)x.V, x.D, to, p.ldh,
+               static_cast<const int32_t*>(nullptr), static_cast<const float*>(nullptr), 0, static_cast<int32_t*>(nullptr),
+               static_cast<float*>(nullptr));
+        W = to;
+    }
+    if (x.N > 0) {
+        Args a{};
+        a.a = h;
+        a.b = W;
+        a.lda = a.ldb = p.ldh;
+        a.M = x.N;
+        a.N = x.V;
+        a.K = x.D;
+        a.stats = reinterpret_cast<float2*>(w + p.stats);
+        a.target = reinterpret_cast<float*>(w + p.target_logit);
+        a.ids = target;
+        go<T, true, true, kStats>(a, p.large, 1, st);
+        launch(join, dim3((uint32_t)((x.N + 31) / 32)), dim3(256), 0, st, a.stats, p.tiles, x.N, a.target, target, coef, lse,
+               x.loss);
+    }
+    if (!grads) return hipGetLastError();
+    if (x.N == 0) {
+        const int64_t n = (int64_t)x.V * x.D;
+        launch(clear<T>, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, st, static_cast<T*>(x.dW), n);
+        return hipGetLastError();
+    }
+    T* G = reinterpret_cast<T*>(w + p.g);
+    float* dh_slab = reinterpret_cast<float*>(w + p.dh);
+    for (int64_t v0 = 0; v0 < x.V; v0 += p.piece) {
+        const int64_t nv = std::min<int64_t>(p.piece, x.V - v0);
+        const T* Wp = W + v0 * p.ldh;
+        Args a{};
+        a.a = h;
+        a.b = Wp;
+        a.lda = a.ldb = p.ldh;
+        a.M = x.N;
+        a.N = nv;
+        a.K = x.D;
+        a.lse = lse;
+        a.ids = target;
+        a.coef = coef;
+        a.n_first = v0;
+        a.out = G;
+        a.ldo = p.piece;
+        a.cols = up(nv, 16 / (int64_t)sizeof(T));
+        go<T, true, true, kGrad>(a, large_tiles(x.N, nv), 1, st);
+        Args b{};
+        b.a = G;
+        b.b = Wp;
+        b.lda = p.piece;
+        b.ldb = p.ldh;
+        b.M = x.N;
+        b.N = x.D;
+        b.K = nv;
+        b.out = x.dh;
+        b.ldo = x.lddh;
+        b.cols = x.D;
+        b.slab = dh_slab;
+        b.add = v0 > 0;
+        if (p.dh_slab) go<T, true, false, kSlab>(b, large_tiles(x.N, x.D), p.dh_splits, st);
+        else go<T, true, false, kStore>(b, large_tiles(x.N, x.D), 1, st);
+        Args c{};
+        c.a = G;
+        c.b = h;
+        c.lda = p.piece;
+        c.ldb = p.ldh;
+        c.M = nv;
+        c.N = x.D;
+        c.K = x.N;
+        T* dW = static_cast<T*>(x.dW) + v0 * x.D;
+        c.out = dW;
+        c.ldo = x.D;
+        c.cols = x.D;
+        c.slab = reinterpret_cast<float*>(w + p.dw);
+        const bool large = large_tiles(p.piece, x.D);
+        if (p.dw_splits > 1) {
+            go<T, false, false, kSlab>(c, large, p.dw_splits, st);
+            launch(sum_slabs<T>, dim3((uint32_t)(nv * ((x.D + 255) / 256))), dim3(256), 0, st, c.slab, p.dw_splits, nv,
+                   (int64_t)x.D, dW, (int64_t)x.D);
+        } else {
+            go<T, false, false, kStore>(c, large, 1, st);
+        }
+    }
+    if (p.dh_slab)
+        launch(sum_slabs<T>, dim3((uint32_t)(x.N * ((x.D + 255) / 256))), dim3(256), 0, st, dh_slab, p.dh_splits, x.N,
+               (int64_t)x.D, static_cast<T*>(x.dh), x.lddh);
+    return hipGetLastError();
+}
+
+hipError_t launch_vocab(const VocabArgs& x, int dtype, void* ws, hipStream_t st) {
+    return dtype == 1 ? vocab_loss<bf16>(x, dtype, ws, st) : vocab_loss<float>(x, dtype, ws, st);
+}
+
+}  // namespace mdl

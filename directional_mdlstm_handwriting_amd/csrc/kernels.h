@@ -395,4 +395,25 @@ int64_t dropout_max_groups();
 hipError_t launch_dropout(int64_t N, int D, int dtype, const void* x, int64_t ldx, const void* r, int64_t ldr, int cut,
                           const uint64_t* rng, void* y, int64_t ldy, hipStream_t st);
 
+// cross entropy over a vocabulary from hidden states and class weights (k_vocab.hip)
+struct VocabArgs {
+    int64_t N;
+    int D, V;
+    const void *h, *W;          // [N][D] at row stride ldh, [V][D]
+    int64_t ldh, lddh;
+    const int32_t* ids;         // [N]
+    const float* w;             // [N] or null
+    float* loss;                // [N]
+    void *dh, *dW;              // [N][D] at row stride lddh, [V][D]; null: the loss alone
+};
+struct VocabPlan {
+    int64_t ldh = 0, tiles = 0, piece = 0, dh_splits = 1, dw_splits = 1;
+    bool pack_w = false, large = false, dh_slab = false;
+    size_t h = 0, w = 0, stats = 0, lse = 0, target_logit = 0, target = 0, coef = 0, g = 0, dh = 0, dw = 0, total = 0;
+};
+int64_t vocab_max_classes();
+int vocab_max_d();
+VocabPlan vocab_plan(int64_t N, int D, int V, int dtype, bool grads);
+hipError_t launch_vocab(const VocabArgs& x, int dtype, void* ws, hipStream_t st);
+
 }  // namespace mdl

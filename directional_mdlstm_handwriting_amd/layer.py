@@ -12,7 +12,8 @@ recurrence along the rows or frames of the packed examples, whole sequences
 at once or a token at a time; ``BlockNorm`` the norms around such a block with
 its gate and residual; ``LinearAttention`` and ``AttentionState`` the recurrence
 with a matrix for a state and a decay for each head; ``Dropout`` a block's
-dropout onto the residual; ``TopKDistill`` the distillation loss of its logits.
+dropout onto the residual; ``TopKDistill`` the distillation loss of its logits,
+``VocabLoss`` the cross entropy over a vocabulary without them.
 """
 
 from __future__ import annotations
@@ -29,7 +30,8 @@ from . import (MDL_BF16, MDL_CELL_LEAKY_LP, MDL_CELL_MDLSTM, MDL_F32, MDL_PACK_A
                mdl_layout_device_size, mdl_layout_rects, mdl_layout_upload, mdl_pack, mdl_pack_level, mdl_scatter, mdl_workspace_size,
                mdl_ctc_head, mdl_ctc_workspace_size, mdl_scan_backward, mdl_scan_forward, mdl_scan_step, mdl_scan_workspace_size,
                mdl_blocknorm_backward, mdl_blocknorm_forward, mdl_blocknorm_workspace_size, mdl_distill, mdl_dropout,
-               mdl_linattn_backward, mdl_linattn_forward, mdl_linattn_step, mdl_linattn_workspace_size, _stream)
+               mdl_linattn_backward, mdl_linattn_forward, mdl_linattn_step, mdl_linattn_workspace_size, mdl_vocab_loss,
+               mdl_vocab_loss_workspace_size, _stream)
 
 
 def _dev(a, device, dtype=torch.float32):
@@ -752,3 +754,43 @@ class Dropout(_Buffers):
     def backward(self, dy, rng=None, out=None, stream=None):
         """dx (the residual's gradient is dy itself); out may be dy itself."""
         return self._apply("dx", dy, None, rng, out, stream)
+
+
+class VocabLoss(_Buffers):
+    """Softmax cross entropy of N rows over V classes from their hidden states of D channels and the classes' weights
+    (mdl_vocab_loss): the loss per row and the gradients of the sum, in one call and without the logits. Holds them and the
+    workspaces, one for each kind of call; results stand until the next call."""
+
+    def __init__(self, N: int, D: int, V: int, x_dtype: str = "f32", device: str = "cuda"):
+        self.device = _device(device)
+        self.N, self.D, self.V = int(N), int(D), int(V)
+        self.x_dtype, self.tdt = _x_dtype(x_dtype)
+        self.ws_bytes = [mdl_vocab_loss_workspace_size(self.N, self.D, self.V, self.x_dtype, g) for g in (False, True)]
+        self.ws = self.ws_loss = self.dh = self.dW = None
+        self.loss = torch.empty(self.N, dtype=torch.float32, device=self.device)
+        self._made(self.device)
+
+    def _buffer(self, name, shape, dtype, stream):
+        t = getattr(self, name)
+        if t is None:
+            t, keep = self._new(stream, shape, dtype, False)
+            if keep:
+                setattr(self, name, t)
+        return t
+
+    def run(self, h, W, ids, w=None, want_grads: bool = True, stream=None):
+        """(loss [N], dh [N][D], dW [V][D]), the gradients None unless wanted: h [N][D] at any row stride, W [V][D], ids
+        int32 [N] (-1: no target), w [N] float32 or None."""
+        stream = self._launch(stream)
+        ldh = _rows("h", h, (self.N, self.D), self.tdt, self.device)
+        _full("W", W, (self.V, self.D), self.tdt, self.device)
+        _full("ids", ids, (self.N,), torch.int32, self.device)
+        _full("w", w, (self.N,), torch.float32, self.device)
+        want_grads = bool(want_grads)
+        ws_bytes = self.ws_bytes[want_grads]
+        ws = self._buffer("ws" if want_grads else "ws_loss", (ws_bytes,), torch.uint8, stream)
+        dh = self._buffer("dh", (self.N, self.D), self.tdt, stream) if want_grads else None
+        dW = self._buffer("dW", (self.V, self.D), self.tdt, stream) if want_grads else None
+        mdl_vocab_loss(self.N, self.D, self.V, self.x_dtype, h, ldh, W, ids, w, self.loss, dh, self.D, dW, ws, ws_bytes,
+                       stream)
+        return self.loss, dh, dW

@@ -649,13 +649,48 @@ int mdl_dropout(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx,
                 const uint64_t* rng, void* y, int64_t ldy, void* stream);
 
 /*
+ * Softmax cross entropy over a vocabulary from the hidden states and the class
+ * weights, with its gradients, without the logits in memory: over N rows of D
+ * channels and V classes,
+ *     z = h W^T,  loss[n] = w[n] (ln sum_c exp z_nc - z_n,ids[n])
+ *     G = w (softmax z - [c = id]),  dh = G W,  dW = G^T h     (gradients of sum loss)
+ * h: [N][D] of `dtype` at row stride ldh, any alignment of the element type; W: [V][D]
+ * without gaps (rows of a whole number of 16 bytes: 16-byte aligned), its rows the
+ * classes' weights; ids [N] int32; w [N] float32 (NULL: ones) weights a row in the
+ * loss. id -1 marks a row without a target. Such a row, and one of weight 0, counts
+ * for nothing, whatever h holds there: loss 0, no gradient. In any other row an id
+ * outside [0, V) gives loss NaN and no gradient (found on the device). A logit that
+ * is NaN or +inf makes its row's loss and gradient NaN (and all of dW, where the
+ * row enters), as a row of which all logits are -inf.
+ * dh [N][D] at row stride lddh and dW [V][D], of `dtype`, both or neither (NULL: the
+ * loss alone); with N = 0, dW alone is given and is zero. dh may be h itself; other
+ * overlaps of outputs with inputs are not allowed.
+ * Logits are float32 sums of the inputs' products and are not rounded; statistics
+ * and losses are float32. G's values are rounded to `dtype` before the products
+ * with W and h, whose sums are float32 and rounded once. The vocabulary is taken in
+ * pieces: the workspace holds one of G, and the logits are formed twice.
+ * ws: >= mdl_vocab_loss_workspace_size bytes (grads: whether dh and dW are wanted),
+ * 16-byte aligned, contents not kept.
+ * Errors: MDL_EINVAL for null tensors, N < 0, D, V < 1, a stride below D, an unknown
+ * dtype, dh without dW or dW without dh, dW over h, W or dh, dh over W, a misaligned
+ * W or workspace; MDL_EUNSUPPORTED for D above 65536 or V above 2^20; MDL_EOVERFLOW
+ * when rows times a stride reach 2^60 or a launch exceeds 2^31 threads (N or V times
+ * D, D rounded up to 256; N times V / 128); MDL_ESIZE for a short workspace.
+ */
+int mdl_vocab_loss_workspace_size(int64_t N, int32_t D, int32_t V, int32_t dtype, int32_t grads, size_t* bytes);
+int mdl_vocab_loss(int64_t N, int32_t D, int32_t V, int32_t dtype, const void* h, int64_t ldh, const void* W,
+                   const int32_t* ids, const float* w, float* loss, void* dh, int64_t lddh, void* dW, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/*
  * Kernel timing (measurement support). mdl_timing(1) makes every later launch
  * of a kernel group (names: "build_maps", "scatter", "zero_fill", "projection",
  * "fwd_wavefront", "dirsum_overlap" (on the library's own stream, concurrent with
  * "fwd_wavefront"), "dirsum", "bwd_wavefront", "wgrad_overlap" (on the library's
  * own stream, concurrent with "bwd_wavefront"), "wgrad", "conv_fwd", "conv_bwd",
  * "ctc_head", "scan_fwd", "scan_bwd", "scan_step", "norm_fwd", "norm_bwd",
- * "distill", "attn_fwd", "attn_bwd", "attn_step", "dropout")
+ * "distill", "attn_fwd", "attn_bwd", "attn_step", "dropout",
+ * "vocab_loss")
  * hand each of its dispatches a HIP event pair that the dispatch itself
  * records (hipExtLaunchKernel): the group's time runs from its first
  * dispatch's start to its last one's end, with no marker packets between

@@ -2,6 +2,7 @@
 
 * linear attention with a decay for each head over packed sequences and its gradients, one token at a time:
   S_t = d S_{t-1} + k_t v_t^T, y_t = scale S_t^T q_t;
+* softmax cross entropy over a vocabulary from hidden states and class weights, and its gradients, row by row;
 * dropout from Philox 4x32-10, one group of eight elements at a time, in Python's integers.
 
 Rows that no sequence holds come back as NaN: no caller may use them.
@@ -57,6 +58,27 @@ def attention_step(q, k, v, state, decay, scale):
     q, k, v, state = (np.asarray(a, np.float64) for a in (q, k, v, state))
     new = np.asarray(decay, np.float64)[:, None, None] * state + k[..., None] * v[..., None, :]
     return scale * (q[..., None] * new).sum(2), new
+
+
+def vocab_loss(h, W, ids, w=None):
+    """(loss [N], dh [N][D], dW [V][D], p [N][V]): rows with id -1 or weight 0 count for nothing (p = 0 there)."""
+    h, W = np.asarray(h, np.float64), np.asarray(W, np.float64)
+    N, V = h.shape[0], W.shape[0]
+    w = np.ones(N) if w is None else np.asarray(w, np.float64)
+    loss, dh, dW, ps = np.zeros(N), np.zeros(h.shape), np.zeros(W.shape), np.zeros((N, V))
+    for n in range(N):
+        if ids[n] == -1 or w[n] == 0:
+            continue
+        z = W @ h[n]
+        m = z.max()
+        e = np.exp(z - m)
+        ps[n] = e / e.sum()
+        loss[n] = w[n] * (m + np.log(e.sum()) - z[ids[n]])
+        g = w[n] * ps[n]
+        g[ids[n]] -= w[n]
+        dh[n] = g @ W
+        dW += np.outer(g, h[n])
+    return loss, dh, dW, ps
 
 
 _M32 = 0xFFFFFFFF

@@ -28,6 +28,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 #define MDL_LDS __attribute__((address_space(3)))
 
 // ---- operand tiles ----------------------------------------------------------------------------------------------
+constexpr uint32_t kOut = 0x80000000u;  // an offset past every buffer's end: the load gives zeros
 // ROWS rows (of the result) by 128 bytes of depth in LDS. ALONG: the operand's rows in memory run along the depth.
 template <typename T, int ROWS, int THREADS, bool ALONG>
 struct Tile {
@@ -36,61 +37,54 @@ struct Tile {
     static_assert(ROWS * 8 % THREADS == 0, "whole chunks a thread");
     const char* base;     // ALONG: row 0 at the depth of the next step; else the next step's first row
     int64_t ld;           // bytes
-    int rows, width;      // ALONG: rows of the tile that exist; else: bytes of a row that exist
+    int edge;             // ALONG: rows of the tile that exist; else: bytes of a row that exist
     int64_t depth;        // ALONG: bytes of depth that are left; else rows
     uint32_t off[per_thread];
+    int at;               // ALONG: this thread's chunks' place in the depth, bytes (the same for all of them)
 
     // row0: the tile's first row of the result, k0: first element of depth, k1: its end
     __device__ inline void init(const void* p, int64_t ld_elems, int64_t row0, int64_t n_rows, int64_t k0, int64_t k1) {
+        static_assert(!ALONG || THREADS % 64 == 0, "whole groups of eight rows between a thread's chunks");
         ld = ld_elems * E;
         if constexpr (ALONG) {
             base = static_cast<const char*>(p) + row0 * ld + k0 * E;
-            rows = (int)(n_rows - row0 < ROWS ? n_rows - row0 : ROWS);
-            width = 0;
+            edge = (int)(n_rows - row0 < ROWS ? n_rows - row0 : ROWS);
             depth = (k1 - k0) * E;
         } else {
             base = static_cast<const char*>(p) + k0 * ld + row0 * E;
-            rows = 0;
             const int64_t left = (n_rows - row0) * E;
-            width = (int)(left < row_bytes ? left : row_bytes);
+            edge = (int)(left < row_bytes ? left : row_bytes);
             depth = k1 - k0;
         }
+        at = 16 * (threadIdx.x % 8 ^ (threadIdx.x / 8 & 7));
 #pragma unroll
         for (int i = 0; i < per_thread; ++i) {
             const int q = i * THREADS + threadIdx.x, r = q / row_chunks, c = q % row_chunks;
-            if constexpr (ALONG) off[i] = (uint32_t)(r * ld) + 16 * (c ^ (r & 7));
-            else off[i] = (uint32_t)(r * ld) + 16 * (c ^ (E == 2 ? (r & 3) << 2 : (r >> 2 & 1) << 3));
+            if constexpr (ALONG) {
+                off[i] = (uint32_t)(r * ld) + at;
+            } else {
+                const int col = 16 * (c ^ (E == 2 ? (r & 3) << 2 : (r >> 2 & 1) << 3));
+                off[i] = col < edge ? (uint32_t)(r * ld) + col : kOut;
+            }
         }
     }
     // the next 128 bytes of depth into the LDS tile; zeros past the depth's end and the operand's edge. Chunks are whole:
     // the depth (ALONG) and the row's width (else) count in chunks of 16 bytes, of which the caller keeps the last one
     // readable and finite.
     __device__ inline void load(char* lds) {
-        constexpr uint32_t kOut = 0x80000000u;
-        const bool any = depth > 0;
-        int64_t records;
-        if constexpr (ALONG) records = any ? (rows - 1) * ld + (depth < 128 ? depth : 128) + 15 : 0;
-        else records = any ? ((depth < BK ? depth : BK) - 1) * ld + width + 15 : 0;
-        const __amdgpu_buffer_rsrc_t r = rsrc(base, records & ~int64_t(15));
-        const bool part = ALONG ? depth < 128 : width < row_bytes;
+        constexpr int64_t most = ALONG ? 128 : BK;
+        const int64_t now = depth < most ? (depth > 0 ? depth : 0) : most;
+        const int64_t records = ALONG ? (edge - 1) * ld + now : (now - 1) * ld + edge;
+        const __amdgpu_buffer_rsrc_t r = rsrc(base, now > 0 ? (records + 15) & ~int64_t(15) : 0);
+        const bool in = !ALONG || at < now;
 #pragma unroll
         for (int i = 0; i < per_thread; ++i) {
-            uint32_t o = off[i];
-            if (part) {
-                const int q = i * THREADS + threadIdx.x, row = q / row_chunks, c = q % row_chunks;
-                if constexpr (ALONG) o = 16 * (c ^ (row & 7)) < depth ? o : kOut;
-                else o = 16 * (c ^ (E == 2 ? (row & 3) << 2 : (row >> 2 & 1) << 3)) < width ? o : kOut;
-            }
             const int first = (i * THREADS + (int)(threadIdx.x & ~63u)) * 16;  // of the wave
+            const int o = (int)(in ? off[i] : kOut);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MDL_LDS void*)(lds + first), 16, o, 0, 0, 0);
         }
-        if constexpr (ALONG) {
-            base += 128;
-            depth -= 128;
-        } else {
-            base += BK * ld;
-            depth -= BK;
-        }
+        base += ALONG ? 128 : BK * ld;
+        depth -= most;
     }
     // this lane's part of the operand for 32 rows from row0 on, at 32 bytes of depth: 16 bytes of row lane % 32, the lower
     // half of the depth in the lower 32 lanes
@@ -146,6 +140,29 @@ struct Shape {  // waves down and across, 32 x 32 tiles of a wave down and acros
 typedef Shape<2, 4, 4, 2> Large;  // 256 x 256
 typedef Shape<2, 2, 2, 2> Small;  // 128 x 128
 
+// 128 bytes of depth of a wave's tiles: a quarter's operands are read while the products of the one before run
+template <typename S, typename TA, typename TB>
+__device__ inline void read_parts(const char* la, const char* lb, int wm, int wn, int s, u32x4 (&x)[S::TM], u32x4 (&y)[S::TN]) {
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) y[j] = TB::part(lb, wn + 32 * j, s);
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i) x[i] = TA::part(la, wm + 32 * i, s);
+}
+template <typename T, typename S, typename TA, typename TB>
+__device__ inline void one_step(const char* la, const char* lb, int wm, int wn, f32x16 (&c)[S::TM][S::TN]) {
+    u32x4 x[2][S::TM], y[2][S::TN];
+    read_parts<S, TA, TB>(la, lb, wm, wn, 0, x[0], y[0]);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        if (s < 3) read_parts<S, TA, TB>(la, lb, wm, wn, s + 1, x[(s + 1) & 1], y[(s + 1) & 1]);
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j) c[i][j] = mma<T>(y[s & 1][j], x[s & 1][i], c[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 struct Args {
     const void *a, *b;            // result rows and columns' operands
     int64_t lda, ldb, M, N, K;
@@ -200,33 +217,18 @@ __global__ __launch_bounds__(S::threads, 2) void product(const Args g) {
         for (int j = 0; j < S::TN; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) c[i][j][e] = 0.f;
-    const auto step = [&](const char* la, const char* lb) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            u32x4 x[S::TM], y[S::TN];
-#pragma unroll
-            for (int i = 0; i < S::TM; ++i) x[i] = TA::part(la, wm + 32 * i, s);
-#pragma unroll
-            for (int j = 0; j < S::TN; ++j) y[j] = TB::part(lb, wn + 32 * j, s);
-#pragma unroll
-            for (int i = 0; i < S::TM; ++i)
-#pragma unroll
-                for (int j = 0; j < S::TN; ++j) c[i][j] = mma<T>(y[j], x[i], c[i][j]);
-        }
-    };
     ta.load(a0);
     tb.load(b0);
     __syncthreads();
-    const int64_t steps = s1 - s0;
-    for (int64_t t = 0; t < steps; t += 2) {
+    // two steps a turn; behind the last one come zeros
+    for (int64_t t = s0; t < s1; t += 2) {
         ta.load(a1);
         tb.load(b1);
-        step(a0, b0);
+        one_step<T, S, TA, TB>(a0, b0, wm, wn, c);
         __syncthreads();
-        if (t + 1 >= steps) break;
         ta.load(a0);
         tb.load(b0);
-        step(a1, b1);
+        one_step<T, S, TA, TB>(a1, b1, wm, wn, c);
         __syncthreads();
     }
     // A lane holds row lane % 32 of each of its tiles, columns 8 (e / 4) + 4 h + e % 4.

@@ -270,45 +270,86 @@ __global__ __launch_bounds__(S::threads, 2) void product(const Args g) {
             g.stats[tn * g.M + m0 + row] = p;
         }
     } else {
+        if constexpr (EPI == kGrad) {
 #pragma unroll
-        for (int i = 0; i < S::TM; ++i) {
-            const int64_t m = m0 + wm + 32 * i + (lane & 31);
-            if (m >= g.M) continue;
-            float lse = 0.f, coef = 0.f;
-            int64_t id = -1;
-            if constexpr (EPI == kGrad) {
-                lse = g.lse[m];
-                coef = g.coef[m];
-                id = (int64_t)g.ids[m] - g.n_first - n0;
+            for (int i = 0; i < S::TM; ++i) {
+                const int64_t m = m0 + wm + 32 * i + (lane & 31);
+                const float lse = m < g.M ? g.lse[m] : 0.f, coef = m < g.M ? g.coef[m] : 0.f;
+                const int64_t id = m < g.M ? (int64_t)g.ids[m] - g.n_first - n0 : -1;
+#pragma unroll
+                for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int n = wn + 32 * j + 8 * (e >> 2) + 4 * h + (e & 3);
+                        const float p = exp_neg<T>(c[i][j][e] - lse) - (n == id ? 1.f : 0.f);
+                        c[i][j][e] = coef == 0.f || n0 + n >= g.N ? 0.f : coef * p;
+                    }
             }
+        }
+        if constexpr (sizeof(T) == 2 && EPI != kSlab) {
+            // Through LDS, so that whole lines leave: a quarter (half) of the tile's rows in each array, their 16-byte
+            // chunks rotated by the row.
+            constexpr int chunks = S::BN / 8;
+            static_assert(TA::bytes == 64 * S::BN * 2 && TB::bytes == TA::bytes, "64 rows an array");
+            const auto part = [&](int row) {
+                const int k = row >> 6;
+                return (k == 0 ? a0 : k == 1 ? b0 : k == 2 ? a1 : b1) + (row & 63) * (S::BN * 2);
+            };
 #pragma unroll
-            for (int j = 0; j < S::TN; ++j)
+            for (int i = 0; i < S::TM; ++i) {
+                const int row = wm + 32 * i + (lane & 31);
+                char* q = part(wm + 32 * i) + (lane & 31) * (S::BN * 2);
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const int n = wn + 32 * j + 2 * e + 4 * h;
-                    float v[4];
+                for (int j = 0; j < S::TN; ++j)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        v[r] = c[i][j][e + r];
-                        if constexpr (EPI == kGrad) {
-                            const float p = exp_neg<T>(v[r] - lse) - (n + r == id ? 1.f : 0.f);
-                            v[r] = coef == 0.f || n0 + n + r >= g.N ? 0.f : coef * p;
-                        }
+                    for (int e = 0; e < 16; e += 4) {
+                        const int n = wn + 32 * j + 2 * e;  // and 4 h
+                        const u32x2 v = {pack_bf16(c[i][j][e], c[i][j][e + 1]), pack_bf16(c[i][j][e + 2], c[i][j][e + 3])};
+                        *reinterpret_cast<u32x2*>(q + 16 * ((n >> 3) ^ (row & (chunks - 1))) + 8 * h) = v;
                     }
-                    if constexpr (EPI == kSlab) {
-                        float* o = g.slab + (split * g.M + m) * g.N + n0 + n;
+            }
+            __syncthreads();
+#pragma unroll 4
+            for (int q = threadIdx.x; q < S::BM * chunks; q += S::threads) {
+                const int row = q / chunks, ch = q % chunks;
+                const int64_t m = m0 + row, n = n0 + 8 * ch;
+                if (m >= g.M || n >= g.cols) continue;
+                const u32x4 v = *reinterpret_cast<const u32x4*>(part(row) + 16 * (ch ^ (row & (chunks - 1))));
+                T* o = static_cast<T*>(g.out) + m * g.ldo + n;
+                if (n + 8 <= g.cols) {
+                    *reinterpret_cast<u32x4_e*>(o) = v;
+                } else {
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (n0 + n + r < g.N) o[r] = g.add ? o[r] + v[r] : v[r];
-                    } else {
-                        T* o = static_cast<T*>(g.out) + m * g.ldo + n0 + n;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const float one[1] = {v[r]};
-                            if (n0 + n + r < g.cols) store_vec<1>(o + r, one);
-                        }
-                    }
+                    for (int r = 0; r < 8; ++r)
+                        if (n + r < g.cols) o[r].u = (uint16_t)(v[r >> 1] >> (16 * (r & 1)));
                 }
+            }
+        } else {
+            // fp32: four neighbours a lane
+            float* out = EPI == kSlab ? g.slab + split * g.M * g.N : reinterpret_cast<float*>(g.out);
+            const int64_t ldo = EPI == kSlab ? g.N : g.ldo, cols = EPI == kSlab ? g.N : g.cols;
+            const bool add = EPI == kSlab && g.add;
+#pragma unroll
+            for (int i = 0; i < S::TM; ++i) {
+                const int64_t m = m0 + wm + 32 * i + (lane & 31);
+                if (m >= g.M) continue;
+#pragma unroll
+                for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const int64_t n = n0 + wn + 32 * j + 2 * e + 4 * h;
+                        float* o = out + m * ldo + n;
+                        f32x4 v = {c[i][j][e], c[i][j][e + 1], c[i][j][e + 2], c[i][j][e + 3]};
+                        if (n + 4 <= cols) {
+                            if (add) v += *reinterpret_cast<const f32x4_e*>(o);
+                            *reinterpret_cast<f32x4_e*>(o) = v;
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (n + r < cols) o[r] = add ? o[r] + v[r] : v[r];
+                        }
+                    }
+            }
         }
     }
 }
@@ -358,19 +399,19 @@ __global__ __launch_bounds__(256) void pack(const T* src, int64_t ld, int64_t n,
     }
 }
 
-// A row's tiles joined, 32 rows by 8 groups of tiles a workgroup.
+// A row's tiles joined, 8 rows by 32 groups of tiles a workgroup.
 __global__ __launch_bounds__(256) void join(const float2* stats, int64_t tiles, int64_t N, const float* target_logit,
                                             const int32_t* target, const float* coef, float* lse, float* loss) {
-    __shared__ float2 part[8][32];
-    const int r = threadIdx.x & 31, grp = threadIdx.x >> 5;
-    const int64_t n = (int64_t)blockIdx.x * 32 + r;
+    __shared__ float2 part[32][8];
+    const int r = threadIdx.x & 7, grp = threadIdx.x >> 3;
+    const int64_t n = (int64_t)blockIdx.x * 8 + r;
     float2 p = make_float2(-INFINITY, 0.f);
     if (n < N)
-        for (int64_t t = grp; t < tiles; t += 8) p = joined(p, stats[t * N + n]);
+        for (int64_t t = grp; t < tiles; t += 32) p = joined(p, stats[t * N + n]);
     part[grp][r] = p;
     __syncthreads();
     if (grp != 0 || n >= N) return;
-    for (int i = 1; i < 8; ++i) p = joined(p, part[i][r]);
+    for (int i = 1; i < 32; ++i) p = joined(p, part[i][r]);
     const float l = p.x + logf(p.y);
     lse[n] = l;
     const int id = target[n];
@@ -385,15 +426,36 @@ __global__ __launch_bounds__(256) void clear(T* p, int64_t n) {
 }
 
 // out = sum of the slabs, in their order
+template <typename T, int V>
+__global__ __launch_bounds__(256) void sum_slabs(const float* slab, int slabs, int64_t M, int64_t N, T* out, int64_t ldo) {
+    const int64_t per = (N + V - 1) / V, i = (int64_t)blockIdx.x * 256 + threadIdx.x, m = i / per, n = i % per * V;
+    if (m >= M) return;
+    float v[V];
+#pragma unroll
+    for (int r = 0; r < V; ++r) v[r] = 0.f;
+    const float* p = slab + m * N + n;
+#pragma unroll 8
+    for (int s = 0; s < slabs; ++s) {
+        float x[V];
+        load_f32<V>(p + s * M * N, x);
+#pragma unroll
+        for (int r = 0; r < V; ++r) v[r] += x[r];
+    }
+    if constexpr (V == 1) {
+        store_vec<1>(out + m * ldo + n, v);
+    } else if constexpr (sizeof(T) == 4) {
+        store_vec<4>(out + m * ldo + n, v);
+    } else {
+        typedef u32x2 u32x2_e __attribute__((aligned(2), may_alias));
+        *reinterpret_cast<u32x2_e*>(out + m * ldo + n) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    }
+}
 template <typename T>
-__global__ __launch_bounds__(256) void sum_slabs(const float* slab, int64_t slabs, int64_t M, int64_t N, T* out,
-                                                 int64_t ldo) {
-    const int64_t per = (N + 255) / 256, m = blockIdx.x / per, n = blockIdx.x % per * 256 + threadIdx.x;
-    if (n >= N) return;
-    float v = 0.f;
-    for (int64_t s = 0; s < slabs; ++s) v += slab[(s * M + m) * N + n];
-    const float one[1] = {v};
-    store_vec<1>(out + m * ldo + n, one);
+void go_sum(const float* slab, int64_t slabs, int64_t M, int64_t N, T* out, int64_t ldo, hipStream_t st) {
+    const int V = N % 4 == 0 ? 4 : 1;
+    const dim3 grid((uint32_t)((M * (N / V) + 255) / 256));
+    if (V == 4) launch(sum_slabs<T, 4>, grid, dim3(256), 0, st, slab, slabs, M, N, out, ldo);
+    else launch(sum_slabs<T, 1>, grid, dim3(256), 0, st, slab, slabs, M, N, out, ldo);
 }
 
 // ---- plan ---------------------------------------------------------------------------------------------------------
@@ -404,11 +466,11 @@ bool large_tiles(int64_t M, int64_t N) {
     return ((M + 255) / 256) * ((N + 255) / 256) >= 192;
 }
 // how often the depth is split where there are few tiles: so that some 512 workgroups share the work, none with less than
-// eight steps of it
+// four steps of it
 int64_t splits_of(int64_t M, int64_t N, int64_t K, int e) {
     if (large_tiles(M, N)) return 1;
     const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128), steps = (K * e + 127) / 128;
-    return std::max<int64_t>(1, std::min<int64_t>({512 / tiles, steps / 8, int64_t(64)}));
+    return std::max<int64_t>(1, std::min<int64_t>({512 / tiles, steps / 4, int64_t(64)}));
 }
 
 }  // namespace
@@ -488,7 +550,7 @@ static hipError_t vocab_loss(const VocabArgs& x, int dtype, void* ws, hipStream_
         a.target = reinterpret_cast<float*>(w + p.target_logit);
         a.ids = target;
         go<T, true, true, kStats>(a, p.large, 1, st);
-        launch(join, dim3((uint32_t)((x.N + 31) / 32)), dim3(256), 0, st, a.stats, p.tiles, x.N, a.target, target, coef, lse,
+        launch(join, dim3((uint32_t)((x.N + 7) / 8)), dim3(256), 0, st, a.stats, p.tiles, x.N, a.target, target, coef, lse,
                x.loss);
     }
     if (!grads) return hipGetLastError();
@@ -548,15 +610,13 @@ static hipError_t vocab_loss(const VocabArgs& x, int dtype, void* ws, hipStream_
         const bool large = large_tiles(p.piece, x.D);
         if (p.dw_splits > 1) {
             go<T, false, false, kSlab>(c, large, p.dw_splits, st);
-            launch(sum_slabs<T>, dim3((uint32_t)(nv * ((x.D + 255) / 256))), dim3(256), 0, st, c.slab, p.dw_splits, nv,
-                   (int64_t)x.D, dW, (int64_t)x.D);
+            go_sum(c.slab, p.dw_splits, nv, x.D, dW, x.D, st);
         } else {
             go<T, false, false, kStore>(c, large, 1, st);
         }
     }
     if (p.dh_slab)
-        launch(sum_slabs<T>, dim3((uint32_t)(x.N * ((x.D + 255) / 256))), dim3(256), 0, st, dh_slab, p.dh_splits, x.N,
-               (int64_t)x.D, static_cast<T*>(x.dh), x.lddh);
+        go_sum(dh_slab, p.dh_splits, x.N, x.D, static_cast<T*>(x.dh), x.lddh, st);
     return hipGetLastError();
 }
 

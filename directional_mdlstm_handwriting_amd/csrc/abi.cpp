@@ -1305,6 +1305,11 @@ static int check_attn_sequences(const std::string& F, int32_t S, int64_t T, int3
         return fail(MDL_EOVERFLOW, F + ": S times the states exceeds 2^31 threads");
     return MDL_OK;
 }
+// as check_stride, for the kernels whose blocks of 64 rows keep their offsets in 31 bits
+static int check_stride23(const std::string& F, const char* name, int64_t rows, int64_t cols, int64_t ld) {
+    if (ld >= (int64_t(1) << 23)) return fail(MDL_EOVERFLOW, F + ": " + name + " reaches 2^23");
+    return check_stride(F, name, rows, cols, ld);
+}
 // whether `bytes` bytes at a and b share any
 static bool share_bytes(const void* a, const void* b, uint64_t bytes) {
     if (!a || !b) return false;
@@ -1337,8 +1342,8 @@ int mdl_linattn_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t H,
     if (rc || (rc = check_attn_sequences(F, S, T, H, Dk, Dv))) return rc;
     if (!seq_off || !decay || (T > 0 && (!q || !k || !v || !y))) return fail(MDL_EINVAL, F + ": null tensor");
     const int64_t nk = (int64_t)H * Dk, nv = (int64_t)H * Dv;
-    if ((rc = check_stride(F, "ldq", T, nk, ldq)) || (rc = check_stride(F, "ldk", T, nk, ldk)) ||
-        (rc = check_stride(F, "ldv", T, nv, ldv)) || (rc = check_stride(F, "ldy", T, nv, ldy)))
+    if ((rc = check_stride23(F, "ldq", T, nk, ldq)) || (rc = check_stride23(F, "ldk", T, nk, ldk)) ||
+        (rc = check_stride23(F, "ldv", T, nv, ldv)) || (rc = check_stride23(F, "ldy", T, nv, ldy)))
         return rc;
     if ((rc = check_ws(F, "mdl_linattn_workspace_size", need, ws, ws_bytes))) return rc;
     if (T > 0 && (rc = check_apart(F, {y, hT}, {q, k, v}))) return rc;
@@ -1386,10 +1391,10 @@ int mdl_linattn_backward(const int64_t* seq_off, int32_t S, int64_t T, int32_t H
     if (!seq_off || !decay || (T > 0 && (!q || !k || !v || !dy || !dq || !dk || !dv)))
         return fail(MDL_EINVAL, F + ": null tensor");
     const int64_t nk = (int64_t)H * Dk, nv = (int64_t)H * Dv;
-    if ((rc = check_stride(F, "ldq", T, nk, ldq)) || (rc = check_stride(F, "ldk", T, nk, ldk)) ||
-        (rc = check_stride(F, "ldv", T, nv, ldv)) || (rc = check_stride(F, "lddy", T, nv, lddy)) ||
-        (rc = check_stride(F, "lddq", T, nk, lddq)) || (rc = check_stride(F, "lddk", T, nk, lddk)) ||
-        (rc = check_stride(F, "lddv", T, nv, lddv)))
+    if ((rc = check_stride23(F, "ldq", T, nk, ldq)) || (rc = check_stride23(F, "ldk", T, nk, ldk)) ||
+        (rc = check_stride23(F, "ldv", T, nv, ldv)) || (rc = check_stride23(F, "lddy", T, nv, lddy)) ||
+        (rc = check_stride23(F, "lddq", T, nk, lddq)) || (rc = check_stride23(F, "lddk", T, nk, lddk)) ||
+        (rc = check_stride23(F, "lddv", T, nv, lddv)))
         return rc;
     if ((rc = check_ws(F, "mdl_linattn_workspace_size", need, ws, ws_bytes))) return rc;
     if (T > 0 && (rc = check_apart(F, {dq, dk, dv}, {q, k, v, dy}))) return rc;

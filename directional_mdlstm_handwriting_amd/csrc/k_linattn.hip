@@ -150,41 +150,64 @@ __device__ inline bool piece_of(const Args& a, int s, int64_t t0, int64_t t1, Pi
 
 // ---- blocks of rows ---------------------------------------------------------------------------------------------
 // n rows of d elements from `first` on in scan order, staged in registers and then laid as an LDS tile of C x D, zero
-// outside: what lies behind a sequence or beside a head never meets a product.
+// outside: what lies behind a sequence or beside a head never meets a product. Every lane loads, without a branch: past the
+// rows the last one, which is laid as zeros, past the row its last 16 bytes, which end with it and are laid there again;
+// the columns past d stay as `zero_fill` left them. Heads of less than 16 bytes go element by element.
 template <typename T, int D>
 struct Rows {
+    typedef typename Op<T>::lds_t E;
     static constexpr int V = Width<T>::v, per = D / V, C = Op<T>::C, n_vec = C * per / kThreads;
     static constexpr int stride = D + 16 / sizeof(T);
     static_assert(n_vec >= 1 && C * per % kThreads == 0, "whole vectors a thread");
     u32x4 q[n_vec];
+    // ld: bytes, below 2^25, so that a block's offsets have 31 bits
     __device__ inline void load(const T* base, int64_t ld, int64_t first, int dir, int n, int d) {
+        const char* low = reinterpret_cast<const char*>(base) + (dir > 0 ? first : first - (n - 1)) * ld;
+        const int col = (int)(threadIdx.x % per) * V, c0 = d < V ? 0 : min(col, d - V);
 #pragma unroll
         for (int i = 0; i < n_vec; ++i) {
-            const int v = i * kThreads + threadIdx.x, r = v / per, c = v % per * V;
-            q[i] = u32x4{0, 0, 0, 0};
-            if (r < n && c < d) {
-                const T* p = base + (first + (int64_t)dir * r) * ld + c;
-                if (c + V <= d) {
-                    q[i] = *reinterpret_cast<const u32x4_e*>(p);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        if (c + e >= d) continue;
-                        if constexpr (sizeof(T) == 2) q[i][e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
-                        else q[i][e] = reinterpret_cast<const uint32_t*>(p)[e];
+            const int r = min((i * kThreads + (int)threadIdx.x) / per, n - 1);
+            const uint32_t o = (uint32_t)(dir > 0 ? r : n - 1 - r) * (uint32_t)ld + (uint32_t)(c0 * sizeof(T));
+            if (d >= V) {
+                q[i] = *reinterpret_cast<const u32x4_e*>(low + o);
+            } else {
+                q[i] = u32x4{0, 0, 0, 0};
+                if (col == 0)
+                    for (int e = 0; e < d; ++e) {
+                        if constexpr (sizeof(T) == 2) {
+                            const uint32_t v = *reinterpret_cast<const uint16_t*>(low + o + 2 * e);
+                            q[i][e >> 1] |= v << (16 * (e & 1));
+                        } else {
+                            q[i][e] = *reinterpret_cast<const uint32_t*>(low + o + 4 * e);
+                        }
                     }
+            }
+        }
+    }
+    __device__ inline void lay(E* t, int n, int d) const {
+        const int col = (int)(threadIdx.x % per) * V;
+#pragma unroll
+        for (int i = 0; i < n_vec; ++i) {
+            const int r = (i * kThreads + (int)threadIdx.x) / per;
+            const bool in = r < n;
+            const u32x4 v = {in ? q[i][0] : 0, in ? q[i][1] : 0, in ? q[i][2] : 0, in ? q[i][3] : 0};
+            if (col + V <= d || (d < V && col == 0)) {
+                *reinterpret_cast<u32x4*>(t + r * stride + col) = v;
+            } else if (col < d) {
+                E* p = t + r * stride + d - V;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    if constexpr (sizeof(T) == 2) p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+                    else p[e] = __uint_as_float(v[e]);
                 }
             }
         }
     }
-    __device__ inline void lay(typename Op<T>::lds_t* t) const {
-#pragma unroll
-        for (int i = 0; i < n_vec; ++i) {
-            const int v = i * kThreads + threadIdx.x, r = v / per, c = v % per * V;
-            *reinterpret_cast<u32x4*>(t + r * stride + c) = q[i];
-        }
-    }
 };
+template <typename E>
+__device__ inline void zero_fill(E* t, int n) {
+    for (int i = threadIdx.x; i < n; i += kThreads) t[i] = 0;
+}
 
 // ---- states -----------------------------------------------------------------------------------------------------
 // A wave holds DC / 4 columns of the state: result tiles of 16 x 16, rows 16 t + 4 g + r, column lane % 16.
@@ -204,26 +227,41 @@ struct State {
 #pragma unroll
             for (int u = 0; u < NT; ++u) x[t][u] *= f;
     }
-    // f(value, element of the stored state) returns the value to keep
-    template <typename F>
-    __device__ inline void each(const Args& a, F f) {
-        const int lane = threadIdx.x & 63, g = lane >> 4, n0 = (threadIdx.x >> 6) * (DC / 4) + (lane & 15);
+    // (the lane is taken as new at each call: the elements' places, alike for all pieces, would otherwise be kept in
+    // registers throughout)
+    __device__ inline void load(const Args& a, const float* p) {
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        const int g = lane >> 4, n0 = (threadIdx.x >> 6) * (DC / 4) + (lane & 15);
+        const int sm = a.trans ? 1 : a.dc, sn = a.trans ? a.da : 1;
 #pragma unroll
-        for (int t = 0; t < AT; ++t)
+        for (int t = 0; t < AT; ++t) {
 #pragma unroll
             for (int u = 0; u < NT; ++u)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int m = 16 * t + 4 * g + r, n = n0 + 16 * u;
-                    if (m < a.da && n < a.dc) x[t][u][r] = f(x[t][u][r], a.trans ? n * a.da + m : m * a.dc + n);
+                    const float v = p[(uint32_t)(min(m, a.da - 1) * sm + min(n, a.dc - 1) * sn)];
+                    x[t][u][r] = m < a.da && n < a.dc ? v : 0.f;
                 }
+            if (t & 1) one_at_a_time();
+        }
     }
-    __device__ inline void load(const Args& a, const float* p) {
-        clear();
-        each(a, [&](float, int e) { return p[e]; });
-    }
-    __device__ inline void store(const Args& a, float* p) {
-        each(a, [&](float v, int e) { return p[e] = v; });
+    __device__ inline void store(const Args& a, float* p) const {
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        const int g = lane >> 4, n0 = (threadIdx.x >> 6) * (DC / 4) + (lane & 15);
+#pragma unroll
+        for (int t = 0; t < AT; ++t) {
+#pragma unroll
+            for (int u = 0; u < NT; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int m = 16 * t + 4 * g + r, n = n0 + 16 * u;
+                    if (m < a.da && n < a.dc) p[(uint32_t)(m * a.dc + n)] = x[t][u][r];
+                }
+            one_at_a_time();
+        }
     }
 };
 
@@ -261,13 +299,20 @@ __device__ inline void add_block(State<DA, DC>& s, const typename Op<T>::lds_t* 
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p) s.x[m][u] = O::mma2(s.x[m][u], b0, b1, w[p][t][u], w[p][t + 1][u]);
         }
+        if (m & 1) one_at_a_time();
     }
 }
 
 // What each piece adds to its sequence's state. bfloat16: w c is split into three terms (24 bits, as fp32 has), so that
 // the states are sums of fp32 products.
+// workgroups a compute unit: the narrow heads' registers allow four
+template <int DA, int DC>
+constexpr int waves_of() {
+    return DA + DC <= 128 ? 4 : 2;
+}
+
 template <typename T, int DA, int DC>
-__global__ __launch_bounds__(kThreads, 2) void states(const Args a) {
+__global__ __launch_bounds__(kThreads, (waves_of<DA, DC>())) void states(const Args a) {
     typedef Op<T> O;
     constexpr int C = O::C, PARTS = sizeof(T) == 2 ? 3 : 1;
     __shared__ alignas(16) typename O::lds_t lb[C * Rows<T, DA>::stride], lc[C * Rows<T, DC>::stride];
@@ -276,7 +321,10 @@ __global__ __launch_bounds__(kThreads, 2) void states(const Args a) {
     const float l2 = log2_of(a.decay[h]);
     const T* pb = static_cast<const T*>(a.b) + (int64_t)h * a.da;
     const T* pc = static_cast<const T*>(a.c) + (int64_t)h * a.dc;
+    const int64_t ldb = a.ldb * (int64_t)sizeof(T), ldc = a.ldc * (int64_t)sizeof(T);
     const int64_t size = (int64_t)a.da * a.dc;
+    zero_fill(lb, C * Rows<T, DA>::stride);
+    zero_fill(lc, C * Rows<T, DC>::stride);
     for (int s = first_past(a.off, a.S, t0); s < a.S; ++s) {
         if (a.off[s] >= t1) break;
         Piece p;
@@ -288,16 +336,16 @@ __global__ __launch_bounds__(kThreads, 2) void states(const Args a) {
         const int64_t from = a.dir > 0 ? p.begin : p.end - 1;
         Rows<T, DA> rb;
         Rows<T, DC> rc;
-        rb.load(pb, a.ldb, from, a.dir, (int)min((int64_t)C, len), a.da);
-        rc.load(pc, a.ldc, from, a.dir, (int)min((int64_t)C, len), a.dc);
+        rb.load(pb, ldb, from, a.dir, (int)min((int64_t)C, len), a.da);
+        rc.load(pc, ldc, from, a.dir, (int)min((int64_t)C, len), a.dc);
         for (int64_t k = 0; k < len; k += C) {
             const int n = (int)min((int64_t)C, len - k);
             __syncthreads();
-            rb.lay(lb);
-            rc.lay(lc);
+            rb.lay(lb, n, a.da);
+            rc.lay(lc, n, a.dc);
             if (k + C < len) {
-                rb.load(pb, a.ldb, from + a.dir * (k + C), a.dir, (int)min((int64_t)C, len - k - C), a.da);
-                rc.load(pc, a.ldc, from + a.dir * (k + C), a.dir, (int)min((int64_t)C, len - k - C), a.dc);
+                rb.load(pb, ldb, from + a.dir * (k + C), a.dir, (int)min((int64_t)C, len - k - C), a.da);
+                rc.load(pc, ldc, from + a.dir * (k + C), a.dir, (int)min((int64_t)C, len - k - C), a.dc);
             }
             __syncthreads();
             if (k > 0) x.scale(power(l2, n));
@@ -324,18 +372,30 @@ __global__ __launch_bounds__(kThreads) void chain(const Args a, int blocks_per_h
         return;
     }
     const int64_t first = o0 / a.L, end = (o1 - 1) / a.L;
-    const float l2 = log2_of(a.decay[h]);
-    for (int64_t i = first; i < end; ++i) {
-        const int64_t t = a.dir > 0 ? i : end - (i - first);     // the tile that is left
-        const int64_t lo = max(o0, t * a.L), hi = min(o1, t * a.L + a.L);
-        float* p = a.slots + ((a.dir > 0 ? t : t - 1) * a.H + h) * size + e;
-        x = __builtin_fmaf(x, power(l2, (int)(hi - lo)), *p);
-        *p = x;
+    const float l2 = log2_of(a.decay[h]), whole = power(l2, a.L);
+    const int64_t hop = (int64_t)a.H * size;
+    // boundaries in scan order; all tiles but the first and last are whole
+    const int64_t n_first = (a.dir > 0 ? min(o1, (first + 1) * a.L) - o0 : o1 - max(o0, end * a.L));
+    float* p = a.slots + ((a.dir > 0 ? first : end - 1) * a.H + h) * size + e;
+    float f = power(l2, (int)n_first);
+    constexpr int U = 8;
+    for (int64_t i = first; i < end; i += U) {
+        float v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u < end) v[u] = p[a.dir * u * hop];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u < end) {
+                x = __builtin_fmaf(x, f, v[u]);
+                p[a.dir * u * hop] = x;
+                f = whole;
+            }
+        p += a.dir * U * hop;
     }
     if (a.last) {
-        const int64_t t = a.dir > 0 ? end : first;
-        const int64_t lo = max(o0, t * a.L), hi = min(o1, t * a.L + a.L);
-        a.last[at] = __builtin_fmaf(x, power(l2, (int)(hi - lo)), a.last[at]);
+        const int64_t n_last = a.dir > 0 ? o1 - max(o0, end * a.L) : min(o1, (first + 1) * a.L) - o0;
+        a.last[at] = __builtin_fmaf(x, power(l2, (int)n_last), a.last[at]);
     }
 }
 
@@ -363,7 +423,7 @@ __device__ inline void store_quad(T* p, f32x4 v, int n) {
 // (two terms there); each is half a step of values that reach the output as a sum with its own half step. Sums and states
 // are fp32.
 template <typename T, int DA, int DC>
-__global__ __launch_bounds__(kThreads, 2) void outputs(const Args a) {
+__global__ __launch_bounds__(kThreads, (waves_of<DA, DC>())) void outputs(const Args a) {
     typedef Op<T> O;
     typedef typename O::Quad Quad;
     constexpr int C = O::C, CT = C / 16, PARTS = sizeof(T) == 2 ? 2 : 1, NT = DC / 64;
@@ -375,10 +435,15 @@ __global__ __launch_bounds__(kThreads, 2) void outputs(const Args a) {
     const int h = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
     const float l2 = log2_of(a.decay[h]);
     const T* pa = static_cast<const T*>(a.a) + (int64_t)h * a.da;
+    const int64_t lda = a.lda * (int64_t)sizeof(T);
     const T* pb = static_cast<const T*>(a.b) + (int64_t)h * a.da;
     const T* pc = static_cast<const T*>(a.c) + (int64_t)h * a.dc;
-    T* po = static_cast<T*>(a.out) + (int64_t)h * a.dc;
+    const int64_t ldb = a.ldb * (int64_t)sizeof(T), ldc = a.ldc * (int64_t)sizeof(T);
+    char* po = reinterpret_cast<char*>(static_cast<T*>(a.out) + (int64_t)h * a.dc);
     const int64_t size = (int64_t)a.da * a.dc;
+    const int64_t ldo = a.ldo * (int64_t)sizeof(T);
+    const bool whole = a.dc % 4 == 0;
+    zero_fill(la, 2 * C * sa + C * sc);
     for (int s = first_past(a.off, a.S, t0); s < a.S; ++s) {
         if (a.off[s] >= t1) break;
         Piece p;
@@ -387,35 +452,43 @@ __global__ __launch_bounds__(kThreads, 2) void outputs(const Args a) {
         Rows<T, DA> ra, rb;
         Rows<T, DC> rc;
         const int n0 = (int)min((int64_t)C, len);
-        ra.load(pa, a.lda, from, a.dir, n0, a.da);
-        rb.load(pb, a.ldb, from, a.dir, n0, a.da);
-        rc.load(pc, a.ldc, from, a.dir, n0, a.dc);
+        ra.load(pa, lda, from, a.dir, n0, a.da);
+        rb.load(pb, ldb, from, a.dir, n0, a.da);
+        rc.load(pc, ldc, from, a.dir, n0, a.dc);
         State<DA, DC> x;
-        bool zero = false;
-        if (p.enters) x.load(a, a.slots + ((a.dir > 0 ? tile - 1 : tile) * a.H + h) * size);
-        else if (a.init) x.load(a, a.init + ((int64_t)s * a.H + h) * size);
-        else {
-            x.clear();
-            zero = true;
-        }
+        const float* enter = p.enters ? a.slots + ((a.dir > 0 ? tile - 1 : tile) * a.H + h) * size
+                             : a.init ? a.init + ((int64_t)s * a.H + h) * size : nullptr;
+        const bool zero = enter == nullptr;
+        if (zero) x.clear();
+        else x.load(a, enter);
         for (int64_t k = 0; k < len; k += C) {
             const int n = (int)min((int64_t)C, len - k);
             __syncthreads();
-            ra.lay(la);
-            rb.lay(lb);
-            rc.lay(lc);
+            ra.lay(la, n, a.da);
+            rb.lay(lb, n, a.da);
+            rc.lay(lc, n, a.dc);
             if (k + C < len) {
                 const int nn = (int)min((int64_t)C, len - k - C);
                 const int64_t f = from + a.dir * (k + C);
-                ra.load(pa, a.lda, f, a.dir, nn, a.da);
-                rb.load(pb, a.ldb, f, a.dir, nn, a.da);
-                rc.load(pc, a.ldc, f, a.dir, nn, a.dc);
+                ra.load(pa, lda, f, a.dir, nn, a.da);
+                rb.load(pb, ldb, f, a.dir, nn, a.da);
+                rc.load(pc, ldc, f, a.dir, nn, a.dc);
             }
             __syncthreads();
-            // (a_i . b_j) d^{i-j}: tiles of 16 x 16 dealt out to the waves, row i at lane % 16, j at 4 g + r
-            for (int t = wave; t < CT * CT; t += 4) {
-                const int it = t / CT, jt = t % CT;
-                if (jt > it) continue;
+            // (a_i . b_j) d^{i-j}: the tiles of 16 x 16 on and below the diagonal, the lowest rows first, dealt out to the
+            // waves; row i at lane % 16, j at 4 g + r
+            constexpr int kPairs = CT * (CT + 1) / 2;
+#pragma unroll
+            for (int k0 = 0; k0 < kPairs; k0 += 4) {
+                const int pair = k0 + wave;
+                if (pair >= kPairs) break;
+                int it = CT - 1, jt = pair;
+#pragma unroll
+                for (int q = CT; q > 1; --q)
+                    if (it == q - 1 && jt >= q) {
+                        jt -= q;
+                        --it;
+                    }
                 f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int m = 0; m < DA; m += 32)
@@ -429,6 +502,7 @@ __global__ __launch_bounds__(kThreads, 2) void outputs(const Args a) {
                 *reinterpret_cast<Quad*>(lp + (16 * it + i) * sp + 16 * jt + 4 * g) = O::make(v);
             }
             __syncthreads();
+            one_at_a_time();
             // outputs: row i at lane % 16, columns 4 g + r of the wave's tiles
             f32x4 o[CT][NT];
 #pragma unroll
@@ -450,6 +524,7 @@ __global__ __launch_bounds__(kThreads, 2) void outputs(const Args a) {
 #pragma unroll
                         for (int u = 0; u < NT; ++u) o[it][u] = O::mma2(o[it][u], x0[u], x1[u], a0, a1);
                     }
+                    one_at_a_time();
                 }
 #pragma unroll
                 for (int it = 0; it < CT; ++it) {
@@ -476,16 +551,17 @@ __global__ __launch_bounds__(kThreads, 2) void outputs(const Args a) {
 #pragma unroll
                     for (int u = 0; u < NT; ++u) o[it][u] = O::mma2(o[it][u], c0[u], c1[u], p0, p1);
                 }
+                one_at_a_time();
             }
 #pragma unroll
             for (int it = 0; it < CT; ++it) {
                 const int row = 16 * it + i;
                 if (row >= n) continue;
-                T* q = po + (from + (int64_t)a.dir * (k + row)) * a.ldo;
+                char* q = po + (from + (int64_t)a.dir * k) * ldo + (int64_t)(a.dir * row) * ldo;
 #pragma unroll
                 for (int u = 0; u < NT; ++u) {
                     const int col = wave * (DC / 4) + 16 * u + 4 * g;
-                    if (col < a.dc) store_quad<T>(q + col, o[it][u] * a.oscale, a.dc - col);
+                    if (col < a.dc) store_quad<T>(reinterpret_cast<T*>(q) + col, o[it][u] * a.oscale, whole ? 4 : a.dc - col);
                 }
             }
             if (k + C < len) {

@@ -604,7 +604,8 @@ int mdl_distill(int64_t N, int32_t V, int32_t k, int32_t dtype, const void* z, i
  * row, an unknown dtype, outputs over inputs as above, n_slots < 1, slots NULL with
  * n_slots < S, or a misaligned workspace; MDL_EUNSUPPORTED for Dk or Dv above 128
  * or H above 65535; MDL_ESIZE for a short workspace; MDL_EOVERFLOW when T reaches
- * 2^36, rows times a stride 2^60, S 2^31 - 64, or a launch 2^31 threads (a sequence,
+ * 2^36, rows times a stride 2^60, a stride of the forward or backward 2^23, S
+ * 2^31 - 64, or a launch 2^31 threads (a sequence,
  * or a row of a step, takes 256 threads a head, and as many more for each 256
  * elements of a sequence's state). With T = 0 the token tensors may be NULL.
  */

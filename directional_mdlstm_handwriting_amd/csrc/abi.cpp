@@ -1292,17 +1292,16 @@ static int check_attn(const std::string& F, int64_t T, int32_t H, int32_t Dk, in
         return fail(MDL_EUNSUPPORTED, F + ": Dk or Dv above " + std::to_string(mdl::linattn_max_d()));
     if (H > 65535) return fail(MDL_EUNSUPPORTED, F + ": H above 65535");
     if (T >= (int64_t(1) << 36)) return fail(MDL_EOVERFLOW, F + ": T reaches 2^36");
-    const mdl::AttnPlan p = mdl::attn_plan(T, H, Dk, Dv);
-    if (p.ntiles > mdl::kMaxLaunchThreads / 256) return fail(MDL_EOVERFLOW, F + ": the launch exceeds 2^31 threads");
-    need = p.total;
+    need = mdl::attn_plan(T, H, Dk, Dv).total;
     return MDL_OK;
 }
 // the sequences of a call whose states are walked: a launch over S times the states' elements
 static int check_attn_sequences(const std::string& F, int32_t S, int64_t T, int32_t H, int32_t Dk, int32_t Dv) {
     int rc = check_sequences(F, S);
     if (rc) return rc;
-    if (S > mdl::kMaxLaunchThreads / 256 / mdl::attn_plan(T, H, Dk, Dv).chain_blocks)
-        return fail(MDL_EOVERFLOW, F + ": S times the states exceeds 2^31 threads");
+    const mdl::AttnPlan p = mdl::attn_plan(T, H, Dk, Dv);
+    if (S > mdl::kMaxLaunchThreads / 256 / p.chain_blocks || (T >> p.log_l) + S > mdl::kMaxLaunchThreads / 256 / H)
+        return fail(MDL_EOVERFLOW, F + ": the launch exceeds 2^31 threads");
     return MDL_OK;
 }
 // as check_stride, for the kernels whose blocks of 64 rows keep their offsets in 31 bits

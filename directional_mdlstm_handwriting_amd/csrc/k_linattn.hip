@@ -8,11 +8,14 @@
 //     out_i = sum_{j <= i} d^{i-j} (a_i . b_j) c_j + d^{i+1} a_i^T E,   E' = d^n E + sum_j d^{n-1-j} b_j c_j^T
 // (one power less on E and one more on E' where the entering state is that of the token itself: the gradients).
 //
-// Tokens are tiled evenly in tiles of L, whatever the sequences; a piece is what a tile holds of a sequence. Three
-// launches: `states` forms what each piece adds to the state (written for a piece whose sequence goes on past its tile to
-// the slot of that boundary, for one that ends in it to the last states), `chain` walks each sequence's boundaries and
-// leaves in each slot the state that enters the next tile, `outputs` walks the pieces block by block. No tile waits for
-// another. The slots of the forward stand in the workspace for the backward's dq.
+// Sequences are cut into tiles of L tokens, each taken by a workgroup a head. Three launches: `states` forms what each tile
+// adds to the state (to the slot of its boundary with the next tile in scan order, or to the last states), `chain` walks each
+// sequence's boundaries and leaves in each slot the state that enters the tile behind it, `outputs` walks the tiles block by
+// block. No tile waits for another. The slots of the forward stand in the workspace for the backward's dq.
+//
+// Which tile a workgroup has follows from the offsets alone, with nothing summed over the sequences: sequence s owns the
+// numbers from off[s] / L + s on, which are at least as many as its tiles (those behind them have nothing to do), and its
+// boundaries the slots from off[s] / L on, which are as many as it can need; T / L + S numbers and T / L slots in all.
 #include "kernels.h"
 #include "seqio.h"
 
@@ -37,7 +40,7 @@ template <>
 struct Op<bf16> {
     typedef uint16_t lds_t;
     typedef u32x2 Quad;
-    static constexpr int C = 64;  // tokens a block
+    static constexpr int C = 32;  // tokens a block
     static __device__ inline Quad make(f32x4 v) { return Quad{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}; }
     static __device__ inline f32x4 values(Quad q) {
         return f32x4{__uint_as_float(q[0] << 16), __uint_as_float(q[0] & 0xffff0000u), __uint_as_float(q[1] << 16),
@@ -88,15 +91,52 @@ __device__ inline float log2_of(float d) { return (float)log2((double)d); }
 // d^e for whole e >= 0, from log2 d: d^0 is 1 also for d = 0
 __device__ inline float power(float l2, int e) { return e == 0 ? 1.f : __builtin_amdgcn_exp2f((float)e * l2); }
 
-// ---- pieces -----------------------------------------------------------------------------------------------------
-// The first of the S sequences whose end lies beyond t (S if none), 64 probes at a time, alike in every wave.
-__device__ inline int first_past(const int64_t* off, int S, int64_t t) {
-    int lo = 0, hi = S;
+// a value that all lanes share, in a scalar register
+__device__ inline float uniform(float x) {
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+
+// What a kernel of this file works on.
+struct Args {
+    const int64_t* off;
+    int S, H;
+    int64_t T;
+    int log_l;                 // log2 of the tokens a tile, L
+    int dir;                   // +1: tokens ascending, -1: descending
+    int post;                  // 1: the entering state is the previous token's; 0: it is the token's own
+    const void *a, *b, *c;     // [T][H][da or dc] at row strides
+    int64_t lda, ldb, ldc;
+    int da, dc, trans;         // states are stored [da][dc], or [dc][da]
+    const float* decay;
+    float pscale, sscale, oscale;  // of a . b, of b c^T in the state, of the output
+    float* slots;              // [T / L][H][da][dc], a tile boundary's state
+    const float* init;         // [S][H][da][dc] or null
+    float* last;               // [S][H][da][dc] or null
+    void* out;                 // [T][H][dc]
+    int64_t ldo;
+};
+
+// offsets that leave [0, T] end there: whatever they hold, no tile leaves the tensors or the slots
+__device__ inline int64_t offset(const Args& a, int64_t s) {
+    const int64_t o = a.off[s];
+    return o < 0 ? 0 : (o > a.T ? a.T : o);
+}
+
+struct Tile {
+    int seq;                   // -1: nothing to do
+    int len;
+    int64_t from;              // first token in scan order
+    int64_t enter, leave;      // slots, or -1 where the sequence begins or ends with the tile
+};
+// The tile with this number: its sequence is the last one whose numbers begin no later (64 probes at a time, alike in every
+// wave).
+__device__ inline Tile tile_of(const Args& a, int64_t number) {
+    int lo = 0, hi = a.S;
     const int lane = threadIdx.x & 63;
     while (lo < hi) {
         const int step = (int)(((int64_t)(hi - lo) + 63) / 64);
         const int64_t p = lo + (int64_t)lane * step;
-        const uint64_t m = __ballot(p < hi && off[p + 1] > t);
+        const uint64_t m = __ballot(p < hi && (offset(a, p) >> a.log_l) + p > number);
         if (m == 0) {
             lo += ((hi - lo - 1) / step) * step + 1;
         } else {
@@ -105,47 +145,19 @@ __device__ inline int first_past(const int64_t* off, int S, int64_t t) {
             if (f > 0) lo += (f - 1) * step + 1;
         }
     }
-    return lo;
-}
-
-// What a kernel of this file works on.
-struct Args {
-    const int64_t* off;
-    int S, H;
-    int64_t T;
-    int L;                     // tokens a tile
-    int64_t ntiles;
-    int dir;                   // +1: tokens ascending, -1: descending
-    int post;                  // 1: the entering state is the previous token's; 0: it is the token's own
-    const void *a, *b, *c;     // [T][H][da or dc] at row strides
-    int64_t lda, ldb, ldc;
-    int da, dc, trans;         // states are stored [da][dc], or [dc][da]
-    const float* decay;
-    float pscale, sscale, oscale;  // of a . b, of b c^T in the state, of the output
-    float* slots;              // [ntiles - 1][H][da][dc], a tile boundary's state
-    const float* init;         // [S][H][da][dc] or null
-    float* last;               // [S][H][da][dc] or null
-    void* out;                 // [T][H][dc]
-    int64_t ldo;
-};
-
-struct Piece {
-    int64_t begin, end;        // tokens
-    bool enters, leaves;       // in scan order: the sequence began, goes on in another tile
-};
-// offsets that leave [0, T] end there: a sequence enters or leaves a tile only where there is a tile to go to
-__device__ inline int64_t offset(const Args& a, int64_t s) {
-    const int64_t o = a.off[s];
-    return o < 0 ? 0 : (o > a.T ? a.T : o);
-}
-__device__ inline bool piece_of(const Args& a, int s, int64_t t0, int64_t t1, Piece& p) {
-    const int64_t o0 = offset(a, s), o1 = offset(a, (int64_t)s + 1);
-    p.begin = o0 > t0 ? o0 : t0;
-    p.end = o1 < t1 ? o1 : t1;
-    const bool before = o0 < t0, after = o1 > t1;
-    p.enters = a.dir > 0 ? before : after;
-    p.leaves = a.dir > 0 ? after : before;
-    return p.begin < p.end;
+    Tile t;
+    t.seq = lo - 1;
+    if (t.seq < 0) return t;
+    const int64_t o0 = offset(a, t.seq), o1 = offset(a, (int64_t)t.seq + 1), L = int64_t(1) << a.log_l;
+    const int64_t slot = number - t.seq, begin = o0 + ((slot - (o0 >> a.log_l)) << a.log_l);
+    if (begin >= o1) t.seq = -1;
+    const int64_t end = begin + L < o1 ? begin + L : o1;
+    const int64_t before = begin > o0 ? slot - 1 : -1, after = end < o1 ? slot : -1;
+    t.len = (int)(end - begin);
+    t.from = a.dir > 0 ? begin : end - 1;
+    t.enter = a.dir > 0 ? before : after;
+    t.leave = a.dir > 0 ? after : before;
+    return t;
 }
 
 // ---- blocks of rows ---------------------------------------------------------------------------------------------
@@ -153,11 +165,11 @@ __device__ inline bool piece_of(const Args& a, int s, int64_t t0, int64_t t1, Pi
 // outside: what lies behind a sequence or beside a head never meets a product. Every lane loads, without a branch: past the
 // rows the last one, which is laid as zeros, past the row its last 16 bytes, which end with it and are laid there again;
 // the columns past d stay as `zero_fill` left them. Heads of less than 16 bytes go element by element.
-template <typename T, int D>
+template <typename T, int D, int PAD>
 struct Rows {
     typedef typename Op<T>::lds_t E;
     static constexpr int V = Width<T>::v, per = D / V, C = Op<T>::C, n_vec = C * per / kThreads;
-    static constexpr int stride = D + 16 / sizeof(T);
+    static constexpr int stride = D + PAD / (int)sizeof(T);
     static_assert(n_vec >= 1 && C * per % kThreads == 0, "whole vectors a thread");
     u32x4 q[n_vec];
     // ld: bytes, below 2^25, so that a block's offsets have 31 bits
@@ -209,11 +221,27 @@ __device__ inline void zero_fill(E* t, int n) {
     for (int i = threadIdx.x; i < n; i += kThreads) t[i] = 0;
 }
 
+// A head's sizes: four waves, with a quarter of the state's columns each. LDS rows are apart by their length and 16 bytes (4
+// banks more than a multiple of the banks: a wave's reads along the rows meet them all), or by 32 (8 banks: its transposing
+// reads, of 8 rows by 32 bytes, do) where those are the most.
+template <typename T, int DA_, int DC_>
+struct Head {
+    typedef T type;
+    typedef Op<T> O;
+    static constexpr int DA = DA_, DC = DC_, C = O::C, CT = C / 16, NT = DC / 64, waves = 4;
+    // waves a SIMD, and so workgroups a compute unit, that the registers allow
+    static constexpr int occupancy = DA + DC > 192 ? 2 : DA + DC > 128 ? 3 : 4;
+    static constexpr int tr = sizeof(T) == 2 ? 32 : 16;
+    typedef Rows<T, DA, 16> RA;
+    typedef Rows<T, DA, tr> RB;
+    typedef Rows<T, DC, tr> RC;
+    static constexpr int sp = C + 16 / (int)sizeof(T);  // of the block's products
+};
 // ---- states -----------------------------------------------------------------------------------------------------
-// A wave holds DC / 4 columns of the state: result tiles of 16 x 16, rows 16 t + 4 g + r, column lane % 16.
-template <int DA, int DC>
+// A wave's 16 NT columns of the state: result tiles of 16 x 16, rows 16 t + 4 g + r, columns 16 u + lane % 16.
+template <int DA, int NT>
 struct State {
-    static constexpr int NT = DC / 64, AT = DA / 16;
+    static constexpr int AT = DA / 16;
     f32x4 x[AT][NT];
     __device__ inline void clear() {
 #pragma unroll
@@ -227,134 +255,134 @@ struct State {
 #pragma unroll
             for (int u = 0; u < NT; ++u) x[t][u] *= f;
     }
-    // (the lane is taken as new at each call: the elements' places, alike for all pieces, would otherwise be kept in
-    // registers throughout)
+    // (the lane is taken as new at each call, or else the elements' places would be kept in registers from the start)
     __device__ inline void load(const Args& a, const float* p) {
         int lane = threadIdx.x & 63;
         asm volatile("" : "+v"(lane));
-        const int g = lane >> 4, n0 = (threadIdx.x >> 6) * (DC / 4) + (lane & 15);
+        const int g = lane >> 4, n0 = (int)(threadIdx.x >> 6) * (16 * NT) + (lane & 15);
+        const bool quads = a.trans && a.da % 4 == 0;  // they lie as they are held
         const int sm = a.trans ? 1 : a.dc, sn = a.trans ? a.da : 1;
 #pragma unroll
-        for (int t = 0; t < AT; ++t) {
+        for (int u = 0; u < NT; ++u) {
+            const int n = n0 + 16 * u;
+            const bool in = n < a.dc;
+            const float* q = p + (uint32_t)(min(n, a.dc - 1) * sn);
+            if (quads) {
 #pragma unroll
-            for (int u = 0; u < NT; ++u)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int m = 16 * t + 4 * g + r, n = n0 + 16 * u;
-                    const float v = p[(uint32_t)(min(m, a.da - 1) * sm + min(n, a.dc - 1) * sn)];
-                    x[t][u][r] = m < a.da && n < a.dc ? v : 0.f;
+                for (int t = 0; t < AT; ++t) {
+                    const int m = 16 * t + 4 * g;
+                    const f32x4 v = *reinterpret_cast<const f32x4_e*>(q + min(m, a.da - 4));
+                    const bool k = in && m < a.da;
+                    x[t][u] = f32x4{k ? v[0] : 0.f, k ? v[1] : 0.f, k ? v[2] : 0.f, k ? v[3] : 0.f};
                 }
-            if (t & 1) one_at_a_time();
+            } else {
+#pragma unroll
+                for (int t = 0; t < AT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int m = 16 * t + 4 * g + r;
+                        const float v = q[(uint32_t)(min(m, a.da - 1) * sm)];
+                        x[t][u][r] = in && m < a.da ? v : 0.f;
+                    }
+            }
+            one_at_a_time();
         }
     }
     __device__ inline void store(const Args& a, float* p) const {
         int lane = threadIdx.x & 63;
         asm volatile("" : "+v"(lane));
-        const int g = lane >> 4, n0 = (threadIdx.x >> 6) * (DC / 4) + (lane & 15);
+        const int g = lane >> 4, n0 = (int)(threadIdx.x >> 6) * (16 * NT) + (lane & 15);
 #pragma unroll
-        for (int t = 0; t < AT; ++t) {
+        for (int u = 0; u < NT; ++u) {
+            const int n = n0 + 16 * u;
+            if (n >= a.dc) continue;
 #pragma unroll
-            for (int u = 0; u < NT; ++u)
+            for (int t = 0; t < AT; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int m = 16 * t + 4 * g + r, n = n0 + 16 * u;
-                    if (m < a.da && n < a.dc) p[(uint32_t)(m * a.dc + n)] = x[t][u][r];
+                    const int m = 16 * t + 4 * g + r;
+                    if (m < a.da) p[(uint32_t)(m * a.dc + n)] = x[t][u][r];
                 }
-            one_at_a_time();
         }
     }
 };
 
-// x += sum over the block's rows j of b_j w_j c_j^T; PARTS: how many bfloat16 terms w c is taken as (one for fp32)
-template <typename T, int DA, int DC, int PARTS>
-__device__ inline void add_block(State<DA, DC>& s, const typename Op<T>::lds_t* B, const typename Op<T>::lds_t* Cv,
-                                 float l2, float scale, int n, int post) {
-    typedef Op<T> O;
-    constexpr int JT = O::C / 16;
-    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15, n0 = (threadIdx.x >> 6) * (DC / 4);
-    constexpr int sb = Rows<T, DA>::stride, sc = Rows<T, DC>::stride;
-    typename O::Quad w[PARTS][JT][State<DA, DC>::NT];
+// x += sum over the block's rows j of b_j f_j c_j^T, f(t) the weights of rows 16 t + 4 g ..; PARTS: how many bfloat16 terms
+// f c is taken as (one for fp32)
+template <typename Hd, int PARTS, typename F>
+__device__ inline void add_block(State<Hd::DA, Hd::NT>& s, const typename Hd::O::lds_t* B, const typename Hd::O::lds_t* Cv, F f) {
+    typedef typename Hd::O O;
+    constexpr int JT = Hd::CT, NT = Hd::NT;
+    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15, n0 = (int)(threadIdx.x >> 6) * (16 * NT);
+    typename O::Quad w[PARTS][JT][NT];
 #pragma unroll
-    for (int t = 0; t < JT; ++t) {
-        f32x4 f;
+    for (int t = 0; t < JT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) f[r] = scale * power(l2, max(n - post - (16 * t + 4 * g + r), 0));
-#pragma unroll
-        for (int u = 0; u < State<DA, DC>::NT; ++u) {
-            f32x4 v = O::values(O::col(Cv, sc, 16 * t, n0 + 16 * u, g, i)) * f;
+        for (int u = 0; u < NT; ++u) {
+            f32x4 v = O::values(O::col(Cv, Hd::RC::stride, 16 * t, n0 + 16 * u, g, i)) * f(t);
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
                 w[p][t][u] = O::make(v);
-                v -= O::values(w[p][t][u]);
+                if (p + 1 < PARTS) v -= O::values(w[p][t][u]);
             }
         }
-    }
 #pragma unroll
-    for (int m = 0; m < State<DA, DC>::AT; ++m) {
+    for (int m = 0; m < Hd::DA / 16; ++m) {
 #pragma unroll
         for (int t = 0; t < JT; t += 2) {
-            const auto b0 = O::col(B, sb, 16 * t, 16 * m, g, i), b1 = O::col(B, sb, 16 * t + 16, 16 * m, g, i);
+            const auto b0 = O::col(B, Hd::RB::stride, 16 * t, 16 * m, g, i);
+            const auto b1 = O::col(B, Hd::RB::stride, 16 * t + 16, 16 * m, g, i);
 #pragma unroll
-            for (int u = 0; u < State<DA, DC>::NT; ++u)
+            for (int u = 0; u < NT; ++u)
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p) s.x[m][u] = O::mma2(s.x[m][u], b0, b1, w[p][t][u], w[p][t + 1][u]);
         }
-        if (m & 1) one_at_a_time();
     }
 }
 
-// What each piece adds to its sequence's state. bfloat16: w c is split into three terms (24 bits, as fp32 has), so that
-// the states are sums of fp32 products.
-// workgroups a compute unit: the narrow heads' registers allow four
-template <int DA, int DC>
-constexpr int waves_of() {
-    return DA + DC <= 128 ? 4 : 2;
-}
-
+// What each tile adds to its sequence's state. bfloat16: f c is split into three terms (24 bits, as fp32 has), so that the
+// states are sums of fp32 products.
 template <typename T, int DA, int DC>
-__global__ __launch_bounds__(kThreads, (waves_of<DA, DC>())) void states(const Args a) {
-    typedef Op<T> O;
-    constexpr int C = O::C, PARTS = sizeof(T) == 2 ? 3 : 1;
-    __shared__ alignas(16) typename O::lds_t lb[C * Rows<T, DA>::stride], lc[C * Rows<T, DC>::stride];
-    const int64_t tile = blockIdx.x, t0 = tile * a.L, t1 = t0 + a.L < a.T ? t0 + a.L : a.T;
-    const int h = blockIdx.y;
-    const float l2 = log2_of(a.decay[h]);
+__global__ __launch_bounds__(kThreads, (Head<T, DA, DC>::occupancy)) void states(const Args a) {
+    typedef Head<T, DA, DC> Hd;
+    typedef typename Hd::O O;
+    constexpr int C = Hd::C, PARTS = sizeof(T) == 2 ? 3 : 1;
+    __shared__ alignas(16) typename O::lds_t lb[C * Hd::RB::stride], lc[C * Hd::RC::stride];
+    const Tile t = tile_of(a, blockIdx.x / (uint32_t)a.H);
+    if (t.seq < 0 || (t.leave < 0 && !a.last)) return;
+    const int h = blockIdx.x % (uint32_t)a.H, g = (threadIdx.x & 63) >> 4;
     const T* pb = static_cast<const T*>(a.b) + (int64_t)h * a.da;
     const T* pc = static_cast<const T*>(a.c) + (int64_t)h * a.dc;
     const int64_t ldb = a.ldb * (int64_t)sizeof(T), ldc = a.ldc * (int64_t)sizeof(T);
-    const int64_t size = (int64_t)a.da * a.dc;
-    zero_fill(lb, C * Rows<T, DA>::stride);
-    zero_fill(lc, C * Rows<T, DC>::stride);
-    for (int s = first_past(a.off, a.S, t0); s < a.S; ++s) {
-        if (a.off[s] >= t1) break;
-        Piece p;
-        if (!piece_of(a, s, t0, t1, p)) continue;
-        if (!p.leaves && !a.last) continue;
-        State<DA, DC> x;
-        x.clear();
-        const int64_t len = p.end - p.begin;
-        const int64_t from = a.dir > 0 ? p.begin : p.end - 1;
-        Rows<T, DA> rb;
-        Rows<T, DC> rc;
-        rb.load(pb, ldb, from, a.dir, (int)min((int64_t)C, len), a.da);
-        rc.load(pc, ldc, from, a.dir, (int)min((int64_t)C, len), a.dc);
-        for (int64_t k = 0; k < len; k += C) {
-            const int n = (int)min((int64_t)C, len - k);
-            __syncthreads();
-            rb.lay(lb, n, a.da);
-            rc.lay(lc, n, a.dc);
-            if (k + C < len) {
-                rb.load(pb, ldb, from + a.dir * (k + C), a.dir, (int)min((int64_t)C, len - k - C), a.da);
-                rc.load(pc, ldc, from + a.dir * (k + C), a.dir, (int)min((int64_t)C, len - k - C), a.dc);
-            }
-            __syncthreads();
-            if (k > 0) x.scale(power(l2, n));
-            add_block<T, DA, DC, PARTS>(x, lb, lc, l2, a.sscale, n, a.post);
+    typename Hd::RB rb;
+    typename Hd::RC rc;
+    rb.load(pb, ldb, t.from, a.dir, min(C, t.len), a.da);
+    rc.load(pc, ldc, t.from, a.dir, min(C, t.len), a.dc);
+    zero_fill(lb, C * Hd::RB::stride);
+    zero_fill(lc, C * Hd::RC::stride);
+    const float l2 = log2_of(a.decay[h]);
+    State<DA, Hd::NT> x;
+    x.clear();
+    for (int k = 0; k < t.len; k += C) {
+        const int n = min(C, t.len - k), next = min(C, t.len - k - C);
+        __syncthreads();
+        rb.lay(lb, n, a.da);
+        rc.lay(lc, n, a.dc);
+        if (next > 0) {
+            rb.load(pb, ldb, t.from + a.dir * (k + C), a.dir, next, a.da);
+            rc.load(pc, ldc, t.from + a.dir * (k + C), a.dir, next, a.dc);
         }
-        const int64_t slot = a.dir > 0 ? tile : tile - 1;
-        float* to = p.leaves ? a.slots + (slot * a.H + h) * size : a.last + ((int64_t)s * a.H + h) * size;
-        x.store(a, to);
+        __syncthreads();
+        if (k > 0) x.scale(power(l2, n));
+        add_block<Hd, PARTS>(x, lb, lc, [&](int q) {
+            f32x4 f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) f[r] = a.sscale * power(l2, max(n - a.post - (16 * q + 4 * g + r), 0));
+            return f;
+        });
     }
+    const int64_t size = (int64_t)a.da * a.dc;
+    x.store(a, t.leave >= 0 ? a.slots + (t.leave * a.H + h) * size : a.last + ((int64_t)t.seq * a.H + h) * size);
 }
 
 // Per sequence, head and four state elements: the boundaries in scan order.
@@ -371,15 +399,15 @@ __global__ __launch_bounds__(kThreads) void chain(const Args a, int blocks_per_h
         if (a.last) a.last[at] = x;
         return;
     }
-    const int64_t first = o0 / a.L, end = (o1 - 1) / a.L;
-    const float l2 = log2_of(a.decay[h]), whole = power(l2, a.L);
+    const int64_t L = int64_t(1) << a.log_l, base = o0 >> a.log_l, end = (o1 - o0 - 1) >> a.log_l;
+    const float l2 = log2_of(a.decay[h]), whole = power(l2, (int)L);
     const int64_t hop = (int64_t)a.H * size;
-    // boundaries in scan order; all tiles but the first and last are whole
-    const int64_t n_first = (a.dir > 0 ? min(o1, (first + 1) * a.L) - o0 : o1 - max(o0, end * a.L));
-    float* p = a.slots + ((a.dir > 0 ? first : end - 1) * a.H + h) * size + e;
-    float f = power(l2, (int)n_first);
+    // boundaries in scan order; all tiles but the sequence's last one are whole
+    const int rest = (int)(o1 - o0 - end * L), lead = end > 0 ? (int)L : rest;
+    float* p = a.slots + ((a.dir > 0 ? base : base + end - 1) * a.H + h) * size + e;
+    float f = power(l2, a.dir > 0 ? lead : rest);
     constexpr int U = 8;
-    for (int64_t i = first; i < end; i += U) {
+    for (int64_t i = 0; i < end; i += U) {
         float v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -393,10 +421,7 @@ __global__ __launch_bounds__(kThreads) void chain(const Args a, int blocks_per_h
             }
         p += a.dir * U * hop;
     }
-    if (a.last) {
-        const int64_t n_last = a.dir > 0 ? o1 - max(o0, end * a.L) : min(o1, (first + 1) * a.L) - o0;
-        a.last[at] = __builtin_fmaf(x, power(l2, (int)n_last), a.last[at]);
-    }
+    if (a.last) a.last[at] = __builtin_fmaf(x, power(l2, a.dir > 0 ? rest : lead), a.last[at]);
 }
 
 template <typename T>
@@ -418,171 +443,170 @@ __device__ inline void store_quad(T* p, f32x4 v, int n) {
     }
 }
 
-// The pieces' outputs, block by block. bfloat16 roundings on the way: of (a . b) d^{i-j} before its product with c, of the
-// entering state before its product with a, and of w c before it is added to the state that is handed on within the tile
+// The tiles' outputs, block by block. bfloat16 roundings on the way: of (a . b) d^{i-j} before its product with c, of the
+// entering state before its product with a, and of f c before it is added to the state that is handed on within the tile
 // (two terms there); each is half a step of values that reach the output as a sum with its own half step. Sums and states
 // are fp32.
 template <typename T, int DA, int DC>
-__global__ __launch_bounds__(kThreads, (waves_of<DA, DC>())) void outputs(const Args a) {
-    typedef Op<T> O;
+__global__ __launch_bounds__(kThreads, (Head<T, DA, DC>::occupancy)) void outputs(const Args a) {
+    typedef Head<T, DA, DC> Hd;
+    typedef typename Hd::O O;
     typedef typename O::Quad Quad;
-    constexpr int C = O::C, CT = C / 16, PARTS = sizeof(T) == 2 ? 2 : 1, NT = DC / 64;
-    constexpr int sa = Rows<T, DA>::stride, sc = Rows<T, DC>::stride, sp = C + 16 / (int)sizeof(T);
+    constexpr int C = Hd::C, CT = Hd::CT, NT = Hd::NT, PARTS = sizeof(T) == 2 ? 2 : 1;
+    constexpr int sa = Hd::RA::stride, sb = Hd::RB::stride, sc = Hd::RC::stride, sp = Hd::sp;
     extern __shared__ u32x4 smem[];
     typename O::lds_t* la = reinterpret_cast<typename O::lds_t*>(smem);
-    typename O::lds_t *lb = la + C * sa, *lc = lb + C * sa, *lp = lc + C * sc;
-    const int64_t tile = blockIdx.x, t0 = tile * a.L, t1 = t0 + a.L < a.T ? t0 + a.L : a.T;
-    const int h = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
-    const float l2 = log2_of(a.decay[h]);
+    typename O::lds_t *lb = la + C * sa, *lc = lb + C * sb, *lp = lc + C * sc;
+    const Tile tile = tile_of(a, blockIdx.x / (uint32_t)a.H);
+    if (tile.seq < 0) return;
+    const int h = blockIdx.x % (uint32_t)a.H, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
     const T* pa = static_cast<const T*>(a.a) + (int64_t)h * a.da;
-    const int64_t lda = a.lda * (int64_t)sizeof(T);
     const T* pb = static_cast<const T*>(a.b) + (int64_t)h * a.da;
     const T* pc = static_cast<const T*>(a.c) + (int64_t)h * a.dc;
-    const int64_t ldb = a.ldb * (int64_t)sizeof(T), ldc = a.ldc * (int64_t)sizeof(T);
+    const int64_t lda = a.lda * (int64_t)sizeof(T), ldb = a.ldb * (int64_t)sizeof(T), ldc = a.ldc * (int64_t)sizeof(T);
     char* po = reinterpret_cast<char*>(static_cast<T*>(a.out) + (int64_t)h * a.dc);
-    const int64_t size = (int64_t)a.da * a.dc;
-    const int64_t ldo = a.ldo * (int64_t)sizeof(T);
+    const int64_t size = (int64_t)a.da * a.dc, ldo = a.ldo * (int64_t)sizeof(T);
     const bool whole = a.dc % 4 == 0;
-    zero_fill(la, 2 * C * sa + C * sc);
-    for (int s = first_past(a.off, a.S, t0); s < a.S; ++s) {
-        if (a.off[s] >= t1) break;
-        Piece p;
-        if (!piece_of(a, s, t0, t1, p)) continue;
-        const int64_t len = p.end - p.begin, from = a.dir > 0 ? p.begin : p.end - 1;
-        Rows<T, DA> ra, rb;
-        Rows<T, DC> rc;
-        const int n0 = (int)min((int64_t)C, len);
-        ra.load(pa, lda, from, a.dir, n0, a.da);
-        rb.load(pb, ldb, from, a.dir, n0, a.da);
-        rc.load(pc, ldc, from, a.dir, n0, a.dc);
-        State<DA, DC> x;
-        const float* enter = p.enters ? a.slots + ((a.dir > 0 ? tile - 1 : tile) * a.H + h) * size
-                             : a.init ? a.init + ((int64_t)s * a.H + h) * size : nullptr;
-        const bool zero = enter == nullptr;
-        if (zero) x.clear();
-        else x.load(a, enter);
-        for (int64_t k = 0; k < len; k += C) {
-            const int n = (int)min((int64_t)C, len - k);
-            __syncthreads();
-            ra.lay(la, n, a.da);
-            rb.lay(lb, n, a.da);
-            rc.lay(lc, n, a.dc);
-            if (k + C < len) {
-                const int nn = (int)min((int64_t)C, len - k - C);
-                const int64_t f = from + a.dir * (k + C);
-                ra.load(pa, lda, f, a.dir, nn, a.da);
-                rb.load(pb, ldb, f, a.dir, nn, a.da);
-                rc.load(pc, ldc, f, a.dir, nn, a.dc);
-            }
-            __syncthreads();
-            // (a_i . b_j) d^{i-j}: the tiles of 16 x 16 on and below the diagonal, the lowest rows first, dealt out to the
-            // waves; row i at lane % 16, j at 4 g + r
-            constexpr int kPairs = CT * (CT + 1) / 2;
+    typename Hd::RA ra;
+    typename Hd::RB rb;
+    typename Hd::RC rc;
+    const auto load = [&](int k, int n) {
+        const int64_t f = tile.from + a.dir * k;
+        ra.load(pa, lda, f, a.dir, n, a.da);
+        rb.load(pb, ldb, f, a.dir, n, a.da);
+        rc.load(pc, ldc, f, a.dir, n, a.dc);
+    };
+    load(0, min(C, tile.len));
+    const float* enter = tile.enter >= 0 ? a.slots + (tile.enter * a.H + h) * size
+                         : a.init ? a.init + ((int64_t)tile.seq * a.H + h) * size : nullptr;
+    State<DA, Hd::NT> x;
+    if (enter) x.load(a, enter);
+    else x.clear();
+    zero_fill(la, C * (sa + sb + sc));
+    // d^e for the e that occur, in two factors: within 16 (a lane's) and of 16s
+    const float l2 = log2_of(a.decay[h]);
+    float d16[CT], row_f = power(l2, i + a.post), near[4], far[4], left[4];
 #pragma unroll
-            for (int k0 = 0; k0 < kPairs; k0 += 4) {
-                const int pair = k0 + wave;
-                if (pair >= kPairs) break;
-                int it = CT - 1, jt = pair;
+    for (int q = 0; q < CT; ++q) d16[q] = uniform(power(l2, 16 * q));
 #pragma unroll
-                for (int q = CT; q > 1; --q)
-                    if (it == q - 1 && jt >= q) {
-                        jt -= q;
-                        --it;
-                    }
-                f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < 4; ++r) {
+        const int e = i - (4 * g + r);
+        near[r] = e < 0 ? 0.f : a.pscale * power(l2, e);
+        far[r] = a.pscale * power(l2, 16 + e);
+        left[r] = a.sscale * power(l2, 16 - a.post - (4 * g + r));
+    }
+    const float d_block = uniform(power(l2, C));
+    for (int k = 0; k < tile.len; k += C) {
+        const int n = min(C, tile.len - k), next = min(C, tile.len - k - C);
+        __syncthreads();
+        ra.lay(la, n, a.da);
+        rb.lay(lb, n, a.da);
+        rc.lay(lc, n, a.dc);
+        if (next > 0) load(k + C, next);
+        __syncthreads();
+        // (a_i . b_j) d^{i-j}: the tiles of 16 x 16 on and below the diagonal, the lowest rows first, dealt out to the
+        // waves; row i at lane % 16, j at 4 g + r
+        constexpr int kPairs = CT * (CT + 1) / 2;
 #pragma unroll
-                for (int m = 0; m < DA; m += 32)
-                    v = O::mma2(v, O::row(lb, sa, 16 * jt + i, m, g), O::row(lb, sa, 16 * jt + i, m + 16, g),
-                                O::row(la, sa, 16 * it + i, m, g), O::row(la, sa, 16 * it + i, m + 16, g));
+        for (int k0 = 0; k0 < kPairs; k0 += Hd::waves) {
+            const int pair = k0 + wave;
+            if (pair >= kPairs) break;
+            int it = CT - 1, jt = pair;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int e = 16 * (it - jt) + i - (4 * g + r);
-                    v[r] = e < 0 ? 0.f : v[r] * (a.pscale * power(l2, e));
+            for (int q = CT; q > 1; --q)
+                if (it == q - 1 && jt >= q) {
+                    jt -= q;
+                    --it;
                 }
-                *reinterpret_cast<Quad*>(lp + (16 * it + i) * sp + 16 * jt + 4 * g) = O::make(v);
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int m = 0; m < DA; m += 32)
+                v = O::mma2(v, O::row(lb, sb, 16 * jt + i, m, g), O::row(lb, sb, 16 * jt + i, m + 16, g),
+                            O::row(la, sa, 16 * it + i, m, g), O::row(la, sa, 16 * it + i, m + 16, g));
+            float f = 1.f;
+#pragma unroll
+            for (int q = 1; q + 1 < CT; ++q) f = it - jt == q + 1 ? d16[q] : f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = it == jt && i < 4 * g + r ? 0.f : v[r] * (it == jt ? near[r] : far[r] * f);
+            *reinterpret_cast<Quad*>(lp + (16 * it + i) * sp + 16 * jt + 4 * g) = O::make(v);
+        }
+        __syncthreads();
+        // outputs: row i at lane % 16, columns 4 g + r of the wave's tiles
+        f32x4 o[CT][NT];
+#pragma unroll
+        for (int it = 0; it < CT; ++it)
+#pragma unroll
+            for (int u = 0; u < NT; ++u) o[it][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (k > 0 || enter) {
+#pragma unroll
+            for (int m = 0; m < DA / 16; m += 2) {
+                Quad x0[NT], x1[NT];
+#pragma unroll
+                for (int u = 0; u < NT; ++u) {
+                    x0[u] = O::make(x.x[m][u]);
+                    x1[u] = O::make(x.x[m + 1][u]);
+                }
+#pragma unroll
+                for (int it = 0; it < CT; ++it) {
+                    const Quad a0 = O::row(la, sa, 16 * it + i, 16 * m, g), a1 = O::row(la, sa, 16 * it + i, 16 * m + 16, g);
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) o[it][u] = O::mma2(o[it][u], x0[u], x1[u], a0, a1);
+                }
             }
-            __syncthreads();
-            one_at_a_time();
-            // outputs: row i at lane % 16, columns 4 g + r of the wave's tiles
-            f32x4 o[CT][NT];
 #pragma unroll
             for (int it = 0; it < CT; ++it)
 #pragma unroll
-                for (int u = 0; u < NT; ++u) o[it][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (k > 0 || !zero) {
+                for (int u = 0; u < NT; ++u) o[it][u] *= row_f * d16[it];
+        }
 #pragma unroll
-                for (int m = 0; m < DA / 16; m += 2) {
-                    Quad x0[NT], x1[NT];
+        for (int t = 0; t < CT; t += 2) {
+            Quad c0[NT], c1[NT];
 #pragma unroll
-                    for (int u = 0; u < NT; ++u) {
-                        x0[u] = O::make(x.x[m][u]);
-                        x1[u] = O::make(x.x[m + 1][u]);
-                    }
-#pragma unroll
-                    for (int it = 0; it < CT; ++it) {
-                        const Quad a0 = O::row(la, sa, 16 * it + i, 16 * m, g), a1 = O::row(la, sa, 16 * it + i, 16 * m + 16, g);
-#pragma unroll
-                        for (int u = 0; u < NT; ++u) o[it][u] = O::mma2(o[it][u], x0[u], x1[u], a0, a1);
-                    }
-                    one_at_a_time();
-                }
-#pragma unroll
-                for (int it = 0; it < CT; ++it) {
-                    const float f = power(l2, 16 * it + i + a.post);
-#pragma unroll
-                    for (int u = 0; u < NT; ++u) o[it][u] *= f;
-                }
+            for (int u = 0; u < NT; ++u) {
+                c0[u] = O::col(lc, sc, 16 * t, 16 * (NT * wave + u), g, i);
+                c1[u] = O::col(lc, sc, 16 * t + 16, 16 * (NT * wave + u), g, i);
             }
 #pragma unroll
-            for (int t = 0; t < CT; t += 2) {
-                Quad c0[NT], c1[NT];
+            for (int it = t; it < CT; ++it) {
+                const Quad p0 = O::row(lp, sp, 16 * it + i, 16 * t, g);
+                // the tile past the diagonal is never written
+                const Quad p1 = it > t ? O::row(lp, sp, 16 * it + i, 16 * t + 16, g) : O::make(f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-                for (int u = 0; u < NT; ++u) {
-                    const int n = wave * (DC / 4) + 16 * u;
-                    c0[u] = O::col(lc, sc, 16 * t, n, g, i);
-                    c1[u] = O::col(lc, sc, 16 * t + 16, n, g, i);
-                }
-#pragma unroll
-                for (int it = 0; it < CT; ++it) {
-                    if (it < t) continue;
-                    const Quad p0 = O::row(lp, sp, 16 * it + i, 16 * t, g);
-                    // the tile past the diagonal is never written
-                    const Quad p1 = it > t ? O::row(lp, sp, 16 * it + i, 16 * t + 16, g) : O::make(f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                    for (int u = 0; u < NT; ++u) o[it][u] = O::mma2(o[it][u], c0[u], c1[u], p0, p1);
-                }
-                one_at_a_time();
+                for (int u = 0; u < NT; ++u) o[it][u] = O::mma2(o[it][u], c0[u], c1[u], p0, p1);
             }
+        }
+        char* q = po + (tile.from + a.dir * k) * ldo;
 #pragma unroll
-            for (int it = 0; it < CT; ++it) {
-                const int row = 16 * it + i;
-                if (row >= n) continue;
-                char* q = po + (from + (int64_t)a.dir * k) * ldo + (int64_t)(a.dir * row) * ldo;
+        for (int it = 0; it < CT; ++it) {
+            const int row = 16 * it + i;
+            if (row >= n) continue;
+            char* qr = q + (int64_t)(a.dir * row) * ldo;
 #pragma unroll
-                for (int u = 0; u < NT; ++u) {
-                    const int col = wave * (DC / 4) + 16 * u + 4 * g;
-                    if (col < a.dc) store_quad<T>(reinterpret_cast<T*>(q) + col, o[it][u] * a.oscale, whole ? 4 : a.dc - col);
-                }
+            for (int u = 0; u < NT; ++u) {
+                const int col = 16 * (NT * wave + u) + 4 * g;
+                if (col < a.dc) store_quad<T>(reinterpret_cast<T*>(qr) + col, o[it][u] * a.oscale, whole ? 4 : a.dc - col);
             }
-            if (k + C < len) {
-                x.scale(power(l2, n));
-                add_block<T, DA, DC, PARTS>(x, lb, lc, l2, a.sscale, n, a.post);
-            }
+        }
+        if (next > 0) {  // of a whole block
+            x.scale(d_block);
+            add_block<Hd, PARTS>(x, lb, lc, [&](int q) {
+                return f32x4{left[0], left[1], left[2], left[3]} * d16[CT - 1 - q];
+            });
         }
     }
 }
 
 template <typename T, int DA, int DC>
 constexpr size_t outputs_lds() {
-    constexpr int C = Op<T>::C;
-    return sizeof(T) * (2 * C * Rows<T, DA>::stride + C * Rows<T, DC>::stride + C * (C + 16 / sizeof(T)));
+    typedef Head<T, DA, DC> Hd;
+    return sizeof(T) * Hd::C * (Hd::RA::stride + Hd::RB::stride + Hd::RC::stride + Hd::sp);
 }
 
 template <typename T, int DA, int DC>
 hipError_t go(const Args& a, int what, hipStream_t st) {
-    const dim3 grid((uint32_t)a.ntiles, (uint32_t)a.H);
+    const dim3 grid((uint32_t)(((a.T >> a.log_l) + a.S) * a.H)), block(kThreads);  // the heads of a tile side by side
     if (what == 0) {
-        launch(states<T, DA, DC>, grid, dim3(kThreads), 0, st, a);
+        launch(states<T, DA, DC>, grid, block, 0, st, a);
     } else {
         constexpr size_t lds = outputs_lds<T, DA, DC>();
         if (lds > 65536) {
@@ -590,7 +614,7 @@ hipError_t go(const Args& a, int what, hipStream_t st) {
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
             if (e != hipSuccess) return e;
         }
-        launch(outputs<T, DA, DC>, grid, dim3(kThreads), lds, st, a);
+        launch(outputs<T, DA, DC>, grid, block, lds, st, a);
     }
     return hipGetLastError();
 }
@@ -686,13 +710,10 @@ int linattn_max_d() { return 128; }
 // some workgroups a compute unit.
 AttnPlan attn_plan(int64_t T, int H, int Dk, int Dv) {
     AttnPlan p;
-    int L = 256;
-    while (L < 2048 && T / (2 * L) * H >= 1024) L *= 2;
-    p.L = L;
-    p.ntiles = (T + L - 1) / L;
+    while (p.log_l < 11 && (T >> (p.log_l + 1)) * H >= 1024) ++p.log_l;
     const int64_t state = (int64_t)H * Dk * Dv;
-    p.slots = (size_t)std::max<int64_t>(p.ntiles - 1, 0) * (size_t)state;
-    p.total = 2 * ((p.slots * sizeof(float) + 15) / 16 * 16);
+    p.nslots = T >> p.log_l;
+    p.total = 2 * (((size_t)p.nslots * (size_t)state * sizeof(float) + 15) / 16 * 16);
     p.chain_blocks = (int64_t)H * ((Dk * (int64_t)Dv + kThreads - 1) / kThreads);
     return p;
 }
@@ -704,8 +725,7 @@ Args args_of(const AttnArgs& x, const AttnPlan& p) {
     a.S = x.S;
     a.H = x.H;
     a.T = x.T;
-    a.L = p.L;
-    a.ntiles = p.ntiles;
+    a.log_l = p.log_l;
     a.decay = x.decay;
     return a;
 }
@@ -732,8 +752,8 @@ hipError_t launch_attn_fwd(const AttnArgs& x, int dtype, void* ws, hipStream_t s
     a.out = x.y;
     a.ldo = x.ldy;
     hipError_t e = hipSuccess;
-    if (x.T > 0 && (p.ntiles > 1 || x.hT) && (e = go_any(a, dtype, 0, st)) != hipSuccess) return e;
-    if ((p.ntiles > 1 || x.hT) && (e = go_chain(a, st)) != hipSuccess) return e;
+    if (x.T > 0 && (p.nslots > 0 || x.hT) && (e = go_any(a, dtype, 0, st)) != hipSuccess) return e;
+    if ((p.nslots > 0 || x.hT) && (e = go_chain(a, st)) != hipSuccess) return e;
     return x.T > 0 ? go_any(a, dtype, 1, st) : e;
 }
 
@@ -756,8 +776,8 @@ hipError_t launch_attn_bwd(const AttnArgs& x, int dtype, void* ws, hipStream_t s
     g.init = x.dhT;
     g.last = x.dh0;
     hipError_t e = hipSuccess;
-    if (x.T > 0 && (p.ntiles > 1 || x.dh0) && (e = go_any(g, dtype, 0, st)) != hipSuccess) return e;
-    if ((p.ntiles > 1 || x.dh0) && (e = go_chain(g, st)) != hipSuccess) return e;
+    if (x.T > 0 && (p.nslots > 0 || x.dh0) && (e = go_any(g, dtype, 0, st)) != hipSuccess) return e;
+    if ((p.nslots > 0 || x.dh0) && (e = go_chain(g, st)) != hipSuccess) return e;
     if (x.T == 0) return e;
     g.pscale = x.scale;
     g.oscale = 1.f;

@@ -379,9 +379,10 @@ struct AttnArgs {
     float *hT, *dh0;                // [S][H][Dk][Dv] or null
 };
 struct AttnPlan {
-    int L = 0;                      // tokens a tile
-    int64_t ntiles = 0, chain_blocks = 0;  // chain_blocks: workgroups a sequence
-    size_t slots = 0, total = 0;    // floats of one direction's tile states; bytes of both
+    int log_l = 8;                  // log2 of the tokens a tile
+    int64_t nslots = 0;             // tile boundaries, states of H heads each
+    int64_t chain_blocks = 0;       // workgroups a sequence
+    size_t total = 0;               // bytes of both directions' slots
 };
 int linattn_max_d();
 AttnPlan attn_plan(int64_t T, int H, int Dk, int Dv);

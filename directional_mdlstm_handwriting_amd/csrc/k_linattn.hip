@@ -25,7 +25,8 @@ namespace mdl {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of chain and step, and of the four waves that share a block's products
+__device__ inline int thread_id() { return (int)threadIdx.x & (kThreads - 1); }
 
 typedef __bf16 bh8 __attribute__((ext_vector_type(8)));
 typedef short h4 __attribute__((ext_vector_type(4)));
@@ -86,8 +87,8 @@ struct Op<float> {
     }
 };
 
-// log2 d in double: near 1 the fp32 instruction's result is good to its last bit only in absolute terms
-__device__ inline float log2_of(float d) { return (float)log2((double)d); }
+// log2 d: the instruction is within 1 ulp of it over all of [1/4, 1), near 1 too (every float was tried)
+__device__ inline float log2_of(float d) { return __builtin_amdgcn_logf(d); }
 // d^e for whole e >= 0, from log2 d: d^0 is 1 also for d = 0
 __device__ inline float power(float l2, int e) { return e == 0 ? 1.f : __builtin_amdgcn_exp2f((float)e * l2); }
 
@@ -104,16 +105,19 @@ struct Args {
     int log_l;                 // log2 of the tokens a tile, L
     int dir;                   // +1: tokens ascending, -1: descending
     int post;                  // 1: the entering state is the previous token's; 0: it is the token's own
-    const void *a, *b, *c;     // [T][H][da or dc] at row strides
-    int64_t lda, ldb, ldc;
-    int da, dc, trans;         // states are stored [da][dc], or [dc][da]
     const float* decay;
     float pscale, sscale, oscale;  // of a . b, of b c^T in the state, of the output
-    float* slots;              // [T / L][H][da][dc], a tile boundary's state
-    const float* init;         // [S][H][da][dc] or null
-    float* last;               // [S][H][da][dc] or null
-    void* out;                 // [T][H][dc]
-    int64_t ldo;
+    float* slots;              // [T / L][H][size], a tile boundary's state
+    const float* init;         // [S][H][size] or null
+    float* last;               // [S][H][size] or null
+    int64_t size;              // elements of a state
+    struct Side {
+        const void *a, *b, *c; // [T][H][da or dc] at row strides
+        int64_t lda, ldb, ldc;
+        int da, dc, trans;     // states are stored [da][dc], or [dc][da]
+        void* out;             // [T][H][dc]
+        int64_t ldo;
+    } side[2];
 };
 
 // offsets that leave [0, T] end there: whatever they hold, no tile leaves the tensors or the slots
@@ -175,10 +179,10 @@ struct Rows {
     // ld: bytes, below 2^25, so that a block's offsets have 31 bits
     __device__ inline void load(const T* base, int64_t ld, int64_t first, int dir, int n, int d) {
         const char* low = reinterpret_cast<const char*>(base) + (dir > 0 ? first : first - (n - 1)) * ld;
-        const int col = (int)(threadIdx.x % per) * V, c0 = d < V ? 0 : min(col, d - V);
+        const int col = thread_id() % per * V, c0 = d < V ? 0 : min(col, d - V);
 #pragma unroll
         for (int i = 0; i < n_vec; ++i) {
-            const int r = min((i * kThreads + (int)threadIdx.x) / per, n - 1);
+            const int r = min((i * kThreads + thread_id()) / per, n - 1);
             const uint32_t o = (uint32_t)(dir > 0 ? r : n - 1 - r) * (uint32_t)ld + (uint32_t)(c0 * sizeof(T));
             if (d >= V) {
                 q[i] = *reinterpret_cast<const u32x4_e*>(low + o);
@@ -197,10 +201,10 @@ struct Rows {
         }
     }
     __device__ inline void lay(E* t, int n, int d) const {
-        const int col = (int)(threadIdx.x % per) * V;
+        const int col = thread_id() % per * V;
 #pragma unroll
         for (int i = 0; i < n_vec; ++i) {
-            const int r = (i * kThreads + (int)threadIdx.x) / per;
+            const int r = (i * kThreads + thread_id()) / per;
             const bool in = r < n;
             const u32x4 v = {in ? q[i][0] : 0, in ? q[i][1] : 0, in ? q[i][2] : 0, in ? q[i][3] : 0};
             if (col + V <= d || (d < V && col == 0)) {
@@ -218,7 +222,7 @@ struct Rows {
 };
 template <typename E>
 __device__ inline void zero_fill(E* t, int n) {
-    for (int i = threadIdx.x; i < n; i += kThreads) t[i] = 0;
+    for (int i = thread_id(); i < n; i += kThreads) t[i] = 0;
 }
 
 // A head's sizes: four waves, with a quarter of the state's columns each. LDS rows are apart by their length and 16 bytes (4
@@ -256,10 +260,10 @@ struct State {
             for (int u = 0; u < NT; ++u) x[t][u] *= f;
     }
     // (the lane is taken as new at each call, or else the elements' places would be kept in registers from the start)
-    __device__ inline void load(const Args& a, const float* p) {
+    __device__ inline void load(const Args::Side& a, const float* p) {
         int lane = threadIdx.x & 63;
         asm volatile("" : "+v"(lane));
-        const int g = lane >> 4, n0 = (int)(threadIdx.x >> 6) * (16 * NT) + (lane & 15);
+        const int g = lane >> 4, n0 = (thread_id() >> 6) * (16 * NT) + (lane & 15);
         const bool quads = a.trans && a.da % 4 == 0;  // they lie as they are held
         const int sm = a.trans ? 1 : a.dc, sn = a.trans ? a.da : 1;
 #pragma unroll
@@ -288,10 +292,10 @@ struct State {
             one_at_a_time();
         }
     }
-    __device__ inline void store(const Args& a, float* p) const {
+    __device__ inline void store(const Args::Side& a, float* p) const {
         int lane = threadIdx.x & 63;
         asm volatile("" : "+v"(lane));
-        const int g = lane >> 4, n0 = (int)(threadIdx.x >> 6) * (16 * NT) + (lane & 15);
+        const int g = lane >> 4, n0 = (thread_id() >> 6) * (16 * NT) + (lane & 15);
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
             const int n = n0 + 16 * u;
@@ -313,7 +317,7 @@ template <typename Hd, int PARTS, typename F>
 __device__ inline void add_block(State<Hd::DA, Hd::NT>& s, const typename Hd::O::lds_t* B, const typename Hd::O::lds_t* Cv, F f) {
     typedef typename Hd::O O;
     constexpr int JT = Hd::CT, NT = Hd::NT;
-    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15, n0 = (int)(threadIdx.x >> 6) * (16 * NT);
+    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15, n0 = (thread_id() >> 6) * (16 * NT);
     typename O::Quad w[PARTS][JT][NT];
 #pragma unroll
     for (int t = 0; t < JT; ++t)
@@ -351,13 +355,15 @@ __global__ __launch_bounds__(kThreads, (Head<T, DA, DC>::occupancy)) void states
     const Tile t = tile_of(a, blockIdx.x / (uint32_t)a.H);
     if (t.seq < 0 || (t.leave < 0 && !a.last)) return;
     const int h = blockIdx.x % (uint32_t)a.H, g = (threadIdx.x & 63) >> 4;
-    const T* pb = static_cast<const T*>(a.b) + (int64_t)h * a.da;
-    const T* pc = static_cast<const T*>(a.c) + (int64_t)h * a.dc;
-    const int64_t ldb = a.ldb * (int64_t)sizeof(T), ldc = a.ldc * (int64_t)sizeof(T);
+    const Args::Side& side = a.side[0];
+    const int da = side.da, dc = side.dc;
+    const T* pb = static_cast<const T*>(side.b) + (int64_t)h * da;
+    const T* pc = static_cast<const T*>(side.c) + (int64_t)h * dc;
+    const int64_t ldb = side.ldb * (int64_t)sizeof(T), ldc = side.ldc * (int64_t)sizeof(T);
     typename Hd::RB rb;
     typename Hd::RC rc;
-    rb.load(pb, ldb, t.from, a.dir, min(C, t.len), a.da);
-    rc.load(pc, ldc, t.from, a.dir, min(C, t.len), a.dc);
+    rb.load(pb, ldb, t.from, a.dir, min(C, t.len), da);
+    rc.load(pc, ldc, t.from, a.dir, min(C, t.len), dc);
     zero_fill(lb, C * Hd::RB::stride);
     zero_fill(lc, C * Hd::RC::stride);
     const float l2 = log2_of(a.decay[h]);
@@ -366,11 +372,11 @@ __global__ __launch_bounds__(kThreads, (Head<T, DA, DC>::occupancy)) void states
     for (int k = 0; k < t.len; k += C) {
         const int n = min(C, t.len - k), next = min(C, t.len - k - C);
         __syncthreads();
-        rb.lay(lb, n, a.da);
-        rc.lay(lc, n, a.dc);
+        rb.lay(lb, n, da);
+        rc.lay(lc, n, dc);
         if (next > 0) {
-            rb.load(pb, ldb, t.from + a.dir * (k + C), a.dir, next, a.da);
-            rc.load(pc, ldc, t.from + a.dir * (k + C), a.dir, next, a.dc);
+            rb.load(pb, ldb, t.from + a.dir * (k + C), a.dir, next, da);
+            rc.load(pc, ldc, t.from + a.dir * (k + C), a.dir, next, dc);
         }
         __syncthreads();
         if (k > 0) x.scale(power(l2, n));
@@ -381,47 +387,55 @@ __global__ __launch_bounds__(kThreads, (Head<T, DA, DC>::occupancy)) void states
             return f;
         });
     }
-    const int64_t size = (int64_t)a.da * a.dc;
-    x.store(a, t.leave >= 0 ? a.slots + (t.leave * a.H + h) * size : a.last + ((int64_t)t.seq * a.H + h) * size);
+    x.store(side, t.leave >= 0 ? a.slots + (t.leave * a.H + h) * a.size : a.last + ((int64_t)t.seq * a.H + h) * a.size);
 }
 
-// Per sequence, head and four state elements: the boundaries in scan order.
+// Per sequence, head and V state elements: the boundaries in scan order, eight read ahead.
+template <int V>
 __global__ __launch_bounds__(kThreads) void chain(const Args a, int blocks_per_head) {
     const int64_t id = blockIdx.x;
     const int eb = (int)(id % blocks_per_head), h = (int)(id / blocks_per_head % a.H);
-    const int64_t s = id / blocks_per_head / a.H, size = (int64_t)a.da * a.dc;
-    const int64_t e = (int64_t)eb * kThreads + threadIdx.x;
-    if (e >= size) return;
-    const int64_t o0 = offset(a, s), o1 = offset(a, s + 1);
-    const int64_t at = (s * a.H + h) * size + e;
-    float x = a.init ? a.init[at] : 0.f;
+    const int64_t s = id / blocks_per_head / a.H, e = ((int64_t)eb * kThreads + threadIdx.x) * V;
+    if (e >= a.size) return;
+    const int64_t o0 = offset(a, s), o1 = offset(a, s + 1), at = (s * a.H + h) * a.size + e;
+    float x[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = 0.f;
+    if (a.init) load_f32<V>(a.init + at, x);
     if (o0 >= o1) {
-        if (a.last) a.last[at] = x;
+        if (a.last) store_f32<V>(a.last + at, x);
         return;
     }
     const int64_t L = int64_t(1) << a.log_l, base = o0 >> a.log_l, end = (o1 - o0 - 1) >> a.log_l;
     const float l2 = log2_of(a.decay[h]), whole = power(l2, (int)L);
-    const int64_t hop = (int64_t)a.H * size;
-    // boundaries in scan order; all tiles but the sequence's last one are whole
+    const int64_t hop = a.dir * a.H * a.size;
+    // all tiles but the sequence's last one are whole
     const int rest = (int)(o1 - o0 - end * L), lead = end > 0 ? (int)L : rest;
-    float* p = a.slots + ((a.dir > 0 ? base : base + end - 1) * a.H + h) * size + e;
-    float f = power(l2, a.dir > 0 ? lead : rest);
+    float* p = a.slots + ((a.dir > 0 ? base : base + end - 1) * a.H + h) * a.size + e;
+    float f = power(l2, a.dir > 0 ? lead : rest), v[V];
     constexpr int U = 8;
     for (int64_t i = 0; i < end; i += U) {
-        float v[U];
+        float w[U][V];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (i + u < end) v[u] = p[a.dir * u * hop];
+            if (i + u < end) load_f32<V>(p + u * hop, w[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (i + u < end) {
-                x = __builtin_fmaf(x, f, v[u]);
-                p[a.dir * u * hop] = x;
+#pragma unroll
+                for (int j = 0; j < V; ++j) x[j] = __builtin_fmaf(x[j], f, w[u][j]);
+                store_f32<V>(p + u * hop, x);
                 f = whole;
             }
-        p += a.dir * U * hop;
+        p += U * hop;
     }
-    if (a.last) a.last[at] = __builtin_fmaf(x, power(l2, a.dir > 0 ? rest : lead), a.last[at]);
+    if (a.last) {
+        load_f32<V>(a.last + at, v);
+        f = power(l2, a.dir > 0 ? rest : lead);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = __builtin_fmaf(x[j], f, v[j]);
+        store_f32<V>(a.last + at, v);
+    }
 }
 
 template <typename T>
@@ -447,42 +461,55 @@ __device__ inline void store_quad(T* p, f32x4 v, int n) {
 // entering state before its product with a, and of f c before it is added to the state that is handed on within the tile
 // (two terms there); each is half a step of values that reach the output as a sum with its own half step. Sums and states
 // are fp32.
-template <typename T, int DA, int DC>
-__global__ __launch_bounds__(kThreads, (Head<T, DA, DC>::occupancy)) void outputs(const Args a) {
+//
+// SIDES 2: two outputs of one tile at once, by four waves each, where the second's b is the first's c and its c the first's b
+// (dv and dk, whose states are each other's transposes): four tensors are read instead of six.
+template <typename T, int DA, int DC, int SIDES>
+__global__ __launch_bounds__(SIDES * kThreads, (Head<T, DA, DC>::occupancy)) void outputs(const Args a) {
     typedef Head<T, DA, DC> Hd;
     typedef typename Hd::O O;
     typedef typename O::Quad Quad;
     constexpr int C = Hd::C, CT = Hd::CT, NT = Hd::NT, PARTS = sizeof(T) == 2 ? 2 : 1;
     constexpr int sa = Hd::RA::stride, sb = Hd::RB::stride, sc = Hd::RC::stride, sp = Hd::sp;
+    static_assert(SIDES == 1 || sb == sc, "one side's c is the other's b");
     extern __shared__ u32x4 smem[];
-    typename O::lds_t* la = reinterpret_cast<typename O::lds_t*>(smem);
-    typename O::lds_t *lb = la + C * sa, *lc = lb + C * sb, *lp = lc + C * sc;
     const Tile tile = tile_of(a, blockIdx.x / (uint32_t)a.H);
     if (tile.seq < 0) return;
-    const int h = blockIdx.x % (uint32_t)a.H, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
-    const T* pa = static_cast<const T*>(a.a) + (int64_t)h * a.da;
-    const T* pb = static_cast<const T*>(a.b) + (int64_t)h * a.da;
-    const T* pc = static_cast<const T*>(a.c) + (int64_t)h * a.dc;
-    const int64_t lda = a.lda * (int64_t)sizeof(T), ldb = a.ldb * (int64_t)sizeof(T), ldc = a.ldc * (int64_t)sizeof(T);
-    char* po = reinterpret_cast<char*>(static_cast<T*>(a.out) + (int64_t)h * a.dc);
-    const int64_t size = (int64_t)a.da * a.dc, ldo = a.ldo * (int64_t)sizeof(T);
-    const bool whole = a.dc % 4 == 0;
+    const int h = blockIdx.x % (uint32_t)a.H;
+    const int sd = SIDES == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+    const int wave = __builtin_amdgcn_readfirstlane(thread_id() >> 6);
+    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+    const Args::Side& side = a.side[sd];
+    // [a][b][products] a side, then c (SIDES 2: the other side's b)
+    constexpr int per_side = C * (sa + sb + sp);
+    typename O::lds_t* la = reinterpret_cast<typename O::lds_t*>(smem) + sd * per_side;
+    typename O::lds_t *lb = la + C * sa, *lp = lb + C * sb;
+    typename O::lds_t* lc = SIDES == 1 ? lp + C * sp : lb + (sd == 0 ? per_side : -per_side);
+    const int da = side.da, dc = side.dc;
+    const T* pa = static_cast<const T*>(side.a) + (int64_t)h * da;
+    const T* pb = static_cast<const T*>(side.b) + (int64_t)h * da;
+    const T* pc = static_cast<const T*>(side.c) + (int64_t)h * dc;
+    const int64_t lda = side.lda * (int64_t)sizeof(T), ldb = side.ldb * (int64_t)sizeof(T), ldc = side.ldc * (int64_t)sizeof(T);
+    char* po = reinterpret_cast<char*>(static_cast<T*>(side.out) + (int64_t)h * dc);
+    const int64_t ldo = side.ldo * (int64_t)sizeof(T);
+    const bool whole = dc % 4 == 0;
     typename Hd::RA ra;
     typename Hd::RB rb;
     typename Hd::RC rc;
     const auto load = [&](int k, int n) {
         const int64_t f = tile.from + a.dir * k;
-        ra.load(pa, lda, f, a.dir, n, a.da);
-        rb.load(pb, ldb, f, a.dir, n, a.da);
-        rc.load(pc, ldc, f, a.dir, n, a.dc);
+        ra.load(pa, lda, f, a.dir, n, da);
+        rb.load(pb, ldb, f, a.dir, n, da);
+        if constexpr (SIDES == 1) rc.load(pc, ldc, f, a.dir, n, dc);
     };
     load(0, min(C, tile.len));
-    const float* enter = tile.enter >= 0 ? a.slots + (tile.enter * a.H + h) * size
-                         : a.init ? a.init + ((int64_t)tile.seq * a.H + h) * size : nullptr;
+    const float* enter = tile.enter >= 0 ? a.slots + (tile.enter * a.H + h) * a.size
+                         : a.init ? a.init + ((int64_t)tile.seq * a.H + h) * a.size : nullptr;
     State<DA, Hd::NT> x;
-    if (enter) x.load(a, enter);
+    if (enter) x.load(side, enter);
     else x.clear();
-    zero_fill(la, C * (sa + sb + sc));
+    zero_fill(la, C * (sa + sb));
+    if constexpr (SIDES == 1) zero_fill(lc, C * sc);
     // d^e for the e that occur, in two factors: within 16 (a lane's) and of 16s
     const float l2 = log2_of(a.decay[h]);
     float d16[CT], row_f = power(l2, i + a.post), near[4], far[4], left[4];
@@ -499,9 +526,9 @@ __global__ __launch_bounds__(kThreads, (Head<T, DA, DC>::occupancy)) void output
     for (int k = 0; k < tile.len; k += C) {
         const int n = min(C, tile.len - k), next = min(C, tile.len - k - C);
         __syncthreads();
-        ra.lay(la, n, a.da);
-        rb.lay(lb, n, a.da);
-        rc.lay(lc, n, a.dc);
+        ra.lay(la, n, da);
+        rb.lay(lb, n, da);
+        if constexpr (SIDES == 1) rc.lay(lc, n, dc);
         if (next > 0) load(k + C, next);
         __syncthreads();
         // (a_i . b_j) d^{i-j}: the tiles of 16 x 16 on and below the diagonal, the lowest rows first, dealt out to the
@@ -584,7 +611,7 @@ __global__ __launch_bounds__(kThreads, (Head<T, DA, DC>::occupancy)) void output
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
                 const int col = 16 * (NT * wave + u) + 4 * g;
-                if (col < a.dc) store_quad<T>(reinterpret_cast<T*>(qr) + col, o[it][u] * a.oscale, whole ? 4 : a.dc - col);
+                if (col < dc) store_quad<T>(reinterpret_cast<T*>(qr) + col, o[it][u] * a.oscale, whole ? 4 : dc - col);
             }
         }
         if (next > 0) {  // of a whole block
@@ -596,40 +623,57 @@ __global__ __launch_bounds__(kThreads, (Head<T, DA, DC>::occupancy)) void output
     }
 }
 
-template <typename T, int DA, int DC>
+template <typename T, int DA, int DC, int SIDES>
 constexpr size_t outputs_lds() {
     typedef Head<T, DA, DC> Hd;
-    return sizeof(T) * Hd::C * (Hd::RA::stride + Hd::RB::stride + Hd::RC::stride + Hd::sp);
+    return sizeof(T) * Hd::C * (SIDES * (Hd::RA::stride + Hd::RB::stride + Hd::sp) + (SIDES == 1 ? Hd::RC::stride : 0));
 }
 
-template <typename T, int DA, int DC>
-hipError_t go(const Args& a, int what, hipStream_t st) {
-    const dim3 grid((uint32_t)(((a.T >> a.log_l) + a.S) * a.H)), block(kThreads);  // the heads of a tile side by side
-    if (what == 0) {
-        launch(states<T, DA, DC>, grid, block, 0, st, a);
-    } else {
-        constexpr size_t lds = outputs_lds<T, DA, DC>();
-        if (lds > 65536) {
-            const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(outputs<T, DA, DC>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-            if (e != hipSuccess) return e;
-        }
-        launch(outputs<T, DA, DC>, grid, block, lds, st, a);
+enum { kStates, kOutputs, kBothOutputs };
+template <typename T, int DA, int DC, int SIDES>
+hipError_t go_outputs(const Args& a, dim3 grid, hipStream_t st) {
+    constexpr size_t lds = outputs_lds<T, DA, DC, SIDES>();
+    if (lds > 65536) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(outputs<T, DA, DC, SIDES>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
     }
+    launch(outputs<T, DA, DC, SIDES>, grid, dim3(SIDES * kThreads), lds, st, a);
     return hipGetLastError();
 }
+template <typename T, int DA, int DC>
+hipError_t go(const Args& a, int what, hipStream_t st) {
+    const dim3 grid((uint32_t)(((a.T >> a.log_l) + a.S) * a.H));  // the heads of a tile side by side
+    if (what == kStates) {
+        launch(states<T, DA, DC>, grid, dim3(kThreads), 0, st, a);
+        return hipGetLastError();
+    }
+    if constexpr (DA == DC) {
+        if (what == kBothOutputs) return go_outputs<T, DA, DC, 2>(a, grid, st);
+    }
+    return go_outputs<T, DA, DC, 1>(a, grid, st);
+}
+// the padded size of keys or values
+constexpr int padded(int d) { return d <= 64 ? 64 : 128; }
 template <typename T>
 hipError_t go_sizes(const Args& a, int what, hipStream_t st) {
-    if (a.da <= 64) return a.dc <= 64 ? go<T, 64, 64>(a, what, st) : go<T, 64, 128>(a, what, st);
-    return a.dc <= 64 ? go<T, 128, 64>(a, what, st) : go<T, 128, 128>(a, what, st);
+    const int da = padded(a.side[0].da), dc = padded(a.side[0].dc);
+    if (da == 64) return dc == 64 ? go<T, 64, 64>(a, what, st) : go<T, 64, 128>(a, what, st);
+    return dc == 64 ? go<T, 128, 64>(a, what, st) : go<T, 128, 128>(a, what, st);
 }
 hipError_t go_any(const Args& a, int dtype, int what, hipStream_t st) {
     return dtype == 1 ? go_sizes<bf16>(a, what, st) : go_sizes<float>(a, what, st);
 }
 
+int64_t chain_blocks(int64_t size) {
+    const int64_t lanes = size % 4 == 0 ? size / 4 : size;
+    return (lanes + kThreads - 1) / kThreads;
+}
 hipError_t go_chain(const Args& a, hipStream_t st) {
-    const int per = (int)(((int64_t)a.da * a.dc + kThreads - 1) / kThreads);
-    launch(chain, dim3((uint32_t)((int64_t)a.S * a.H * per)), dim3(kThreads), 0, st, a, per);
+    const int per = (int)chain_blocks(a.size);
+    const dim3 grid((uint32_t)((int64_t)a.S * a.H * per));
+    if (a.size % 4 == 0) launch(chain<4>, grid, dim3(kThreads), 0, st, a, per);
+    else launch(chain<1>, grid, dim3(kThreads), 0, st, a, per);
     return hipGetLastError();
 }
 
@@ -706,15 +750,19 @@ __global__ __launch_bounds__(kThreads) void step(const StepArgs a) {
 
 int linattn_max_d() { return 128; }
 
-// Tiles: long enough that the slots (a state a tile and head) stay few beside the tokens, short enough that there are
-// some workgroups a compute unit.
+// Tiles: as long as leaves some workgroups a compute unit, since a tile costs its state's way to memory and back: up to
+// four times a head's size (a quarter of its tokens' bytes) for two a compute unit, beyond that only for six. At 1000 x 8
+// heads of 64 (fp32, forward) tiles of 64 take 24 us and of 256 43; at 20597 x 8 of 64 (bf16, both ways) 207 and 172; at
+// 208246 x 8 of 128 tiles of 256 take 3141, of 1024 2364 and of 2048 2322.
 AttnPlan attn_plan(int64_t T, int H, int Dk, int Dv) {
     AttnPlan p;
-    while (p.log_l < 11 && (T >> (p.log_l + 1)) * H >= 1024) ++p.log_l;
-    const int64_t state = (int64_t)H * Dk * Dv;
+    p.log_l = 6;
+    const int D = std::max(Dk, Dv);
+    while (p.log_l < 11 && (T >> (p.log_l + 1)) * H >= (2 << p.log_l <= 4 * D ? 512 : 1536)) ++p.log_l;
+    const int64_t size = (int64_t)Dk * Dv;
     p.nslots = T >> p.log_l;
-    p.total = 2 * (((size_t)p.nslots * (size_t)state * sizeof(float) + 15) / 16 * 16);
-    p.chain_blocks = (int64_t)H * ((Dk * (int64_t)Dv + kThreads - 1) / kThreads);
+    p.total = 2 * (((size_t)p.nslots * (size_t)(H * size) * sizeof(float) + 15) / 16 * 16);
+    p.chain_blocks = H * chain_blocks(size);
     return p;
 }
 
@@ -727,7 +775,15 @@ Args args_of(const AttnArgs& x, const AttnPlan& p) {
     a.T = x.T;
     a.log_l = p.log_l;
     a.decay = x.decay;
+    a.size = (int64_t)x.Dk * x.Dv;
     return a;
+}
+struct Rows_ {  // a tensor's rows
+    const void* p;
+    int64_t ld;
+};
+Args::Side side_of(Rows_ a, Rows_ b, Rows_ c, int da, int dc, int trans, void* out, int64_t ldo) {
+    return Args::Side{a.p, b.p, c.p, a.ld, b.ld, c.ld, da, dc, trans, out, ldo};
 }
 }  // namespace
 
@@ -736,87 +792,54 @@ hipError_t launch_attn_fwd(const AttnArgs& x, int dtype, void* ws, hipStream_t s
     Args a = args_of(x, p);
     a.dir = x.reverse ? -1 : 1;
     a.post = 1;
-    a.a = x.q;
-    a.b = x.k;
-    a.c = x.v;
-    a.lda = x.ldq;
-    a.ldb = x.ldk;
-    a.ldc = x.ldv;
-    a.da = x.Dk;
-    a.dc = x.Dv;
     a.pscale = a.sscale = 1.f;
     a.oscale = x.scale;
     a.slots = static_cast<float*>(ws);
     a.init = x.h0;
     a.last = x.hT;
-    a.out = x.y;
-    a.ldo = x.ldy;
+    a.side[0] = side_of({x.q, x.ldq}, {x.k, x.ldk}, {x.v, x.ldv}, x.Dk, x.Dv, 0, x.y, x.ldy);
     hipError_t e = hipSuccess;
-    if (x.T > 0 && (p.nslots > 0 || x.hT) && (e = go_any(a, dtype, 0, st)) != hipSuccess) return e;
-    if ((p.nslots > 0 || x.hT) && (e = go_chain(a, st)) != hipSuccess) return e;
-    return x.T > 0 ? go_any(a, dtype, 1, st) : e;
+    const bool states = p.nslots > 0 || x.hT;
+    if (states && x.T > 0 && (e = go_any(a, dtype, kStates, st)) != hipSuccess) return e;
+    if (states && (e = go_chain(a, st)) != hipSuccess) return e;
+    return x.T > 0 ? go_any(a, dtype, kOutputs, st) : e;
 }
 
 hipError_t launch_attn_bwd(const AttnArgs& x, int dtype, void* ws, hipStream_t st) {
     const AttnPlan p = attn_plan(x.T, x.H, x.Dk, x.Dv);
-    float* fwd = static_cast<float*>(ws);
-    float* bwd = reinterpret_cast<float*>(static_cast<char*>(ws) + p.total / 2);
+    const Rows_ q{x.q, x.ldq}, k{x.k, x.ldk}, v{x.v, x.ldv}, dy{x.dy, x.lddy};
     // the state's gradient, against the forward's order
     Args g = args_of(x, p);
     g.dir = x.reverse ? 1 : -1;
     g.post = 0;
-    g.b = x.q;
-    g.c = x.dy;
-    g.ldb = x.ldq;
-    g.ldc = x.lddy;
-    g.da = x.Dk;
-    g.dc = x.Dv;
-    g.sscale = x.scale;
-    g.slots = bwd;
+    g.pscale = g.sscale = x.scale;
+    g.oscale = 1.f;
+    g.slots = reinterpret_cast<float*>(static_cast<char*>(ws) + p.total / 2);
     g.init = x.dhT;
     g.last = x.dh0;
+    g.side[0] = side_of(k, q, dy, x.Dk, x.Dv, 0, x.dv, x.lddv);
+    g.side[1] = side_of(v, dy, q, x.Dv, x.Dk, 1, x.dk, x.lddk);
     hipError_t e = hipSuccess;
-    if (x.T > 0 && (p.nslots > 0 || x.dh0) && (e = go_any(g, dtype, 0, st)) != hipSuccess) return e;
-    if ((p.nslots > 0 || x.dh0) && (e = go_chain(g, st)) != hipSuccess) return e;
+    const bool states = p.nslots > 0 || x.dh0;
+    if (states && x.T > 0 && (e = go_any(g, dtype, kStates, st)) != hipSuccess) return e;
+    if (states && (e = go_chain(g, st)) != hipSuccess) return e;
     if (x.T == 0) return e;
-    g.pscale = x.scale;
-    g.oscale = 1.f;
-    g.a = x.k;
-    g.lda = x.ldk;
-    g.out = x.dv;
-    g.ldo = x.lddv;
-    if ((e = go_any(g, dtype, 1, st)) != hipSuccess) return e;
-    g.a = x.v;
-    g.b = x.dy;
-    g.c = x.q;
-    g.lda = x.ldv;
-    g.ldb = x.lddy;
-    g.ldc = x.ldq;
-    g.da = x.Dv;
-    g.dc = x.Dk;
-    g.trans = 1;
-    g.out = x.dk;
-    g.ldo = x.lddk;
-    if ((e = go_any(g, dtype, 1, st)) != hipSuccess) return e;
+    if (padded(x.Dk) == padded(x.Dv)) {
+        if ((e = go_any(g, dtype, kBothOutputs, st)) != hipSuccess) return e;
+    } else {
+        if ((e = go_any(g, dtype, kOutputs, st)) != hipSuccess) return e;
+        g.side[0] = g.side[1];
+        if ((e = go_any(g, dtype, kOutputs, st)) != hipSuccess) return e;
+    }
     Args f = args_of(x, p);
     f.dir = x.reverse ? -1 : 1;
     f.post = 1;
-    f.a = x.dy;
-    f.b = x.v;
-    f.c = x.k;
-    f.lda = x.lddy;
-    f.ldb = x.ldv;
-    f.ldc = x.ldk;
-    f.da = x.Dv;
-    f.dc = x.Dk;
-    f.trans = 1;
     f.pscale = f.sscale = 1.f;
     f.oscale = x.scale;
-    f.slots = fwd;
+    f.slots = static_cast<float*>(ws);
     f.init = x.h0;
-    f.out = x.dq;
-    f.ldo = x.lddq;
-    return go_any(f, dtype, 1, st);
+    f.side[0] = side_of(dy, v, k, x.Dv, x.Dk, 1, x.dq, x.lddq);
+    return go_any(f, dtype, kOutputs, st);
 }
 
 hipError_t launch_attn_step(const AttnArgs& x, int dtype, const int32_t* slots, int n_slots, const float* h_in,

@@ -379,7 +379,7 @@ struct AttnArgs {
     float *hT, *dh0;                // [S][H][Dk][Dv] or null
 };
 struct AttnPlan {
-    int log_l = 8;                  // log2 of the tokens a tile
+    int log_l = 0;                  // log2 of the tokens a tile
     int64_t nslots = 0;             // tile boundaries, states of H heads each
     int64_t chain_blocks = 0;       // workgroups a sequence
     size_t total = 0;               // bytes of both directions' slots

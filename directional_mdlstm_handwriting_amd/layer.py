@@ -180,10 +180,12 @@ def flat_input(xs: Sequence[np.ndarray], x_dtype: str, device) -> torch.Tensor:
 
 
 class PackedStack:
-    """MDLSTM -> block conv -> MDLSTM -> block conv -> MDLSTM, re-packed per level."""
+    """MDLSTM -> block conv -> MDLSTM -> block conv -> MDLSTM, re-packed per level. With `dropout` above 0 (the pages train
+    with dropout), what a level after the first reads is dropped with that probability; a backward takes the masks of the
+    forward before it, and advance_dropout() before the next step draws new ones."""
 
     def __init__(self, heights, widths, C: int, Hs: Sequence[int], couts: Sequence[int], canvas_w_min: Sequence[int],
-                 sep: int = 1, kh: int = 2, kw: int = 4, device: str = "cuda"):
+                 sep: int = 1, kh: int = 2, kw: int = 4, device: str = "cuda", dropout: float = 0.0, seed: int = 0):
         self.kh, self.kw = kh, kw
         self.levels: List[PackedLayer] = []
         c_in = C
@@ -205,13 +207,32 @@ class PackedStack:
             self.conv_ws.append((torch.empty(max(nb, 4), dtype=torch.uint8, device=device), nb))
             self.dx_canvas.append(torch.empty_like(lk1.x_canvas, dtype=torch.float32))
             self.dh_dirs.append(torch.empty_like(lk.h_dirs))
+        self.drops = []
+        if dropout != 0.0:
+            for lvl, lay in enumerate(self.levels[1:]):
+                Hc, Wc, cin = lay.x_canvas.shape
+                self.drops.append(Dropout(Hc * Wc, cin, dropout, "f32", seed=seed, call=lvl, device=device))
+        self._dropped = False
 
     @property
     def level_sizes(self):
         """Per level, the (heights, widths) of its examples."""
         return [lay.dl.sizes() for lay in self.levels]
 
-    def forward(self, x_flat, params: Sequence[DeviceParams], convs, stream=None):
+    def advance_dropout(self, stream=None):
+        """New masks from here on, other ones for each level and step."""
+        for d in self.drops:
+            d.advance(len(self.drops), stream)
+
+    def _drop(self, lvl: int, canvas: torch.Tensor, backward: bool, stream):
+        """The canvas that level `lvl` reads, or its gradient, in place."""
+        d = self.drops[lvl - 1]
+        flat = canvas.view(d.N, d.D)
+        (d.backward if backward else d.forward)(flat, out=flat, stream=stream)
+
+    def forward(self, x_flat, params: Sequence[DeviceParams], convs, stream=None, train: bool = True):
+        """train False: nothing is dropped (the backward of such a forward drops nothing either)."""
+        self._dropped = bool(self.drops) and train
         L0 = self.levels[0]
         L0.scatter(x_flat, stream)
         for lvl, lay in enumerate(self.levels):
@@ -221,6 +242,8 @@ class PackedStack:
                 W, b = convs[lvl]
                 mdl_blockconv_forward(lay.dl.layout, lay.dl.desc, nxt.dl.layout, nxt.dl.desc, lay.h_dirs, lay.H,
                                       self.kh, self.kw, W, b, self.couts[lvl], nxt.x_canvas, stream)
+                if self._dropped:
+                    self._drop(lvl + 1, nxt.x_canvas, False, stream)
         self.levels[-1].dirsum(stream)
         return self.levels[-1].y
 
@@ -243,6 +266,8 @@ class PackedStack:
                 W, _ = convs[lvl - 1]
                 dW, db = cgrads[lvl - 1]
                 wsb, nb = self.conv_ws[lvl - 1]
+                if self._dropped:
+                    self._drop(lvl, self.dx_canvas[lvl - 1], True, stream)
                 mdl_blockconv_backward(prev.dl.layout, prev.dl.desc, lay.dl.layout, lay.dl.desc, prev.h_dirs, prev.H,
                                        self.kh, self.kw, W, self.couts[lvl - 1], self.dx_canvas[lvl - 1],
                                        self.dh_dirs[lvl - 1], dW, db, wsb, nb, stream)

@@ -3,10 +3,14 @@
 //
 //   z = h W^T,  loss_n = w_n (ln sum_c exp z_nc - z_n,id),  G = w (softmax z - [c = id]),  dh = G W,  dW = G^T h
 //
-// A first product over the whole vocabulary leaves per row and 256 (or 128) classes their maximum and sum of exponentials,
-// and the target's logit; `join` makes the losses of them. Then, piece of the vocabulary by piece, a second product of the
-// same operands forms G of the piece (its values rounded once to the inputs' type), and two more take it into dh and dW.
-// So the memory held is that of one piece, and the work is 8 N V D operations where 6 N V D are the least.
+// A first product leaves per row and 256 (or 128) classes their maximum and sum of exponentials, and the target's logit;
+// `join` makes the losses of them. What the gradients then need of the logits is held for a piece of them at a time, up to 128
+// MB, in one of two ways. Logits kept: the first product, a block of rows at a time, also writes the block's logits (fp32),
+// `grad` makes G of them, and two products take G into dh and dW: 6 N V D operations. Logits formed again: behind the first
+// product over all rows, piece of the vocabulary by piece, a second one of the same operands forms G of the piece, and two
+// more take it into dh and dW: 8 N V D operations, but nothing is written that is not G. Kept are they where one block takes
+// all rows, and for fp32 always, whose products are the dearer half: 4096 x 2048 over 32000 classes in fp32 takes 15.6 ms
+// with the logits formed again. Several blocks in bfloat16 would have dW's sums read and written once a block.
 //
 // Products: tiles of BM x BN by 8 (4) waves, 32 x 32 results of the matrix instructions (32x32x16 bfloat16, 32x32x2 fp32),
 // 128 bytes of depth at a time from global memory straight into LDS, one step ahead of the products. An operand whose rows
@@ -139,6 +143,8 @@ struct Shape {  // waves down and across, 32 x 32 tiles of a wave down and acros
 };
 typedef Shape<2, 4, 4, 2> Large;  // 256 x 256
 typedef Shape<2, 2, 2, 2> Small;  // 128 x 128
+typedef Shape<1, 4, 1, 1> Thin;   // 32 x 128
+enum Size { kLarge, kSmall, kThin };
 
 // 128 bytes of depth of a wave's tiles: a quarter's operands are read while the products of the one before run
 template <typename S, typename TA, typename TB>
@@ -169,6 +175,7 @@ struct Args {
     int64_t tiles_m, tiles_n, splits;
     // epilogues
     float2* stats;                // [tiles_n][M] maximum and sum
+    float* logits;                // [M] at ldo, or null
     float *target, *lse;          // [M]
     const int32_t* ids;           // [M] -1: none
     const float* coef;            // [M]
@@ -180,6 +187,42 @@ struct Args {
 };
 
 enum { kStats, kGrad, kStore, kSlab };
+
+// A wave's tiles as they lie, four neighbours of a row a lane; onto what is there with `add` (fp32 alone).
+template <typename S, typename E>
+__device__ inline void store_direct(const f32x16 (&c)[S::TM][S::TN], E* out, int64_t ldo, int64_t cols, bool add, int64_t M,
+                                    int64_t m0, int64_t n0, int wm) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i) {
+        const int64_t m = m0 + wm + 32 * i + (lane & 31);
+        if (m >= M) continue;
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const int64_t n = n0 + 32 * j + 2 * e + 4 * (lane >> 5);
+                E* o = out + m * ldo + n;
+                f32x4 v = {c[i][j][e], c[i][j][e + 1], c[i][j][e + 2], c[i][j][e + 3]};
+                if constexpr (sizeof(E) == 2) {
+                    typedef u32x2 u32x2_e __attribute__((aligned(2), may_alias));
+                    const u32x2 q = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                    if (n + 4 <= cols) *reinterpret_cast<u32x2_e*>(o) = q;
+                    else
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (n + r < cols) o[r].u = (uint16_t)(q[r >> 1] >> (16 * (r & 1)));
+                } else if (n + 4 <= cols) {
+                    if (add) v += *reinterpret_cast<const f32x4_e*>(o);
+                    *reinterpret_cast<f32x4_e*>(o) = v;
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (n + r < cols) o[r] = add ? o[r] + v[r] : v[r];
+                }
+            }
+    }
+}
 
 template <typename T, typename S, bool AA, bool BA, int EPI>
 __global__ __launch_bounds__(S::threads, 2) void product(const Args g) {
@@ -226,6 +269,7 @@ __global__ __launch_bounds__(S::threads, 2) void product(const Args g) {
         tb.load(b1);
         one_step<T, S, TA, TB>(a0, b0, wm, wn, c);
         __syncthreads();
+        if (S::TM * S::TN <= 4 && t + 1 >= s1) break;  // (in the large tiles a branch here costs registers)
         ta.load(a0);
         tb.load(b0);
         one_step<T, S, TA, TB>(a1, b1, wm, wn, c);
@@ -233,6 +277,7 @@ __global__ __launch_bounds__(S::threads, 2) void product(const Args g) {
     }
     // A lane holds row lane % 32 of each of its tiles, columns 8 (e / 4) + 4 h + e % 4.
     if constexpr (EPI == kStats) {
+        if (g.logits) store_direct<S>(c, g.logits, g.ldo, g.N, false, g.M, m0, n0 + wn, wm);
         float2* part = reinterpret_cast<float2*>(a0);  // [WN][BM]; all reads of the tiles are done
         const int64_t limit = g.N - n0;
 #pragma unroll
@@ -286,7 +331,7 @@ __global__ __launch_bounds__(S::threads, 2) void product(const Args g) {
                     }
             }
         }
-        if constexpr (sizeof(T) == 2 && EPI != kSlab) {
+        if constexpr (sizeof(T) == 2 && EPI != kSlab && S::TM * S::TN > 1) {
             // Through LDS, so that whole lines leave: a quarter (half) of the tile's rows in each array, their 16-byte
             // chunks rotated by the row.
             constexpr int chunks = S::BN / 8;
@@ -325,44 +370,26 @@ __global__ __launch_bounds__(S::threads, 2) void product(const Args g) {
                 }
             }
         } else {
-            // fp32: four neighbours a lane
-            float* out = EPI == kSlab ? g.slab + split * g.M * g.N : reinterpret_cast<float*>(g.out);
-            const int64_t ldo = EPI == kSlab ? g.N : g.ldo, cols = EPI == kSlab ? g.N : g.cols;
-            const bool add = EPI == kSlab && g.add;
-#pragma unroll
-            for (int i = 0; i < S::TM; ++i) {
-                const int64_t m = m0 + wm + 32 * i + (lane & 31);
-                if (m >= g.M) continue;
-#pragma unroll
-                for (int j = 0; j < S::TN; ++j)
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const int64_t n = n0 + wn + 32 * j + 2 * e + 4 * h;
-                        float* o = out + m * ldo + n;
-                        f32x4 v = {c[i][j][e], c[i][j][e + 1], c[i][j][e + 2], c[i][j][e + 3]};
-                        if (n + 4 <= cols) {
-                            if (add) v += *reinterpret_cast<const f32x4_e*>(o);
-                            *reinterpret_cast<f32x4_e*>(o) = v;
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (n + r < cols) o[r] = add ? o[r] + v[r] : v[r];
-                        }
-                    }
-            }
+            if constexpr (EPI == kSlab)
+                store_direct<S>(c, g.slab + split * g.M * g.N, g.N, g.N, g.add != 0, g.M, m0, n0 + wn, wm);
+            else
+                store_direct<S>(c, static_cast<T*>(g.out), g.ldo, g.cols, false, g.M, m0, n0 + wn, wm);
         }
     }
 }
 
-template <typename T, bool AA, bool BA, int EPI>
-void go(Args g, bool large, int64_t splits, hipStream_t st) {
-    const int64_t bm = large ? Large::BM : Small::BM, bn = large ? Large::BN : Small::BN;
-    g.tiles_m = (g.M + bm - 1) / bm;
-    g.tiles_n = (g.N + bn - 1) / bn;
+template <typename T, typename S, bool AA, bool BA, int EPI>
+void go_shape(Args g, int64_t splits, hipStream_t st) {
+    g.tiles_m = (g.M + S::BM - 1) / S::BM;
+    g.tiles_n = (g.N + S::BN - 1) / S::BN;
     g.splits = splits;
-    const dim3 grid((uint32_t)(g.tiles_m * g.tiles_n * splits));
-    if (large) launch(product<T, Large, AA, BA, EPI>, grid, dim3(Large::threads), 0, st, g);
-    else launch(product<T, Small, AA, BA, EPI>, grid, dim3(Small::threads), 0, st, g);
+    launch(product<T, S, AA, BA, EPI>, dim3((uint32_t)(g.tiles_m * g.tiles_n * splits)), dim3(S::threads), 0, st, g);
+}
+template <typename T, bool AA, bool BA, int EPI>
+void go(const Args& g, Size size, int64_t splits, hipStream_t st) {
+    if (size == kLarge) go_shape<T, Large, AA, BA, EPI>(g, splits, st);
+    else if (size == kSmall || !AA) go_shape<T, Small, AA, BA, EPI>(g, splits, st);
+    else if constexpr (AA) go_shape<T, Thin, AA, BA, EPI>(g, splits, st);
 }
 
 // ---- the rows before and after ------------------------------------------------------------------------------------
@@ -418,6 +445,27 @@ __global__ __launch_bounds__(256) void join(const float2* stats, int64_t tiles, 
     loss[n] = id >= 0 ? coef[n] * (l - target_logit[n]) : (id == -1 ? 0.f : NAN);
 }
 
+// G of a block of rows from its logits, eight neighbours a thread; zeros past the classes. fp32: over the logits.
+template <typename T>
+__global__ __launch_bounds__(256) void grad(const float* z, int64_t ld, int64_t rows, int V, const float* lse, const float* coef,
+                                            const int32_t* target, T* out) {
+    const uint32_t per = (uint32_t)(ld / 8), i = blockIdx.x * 256u + threadIdx.x, m = i / per;
+    if (m >= rows) return;
+    const int v = (int)(i - m * per) * 8, id = target[m];
+    const float l = lse[m], k = coef[m];
+    float x[8];
+    load_f32<8>(z + m * ld + v, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        x[e] = k == 0.f || v + e >= V ? 0.f : k * (exp_neg<T>(x[e] - l) - (v + e == id ? 1.f : 0.f));
+    T* o = out + m * ld + v;
+    if constexpr (sizeof(T) == 4) {
+        store_f32<8>(o, x);
+    } else {
+        *reinterpret_cast<u32x4*>(o) = u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+    }
+}
+
 template <typename T>
 __global__ __launch_bounds__(256) void clear(T* p, int64_t n) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -461,15 +509,18 @@ void go_sum(const float* slab, int64_t slabs, int64_t M, int64_t N, T* out, int6
 // ---- plan ---------------------------------------------------------------------------------------------------------
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-// the larger tiles where they fill the compute units
-bool large_tiles(int64_t M, int64_t N) {
-    return ((M + 255) / 256) * ((N + 255) / 256) >= 192;
+// The larger tiles where they fill the compute units; the thin ones for few rows: those of 128 would spend most of their
+// products on rows that are not there, which fp32 feels first.
+Size size_of(int64_t M, int64_t N, int64_t K, int e, bool along) {
+    if (((M + 255) / 256) * ((N + 255) / 256) >= 192 && K * e > 3 * 128) return kLarge;
+    return along && M <= (e == 4 ? 64 : 32) ? kThin : kSmall;
 }
 // how often the depth is split where there are few tiles: so that some 512 workgroups share the work, none with less than
 // four steps of it
-int64_t splits_of(int64_t M, int64_t N, int64_t K, int e) {
-    if (large_tiles(M, N)) return 1;
-    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128), steps = (K * e + 127) / 128;
+int64_t splits_of(int64_t M, int64_t N, int64_t K, int e, bool along) {
+    const Size size = size_of(M, N, K, e, along);
+    if (size == kLarge) return 1;
+    const int64_t bm = size == kThin ? 32 : 128, tiles = ((M + bm - 1) / bm) * ((N + 127) / 128), steps = (K * e + 127) / 128;
     return std::max<int64_t>(1, std::min<int64_t>({512 / tiles, steps / 4, int64_t(64)}));
 }
 
@@ -480,14 +531,30 @@ int64_t vocab_max_classes() { return int64_t(1) << 20; }
 int vocab_max_d() { return 1 << 16; }
 
 // Workspace: the hidden states as they meet the products, the weights too where their rows are no whole number of chunks,
-// the tiles' statistics, a row's numbers, and with gradients a piece of G, dh's slabs and dW's.
+// the tiles' statistics, a row's numbers, and with gradients a block of logits or a piece of G (or both), dh's slabs and dW's.
 VocabPlan vocab_plan(int64_t N, int D, int V, int dtype, bool grads) {
     const int e = dtype == 1 ? 2 : 4, chunk = 16 / e;
+    constexpr int64_t kHeld = int64_t(128) << 20;
     VocabPlan p;
     p.ldh = up(D, chunk);
     p.pack_w = D % chunk != 0;
-    p.large = large_tiles(N, V);
-    p.tiles = (V + (p.large ? 255 : 127)) / (p.large ? 256 : 128);
+    p.rows = std::max<int64_t>(N, 1);
+    p.piece = up(V, 256);
+    grads = grads && N > 0;
+    if (grads) {
+        const int64_t fit = std::max<int64_t>(kHeld / 4 / V / 128 * 128, 128);
+        p.keep = e == 4 || N <= fit;
+        if (p.keep) {
+            const int64_t blocks = (N + fit - 1) / fit;
+            p.rows = std::min(N, up((N + blocks - 1) / blocks, 128));
+            p.piece = up(V, 8);
+        } else {  // at least 2048 classes
+            p.piece = std::min(p.piece, std::max<int64_t>(2048, kHeld / (N * e) / 256 * 256));
+            const int64_t pieces = (V + p.piece - 1) / p.piece;
+            p.piece = up((V + pieces - 1) / pieces, 256);
+        }
+    }
+    p.tiles = (V + 127) / 128;  // at most
     size_t at = 0;
     const auto take = [&](size_t bytes) {
         const size_t o = at;
@@ -496,129 +563,166 @@ VocabPlan vocab_plan(int64_t N, int D, int V, int dtype, bool grads) {
     };
     p.h = take((size_t)N * p.ldh * e);
     p.w = take(p.pack_w ? (size_t)V * p.ldh * e : 0);
-    p.stats = take((size_t)p.tiles * N * sizeof(float2));
+    p.stats = take((size_t)p.tiles * p.rows * sizeof(float2));
     p.lse = take((size_t)N * 4);
     p.target_logit = take((size_t)N * 4);
     p.target = take((size_t)N * 4);
     p.coef = take((size_t)N * 4);
-    if (grads && N > 0) {
-        // a piece of G holds up to 128 MB, so that it stays in the cache between the products; at least 2048 classes
-        const int64_t fit = (int64_t(128) << 20) / (N * e) / 256 * 256;
-        p.piece = std::min<int64_t>(up(V, 256), std::max<int64_t>(2048, fit));
-        const int64_t pieces = (V + p.piece - 1) / p.piece;
-        p.piece = up((V + pieces - 1) / pieces, 256);
-        p.dh_splits = splits_of(N, D, p.piece, e);
-        p.dw_splits = splits_of(p.piece, D, N, e);
-        p.g = take((size_t)N * p.piece * e);
-        p.dh_slab = p.dh_splits > 1 || p.piece < V;
-        p.dh = take(p.dh_slab ? (size_t)p.dh_splits * N * D * 4 : 0);
-        p.dw = take(p.dw_splits > 1 ? (size_t)p.dw_splits * p.piece * D * 4 : 0);
+    if (grads) {
+        const int64_t cols = std::min<int64_t>(p.piece, V);
+        p.dh_splits = splits_of(p.rows, D, cols, e, true);
+        p.dw_splits = splits_of(cols, D, p.rows, e, false);
+        p.logits = take(p.keep ? (size_t)p.rows * p.piece * 4 : 0);
+        p.g = p.keep && e == 4 ? p.logits : take((size_t)p.rows * p.piece * e);
+        p.dh_slab = p.dh_splits > 1 || cols < V;
+        p.dh = take(p.dh_slab ? (size_t)p.dh_splits * p.rows * D * 4 : 0);
+        p.dw = take(p.dw_splits > 1 ? (size_t)p.dw_splits * cols * D * 4 : 0);
     }
     p.total = at;
     return p;
 }
 
+namespace {
+
 template <typename T>
-static hipError_t vocab_loss(const VocabArgs& x, int dtype, void* ws, hipStream_t st) {
-    const bool grads = x.dW != nullptr;
-    const VocabPlan p = vocab_plan(x.N, x.D, x.V, dtype, grads);
-    char* w = static_cast<char*>(ws);
-    T* h = reinterpret_cast<T*>(w + p.h);
-    const T* W = static_cast<const T*>(x.W);
-    int32_t* target = reinterpret_cast<int32_t*>(w + p.target);
-    float* coef = reinterpret_cast<float*>(w + p.coef);
-    float* lse = reinterpret_cast<float*>(w + p.lse);
-    if (x.N > 0)
-        launch(pack<T, true>, dim3((uint32_t)((x.N + 3) / 4)), dim3(256), 0, st, static_cast<const T*>(x.h), x.ldh, x.N, x.D, h,
-               p.ldh, x.ids, x.w, x.V, target, coef);
-    if (p.pack_w && x.N > 0) {
-        T* to = reinterpret_cast<T*>(w + p.w);
-        launch(pack<T, false>, dim3((uint32_t)((x.V + 3) / 4)), dim3(256), 0, st, W, (int64_t)x.D, (int64_t)x.V, x.D, to, p.ldh,
-               static_cast<const int32_t*>(nullptr), static_cast<const float*>(nullptr), 0, static_cast<int32_t*>(nullptr),
-               static_cast<float*>(nullptr));
-        W = to;
+struct Vocab {
+    const VocabArgs& x;
+    const VocabPlan& p;
+    char* ws;
+    const T* W;  // rows of ldh
+    hipStream_t st;
+
+    template <typename U>
+    U* at(size_t o, int64_t i = 0) const {
+        return reinterpret_cast<U*>(ws + o) + i;
     }
-    if (x.N > 0) {
+    // the logits of rows r0 .. against classes v0 ..
+    Args logits(int64_t r0, int64_t rows, int64_t v0, int64_t cols) const {
         Args a{};
-        a.a = h;
-        a.b = W;
+        a.a = at<T>(p.h, r0 * p.ldh);
+        a.b = W + v0 * p.ldh;
         a.lda = a.ldb = p.ldh;
-        a.M = x.N;
-        a.N = x.V;
+        a.M = rows;
+        a.N = cols;
         a.K = x.D;
-        a.stats = reinterpret_cast<float2*>(w + p.stats);
-        a.target = reinterpret_cast<float*>(w + p.target_logit);
-        a.ids = target;
-        go<T, true, true, kStats>(a, p.large, 1, st);
-        launch(join, dim3((uint32_t)((x.N + 7) / 8)), dim3(256), 0, st, a.stats, p.tiles, x.N, a.target, target, coef, lse,
-               x.loss);
-    }
-    if (!grads) return hipGetLastError();
-    if (x.N == 0) {
-        const int64_t n = (int64_t)x.V * x.D;
-        launch(clear<T>, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, st, static_cast<T*>(x.dW), n);
-        return hipGetLastError();
-    }
-    T* G = reinterpret_cast<T*>(w + p.g);
-    float* dh_slab = reinterpret_cast<float*>(w + p.dh);
-    for (int64_t v0 = 0; v0 < x.V; v0 += p.piece) {
-        const int64_t nv = std::min<int64_t>(p.piece, x.V - v0);
-        const T* Wp = W + v0 * p.ldh;
-        Args a{};
-        a.a = h;
-        a.b = Wp;
-        a.lda = a.ldb = p.ldh;
-        a.M = x.N;
-        a.N = nv;
-        a.K = x.D;
-        a.lse = lse;
-        a.ids = target;
-        a.coef = coef;
+        a.ids = at<int32_t>(p.target, r0);
         a.n_first = v0;
-        a.out = G;
         a.ldo = p.piece;
-        a.cols = up(nv, 16 / (int64_t)sizeof(T));
-        go<T, true, true, kGrad>(a, large_tiles(x.N, nv), 1, st);
+        return a;
+    }
+    Size size(const Args& a, bool along) const { return size_of(a.M, a.N, a.K, sizeof(T), along); }
+    // losses of rows r0 .., their logits kept where there is a place for them
+    void losses(int64_t r0, int64_t rows, bool keep) const {
+        Args a = logits(r0, rows, 0, x.V);
+        a.stats = at<float2>(p.stats);
+        a.target = at<float>(p.target_logit, r0);
+        if (keep) a.logits = at<float>(p.logits);
+        const Size s = size(a, true);
+        go<T, true, true, kStats>(a, s, 1, st);
+        const int64_t tiles = (x.V + (s == kLarge ? 255 : 127)) / (s == kLarge ? 256 : 128);
+        launch(join, dim3((uint32_t)((rows + 7) / 8)), dim3(256), 0, st, a.stats, tiles, rows, a.target, a.ids,
+               at<float>(p.coef, r0), at<float>(p.lse, r0), x.loss + r0);
+    }
+    // G of rows r0 .. and classes v0 .. is at p.g: into dh (first, last: of the pieces) and dW (the same, of the blocks)
+    void take(int64_t r0, int64_t rows, int64_t v0, int64_t cols, bool first_piece, bool last_piece, bool first_block,
+              bool last_block) const {
+        const T* G = at<T>(p.g);
         Args b{};
         b.a = G;
-        b.b = Wp;
+        b.b = W + v0 * p.ldh;
         b.lda = p.piece;
         b.ldb = p.ldh;
-        b.M = x.N;
+        b.M = rows;
         b.N = x.D;
-        b.K = nv;
-        b.out = x.dh;
+        b.K = cols;
+        T* dh = static_cast<T*>(x.dh) + r0 * x.lddh;
+        b.out = dh;
         b.ldo = x.lddh;
         b.cols = x.D;
-        b.slab = dh_slab;
-        b.add = v0 > 0;
-        if (p.dh_slab) go<T, true, false, kSlab>(b, large_tiles(x.N, x.D), p.dh_splits, st);
-        else go<T, true, false, kStore>(b, large_tiles(x.N, x.D), 1, st);
+        b.slab = at<float>(p.dh);
+        b.add = !first_piece;
+        const Size sh = size_of(p.rows, x.D, std::min<int64_t>(p.piece, x.V), sizeof(T), true);
+        if (p.dh_slab) go<T, true, false, kSlab>(b, sh, p.dh_splits, st);
+        else go<T, true, false, kStore>(b, sh, 1, st);
+        if (p.dh_slab && last_piece) go_sum(b.slab, p.dh_splits, rows, x.D, dh, x.lddh, st);
+
         Args c{};
         c.a = G;
-        c.b = h;
+        c.b = at<T>(p.h, r0 * p.ldh);
         c.lda = p.piece;
         c.ldb = p.ldh;
-        c.M = nv;
+        c.M = cols;
         c.N = x.D;
-        c.K = x.N;
+        c.K = rows;
         T* dW = static_cast<T*>(x.dW) + v0 * x.D;
         c.out = dW;
         c.ldo = x.D;
         c.cols = x.D;
-        c.slab = reinterpret_cast<float*>(w + p.dw);
-        const bool large = large_tiles(p.piece, x.D);
+        c.add = !first_block;
+        const Size sw = size_of(std::min<int64_t>(p.piece, x.V), x.D, p.rows, sizeof(T), false);
         if (p.dw_splits > 1) {
-            go<T, false, false, kSlab>(c, large, p.dw_splits, st);
-            go_sum(c.slab, p.dw_splits, nv, x.D, dW, x.D, st);
+            c.slab = at<float>(p.dw);
+            go<T, false, false, kSlab>(c, sw, p.dw_splits, st);
+            if (last_block) go_sum(c.slab, p.dw_splits, cols, x.D, dW, x.D, st);
+        } else if (sizeof(T) == 4 && !(first_block && last_block)) {
+            c.slab = reinterpret_cast<float*>(dW);  // blocks are several in fp32 alone: dW is its own slab
+            go<T, false, false, kSlab>(c, sw, 1, st);
         } else {
-            go<T, false, false, kStore>(c, large, 1, st);
+            go<T, false, false, kStore>(c, sw, 1, st);
         }
     }
-    if (p.dh_slab)
-        go_sum(dh_slab, p.dh_splits, x.N, x.D, static_cast<T*>(x.dh), x.lddh, st);
+
+    void run(bool grads) const {
+        if (!p.keep) losses(0, x.N, false);
+        if (!grads) return;
+        if (p.keep) {
+            for (int64_t r0 = 0; r0 < x.N; r0 += p.rows) {
+                const int64_t rows = std::min(p.rows, x.N - r0);
+                losses(r0, rows, true);
+                const int64_t n = rows * (p.piece / 8);
+                launch(grad<T>, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, st, at<float>(p.logits), p.piece, rows, x.V,
+                       at<float>(p.lse, r0), at<float>(p.coef, r0), at<int32_t>(p.target, r0), at<T>(p.g));
+                take(r0, rows, 0, x.V, true, true, r0 == 0, r0 + rows == x.N);
+            }
+            return;
+        }
+        for (int64_t v0 = 0; v0 < x.V; v0 += p.piece) {
+            const int64_t cols = std::min<int64_t>(p.piece, x.V - v0);
+            Args a = logits(0, x.N, v0, cols);
+            a.lse = at<float>(p.lse);
+            a.coef = at<float>(p.coef);
+            a.out = at<T>(p.g);
+            a.cols = up(cols, 16 / (int64_t)sizeof(T));
+            go<T, true, true, kGrad>(a, size(a, true), 1, st);
+            take(0, x.N, v0, cols, v0 == 0, v0 + cols == x.V, true, true);
+        }
+    }
+};
+
+template <typename T>
+hipError_t vocab_loss(const VocabArgs& x, int dtype, void* ws, hipStream_t st) {
+    const bool grads = x.dW != nullptr;
+    if (x.N == 0) {
+        const int64_t n = (int64_t)x.V * x.D;
+        if (grads) launch(clear<T>, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, st, static_cast<T*>(x.dW), n);
+        return hipGetLastError();
+    }
+    const VocabPlan p = vocab_plan(x.N, x.D, x.V, dtype, grads);
+    Vocab<T> v{x, p, static_cast<char*>(ws), static_cast<const T*>(x.W), st};
+    launch(pack<T, true>, dim3((uint32_t)((x.N + 3) / 4)), dim3(256), 0, st, static_cast<const T*>(x.h), x.ldh, x.N, x.D,
+           v.template at<T>(p.h), p.ldh, x.ids, x.w, x.V, v.template at<int32_t>(p.target), v.template at<float>(p.coef));
+    if (p.pack_w) {
+        T* to = v.template at<T>(p.w);
+        launch(pack<T, false>, dim3((uint32_t)((x.V + 3) / 4)), dim3(256), 0, st, v.W, (int64_t)x.D, (int64_t)x.V, x.D, to, p.ldh,
+               static_cast<const int32_t*>(nullptr), static_cast<const float*>(nullptr), 0, static_cast<int32_t*>(nullptr),
+               static_cast<float*>(nullptr));
+        v.W = to;
+    }
+    v.run(grads);
     return hipGetLastError();
 }
+
+}  // namespace
 
 hipError_t launch_vocab(const VocabArgs& x, int dtype, void* ws, hipStream_t st) {
     return dtype == 1 ? vocab_loss<bf16>(x, dtype, ws, st) : vocab_loss<float>(x, dtype, ws, st);

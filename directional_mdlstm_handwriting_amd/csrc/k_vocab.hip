@@ -4,8 +4,8 @@
 //   z = h W^T,  loss_n = w_n (ln sum_c exp z_nc - z_n,id),  G = w (softmax z - [c = id]),  dh = G W,  dW = G^T h
 //
 // A first product leaves per row and 256 (or 128) classes their maximum and sum of exponentials, and the target's logit;
-// `join` makes the losses of them. What the gradients then need of the logits is held for a piece of them at a time, up to 128
-// MB, in one of two ways. Logits kept: the first product, a block of rows at a time, also writes the block's logits (fp32),
+// `join` makes the losses of them. What the gradients then need of the logits is held for a piece of them at a time, in one of two
+// ways. Logits kept: the first product, a block of rows at a time, also writes the block's logits (fp32),
 // `grad` makes G of them, and two products take G into dh and dW: 6 N V D operations. Logits formed again: behind the first
 // product over all rows, piece of the vocabulary by piece, a second one of the same operands forms G of the piece, and two
 // more take it into dh and dW: 8 N V D operations, but nothing is written that is not G. Kept are they where one block takes
@@ -512,8 +512,9 @@ int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 // The larger tiles where they fill the compute units; the thin ones for few rows: those of 128 would spend most of their
 // products on rows that are not there, which fp32 feels first.
 Size size_of(int64_t M, int64_t N, int64_t K, int e, bool along) {
-    if (((M + 255) / 256) * ((N + 255) / 256) >= 192 && K * e > 3 * 128) return kLarge;
-    return along && M <= (e == 4 ? 64 : 32) ? kThin : kSmall;
+    if (along && M <= (e == 4 ? 64 : 32)) return kThin;
+    const bool fills = ((M + 255) / 256) * ((N + 255) / 256) >= 192;
+    return fills && M > 128 && N > 128 && K * e > 3 * 128 ? kLarge : kSmall;
 }
 // how often the depth is split where there are few tiles: so that some 512 workgroups share the work, none with less than
 // four steps of it
@@ -534,7 +535,7 @@ int vocab_max_d() { return 1 << 16; }
 // the tiles' statistics, a row's numbers, and with gradients a block of logits or a piece of G (or both), dh's slabs and dW's.
 VocabPlan vocab_plan(int64_t N, int D, int V, int dtype, bool grads) {
     const int e = dtype == 1 ? 2 : 4, chunk = 16 / e;
-    constexpr int64_t kHeld = int64_t(128) << 20;
+    constexpr int64_t kMB = int64_t(1) << 20;
     VocabPlan p;
     p.ldh = up(D, chunk);
     p.pack_w = D % chunk != 0;
@@ -542,14 +543,16 @@ VocabPlan vocab_plan(int64_t N, int D, int V, int dtype, bool grads) {
     p.piece = up(V, 256);
     grads = grads && N > 0;
     if (grads) {
-        const int64_t fit = std::max<int64_t>(kHeld / 4 / V / 128 * 128, 128);
-        p.keep = e == 4 || N <= fit;
+        // logits of up to 256 MB; in bfloat16 they cost 8 bytes of traffic each beside G's, and formed again 2 D operations:
+        // as much at some 800 channels, unless all of it stays in the caches
+        const int64_t fit = std::max<int64_t>(256 * kMB / 4 / V / 128 * 128, 128);
+        p.keep = e == 4 || (N <= fit && (D >= 768 || N * V * 4 <= 32 * kMB));
         if (p.keep) {
             const int64_t blocks = (N + fit - 1) / fit;
             p.rows = std::min(N, up((N + blocks - 1) / blocks, 128));
             p.piece = up(V, 8);
         } else {  // at least 2048 classes
-            p.piece = std::min(p.piece, std::max<int64_t>(2048, kHeld / (N * e) / 256 * 256));
+            p.piece = std::min(p.piece, std::max<int64_t>(2048, 128 * kMB / (N * e) / 256 * 256));
             const int64_t pieces = (V + p.piece - 1) / p.piece;
             p.piece = up((V + pieces - 1) / pieces, 256);
         }

@@ -39,7 +39,6 @@ template <typename T>
 struct Op;
 template <>
 struct Op<bf16> {
-    typedef uint16_t lds_t;
     typedef u32x2 Quad;
     static constexpr int C = 32;  // tokens a block
     static __device__ inline Quad make(f32x4 v) { return Quad{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}; }
@@ -52,21 +51,9 @@ struct Op<bf16> {
         const u32x4 x = {x0[0], x0[1], x1[0], x1[1]}, y = {y0[0], y0[1], y1[0], y1[1]};
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bh8, x), __builtin_bit_cast(bh8, y), c, 0, 0, 0);
     }
-    // row `row` of an LDS tile, columns col0 + 4 g ..
-    static __device__ inline Quad row(const lds_t* t, int stride, int row, int col0, int g) {
-        return *reinterpret_cast<const Quad*>(t + row * stride + col0 + 4 * g);
-    }
-    // column col0 + lane % 16 of an LDS tile, rows row0 + 4 g ..: a transposing read, in which each group of 16 lanes
-    // names 4 rows of 16 values
-    static __device__ inline Quad col(const lds_t* t, int stride, int row0, int col0, int g, int i) {
-        typedef __attribute__((address_space(3))) h4* P;
-        const lds_t* p = t + (row0 + 4 * g + (i >> 2)) * stride + col0 + 4 * (i & 3);
-        return __builtin_bit_cast(Quad, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p)));
-    }
 };
 template <>
 struct Op<float> {
-    typedef float lds_t;
     typedef f32x4 Quad;
     static constexpr int C = 32;
     static __device__ inline Quad make(f32x4 v) { return v; }
@@ -77,13 +64,6 @@ struct Op<float> {
 #pragma unroll
         for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x1[r], y1[r], c, 0, 0, 0);
         return c;
-    }
-    static __device__ inline Quad row(const lds_t* t, int stride, int row, int col0, int g) {
-        return *reinterpret_cast<const Quad*>(t + row * stride + col0 + 4 * g);
-    }
-    static __device__ inline Quad col(const lds_t* t, int stride, int row0, int col0, int g, int i) {
-        const lds_t* p = t + (row0 + 4 * g) * stride + col0 + i;
-        return Quad{p[0], p[stride], p[2 * stride], p[3 * stride]};
     }
 };
 
@@ -165,19 +145,84 @@ __device__ inline Tile tile_of(const Args& a, int64_t number) {
 }
 
 // ---- blocks of rows ---------------------------------------------------------------------------------------------
-// n rows of d elements from `first` on in scan order, staged in registers and then laid as an LDS tile of C x D, zero
-// outside: what lies behind a sequence or beside a head never meets a product. Every lane loads, without a branch: past the
-// rows the last one, which is laid as zeros, past the row its last 16 bytes, which end with it and are laid there again;
-// the columns past d stay as `zero_fill` left them. Heads of less than 16 bytes go element by element.
-template <typename T, int D, int PAD>
+// An LDS tile of C rows of D elements, in whose rows the 16-byte chunks change places with the row: a wave's reads along the
+// rows (16 of them, 32 or 64 bytes each) and across them meet all banks, and nothing lies between the rows, as the loads that
+// go straight to LDS need it.
+template <typename T, int D>
+struct Plane {
+    typedef typename Op<T>::Quad Quad;
+    static constexpr int E = sizeof(T), C = Op<T>::C, row_bytes = D * E, bytes = C * row_bytes;
+    static __device__ inline int turn(int r) { return row_bytes == 128 ? r >> 1 & 7 : r & 15; }
+    // the place of byte c of row r
+    static __device__ inline int at(int r, int c) { return r * row_bytes + (((c >> 4) ^ turn(r)) << 4) + (c & 15); }
+    // A lane's reads: of row i = lane % 16, columns 4 g .., and of column i, rows 4 g .. (bfloat16: by a transposing read, in
+    // which each group of 16 lanes names 4 rows of 16 values), at the tile of 16 x 16 from row0, col0 on: what col0 adds to the
+    // place is a change of some of its chunk's bits. The places are found again for each block (the constructor's lane is
+    // taken as new): kept, they would take some twenty registers.
+    int by_row, by_col;
+    __device__ inline Plane() {
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        const int g = lane >> 4, i = lane & 15;
+        by_row = at(i, 4 * g * E);
+        by_col = E == 2 ? at(4 * g + (i >> 2), 4 * (i & 3) * E) : at(4 * g, i * E);
+    }
+    __device__ inline Quad row(const char* t, int row0, int col0) const {
+        return *reinterpret_cast<const Quad*>(t + row0 * row_bytes + (by_row ^ (col0 * E)));
+    }
+    __device__ inline Quad col(const char* t, int row0, int col0) const {
+        if constexpr (E == 2) {
+            typedef __attribute__((address_space(3))) h4* P;
+            const char* p = t + row0 * row_bytes + (by_col ^ (col0 * E));
+            return __builtin_bit_cast(Quad, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p)));
+        } else {
+            Quad q;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                q[e] = *reinterpret_cast<const float*>(t + (row0 + e) * row_bytes + (by_col ^ (col0 * E) ^ (e << 4)));
+            return q;
+        }
+    }
+};
+
+constexpr uint32_t kOut = 0x80000000u;  // an offset past every buffer's end: the load gives zeros
+
+// n rows of d elements from `first` on in scan order to a plane, zero outside: what lies behind a sequence or beside a head
+// never meets a product. ld: bytes, below 2^25, so that a block's offsets have 31 bits.
+// WIDE 16 or 4: straight to LDS, that many bytes a lane; rows start and end at multiples of it.
+// WIDE 0: staged in registers (load) and then laid (lay), any alignment. Every lane loads, without a branch: past the rows the
+// last one, which is laid as zeros, past the row its last 16 bytes, which end with it and are laid there again; the columns
+// past d stay as `zero_fill` left them. Heads of less than 16 bytes go element by element.
+template <typename T, int D, int WIDE>
 struct Rows {
-    typedef typename Op<T>::lds_t E;
+    typedef Plane<T, D> P;
+    static constexpr int C = Op<T>::C, E = sizeof(T), n = P::bytes / (kThreads * WIDE);
+    static_assert((WIDE == 16 || WIDE == 4) && P::bytes % (kThreads * WIDE) == 0, "whole loads a thread");
+    __device__ inline void load(const T* base, int64_t ld, int64_t first, int dir, int rows, int d, char* to) {
+        const char* low = reinterpret_cast<const char*>(base) + (dir > 0 ? first : first - (C - 1)) * ld;
+        const __amdgpu_buffer_rsrc_t buf = rsrc(low, 0x7fffffff);
+        int tid = thread_id();
+        if constexpr (n > 2) asm volatile("" : "+v"(tid));  // many loads: their places are found again, not kept
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const int q = (i * kThreads + tid) * WIDE, r = q / P::row_bytes, at = q % P::row_bytes;
+            const int c = (((at >> 4) ^ P::turn(r)) << 4) + (at & 15);
+            const uint32_t o = (uint32_t)(dir > 0 ? r : C - 1 - r) * (uint32_t)ld + (uint32_t)c;
+            const int off = (int)(r < rows && c < d * E ? o : kOut);
+            char* l = to + (i * kThreads + (thread_id() & ~63)) * WIDE;  // of the wave
+            typedef __attribute__((address_space(3))) void* L;
+            if constexpr (WIDE == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (L)l, 16, off, 0, 0, 0);
+            else __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (L)l, 4, off, 0, 0, 0);
+        }
+    }
+};
+template <typename T, int D>
+struct Rows<T, D, 0> {
+    typedef Plane<T, D> P;
     static constexpr int V = Width<T>::v, per = D / V, C = Op<T>::C, n_vec = C * per / kThreads;
-    static constexpr int stride = D + PAD / (int)sizeof(T);
     static_assert(n_vec >= 1 && C * per % kThreads == 0, "whole vectors a thread");
     u32x4 q[n_vec];
-    // ld: bytes, below 2^25, so that a block's offsets have 31 bits
-    __device__ inline void load(const T* base, int64_t ld, int64_t first, int dir, int n, int d) {
+    __device__ inline void load(const T* base, int64_t ld, int64_t first, int dir, int n, int d, char*) {
         const char* low = reinterpret_cast<const char*>(base) + (dir > 0 ? first : first - (n - 1)) * ld;
         const int col = thread_id() % per * V, c0 = d < V ? 0 : min(col, d - V);
 #pragma unroll
@@ -200,7 +245,7 @@ struct Rows {
             }
         }
     }
-    __device__ inline void lay(E* t, int n, int d) const {
+    __device__ inline void lay(char* t, int n, int d) const {
         const int col = thread_id() % per * V;
 #pragma unroll
         for (int i = 0; i < n_vec; ++i) {
@@ -208,38 +253,45 @@ struct Rows {
             const bool in = r < n;
             const u32x4 v = {in ? q[i][0] : 0, in ? q[i][1] : 0, in ? q[i][2] : 0, in ? q[i][3] : 0};
             if (col + V <= d || (d < V && col == 0)) {
-                *reinterpret_cast<u32x4*>(t + r * stride + col) = v;
+                *reinterpret_cast<u32x4*>(t + P::at(r, col * (int)sizeof(T))) = v;
             } else if (col < d) {
-                E* p = t + r * stride + d - V;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    if constexpr (sizeof(T) == 2) p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-                    else p[e] = __uint_as_float(v[e]);
+                    char* p = t + P::at(r, (d - V + e) * (int)sizeof(T));
+                    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint16_t*>(p) = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+                    else *reinterpret_cast<uint32_t*>(p) = v[e];
                 }
             }
         }
     }
 };
-template <typename E>
-__device__ inline void zero_fill(E* t, int n) {
-    for (int i = thread_id(); i < n; i += kThreads) t[i] = 0;
+__device__ inline void zero_fill(char* t, int bytes) {
+    for (int i = 16 * thread_id(); i < bytes; i += 16 * kThreads) *reinterpret_cast<u32x4*>(t + i) = u32x4{0, 0, 0, 0};
 }
 
-// A head's sizes: four waves, with a quarter of the state's columns each. LDS rows are apart by their length and 16 bytes (4
-// banks more than a multiple of the banks: a wave's reads along the rows meet them all), or by 32 (8 banks: its transposing
-// reads, of 8 rows by 32 bytes, do) where those are the most.
-template <typename T, int DA_, int DC_>
+// All waves of the workgroup meet here: with what they wrote to LDS done, and (ALL) their loads to LDS, which an ordinary
+// barrier would wait for at either place. The waits' counters: 0xC07F lgkmcnt(0), 0x0070 vmcnt(0) and lgkmcnt(0).
+template <bool ALL>
+__device__ inline void meet() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(ALL ? 0x0070 : 0xC07F);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// A head's sizes: four waves, with a quarter of the state's columns each.
+template <typename T, int DA_, int DC_, int WIDE_>
 struct Head {
     typedef T type;
     typedef Op<T> O;
-    static constexpr int DA = DA_, DC = DC_, C = O::C, CT = C / 16, NT = DC / 64, waves = 4;
+    static constexpr int DA = DA_, DC = DC_, WIDE = WIDE_, C = O::C, CT = C / 16, NT = DC / 64, waves = 4;
     // waves a SIMD, and so workgroups a compute unit, that the registers allow
-    static constexpr int occupancy = DA + DC > 192 ? 2 : DA + DC > 128 ? 3 : 4;
-    static constexpr int tr = sizeof(T) == 2 ? 32 : 16;
-    typedef Rows<T, DA, 16> RA;
-    typedef Rows<T, DA, tr> RB;
-    typedef Rows<T, DC, tr> RC;
-    static constexpr int sp = C + 16 / (int)sizeof(T);  // of the block's products
+    static constexpr int occupancy = DA + DC == 128 ? 4 : WIDE == 0 && (DA + DC > 192 || sizeof(T) == 4) ? 2 : 3;
+    typedef Plane<T, DA> PA;
+    typedef Plane<T, DC> PC;
+    typedef Rows<T, DA, WIDE> RA;
+    typedef Rows<T, DC, WIDE> RC;
+    static constexpr int sp = C * (int)sizeof(T) + 16;  // bytes between the rows of a block's products
 };
 // ---- states -----------------------------------------------------------------------------------------------------
 // A wave's 16 NT columns of the state: result tiles of 16 x 16, rows 16 t + 4 g + r, columns 16 u + lane % 16.
@@ -314,16 +366,18 @@ struct State {
 // x += sum over the block's rows j of b_j f_j c_j^T, f(t) the weights of rows 16 t + 4 g ..; PARTS: how many bfloat16 terms
 // f c is taken as (one for fp32)
 template <typename Hd, int PARTS, typename F>
-__device__ inline void add_block(State<Hd::DA, Hd::NT>& s, const typename Hd::O::lds_t* B, const typename Hd::O::lds_t* Cv, F f) {
+__device__ inline void add_block(State<Hd::DA, Hd::NT>& s, const char* B, const char* Cv, F f) {
     typedef typename Hd::O O;
     constexpr int JT = Hd::CT, NT = Hd::NT;
-    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15, n0 = (thread_id() >> 6) * (16 * NT);
+    const int n0 = __builtin_amdgcn_readfirstlane(thread_id() >> 6) * (16 * NT);
+    const typename Hd::PA pb;
+    const typename Hd::PC pc;
     typename O::Quad w[PARTS][JT][NT];
 #pragma unroll
     for (int t = 0; t < JT; ++t)
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            f32x4 v = O::values(O::col(Cv, Hd::RC::stride, 16 * t, n0 + 16 * u, g, i)) * f(t);
+            f32x4 v = O::values(pc.col(Cv, 16 * t, n0 + 16 * u)) * f(t);
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
                 w[p][t][u] = O::make(v);
@@ -334,8 +388,7 @@ __device__ inline void add_block(State<Hd::DA, Hd::NT>& s, const typename Hd::O:
     for (int m = 0; m < Hd::DA / 16; ++m) {
 #pragma unroll
         for (int t = 0; t < JT; t += 2) {
-            const auto b0 = O::col(B, Hd::RB::stride, 16 * t, 16 * m, g, i);
-            const auto b1 = O::col(B, Hd::RB::stride, 16 * t + 16, 16 * m, g, i);
+            const auto b0 = pb.col(B, 16 * t, 16 * m), b1 = pb.col(B, 16 * t + 16, 16 * m);
 #pragma unroll
             for (int u = 0; u < NT; ++u)
 #pragma unroll
@@ -346,12 +399,12 @@ __device__ inline void add_block(State<Hd::DA, Hd::NT>& s, const typename Hd::O:
 
 // What each tile adds to its sequence's state. bfloat16: f c is split into three terms (24 bits, as fp32 has), so that the
 // states are sums of fp32 products.
-template <typename T, int DA, int DC>
-__global__ __launch_bounds__(kThreads, (Head<T, DA, DC>::occupancy)) void states(const Args a) {
-    typedef Head<T, DA, DC> Hd;
-    typedef typename Hd::O O;
-    constexpr int C = Hd::C, PARTS = sizeof(T) == 2 ? 3 : 1;
-    __shared__ alignas(16) typename O::lds_t lb[C * Hd::RB::stride], lc[C * Hd::RC::stride];
+template <typename T, int DA, int DC, int WIDE>
+__global__ __launch_bounds__(kThreads, (Head<T, DA, DC, WIDE>::occupancy)) void states(const Args a) {
+    typedef Head<T, DA, DC, WIDE> Hd;
+    constexpr int C = Hd::C, PARTS = sizeof(T) == 2 ? 3 : 1, nb = Hd::PA::bytes, nc = Hd::PC::bytes;
+    // two sets of planes, of which the compiler sees that loads into one do not meet the reads of the other
+    __shared__ alignas(16) char t0[nb + nc], t1[WIDE > 0 ? nb + nc : 16];
     const Tile t = tile_of(a, blockIdx.x / (uint32_t)a.H);
     if (t.seq < 0 || (t.leave < 0 && !a.last)) return;
     const int h = blockIdx.x % (uint32_t)a.H, g = (threadIdx.x & 63) >> 4;
@@ -360,32 +413,48 @@ __global__ __launch_bounds__(kThreads, (Head<T, DA, DC>::occupancy)) void states
     const T* pb = static_cast<const T*>(side.b) + (int64_t)h * da;
     const T* pc = static_cast<const T*>(side.c) + (int64_t)h * dc;
     const int64_t ldb = side.ldb * (int64_t)sizeof(T), ldc = side.ldc * (int64_t)sizeof(T);
-    typename Hd::RB rb;
+    typename Hd::RA rb;
     typename Hd::RC rc;
-    rb.load(pb, ldb, t.from, a.dir, min(C, t.len), da);
-    rc.load(pc, ldc, t.from, a.dir, min(C, t.len), dc);
-    zero_fill(lb, C * Hd::RB::stride);
-    zero_fill(lc, C * Hd::RC::stride);
+    const auto load = [&](int k, char* to) {
+        const int n = min(C, t.len - k);
+        rb.load(pb, ldb, t.from + a.dir * k, a.dir, n, da, to);
+        rc.load(pc, ldc, t.from + a.dir * k, a.dir, n, dc, to + nb);
+    };
+    load(0, t0);
     const float l2 = log2_of(a.decay[h]);
     State<DA, Hd::NT> x;
     x.clear();
-    for (int k = 0; k < t.len; k += C) {
-        const int n = min(C, t.len - k), next = min(C, t.len - k - C);
-        __syncthreads();
-        rb.lay(lb, n, da);
-        rc.lay(lc, n, dc);
-        if (next > 0) {
-            rb.load(pb, ldb, t.from + a.dir * (k + C), a.dir, next, da);
-            rc.load(pc, ldc, t.from + a.dir * (k + C), a.dir, next, dc);
-        }
-        __syncthreads();
+    const auto add = [&](int k, const char* p) {
+        const int n = min(C, t.len - k);
         if (k > 0) x.scale(power(l2, n));
-        add_block<Hd, PARTS>(x, lb, lc, [&](int q) {
+        add_block<Hd, PARTS>(x, p, p + nb, [&](int q) {
             f32x4 f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) f[r] = a.sscale * power(l2, max(n - a.post - (16 * q + 4 * g + r), 0));
             return f;
         });
+    };
+    if constexpr (WIDE > 0) {
+        for (int k = 0; k < t.len; k += 2 * C) {
+            meet<true>();
+            if (k + C < t.len) load(k + C, t1);
+            add(k, t0);
+            if (k + C >= t.len) break;
+            meet<true>();
+            if (k + 2 * C < t.len) load(k + 2 * C, t0);
+            add(k + C, t1);
+        }
+    } else {
+        zero_fill(t0, nb + nc);
+        for (int k = 0; k < t.len; k += C) {
+            const int n = min(C, t.len - k);
+            __syncthreads();
+            rb.lay(t0, n, da);
+            rc.lay(t0 + nb, n, dc);
+            if (k + C < t.len) load(k + C, t0);
+            __syncthreads();
+            add(k, t0);
+        }
     }
     x.store(side, t.leave >= 0 ? a.slots + (t.leave * a.H + h) * a.size : a.last + ((int64_t)t.seq * a.H + h) * a.size);
 }
@@ -464,15 +533,19 @@ __device__ inline void store_quad(T* p, f32x4 v, int n) {
 //
 // SIDES 2: two outputs of one tile at once, by four waves each, where the second's b is the first's c and its c the first's b
 // (dv and dk, whose states are each other's transposes): four tensors are read instead of six.
-template <typename T, int DA, int DC, int SIDES>
-__global__ __launch_bounds__(SIDES * kThreads, (Head<T, DA, DC>::occupancy)) void outputs(const Args a) {
-    typedef Head<T, DA, DC> Hd;
+template <typename T, int DA, int DC, int WIDE, int SIDES>
+__global__ __launch_bounds__(SIDES * kThreads, (SIDES == 2 && DA > 64 ? 2 : Head<T, DA, DC, WIDE>::occupancy)) void outputs(const Args a) {
+    typedef Head<T, DA, DC, WIDE> Hd;
     typedef typename Hd::O O;
     typedef typename O::Quad Quad;
-    constexpr int C = Hd::C, CT = Hd::CT, NT = Hd::NT, PARTS = sizeof(T) == 2 ? 2 : 1;
-    constexpr int sa = Hd::RA::stride, sb = Hd::RB::stride, sc = Hd::RC::stride, sp = Hd::sp;
-    static_assert(SIDES == 1 || sb == sc, "one side's c is the other's b");
-    extern __shared__ u32x4 smem[];
+    typedef typename Hd::PA PA;
+    typedef typename Hd::PC PC;
+    static_assert(SIDES == 1 || DA == DC, "one side's c is the other's b");
+    constexpr int C = Hd::C, CT = Hd::CT, NT = Hd::NT, PARTS = sizeof(T) == 2 ? 2 : 1, sp = Hd::sp;
+    // [a][b] a side, then c (SIDES 2: the other side's b); two sets, of which the compiler sees that loads into one do not
+    // meet the reads of the other
+    constexpr int na = PA::bytes, per_side = 2 * na, all = SIDES * per_side + (SIDES == 1 ? PC::bytes : 0);
+    __shared__ alignas(16) char t0[all], t1[WIDE > 0 ? all : 16], products[SIDES * C * sp];
     const Tile tile = tile_of(a, blockIdx.x / (uint32_t)a.H);
     if (tile.seq < 0) return;
     const int h = blockIdx.x % (uint32_t)a.H;
@@ -480,11 +553,8 @@ __global__ __launch_bounds__(SIDES * kThreads, (Head<T, DA, DC>::occupancy)) voi
     const int wave = __builtin_amdgcn_readfirstlane(thread_id() >> 6);
     const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
     const Args::Side& side = a.side[sd];
-    // [a][b][products] a side, then c (SIDES 2: the other side's b)
-    constexpr int per_side = C * (sa + sb + sp);
-    typename O::lds_t* la = reinterpret_cast<typename O::lds_t*>(smem) + sd * per_side;
-    typename O::lds_t *lb = la + C * sa, *lp = lb + C * sb;
-    typename O::lds_t* lc = SIDES == 1 ? lp + C * sp : lb + (sd == 0 ? per_side : -per_side);
+    const int own = sd * per_side, at_c = SIDES == 1 ? per_side : (1 - sd) * per_side + na;
+    char* lp = products + sd * C * sp;
     const int da = side.da, dc = side.dc;
     const T* pa = static_cast<const T*>(side.a) + (int64_t)h * da;
     const T* pb = static_cast<const T*>(side.b) + (int64_t)h * da;
@@ -493,23 +563,21 @@ __global__ __launch_bounds__(SIDES * kThreads, (Head<T, DA, DC>::occupancy)) voi
     char* po = reinterpret_cast<char*>(static_cast<T*>(side.out) + (int64_t)h * dc);
     const int64_t ldo = side.ldo * (int64_t)sizeof(T);
     const bool whole = dc % 4 == 0;
-    typename Hd::RA ra;
-    typename Hd::RB rb;
+    typename Hd::RA ra, rb;
     typename Hd::RC rc;
-    const auto load = [&](int k, int n) {
+    const auto load = [&](int k, char* to) {
+        const int n = min(C, tile.len - k);
         const int64_t f = tile.from + a.dir * k;
-        ra.load(pa, lda, f, a.dir, n, da);
-        rb.load(pb, ldb, f, a.dir, n, da);
-        if constexpr (SIDES == 1) rc.load(pc, ldc, f, a.dir, n, dc);
+        ra.load(pa, lda, f, a.dir, n, da, to + own);
+        rb.load(pb, ldb, f, a.dir, n, da, to + own + na);
+        if constexpr (SIDES == 1) rc.load(pc, ldc, f, a.dir, n, dc, to + at_c);
     };
-    load(0, min(C, tile.len));
+    load(0, t0);
     const float* enter = tile.enter >= 0 ? a.slots + (tile.enter * a.H + h) * a.size
                          : a.init ? a.init + ((int64_t)tile.seq * a.H + h) * a.size : nullptr;
-    State<DA, Hd::NT> x;
+    State<DA, NT> x;
     if (enter) x.load(side, enter);
     else x.clear();
-    zero_fill(la, C * (sa + sb));
-    if constexpr (SIDES == 1) zero_fill(lc, C * sc);
     // d^e for the e that occur, in two factors: within 16 (a lane's) and of 16s
     const float l2 = log2_of(a.decay[h]);
     float d16[CT], row_f = power(l2, i + a.post), near[4], far[4], left[4];
@@ -523,42 +591,40 @@ __global__ __launch_bounds__(SIDES * kThreads, (Head<T, DA, DC>::occupancy)) voi
         left[r] = a.sscale * power(l2, 16 - a.post - (4 * g + r));
     }
     const float d_block = uniform(power(l2, C));
-    for (int k = 0; k < tile.len; k += C) {
-        const int n = min(C, tile.len - k), next = min(C, tile.len - k - C);
-        __syncthreads();
-        ra.lay(la, n, da);
-        rb.lay(lb, n, da);
-        if constexpr (SIDES == 1) rc.lay(lc, n, dc);
-        if (next > 0) load(k + C, next);
-        __syncthreads();
-        // (a_i . b_j) d^{i-j}: the tiles of 16 x 16 on and below the diagonal, the lowest rows first, dealt out to the
-        // waves; row i at lane % 16, j at 4 g + r
+
+    // (a_i . b_j) d^{i-j}: the tiles of 16 x 16 on and below the diagonal, the lowest rows first, dealt out to the waves; row
+    // i at lane % 16, j at 4 g + r
+    const auto multiply = [&](const char* set) {
+        const char *la = set + own, *lb = la + na;
         constexpr int kPairs = CT * (CT + 1) / 2;
+        static_assert(kPairs <= Hd::waves, "a tile a wave");
+        if (wave >= kPairs) return;
+        int it = CT - 1, jt = wave;
 #pragma unroll
-        for (int k0 = 0; k0 < kPairs; k0 += Hd::waves) {
-            const int pair = k0 + wave;
-            if (pair >= kPairs) break;
-            int it = CT - 1, jt = pair;
+        for (int q = CT; q > 1; --q)
+            if (it == q - 1 && jt >= q) {
+                jt -= q;
+                --it;
+            }
+        const PA plane;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int q = CT; q > 1; --q)
-                if (it == q - 1 && jt >= q) {
-                    jt -= q;
-                    --it;
-                }
-            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        for (int m = 0; m < DA; m += 32)
+            v = O::mma2(v, plane.row(lb, 16 * jt, m), plane.row(lb, 16 * jt, m + 16), plane.row(la, 16 * it, m),
+                        plane.row(la, 16 * it, m + 16));
 #pragma unroll
-            for (int m = 0; m < DA; m += 32)
-                v = O::mma2(v, O::row(lb, sb, 16 * jt + i, m, g), O::row(lb, sb, 16 * jt + i, m + 16, g),
-                            O::row(la, sa, 16 * it + i, m, g), O::row(la, sa, 16 * it + i, m + 16, g));
-            float f = 1.f;
-#pragma unroll
-            for (int q = 1; q + 1 < CT; ++q) f = it - jt == q + 1 ? d16[q] : f;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = it == jt && i < 4 * g + r ? 0.f : v[r] * (it == jt ? near[r] : far[r] * f);
-            *reinterpret_cast<Quad*>(lp + (16 * it + i) * sp + 16 * jt + 4 * g) = O::make(v);
-        }
-        __syncthreads();
-        // outputs: row i at lane % 16, columns 4 g + r of the wave's tiles
+        for (int r = 0; r < 4; ++r) v[r] = it == jt && i < 4 * g + r ? 0.f : v[r] * (it == jt ? near[r] : far[r]);
+        static_assert(CT == 2, "tiles are on the diagonal or next to it");
+        *reinterpret_cast<Quad*>(lp + (16 * it + i) * sp + (16 * jt + 4 * g) * (int)sizeof(T)) = O::make(v);
+    };
+    const auto product_row = [&](int it, int jt) {
+        return *reinterpret_cast<const Quad*>(lp + (16 * it + i) * sp + (16 * jt + 4 * g) * (int)sizeof(T));
+    };
+    // outputs: row i at lane % 16, columns 4 g + r of the wave's tiles; then the state behind the block
+    const auto finish = [&](int k, const char* set) {
+        const char *la = set + own, *lb = la + na, *lc = set + at_c;
+        const PA plane;
+        const PC plane_c;
         f32x4 o[CT][NT];
 #pragma unroll
         for (int it = 0; it < CT; ++it)
@@ -575,7 +641,7 @@ __global__ __launch_bounds__(SIDES * kThreads, (Head<T, DA, DC>::occupancy)) voi
                 }
 #pragma unroll
                 for (int it = 0; it < CT; ++it) {
-                    const Quad a0 = O::row(la, sa, 16 * it + i, 16 * m, g), a1 = O::row(la, sa, 16 * it + i, 16 * m + 16, g);
+                    const Quad a0 = plane.row(la, 16 * it, 16 * m), a1 = plane.row(la, 16 * it, 16 * m + 16);
 #pragma unroll
                     for (int u = 0; u < NT; ++u) o[it][u] = O::mma2(o[it][u], x0[u], x1[u], a0, a1);
                 }
@@ -590,14 +656,14 @@ __global__ __launch_bounds__(SIDES * kThreads, (Head<T, DA, DC>::occupancy)) voi
             Quad c0[NT], c1[NT];
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
-                c0[u] = O::col(lc, sc, 16 * t, 16 * (NT * wave + u), g, i);
-                c1[u] = O::col(lc, sc, 16 * t + 16, 16 * (NT * wave + u), g, i);
+                c0[u] = plane_c.col(lc, 16 * t, 16 * (NT * wave + u));
+                c1[u] = plane_c.col(lc, 16 * t + 16, 16 * (NT * wave + u));
             }
 #pragma unroll
             for (int it = t; it < CT; ++it) {
-                const Quad p0 = O::row(lp, sp, 16 * it + i, 16 * t, g);
+                const Quad p0 = product_row(it, t);
                 // the tile past the diagonal is never written
-                const Quad p1 = it > t ? O::row(lp, sp, 16 * it + i, 16 * t + 16, g) : O::make(f32x4{0.f, 0.f, 0.f, 0.f});
+                const Quad p1 = it > t ? product_row(it, t + 1) : O::make(f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
                 for (int u = 0; u < NT; ++u) o[it][u] = O::mma2(o[it][u], c0[u], c1[u], p0, p1);
             }
@@ -606,7 +672,7 @@ __global__ __launch_bounds__(SIDES * kThreads, (Head<T, DA, DC>::occupancy)) voi
 #pragma unroll
         for (int it = 0; it < CT; ++it) {
             const int row = 16 * it + i;
-            if (row >= n) continue;
+            if (row >= tile.len - k) continue;
             char* qr = q + (int64_t)(a.dir * row) * ldo;
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
@@ -614,52 +680,87 @@ __global__ __launch_bounds__(SIDES * kThreads, (Head<T, DA, DC>::occupancy)) voi
                 if (col < dc) store_quad<T>(reinterpret_cast<T*>(qr) + col, o[it][u] * a.oscale, whole ? 4 : dc - col);
             }
         }
-        if (next > 0) {  // of a whole block
+        if (k + C < tile.len) {  // of a whole block
             x.scale(d_block);
             add_block<Hd, PARTS>(x, lb, lc, [&](int q) {
                 return f32x4{left[0], left[1], left[2], left[3]} * d16[CT - 1 - q];
             });
         }
-    }
-}
+    };
 
-template <typename T, int DA, int DC, int SIDES>
-constexpr size_t outputs_lds() {
-    typedef Head<T, DA, DC> Hd;
-    return sizeof(T) * Hd::C * (SIDES * (Hd::RA::stride + Hd::RB::stride + Hd::sp) + (SIDES == 1 ? Hd::RC::stride : 0));
+    if constexpr (WIDE > 0) {
+        for (int k = 0; k < tile.len; k += 2 * C) {
+            meet<true>();
+            if (k + C < tile.len) load(k + C, t1);
+            multiply(t0);
+            meet<false>();
+            finish(k, t0);
+            if (k + C >= tile.len) break;
+            meet<true>();
+            if (k + 2 * C < tile.len) load(k + 2 * C, t0);
+            multiply(t1);
+            meet<false>();
+            finish(k + C, t1);
+        }
+    } else {
+        zero_fill(t0 + own, per_side);
+        if constexpr (SIDES == 1) zero_fill(t0 + at_c, PC::bytes);
+        for (int k = 0; k < tile.len; k += C) {
+            const int n = min(C, tile.len - k);
+            __syncthreads();
+            ra.lay(t0 + own, n, da);
+            rb.lay(t0 + own + na, n, da);
+            if constexpr (SIDES == 1) rc.lay(t0 + at_c, n, dc);
+            if (k + C < tile.len) load(k + C, t0);
+            __syncthreads();
+            multiply(t0);
+            __syncthreads();
+            finish(k, t0);
+        }
+    }
 }
 
 enum { kStates, kOutputs, kBothOutputs };
-template <typename T, int DA, int DC, int SIDES>
-hipError_t go_outputs(const Args& a, dim3 grid, hipStream_t st) {
-    constexpr size_t lds = outputs_lds<T, DA, DC, SIDES>();
-    if (lds > 65536) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(outputs<T, DA, DC, SIDES>),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-        if (e != hipSuccess) return e;
-    }
-    launch(outputs<T, DA, DC, SIDES>, grid, dim3(SIDES * kThreads), lds, st, a);
-    return hipGetLastError();
-}
-template <typename T, int DA, int DC>
+template <typename T, int DA, int DC, int WIDE>
 hipError_t go(const Args& a, int what, hipStream_t st) {
     const dim3 grid((uint32_t)(((a.T >> a.log_l) + a.S) * a.H));  // the heads of a tile side by side
     if (what == kStates) {
-        launch(states<T, DA, DC>, grid, dim3(kThreads), 0, st, a);
-        return hipGetLastError();
+        launch(states<T, DA, DC, WIDE>, grid, dim3(kThreads), 0, st, a);
+    } else if (what == kOutputs) {
+        launch(outputs<T, DA, DC, WIDE, 1>, grid, dim3(kThreads), 0, st, a);
+    } else {
+        if constexpr (DA == DC) launch(outputs<T, DA, DC, WIDE, 2>, grid, dim3(2 * kThreads), 0, st, a);
+        else return hipErrorInvalidValue;
     }
-    if constexpr (DA == DC) {
-        if (what == kBothOutputs) return go_outputs<T, DA, DC, 2>(a, grid, st);
+    return hipGetLastError();
+}
+// Rows that start and end at multiples of 16 bytes go straight to LDS; so do those of fp32 heads up to 64 whatever they are,
+// 4 bytes a lane. Wider fp32 heads are staged in registers: two sets of planes would leave room for one workgroup.
+bool whole_chunks(const Args& a, int what, int e) {
+    const auto fits = [&](const void* p, int64_t ld, int d) {
+        return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * e % 16 == 0 && (int64_t)d * e % 16 == 0);
+    };
+    bool all = true;
+    for (int i = 0; i < (what == kBothOutputs ? 2 : 1); ++i) {
+        const Args::Side& s = a.side[i];
+        all = all && (what == kStates || fits(s.a, s.lda, s.da)) && fits(s.b, s.ldb, s.da) && fits(s.c, s.ldc, s.dc);
     }
-    return go_outputs<T, DA, DC, 1>(a, grid, st);
+    return all;
+}
+template <typename T, int DA, int DC>
+hipError_t go_wide(const Args& a, int what, hipStream_t st) {
+    const bool chunks = whole_chunks(a, what, sizeof(T));
+    if constexpr (sizeof(T) == 2) return chunks ? go<T, DA, DC, 16>(a, what, st) : go<T, DA, DC, 0>(a, what, st);
+    else if constexpr (DA + DC == 128) return chunks ? go<T, DA, DC, 16>(a, what, st) : go<T, DA, DC, 0>(a, what, st);
+    else return go<T, DA, DC, 0>(a, what, st);
 }
 // the padded size of keys or values
 constexpr int padded(int d) { return d <= 64 ? 64 : 128; }
 template <typename T>
 hipError_t go_sizes(const Args& a, int what, hipStream_t st) {
     const int da = padded(a.side[0].da), dc = padded(a.side[0].dc);
-    if (da == 64) return dc == 64 ? go<T, 64, 64>(a, what, st) : go<T, 64, 128>(a, what, st);
-    return dc == 64 ? go<T, 128, 64>(a, what, st) : go<T, 128, 128>(a, what, st);
+    if (da == 64) return dc == 64 ? go_wide<T, 64, 64>(a, what, st) : go_wide<T, 64, 128>(a, what, st);
+    return dc == 64 ? go_wide<T, 128, 64>(a, what, st) : go_wide<T, 128, 128>(a, what, st);
 }
 hipError_t go_any(const Args& a, int dtype, int what, hipStream_t st) {
     return dtype == 1 ? go_sizes<bf16>(a, what, st) : go_sizes<float>(a, what, st);

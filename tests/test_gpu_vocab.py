@@ -108,7 +108,7 @@ def test_large_logits(dtype):
 
 
 @pytest.mark.parametrize("dtype,N,D,V", [("bf16", 16500, 24, 8000), ("f32", 5000, 8, 9000), ("bf16", 700, 40, 60000),
-                                         ("bf16", 6000, 256, 12800), ("f32", 1000, 64, 70000), ("f32", 40, 300, 9001)])
+                                         ("bf16", 6000, 256, 12800), ("f32", 1000, 64, 70000), ("f32", 40, 300, 9001), ("f32", 9000, 8, 9000)])
 def test_pieces_and_large_tiles(dtype, N, D, V):
     """Vocabularies of several pieces, and sizes that take the larger tiles; the reference in float64 on the device."""
     h, W, ids, w = _inputs(17, N, D, V, dtype)

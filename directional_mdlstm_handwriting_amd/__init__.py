@@ -93,7 +93,7 @@ _SIGS = [
     ("mdl_blocknorm_backward", _I32, [_I64, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _F32, _P, _P, _I64,
                                       _P, _P, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
     ("mdl_distill", _I32, [_I64, _I32, _I32, _I32, _P, _I64, _P, _P, _I32, _P, _F32, _P, _P, _I64, _P]),
-    ("mdl_linattn_workspace_size", _I32, [_I64, _I32, _I32, _I32, _I32, ctypes.POINTER(_SZ)]),
+    ("mdl_linattn_workspace_size", _I32, [_I32, _I64, _I32, _I32, _I32, _I32, ctypes.POINTER(_SZ)]),
     ("mdl_linattn_forward", _I32, [_P, _I32, _I64, _I32, _I32, _I32, _I32, _I32, _P, _F32, _P, _I64, _P, _I64, _P, _I64,
                                    _P, _P, _I64, _P, _P, _SZ, _P]),
     ("mdl_linattn_backward", _I32, [_P, _I32, _I64, _I32, _I32, _I32, _I32, _I32, _P, _F32, _P, _I64, _P, _I64, _P,
@@ -410,9 +410,9 @@ def mdl_distill(N: int, V: int, k: int, dtype: int, z, ldz: int, ids, t, t_dtype
                             _ptr(dz), ldd, _stream(stream)))
 
 
-def mdl_linattn_workspace_size(T: int, H: int, Dk: int, Dv: int, dtype: int) -> int:
+def mdl_linattn_workspace_size(S: int, T: int, H: int, Dk: int, Dv: int, dtype: int) -> int:
     b = _SZ()
-    _check(_lib.mdl_linattn_workspace_size(T, H, Dk, Dv, dtype, ctypes.byref(b)))
+    _check(_lib.mdl_linattn_workspace_size(S, T, H, Dk, Dv, dtype, ctypes.byref(b)))
     return b.value
 
 

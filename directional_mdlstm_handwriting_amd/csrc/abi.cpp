@@ -1283,28 +1283,30 @@ int mdl_distill(int64_t N, int32_t V, int32_t k, int32_t dtype, const void* z, i
 }
 
 // ---- linear attention with a decay for each head -------------------------------------------------------
-// sizes of an attention call; need receives the workspace bytes
-static int check_attn(const std::string& F, int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype, size_t& need) {
+// a head's sizes, as all attention calls take them
+static int check_heads(const std::string& F, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype) {
     int rc = check_dtype(F, dtype);
     if (rc) return rc;
-    if (T < 0 || H < 1 || Dk < 1 || Dv < 1) return fail(MDL_EINVAL, F + ": need T >= 0 and H, Dk, Dv >= 1");
+    if (H < 1 || Dk < 1 || Dv < 1) return fail(MDL_EINVAL, F + ": need H, Dk, Dv >= 1");
     if (Dk > mdl::linattn_max_d() || Dv > mdl::linattn_max_d())
         return fail(MDL_EUNSUPPORTED, F + ": Dk or Dv above " + std::to_string(mdl::linattn_max_d()));
     if (H > 65535) return fail(MDL_EUNSUPPORTED, F + ": H above 65535");
+    return MDL_OK;
+}
+// sizes of a call over sequences; need receives the workspace bytes
+static int check_attn(const std::string& F, int32_t S, int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype,
+                      size_t& need) {
+    int rc = check_heads(F, H, Dk, Dv, dtype);
+    if (rc || (rc = check_sequences(F, S))) return rc;
+    if (T < 0) return fail(MDL_EINVAL, F + ": need T >= 0");
     if (T >= (int64_t(1) << 36)) return fail(MDL_EOVERFLOW, F + ": T reaches 2^36");
-    need = mdl::attn_plan(T, H, Dk, Dv).total;
+    const mdl::AttnPlan p = mdl::attn_plan(S, T, H, Dk, Dv);
+    const int64_t most = mdl::kMaxLaunchThreads / 512;
+    if (S > most / p.chain_blocks || T / p.L + S > most / H) return fail(MDL_EOVERFLOW, F + ": the launch exceeds 2^31 threads");
+    need = p.total;
     return MDL_OK;
 }
-// the sequences of a call whose states are walked: a launch over S times the states' elements
-static int check_attn_sequences(const std::string& F, int32_t S, int64_t T, int32_t H, int32_t Dk, int32_t Dv) {
-    int rc = check_sequences(F, S);
-    if (rc) return rc;
-    const mdl::AttnPlan p = mdl::attn_plan(T, H, Dk, Dv);
-    if (S > mdl::kMaxLaunchThreads / 256 / p.chain_blocks || (T >> p.log_l) + S > mdl::kMaxLaunchThreads / 256 / H)
-        return fail(MDL_EOVERFLOW, F + ": the launch exceeds 2^31 threads");
-    return MDL_OK;
-}
-// as check_stride, for the kernels whose blocks of 64 rows keep their offsets in 31 bits
+// as check_stride, for the kernels whose blocks of rows keep their offsets in 31 bits
 static int check_stride23(const std::string& F, const char* name, int64_t rows, int64_t cols, int64_t ld) {
     if (ld >= (int64_t(1) << 23)) return fail(MDL_EOVERFLOW, F + ": " + name + " reaches 2^23");
     return check_stride(F, name, rows, cols, ld);
@@ -1319,11 +1321,11 @@ static uint64_t state_bytes(int32_t S, int32_t H, int32_t Dk, int32_t Dv) {
     return (uint64_t)S * (uint64_t)H * (uint64_t)Dk * (uint64_t)Dv * 4;
 }
 
-int mdl_linattn_workspace_size(int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype, size_t* bytes) {
+int mdl_linattn_workspace_size(int32_t S, int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype, size_t* bytes) {
     GUARD_BEGIN
     if (!bytes) return fail(MDL_EINVAL, "mdl_linattn_workspace_size: null argument");
     size_t need = 0;
-    const int rc = check_attn("mdl_linattn_workspace_size", T, H, Dk, Dv, dtype, need);
+    const int rc = check_attn("mdl_linattn_workspace_size", S, T, H, Dk, Dv, dtype, need);
     if (rc) return rc;
     *bytes = need;
     return MDL_OK;
@@ -1337,8 +1339,8 @@ int mdl_linattn_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t H,
     GUARD_BEGIN
     const std::string F("mdl_linattn_forward");
     size_t need = 0;
-    int rc = check_attn(F, T, H, Dk, Dv, dtype, need);
-    if (rc || (rc = check_attn_sequences(F, S, T, H, Dk, Dv))) return rc;
+    int rc = check_attn(F, S, T, H, Dk, Dv, dtype, need);
+    if (rc) return rc;
     if (!seq_off || !decay || (T > 0 && (!q || !k || !v || !y))) return fail(MDL_EINVAL, F + ": null tensor");
     const int64_t nk = (int64_t)H * Dk, nv = (int64_t)H * Dv;
     if ((rc = check_stride23(F, "ldq", T, nk, ldq)) || (rc = check_stride23(F, "ldk", T, nk, ldk)) ||
@@ -1385,8 +1387,8 @@ int mdl_linattn_backward(const int64_t* seq_off, int32_t S, int64_t T, int32_t H
     GUARD_BEGIN
     const std::string F("mdl_linattn_backward");
     size_t need = 0;
-    int rc = check_attn(F, T, H, Dk, Dv, dtype, need);
-    if (rc || (rc = check_attn_sequences(F, S, T, H, Dk, Dv))) return rc;
+    int rc = check_attn(F, S, T, H, Dk, Dv, dtype, need);
+    if (rc) return rc;
     if (!seq_off || !decay || (T > 0 && (!q || !k || !v || !dy || !dq || !dk || !dv)))
         return fail(MDL_EINVAL, F + ": null tensor");
     const int64_t nk = (int64_t)H * Dk, nv = (int64_t)H * Dv;
@@ -1442,8 +1444,7 @@ int mdl_linattn_step(int32_t S, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype
                      void* stream) {
     GUARD_BEGIN
     const std::string F("mdl_linattn_step");
-    size_t need = 0;
-    int rc = check_attn(F, 0, H, Dk, Dv, dtype, need);
+    int rc = check_heads(F, H, Dk, Dv, dtype);
     if (rc) return rc;
     if (S < 1 || n_slots < 1) return fail(MDL_EINVAL, F + ": need S and n_slots >= 1");
     if (!decay || !q || !k || !v || !h_in || !h_out || !y) return fail(MDL_EINVAL, F + ": null tensor");

@@ -82,7 +82,8 @@ struct Args {
     const int64_t* off;
     int S, H;
     int64_t T;
-    int log_l;                 // log2 of the tokens a tile, L
+    int L;                     // tokens a tile
+    double inv_l;              // 1 / L
     int dir;                   // +1: tokens ascending, -1: descending
     int post;                  // 1: the entering state is the previous token's; 0: it is the token's own
     const float* decay;
@@ -106,6 +107,15 @@ __device__ inline int64_t offset(const Args& a, int64_t s) {
     return o < 0 ? 0 : (o > a.T ? a.T : o);
 }
 
+// floor(x / L) for 0 <= x < 2^40: the product is off by less than one
+__device__ inline int64_t over_l(const Args& a, int64_t x) {
+    int64_t q = (int64_t)((double)x * a.inv_l);
+    const int64_t r = x - q * a.L;
+    q -= r < 0;
+    q += r >= a.L;
+    return q;
+}
+
 struct Tile {
     int seq;                   // -1: nothing to do
     int len;
@@ -120,7 +130,7 @@ __device__ inline Tile tile_of(const Args& a, int64_t number) {
     while (lo < hi) {
         const int step = (int)(((int64_t)(hi - lo) + 63) / 64);
         const int64_t p = lo + (int64_t)lane * step;
-        const uint64_t m = __ballot(p < hi && (offset(a, p) >> a.log_l) + p > number);
+        const uint64_t m = __ballot(p < hi && over_l(a, offset(a, p)) + p > number);
         if (m == 0) {
             lo += ((hi - lo - 1) / step) * step + 1;
         } else {
@@ -132,8 +142,8 @@ __device__ inline Tile tile_of(const Args& a, int64_t number) {
     Tile t;
     t.seq = lo - 1;
     if (t.seq < 0) return t;
-    const int64_t o0 = offset(a, t.seq), o1 = offset(a, (int64_t)t.seq + 1), L = int64_t(1) << a.log_l;
-    const int64_t slot = number - t.seq, begin = o0 + ((slot - (o0 >> a.log_l)) << a.log_l);
+    const int64_t o0 = offset(a, t.seq), o1 = offset(a, (int64_t)t.seq + 1), L = a.L;
+    const int64_t slot = number - t.seq, begin = o0 + (slot - over_l(a, o0)) * L;
     if (begin >= o1) t.seq = -1;
     const int64_t end = begin + L < o1 ? begin + L : o1;
     const int64_t before = begin > o0 ? slot - 1 : -1, after = end < o1 ? slot : -1;
@@ -400,7 +410,7 @@ __device__ inline void add_block(State<Hd::DA, Hd::NT>& s, const char* B, const 
 // What each tile adds to its sequence's state. bfloat16: f c is split into three terms (24 bits, as fp32 has), so that the
 // states are sums of fp32 products.
 template <typename T, int DA, int DC, int WIDE>
-__global__ __launch_bounds__(kThreads, (Head<T, DA, DC, WIDE>::occupancy)) void states(const Args a) {
+__global__ __launch_bounds__(kThreads, (WIDE > 0 ? 4 : Head<T, DA, DC, WIDE>::occupancy)) void states(const Args a) {
     typedef Head<T, DA, DC, WIDE> Hd;
     constexpr int C = Hd::C, PARTS = sizeof(T) == 2 ? 3 : 1, nb = Hd::PA::bytes, nc = Hd::PC::bytes;
     // two sets of planes, of which the compiler sees that loads into one do not meet the reads of the other
@@ -439,10 +449,11 @@ __global__ __launch_bounds__(kThreads, (Head<T, DA, DC, WIDE>::occupancy)) void 
             meet<true>();
             if (k + C < t.len) load(k + C, t1);
             add(k, t0);
-            if (k + C >= t.len) break;
-            meet<true>();
-            if (k + 2 * C < t.len) load(k + 2 * C, t0);
-            add(k + C, t1);
+            if (k + C < t.len) {
+                meet<true>();
+                if (k + 2 * C < t.len) load(k + 2 * C, t0);
+                add(k + C, t1);
+            }
         }
     } else {
         zero_fill(t0, nb + nc);
@@ -475,7 +486,7 @@ __global__ __launch_bounds__(kThreads) void chain(const Args a, int blocks_per_h
         if (a.last) store_f32<V>(a.last + at, x);
         return;
     }
-    const int64_t L = int64_t(1) << a.log_l, base = o0 >> a.log_l, end = (o1 - o0 - 1) >> a.log_l;
+    const int64_t L = a.L, base = over_l(a, o0), end = over_l(a, o1 - o0 - 1);
     const float l2 = log2_of(a.decay[h]), whole = power(l2, (int)L);
     const int64_t hop = a.dir * a.H * a.size;
     // all tiles but the sequence's last one are whole
@@ -695,12 +706,13 @@ __global__ __launch_bounds__(SIDES * kThreads, (SIDES == 2 && DA > 64 ? 2 : Head
             multiply(t0);
             meet<false>();
             finish(k, t0);
-            if (k + C >= tile.len) break;
-            meet<true>();
-            if (k + 2 * C < tile.len) load(k + 2 * C, t0);
-            multiply(t1);
-            meet<false>();
-            finish(k + C, t1);
+            if (k + C < tile.len) {
+                meet<true>();
+                if (k + 2 * C < tile.len) load(k + 2 * C, t0);
+                multiply(t1);
+                meet<false>();
+                finish(k + C, t1);
+            }
         }
     } else {
         zero_fill(t0 + own, per_side);
@@ -723,7 +735,7 @@ __global__ __launch_bounds__(SIDES * kThreads, (SIDES == 2 && DA > 64 ? 2 : Head
 enum { kStates, kOutputs, kBothOutputs };
 template <typename T, int DA, int DC, int WIDE>
 hipError_t go(const Args& a, int what, hipStream_t st) {
-    const dim3 grid((uint32_t)(((a.T >> a.log_l) + a.S) * a.H));  // the heads of a tile side by side
+    const dim3 grid((uint32_t)((a.T / a.L + a.S) * a.H));  // the heads of a tile side by side
     if (what == kStates) {
         launch(states<T, DA, DC, WIDE>, grid, dim3(kThreads), 0, st, a);
     } else if (what == kOutputs) {
@@ -851,17 +863,17 @@ __global__ __launch_bounds__(kThreads) void step(const StepArgs a) {
 
 int linattn_max_d() { return 128; }
 
-// Tiles: as long as leaves some workgroups a compute unit, since a tile costs its state's way to memory and back: up to
-// four times a head's size (a quarter of its tokens' bytes) for two a compute unit, beyond that only for six. At 1000 x 8
-// heads of 64 (fp32, forward) tiles of 64 take 24 us and of 256 43; at 20597 x 8 of 64 (bf16, both ways) 207 and 172; at
-// 208246 x 8 of 128 tiles of 256 take 3141, of 1024 2364 and of 2048 2322.
-AttnPlan attn_plan(int64_t T, int H, int Dk, int Dv) {
+// Tiles: so many that their workgroups fill the chip a whole number of times, as many tiles as sequences at least beside the
+// sequences' own (whose last tiles are short): once where the sequences are long, since a tile costs its state's way to
+// memory and back. Wide heads have three workgroups a compute unit, narrow ones four.
+AttnPlan attn_plan(int S, int64_t T, int H, int Dk, int Dv) {
     AttnPlan p;
-    p.log_l = 6;
-    const int D = std::max(Dk, Dv);
-    while (p.log_l < 11 && (T >> (p.log_l + 1)) * H >= (2 << p.log_l <= 4 * D ? 512 : 1536)) ++p.log_l;
+    const int64_t fill = (std::max(Dk, Dv) > 64 ? 3 : 4) * 256;
+    const int64_t rounds = std::max<int64_t>(1, (2 * (int64_t)S * H + fill - 1) / fill);
+    const int64_t tiles = std::max<int64_t>(1, (fill * rounds + H - 1) / H - S);
+    p.L = (int)std::min<int64_t>(4096, std::max<int64_t>(64, (T + tiles * 32 - 1) / (tiles * 32) * 32));
     const int64_t size = (int64_t)Dk * Dv;
-    p.nslots = T >> p.log_l;
+    p.nslots = T / p.L;
     p.total = 2 * (((size_t)p.nslots * (size_t)(H * size) * sizeof(float) + 15) / 16 * 16);
     p.chain_blocks = H * chain_blocks(size);
     return p;
@@ -874,7 +886,8 @@ Args args_of(const AttnArgs& x, const AttnPlan& p) {
     a.S = x.S;
     a.H = x.H;
     a.T = x.T;
-    a.log_l = p.log_l;
+    a.L = p.L;
+    a.inv_l = 1.0 / p.L;
     a.decay = x.decay;
     a.size = (int64_t)x.Dk * x.Dv;
     return a;
@@ -889,7 +902,7 @@ Args::Side side_of(Rows_ a, Rows_ b, Rows_ c, int da, int dc, int trans, void* o
 }  // namespace
 
 hipError_t launch_attn_fwd(const AttnArgs& x, int dtype, void* ws, hipStream_t st) {
-    const AttnPlan p = attn_plan(x.T, x.H, x.Dk, x.Dv);
+    const AttnPlan p = attn_plan(x.S, x.T, x.H, x.Dk, x.Dv);
     Args a = args_of(x, p);
     a.dir = x.reverse ? -1 : 1;
     a.post = 1;
@@ -907,7 +920,7 @@ hipError_t launch_attn_fwd(const AttnArgs& x, int dtype, void* ws, hipStream_t s
 }
 
 hipError_t launch_attn_bwd(const AttnArgs& x, int dtype, void* ws, hipStream_t st) {
-    const AttnPlan p = attn_plan(x.T, x.H, x.Dk, x.Dv);
+    const AttnPlan p = attn_plan(x.S, x.T, x.H, x.Dk, x.Dv);
     const Rows_ q{x.q, x.ldq}, k{x.k, x.ldk}, v{x.v, x.ldv}, dy{x.dy, x.lddy};
     // the state's gradient, against the forward's order
     Args g = args_of(x, p);

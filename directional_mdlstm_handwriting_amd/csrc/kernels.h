@@ -379,13 +379,13 @@ struct AttnArgs {
     float *hT, *dh0;                // [S][H][Dk][Dv] or null
 };
 struct AttnPlan {
-    int log_l = 0;                  // log2 of the tokens a tile
+    int L = 0;                      // tokens a tile
     int64_t nslots = 0;             // tile boundaries, states of H heads each
     int64_t chain_blocks = 0;       // workgroups a sequence
     size_t total = 0;               // bytes of both directions' slots
 };
 int linattn_max_d();
-AttnPlan attn_plan(int64_t T, int H, int Dk, int Dv);
+AttnPlan attn_plan(int S, int64_t T, int H, int Dk, int Dv);
 hipError_t launch_attn_fwd(const AttnArgs& a, int dtype, void* ws, hipStream_t st);
 hipError_t launch_attn_bwd(const AttnArgs& a, int dtype, void* ws, hipStream_t st);
 hipError_t launch_attn_step(const AttnArgs& a, int dtype, const int32_t* slots, int n_slots, const float* h_in,

@@ -647,7 +647,7 @@ class LinearAttention(_Buffers):
         self.reverse, self.scale = int(bool(reverse)), float(Dk ** -0.5 if scale is None else scale)
         self.x_dtype, self.tdt = _x_dtype(x_dtype)
         self.decay = _decays(decay, self.H, self.device)
-        self.ws_bytes = mdl_linattn_workspace_size(self.T, self.H, self.Dk, self.Dv, self.x_dtype)
+        self.ws_bytes = mdl_linattn_workspace_size(self.S, self.T, self.H, self.Dk, self.Dv, self.x_dtype)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         # zeros: rows in no sequence are never written
         self.y = torch.zeros(self.T, self.H * self.Dv, dtype=self.tdt, device=self.device)

@@ -609,7 +609,7 @@ int mdl_distill(int64_t N, int32_t V, int32_t k, int32_t dtype, const void* z, i
  * or a row of a step, takes 256 threads a head, and as many more for each 256
  * elements of a sequence's state). With T = 0 the token tensors may be NULL.
  */
-int mdl_linattn_workspace_size(int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype, size_t* bytes);
+int mdl_linattn_workspace_size(int32_t S, int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype, size_t* bytes);
 int mdl_linattn_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype,
                         int32_t reverse, const float* decay, float scale, const void* q, int64_t ldq, const void* k,
                         int64_t ldk, const void* v, int64_t ldv, const float* h0, void* y, int64_t ldy, float* hT,

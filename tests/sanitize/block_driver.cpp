@@ -39,7 +39,7 @@ int main() {
     for (int64_t T : big)
         for (int32_t H : wide)
             for (int32_t D : wide) {
-                REFUSED(mdl_linattn_workspace_size(T, H, D, D, MDL_F32, &bytes));
+                REFUSED(mdl_linattn_workspace_size(H, T, 2, D, D, MDL_F32, &bytes));
                 REFUSED(mdl_linattn_forward(off, H, T, H, D, 7, MDL_BF16, 0, fl(1), 1.f, at(2), T, at(3), T, at(4), T, fl(5),
                                             at(6), T, fl(7), at(8), SIZE_MAX, nullptr));
                 REFUSED(mdl_linattn_backward(off, H, T, H, 7, D, MDL_F32, 1, fl(1), 1.f, at(2), T, at(3), T, at(4), T, fl(5),
@@ -55,7 +55,7 @@ int main() {
     for (int64_t T : some)
         for (int32_t H : wide)
             for (int32_t D : wide) {
-                ANSWERED(mdl_linattn_workspace_size(T, H, D, 128, MDL_F32, &bytes));
+                ANSWERED(mdl_linattn_workspace_size(D, T, H, 128, 7, MDL_F32, &bytes));
                 ANSWERED(mdl_vocab_loss_workspace_size(T, H, D, MDL_BF16, 1, &bytes));
                 ANSWERED(mdl_vocab_loss_workspace_size(T, D, H, MDL_F32, 0, &bytes));
                 // no workspace where one is needed, or a stride below its row: refused whatever the sizes

@@ -78,13 +78,14 @@ def test_attention_step_refuses(change, code):
 
 def test_attention_workspace_sizes():
     f = M.mdl_linattn_workspace_size
-    assert f(0, 2, 8, 8, M.MDL_F32) == 0
-    assert f(1, 2, 8, 8, M.MDL_BF16) == 0
-    assert f(100000, 2, 8, 8, M.MDL_BF16) > 0
-    assert _code(f, 5, 2, 8, 8, 3) == M.MDL_EINVAL
-    assert _code(f, -1, 2, 8, 8, M.MDL_F32) == M.MDL_EINVAL
-    assert _code(f, 5, 2, 8, 200, M.MDL_F32) == M.MDL_EUNSUPPORTED
-    assert _code(f, 1 << 50, 2, 8, 8, M.MDL_F32) == M.MDL_EOVERFLOW
+    assert f(1, 0, 2, 8, 8, M.MDL_F32) == 0
+    assert f(3, 1, 2, 8, 8, M.MDL_BF16) == 0
+    assert f(1, 100000, 2, 8, 8, M.MDL_BF16) > 0
+    assert _code(f, 1, 5, 2, 8, 8, 3) == M.MDL_EINVAL
+    assert _code(f, 0, 5, 2, 8, 8, M.MDL_F32) == M.MDL_EINVAL
+    assert _code(f, 1, -1, 2, 8, 8, M.MDL_F32) == M.MDL_EINVAL
+    assert _code(f, 1, 5, 2, 8, 200, M.MDL_F32) == M.MDL_EUNSUPPORTED
+    assert _code(f, 1, 1 << 50, 2, 8, 8, M.MDL_F32) == M.MDL_EOVERFLOW
 
 
 DROP = dict(N=10, D=8, dtype=M.MDL_F32, x=A(0), ldx=8, r=A(1), ldr=8, p=0.1, rng=A(2), y=A(3), ldy=8, stream=0)

@@ -864,12 +864,14 @@ __global__ __launch_bounds__(kThreads) void step(const StepArgs a) {
 int linattn_max_d() { return 128; }
 
 // Tiles: so many that their workgroups fill the chip a whole number of times, as many tiles as sequences at least beside the
-// sequences' own (whose last tiles are short): once where the sequences are long, since a tile costs its state's way to
-// memory and back. Wide heads have three workgroups a compute unit, narrow ones four.
+// sequences' own (whose last tiles are short): once where there are few sequences, since a tile costs its state's way to
+// memory and back, else four times, since tiles of many lengths do not end together. Wide heads have three workgroups a
+// compute unit, narrow ones four. At 656603 x 50 (fp32, 1024 sequences, both ways) tiles of 224 take 987 us, of 672 1101.
 AttnPlan attn_plan(int S, int64_t T, int H, int Dk, int Dv) {
     AttnPlan p;
     const int64_t fill = (std::max(Dk, Dv) > 64 ? 3 : 4) * 256;
-    const int64_t rounds = std::max<int64_t>(1, (2 * (int64_t)S * H + fill - 1) / fill);
+    int64_t rounds = std::max<int64_t>(1, (2 * (int64_t)S * H + fill - 1) / fill);
+    if (rounds > 1) rounds = std::max<int64_t>(rounds, 4);
     const int64_t tiles = std::max<int64_t>(1, (fill * rounds + H - 1) / H - S);
     p.L = (int)std::min<int64_t>(4096, std::max<int64_t>(64, (T + tiles * 32 - 1) / (tiles * 32) * 32));
     const int64_t size = (int64_t)Dk * Dv;

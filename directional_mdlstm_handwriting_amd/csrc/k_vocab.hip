@@ -263,17 +263,18 @@ __global__ __launch_bounds__(S::threads, 2) void product(const Args g) {
     ta.load(a0);
     tb.load(b0);
     __syncthreads();
-    // two steps a turn; behind the last one come zeros
+    // two steps a turn; what is loaded behind the last one are zeros
     for (int64_t t = s0; t < s1; t += 2) {
         ta.load(a1);
         tb.load(b1);
         one_step<T, S, TA, TB>(a0, b0, wm, wn, c);
         __syncthreads();
-        if (S::TM * S::TN <= 4 && t + 1 >= s1) break;  // (in the large tiles a branch here costs registers)
-        ta.load(a0);
-        tb.load(b0);
-        one_step<T, S, TA, TB>(a1, b1, wm, wn, c);
-        __syncthreads();
+        if (t + 1 < s1) {
+            ta.load(a0);
+            tb.load(b0);
+            one_step<T, S, TA, TB>(a1, b1, wm, wn, c);
+            __syncthreads();
+        }
     }
     // A lane holds row lane % 32 of each of its tiles, columns 8 (e / 4) + 4 h + e % 4.
     if constexpr (EPI == kStats) {
@@ -509,20 +510,22 @@ void go_sum(const float* slab, int64_t slabs, int64_t M, int64_t N, T* out, int6
 // ---- plan ---------------------------------------------------------------------------------------------------------
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-// The larger tiles where they fill the compute units; the thin ones for few rows: those of 128 would spend most of their
-// products on rows that are not there, which fp32 feels first.
-Size size_of(int64_t M, int64_t N, int64_t K, int e, bool along) {
+// The larger tiles where they fill the compute units; the thin ones for few rows, where those of 128 would spend most of
+// their products on rows that are not there, which fp32 feels first, and for few tiles whose depth is not split.
+Size size_of(int64_t M, int64_t N, int64_t K, int e, bool along, bool split) {
     if (along && M <= (e == 4 ? 64 : 32)) return kThin;
     const bool fills = ((M + 255) / 256) * ((N + 255) / 256) >= 192;
-    return fills && M > 128 && N > 128 && K * e > 3 * 128 ? kLarge : kSmall;
+    if (fills && M > 128 && N > 128 && K * e > 3 * 128) return kLarge;
+    const int64_t small = ((M + 127) / 128) * ((N + 127) / 128) * (split ? std::max<int64_t>(1, K * e / 128 / 2) : 1);
+    return along && small < 128 ? kThin : kSmall;
 }
 // how often the depth is split where there are few tiles: so that some 512 workgroups share the work, none with less than
-// four steps of it
+// two steps of it
 int64_t splits_of(int64_t M, int64_t N, int64_t K, int e, bool along) {
-    const Size size = size_of(M, N, K, e, along);
+    const Size size = size_of(M, N, K, e, along, true);
     if (size == kLarge) return 1;
     const int64_t bm = size == kThin ? 32 : 128, tiles = ((M + bm - 1) / bm) * ((N + 127) / 128), steps = (K * e + 127) / 128;
-    return std::max<int64_t>(1, std::min<int64_t>({512 / tiles, steps / 4, int64_t(64)}));
+    return std::max<int64_t>(1, std::min<int64_t>({512 / tiles, steps / 2, int64_t(128)}));
 }
 
 }  // namespace
@@ -613,14 +616,14 @@ struct Vocab {
         a.ldo = p.piece;
         return a;
     }
-    Size size(const Args& a, bool along) const { return size_of(a.M, a.N, a.K, sizeof(T), along); }
+    Size size(const Args& a) const { return size_of(a.M, a.N, a.K, sizeof(T), true, false); }  // of the logits
     // losses of rows r0 .., their logits kept where there is a place for them
     void losses(int64_t r0, int64_t rows, bool keep) const {
         Args a = logits(r0, rows, 0, x.V);
         a.stats = at<float2>(p.stats);
         a.target = at<float>(p.target_logit, r0);
         if (keep) a.logits = at<float>(p.logits);
-        const Size s = size(a, true);
+        const Size s = size(a);
         go<T, true, true, kStats>(a, s, 1, st);
         const int64_t tiles = (x.V + (s == kLarge ? 255 : 127)) / (s == kLarge ? 256 : 128);
         launch(join, dim3((uint32_t)((rows + 7) / 8)), dim3(256), 0, st, a.stats, tiles, rows, a.target, a.ids,
@@ -644,7 +647,7 @@ struct Vocab {
         b.cols = x.D;
         b.slab = at<float>(p.dh);
         b.add = !first_piece;
-        const Size sh = size_of(p.rows, x.D, std::min<int64_t>(p.piece, x.V), sizeof(T), true);
+        const Size sh = size_of(p.rows, x.D, std::min<int64_t>(p.piece, x.V), sizeof(T), true, true);
         if (p.dh_slab) go<T, true, false, kSlab>(b, sh, p.dh_splits, st);
         else go<T, true, false, kStore>(b, sh, 1, st);
         if (p.dh_slab && last_piece) go_sum(b.slab, p.dh_splits, rows, x.D, dh, x.lddh, st);
@@ -662,7 +665,7 @@ struct Vocab {
         c.ldo = x.D;
         c.cols = x.D;
         c.add = !first_block;
-        const Size sw = size_of(std::min<int64_t>(p.piece, x.V), x.D, p.rows, sizeof(T), false);
+        const Size sw = size_of(std::min<int64_t>(p.piece, x.V), x.D, p.rows, sizeof(T), false, true);
         if (p.dw_splits > 1) {
             c.slab = at<float>(p.dw);
             go<T, false, false, kSlab>(c, sw, p.dw_splits, st);
@@ -696,7 +699,7 @@ struct Vocab {
             a.coef = at<float>(p.coef);
             a.out = at<T>(p.g);
             a.cols = up(cols, 16 / (int64_t)sizeof(T));
-            go<T, true, true, kGrad>(a, size(a, true), 1, st);
+            go<T, true, true, kGrad>(a, size(a), 1, st);
             take(0, x.N, v0, cols, v0 == 0, v0 + cols == x.V, true, true);
         }
     }

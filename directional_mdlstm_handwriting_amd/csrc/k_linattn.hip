@@ -199,15 +199,15 @@ constexpr uint32_t kOut = 0x80000000u;  // an offset past every buffer's end: th
 
 // n rows of d elements from `first` on in scan order to a plane, zero outside: what lies behind a sequence or beside a head
 // never meets a product. ld: bytes, below 2^25, so that a block's offsets have 31 bits.
-// WIDE 16 or 4: straight to LDS, that many bytes a lane; rows start and end at multiples of it.
-// WIDE 0: staged in registers (load) and then laid (lay), any alignment. Every lane loads, without a branch: past the rows the
+// DIRECT: straight to LDS, 16 bytes a lane; rows start and end at multiples of it.
+// Else staged in registers (load) and then laid (lay), any alignment. Every lane loads, without a branch: past the rows the
 // last one, which is laid as zeros, past the row its last 16 bytes, which end with it and are laid there again; the columns
 // past d stay as `zero_fill` left them. Heads of less than 16 bytes go element by element.
-template <typename T, int D, int WIDE>
+template <typename T, int D, bool DIRECT>
 struct Rows {
     typedef Plane<T, D> P;
-    static constexpr int C = Op<T>::C, E = sizeof(T), n = P::bytes / (kThreads * WIDE);
-    static_assert((WIDE == 16 || WIDE == 4) && P::bytes % (kThreads * WIDE) == 0, "whole loads a thread");
+    static constexpr int C = Op<T>::C, E = sizeof(T), n = P::bytes / (kThreads * 16);
+    static_assert(P::bytes % (kThreads * 16) == 0, "whole loads a thread");
     __device__ inline void load(const T* base, int64_t ld, int64_t first, int dir, int rows, int d, char* to) {
         const char* low = reinterpret_cast<const char*>(base) + (dir > 0 ? first : first - (C - 1)) * ld;
         const __amdgpu_buffer_rsrc_t buf = rsrc(low, 0x7fffffff);
@@ -215,19 +215,18 @@ struct Rows {
         if constexpr (n > 2) asm volatile("" : "+v"(tid));  // many loads: their places are found again, not kept
 #pragma unroll
         for (int i = 0; i < n; ++i) {
-            const int q = (i * kThreads + tid) * WIDE, r = q / P::row_bytes, at = q % P::row_bytes;
-            const int c = (((at >> 4) ^ P::turn(r)) << 4) + (at & 15);
+            const int q = (i * kThreads + tid) * 16, r = q / P::row_bytes, at = q % P::row_bytes;
+            const int c = ((at >> 4) ^ P::turn(r)) << 4;
             const uint32_t o = (uint32_t)(dir > 0 ? r : C - 1 - r) * (uint32_t)ld + (uint32_t)c;
             const int off = (int)(r < rows && c < d * E ? o : kOut);
-            char* l = to + (i * kThreads + (thread_id() & ~63)) * WIDE;  // of the wave
+            char* l = to + (i * kThreads + (thread_id() & ~63)) * 16;  // of the wave
             typedef __attribute__((address_space(3))) void* L;
-            if constexpr (WIDE == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (L)l, 16, off, 0, 0, 0);
-            else __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (L)l, 4, off, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (L)l, 16, off, 0, 0, 0);
         }
     }
 };
 template <typename T, int D>
-struct Rows<T, D, 0> {
+struct Rows<T, D, false> {
     typedef Plane<T, D> P;
     static constexpr int V = Width<T>::v, per = D / V, C = Op<T>::C, n_vec = C * per / kThreads;
     static_assert(n_vec >= 1 && C * per % kThreads == 0, "whole vectors a thread");
@@ -290,17 +289,18 @@ __device__ inline void meet() {
 }
 
 // A head's sizes: four waves, with a quarter of the state's columns each.
-template <typename T, int DA_, int DC_, int WIDE_>
+template <typename T, int DA_, int DC_, bool DIRECT_>
 struct Head {
     typedef T type;
     typedef Op<T> O;
-    static constexpr int DA = DA_, DC = DC_, WIDE = WIDE_, C = O::C, CT = C / 16, NT = DC / 64, waves = 4;
+    static constexpr bool DIRECT = DIRECT_;
+    static constexpr int DA = DA_, DC = DC_, C = O::C, CT = C / 16, NT = DC / 64, waves = 4;
     // waves a SIMD, and so workgroups a compute unit, that the registers allow
-    static constexpr int occupancy = DA + DC == 128 ? 4 : WIDE == 0 && (DA + DC > 192 || sizeof(T) == 4) ? 2 : 3;
+    static constexpr int occupancy = DA + DC == 128 ? 4 : !DIRECT && (DA + DC > 192 || sizeof(T) == 4) ? 2 : 3;
     typedef Plane<T, DA> PA;
     typedef Plane<T, DC> PC;
-    typedef Rows<T, DA, WIDE> RA;
-    typedef Rows<T, DC, WIDE> RC;
+    typedef Rows<T, DA, DIRECT> RA;
+    typedef Rows<T, DC, DIRECT> RC;
     static constexpr int sp = C * (int)sizeof(T) + 16;  // bytes between the rows of a block's products
 };
 // ---- states -----------------------------------------------------------------------------------------------------
@@ -409,12 +409,12 @@ __device__ inline void add_block(State<Hd::DA, Hd::NT>& s, const char* B, const 
 
 // What each tile adds to its sequence's state. bfloat16: f c is split into three terms (24 bits, as fp32 has), so that the
 // states are sums of fp32 products.
-template <typename T, int DA, int DC, int WIDE>
-__global__ __launch_bounds__(kThreads, (WIDE > 0 ? 4 : Head<T, DA, DC, WIDE>::occupancy)) void states(const Args a) {
-    typedef Head<T, DA, DC, WIDE> Hd;
+template <typename T, int DA, int DC, bool DIRECT>
+__global__ __launch_bounds__(kThreads, (DIRECT ? 4 : Head<T, DA, DC, DIRECT>::occupancy)) void states(const Args a) {
+    typedef Head<T, DA, DC, DIRECT> Hd;
     constexpr int C = Hd::C, PARTS = sizeof(T) == 2 ? 3 : 1, nb = Hd::PA::bytes, nc = Hd::PC::bytes;
     // two sets of planes, of which the compiler sees that loads into one do not meet the reads of the other
-    __shared__ alignas(16) char t0[nb + nc], t1[WIDE > 0 ? nb + nc : 16];
+    __shared__ alignas(16) char t0[nb + nc], t1[DIRECT ? nb + nc : 16];
     const Tile t = tile_of(a, blockIdx.x / (uint32_t)a.H);
     if (t.seq < 0 || (t.leave < 0 && !a.last)) return;
     const int h = blockIdx.x % (uint32_t)a.H, g = (threadIdx.x & 63) >> 4;
@@ -444,7 +444,7 @@ __global__ __launch_bounds__(kThreads, (WIDE > 0 ? 4 : Head<T, DA, DC, WIDE>::oc
             return f;
         });
     };
-    if constexpr (WIDE > 0) {
+    if constexpr (DIRECT) {
         for (int k = 0; k < t.len; k += 2 * C) {
             meet<true>();
             if (k + C < t.len) load(k + C, t1);
@@ -544,9 +544,9 @@ __device__ inline void store_quad(T* p, f32x4 v, int n) {
 //
 // SIDES 2: two outputs of one tile at once, by four waves each, where the second's b is the first's c and its c the first's b
 // (dv and dk, whose states are each other's transposes): four tensors are read instead of six.
-template <typename T, int DA, int DC, int WIDE, int SIDES>
-__global__ __launch_bounds__(SIDES * kThreads, (SIDES == 2 && DA > 64 ? 2 : Head<T, DA, DC, WIDE>::occupancy)) void outputs(const Args a) {
-    typedef Head<T, DA, DC, WIDE> Hd;
+template <typename T, int DA, int DC, bool DIRECT, int SIDES>
+__global__ __launch_bounds__(SIDES * kThreads, (SIDES == 2 && DA > 64 ? 2 : Head<T, DA, DC, DIRECT>::occupancy)) void outputs(const Args a) {
+    typedef Head<T, DA, DC, DIRECT> Hd;
     typedef typename Hd::O O;
     typedef typename O::Quad Quad;
     typedef typename Hd::PA PA;
@@ -556,7 +556,7 @@ __global__ __launch_bounds__(SIDES * kThreads, (SIDES == 2 && DA > 64 ? 2 : Head
     // [a][b] a side, then c (SIDES 2: the other side's b); two sets, of which the compiler sees that loads into one do not
     // meet the reads of the other
     constexpr int na = PA::bytes, per_side = 2 * na, all = SIDES * per_side + (SIDES == 1 ? PC::bytes : 0);
-    __shared__ alignas(16) char t0[all], t1[WIDE > 0 ? all : 16], products[SIDES * C * sp];
+    __shared__ alignas(16) char t0[all], t1[DIRECT ? all : 16], products[SIDES * C * sp];
     const Tile tile = tile_of(a, blockIdx.x / (uint32_t)a.H);
     if (tile.seq < 0) return;
     const int h = blockIdx.x % (uint32_t)a.H;
@@ -699,7 +699,7 @@ __global__ __launch_bounds__(SIDES * kThreads, (SIDES == 2 && DA > 64 ? 2 : Head
         }
     };
 
-    if constexpr (WIDE > 0) {
+    if constexpr (DIRECT) {
         for (int k = 0; k < tile.len; k += 2 * C) {
             meet<true>();
             if (k + C < tile.len) load(k + C, t1);
@@ -733,21 +733,22 @@ __global__ __launch_bounds__(SIDES * kThreads, (SIDES == 2 && DA > 64 ? 2 : Head
 }
 
 enum { kStates, kOutputs, kBothOutputs };
-template <typename T, int DA, int DC, int WIDE>
+template <typename T, int DA, int DC, bool DIRECT>
 hipError_t go(const Args& a, int what, hipStream_t st) {
     const dim3 grid((uint32_t)((a.T / a.L + a.S) * a.H));  // the heads of a tile side by side
     if (what == kStates) {
-        launch(states<T, DA, DC, WIDE>, grid, dim3(kThreads), 0, st, a);
+        launch(states<T, DA, DC, DIRECT>, grid, dim3(kThreads), 0, st, a);
     } else if (what == kOutputs) {
-        launch(outputs<T, DA, DC, WIDE, 1>, grid, dim3(kThreads), 0, st, a);
+        launch(outputs<T, DA, DC, DIRECT, 1>, grid, dim3(kThreads), 0, st, a);
     } else {
-        if constexpr (DA == DC) launch(outputs<T, DA, DC, WIDE, 2>, grid, dim3(2 * kThreads), 0, st, a);
+        if constexpr (DA == DC) launch(outputs<T, DA, DC, DIRECT, 2>, grid, dim3(2 * kThreads), 0, st, a);
         else return hipErrorInvalidValue;
     }
     return hipGetLastError();
 }
-// Rows that start and end at multiples of 16 bytes go straight to LDS; so do those of fp32 heads up to 64 whatever they are,
-// 4 bytes a lane. Wider fp32 heads are staged in registers: two sets of planes would leave room for one workgroup.
+// Rows that start and end at multiples of 16 bytes go straight to LDS. Others are staged in registers, and so are fp32 heads
+// wider than 64: two sets of planes would leave room for one workgroup. (At 656603 x 50 in fp32, heads of 50, 4 bytes a lane
+// straight to LDS took longer than the registers' way.)
 bool whole_chunks(const Args& a, int what, int e) {
     const auto fits = [&](const void* p, int64_t ld, int d) {
         return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * e % 16 == 0 && (int64_t)d * e % 16 == 0);
@@ -762,9 +763,9 @@ bool whole_chunks(const Args& a, int what, int e) {
 template <typename T, int DA, int DC>
 hipError_t go_wide(const Args& a, int what, hipStream_t st) {
     const bool chunks = whole_chunks(a, what, sizeof(T));
-    if constexpr (sizeof(T) == 2) return chunks ? go<T, DA, DC, 16>(a, what, st) : go<T, DA, DC, 0>(a, what, st);
-    else if constexpr (DA + DC == 128) return chunks ? go<T, DA, DC, 16>(a, what, st) : go<T, DA, DC, 0>(a, what, st);
-    else return go<T, DA, DC, 0>(a, what, st);
+    if constexpr (sizeof(T) == 2) return chunks ? go<T, DA, DC, true>(a, what, st) : go<T, DA, DC, false>(a, what, st);
+    else if constexpr (DA + DC == 128) return chunks ? go<T, DA, DC, true>(a, what, st) : go<T, DA, DC, false>(a, what, st);
+    else return go<T, DA, DC, false>(a, what, st);
 }
 // the padded size of keys or values
 constexpr int padded(int d) { return d <= 64 ? 64 : 128; }

@@ -605,9 +605,10 @@ int mdl_distill(int64_t N, int32_t V, int32_t k, int32_t dtype, const void* z, i
  * n_slots < S, or a misaligned workspace; MDL_EUNSUPPORTED for Dk or Dv above 128
  * or H above 65535; MDL_ESIZE for a short workspace; MDL_EOVERFLOW when T reaches
  * 2^36, rows times a stride 2^60, a stride of the forward or backward 2^23, S
- * 2^31 - 64, or a launch 2^31 threads (a sequence,
- * or a row of a step, takes 256 threads a head, and as many more for each 256
- * elements of a sequence's state). With T = 0 the token tensors may be NULL.
+ * 2^31 - 64, or a launch 2^31 threads (512 a head for each sequence and for each
+ * tile of tokens, of which there are at most T / 64; 512 a sequence, head and 256
+ * elements of a state; 256 a row of a step and head). With T = 0 the token tensors
+ * may be NULL.
  */
 int mdl_linattn_workspace_size(int32_t S, int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype, size_t* bytes);
 int mdl_linattn_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype,
@@ -668,8 +669,10 @@ int mdl_dropout(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx,
  * overlaps of outputs with inputs are not allowed.
  * Logits are float32 sums of the inputs' products and are not rounded; statistics
  * and losses are float32. G's values are rounded to `dtype` before the products
- * with W and h, whose sums are float32 and rounded once. The vocabulary is taken in
- * pieces: the workspace holds one of G, and the logits are formed twice.
+ * with W and h, whose sums are float32 and rounded once. The workspace holds logits
+ * of a block of rows (up to 256 MB of them, or 128 rows) or G of a piece of the
+ * vocabulary (up to 128 MB, or 2048 classes), whatever N and V are; where it holds
+ * the latter, the logits are formed twice.
  * ws: >= mdl_vocab_loss_workspace_size bytes (grads: whether dh and dW are wanted),
  * 16-byte aligned, contents not kept.
  * Errors: MDL_EINVAL for null tensors, N < 0, D, V < 1, a stride below D, an unknown

@@ -3,14 +3,14 @@
 //
 //   z = h W^T,  loss_n = w_n (ln sum_c exp z_nc - z_n,id),  G = w (softmax z - [c = id]),  dh = G W,  dW = G^T h
 //
-// A first product leaves per row and 256 (or 128) classes their maximum and sum of exponentials, and the target's logit;
-// `join` makes the losses of them. What the gradients then need of the logits is held for a piece of them at a time, in one of two
-// ways. Logits kept: the first product, a block of rows at a time, also writes the block's logits (fp32),
-// `grad` makes G of them, and two products take G into dh and dW: 6 N V D operations. Logits formed again: behind the first
-// product over all rows, piece of the vocabulary by piece, a second one of the same operands forms G of the piece, and two
-// more take it into dh and dW: 8 N V D operations, but nothing is written that is not G. Kept are they where one block takes
-// all rows, and for fp32 always, whose products are the dearer half: 4096 x 2048 over 32000 classes in fp32 takes 15.6 ms
-// with the logits formed again. Several blocks in bfloat16 would have dW's sums read and written once a block.
+// A first product, a block of rows at a time, leaves per row and 256 (or 128) classes their maximum and sum of exponentials,
+// and the target's logit; `join` makes the losses of them. With gradients it also keeps the block's logits: in fp32 as they
+// are, in bfloat16 the exponentials below their tile's maximum as 16 bits of half precision (a rounding of 2^-11 of the value,
+// an eighth of the one G is about to get, or of 2^-25 of the maximum; the target's own, from which 1 is taken, comes from its
+// fp32 logit). `grad` makes G of them where they lie, and two products take G into dh and dW: 6 N V D operations. Several
+// blocks add up dW in fp32, which costs 8 bytes an element and block: at 1024 rows a quarter of the block's products.
+// (Forming the logits again, once the statistics are known, is 8 N V D operations and nothing written but G: 4096 x 2048 over
+// 32000 classes in bfloat16 took 1985 us that way and takes 1550, in fp32 15.6 and 12.0 ms.)
 //
 // Products: tiles of BM x BN by 8 (4) waves, 32 x 32 results of the matrix instructions (32x32x16 bfloat16, 32x32x2 fp32),
 // 128 bytes of depth at a time from global memory straight into LDS, one step ahead of the products. An operand whose rows
@@ -175,21 +175,26 @@ struct Args {
     int64_t tiles_m, tiles_n, splits;
     // epilogues
     float2* stats;                // [tiles_n][M] maximum and sum
-    float* logits;                // [M] at ldo, or null
-    float *target, *lse;          // [M]
+    float* target;                // [M]
     const int32_t* ids;           // [M] -1: none
-    const float* coef;            // [M]
-    int64_t n_first;              // class of column 0
-    void* out;
-    int64_t ldo, cols;            // cols: columns that are written (zeros past N)
+    void* out;                    // [M] at ldo; kStats: the logits or exponentials, or null
+    int64_t ldo, cols;            // cols: columns that are written
     float* slab;                  // [splits][M][N]
     int add;                      // onto what the slab holds
 };
 
-enum { kStats, kGrad, kStore, kSlab };
+enum { kStats, kStore, kSlab };
+
+// two values as 16 bits each, the nearest ones: half precision or bfloat16
+template <bool HALF>
+__device__ inline uint32_t pack16(float a, float b) {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    if constexpr (HALF) return __builtin_bit_cast(uint32_t, h2{(_Float16)a, (_Float16)b});
+    else return pack_bf16(a, b);
+}
 
 // A wave's tiles as they lie, four neighbours of a row a lane; onto what is there with `add` (fp32 alone).
-template <typename S, typename E>
+template <typename S, bool HALF = false, typename E>
 __device__ inline void store_direct(const f32x16 (&c)[S::TM][S::TN], E* out, int64_t ldo, int64_t cols, bool add, int64_t M,
                                     int64_t m0, int64_t n0, int wm) {
     const int lane = threadIdx.x & 63;
@@ -206,7 +211,7 @@ __device__ inline void store_direct(const f32x16 (&c)[S::TM][S::TN], E* out, int
                 f32x4 v = {c[i][j][e], c[i][j][e + 1], c[i][j][e + 2], c[i][j][e + 3]};
                 if constexpr (sizeof(E) == 2) {
                     typedef u32x2 u32x2_e __attribute__((aligned(2), may_alias));
-                    const u32x2 q = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                    const u32x2 q = {pack16<HALF>(v[0], v[1]), pack16<HALF>(v[2], v[3])};
                     if (n + 4 <= cols) *reinterpret_cast<u32x2_e*>(o) = q;
                     else
 #pragma unroll
@@ -224,12 +229,57 @@ __device__ inline void store_direct(const f32x16 (&c)[S::TM][S::TN], E* out, int
     }
 }
 
+// A workgroup's tile as 16 bits each, through LDS (in which no tile is read any more), so that whole lines leave: a quarter
+// (half) of the tile's rows in each array, their 16-byte chunks rotated by the row.
+template <typename S, bool HALF, typename E>
+__device__ inline void store_lines(const f32x16 (&c)[S::TM][S::TN], char* a0, char* b0, char* a1, char* b1, E* out, int64_t ldo,
+                                   int64_t cols, int64_t M, int64_t m0, int64_t n0, int wm, int wn) {
+    constexpr int chunks = S::BN / 8;
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const auto part = [&](int row) {
+        const int k = row >> 6;
+        return (k == 0 ? a0 : k == 1 ? b0 : k == 2 ? a1 : b1) + (row & 63) * (S::BN * 2);
+    };
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i) {
+        const int row = wm + 32 * i + (lane & 31);
+        char* q = part(wm + 32 * i) + (lane & 31) * (S::BN * 2);
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const int n = wn + 32 * j + 2 * e;  // and 4 h
+                const u32x2 v = {pack16<HALF>(c[i][j][e], c[i][j][e + 1]), pack16<HALF>(c[i][j][e + 2], c[i][j][e + 3])};
+                *reinterpret_cast<u32x2*>(q + 16 * ((n >> 3) ^ (row & (chunks - 1))) + 8 * h) = v;
+            }
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int q = threadIdx.x; q < S::BM * chunks; q += S::threads) {
+        const int row = q / chunks, ch = q % chunks;
+        const int64_t m = m0 + row, n = n0 + 8 * ch;
+        if (m >= M || n >= cols) continue;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(part(row) + 16 * (ch ^ (row & (chunks - 1))));
+        E* o = out + m * ldo + n;
+        if (n + 8 <= cols) {
+            *reinterpret_cast<u32x4_e*>(o) = v;
+        } else {
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (n + r < cols) o[r].u = (uint16_t)(v[r >> 1] >> (16 * (r & 1)));
+        }
+    }
+}
+
 template <typename T, typename S, bool AA, bool BA, int EPI>
 __global__ __launch_bounds__(S::threads, 2) void product(const Args g) {
     typedef Tile<T, S::BM, S::threads, AA> TA;
     typedef Tile<T, S::BN, S::threads, BA> TB;
     // four arrays: the compiler sees that loads into one pair do not meet the reads of the other
     __shared__ alignas(16) char a0[TA::bytes], b0[TB::bytes], a1[TA::bytes], b1[TB::bytes];
+    __shared__ float2 part[EPI == kStats ? S::WN : 1][S::BM];  // a wave's (maximum, sum) of a row
+    constexpr bool kLines = sizeof(T) == 2 && S::TM * S::TN > 1;
+    static_assert(!kLines || (TA::bytes == 64 * S::BN * 2 && TB::bytes == TA::bytes), "64 rows an array");
     // neighbouring workgroups go to the eight dies in turn: each die takes one run of tiles, in groups of 8 rows of tiles
     const int64_t total = (int64_t)gridDim.x;
     int64_t id = blockIdx.x;
@@ -278,8 +328,9 @@ __global__ __launch_bounds__(S::threads, 2) void product(const Args g) {
     }
     // A lane holds row lane % 32 of each of its tiles, columns 8 (e / 4) + 4 h + e % 4.
     if constexpr (EPI == kStats) {
-        if (g.logits) store_direct<S>(c, g.logits, g.ldo, g.N, false, g.M, m0, n0 + wn, wm);
-        float2* part = reinterpret_cast<float2*>(a0);  // [WN][BM]; all reads of the tiles are done
+        T* kept = static_cast<T*>(g.out);
+        if constexpr (sizeof(T) == 4)
+            if (kept) store_direct<S>(c, kept, g.ldo, g.N, false, g.M, m0, n0 + wn, wm);
         const int64_t limit = g.N - n0;
 #pragma unroll
         for (int i = 0; i < S::TM; ++i) {
@@ -297,85 +348,52 @@ __global__ __launch_bounds__(S::threads, 2) void product(const Args g) {
                     top = fmaxf(top, c[i][j][e]);
                 }
             top = fmaxf(top, __shfl_xor(top, 32));
+            if (h == 0) part[wave % S::WN][row].x = top;
+        }
+        __syncthreads();
+        const auto top_of = [&](int row) {
+            float t = part[0][row].x;
+#pragma unroll
+            for (int w = 1; w < S::WN; ++w) t = fmaxf(t, part[w][row].x);
+            return t;
+        };
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i) {
+            const int row = wm + 32 * i + (lane & 31);
             // a row of -inf alone: sum 0, and NaN where one of them is NaN, which the maximum passes over
-            const float base = top == -INFINITY ? 0.f : top;
+            const float top = top_of(row), base = top == -INFINITY ? 0.f : top;
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < S::TN; ++j)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) sum += exp_neg<T>(c[i][j][e] - base);
+                for (int e = 0; e < 16; ++e) {
+                    c[i][j][e] = exp_neg<T>(c[i][j][e] - base);
+                    sum += c[i][j][e];
+                }
             sum += __shfl_xor(sum, 32);
-            if (h == 0) part[wave % S::WN * S::BM + row] = make_float2(top, sum);
+            if (h == 0) part[wave % S::WN][row].y = sum;
         }
-        __syncthreads();
+        if constexpr (kLines) {
+            if (kept) store_lines<S, true>(c, a0, b0, a1, b1, kept, g.ldo, g.cols, g.M, m0, n0, wm, wn);
+            else __syncthreads();
+        } else {
+            if constexpr (sizeof(T) == 2)
+                if (kept) store_direct<S, true>(c, kept, g.ldo, g.cols, false, g.M, m0, n0 + wn, wm);
+            __syncthreads();
+        }
         for (int row = threadIdx.x; row < S::BM; row += S::threads) {
             if (m0 + row >= g.M) continue;
-            float2 p = part[row];
+            float sum = 0.f;
 #pragma unroll
-            for (int w = 1; w < S::WN; ++w) p = joined(p, part[w * S::BM + row]);
-            g.stats[tn * g.M + m0 + row] = p;
+            for (int w = 0; w < S::WN; ++w) sum += part[w][row].y;
+            g.stats[tn * g.M + m0 + row] = make_float2(top_of(row), sum);
         }
+    } else if constexpr (EPI == kSlab) {
+        store_direct<S>(c, g.slab + split * g.M * g.N, g.N, g.N, g.add != 0, g.M, m0, n0 + wn, wm);
+    } else if constexpr (kLines) {
+        store_lines<S, false>(c, a0, b0, a1, b1, static_cast<T*>(g.out), g.ldo, g.cols, g.M, m0, n0, wm, wn);
     } else {
-        if constexpr (EPI == kGrad) {
-#pragma unroll
-            for (int i = 0; i < S::TM; ++i) {
-                const int64_t m = m0 + wm + 32 * i + (lane & 31);
-                const float lse = m < g.M ? g.lse[m] : 0.f, coef = m < g.M ? g.coef[m] : 0.f;
-                const int64_t id = m < g.M ? (int64_t)g.ids[m] - g.n_first - n0 : -1;
-#pragma unroll
-                for (int j = 0; j < S::TN; ++j)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int n = wn + 32 * j + 8 * (e >> 2) + 4 * h + (e & 3);
-                        const float p = exp_neg<T>(c[i][j][e] - lse) - (n == id ? 1.f : 0.f);
-                        c[i][j][e] = coef == 0.f || n0 + n >= g.N ? 0.f : coef * p;
-                    }
-            }
-        }
-        if constexpr (sizeof(T) == 2 && EPI != kSlab && S::TM * S::TN > 1) {
-            // Through LDS, so that whole lines leave: a quarter (half) of the tile's rows in each array, their 16-byte
-            // chunks rotated by the row.
-            constexpr int chunks = S::BN / 8;
-            static_assert(TA::bytes == 64 * S::BN * 2 && TB::bytes == TA::bytes, "64 rows an array");
-            const auto part = [&](int row) {
-                const int k = row >> 6;
-                return (k == 0 ? a0 : k == 1 ? b0 : k == 2 ? a1 : b1) + (row & 63) * (S::BN * 2);
-            };
-#pragma unroll
-            for (int i = 0; i < S::TM; ++i) {
-                const int row = wm + 32 * i + (lane & 31);
-                char* q = part(wm + 32 * i) + (lane & 31) * (S::BN * 2);
-#pragma unroll
-                for (int j = 0; j < S::TN; ++j)
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const int n = wn + 32 * j + 2 * e;  // and 4 h
-                        const u32x2 v = {pack_bf16(c[i][j][e], c[i][j][e + 1]), pack_bf16(c[i][j][e + 2], c[i][j][e + 3])};
-                        *reinterpret_cast<u32x2*>(q + 16 * ((n >> 3) ^ (row & (chunks - 1))) + 8 * h) = v;
-                    }
-            }
-            __syncthreads();
-#pragma unroll 4
-            for (int q = threadIdx.x; q < S::BM * chunks; q += S::threads) {
-                const int row = q / chunks, ch = q % chunks;
-                const int64_t m = m0 + row, n = n0 + 8 * ch;
-                if (m >= g.M || n >= g.cols) continue;
-                const u32x4 v = *reinterpret_cast<const u32x4*>(part(row) + 16 * (ch ^ (row & (chunks - 1))));
-                T* o = static_cast<T*>(g.out) + m * g.ldo + n;
-                if (n + 8 <= g.cols) {
-                    *reinterpret_cast<u32x4_e*>(o) = v;
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        if (n + r < g.cols) o[r].u = (uint16_t)(v[r >> 1] >> (16 * (r & 1)));
-                }
-            }
-        } else {
-            if constexpr (EPI == kSlab)
-                store_direct<S>(c, g.slab + split * g.M * g.N, g.N, g.N, g.add != 0, g.M, m0, n0 + wn, wm);
-            else
-                store_direct<S>(c, static_cast<T*>(g.out), g.ldo, g.cols, false, g.M, m0, n0 + wn, wm);
-        }
+        store_direct<S>(c, static_cast<T*>(g.out), g.ldo, g.cols, false, g.M, m0, n0 + wn, wm);
     }
 }
 
@@ -446,24 +464,40 @@ __global__ __launch_bounds__(256) void join(const float2* stats, int64_t tiles, 
     loss[n] = id >= 0 ? coef[n] * (l - target_logit[n]) : (id == -1 ? 0.f : NAN);
 }
 
-// G of a block of rows from its logits, eight neighbours a thread; zeros past the classes. fp32: over the logits.
+// G of a block of rows over what is kept of its logits, eight neighbours a thread; zeros past the classes.
+struct GradArgs {
+    int64_t ld, rows;
+    int V, tile;               // classes a tile of the statistics
+    const float2* stats;
+    const float *lse, *coef, *target_logit;
+    const int32_t* target;
+};
 template <typename T>
-__global__ __launch_bounds__(256) void grad(const float* z, int64_t ld, int64_t rows, int V, const float* lse, const float* coef,
-                                            const int32_t* target, T* out) {
-    const uint32_t per = (uint32_t)(ld / 8), i = blockIdx.x * 256u + threadIdx.x, m = i / per;
-    if (m >= rows) return;
-    const int v = (int)(i - m * per) * 8, id = target[m];
-    const float l = lse[m], k = coef[m];
+__global__ __launch_bounds__(256) void grad(const GradArgs a, T* G) {
+    const uint32_t per = (uint32_t)(a.ld / 8), i = blockIdx.x * 256u + threadIdx.x, m = i / per;
+    if (m >= a.rows) return;
+    const int v = (int)(i - m * per) * 8, id = a.target[m];
+    const float l = a.lse[m], k = a.coef[m];
+    T* p = G + m * a.ld + v;
     float x[8];
-    load_f32<8>(z + m * ld + v, x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        x[e] = k == 0.f || v + e >= V ? 0.f : k * (exp_neg<T>(x[e] - l) - (v + e == id ? 1.f : 0.f));
-    T* o = out + m * ld + v;
     if constexpr (sizeof(T) == 4) {
-        store_f32<8>(o, x);
+        load_f32<8>(p, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = exp_neg<T>(x[e] - l);
     } else {
-        *reinterpret_cast<u32x4*>(o) = u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+        typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+        const h8 q = __builtin_bit_cast(h8, *reinterpret_cast<const u32x4*>(p));
+        const float f = exp_neg<T>(a.stats[v / a.tile * a.rows + m].x - l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (float)q[e] * f;
+    }
+    const float own = id >= v && id < v + 8 ? exp_neg<T>(a.target_logit[m] - l) - 1.f : 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = k == 0.f || v + e >= a.V ? 0.f : k * (v + e == id ? own : x[e]);
+    if constexpr (sizeof(T) == 4) {
+        store_f32<8>(p, x);
+    } else {
+        *reinterpret_cast<u32x4*>(p) = u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
     }
 }
 
@@ -510,20 +544,28 @@ void go_sum(const float* slab, int64_t slabs, int64_t M, int64_t N, T* out, int6
 // ---- plan ---------------------------------------------------------------------------------------------------------
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
+// How often the depth of larger tiles is split so that they fill the compute units; 0: they do not. (dh of 4096 x 2048 over
+// 32000 classes: 484 us in 2 parts, 600 in the smaller tiles; of 1000 x 512 over 100003: 126 in 32 parts, 166.)
+int64_t large_splits(int64_t M, int64_t N, int64_t K, int e, bool split) {
+    const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256), steps = (K * e + 127) / 128;
+    if (M <= 128 || N <= 128 || steps <= 3) return 0;
+    if (tiles >= 192) return 1;
+    const int64_t n = split ? std::min<int64_t>({256 / tiles, steps / 32, int64_t(32)}) : 1;
+    return tiles * n >= 192 ? n : 0;
+}
 // The larger tiles where they fill the compute units; the thin ones for few rows, where those of 128 would spend most of
 // their products on rows that are not there, which fp32 feels first, and for few tiles whose depth is not split.
 Size size_of(int64_t M, int64_t N, int64_t K, int e, bool along, bool split) {
     if (along && M <= (e == 4 ? 64 : 32)) return kThin;
-    const bool fills = ((M + 255) / 256) * ((N + 255) / 256) >= 192;
-    if (fills && M > 128 && N > 128 && K * e > 3 * 128) return kLarge;
+    if (large_splits(M, N, K, e, split)) return kLarge;
     const int64_t small = ((M + 127) / 128) * ((N + 127) / 128) * (split ? std::max<int64_t>(1, K * e / 128 / 2) : 1);
     return along && small < 128 ? kThin : kSmall;
 }
-// how often the depth is split where there are few tiles: so that some 512 workgroups share the work, none with less than
-// two steps of it
+// how often the depth is split where there are few tiles: so that some 512 workgroups share the work (of the larger tiles
+// 256), none with less than two steps of it
 int64_t splits_of(int64_t M, int64_t N, int64_t K, int e, bool along) {
     const Size size = size_of(M, N, K, e, along, true);
-    if (size == kLarge) return 1;
+    if (size == kLarge) return large_splits(M, N, K, e, true);
     const int64_t bm = size == kThin ? 32 : 128, tiles = ((M + bm - 1) / bm) * ((N + 127) / 128), steps = (K * e + 127) / 128;
     return std::max<int64_t>(1, std::min<int64_t>({512 / tiles, steps / 2, int64_t(128)}));
 }
@@ -535,7 +577,7 @@ int64_t vocab_max_classes() { return int64_t(1) << 20; }
 int vocab_max_d() { return 1 << 16; }
 
 // Workspace: the hidden states as they meet the products, the weights too where their rows are no whole number of chunks,
-// the tiles' statistics, a row's numbers, and with gradients a block of logits or a piece of G (or both), dh's slabs and dW's.
+// the tiles' statistics, a row's numbers, and with gradients G of a block of rows, dh's slabs and dW's.
 VocabPlan vocab_plan(int64_t N, int D, int V, int dtype, bool grads) {
     const int e = dtype == 1 ? 2 : 4, chunk = 16 / e;
     constexpr int64_t kMB = int64_t(1) << 20;
@@ -543,22 +585,13 @@ VocabPlan vocab_plan(int64_t N, int D, int V, int dtype, bool grads) {
     p.ldh = up(D, chunk);
     p.pack_w = D % chunk != 0;
     p.rows = std::max<int64_t>(N, 1);
-    p.piece = up(V, 256);
+    p.ldg = up(V, 8);
     grads = grads && N > 0;
-    if (grads) {
-        // logits of up to 256 MB; in bfloat16 they cost 8 bytes of traffic each beside G's, and formed again 2 D operations:
-        // as much at some 800 channels, unless all of it stays in the caches
-        const int64_t fit = std::max<int64_t>(256 * kMB / 4 / V / 128 * 128, 128);
-        p.keep = e == 4 || (N <= fit && (D >= 768 || N * V * 4 <= 32 * kMB));
-        if (p.keep) {
-            const int64_t blocks = (N + fit - 1) / fit;
-            p.rows = std::min(N, up((N + blocks - 1) / blocks, 128));
-            p.piece = up(V, 8);
-        } else {  // at least 2048 classes
-            p.piece = std::min(p.piece, std::max<int64_t>(2048, 128 * kMB / (N * e) / 256 * 256));
-            const int64_t pieces = (V + p.piece - 1) / p.piece;
-            p.piece = up((V + pieces - 1) / pieces, 256);
-        }
+    int64_t blocks = 1;
+    if (grads) {  // G of up to 256 MB, or 1024 rows (fp32, whose products are ten times as dear: 128)
+        const int64_t fit = std::max<int64_t>(256 * kMB / e / V / 128 * 128, e == 4 ? 128 : 1024);
+        blocks = (N + fit - 1) / fit;
+        p.rows = std::min(N, up((N + blocks - 1) / blocks, 128));
     }
     p.tiles = (V + 127) / 128;  // at most
     size_t at = 0;
@@ -575,14 +608,12 @@ VocabPlan vocab_plan(int64_t N, int D, int V, int dtype, bool grads) {
     p.target = take((size_t)N * 4);
     p.coef = take((size_t)N * 4);
     if (grads) {
-        const int64_t cols = std::min<int64_t>(p.piece, V);
-        p.dh_splits = splits_of(p.rows, D, cols, e, true);
-        p.dw_splits = splits_of(cols, D, p.rows, e, false);
-        p.logits = take(p.keep ? (size_t)p.rows * p.piece * 4 : 0);
-        p.g = p.keep && e == 4 ? p.logits : take((size_t)p.rows * p.piece * e);
-        p.dh_slab = p.dh_splits > 1 || cols < V;
-        p.dh = take(p.dh_slab ? (size_t)p.dh_splits * p.rows * D * 4 : 0);
-        p.dw = take(p.dw_splits > 1 ? (size_t)p.dw_splits * cols * D * 4 : 0);
+        p.dh_splits = splits_of(p.rows, D, V, e, true);
+        p.dw_splits = splits_of(V, D, p.rows, e, false);
+        p.g = take((size_t)p.rows * p.ldg * e);
+        p.dh = take(p.dh_splits > 1 ? (size_t)p.dh_splits * p.rows * D * 4 : 0);
+        p.dw_slab = p.dw_splits > 1 || (e == 2 && blocks > 1);  // (blocks of fp32 add up in dW itself)
+        p.dw = take(p.dw_slab ? (size_t)p.dw_splits * V * D * 4 : 0);
     }
     p.total = at;
     return p;
@@ -602,76 +633,73 @@ struct Vocab {
     U* at(size_t o, int64_t i = 0) const {
         return reinterpret_cast<U*>(ws + o) + i;
     }
-    // the logits of rows r0 .. against classes v0 ..
-    Args logits(int64_t r0, int64_t rows, int64_t v0, int64_t cols) const {
+    // losses of rows r0 .., and G of them where there are gradients
+    void losses(int64_t r0, int64_t rows, bool grads) const {
         Args a{};
         a.a = at<T>(p.h, r0 * p.ldh);
-        a.b = W + v0 * p.ldh;
+        a.b = W;
         a.lda = a.ldb = p.ldh;
         a.M = rows;
-        a.N = cols;
+        a.N = x.V;
         a.K = x.D;
         a.ids = at<int32_t>(p.target, r0);
-        a.n_first = v0;
-        a.ldo = p.piece;
-        return a;
-    }
-    Size size(const Args& a) const { return size_of(a.M, a.N, a.K, sizeof(T), true, false); }  // of the logits
-    // losses of rows r0 .., their logits kept where there is a place for them
-    void losses(int64_t r0, int64_t rows, bool keep) const {
-        Args a = logits(r0, rows, 0, x.V);
         a.stats = at<float2>(p.stats);
         a.target = at<float>(p.target_logit, r0);
-        if (keep) a.logits = at<float>(p.logits);
-        const Size s = size(a);
+        if (grads) a.out = at<T>(p.g);
+        a.ldo = a.cols = p.ldg;
+        const Size s = size_of(rows, x.V, x.D, sizeof(T), true, false);
         go<T, true, true, kStats>(a, s, 1, st);
-        const int64_t tiles = (x.V + (s == kLarge ? 255 : 127)) / (s == kLarge ? 256 : 128);
-        launch(join, dim3((uint32_t)((rows + 7) / 8)), dim3(256), 0, st, a.stats, tiles, rows, a.target, a.ids,
-               at<float>(p.coef, r0), at<float>(p.lse, r0), x.loss + r0);
+        const int tile = s == kLarge ? 256 : 128;
+        const float *coef = at<float>(p.coef, r0), *lse = at<float>(p.lse, r0);
+        launch(join, dim3((uint32_t)((rows + 7) / 8)), dim3(256), 0, st, a.stats, (int64_t)((x.V + tile - 1) / tile), rows, a.target,
+               a.ids, coef, at<float>(p.lse, r0), x.loss + r0);
+        if (!grads) return;
+        const GradArgs g{p.ldg, rows, x.V, tile, a.stats, lse, coef, a.target, a.ids};
+        launch(grad<T>, dim3((uint32_t)((rows * (p.ldg / 8) + 255) / 256)), dim3(256), 0, st, g, at<T>(p.g));
     }
-    // G of rows r0 .. and classes v0 .. is at p.g: into dh (first, last: of the pieces) and dW (the same, of the blocks)
-    void take(int64_t r0, int64_t rows, int64_t v0, int64_t cols, bool first_piece, bool last_piece, bool first_block,
-              bool last_block) const {
-        const T* G = at<T>(p.g);
+    // G of rows r0 .. into dh, and into dW, which is a sum over the blocks of rows
+    void take(int64_t r0, int64_t rows) const {
         Args b{};
-        b.a = G;
-        b.b = W + v0 * p.ldh;
-        b.lda = p.piece;
+        b.a = at<T>(p.g);
+        b.b = W;
+        b.lda = p.ldg;
         b.ldb = p.ldh;
         b.M = rows;
         b.N = x.D;
-        b.K = cols;
+        b.K = x.V;
         T* dh = static_cast<T*>(x.dh) + r0 * x.lddh;
         b.out = dh;
         b.ldo = x.lddh;
         b.cols = x.D;
         b.slab = at<float>(p.dh);
-        b.add = !first_piece;
-        const Size sh = size_of(p.rows, x.D, std::min<int64_t>(p.piece, x.V), sizeof(T), true, true);
-        if (p.dh_slab) go<T, true, false, kSlab>(b, sh, p.dh_splits, st);
-        else go<T, true, false, kStore>(b, sh, 1, st);
-        if (p.dh_slab && last_piece) go_sum(b.slab, p.dh_splits, rows, x.D, dh, x.lddh, st);
+        const Size sh = size_of(p.rows, x.D, x.V, sizeof(T), true, true);
+        if (p.dh_splits > 1) {
+            go<T, true, false, kSlab>(b, sh, p.dh_splits, st);
+            go_sum(b.slab, p.dh_splits, rows, x.D, dh, x.lddh, st);
+        } else {
+            go<T, true, false, kStore>(b, sh, 1, st);
+        }
 
+        const bool first = r0 == 0, last = r0 + rows == x.N;
         Args c{};
-        c.a = G;
+        c.a = at<T>(p.g);
         c.b = at<T>(p.h, r0 * p.ldh);
-        c.lda = p.piece;
+        c.lda = p.ldg;
         c.ldb = p.ldh;
-        c.M = cols;
+        c.M = x.V;
         c.N = x.D;
         c.K = rows;
-        T* dW = static_cast<T*>(x.dW) + v0 * x.D;
+        T* dW = static_cast<T*>(x.dW);
         c.out = dW;
-        c.ldo = x.D;
-        c.cols = x.D;
-        c.add = !first_block;
-        const Size sw = size_of(std::min<int64_t>(p.piece, x.V), x.D, p.rows, sizeof(T), false, true);
-        if (p.dw_splits > 1) {
+        c.ldo = c.cols = x.D;
+        c.add = !first;
+        const Size sw = size_of(x.V, x.D, p.rows, sizeof(T), false, true);
+        if (p.dw_slab) {
             c.slab = at<float>(p.dw);
             go<T, false, false, kSlab>(c, sw, p.dw_splits, st);
-            if (last_block) go_sum(c.slab, p.dw_splits, cols, x.D, dW, x.D, st);
-        } else if (sizeof(T) == 4 && !(first_block && last_block)) {
-            c.slab = reinterpret_cast<float*>(dW);  // blocks are several in fp32 alone: dW is its own slab
+            if (last) go_sum(c.slab, p.dw_splits, x.V, x.D, dW, x.D, st);
+        } else if (!(first && last)) {  // fp32: dW is its own slab
+            c.slab = reinterpret_cast<float*>(dW);
             go<T, false, false, kSlab>(c, sw, 1, st);
         } else {
             go<T, false, false, kStore>(c, sw, 1, st);
@@ -679,28 +707,10 @@ struct Vocab {
     }
 
     void run(bool grads) const {
-        if (!p.keep) losses(0, x.N, false);
-        if (!grads) return;
-        if (p.keep) {
-            for (int64_t r0 = 0; r0 < x.N; r0 += p.rows) {
-                const int64_t rows = std::min(p.rows, x.N - r0);
-                losses(r0, rows, true);
-                const int64_t n = rows * (p.piece / 8);
-                launch(grad<T>, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, st, at<float>(p.logits), p.piece, rows, x.V,
-                       at<float>(p.lse, r0), at<float>(p.coef, r0), at<int32_t>(p.target, r0), at<T>(p.g));
-                take(r0, rows, 0, x.V, true, true, r0 == 0, r0 + rows == x.N);
-            }
-            return;
-        }
-        for (int64_t v0 = 0; v0 < x.V; v0 += p.piece) {
-            const int64_t cols = std::min<int64_t>(p.piece, x.V - v0);
-            Args a = logits(0, x.N, v0, cols);
-            a.lse = at<float>(p.lse);
-            a.coef = at<float>(p.coef);
-            a.out = at<T>(p.g);
-            a.cols = up(cols, 16 / (int64_t)sizeof(T));
-            go<T, true, true, kGrad>(a, size(a), 1, st);
-            take(0, x.N, v0, cols, v0 == 0, v0 + cols == x.V, true, true);
+        for (int64_t r0 = 0; r0 < x.N; r0 += p.rows) {
+            const int64_t rows = std::min(p.rows, x.N - r0);
+            losses(r0, rows, grads);
+            if (grads) take(r0, rows);
         }
     }
 };

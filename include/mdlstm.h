@@ -667,12 +667,13 @@ int mdl_dropout(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx,
  * dh [N][D] at row stride lddh and dW [V][D], of `dtype`, both or neither (NULL: the
  * loss alone); with N = 0, dW alone is given and is zero. dh may be h itself; other
  * overlaps of outputs with inputs are not allowed.
- * Logits are float32 sums of the inputs' products and are not rounded; statistics
- * and losses are float32. G's values are rounded to `dtype` before the products
- * with W and h, whose sums are float32 and rounded once. The workspace holds logits
- * of a block of rows (up to 256 MB of them, or 128 rows) or G of a piece of the
- * vocabulary (up to 128 MB, or 2048 classes), whatever N and V are; where it holds
- * the latter, the logits are formed twice.
+ * Logits are float32 sums of the inputs' products; statistics and losses are float32.
+ * With gradients, bfloat16 keeps a block of rows' exponentials in half precision
+ * (the target's in float32), fp32 its logits as they are. G's values are rounded to
+ * `dtype` before the products with W and h, whose sums are float32 and rounded once.
+ * The workspace holds that block as G (up to 256 MB of it, or 1024 rows in bfloat16
+ * and 128 in float32, whatever N is) and, in bfloat16 where there are several, a
+ * float32 dW.
  * ws: >= mdl_vocab_loss_workspace_size bytes (grads: whether dh and dW are wanted),
  * 16-byte aligned, contents not kept.
  * Errors: MDL_EINVAL for null tensors, N < 0, D, V < 1, a stride below D, an unknown

@@ -69,7 +69,12 @@ def tolerances(h, W, ids, w, ref, dtype):
     hot = np.zeros((N, V))
     hot[np.arange(N)[live], ids[live]] = 1
     G = aw * np.abs(p - hot)
-    dG = aw * p * ((dz + dlse)[:, None] + (np.abs(z - lse[:, None]) + 4) * U) + (2 * U + HALF[dtype] * 1.01) * G
+    # bfloat16: what is kept of a logit is q = exp(z - top) <= 1, top its tile's maximum, in half precision, whose error is
+    # 2^-11 q at most, or 2^-25 below its smallest normal number; then p = q exp(top - lse), so that p is off by 2^-11 p or
+    # by 2^-25 exp(top - lse) = 2^-25 of the tile's largest p. The target's p does not come from there. (The second
+    # exponential is 4 U, and |z - top| + |top - lse| is |z - lse|.)
+    kept = (1 - hot) * (p * 2.0 ** -11 + p.max(1)[:, None] * 2.0 ** -25 + 4 * U * p) if dtype == "bf16" else 0
+    dG = aw * (p * ((dz + dlse)[:, None] + (np.abs(z - lse[:, None]) + 4) * U) + kept) + (2 * U + HALF[dtype] * 1.01) * G
     th = dG @ np.abs(W) + (V + 2) * U * (G @ np.abs(W))
     tW = dG.T @ np.abs(h) + (N + 2) * U * (G.T @ np.abs(h))
     return tl, th + HALF[dtype] * (np.abs(dh) + th), tW + HALF[dtype] * (np.abs(dW) + tW)
@@ -108,9 +113,11 @@ def test_large_logits(dtype):
 
 
 @pytest.mark.parametrize("dtype,N,D,V", [("bf16", 16500, 24, 8000), ("f32", 5000, 8, 9000), ("bf16", 700, 40, 60000),
-                                         ("bf16", 6000, 256, 12800), ("f32", 1000, 64, 70000), ("f32", 40, 300, 9001), ("f32", 9000, 8, 9000)])
+                                         ("bf16", 6000, 256, 12800), ("f32", 1000, 64, 70000), ("f32", 40, 300, 9001), ("f32", 9000, 8, 9000),
+                                         ("bf16", 2500, 24, 130001), ("bf16", 40000, 24, 8000), ("bf16", 3500, 512, 40000),
+                                         ("bf16", 1024, 512, 50000)])
 def test_pieces_and_large_tiles(dtype, N, D, V):
-    """Vocabularies of several pieces, and sizes that take the larger tiles; the reference in float64 on the device."""
+    """Several blocks of rows, and sizes that take the larger tiles; the reference in float64 on the device."""
     h, W, ids, w = _inputs(17, N, D, V, dtype)
     vl = VocabLoss(N, D, V, dtype, device=DEV)
     loss, dh, dW = vl.run(h, W, ids, w)
@@ -133,6 +140,8 @@ def test_pieces_and_large_tiles(dtype, N, D, V):
         dz = (D + 2) * U * zmax
         dl = dz + (80 + V / 512) * U + 2 * U * lse.abs()
         dg = wd[a:a + 1000, None] * p * ((dz + dl)[:, None] + ((z - lse[:, None]).abs() + 4) * U)
+        if dtype == "bf16":  # the rounding of what is kept, as in tolerances()
+            dg += wd[a:a + 1000, None] * (p * 2.0 ** -11 + p.max(1).values[:, None] * 2.0 ** -25 + 4 * U * p)
         dg += (2 * U + 1.01 * HALF[dtype]) * g.abs()
         eps = torch.cat([eps, wd[a:a + 1000] * (dz + dl + 2 * U * (lse.abs() + z[r, i].abs()))]) if a else \
             wd[a:a + 1000] * (dz + dl + 2 * U * (lse.abs() + z[r, i].abs()))

@@ -445,19 +445,29 @@ __global__ __launch_bounds__(256) void pack(const T* src, int64_t ld, int64_t n,
     }
 }
 
-// A row's tiles joined, 8 rows by 32 groups of tiles a workgroup.
+// A row's tiles joined, 8 rows by 32 groups of tiles a workgroup: each group's own, then the groups of a wave, then the waves.
 __global__ __launch_bounds__(256) void join(const float2* stats, int64_t tiles, int64_t N, const float* target_logit,
                                             const int32_t* target, const float* coef, float* lse, float* loss) {
-    __shared__ float2 part[32][8];
+    __shared__ float2 part[4][8];
     const int r = threadIdx.x & 7, grp = threadIdx.x >> 3;
     const int64_t n = (int64_t)blockIdx.x * 8 + r;
     float2 p = make_float2(-INFINITY, 0.f);
-    if (n < N)
-        for (int64_t t = grp; t < tiles; t += 32) p = joined(p, stats[t * N + n]);
-    part[grp][r] = p;
+    if (n < N) {
+        constexpr int U = 4;  // loads at once
+        for (int64_t t = grp; t < tiles; t += 32 * U) {
+            float2 q[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = t + 32 * u < tiles ? stats[(t + 32 * u) * N + n] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int u = 0; u < U; ++u) p = joined(p, q[u]);
+        }
+    }
+#pragma unroll
+    for (int m = 8; m < 64; m *= 2) p = joined(p, make_float2(__shfl_xor(p.x, m), __shfl_xor(p.y, m)));
+    if ((threadIdx.x & 63) < 8) part[threadIdx.x >> 6][r] = p;
     __syncthreads();
     if (grp != 0 || n >= N) return;
-    for (int i = 1; i < 32; ++i) p = joined(p, part[i][r]);
+    for (int i = 1; i < 4; ++i) p = joined(p, part[i][r]);
     const float l = p.x + logf(p.y);
     lse[n] = l;
     const int id = target[n];

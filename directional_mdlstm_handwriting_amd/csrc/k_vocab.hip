@@ -337,16 +337,25 @@ __global__ __launch_bounds__(S::threads, 2) void product(const Args g) {
             const int row = wm + 32 * i + (lane & 31);
             const int64_t m = m0 + row;
             const int64_t id = m < g.M ? (int64_t)g.ids[m] - n0 : -1;
+            if (__any(id >= wn && id < wn + 32 * S::TN)) {  // few waves hold a target
+#pragma unroll
+                for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (wn + 32 * j + 8 * (e >> 2) + 4 * h + (e & 3) == id) g.target[m] = c[i][j][e];
+            }
+            if (limit < S::BN) {
+#pragma unroll
+                for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (wn + 32 * j + 8 * (e >> 2) + 4 * h + (e & 3) >= limit) c[i][j][e] = -INFINITY;
+            }
             float top = -INFINITY;
 #pragma unroll
             for (int j = 0; j < S::TN; ++j)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int n = wn + 32 * j + 8 * (e >> 2) + 4 * h + (e & 3);
-                    if (n >= limit) c[i][j][e] = -INFINITY;
-                    if (n == id) g.target[m] = c[i][j][e];
-                    top = fmaxf(top, c[i][j][e]);
-                }
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, c[i][j][e]);
             top = fmaxf(top, __shfl_xor(top, 32));
             if (h == 0) part[wave % S::WN][row].x = top;
         }

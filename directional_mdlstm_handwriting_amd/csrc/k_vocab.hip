@@ -420,8 +420,9 @@ void go_shape(Args g, int64_t splits, hipStream_t st) {
 }
 template <typename T, bool AA, bool BA, int EPI>
 void go(const Args& g, Size size, int64_t splits, hipStream_t st) {
-    if (size == kLarge) go_shape<T, Large, AA, BA, EPI>(g, splits, st);
-    else if (size == kSmall || !AA) go_shape<T, Small, AA, BA, EPI>(g, splits, st);
+    if (size == kLarge) {
+        if constexpr (sizeof(T) == 2) go_shape<T, Large, AA, BA, EPI>(g, splits, st);
+    } else if (size == kSmall || !AA) go_shape<T, Small, AA, BA, EPI>(g, splits, st);
     else if constexpr (AA) go_shape<T, Thin, AA, BA, EPI>(g, splits, st);
 }
 
@@ -568,30 +569,44 @@ void go_sum(const float* slab, int64_t slabs, int64_t M, int64_t N, T* out, int6
 // ---- plan ---------------------------------------------------------------------------------------------------------
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-// How often the depth of larger tiles is split so that they fill the compute units; 0: they do not. (dh of 4096 x 2048 over
-// 32000 classes: 484 us in 2 parts, 600 in the smaller tiles; of 1000 x 512 over 100003: 126 in 32 parts, 166.)
-int64_t large_splits(int64_t M, int64_t N, int64_t K, int e, bool split) {
-    const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256), steps = (K * e + 127) / 128;
-    if (M <= 128 || N <= 128 || steps <= 3) return 0;
-    if (tiles >= 192) return 1;
-    const int64_t n = split ? std::min<int64_t>({256 / tiles, steps / 32, int64_t(32)}) : 1;
-    return tiles * n >= 192 ? n : 0;
-}
-// The larger tiles where they fill the compute units; the thin ones for few rows, where those of 128 would spend most of
-// their products on rows that are not there, which fp32 feels first, and for few tiles whose depth is not split.
-Size size_of(int64_t M, int64_t N, int64_t K, int e, bool along, bool split) {
-    if (along && M <= (e == 4 ? 64 : 32)) return kThin;
-    if (large_splits(M, N, K, e, split)) return kLarge;
-    const int64_t small = ((M + 127) / 128) * ((N + 127) / 128) * (split ? std::max<int64_t>(1, K * e / 128 / 2) : 1);
-    return along && small < 128 ? kThin : kSmall;
-}
-// how often the depth is split where there are few tiles: so that some 512 workgroups share the work (of the larger tiles
-// 256), none with less than two steps of it
-int64_t splits_of(int64_t M, int64_t N, int64_t K, int e, bool along) {
-    const Size size = size_of(M, N, K, e, along, true);
-    if (size == kLarge) return large_splits(M, N, K, e, true);
-    const int64_t bm = size == kThin ? 32 : 128, tiles = ((M + bm - 1) / bm) * ((N + 127) / 128), steps = (K * e + 127) / 128;
-    return std::max<int64_t>(1, std::min<int64_t>({512 / tiles, steps / 2, int64_t(128)}));
+struct Cut {
+    Size size;
+    int64_t splits;  // parts of the depth, whose sums are joined afterwards
+};
+// How a product is cut. Thin tiles for few rows, where those of 128 would spend most of their products on rows that are not
+// there, which fp32 feels first, and for few tiles whose depth is not split. Otherwise what an estimate of the time says: a
+// compute unit takes one of the larger tiles at a time or two small ones, rounds come out even or not, a part of the depth
+// costs its sums' way to memory and back, a round its loads' latency and its results. In fp32 the small tiles are as fast as
+// the larger ones (4096 x 2048 over 32000: 12.0 ms both) and leave less of the last round idle (19795 x 1664 over 4193: 6.8
+// ms, 8.9 in the larger ones), so that the larger ones are bfloat16's alone (dh of 4096 x 2048 over 32000: 484 us in 2 parts
+// of larger tiles, 600 in small ones).
+Cut cut_of(int64_t M, int64_t N, int64_t K, int e, bool along, bool split) {
+    const int64_t steps = (K * e + 127) / 128;
+    const auto tiles_of = [&](int64_t b) { return ((M + b - 1) / b) * ((N + b - 1) / b); };
+    const int64_t small = tiles_of(128), most = split ? std::max<int64_t>(1, steps / 2) : 1;
+    if (along && (M <= (e == 4 ? 64 : 32) || small * most < 128)) {
+        const int64_t tiles = ((M + 31) / 32) * ((N + 127) / 128);
+        return {kThin, split ? std::max<int64_t>(1, std::min<int64_t>({512 / tiles, most, int64_t(128)})) : 1};
+    }
+    Cut best{kSmall, 1};
+    double least = 1e300;
+    const auto look = [&](Size size, int64_t tiles, double rate, double round, int64_t n) {
+        const double b = size == kLarge ? 256 : 128;
+        const int64_t t = tiles * n, rest = t % 512;
+        const double rounds = size == kLarge ? (double)((t + 255) / 256) : (double)(t / 512) * 2 + (rest > 256 ? 2. : rest > 0 ? 1.3 : 0.);
+        const double sums = n > 1 ? 5e-6 + 8. * (double)n * (double)M * (double)N / 5e12 : 0.;
+        const double cost = rounds * (2. * b * b * (double)K / (double)n / (rate / 256) + round) + sums;
+        if (cost < least) {
+            least = cost;
+            best = {size, n};
+        }
+    };
+    for (const int64_t n : {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 20, 24, 32, 48, 64, 96, 128}) {
+        if (n > most) break;
+        look(kSmall, small, e == 2 ? 0.85e15 : 1.35e14, 1.5e-6, n);
+        if (e == 2 && M > 128 && N > 128 && steps / n > 3) look(kLarge, tiles_of(256), 1.1e15, 3e-6, n);
+    }
+    return best;
 }
 
 }  // namespace
@@ -632,8 +647,11 @@ VocabPlan vocab_plan(int64_t N, int D, int V, int dtype, bool grads) {
     p.target = take((size_t)N * 4);
     p.coef = take((size_t)N * 4);
     if (grads) {
-        p.dh_splits = splits_of(p.rows, D, V, e, true);
-        p.dw_splits = splits_of(V, D, p.rows, e, false);
+        const Cut dh = cut_of(p.rows, D, V, e, true, true), dw = cut_of(V, D, p.rows, e, false, true);
+        p.dh_size = dh.size;
+        p.dh_splits = dh.splits;
+        p.dw_size = dw.size;
+        p.dw_splits = dw.splits;
         p.g = take((size_t)p.rows * p.ldg * e);
         p.dh = take(p.dh_splits > 1 ? (size_t)p.dh_splits * p.rows * D * 4 : 0);
         p.dw_slab = p.dw_splits > 1 || (e == 2 && blocks > 1);  // (blocks of fp32 add up in dW itself)
@@ -671,7 +689,7 @@ struct Vocab {
         a.target = at<float>(p.target_logit, r0);
         if (grads) a.out = at<T>(p.g);
         a.ldo = a.cols = p.ldg;
-        const Size s = size_of(rows, x.V, x.D, sizeof(T), true, false);
+        const Size s = cut_of(rows, x.V, x.D, sizeof(T), true, false).size;
         go<T, true, true, kStats>(a, s, 1, st);
         const int tile = s == kLarge ? 256 : 128;
         const float *coef = at<float>(p.coef, r0), *lse = at<float>(p.lse, r0);
@@ -696,7 +714,7 @@ struct Vocab {
         b.ldo = x.lddh;
         b.cols = x.D;
         b.slab = at<float>(p.dh);
-        const Size sh = size_of(p.rows, x.D, x.V, sizeof(T), true, true);
+        const Size sh = (Size)p.dh_size;
         if (p.dh_splits > 1) {
             go<T, true, false, kSlab>(b, sh, p.dh_splits, st);
             go_sum(b.slab, p.dh_splits, rows, x.D, dh, x.lddh, st);
@@ -717,7 +735,7 @@ struct Vocab {
         c.out = dW;
         c.ldo = c.cols = x.D;
         c.add = !first;
-        const Size sw = size_of(x.V, x.D, p.rows, sizeof(T), false, true);
+        const Size sw = (Size)p.dw_size;
         if (p.dw_slab) {
             c.slab = at<float>(p.dw);
             go<T, false, false, kSlab>(c, sw, p.dw_splits, st);

@@ -411,6 +411,7 @@ struct VocabPlan {
     int64_t ldh = 0, tiles = 0;
     int64_t rows = 0, ldg = 0;        // rows a block, and a row of G
     int64_t dh_splits = 1, dw_splits = 1;
+    int dh_size = 0, dw_size = 0;     // of their products' tiles
     bool pack_w = false, dw_slab = false;
     size_t h = 0, w = 0, stats = 0, lse = 0, target_logit = 0, target = 0, coef = 0, g = 0, dh = 0, dw = 0, total = 0;
 };

@@ -18,9 +18,9 @@
 // boundaries the slots from off[s] / L on, which are as many as it can need; T / L + S numbers and T / L slots in all.
 //
 // What bounds it. bfloat16: memory. Both ways over 4 documents (208246 tokens, 8 heads of 128 + 128) move each tensor 18 times
-// (426 MB each; states 2, outputs 4, states 2, dv and dk 6, dq 4) where 8 would do, in 1.93 ms: 217 + 406 + 215 + 674 + 398 us
-// and two chains of 19, 3.8 to 4.2 TB/s, the matrix units busy for 19 to 33 % of the cycles. fp32 with heads of 50 (656603
-// tokens, 1024 sequences): the matrix units, busy for 50 % of them in the outputs (195 + 399 + 199 of 940 us; 64 x 64 padded).
+// (426 MB each; states 2, outputs 4, states 2, dv and dk 6, dq 4) where 8 would do, in 1.93 ms: 219 + 404 + 217 + 688 + 402 us
+// and two chains of 19, 3.7 to 4.2 TB/s, the matrix units busy for 19 to 33 % of the cycles. fp32 with heads of 50 (656603
+// tokens, 1024 sequences): the matrix units, busy for 50 % of them in the outputs (200 + 405 + 205 us of 941 in all; 64 x 64 padded).
 #include "kernels.h"
 #include "seqio.h"
 
@@ -873,7 +873,7 @@ int linattn_max_d() { return 128; }
 // Tiles: so many that their workgroups fill the chip a whole number of times, as many tiles as sequences at least beside the
 // sequences' own (whose last tiles are short): once where there are few sequences, since a tile costs its state's way to
 // memory and back, else four times, since tiles of many lengths do not end together. Wide heads have three workgroups a
-// compute unit, narrow ones four. At 656603 x 50 (fp32, 1024 sequences, both ways) tiles of 224 take 987 us, of 672 1101.
+// compute unit, narrow ones four. At 656603 x 50 (fp32, 1024 sequences, both ways) tiles of 224 take 941 to 987 us, of 672 1101.
 AttnPlan attn_plan(int S, int64_t T, int H, int Dk, int Dv) {
     AttnPlan p;
     const int64_t fill = (std::max(Dk, Dv) > 64 ? 3 : 4) * 256;

@@ -10,7 +10,7 @@
 // fp32 logit). `grad` makes G of them where they lie, and two products take G into dh and dW: 6 N V D operations. Several
 // blocks add up dW in fp32, which costs 8 bytes an element and block: at 1024 rows a quarter of the block's products.
 // (Forming the logits again, once the statistics are known, is 8 N V D operations and nothing written but G: 4096 x 2048 over
-// 32000 classes in bfloat16 took 1985 us that way and takes 1550, in fp32 15.6 and 12.0 ms.)
+// 32000 classes in bfloat16 took 1985 us that way and takes 1536, in fp32 15.6 and 12.0 ms.)
 //
 // Products: tiles of BM x BN by 8 (4) waves, 32 x 32 results of the matrix instructions (32x32x16 bfloat16, 32x32x2 fp32),
 // 128 bytes of depth at a time from global memory straight into LDS, one step ahead of the products. An operand whose rows
@@ -18,8 +18,8 @@
 // all banks (turned by every row: 3.9 cycles of conflicts a read, now 0.2, and the same time); one whose rows run across it
 // is laid as it comes and read by transposing reads (bfloat16) or word by word (fp32).
 //
-// Measured, 4096 x 2048 over 32000 classes in bfloat16 (537 GFLOP a product): logits and statistics 563 us, of which writing
-// 262 MB is some 50, dh 495 + 14, dW 469 (0.95, 1.08 and 1.14 PFLOP/s; the matrix units are busy for 51, 55 and 61 % of the
+// Measured, 4096 x 2048 over 32000 classes in bfloat16 (537 GFLOP a product): logits and statistics 576 us, of which writing
+// 262 MB is some 50, dh 501 + 14, dW 488 (0.93, 1.07 and 1.10 PFLOP/s; the matrix units are busy for 51, 55 and 61 % of the
 // cycles; the library's 8192^3 reaches 1.39), G 84 (524 MB at 6.2 TB/s), packing and joining 16.
 #include "kernels.h"
 #include "seqio.h"
@@ -578,7 +578,7 @@ struct Cut {
 // compute unit takes one of the larger tiles at a time or two small ones, rounds come out even or not, a part of the depth
 // costs its sums' way to memory and back, a round its loads' latency and its results. In fp32 the small tiles are as fast as
 // the larger ones (4096 x 2048 over 32000: 12.0 ms both) and leave less of the last round idle (19795 x 1664 over 4193: 6.8
-// ms, 8.9 in the larger ones), so that the larger ones are bfloat16's alone (dh of 4096 x 2048 over 32000: 484 us in 2 parts
+// ms, 8.9 in the larger ones), so that the larger ones are bfloat16's alone (dh of 4096 x 2048 over 32000: 501 us in 2 parts
 // of larger tiles, 600 in small ones).
 Cut cut_of(int64_t M, int64_t N, int64_t K, int e, bool along, bool split) {
     const int64_t steps = (K * e + 127) / 128;

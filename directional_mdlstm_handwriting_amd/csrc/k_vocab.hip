@@ -5,9 +5,9 @@
 //
 // A first product, a block of rows at a time, leaves per row and 256 (or 128) classes their maximum and sum of exponentials,
 // and the target's logit; `join` makes the losses of them. With gradients it also keeps the block's logits: in fp32 as they
-// are, in bfloat16 the exponentials below their tile's maximum as 16 bits of half precision (a rounding of 2^-11 of the value,
-// an eighth of the one G is about to get, or of 2^-25 of the maximum; the target's own, from which 1 is taken, comes from its
-// fp32 logit). `grad` makes G of them where they lie, and two products take G into dh and dW: 6 N V D operations. Several
+// are, in bfloat16 the exponentials below their tile's maximum, times 2^15, as 16 bits of half precision (a rounding of 2^-11
+// of the value, an eighth of the one G is about to get, or of 2^-40 of the maximum; the target's own, from which 1 is taken,
+// comes from its fp32 logit). `grad` makes G of them where they lie, and two products take G into dh and dW: 6 N V D operations. Several
 // blocks add up dW in fp32, which costs 8 bytes an element and block: at 1024 rows a quarter of the block's products.
 // (Forming the logits again, once the statistics are known, is 8 N V D operations and nothing written but G: 4096 x 2048 over
 // 32000 classes in bfloat16 took 1985 us that way and takes 1536, in fp32 15.6 and 12.0 ms.)
@@ -190,11 +190,13 @@ struct Args {
 
 enum { kStats, kStore, kSlab };
 
-// two values as 16 bits each, the nearest ones: half precision or bfloat16
+// two values as 16 bits each, the nearest ones: exponentials of at most 1 times kHalfScale in half precision (1 becomes 2^15,
+// half precision's largest power of 2, and what is 2^-29 of it still has all its bits), or bfloat16
+constexpr float kHalfScale = 32768.f;
 template <bool HALF>
 __device__ inline uint32_t pack16(float a, float b) {
     typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-    if constexpr (HALF) return __builtin_bit_cast(uint32_t, h2{(_Float16)a, (_Float16)b});
+    if constexpr (HALF) return __builtin_bit_cast(uint32_t, h2{(_Float16)(a * kHalfScale), (_Float16)(b * kHalfScale)});
     else return pack_bf16(a, b);
 }
 
@@ -512,7 +514,7 @@ __global__ __launch_bounds__(256) void grad(const GradArgs a, T* G) {
     } else {
         typedef _Float16 h8 __attribute__((ext_vector_type(8)));
         const h8 q = __builtin_bit_cast(h8, *reinterpret_cast<const u32x4*>(p));
-        const float f = exp_neg<T>(a.stats[v / a.tile * a.rows + m].x - l);
+        const float f = exp_neg<T>(a.stats[v / a.tile * a.rows + m].x - l) * (1.f / kHalfScale);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = (float)q[e] * f;
     }

@@ -3,11 +3,14 @@
 //
 //   z = h W^T,  loss_n = w_n (ln sum_c exp z_nc - z_n,id),  G = w (softmax z - [c = id]),  dh = G W,  dW = G^T h
 //
-// A first product, a block of rows at a time, leaves per row and 256 (or 128) classes their maximum and sum of exponentials,
-// and the target's logit; `join` makes the losses of them. With gradients it also keeps the block's logits: in fp32 as they
+// A first product, a block of rows at a time, leaves per row and 256 (or 128) classes the maximum and sum of exponentials of
+// those that are not the target, and the target's logit; `join` makes the losses of them. With the target t apart, and e_c =
+// exp(z_c - top) below the larger of the others' maximum and z_t,
+//   loss = w ln(1 + sum e_c) where z_t is the larger, w (top - z_t + ln(e_t + sum e_c)) else,  p_t - 1 = -sum e_c / (e_t + sum e_c)
+// in which nothing cancels: a row that is sure of its target has its small loss and gradient, whatever its logits have in
+// common (as one float, the logarithm of the whole sum is off by half a step of the largest logit). With gradients it also keeps the block's logits: in fp32 as they
 // are, in bfloat16 the exponentials below their tile's maximum, times 2^15, as 16 bits of half precision (a rounding of 2^-11
-// of the value, an eighth of the one G is about to get, or of 2^-40 of the maximum; the target's own, from which 1 is taken,
-// comes from its fp32 logit). `grad` makes G of them where they lie, and two products take G into dh and dW: 6 N V D operations. Several
+// of the value, an eighth of the one G is about to get, or of 2^-40 of the maximum). `grad` makes G of them where they lie, and two products take G into dh and dW: 6 N V D operations. Several
 // blocks add up dW in fp32, which costs 8 bytes an element and block: at 1024 rows a quarter of the block's products.
 // (Forming the logits again, once the statistics are known, is 8 N V D operations and nothing written but G: 4096 x 2048 over
 // 32000 classes in bfloat16 took 1985 us that way and takes 1536, in fp32 15.6 and 12.0 ms.)
@@ -349,7 +352,10 @@ __global__ __launch_bounds__(S::threads, 2) void product(const Args g) {
                 for (int j = 0; j < S::TN; ++j)
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        if (wn + 32 * j + 8 * (e >> 2) + 4 * h + (e & 3) == id) g.target[m] = c[i][j][e];
+                        if (wn + 32 * j + 8 * (e >> 2) + 4 * h + (e & 3) == id) {
+                            g.target[m] = c[i][j][e];
+                            c[i][j][e] = -INFINITY;  // the statistics are the other classes'
+                        }
             }
             if (limit < S::BN) {
 #pragma unroll
@@ -462,9 +468,11 @@ __global__ __launch_bounds__(256) void pack(const T* src, int64_t ld, int64_t n,
     }
 }
 
-// A row's tiles joined, 8 rows by 32 groups of tiles a workgroup: each group's own, then the groups of a wave, then the waves.
-__global__ __launch_bounds__(256) void join(const float2* stats, int64_t tiles, int64_t N, const float* target_logit,
-                                            const int32_t* target, const float* coef, float* lse, float* loss) {
+// A row's tiles joined, 8 rows by 32 groups of tiles a workgroup: each group's own, then the groups of a wave, then the waves,
+// then the target. Leaves the loss and, for `grad`, the row's maximum, the inverse of its sum below it, and the target's p - 1
+// (where its logit was).
+__global__ __launch_bounds__(256) void join(const float2* stats, int64_t tiles, int64_t N, float* own,
+                                            const int32_t* target, const float* coef, float2* norm, float* loss) {
     __shared__ float2 part[4][8];
     const int r = threadIdx.x & 7, grp = threadIdx.x >> 3;
     const int64_t n = (int64_t)blockIdx.x * 8 + r;
@@ -485,10 +493,19 @@ __global__ __launch_bounds__(256) void join(const float2* stats, int64_t tiles, 
     __syncthreads();
     if (grp != 0 || n >= N) return;
     for (int i = 1; i < 4; ++i) p = joined(p, part[i][r]);
-    const float l = p.x + logf(p.y);
-    lse[n] = l;
     const int id = target[n];
-    loss[n] = id >= 0 ? coef[n] * (l - target_logit[n]) : (id == -1 ? 0.f : NAN);
+    if (id < 0) {
+        norm[n] = make_float2(0.f, 0.f);
+        own[n] = 0.f;
+        loss[n] = id == -1 ? 0.f : NAN;
+        return;
+    }
+    // NaN and +inf among the logits, and -inf in all of them, make one of the exponentials NaN, and with it everything
+    const float z = own[n], top = fmaxf(p.x, z);
+    const float others = p.y * exp_neg<float>(p.x - top), t = exp_neg<float>(z - top), sum = others + t;
+    norm[n] = make_float2(top, 1.f / sum);
+    own[n] = -others / sum;
+    loss[n] = coef[n] * (z >= p.x ? log1pf(others * t) : p.x - z + logf(sum));
 }
 
 // G of a block of rows over what is kept of its logits, eight neighbours a thread; zeros past the classes.
@@ -496,7 +513,8 @@ struct GradArgs {
     int64_t ld, rows;
     int V, tile;               // classes a tile of the statistics
     const float2* stats;
-    const float *lse, *coef, *target_logit;
+    const float2* norm;
+    const float *coef, *own;
     const int32_t* target;
 };
 template <typename T>
@@ -504,21 +522,22 @@ __global__ __launch_bounds__(256) void grad(const GradArgs a, T* G) {
     const uint32_t per = (uint32_t)(a.ld / 8), i = blockIdx.x * 256u + threadIdx.x, m = i / per;
     if (m >= a.rows) return;
     const int v = (int)(i - m * per) * 8, id = a.target[m];
-    const float l = a.lse[m], k = a.coef[m];
+    const float2 row = a.norm[m];
+    const float k = a.coef[m];
     T* p = G + m * a.ld + v;
     float x[8];
     if constexpr (sizeof(T) == 4) {
         load_f32<8>(p, x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = exp_neg<T>(x[e] - l);
+        for (int e = 0; e < 8; ++e) x[e] = exp_neg<T>(x[e] - row.x) * row.y;
     } else {
         typedef _Float16 h8 __attribute__((ext_vector_type(8)));
         const h8 q = __builtin_bit_cast(h8, *reinterpret_cast<const u32x4*>(p));
-        const float f = exp_neg<T>(a.stats[v / a.tile * a.rows + m].x - l) * (1.f / kHalfScale);
+        const float f = exp_neg<T>(a.stats[v / a.tile * a.rows + m].x - row.x) * row.y * (1.f / kHalfScale);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = (float)q[e] * f;
     }
-    const float own = id >= v && id < v + 8 ? exp_neg<T>(a.target_logit[m] - l) - 1.f : 0.f;
+    const float own = a.own[m];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = k == 0.f || v + e >= a.V ? 0.f : k * (v + e == id ? own : x[e]);
     if constexpr (sizeof(T) == 4) {
@@ -644,7 +663,7 @@ VocabPlan vocab_plan(int64_t N, int D, int V, int dtype, bool grads) {
     p.h = take((size_t)N * p.ldh * e);
     p.w = take(p.pack_w ? (size_t)V * p.ldh * e : 0);
     p.stats = take((size_t)p.tiles * p.rows * sizeof(float2));
-    p.lse = take((size_t)N * 4);
+    p.norm = take((size_t)N * 8);
     p.target_logit = take((size_t)N * 4);
     p.target = take((size_t)N * 4);
     p.coef = take((size_t)N * 4);
@@ -694,11 +713,12 @@ struct Vocab {
         const Size s = cut_of(rows, x.V, x.D, sizeof(T), true, false).size;
         go<T, true, true, kStats>(a, s, 1, st);
         const int tile = s == kLarge ? 256 : 128;
-        const float *coef = at<float>(p.coef, r0), *lse = at<float>(p.lse, r0);
+        const float* coef = at<float>(p.coef, r0);
+        float2* norm = at<float2>(p.norm, r0);
         launch(join, dim3((uint32_t)((rows + 7) / 8)), dim3(256), 0, st, a.stats, (int64_t)((x.V + tile - 1) / tile), rows, a.target,
-               a.ids, coef, at<float>(p.lse, r0), x.loss + r0);
+               a.ids, coef, norm, x.loss + r0);
         if (!grads) return;
-        const GradArgs g{p.ldg, rows, x.V, tile, a.stats, lse, coef, a.target, a.ids};
+        const GradArgs g{p.ldg, rows, x.V, tile, a.stats, norm, coef, a.target, a.ids};
         launch(grad<T>, dim3((uint32_t)((rows * (p.ldg / 8) + 255) / 256)), dim3(256), 0, st, g, at<T>(p.g));
     }
     // G of rows r0 .. into dh, and into dW, which is a sum over the blocks of rows

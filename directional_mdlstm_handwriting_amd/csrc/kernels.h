@@ -413,7 +413,7 @@ struct VocabPlan {
     int64_t dh_splits = 1, dw_splits = 1;
     int dh_size = 0, dw_size = 0;     // of their products' tiles
     bool pack_w = false, dw_slab = false;
-    size_t h = 0, w = 0, stats = 0, lse = 0, target_logit = 0, target = 0, coef = 0, g = 0, dh = 0, dw = 0, total = 0;
+    size_t h = 0, w = 0, stats = 0, norm = 0, target_logit = 0, target = 0, coef = 0, g = 0, dh = 0, dw = 0, total = 0;
 };
 int64_t vocab_max_classes();
 int vocab_max_d();

@@ -667,10 +667,12 @@ int mdl_dropout(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx,
  * dh [N][D] at row stride lddh and dW [V][D], of `dtype`, both or neither (NULL: the
  * loss alone); with N = 0, dW alone is given and is zero. dh may be h itself; other
  * overlaps of outputs with inputs are not allowed.
- * Logits are float32 sums of the inputs' products; statistics and losses are float32.
+ * Logits are float32 sums of the inputs' products; statistics and losses are float32,
+ * the target's apart from the others', so that a small loss or p - 1 is right
+ * relative to itself.
  * With gradients, bfloat16 keeps a block of rows' exponentials in half precision,
  * to 2^-11 of each or 2^-40 of the largest of the 256 classes around it (the
- * target's in float32), fp32 its logits as they are. G's values are rounded to
+ * target's is not among them), fp32 its logits as they are. G's values are rounded to
  * `dtype` before the products with W and h, whose sums are float32 and rounded once.
  * The workspace holds that block as G (up to 256 MB of it, or 1024 rows in bfloat16
  * and 128 in float32, whatever N is) and, in bfloat16 where there are several, a

@@ -110,6 +110,25 @@ def test_classes_far_below_the_best_one(V, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,target", [(90, 0), (90, 89), (700, 300), (700, 699), (257, 256), (2, 1)])
+@pytest.mark.parametrize("offset", [0, 30, 300, -300])
+@pytest.mark.parametrize("gap", [10, 14, 18, 30])
+def test_sure_rows(gap, offset, V, target, dtype):
+    """Losses and gradients of e^-10 to e^-68 beside logits of up to some hundreds: right relative to themselves."""
+    N = 33
+    gaps = gap + np.arange(V) % 5.0
+    gaps[target] = 0.0
+    h, W = _inputs(gap + V, offset, 1 + np.arange(N) % 2, gaps, dtype)
+    ids = np.full(N, target, np.int64)
+    w = torch.rand(N, generator=torch.Generator().manual_seed(2)) + 0.25
+    vl = VocabLoss(N, D, V, dtype, device=DEV)
+    got = [t.clone() for t in vl.run(h, W, torch.as_tensor(ids, dtype=torch.int32, device=DEV), w.to(DEV))]
+    check(h, W, ids, _np(w), dtype, got)
+    alone = vl.run(h, W, torch.as_tensor(ids, dtype=torch.int32, device=DEV), w.to(DEV), want_grads=False)[0]
+    assert torch.equal(alone, got[0])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [90, 700])
 @pytest.mark.parametrize("offset", [0, 300, -300])
 def test_rows_with_impossible_targets(offset, V, dtype):
@@ -123,3 +142,32 @@ def test_rows_with_impossible_targets(offset, V, dtype):
     vl = VocabLoss(N, D, V, dtype, device=DEV)
     got = vl.run(h, W, torch.as_tensor(ids, dtype=torch.int32, device=DEV))
     check(h, W, ids, w, dtype, got)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [1, 5, 300])
+def test_targets_of_infinite_logits(V, dtype):
+    """A target of +inf or NaN: NaN in its row's loss and gradient; of -inf: loss +inf, the target's gradient -w, none from it
+    to the others; all other classes -inf: loss 0."""
+    W = torch.zeros(V, 8)
+    t = V - 1
+    W[t, 0], W[t, 1], W[t, 2] = float("inf"), float("nan"), -float("inf")
+    W[:t, 3] = -float("inf")
+    # a zero beside an infinity is NaN, so each row's product is formed apart: one column of W at a time
+    ids = torch.full((1,), t, dtype=torch.int32, device=DEV)
+    vl = VocabLoss(1, 1, V, dtype, device=DEV)
+    one = torch.ones(1, 1, dtype=TDT[dtype], device=DEV)
+    out = []
+    for i in range(4):
+        loss, dh, dW = vl.run(one, W[:, i:i + 1].contiguous().to(TDT[dtype]).to(DEV), ids)
+        out.append((float(loss[0]), dW[:, 0].float().cpu()))
+    for loss, dW in out[:2]:
+        assert np.isnan(loss) and torch.isnan(dW).all()
+    loss, dW = out[2]
+    if V == 1:
+        assert np.isnan(loss)
+    else:
+        assert loss == float("inf") and float(dW[t]) == -1.0
+        assert torch.allclose(dW[:t], torch.full((V - 1,), 1 / (V - 1)), rtol=2.0 ** -7)
+    loss, dW = out[3]
+    assert loss == 0.0 and (dW == 0).all()

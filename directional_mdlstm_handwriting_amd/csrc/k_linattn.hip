@@ -72,10 +72,18 @@ struct Op<float> {
     }
 };
 
-// log2 d: the instruction is within 1 ulp of it over all of [1/4, 1), near 1 too (every float was tried)
-__device__ inline float log2_of(float d) { return __builtin_amdgcn_logf(d); }
-// d^e for whole e >= 0, from log2 d: d^0 is 1 also for d = 0
-__device__ inline float power(float l2, int e) { return e == 0 ? 1.f : __builtin_amdgcn_exp2f((float)e * l2); }
+// A head's decay d, as its powers take it: log2 |d| and the sign. The instruction is within 1 ulp of log2 over all of
+// [1/4, 1), near 1 too (every float was tried).
+struct Decay {
+    float l2;
+    uint32_t sign;
+};
+__device__ inline Decay decay_of(float d) { return {__builtin_amdgcn_logf(fabsf(d)), __float_as_uint(d) & 0x80000000u}; }
+// d^e for whole e >= 0: d^0 is 1 also for d = 0, and odd powers of a decay below 0 are
+__device__ inline float power(Decay d, int e) {
+    const float m = e == 0 ? 1.f : __builtin_amdgcn_exp2f((float)e * d.l2);
+    return __uint_as_float(__float_as_uint(m) ^ ((uint32_t)e << 31 & d.sign));
+}
 
 // a value that all lanes share, in a scalar register
 __device__ inline float uniform(float x) {
@@ -436,16 +444,16 @@ __global__ __launch_bounds__(kThreads, (DIRECT ? 4 : Head<T, DA, DC, DIRECT>::oc
         rc.load(pc, ldc, t.from + a.dir * k, a.dir, n, dc, to + nb);
     };
     load(0, t0);
-    const float l2 = log2_of(a.decay[h]);
+    const Decay d = decay_of(a.decay[h]);
     State<DA, Hd::NT> x;
     x.clear();
     const auto add = [&](int k, const char* p) {
         const int n = min(C, t.len - k);
-        if (k > 0) x.scale(power(l2, n));
+        if (k > 0) x.scale(power(d, n));
         add_block<Hd, PARTS>(x, p, p + nb, [&](int q) {
             f32x4 f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) f[r] = a.sscale * power(l2, max(n - a.post - (16 * q + 4 * g + r), 0));
+            for (int r = 0; r < 4; ++r) f[r] = a.sscale * power(d, max(n - a.post - (16 * q + 4 * g + r), 0));
             return f;
         });
     };
@@ -492,12 +500,13 @@ __global__ __launch_bounds__(kThreads) void chain(const Args a, int blocks_per_h
         return;
     }
     const int64_t L = a.L, base = over_l(a, o0), end = over_l(a, o1 - o0 - 1);
-    const float l2 = log2_of(a.decay[h]), whole = power(l2, (int)L);
+    const Decay d = decay_of(a.decay[h]);
+    const float whole = power(d, (int)L);
     const int64_t hop = a.dir * a.H * a.size;
     // all tiles but the sequence's last one are whole
     const int rest = (int)(o1 - o0 - end * L), lead = end > 0 ? (int)L : rest;
     float* p = a.slots + ((a.dir > 0 ? base : base + end - 1) * a.H + h) * a.size + e;
-    float f = power(l2, a.dir > 0 ? lead : rest), v[V];
+    float f = power(d, a.dir > 0 ? lead : rest), v[V];
     constexpr int U = 8;
     for (int64_t i = 0; i < end; i += U) {
         float w[U][V];
@@ -516,7 +525,7 @@ __global__ __launch_bounds__(kThreads) void chain(const Args a, int blocks_per_h
     }
     if (a.last) {
         load_f32<V>(a.last + at, v);
-        f = power(l2, a.dir > 0 ? rest : lead);
+        f = power(d, a.dir > 0 ? rest : lead);
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = __builtin_fmaf(x[j], f, v[j]);
         store_f32<V>(a.last + at, v);
@@ -595,18 +604,18 @@ __global__ __launch_bounds__(SIDES * kThreads, (SIDES == 2 && DA > 64 ? 2 : Head
     if (enter) x.load(side, enter);
     else x.clear();
     // d^e for the e that occur, in two factors: within 16 (a lane's) and of 16s
-    const float l2 = log2_of(a.decay[h]);
-    float d16[CT], row_f = power(l2, i + a.post), near[4], far[4], left[4];
+    const Decay d = decay_of(a.decay[h]);
+    float d16[CT], row_f = power(d, i + a.post), near[4], far[4], left[4];
 #pragma unroll
-    for (int q = 0; q < CT; ++q) d16[q] = uniform(power(l2, 16 * q));
+    for (int q = 0; q < CT; ++q) d16[q] = uniform(power(d, 16 * q));
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int e = i - (4 * g + r);
-        near[r] = e < 0 ? 0.f : a.pscale * power(l2, e);
-        far[r] = a.pscale * power(l2, 16 + e);
-        left[r] = a.sscale * power(l2, 16 - a.post - (4 * g + r));
+        near[r] = e < 0 ? 0.f : a.pscale * power(d, e);
+        far[r] = a.pscale * power(d, 16 + e);
+        left[r] = a.sscale * power(d, 16 - a.post - (4 * g + r));
     }
-    const float d_block = uniform(power(l2, C));
+    const float d_block = uniform(power(d, C));
 
     // (a_i . b_j) d^{i-j}: the tiles of 16 x 16 on and below the diagonal, the lowest rows first, dealt out to the waves; row
     // i at lane % 16, j at 4 g + r

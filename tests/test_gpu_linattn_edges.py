@@ -1,4 +1,6 @@
-"""Linear attention with decays outside [0, 1].
+"""Linear attention where the other tests do not look: tiles of four and more blocks of 32 tokens for heads of every padded
+size, rows of whole 16-byte chunks or not; inputs above zero, so that an output is the sum of its terms' magnitudes and a
+wrong power of the decay shows; decays below 0 and above 1; gradients along their own direction.
 
 The reference walks the tokens in float64 on the device. Beside each state R it keeps E, the same sum with each term
 weighted by its distance in tokens: an output a^T R is off by at most
@@ -101,6 +103,29 @@ def _compare(lens, H, Dk, Dv, decay, dtype, reverse, positive, seed):
     return at
 
 
+DECAYS = 1 - 2.0 ** -np.arange(1.0, 10.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 64), (128, 64), (64, 128), (50, 50), (65, 63), (100, 100), (24, 128), (7, 9)])
+def test_tiles_of_many_blocks(Dk, Dv, reverse, dtype):
+    """96 heads and 900 tokens: tiles of 128 or 160 tokens, so that each buffer of a block is filled again and again."""
+    H = 96
+    print(f"[gpu] many blocks {Dk} {Dv} {reverse} {dtype}", flush=True)
+    at = _compare([523, 377], H, Dk, Dv, DECAYS[np.arange(H) % len(DECAYS)], dtype, reverse, True, Dk + Dv)
+    assert at.ws_bytes <= 2 * (900 // 96) * H * Dk * Dv * 4 + 32      # a state for each end of a tile of 96 tokens or more
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_long_sequences_above_zero(dtype):
+    """Tiles of 320 tokens, 16 of them in a row: one power of the slowest decay too many at a tile's end is 2^-9 of what it
+    brings, in fp32 many times the bound."""
+    H = 40
+    print(f"[gpu] long above zero {dtype}", flush=True)
+    _compare([5000, 1, 2000], H, 8, 8, DECAYS[np.arange(H) % len(DECAYS)], dtype, False, True, 3)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("reverse", [False, True])
 @pytest.mark.parametrize("decay", [-0.5, -0.97, -1.0, -0.0, -1e-30, 1.01, -1.01])
@@ -109,3 +134,38 @@ def test_decays_outside_zero_to_one(decay, reverse, dtype):
     print(f"[gpu] decay {decay} {reverse} {dtype}", flush=True)
     for positive in (False, True):
         _compare([301, 70, 1, 97], 1, 32, 48, [decay], dtype, reverse, positive, 5)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_against_differences_along_themselves(dtype):
+    """The loss sum(y w) + sum(hT u) moved along each gradient itself, where the change is the sum of the gradient's squares
+    and no term cancels another: half a step of bfloat16 on the way and one at the end, twice each."""
+    T, H, Dk, Dv, lens = 127, 2, 16, 24, [37, 90]
+    off = np.concatenate([[0], np.cumsum(lens)])
+    g = torch.Generator().manual_seed(9)
+    q, k, v, w = (torch.randn(T, H * n, generator=g).to(TDT[dtype]).to(DEV) for n in (Dk, Dk, Dv, Dv))
+    h0, u = (torch.randn(2, H, Dk, Dv, generator=g).to(DEV) for _ in range(2))
+    dec = torch.tensor([0.9, 0.98], device=DEV)
+    at = LinearAttention(off, T, H, Dk, Dv, dec, dtype, device=DEV)
+    at.forward(q, k, v, h0)
+    grads = at.backward(q, k, v, w, h0, u)
+    torch.cuda.synchronize()
+    base = [t.double().reshape(T, H, -1) for t in (q, k, v)] + [h0.double()]
+    scale = float(np.float32(at.scale))
+
+    def loss(q, k, v, h):
+        total = 0.0
+        for s in range(2):
+            tok = range(int(off[s]), int(off[s + 1]))
+            y, _, R, _ = walk(tok, q, k, v, dec.double(), h[s], True, 1.0)
+            total += float((scale * y * w.double().reshape(T, H, -1)).sum() + (R * u[s].double()).sum())
+        return total
+
+    for i, G in enumerate(grads):
+        e = G.double().reshape(base[i].shape)
+        e = e / e.abs().max()
+        # the loss is linear in each input: the difference is exact but for rounding
+        diff = loss(*[b + 0.5 * e if j == i else b for j, b in enumerate(base)]) - \
+            loss(*[b - 0.5 * e if j == i else b for j, b in enumerate(base)])
+        want = float((G.double().reshape(e.shape) * e).sum())
+        assert abs(diff - want) <= (4 * HALF[dtype] + 3000 * U) * want, i

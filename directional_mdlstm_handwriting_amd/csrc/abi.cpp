@@ -1495,6 +1495,10 @@ int mdl_dropout(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx,
     if (reinterpret_cast<uintptr_t>(rng) % 8) return fail(MDL_EINVAL, F + ": rng not 8-byte aligned");
     if ((rc = check_stride(F, "ldx", N, D, ldx)) || (rc = check_stride(F, "ldy", N, D, ldy))) return rc;
     if (r && (rc = check_stride(F, "ldr", N, D, ldr))) return rc;
+    if ((rc = check_apart(F, {y}, {rng}))) return rc;
+    // elements are read and written by the same thread only where both lie alike
+    if (N > 1 && ((y == x && ldy != ldx) || (y == r && ldy != ldr)))
+        return fail(MDL_EINVAL, F + ": y over x or r at another stride");
     if (N > mdl::dropout_max_groups() / (((int64_t)D + 7) / 8))
         return fail(MDL_EOVERFLOW, F + ": the launch exceeds 2^31 threads");
     hipError_t e;

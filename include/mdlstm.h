@@ -644,7 +644,8 @@ int mdl_linattn_step(int32_t S, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype
  * r); any alignment of the element type. One float32 sum, rounded once. y may be x
  * or r at the same stride; other overlaps are not allowed.
  * Errors: MDL_EINVAL for null tensors, N < 0, D < 1, a stride below D, an unknown
- * dtype, p outside [0, 1) or rounded to 1, or a misaligned rng; MDL_EOVERFLOW when
+ * dtype, p outside [0, 1) or rounded to 1, y over x or r at another stride (with one
+ * row, none) or over rng, or a misaligned rng; MDL_EOVERFLOW when
  * rows times a stride reach 2^60 or N ceil(D / 8) exceeds 2^33.
  */
 int mdl_dropout(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx, const void* r, int64_t ldr, float p,

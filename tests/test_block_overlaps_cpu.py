@@ -1,0 +1,20 @@
+"""Outputs over inputs that dropout refuses, without a GPU. The addresses given are never followed."""
+
+import pytest
+
+import directional_mdlstm_handwriting_amd as M
+from test_block_refusals_cpu import DROP, A, _code, _with
+
+
+@pytest.mark.parametrize("change", [
+    dict(y=A(3), ldy=9), dict(y=A(3), ldx=9), dict(y=A(0), ldy=9), dict(y=A(0), ldx=9), dict(y=A(1), ldr=9),
+    dict(y=A(1), ldy=10), dict(y=A(2)),
+])
+def test_dropout_over_its_inputs_at_another_stride(change):
+    base = _with(DROP, ldx=8, ldr=8, ldy=8, **{k: v for k, v in change.items() if k == "y"})
+    rest = {k: v for k, v in change.items() if k != "y"}
+    if base["y"] == A(3):                    # apart: nothing to refuse but what is refused anyway
+        assert _code(M.mdl_dropout, **_with(base, x=None, **rest)) == M.MDL_EINVAL
+    else:
+        assert _code(M.mdl_dropout, **_with(base, **rest)) == M.MDL_EINVAL
+        assert "over" in M.mdl_last_error()

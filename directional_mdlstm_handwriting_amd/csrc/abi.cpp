@@ -1553,7 +1553,7 @@ int mdl_vocab_loss(int64_t N, int32_t D, int32_t V, int32_t dtype, const void* h
     if (D % (dtype == MDL_BF16 ? 8 : 4) == 0 && reinterpret_cast<uintptr_t>(W) % 16)
         return fail(MDL_EINVAL, F + ": W not 16-byte aligned");
     if ((rc = check_ws(F, "mdl_vocab_loss_workspace_size", need, ws, ws_bytes))) return rc;
-    if ((rc = check_apart(F, {dW}, {h, W, dh})) || (rc = check_apart(F, {dh}, {W}))) return rc;
+    if ((rc = check_apart(F, {dW, loss}, {h, W, ids, w, dh})) || (rc = check_apart(F, {dh}, {W, ids, w}))) return rc;
     const mdl::VocabArgs a{N, D, V, h, W, ldh, lddh, ids, w, loss, dh, dW};
     hipError_t e;
     {

@@ -681,8 +681,8 @@ int mdl_dropout(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx,
  * ws: >= mdl_vocab_loss_workspace_size bytes (grads: whether dh and dW are wanted),
  * 16-byte aligned, contents not kept.
  * Errors: MDL_EINVAL for null tensors, N < 0, D, V < 1, a stride below D, an unknown
- * dtype, dh without dW or dW without dh, dW over h, W or dh, dh over W, a misaligned
- * W or workspace; MDL_EUNSUPPORTED for D above 65536 or V above 2^20; MDL_EOVERFLOW
+ * dtype, dh without dW or dW without dh, dW, loss or dh over another tensor (dh over
+ * h apart), a misaligned W or workspace; MDL_EUNSUPPORTED for D above 65536 or V above 2^20; MDL_EOVERFLOW
  * when rows times a stride reach 2^60 or a launch exceeds 2^31 threads (N or V times
  * D, D rounded up to 256; N times V / 128); MDL_ESIZE for a short workspace.
  */

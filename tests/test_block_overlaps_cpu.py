@@ -1,9 +1,9 @@
-"""Outputs over inputs that dropout refuses, without a GPU. The addresses given are never followed."""
+"""Outputs over inputs that dropout and the vocabulary's cross entropy refuse, without a GPU. The addresses given are never followed."""
 
 import pytest
 
 import directional_mdlstm_handwriting_amd as M
-from test_block_refusals_cpu import DROP, A, _code, _with
+from test_block_refusals_cpu import DROP, VOCAB, A, _code, _with
 
 
 @pytest.mark.parametrize("change", [
@@ -18,3 +18,10 @@ def test_dropout_over_its_inputs_at_another_stride(change):
     else:
         assert _code(M.mdl_dropout, **_with(base, **rest)) == M.MDL_EINVAL
         assert "over" in M.mdl_last_error()
+
+
+@pytest.mark.parametrize("change", [dict(loss=A(0)), dict(loss=A(1)), dict(loss=A(2)), dict(loss=A(3)), dict(loss=A(5)),
+                                    dict(loss=A(6)), dict(dh=A(2)), dict(dh=A(3)), dict(dW=A(2)), dict(dW=A(3))])
+def test_vocab_loss_over_its_tensors(change):
+    assert _code(M.mdl_vocab_loss, **_with(VOCAB, **change)) == M.MDL_EINVAL
+    assert "over" in M.mdl_last_error()

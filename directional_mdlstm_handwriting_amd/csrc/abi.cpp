@@ -1347,7 +1347,8 @@ int mdl_linattn_forward(const int64_t* seq_off, int32_t S, int64_t T, int32_t H,
         (rc = check_stride23(F, "ldv", T, nv, ldv)) || (rc = check_stride23(F, "ldy", T, nv, ldy)))
         return rc;
     if ((rc = check_ws(F, "mdl_linattn_workspace_size", need, ws, ws_bytes))) return rc;
-    if (T > 0 && (rc = check_apart(F, {y, hT}, {q, k, v}))) return rc;
+    if ((rc = check_apart(F, {hT}, {seq_off, decay}))) return rc;
+    if (T > 0 && (rc = check_apart(F, {y, hT}, {seq_off, decay, q, k, v, h0}))) return rc;
     if (share_bytes(h0, hT, state_bytes(S, H, Dk, Dv))) return fail(MDL_EINVAL, F + ": hT over h0");
     mdl::AttnArgs a{};
     a.off = seq_off;
@@ -1398,7 +1399,8 @@ int mdl_linattn_backward(const int64_t* seq_off, int32_t S, int64_t T, int32_t H
         (rc = check_stride23(F, "lddv", T, nv, lddv)))
         return rc;
     if ((rc = check_ws(F, "mdl_linattn_workspace_size", need, ws, ws_bytes))) return rc;
-    if (T > 0 && (rc = check_apart(F, {dq, dk, dv}, {q, k, v, dy}))) return rc;
+    if ((rc = check_apart(F, {dh0}, {seq_off, decay}))) return rc;
+    if (T > 0 && (rc = check_apart(F, {dq, dk, dv, dh0}, {seq_off, decay, q, k, v, dy, h0, dhT}))) return rc;
     if (share_bytes(h0, dh0, state_bytes(S, H, Dk, Dv)) || share_bytes(dhT, dh0, state_bytes(S, H, Dk, Dv)))
         return fail(MDL_EINVAL, F + ": dh0 over h0 or dhT");
     mdl::AttnArgs a{};

@@ -1,9 +1,9 @@
-"""Outputs over inputs that dropout and the vocabulary's cross entropy refuse, without a GPU. The addresses given are never followed."""
+"""Outputs over inputs that linear attention, dropout and the vocabulary's cross entropy refuse, without a GPU. The addresses given are never followed."""
 
 import pytest
 
 import directional_mdlstm_handwriting_amd as M
-from test_block_refusals_cpu import DROP, VOCAB, A, _code, _with
+from test_block_refusals_cpu import ATTN_B, ATTN_F, DROP, VOCAB, A, _code, _with
 
 
 @pytest.mark.parametrize("change", [
@@ -24,4 +24,17 @@ def test_dropout_over_its_inputs_at_another_stride(change):
                                     dict(loss=A(6)), dict(dh=A(2)), dict(dh=A(3)), dict(dW=A(2)), dict(dW=A(3))])
 def test_vocab_loss_over_its_tensors(change):
     assert _code(M.mdl_vocab_loss, **_with(VOCAB, **change)) == M.MDL_EINVAL
+    assert "over" in M.mdl_last_error()
+
+
+@pytest.mark.parametrize("change", [dict(y=A(5)), dict(y=A(1)), dict(y=A(0)), dict(hT=A(1)), dict(hT=A(0)), dict(hT=A(6))])
+def test_attention_forward_over_states_and_decays(change):
+    assert _code(M.mdl_linattn_forward, **_with(ATTN_F, **change)) == M.MDL_EINVAL
+    assert "over" in M.mdl_last_error()
+
+
+@pytest.mark.parametrize("change", [dict(dq=A(5)), dict(dk=A(7)), dict(dv=A(1)), dict(dv=A(0)), dict(dh0=A(2)), dict(dh0=A(6)),
+                                    dict(dh0=A(8)), dict(dh0=A(10)), dict(dh0=A(1)), dict(dq=A(11))])
+def test_attention_backward_over_states_and_decays(change):
+    assert _code(M.mdl_linattn_backward, **_with(ATTN_B, **change)) == M.MDL_EINVAL
     assert "over" in M.mdl_last_error()

@@ -1456,7 +1456,10 @@ int mdl_linattn_step(int32_t S, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype
     if ((rc = check_stride(F, "ldq", S, nk, ldq)) || (rc = check_stride(F, "ldk", S, nk, ldk)) ||
         (rc = check_stride(F, "ldv", S, nv, ldv)) || (rc = check_stride(F, "ldy", S, nv, ldy)))
         return rc;
-    if ((rc = check_apart(F, {y}, {q, k, v}))) return rc;
+    if ((rc = check_apart(F, {y, h_out}, {q, k, v, decay, slots})) || (rc = check_apart(F, {y}, {h_in}))) return rc;
+    // a row's states are read and written by one workgroup only where both arrays are one
+    if (h_in != h_out && share_bytes(h_in, h_out, state_bytes(n_slots, H, Dk, Dv)))
+        return fail(MDL_EINVAL, F + ": h_out over a part of h_in");
     mdl::AttnArgs a{};
     a.S = S;
     a.H = H;

@@ -596,8 +596,8 @@ int mdl_distill(int64_t N, int32_t V, int32_t k, int32_t dtype, const void* z, i
  *
  * mdl_linattn_step: one token for each of S streams (serving). Row i advances the
  * states slots[i] (device, int32; i itself if NULL) from h_in to h_out
- * ([n_slots][H][Dk][Dv] float32; the same array to update in place) and writes
- * row i of y. A row whose slot lies outside [0, n_slots) is left out: neither its
+ * ([n_slots][H][Dk][Dv] float32; the same array to update in place, no other
+ * overlap) and writes row i of y. A row whose slot lies outside [0, n_slots) is left out: neither its
  * y nor any state is written. Slots must differ from each other.
  *
  * Errors: MDL_EINVAL for null tensors, S, H, Dk, Dv < 1, T < 0, a stride below its

@@ -3,7 +3,7 @@
 import pytest
 
 import directional_mdlstm_handwriting_amd as M
-from test_block_refusals_cpu import ATTN_B, ATTN_F, DROP, VOCAB, A, _code, _with
+from test_block_refusals_cpu import ATTN_B, ATTN_F, ATTN_S, DROP, VOCAB, A, _code, _with
 
 
 @pytest.mark.parametrize("change", [
@@ -37,4 +37,13 @@ def test_attention_forward_over_states_and_decays(change):
                                     dict(dh0=A(8)), dict(dh0=A(10)), dict(dh0=A(1)), dict(dq=A(11))])
 def test_attention_backward_over_states_and_decays(change):
     assert _code(M.mdl_linattn_backward, **_with(ATTN_B, **change)) == M.MDL_EINVAL
+    assert "over" in M.mdl_last_error()
+
+
+# nine slots of 2 x 8 x 4 floats
+@pytest.mark.parametrize("change", [dict(h_out=A(6) + 4), dict(h_out=A(6) + 256), dict(h_out=A(6) - 9 * 256 + 4),
+                                    dict(y=A(6)), dict(h_out=A(9), y=A(9)), dict(y=A(1)), dict(y=A(5)), dict(h_out=A(2)),
+                                    dict(h_out=A(1))])
+def test_attention_step_over_states(change):
+    assert _code(M.mdl_linattn_step, **_with(ATTN_S, **change)) == M.MDL_EINVAL
     assert "over" in M.mdl_last_error()

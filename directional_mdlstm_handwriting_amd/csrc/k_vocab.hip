@@ -654,6 +654,8 @@ VocabPlan vocab_plan(int64_t N, int D, int V, int dtype, bool grads) {
         p.rows = std::min(N, up((N + blocks - 1) / blocks, 128));
     }
     p.tiles = (V + 127) / 128;  // at most
+    // 256 threads a tile of 128 x 128 logits: the loss alone of very many rows takes several launches
+    p.rows = std::min<int64_t>(p.rows, kMaxLaunchThreads / 256 / p.tiles * 128);
     size_t at = 0;
     const auto take = [&](size_t bytes) {
         const size_t o = at;

@@ -1,4 +1,5 @@
-"""Outputs over inputs that linear attention, dropout and the vocabulary's cross entropy refuse, without a GPU. The addresses given are never followed."""
+"""Outputs over inputs that linear attention, dropout and the vocabulary's cross entropy refuse, without a GPU, and sizes of
+workspaces at a launch's limits. The addresses given are never followed."""
 
 import pytest
 
@@ -47,3 +48,12 @@ def test_attention_backward_over_states_and_decays(change):
 def test_attention_step_over_states(change):
     assert _code(M.mdl_linattn_step, **_with(ATTN_S, **change)) == M.MDL_EINVAL
     assert "over" in M.mdl_last_error()
+
+
+def test_vocab_loss_alone_in_launches_of_a_legal_size():
+    """The loss alone of 2^23 rows over 32768 classes: one launch would have 2^16 x 2^8 tiles of 256 threads, 2^32. It is made
+    of several, whose statistics (8 bytes a row and tile of 128 classes) the workspace holds one of."""
+    f = M.mdl_vocab_loss_workspace_size
+    N, V = 1 << 23, 1 << 15
+    rows = N * (16 + 4 * 4)                  # the hidden states of 8 channels and a row's numbers
+    assert f(N, 8, V, M.MDL_BF16, False) < rows + N * 4 + (1 << 16) + (N // 2) * (V // 128) * 8

@@ -171,3 +171,24 @@ def test_targets_of_infinite_logits(V, dtype):
         assert torch.allclose(dW[:t], torch.full((V - 1,), 1 / (V - 1)), rtol=2.0 ** -7)
     loss, dW = out[3]
     assert loss == 0.0 and (dW == 0).all()
+
+
+def test_more_rows_than_a_launch_takes():
+    """The loss alone of 2^23 rows over 2^15 classes, whose tiles one launch cannot count: each row as by itself, at the ends
+    and around the middle, where one launch ends and the next begins."""
+    N, K, V = 1 << 23, 8, 1 << 15
+    print("[gpu] many rows", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    h = torch.randn(N, K, generator=g, device=DEV).to(torch.bfloat16)
+    W = torch.randn(V, K, generator=g, device=DEV).to(torch.bfloat16)
+    ids = torch.randint(0, V, (N,), generator=g, device=DEV, dtype=torch.int32)
+    loss = VocabLoss(N, K, V, "bf16", device=DEV).run(h, W, ids, want_grads=False)[0]
+    mid = N // 2
+    at = torch.cat([torch.arange(a, b, device=DEV) for a, b in ((0, 70), (mid - 70, mid + 70), (N - 70, N))])
+    z = h[at].double() @ W.double().t().contiguous()
+    lse, zt = torch.logsumexp(z, 1), z[torch.arange(len(at), device=DEV), ids[at].long()]
+    # a logit is a sum of 8 products, the rest as the file's other bounds, and |x| u of the exponentials' arguments
+    big = (h[at].double().abs() @ W.double().abs().t().contiguous()).max(1).values
+    tol = 2 * (K + 2) * U * big + (200 + V / 512 + 2 * big) * U + 2 * U * (lse - zt)
+    assert bool(((loss[at].double() - (lse - zt)).abs() <= tol).all())
+    assert bool(torch.isfinite(loss).all())

@@ -537,7 +537,7 @@ __global__ __launch_bounds__(256) void grad(const GradArgs a, T* G) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = (float)q[e] * f;
     }
-    const float own = a.own[m];
+    const float own = id >= v && id < v + 8 ? a.own[m] : 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = k == 0.f || v + e >= a.V ? 0.f : k * (v + e == id ? own : x[e]);
     if constexpr (sizeof(T) == 4) {
@@ -655,7 +655,7 @@ VocabPlan vocab_plan(int64_t N, int D, int V, int dtype, bool grads) {
     }
     p.tiles = (V + 127) / 128;  // at most
     // 256 threads a tile of 128 x 128 logits: the loss alone of very many rows takes several launches
-    p.rows = std::min<int64_t>(p.rows, kMaxLaunchThreads / 256 / p.tiles * 128);
+    if (!grads) p.rows = std::min<int64_t>(p.rows, kMaxLaunchThreads / 256 / p.tiles * 128);
     size_t at = 0;
     const auto take = [&](size_t bytes) {
         const size_t o = at;

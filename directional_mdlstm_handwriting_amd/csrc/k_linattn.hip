@@ -18,9 +18,13 @@
 // boundaries the slots from off[s] / L on, which are as many as it can need; T / L + S numbers and T / L slots in all.
 //
 // What bounds it. bfloat16: memory. Both ways over 4 documents (208246 tokens, 8 heads of 128 + 128) move each tensor 18 times
-// (426 MB each; states 2, outputs 4, states 2, dv and dk 6, dq 4) where 8 would do, in 1.93 ms: 219 + 404 + 217 + 688 + 402 us
-// and two chains of 19, 3.7 to 4.2 TB/s, the matrix units busy for 19 to 33 % of the cycles. fp32 with heads of 50 (656603
-// tokens, 1024 sequences): the matrix units, busy for 50 % of them in the outputs (200 + 405 + 205 us of 941 in all; 64 x 64 padded).
+// (426 MB each; states 2, outputs 4, states 2, dv and dk 6, dq 4) where 8 would do, in 1.91 to 1.94 ms: 222 + 402 + 217 + 665 +
+// 405 us and two chains of 19, 3.8 to 4.3 TB/s, the matrix units busy for 19 to 30 % of the cycles. fp32 with heads of 50 (656603
+// tokens, 1024 sequences): the matrix units, busy for 50 % of them in the outputs (192 + 392 + 196 us of 942 in all; 64 x 64
+// padded, products whose depth is a head's channels run 16 steps of 4 where 13 hold values).
+//
+// Heads are padded to 64 or 128 channels, so narrow ones cost what 64 do: 20597 tokens of 8 heads, both ways, take 119, 108 and
+// 115 us for heads of 8, 16 and 32 in bfloat16 (140 for 64) and 301, 252 and 281 in fp32 (305 for 64).
 #include "kernels.h"
 #include "seqio.h"
 
@@ -168,9 +172,10 @@ __device__ inline Tile tile_of(const Args& a, int64_t number) {
 }
 
 // ---- blocks of rows ---------------------------------------------------------------------------------------------
-// An LDS tile of C rows of D elements, in whose rows the 16-byte chunks change places with the row: a wave's reads along the
-// rows (16 of them, 32 or 64 bytes each) and across them meet all banks, and nothing lies between the rows, as the loads that
-// go straight to LDS need it.
+// An LDS tile of C rows of D elements, in whose rows the 16-byte chunks change places with the row, so that reads of 16 rows
+// spread over the banks; nothing lies between the rows, as the loads that go straight to LDS need it. fp32 has hardly any
+// conflicts left (0 to 0.2 cycles an LDS instruction), bfloat16 2.0 in `states` and 2.6 to 2.8 in `outputs`: an order that
+// took these down to 0 and 1.6 left the kernels' times as they were and was not kept.
 template <typename T, int D>
 struct Plane {
     typedef typename Op<T>::Quad Quad;
@@ -308,7 +313,9 @@ struct Head {
     typedef Op<T> O;
     static constexpr bool DIRECT = DIRECT_;
     static constexpr int DA = DA_, DC = DC_, C = O::C, CT = C / 16, NT = DC / 64, waves = 4;
-    // waves a SIMD, and so workgroups a compute unit, that the registers allow
+    // waves a SIMD that the registers are to allow: of workgroups of four waves, so many a compute unit. (`outputs` with two
+    // sides of wide heads has eight waves and 156 registers: one workgroup. fp32 outputs of 128 + 128 channels fill all 256
+    // registers and keep 8 more in scratch.)
     static constexpr int occupancy = DA + DC == 128 ? 4 : !DIRECT && (DA + DC > 192 || sizeof(T) == 4) ? 2 : 3;
     typedef Plane<T, DA> PA;
     typedef Plane<T, DC> PC;
@@ -881,8 +888,10 @@ int linattn_max_d() { return 128; }
 
 // Tiles: so many that their workgroups fill the chip a whole number of times, as many tiles as sequences at least beside the
 // sequences' own (whose last tiles are short): once where there are few sequences, since a tile costs its state's way to
-// memory and back, else four times, since tiles of many lengths do not end together. Wide heads have three workgroups a
-// compute unit, narrow ones four. At 656603 x 50 (fp32, 1024 sequences, both ways) tiles of 224 take 941 to 987 us, of 672 1101.
+// memory and back, else four times, since tiles of many lengths do not end together. Counted are the workgroups a compute
+// unit takes of bfloat16 in whole chunks: three with wide heads, four with narrow ones. All launches of both directions share
+// the tiles; wide heads in fp32 or of other rows have two (20597 x 8 x 128 in fp32, both ways: 1026 us, 5 times the matrix
+// units' floor; 20597 x 8 x 100 in bfloat16: 391 us, 316 for 128), the launch of dv and dk one. At 656603 x 50 (fp32, 1024 sequences, both ways) tiles of 224 take 941 to 987 us, of 672 1101.
 AttnPlan attn_plan(int S, int64_t T, int H, int Dk, int Dv) {
     AttnPlan p;
     const int64_t fill = (std::max(Dk, Dv) > 64 ? 3 : 4) * 256;

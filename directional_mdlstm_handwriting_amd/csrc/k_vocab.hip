@@ -1,5 +1,5 @@
-// k_vocab.hip — softmax cross entropy over a vocabulary from the hidden states and the class weights, with its gradients,
-// without the logits in memory.
+// k_vocab.hip — softmax cross entropy over a vocabulary from the hidden states and the class weights, with its gradients:
+// of all the logits, no more than a block of rows' is ever held (up to 256 MB, or 1024 rows), and for the loss alone none.
 //
 //   z = h W^T,  loss_n = w_n (ln sum_c exp z_nc - z_n,id),  G = w (softmax z - [c = id]),  dh = G W,  dW = G^T h
 //
@@ -13,7 +13,8 @@
 // of the value, an eighth of the one G is about to get, or of 2^-40 of the maximum). `grad` makes G of them where they lie, and two products take G into dh and dW: 6 N V D operations. Several
 // blocks add up dW in fp32, which costs 8 bytes an element and block: at 1024 rows a quarter of the block's products.
 // (Forming the logits again, once the statistics are known, is 8 N V D operations and nothing written but G: 4096 x 2048 over
-// 32000 classes in bfloat16 took 1985 us that way and takes 1536, in fp32 15.6 and 12.0 ms.)
+// 32000 classes in bfloat16 took 1985 us that way and takes 1507 to 1553, in fp32 15.6 and 12.1 ms. 16384 x 2048 over 131072
+// classes, 16 blocks of 1024 rows, takes 31.0 ms: 0.85 PFLOP/s where one block of 4096 rows over 32000 reaches 1.05.)
 //
 // Products: tiles of BM x BN by 8 (4) waves, 32 x 32 results of the matrix instructions (32x32x16 bfloat16, 32x32x2 fp32),
 // 128 bytes of depth at a time from global memory straight into LDS, one step ahead of the products. An operand whose rows
@@ -21,9 +22,10 @@
 // all banks (turned by every row: 3.9 cycles of conflicts a read, now 0.2, and the same time); one whose rows run across it
 // is laid as it comes and read by transposing reads (bfloat16) or word by word (fp32).
 //
-// Measured, 4096 x 2048 over 32000 classes in bfloat16 (537 GFLOP a product): logits and statistics 576 us, of which writing
-// 262 MB is some 50, dh 501 + 14, dW 488 (0.93, 1.07 and 1.10 PFLOP/s; the matrix units are busy for 51, 55 and 61 % of the
-// cycles; the library's 8192^3 reaches 1.39), G 84 (524 MB at 6.2 TB/s), packing and joining 16.
+// Measured, 4096 x 2048 over 32000 classes in bfloat16 (537 GFLOP a product): logits and statistics 575 us, of which writing
+// 262 MB is some 50 to 100 (the loss alone, all launches, takes 470 to 486), dh 495 + 14, dW 481 (0.93, 1.08 and 1.12 PFLOP/s;
+// the matrix units are busy for 51, 55 and 61 % of the cycles; the library's 8192^3 reaches 1.39), G 85 (524 MB at 6.2 TB/s),
+// packing and joining 16.
 #include "kernels.h"
 #include "seqio.h"
 
@@ -598,8 +600,8 @@ struct Cut {
 // there, which fp32 feels first, and for few tiles whose depth is not split. Otherwise what an estimate of the time says: a
 // compute unit takes one of the larger tiles at a time or two small ones, rounds come out even or not, a part of the depth
 // costs its sums' way to memory and back, a round its loads' latency and its results. In fp32 the small tiles are as fast as
-// the larger ones (4096 x 2048 over 32000: 12.0 ms both) and leave less of the last round idle (19795 x 1664 over 4193: 6.8
-// ms, 8.9 in the larger ones), so that the larger ones are bfloat16's alone (dh of 4096 x 2048 over 32000: 501 us in 2 parts
+// the larger ones (4096 x 2048 over 32000: 12.0 ms both when they were compared) and leave less of the last round idle (19795 x 1664 over 4193: 6.8
+// ms, 8.9 in the larger ones), so that the larger ones are bfloat16's alone (dh of 4096 x 2048 over 32000: 495 us in 2 parts
 // of larger tiles, 600 in small ones).
 Cut cut_of(int64_t M, int64_t N, int64_t K, int e, bool along, bool split) {
     const int64_t steps = (K * e + 127) / 128;

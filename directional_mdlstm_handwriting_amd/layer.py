@@ -13,7 +13,7 @@ at once or a token at a time; ``BlockNorm`` the norms around such a block with
 its gate and residual; ``LinearAttention`` and ``AttentionState`` the recurrence
 with a matrix for a state and a decay for each head; ``Dropout`` a block's
 dropout onto the residual; ``TopKDistill`` the distillation loss of its logits,
-``VocabLoss`` the cross entropy over a vocabulary without them.
+``VocabLoss`` the cross entropy over a vocabulary from hidden states and class weights.
 """
 
 from __future__ import annotations
@@ -783,8 +783,8 @@ class Dropout(_Buffers):
 
 class VocabLoss(_Buffers):
     """Softmax cross entropy of N rows over V classes from their hidden states of D channels and the classes' weights
-    (mdl_vocab_loss): the loss per row and the gradients of the sum, in one call and without the logits. Holds them and the
-    workspaces, one for each kind of call; results stand until the next call."""
+    (mdl_vocab_loss): the loss per row and the gradients of the sum, in one call, whose workspace has the logits of a block of
+    rows at most. Holds results and workspaces, one for each kind of call; results stand until the next call."""
 
     def __init__(self, N: int, D: int, V: int, x_dtype: str = "f32", device: str = "cuda"):
         self.device = _device(device)

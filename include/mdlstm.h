@@ -653,8 +653,8 @@ int mdl_dropout(int64_t N, int32_t D, int32_t dtype, const void* x, int64_t ldx,
 
 /*
  * Softmax cross entropy over a vocabulary from the hidden states and the class
- * weights, with its gradients, without the logits in memory: over N rows of D
- * channels and V classes,
+ * weights, with its gradients, holding the logits of a block of rows at most: over N
+ * rows of D channels and V classes,
  *     z = h W^T,  loss[n] = w[n] (ln sum_c exp z_nc - z_n,ids[n])
  *     G = w (softmax z - [c = id]),  dh = G W,  dW = G^T h     (gradients of sum loss)
  * h: [N][D] of `dtype` at row stride ldh, any alignment of the element type; W: [V][D]
